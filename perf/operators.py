@@ -446,11 +446,11 @@ def _exact_rope(x, pos, d, layout, kw, inverse):
 def _exact_e4m3(c):
     """The values that E4M3 codes with a power-of-two row scale stand for."""
     x = c.double()
-    top = x.abs().amax(-1, keepdim=True)
-    e = torch.where(top > 0, torch.ceil(torch.log2(top.clamp_min(1e-300) / 448.0)), torch.zeros_like(top))
-    u = x / torch.exp2(e)
-    step = torch.exp2(torch.floor(torch.log2(u.abs().clamp_min(2.0 ** -6))).clamp(-6, 8) - 3)
-    return torch.round(u / step) * step * torch.exp2(e)          # torch.round: ties to even
+    m, ex = torch.frexp(x.abs().amax(-1, keepdim=True))          # 448 = 0.875 * 2^9
+    e = torch.where(m > 0, ex - 9 + (m > 0.875), 0)
+    u = torch.ldexp(x, -e)
+    step = torch.ldexp(torch.ones_like(u), torch.frexp(u.abs().clamp_min(2.0 ** -6))[1] - 4)   # 2^(floor(log2 u) - 3)
+    return torch.ldexp(torch.round(u / step) * step, e)          # torch.round: ties to even
 
 
 def exact(case, seed):
