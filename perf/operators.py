@@ -152,13 +152,18 @@ def _randn(g, shape, std=1.0):
     return (torch.randn(shape, generator=g, device=DEV) * std).to(torch.bfloat16)
 
 
+def _pow2(e):
+    """2^e in 64 bits from its bit pattern (a power function may be off by an ulp)."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
 def _fp8_rows(c):
     """bf16 rows -> E4M3 codes and the power-of-two scale of each row (the smallest
     2^e with max |x| 2^-e <= 448)."""
     x = c.float()
     m, ex = torch.frexp(x.abs().amax(-1))
     e = torch.where(m == 0, torch.zeros_like(ex), torch.where(m <= 0.875, ex - 9, ex - 8))
-    s = torch.ldexp(torch.ones_like(m), e)
+    s = _pow2(e).float()
     return (x / s[:, None]).to(torch.float8_e4m3fn), s
 
 
@@ -448,9 +453,9 @@ def _exact_e4m3(c):
     x = c.double()
     m, ex = torch.frexp(x.abs().amax(-1, keepdim=True))          # 448 = 0.875 * 2^9
     e = torch.where(m > 0, ex - 9 + (m > 0.875), 0)
-    u = torch.ldexp(x, -e)
-    step = torch.ldexp(torch.ones_like(u), torch.frexp(u.abs().clamp_min(2.0 ** -6))[1] - 4)   # 2^(floor(log2 u) - 3)
-    return torch.ldexp(torch.round(u / step) * step, e)          # torch.round: ties to even
+    u = x * _pow2(-e)
+    step = _pow2(torch.frexp(u.abs().clamp_min(2.0 ** -6))[1] - 4)     # 2^(floor(log2 u) - 3)
+    return torch.round(u / step) * step * _pow2(e)               # torch.round: ties to even
 
 
 def exact(case, seed):
