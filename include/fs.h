@@ -483,10 +483,164 @@ fs_status fs_farskip_stack_backward(const fs_layer_desc* desc, int32_t L, int32_
                                     const float* d_os, float* dx, const fs_block_grads* grads,
                                     void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- attention
+ * The operators of an attention sub-layer whose keys and values come from one
+ * latent vector per token (latent attention, the attention of the DeepSeek
+ * models): rotary positions, the paged cache of latent vectors, the absorbed
+ * form that reads it for the newest tokens, and the expanded form over whole
+ * sequences with its gradient.  They serve the real sub-block where
+ * fs_attn_standin stands in for it: its fp32 `extra` of fs_combine takes the
+ * output projection of these calls' results.
+ *
+ * Per token: a latent vector c (512) and one rotary key k_r (64) shared by all
+ * heads; per head the expanded key part k_n = W_UK c (128) and value v = W_UV c
+ * (128); queries q = [q_n (128) | q_r (64)].  With q_l = W_UK^T q_n (512),
+ *   q_n . k_n = q_l . c   and   sum_j p_j v_j = W_UV sum_j p_j c_j,
+ * so a few new tokens attend over the cached c directly (absorbed form); the
+ * per-head products with W_UK and W_UV are the caller's.  These widths are
+ * fixed, heads 1 .. 128, activations bf16 (scores, softmax statistics and sums
+ * fp32; probabilities enter the second product as bf16).
+ *
+ * Row operands are (pointer, row stride, head stride) in elements, the vector
+ * itself contiguous: 16-byte aligned pointers, strides multiples of 16 bytes
+ * and at most 2^36 elements, not zero where the extent is above one (a
+ * broadcast operand is FS_ERR_UNSUPPORTED; a negative stride or an output whose
+ * vectors overlap is FS_ERR_INVALID_ARG).  Index arrays and lse need only their
+ * own type's alignment.  Outputs must not overlap inputs (fs_rope: in place is
+ * allowed with the same pointer and strides).  The workspaces hold nothing
+ * between calls; calls that may run at the same time (two streams, two graphs)
+ * need one each. */
+typedef struct {
+    const void* p;
+    int64_t row, head;
+} fs_rows;
+typedef struct {
+    void* p;
+    int64_t row, head;
+} fs_rows_out;
+
+/* Rotary positions.  Pair i of the rotated part (elements 2i, 2i + 1, or with
+ * FS_ROPE_HALF i, i + d_rot / 2) turns by pos * f_i:
+ *   y_a = m (a cos - b sin), y_b = m (a sin + b cos),  m = mscale,
+ *   f_i = base^(-2 i / d_rot); with factor > 1 (a model of orig_len positions
+ *   used up to factor times as far) f_i moves to f_i / factor along a ramp over
+ *   i: 0 at the pair that makes beta_fast turns over orig_len, 1 at beta_slow:
+ *   lo = max(0, floor(i(beta_fast))), hi = min(d_rot - 1, ceil(i(beta_slow))),
+ *   i(n) = d_rot log(orig_len / (2 pi n)) / (2 log base),
+ *   ramp = clamp((i - lo) / max(hi - lo, 1e-3), 0, 1).
+ * Angles are reduced exactly (64-bit fractions of a turn), so far positions
+ * keep fp32 accuracy.  inverse rotates by minus the angle (m unchanged): the
+ * gradient of the forward call.  d_rot: a multiple of 16 up to 256. */
+typedef enum { FS_ROPE_INTERLEAVED = 0, FS_ROPE_HALF = 1 } fs_rope_layout;
+typedef struct {
+    int32_t d_rot;
+    int32_t layout;      /* fs_rope_layout */
+    double base;         /* > 1 */
+    double factor;       /* >= 1; 1 = no scaling (the next three are not read) */
+    double orig_len, beta_fast, beta_slow;
+    double mscale;       /* > 0 */
+} fs_rope_desc;
+
+/* Rotates the d_rot elements at x + t x_row + h x_head of T tokens and H heads
+ * (dtype FS_BF16 or FS_F32; for a part of the head, pass the pointer of its
+ * first rotated element) into y.  pos [T] int32, any value. */
+fs_status fs_rope(const fs_rope_desc* rope, int64_t T, int32_t H, int32_t dtype, const int32_t* pos, const void* x,
+                  int64_t x_row, int64_t x_head, void* y, int64_t y_row, int64_t y_head, int32_t inverse,
+                  void* stream);
+
+/* Paged latent cache: n_pages pages of page_size token records (slot = page
+ * page_size + offset), contiguous.  A record is
+ *   FS_BF16: c (512 bf16), k_r (64 bf16): 1152 bytes;
+ *   FS_FP8:  512 E4M3 codes of c, k_r (64 bf16), the fp32 scale of c, 12 zero
+ *            bytes: 656 bytes.  c is quantised as a row of FS_FP8 (scale 2^e, e
+ *            the smallest integer with max |c_i| 2^-e <= 448, nearest even), so
+ *            a value read back is code * scale exactly.
+ * page_size >= 1; n_pages < 2^31. */
+typedef struct {
+    int64_t n_pages;
+    int32_t page_size;
+    int32_t dtype;       /* FS_BF16 or FS_FP8 */
+} fs_latent_cache;
+
+/* Bytes of the cache, 0 for an invalid desc. */
+size_t fs_latent_cache_bytes(const fs_latent_cache* desc);
+
+/* Writes T token rows c [T, 512] (row stride c_row), k_rope [T, 64] (k_row) to
+ * the records of slots [T] (int64).  rope (d_rot = 64) with pos [T] rotates the
+ * rotary key on the way; rope NULL stores it as it is.  A negative slot is a
+ * padding row and writes nothing; a slot past the cache sets the device error
+ * word (code 5) and writes nothing.  A slot given twice holds an unspecified
+ * mixture of its rows. */
+fs_status fs_latent_cache_write(const fs_latent_cache* desc, int64_t T, const void* c, int64_t c_row,
+                                const void* k_rope, int64_t k_row, const fs_rope_desc* rope, const int32_t* pos,
+                                const int64_t* slots, void* cache, void* stream);
+
+/* Reads the records of slots [T] back as bf16 rows c [T, 512], k_rope [T, 64]
+ * (the expanded form's input for an already cached prefix).  Rows with a
+ * negative slot are left as they were; a slot past the cache sets the device
+ * error word (code 5) and leaves its row. */
+fs_status fs_latent_cache_read(const fs_latent_cache* desc, const void* cache, int64_t T, const int64_t* slots,
+                               void* c, int64_t c_row, void* k_rope, int64_t k_row, void* stream);
+
+/* Absorbed latent attention of the n_q newest tokens of each of B sequences
+ * over the paged cache (which already holds them).  Query row b n_q + j, head h:
+ *   s_i = scale (q_l . c_i + q_r . k_i),  i < seq_lens[b] - (n_q - 1 - j)
+ *   out = sum_i softmax(s)_i c_i (bf16),  lse = log sum_i exp(s_i) (fp32)
+ * q_latent [B n_q, heads, 512], q_rope [B n_q, heads, 64] -> out [B n_q, heads,
+ * 512], lse [B n_q, heads] contiguous (NULL = not written).  Position i of
+ * sequence b is offset i % page_size of page block_table[b table_row + i /
+ * page_size]; the table's entries past the sequence are not read.  A row that
+ * sees no position gives out = 0, lse = -inf.  A length outside [0, max_pages
+ * page_size] (that sequence counts as empty) or a page outside [0, n_pages)
+ * (its positions are left out) sets the device error word (code 5).
+ * n_q 1 .. 16.  The length is split over the SMs and joined in a fixed order:
+ * results do not depend on timing.  ws: fs_latent_decode_ws_bytes bytes,
+ * 256-byte aligned. */
+size_t fs_latent_decode_ws_bytes(int32_t heads, int32_t B, int32_t n_q);
+fs_status fs_latent_decode(const fs_latent_cache* desc, int32_t heads, int32_t B, int32_t n_q,
+                           const fs_rows* q_latent, const fs_rows* q_rope, const void* cache,
+                           const int32_t* block_table, int32_t max_pages, int64_t table_row, const int32_t* seq_lens,
+                           float scale, const fs_rows_out* out, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Expanded latent attention over n_seqs packed sequences: sequence b has query
+ * rows [cu_q[b], cu_q[b+1]) of Tq and key rows [cu_k[b], cu_k[b+1]) of Tk
+ * (device int32 [n_seqs + 1], non-decreasing; either may be empty).  causal:
+ * the last query sees the last key (query i of lq sees keys 0 .. lk - lq + i),
+ * so more keys than queries is a cached prefix. */
+typedef struct {
+    int32_t heads, n_seqs, Tq, Tk;
+    int32_t causal;
+    float scale;
+} fs_latent_prefill_desc;
+
+/* q [Tq, heads, 192], k_nope [Tk, heads, 128], k_rope [Tk, 64] (head stride not
+ * read), v [Tk, heads, 128] -> out [Tq, heads, 128], lse [heads, Tq] fp32.  A
+ * query that sees no key gives out = 0, lse = -inf; rows outside every sequence
+ * are left as they were.  Inconsistent offsets set the device error word (code
+ * 2) and leave their sequence. */
+fs_status fs_latent_prefill(const fs_latent_prefill_desc* desc, const fs_rows* q, const fs_rows* k_nope,
+                            const fs_rows* k_rope, const fs_rows* v, const int32_t* cu_q, const int32_t* cu_k,
+                            const fs_rows_out* out, float* lse, void* stream);
+
+/* Its gradient, from the forward's out and lse and d_out [Tq, heads, 128]:
+ *   p = exp(s - lse), ds = scale p (d_out . v - <d_out, out>)
+ *   dq = sum_j ds k, dk_nope = sum_i ds q_n, dk_rope = sum over heads and i of ds q_r, dv = sum_i p d_out
+ * (p and ds enter the products as bf16, sums fp32, each gradient rounded once to
+ * bf16).  Every sum has a fixed order.  Keys that no query sees get zeros; rows
+ * outside every sequence are left as they were.  ws:
+ * fs_latent_prefill_backward_ws_bytes bytes, 256-byte aligned. */
+size_t fs_latent_prefill_backward_ws_bytes(int32_t heads, int32_t Tq, int32_t Tk);
+fs_status fs_latent_prefill_backward(const fs_latent_prefill_desc* desc, const fs_rows* q, const fs_rows* k_nope,
+                                     const fs_rows* k_rope, const fs_rows* v, const int32_t* cu_q,
+                                     const int32_t* cu_k, const fs_rows* out, const float* lse, const fs_rows* d_out,
+                                     const fs_rows_out* dq, const fs_rows_out* dk_nope, const fs_rows_out* dk_rope,
+                                     const fs_rows_out* dv, void* ws, size_t ws_bytes, void* stream);
+
 /* Read and clear the device error word (synchronises the device).  FS_OK when
  * no kernel recorded a fault; FS_ERR_DEVICE_STATE otherwise, with the raw code
  * in *code when code != NULL (1 = expert index out of range, 2 = inconsistent
- * offsets, 3 = pipeline wait timed out, 4 = size beyond a kernel limit). */
+ * offsets, 3 = pipeline wait timed out, 4 = size beyond a kernel limit, 5 = a
+ * cache slot, page or sequence length out of range). */
 fs_status fs_get_error(int32_t* code);
 
 /* Self-test of the kernels' bounded waits: one kernel waits on a barrier that

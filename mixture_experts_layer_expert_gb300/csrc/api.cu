@@ -68,6 +68,7 @@ static fs_status cuda_status(cudaError_t e) {
     std::snprintf(g_last_cuda, sizeof g_last_cuda, "%s: %s", cudaGetErrorName(e), cudaGetErrorString(e));
     return FS_ERR_CUDA;
 }
+int cuda_error_status(cudaError_t e) { return cuda_status(e); }
 
 #define FS_TRY(expr)                               \
     do {                                           \

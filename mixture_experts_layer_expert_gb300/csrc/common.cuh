@@ -20,6 +20,7 @@ enum : int {
     DEV_ERR_OFFSETS = 2,        // offsets not monotone or beyond the row capacity
     DEV_ERR_TIMEOUT = 3,        // a pipeline wait ran past its time limit
     DEV_ERR_LIMIT = 4,          // a size beyond a kernel's compiled limit
+    DEV_ERR_PAGE = 5,           // a cache slot, page number or sequence length out of range
 };
 
 // The error word lives in device memory owned by the library (api.cu); every

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -203,5 +204,63 @@ cudaError_t launch_zero(void* dst, size_t bytes, cudaStream_t st);              
 // transposed weight packs (mode 0 W13^T, 1 W3^T, 2 W3cat^T, 3 W_R^T) in the tiled layout [G][N'/256][K'/64][256][64]
 cudaError_t launch_pack_t(int mode, int G, int Np, int Kp, int c, int d, int cs, int E, const void* a, const void* b,
                           void* out, cudaStream_t st);
+
+// Records a CUDA error's text for fs_last_cuda_error (api.cu); the library status.
+int cuda_error_status(cudaError_t e);
+
+// rope.cu
+struct RopeTab;
+cudaError_t launch_rope(const RopeTab& tab, bool f32, long long T, int H, const int32_t* pos, const void* x,
+                        long long x_row, long long x_head, void* y, long long y_row, long long y_head,
+                        cudaStream_t st);
+
+// latent_cache.cu (tab nullable: the rotary key is stored as it comes)
+cudaError_t launch_cache_write(const RopeTab* tab, bool fp8, long long T, const void* c, long long c_row,
+                               const void* kr, long long kr_row, const int32_t* pos, const int64_t* slots, void* cache,
+                               long long n_slots, cudaStream_t st);
+cudaError_t launch_cache_read(bool fp8, long long T, const int64_t* slots, const void* cache, long long n_slots,
+                              void* c, long long c_row, void* kr, long long kr_row, cudaStream_t st);
+
+// latent_decode.cu: query row b n_q + j, head h (strides in elements)
+struct LatentDecodeArgs {
+    int H, B, n_q, page_size, max_pages;
+    long long n_pages, table_row;
+    const __nv_bfloat16* ql;
+    long long ql_row, ql_head;
+    const __nv_bfloat16* qr;
+    long long qr_row, qr_head;
+    const uint8_t* cache;
+    const int32_t* table;
+    const int32_t* seq_lens;
+    float scale;
+    __nv_bfloat16* out;
+    long long o_row, o_head;
+    float* lse;
+    int* err;
+};
+size_t latent_decode_ws_bytes(int H, int B, int n_q);
+cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, cudaStream_t st);
+
+// latent_prefill.cu (strides in elements); the backward reads out, lse and d_out
+struct LatentPrefillArgs {
+    int H, B, Tq, Tk, causal;
+    float scale;
+    const __nv_bfloat16 *q, *kn, *kr, *v;
+    long long q_row, q_head, kn_row, kn_head, kr_row, v_row, v_head;
+    const int32_t *cu_q, *cu_k;
+    const __nv_bfloat16* out;
+    __nv_bfloat16* out_w;
+    long long o_row, o_head;
+    const float* lse;
+    float* lse_w;
+    const __nv_bfloat16* d_out;
+    long long do_row, do_head;
+    __nv_bfloat16 *dq, *dkn, *dkr, *dv;
+    long long dq_row, dq_head, dkn_row, dkn_head, dkr_row, dv_row, dv_head;
+    int* err;
+};
+size_t latent_backward_ws_bytes(int H, int Tq, int Tk);
+cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t st);
+cudaError_t launch_latent_backward(const LatentPrefillArgs& a, void* ws, cudaStream_t st);
 
 }  // namespace fs

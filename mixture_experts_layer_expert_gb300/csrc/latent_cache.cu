@@ -1,0 +1,143 @@
+// latent_cache.cu -- writing token rows into the paged latent cache (bf16, or
+// quantised to FP8 with one power-of-two scale per token; the rotary key rotated
+// on the way) and reading records back as bf16 rows.
+//
+// Memory bound: 1,152 bytes of bf16 rows on one side, a record (1,152 or 656
+// bytes) on the other.  One warp per token: each lane holds 16 consecutive
+// latent elements, so the row maximum is one warp reduction, 16 codes leave as
+// one 16-byte store, and nothing is read twice; lanes 0-7 carry the rotary key.
+#include "kernels.h"
+#include "latent.cuh"
+
+namespace fs {
+
+// 8 elements [8l, 8l + 8) of the rotated 64-element key of lane l (l < 8).
+__device__ __forceinline__ uint4 rotate_key8(const RopeTab& tab, const __nv_bfloat16* kr, int l, int pos) {
+    const uint4 own = *reinterpret_cast<const uint4*>(kr + 8 * l);
+    const uint32_t w[4] = {own.x, own.y, own.z, own.w};
+    uint32_t o[4];
+    if (!tab.half) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 cs = rope_cs(tab, 4 * l + i, pos);
+            const float a = bf16lo(w[i]), b = bf16hi(w[i]);
+            o[i] = pack_bf16x2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
+        }
+    } else {
+        const bool first = l < 4;                // element i pairs with i + 32
+        const uint4 oth = *reinterpret_cast<const uint4*>(kr + 8 * (first ? l + 4 : l - 4));
+        const uint32_t q[4] = {oth.x, oth.y, oth.z, oth.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 c0 = rope_cs(tab, 8 * (l & 3) + 2 * i, pos), c1 = rope_cs(tab, 8 * (l & 3) + 2 * i + 1, pos);
+            const float s0 = first ? -c0.y : c0.y, s1 = first ? -c1.y : c1.y;
+            o[i] = pack_bf16x2(bf16lo(w[i]) * c0.x + bf16lo(q[i]) * s0, bf16hi(w[i]) * c1.x + bf16hi(q[i]) * s1);
+        }
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(256)
+cache_write_kernel(const __grid_constant__ RopeTab tab, long long T, const __nv_bfloat16* __restrict__ c,
+                   long long c_row, const __nv_bfloat16* __restrict__ kr, long long kr_row,
+                   const int32_t* __restrict__ pos, const int64_t* __restrict__ slots, uint8_t* __restrict__ cache,
+                   long long n_slots, int* err) {
+    const int lane = threadIdx.x & 31;
+    const long long t = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    if (t >= T) return;
+    const long long slot = __ldg(slots + t);
+    if (slot < 0) return;                        // a padding row: nothing is written
+    if (slot >= n_slots) {
+        if (lane == 0) set_dev_error(err, DEV_ERR_PAGE);
+        return;
+    }
+    uint8_t* rec = cache + slot * (FP8 ? kRecFp8 : kRecBf16);
+    const uint4* src = reinterpret_cast<const uint4*>(c + t * c_row) + 2 * lane;
+    const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
+    if (lane < 8) {
+        const __nv_bfloat16* k = kr + t * kr_row;
+        const uint4 w = pos ? rotate_key8(tab, k, lane, __ldg(pos + t)) : *reinterpret_cast<const uint4*>(k + 8 * lane);
+        *reinterpret_cast<uint4*>(rec + (FP8 ? kFp8RopeOff : 2 * kLatent) + 16 * lane) = w;
+    }
+    if constexpr (FP8) {
+        const RowQuant q = row_quant(warp_max(fmaxf(absmax_bf16x8(v0), absmax_bf16x8(v1))));
+        const uint2 a = quant_bf16x8(v0, q), b = quant_bf16x8(v1, q);
+        reinterpret_cast<uint4*>(rec)[lane] = make_uint4(a.x, a.y, b.x, b.y);
+        if (lane == 8) *reinterpret_cast<uint4*>(rec + kFp8ScaleOff) = make_uint4(__float_as_uint(q.scale), 0, 0, 0);
+    } else {
+        reinterpret_cast<uint4*>(rec)[2 * lane] = v0;
+        reinterpret_cast<uint4*>(rec)[2 * lane + 1] = v1;
+    }
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(256)
+cache_read_kernel(long long T, const int64_t* __restrict__ slots, const uint8_t* __restrict__ cache,
+                  long long n_slots, __nv_bfloat16* __restrict__ c, long long c_row, __nv_bfloat16* __restrict__ kr,
+                  long long kr_row, int* err) {
+    const int lane = threadIdx.x & 31;
+    const long long t = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    if (t >= T) return;
+    const long long slot = __ldg(slots + t);
+    if (slot < 0) return;                        // a padding row: left as it was
+    if (slot >= n_slots) {
+        if (lane == 0) set_dev_error(err, DEV_ERR_PAGE);
+        return;
+    }
+    const uint8_t* rec = cache + slot * (FP8 ? kRecFp8 : kRecBf16);
+    uint4 o0, o1;
+    if constexpr (FP8) {
+        const uint4 w = *(reinterpret_cast<const uint4*>(rec) + lane);
+        const float s = *reinterpret_cast<const float*>(rec + kFp8ScaleOff);
+        o0 = make_uint4(e4m3x2_to_bf16x2(w.x & 0xffffu, s), e4m3x2_to_bf16x2(w.x >> 16, s),
+                        e4m3x2_to_bf16x2(w.y & 0xffffu, s), e4m3x2_to_bf16x2(w.y >> 16, s));
+        o1 = make_uint4(e4m3x2_to_bf16x2(w.z & 0xffffu, s), e4m3x2_to_bf16x2(w.z >> 16, s),
+                        e4m3x2_to_bf16x2(w.w & 0xffffu, s), e4m3x2_to_bf16x2(w.w >> 16, s));
+    } else {
+        o0 = reinterpret_cast<const uint4*>(rec)[2 * lane];
+        o1 = reinterpret_cast<const uint4*>(rec)[2 * lane + 1];
+    }
+    uint4* dst = reinterpret_cast<uint4*>(c + t * c_row) + 2 * lane;
+    dst[0] = o0;
+    dst[1] = o1;
+    if (lane < 8)
+        *reinterpret_cast<uint4*>(kr + t * kr_row + 8 * lane) =
+            *reinterpret_cast<const uint4*>(rec + (FP8 ? kFp8RopeOff : 2 * kLatent) + 16 * lane);
+}
+
+cudaError_t launch_cache_write(const RopeTab* tab, bool fp8, long long T, const void* c, long long c_row,
+                               const void* kr, long long kr_row, const int32_t* pos, const int64_t* slots, void* cache,
+                               long long n_slots, cudaStream_t st) {
+    static const RopeTab none{};
+    const RopeTab& rt = tab ? *tab : none;
+    const int32_t* p = tab ? pos : nullptr;
+    const unsigned blocks = static_cast<unsigned>((T + 7) / 8);
+    auto* cc = static_cast<const __nv_bfloat16*>(c);
+    auto* kk = static_cast<const __nv_bfloat16*>(kr);
+    auto* out = static_cast<uint8_t*>(cache);
+    int* err = dev_error_ptr();
+    if (fp8)
+        cache_write_kernel<true><<<blocks, 256, 0, st>>>(rt, T, cc, c_row, kk, kr_row, p, slots, out, n_slots, err);
+    else
+        cache_write_kernel<false><<<blocks, 256, 0, st>>>(rt, T, cc, c_row, kk, kr_row, p, slots, out, n_slots, err);
+    count_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_read(bool fp8, long long T, const int64_t* slots, const void* cache, long long n_slots,
+                              void* c, long long c_row, void* kr, long long kr_row, cudaStream_t st) {
+    const unsigned blocks = static_cast<unsigned>((T + 7) / 8);
+    auto* in = static_cast<const uint8_t*>(cache);
+    auto* cc = static_cast<__nv_bfloat16*>(c);
+    auto* kk = static_cast<__nv_bfloat16*>(kr);
+    int* err = dev_error_ptr();
+    if (fp8)
+        cache_read_kernel<true><<<blocks, 256, 0, st>>>(T, slots, in, n_slots, cc, c_row, kk, kr_row, err);
+    else
+        cache_read_kernel<false><<<blocks, 256, 0, st>>>(T, slots, in, n_slots, cc, c_row, kk, kr_row, err);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace fs

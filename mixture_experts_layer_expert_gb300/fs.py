@@ -51,7 +51,25 @@ class BlockGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("dw_r", "dw1", "dw2", "dw3", "dw1_shared", "dw2_shared", "dw3_shared")]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("d_rot", ctypes.c_int32), ("layout", ctypes.c_int32)] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "orig_len", "beta_fast", "beta_slow", "mscale")]
+
+
+class LatentCache(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class LatentPrefillDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads", "n_seqs", "Tq", "Tk", "causal")] + [("scale", ctypes.c_float)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_void_p), ("row", ctypes.c_int64), ("head", ctypes.c_int64)]
+
+
 _VP, _I32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+_I64, _RP = ctypes.c_int64, ctypes.POINTER(Rows)
 _SIGS = {
     "fs_workspace_bytes": (_SZ, [ctypes.POINTER(LayerDesc), ctypes.c_int]),
     "fs_pack_w13": (_I32, [_I32, _I32, _I32, _I32, _VP, _VP, _VP, _VP]),
@@ -91,6 +109,18 @@ _SIGS = {
     "fs_mx_rows_bytes": (_SZ, [ctypes.c_int64, _I32]),
     "fs_quantize_rows_mx": (_I32, [ctypes.c_int64, _I32, _VP, _VP, _VP]),
     "fs_dispatch_rows": (ctypes.c_int64, [ctypes.POINTER(LayerDesc)]),
+    "fs_rope": (_I32, [ctypes.POINTER(RopeDesc), _I64, _I32, _I32, _VP, _VP, _I64, _I64, _VP, _I64, _I64, _I32, _VP]),
+    "fs_latent_cache_bytes": (_SZ, [ctypes.POINTER(LatentCache)]),
+    "fs_latent_cache_write": (_I32, [ctypes.POINTER(LatentCache), _I64, _VP, _I64, _VP, _I64, ctypes.POINTER(RopeDesc),
+                                     _VP, _VP, _VP, _VP]),
+    "fs_latent_cache_read": (_I32, [ctypes.POINTER(LatentCache), _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP]),
+    "fs_latent_decode_ws_bytes": (_SZ, [_I32, _I32, _I32]),
+    "fs_latent_decode": (_I32, [ctypes.POINTER(LatentCache), _I32, _I32, _I32, _RP, _RP, _VP, _VP, _I32, _I64, _VP,
+                                ctypes.c_float, _RP, _VP, _VP, _SZ, _VP]),
+    "fs_latent_prefill": (_I32, [ctypes.POINTER(LatentPrefillDesc), _RP, _RP, _RP, _RP, _VP, _VP, _RP, _VP, _VP]),
+    "fs_latent_prefill_backward_ws_bytes": (_SZ, [_I32, _I32, _I32]),
+    "fs_latent_prefill_backward": (_I32, [ctypes.POINTER(LatentPrefillDesc), _RP, _RP, _RP, _RP, _VP, _VP, _RP, _VP,
+                                          _RP, _RP, _RP, _RP, _RP, _VP, _SZ, _VP]),
     "fs_get_error": (_I32, [ctypes.POINTER(ctypes.c_int32)]),
     "fs_launch_count": (ctypes.c_uint64, []),
     "fs_selftest_wait_timeout": (_I32, [_I32, _VP]),
@@ -516,3 +546,159 @@ class FarSkipTrainer:
                                                gr, _p(self.ws_b), _nbytes(self.ws_b), _stream(stream)),
                "fs_farskip_stack_backward")
         return out, self.grads
+
+
+# ----------------------------------------------------------------- attention
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+LATENT, ROPE_DIM, NOPE_DIM, V_DIM = 512, 64, 128, 128      # widths of the latent-attention operators
+LATENT_RECORD = {"bf16": 2 * (LATENT + ROPE_DIM), "fp8": LATENT + 2 * ROPE_DIM + 16}      # bytes per cached token
+
+
+def _operand(what: str, t: torch.Tensor, shape, dtype=torch.bfloat16, strided=True):
+    """Refuse a tensor whose shape, type, inner stride or device the call could not take:
+    the C entry sees only a pointer."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise FsError(1, what, "got %s %s, expected %s %s" % (tuple(t.shape), t.dtype, tuple(shape), dtype))
+    if (t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1) or (not strided and not t.is_contiguous()):
+        raise FsError(1, what, "strides %s" % (t.stride(),))
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise FsError(1, what, "tensor on %s, not on the current device" % t.device)
+
+
+def _rows(t: torch.Tensor) -> Rows:
+    """[rows, heads, width] or [rows, width] -> (pointer, row stride, head stride)."""
+    return Rows(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0)
+
+
+def make_rope(d_rot: int, layout: str = "interleaved", base: float = 10000.0, factor: float = 1.0,
+              orig_len: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0, mscale: float = 1.0) -> RopeDesc:
+    return RopeDesc(d_rot, ROPE_LAYOUTS[layout], base, factor, orig_len, beta_fast, beta_slow, mscale)
+
+
+def fs_rope(rope: RopeDesc, pos, x, y, inverse: bool = False, stream=None):
+    """Rotate x [T, H, d_rot] (a view of the rotated part of each head) into y (which may be x)."""
+    T, H = x.shape[0], x.shape[1]
+    dt = torch.float32 if x.dtype == torch.float32 else torch.bfloat16
+    _operand("fs_rope x", x, (T, H, rope.d_rot), dt)
+    _operand("fs_rope y", y, (T, H, rope.d_rot), dt)
+    _operand("fs_rope pos", pos, (T,), torch.int32)
+    _check(lib().fs_rope(ctypes.byref(rope), T, H, _dtype_code(x), _p(pos), _p(x), x.stride(0), x.stride(1), _p(y),
+                         y.stride(0), y.stride(1), int(inverse), _stream(stream)), "fs_rope")
+
+
+def make_latent_cache(n_pages: int, page_size: int, dtype: str = "bf16") -> LatentCache:
+    return LatentCache(n_pages, page_size, DTYPES[dtype])
+
+
+def fs_latent_cache_bytes(desc: LatentCache) -> int:
+    return int(lib().fs_latent_cache_bytes(ctypes.byref(desc)))
+
+
+def latent_cache_empty(desc: LatentCache, device="cuda") -> torch.Tensor:
+    """A cache tensor: [n_pages, page_size, 576] bf16, or [n_pages, page_size, 656] bytes for FP8."""
+    if fs_latent_cache_bytes(desc) == 0:
+        raise FsError(1, "fs_latent_cache_bytes")
+    if desc.dtype == FS_BF16:
+        return torch.empty((desc.n_pages, desc.page_size, LATENT + ROPE_DIM), dtype=torch.bfloat16, device=device)
+    return torch.empty((desc.n_pages, desc.page_size, LATENT_RECORD["fp8"]), dtype=torch.uint8, device=device)
+
+
+def _cache_operand(what, desc, cache):
+    f8 = desc.dtype == FS_FP8
+    _operand(what, cache, (desc.n_pages, desc.page_size, LATENT_RECORD["fp8"] if f8 else LATENT + ROPE_DIM),
+             torch.uint8 if f8 else torch.bfloat16, strided=False)
+
+
+def fs_latent_cache_write(desc: LatentCache, c, k_rope, slots, cache, rope: RopeDesc | None = None, pos=None,
+                          stream=None):
+    """Write c [T, 512], k_rope [T, 64] (rotated by rope at pos when given) to the slots [T] (int64; negative: skipped)."""
+    T, what = c.shape[0], "fs_latent_cache_write"
+    _operand(what + " c", c, (T, LATENT))
+    _operand(what + " k_rope", k_rope, (T, ROPE_DIM))
+    _operand(what + " slots", slots, (T,), torch.int64)
+    _cache_operand(what + " cache", desc, cache)
+    if pos is not None:
+        _operand(what + " pos", pos, (T,), torch.int32)
+    _check(lib().fs_latent_cache_write(ctypes.byref(desc), T, _p(c), c.stride(0), _p(k_rope), k_rope.stride(0),
+                                       None if rope is None else ctypes.byref(rope), _p(pos), _p(slots), _p(cache),
+                                       _stream(stream)), what)
+
+
+def fs_latent_cache_read(desc: LatentCache, cache, slots, c, k_rope, stream=None):
+    """Read the records of slots [T] back into c [T, 512], k_rope [T, 64] (rows with a negative slot are left)."""
+    T, what = slots.shape[0], "fs_latent_cache_read"
+    _operand(what + " slots", slots, (T,), torch.int64)
+    _operand(what + " c", c, (T, LATENT))
+    _operand(what + " k_rope", k_rope, (T, ROPE_DIM))
+    _cache_operand(what + " cache", desc, cache)
+    _check(lib().fs_latent_cache_read(ctypes.byref(desc), _p(cache), T, _p(slots), _p(c), c.stride(0), _p(k_rope),
+                                      k_rope.stride(0), _stream(stream)), what)
+
+
+def fs_latent_decode_ws_bytes(heads: int, B: int, n_q: int = 1) -> int:
+    return int(lib().fs_latent_decode_ws_bytes(heads, B, n_q))
+
+
+def fs_latent_decode(desc: LatentCache, q_latent, q_rope, cache, block_table, seq_lens, scale, out, lse, ws,
+                     stream=None):
+    """Absorbed attention of the newest n_q tokens of B sequences: q_latent [B n_q, H, 512], q_rope [B n_q, H, 64],
+    block_table [B, max_pages] int32, seq_lens [B] int32 -> out [B n_q, H, 512], lse [B n_q, H] (or None);
+    ws: fs_latent_decode_ws_bytes(H, B, n_q) bytes."""
+    what, (rows, H) = "fs_latent_decode", q_latent.shape[:2]
+    B, max_pages = block_table.shape
+    n_q = rows // max(B, 1)
+    _operand(what + " q_latent", q_latent, (B * n_q, H, LATENT))
+    _operand(what + " q_rope", q_rope, (B * n_q, H, ROPE_DIM))
+    _operand(what + " out", out, (B * n_q, H, LATENT))
+    _operand(what + " block_table", block_table, (B, max_pages), torch.int32)
+    _operand(what + " seq_lens", seq_lens, (B,), torch.int32)
+    _cache_operand(what + " cache", desc, cache)
+    if lse is not None:
+        _operand(what + " lse", lse, (B * n_q, H), torch.float32, strided=False)
+    _check(lib().fs_latent_decode(ctypes.byref(desc), H, B, n_q, _rows(q_latent), _rows(q_rope), _p(cache),
+                                  _p(block_table), max_pages, block_table.stride(0), _p(seq_lens), scale, _rows(out),
+                                  _p(lse), _p(ws), _nbytes(ws), _stream(stream)), what)
+
+
+def _prefill_operands(what, q, k_nope, k_rope, v, cu_q, cu_k, causal, scale) -> LatentPrefillDesc:
+    (Tq, H), Tk, B = q.shape[:2], k_rope.shape[0], cu_q.shape[0] - 1
+    _operand(what + " q", q, (Tq, H, NOPE_DIM + ROPE_DIM))
+    _operand(what + " k_nope", k_nope, (Tk, H, NOPE_DIM))
+    _operand(what + " k_rope", k_rope, (Tk, ROPE_DIM))
+    _operand(what + " v", v, (Tk, H, V_DIM))
+    _operand(what + " cu_q", cu_q, (B + 1,), torch.int32)
+    _operand(what + " cu_k", cu_k, (B + 1,), torch.int32)
+    return LatentPrefillDesc(H, B, Tq, Tk, int(causal), scale)
+
+
+def fs_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, causal, scale, out, lse, stream=None):
+    """Expanded attention over packed sequences: q [Tq, H, 192], k_nope and v [Tk, H, 128], k_rope [Tk, 64],
+    cu_q and cu_k [B + 1] int32 -> out [Tq, H, 128], lse [H, Tq] fp32."""
+    what = "fs_latent_prefill"
+    d = _prefill_operands(what, q, k_nope, k_rope, v, cu_q, cu_k, causal, scale)
+    _operand(what + " out", out, (d.Tq, d.heads, V_DIM))
+    _operand(what + " lse", lse, (d.heads, d.Tq), torch.float32, strided=False)
+    _check(lib().fs_latent_prefill(ctypes.byref(d), _rows(q), _rows(k_nope), _rows(k_rope), _rows(v), _p(cu_q),
+                                   _p(cu_k), _rows(out), _p(lse), _stream(stream)), what)
+
+
+def fs_latent_prefill_backward_ws_bytes(heads: int, Tq: int, Tk: int) -> int:
+    return int(lib().fs_latent_prefill_backward_ws_bytes(heads, Tq, Tk))
+
+
+def fs_latent_prefill_backward(q, k_nope, k_rope, v, cu_q, cu_k, causal, scale, out, lse, d_out, dq, dk_nope, dk_rope,
+                               dv, ws, stream=None):
+    """Gradient of fs_latent_prefill from its out and lse: dq, dk_nope, dk_rope (summed over the heads), dv in the
+    inputs' shapes; ws: fs_latent_prefill_backward_ws_bytes(H, Tq, Tk) bytes."""
+    what = "fs_latent_prefill_backward"
+    d = _prefill_operands(what, q, k_nope, k_rope, v, cu_q, cu_k, causal, scale)
+    _operand(what + " out", out, (d.Tq, d.heads, V_DIM))
+    _operand(what + " d_out", d_out, (d.Tq, d.heads, V_DIM))
+    _operand(what + " lse", lse, (d.heads, d.Tq), torch.float32, strided=False)
+    for name, g, like in (("dq", dq, q), ("dk_nope", dk_nope, k_nope), ("dk_rope", dk_rope, k_rope), ("dv", dv, v)):
+        _operand(what + " " + name, g, like.shape)
+    _check(lib().fs_latent_prefill_backward(ctypes.byref(d), _rows(q), _rows(k_nope), _rows(k_rope), _rows(v),
+                                            _p(cu_q), _p(cu_k), _rows(out), _p(lse), _rows(d_out), _rows(dq),
+                                            _rows(dk_nope), _rows(dk_rope), _rows(dv), _p(ws), _nbytes(ws),
+                                            _stream(stream)), what)
