@@ -107,6 +107,8 @@ bool tc_up_pair();
 // pieces (64-byte swizzle).  num_sms: SMs of the current device.
 cudaError_t make_map(CUtensorMap* m, const void* base, long long rows, long long cols, int box_rows, bool f8 = false);
 cudaError_t make_map_blocked(CUtensorMap* m, const void* base, long long nblocks, int box_rows, bool f8 = false);
+cudaError_t make_map_rows(CUtensorMap* m, const void* base, long long rows, int heads, int width, long long row,
+                          long long head, int box_rows);
 cudaError_t make_out_map_bf16(CUtensorMap* m, void* base, long long rows, long long cols, long long ldo);
 cudaError_t num_sms(int* out);
 // Raise fn's dynamic shared memory limit to `bytes` on the current device, once

@@ -59,4 +59,57 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes16, float sca
     return pack_bf16x2(f.x * scale, f.y * scale);
 }
 
+// One packed sequence: query rows [q0, q0 + lq), key rows [k0, k0 + lk).
+struct PackedSeq {
+    int q0, lq, k0, lk;
+};
+
+// Whole warp: the sequence and the tile inside it of row tile `tile` (tiles of
+// `rows` rows; by_key: of the key rows, else of the query rows), sequences in
+// order.  Returns the tile's index in its sequence, or -1 past the last tile.
+// Inconsistent offsets (decreasing, or outside [0, Tq] / [0, Tk]) record an
+// error and count as an empty sequence.
+__device__ __forceinline__ int find_tile(const int32_t* cu_q, const int32_t* cu_k, int B, int Tq, int Tk, int rows,
+                                         bool by_key, int tile, int* err, PackedSeq* out) {
+    const int lane = threadIdx.x & 31;
+    int before = 0;
+    for (int b0 = 0; b0 < B; b0 += 32) {
+        const int b = b0 + lane;
+        PackedSeq s{0, 0, 0, 0};
+        if (b < B) {
+            const int qa = __ldg(cu_q + b), qb = __ldg(cu_q + b + 1), ka = __ldg(cu_k + b), kb = __ldg(cu_k + b + 1);
+            if (qa < 0 || qb < qa || qb > Tq || ka < 0 || kb < ka || kb > Tk)
+                set_dev_error(err, DEV_ERR_OFFSETS);
+            else
+                s = PackedSeq{qa, qb - qa, ka, kb - ka};
+        }
+        const int n = ((by_key ? s.lk : s.lq) + rows - 1) / rows;
+        int end = n;                                         // inclusive prefix sum over the lanes
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, end, d);
+            if (lane >= d) end += v;
+        }
+        end += before;
+        const unsigned past = __ballot_sync(0xffffffffu, end > tile);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            out->q0 = __shfl_sync(0xffffffffu, s.q0, l);
+            out->lq = __shfl_sync(0xffffffffu, s.lq, l);
+            out->k0 = __shfl_sync(0xffffffffu, s.k0, l);
+            out->lk = __shfl_sync(0xffffffffu, s.lk, l);
+            return tile - __shfl_sync(0xffffffffu, end - n, l);
+        }
+        before = __shfl_sync(0xffffffffu, end, 31);
+    }
+    return -1;
+}
+
+// 2^x (x <= 0 here up to rounding): one hardware operation, relative error about 2^-22.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 }  // namespace fs

@@ -1,170 +1,459 @@
-// latent_prefill.cu -- expanded latent attention over packed sequences, and its
-// gradient:
+// latent_prefill.cu -- expanded latent attention over packed sequences:
 //   s_ij = scale (q_n,i . k_n,j + q_r,i . k_r,j),  out_i = sum_j softmax(s_i)_j v_j,  lse_i = log sum_j exp(s_ij)
-//   p = exp(s - lse), dp = d_out . v, ds = scale p (dp - <d_out, out>)
-//   dq = sum_j ds k, dk_n = sum_i ds q_n, dk_r = sum_heads sum_i ds q_r, dv = sum_i p d_out
+//
+// One pass over the keys with a running maximum M and sum l per query row, on
+// the tensor cores.  A work item is 256 query rows of one head, as two tiles of
+// 128 (t = 0, 1); keys come in tiles of 128:
+//   S_t = Q_t K^T     128 x 128 x 192, operands in shared memory, S in TMEM
+//   P_t = 2^(S_t scale log2 e - M), bf16, back into S_t's TMEM columns
+//   O_t += P_t V      128 x 128 x 128, P from TMEM, V read MN-major where TMA left it
+// TMEM: S_0, S_1, O_0, O_1, 128 columns each.  While one tile's softmax runs on
+// its four warps, the other tile's MMAs run, so the tensor cores see a stream
+// of S_0(i+1), PV_1(i), S_1(i+1), PV_0(i+1), ...: MMAs of one thread execute in
+// issue order, so S_t(i+1) may overwrite P_t(i) right behind PV_t(i).
+// O is rescaled only when a row's maximum grows by more than 8 (a factor 2^8):
+// P then stays below 2^8, which costs no precision in bf16 or fp32, and the
+// TMEM round trip of O is rare after a sequence's first tiles.
+//
+// Bound: 2 x 128 x 128 x 320 flops per key tile and query tile; q, k, v and out
+// are a few bytes per thousand flops.  Exponentials, 128 x 128 per tile, take
+// less issue time than the tile's MMAs.
+//
+// Warps 0-3 / 4-7: softmax and output of tile 0 / 1 (thread = row = TMEM lane);
+// warp 8: work distribution and TMA loads; warp 9: MMA issue.  K, V and the
+// shared rotary key go through a ring of eight 16 KB units (128 rows x 64
+// columns): three of K (two of k_n, one of k_r), two of V per key tile.
+// Blocks take further items from the grid's not yet started blocks (cluster
+// launch control), so the next item's loads overlap this item's last tiles, and
+// items are numbered with the longest key range of each sequence first.
 #include <math_constants.h>
 
 #include "kernels.h"
 #include "latent.cuh"
 
 namespace fs {
+namespace pf {
 
-// Sequence of packed row t: cu[b] <= t < cu[b + 1]; -1 past the last one.
-__device__ __forceinline__ int seq_of(const int32_t* cu, int B, int t) {
-    if (t < cu[0] || t >= cu[B]) return -1;
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= t) lo = mid; else hi = mid;
-    }
-    return lo;
-}
+constexpr int TQ = 128, TK = 128;
+constexpr int UNIT = 128 * 64 * 2;              // 16 KB
+constexpr int NU = 8;                           // ring units
+constexpr int Q_UNITS = 6;                      // two tiles x 192 columns
+constexpr int RING_OFF = Q_UNITS * UNIT;
+constexpr int BAR_OFF = RING_OFF + NU * UNIT;
+constexpr int THREADS = 320;
+constexpr size_t SMEM = 1024 + BAR_OFF + 512;
+constexpr float kRescale = 8.0f;                // log2 of the growth of the maximum that rescales O
 
-struct Seq { int q0, q1, k0, k1; bool ok; };
-__device__ __forceinline__ Seq seq_at(const LatentPrefillArgs& a, int b) {
-    Seq s{a.cu_q[b], a.cu_q[b + 1], a.cu_k[b], a.cu_k[b + 1], true};
-    s.ok = s.q0 >= 0 && s.q1 >= s.q0 && s.q1 <= a.Tq && s.k0 >= 0 && s.k1 >= s.k0 && s.k1 <= a.Tk;
-    if (!s.ok) set_dev_error(a.err, DEV_ERR_OFFSETS);
-    return s;
-}
+struct Item {
+    int valid;            // 1: work, 0: nothing to do for this number, -1: no more items
+    int head, row0, rows; // first query row, rows of the item (1 .. 256)
+    int k0, lk;           // first key row, keys
+    int off;              // lk - lq + (first row's index in its sequence): row r sees keys < off + r + 1 (causal)
+    int n[2];             // key tiles of each query tile
+};
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-    return v;
-}
-template <int N>
-__device__ __forceinline__ void ld_bf16(float (&v)[N], const __nv_bfloat16* p) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __bfloat162float(p[i]);
-}
-template <int N>
-__device__ __forceinline__ float dot(const float (&x)[N], const float (&y)[N]) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += x[i] * y[i];
-    return s;
-}
-template <int N>
-__device__ __forceinline__ void st_bf16(__nv_bfloat16* p, const float (&v)[N]) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = __float2bfloat16(v[i]);
+struct Shared {
+    uint64_t full[NU], empty[NU], q_full, q_empty, s_full[2], p_full[2], pv_done[2], item_full[2], item_empty[2];
+    uint64_t next_bar, fin;
+    alignas(16) uint32_t next_resp[4];
+    uint32_t tmem;
+    int abort_flag;
+    Item item[2];
+};
+static_assert(sizeof(Shared) <= 512, "barrier area");
+
+__device__ __forceinline__ int row_limit(const Item& it, bool causal, int r) {
+    return causal ? min(it.lk, it.off + r + 1) : it.lk;
 }
 
-// One warp per (query, head): out and lse (BWD = false) or dq (BWD = true).
-// Lane l holds elements 4 l .. 4 l + 3 of the unrotated part and of v, 2 l and 2 l + 1 of the rotary part.
-template <bool BWD>
-__global__ void __launch_bounds__(128) prefill_query_kernel(LatentPrefillArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long w = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (w >= static_cast<long long>(a.Tq) * a.H) return;
-    const int t = static_cast<int>(w / a.H), h = static_cast<int>(w % a.H);
-    const int b = seq_of(a.cu_q, a.B, t);
-    if (b < 0) return;
-    const Seq s = seq_at(a, b);
-    if (!s.ok) return;
-    const int end = a.causal ? min(s.k1, s.k1 - (s.q1 - t) + 1) : s.k1;
-    float qn[4], qr[2], acc[4] = {}, accr[2] = {}, dO[4] = {};
-    const __nv_bfloat16* q = a.q + t * a.q_row + h * a.q_head;
-    ld_bf16(qn, q + 4 * lane);
-    ld_bf16(qr, q + kNope + 2 * lane);
-    float m = -CUDART_INF_F, z = 0.f, lse = 0.f, delta = 0.f;
-    if constexpr (BWD) {
-        float o[4];
-        ld_bf16(dO, a.d_out + t * a.do_row + h * a.do_head + 4 * lane);
-        ld_bf16(o, a.out + t * a.o_row + h * a.o_head + 4 * lane);
-        delta = warp_sum(dot(dO, o));
-        lse = a.lse[static_cast<long long>(h) * a.Tq + t];
-    }
-    for (int j = s.k0; j < end; ++j) {
-        float kn[4], kr[2], v[4];
-        ld_bf16(kn, a.kn + j * a.kn_row + h * a.kn_head + 4 * lane);
-        ld_bf16(kr, a.kr + j * a.kr_row + 2 * lane);
-        ld_bf16(v, a.v + j * a.v_row + h * a.v_head + 4 * lane);
-        const float x = warp_sum(dot(qn, kn) + dot(qr, kr)) * a.scale;
-        if constexpr (BWD) {
-            const float ds = __expf(x - lse) * (warp_sum(dot(dO, v)) - delta) * a.scale;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] += ds * kn[i];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) accr[i] += ds * kr[i];
-        } else {
-            const float mn = fmaxf(m, x);
-            if (mn == -CUDART_INF_F) continue;
-            const float al = __expf(m - mn), p = __expf(x - mn);
-            z = z * al + p;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[i] = acc[i] * al + p * v[i];
-            m = mn;
+// Softmax of one query tile: the calling thread owns row r of the item (TMEM lane r & 127).
+struct RowState {
+    float m, l;           // running maximum (log2 units, scaled), sum of 2^(s - m)
+};
+
+__global__ void __launch_bounds__(THREADS, 1)
+prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKn,
+               const __grid_constant__ CUtensorMap tmKr, const __grid_constant__ CUtensorMap tmV,
+               const LatentPrefillArgs a, const int max_tiles) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Shared& sh = *reinterpret_cast<Shared*>(smem + BAR_OFF);
+    volatile int* abort_flag = &sh.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NU; ++i) { mbar_init(smem_u32(&sh.full[i]), 1); mbar_init(smem_u32(&sh.empty[i]), 1); }
+        mbar_init(smem_u32(&sh.q_full), 1);
+        mbar_init(smem_u32(&sh.q_empty), 1);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&sh.s_full[t]), 1);
+            mbar_init(smem_u32(&sh.p_full[t]), 128);
+            mbar_init(smem_u32(&sh.pv_done[t]), 1);
+            mbar_init(smem_u32(&sh.item_full[t]), 1);
+            mbar_init(smem_u32(&sh.item_empty[t]), 9);
         }
+        mbar_init(smem_u32(&sh.next_bar), 1);
+        mbar_init(smem_u32(&sh.fin), 1);
+        sh.abort_flag = 0;
+        fence_mbar_init();
     }
-    if constexpr (BWD) {
-        __nv_bfloat16* d = a.dq + t * a.dq_row + h * a.dq_head;
-        st_bf16(d + 4 * lane, acc);
-        st_bf16(d + kNope + 2 * lane, accr);
+    if (warp == 9) {
+        tmem_alloc(smem_u32(&sh.tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm_s = sh.tmem, tm_o = sh.tmem + 256;      // S_t at 128 t, O_t at 256 + 128 t
+
+    if (warp == 8) {
+        // ------------------------------------------------ items and loads
+        if (lane == 0) {
+            tma_prefetch_desc(&tmQ); tma_prefetch_desc(&tmKn); tma_prefetch_desc(&tmKr); tma_prefetch_desc(&tmV);
+        }
+        uint32_t u = 0;               // units loaded so far
+        uint32_t nq = 0;              // Q loads so far
+        int id = blockIdx.x;
+        bool ok = true;
+        uint32_t k = 0;
+        for (; ok; ++k) {
+            const uint32_t slot = k & 1, use = k >> 1;
+            if (lane == 0 && id >= 0) {
+                mbar_arrive_expect_tx(smem_u32(&sh.next_bar), 16);
+                next_block_request(smem_u32(sh.next_resp), smem_u32(&sh.next_bar));
+            }
+            Item it{};
+            it.valid = id < 0 ? -1 : 0;
+            if (id >= 0) {
+                it.head = id / max_tiles;
+                // counted from the back: the last tiles of a sequence have the longest key ranges
+                PackedSeq s;
+                const int tile = find_tile(a.cu_q, a.cu_k, a.B, a.Tq, a.Tk, 2 * TQ, false,
+                                           max_tiles - 1 - (id - it.head * max_tiles), a.err, &s);
+                if (tile >= 0) {
+                    it.valid = 1;
+                    it.row0 = s.q0 + tile * 2 * TQ;
+                    it.rows = min(2 * TQ, s.lq - tile * 2 * TQ);
+                    it.k0 = s.k0;
+                    it.lk = s.lk;
+                    it.off = s.lk - s.lq + tile * 2 * TQ;
+                    for (int t = 0; t < 2; ++t) {
+                        const int last = min(it.rows, TQ * (t + 1)) - 1;
+                        it.n[t] = last < TQ * t ? 0 : (max(0, row_limit(it, a.causal, last)) + TK - 1) / TK;
+                    }
+                }
+            }
+            if (lane == 0) ok = mbar_wait(smem_u32(&sh.item_empty[slot]), (use & 1) ^ 1, abort_flag, a.err);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if (lane == 0) {
+                sh.item[slot] = it;
+                mbar_arrive(smem_u32(&sh.item_full[slot]));
+            }
+            if (id < 0) break;
+            const int n = max(it.n[0], it.n[1]);
+            if (it.valid == 1 && n > 0 && lane == 0) {
+                ok = mbar_wait(smem_u32(&sh.q_empty), (nq & 1) ^ 1, abort_flag, a.err);
+                if (ok) {
+                    ++nq;
+                    const uint32_t fb = smem_u32(&sh.q_full);
+                    const int tiles = it.rows > TQ ? 2 : 1;
+                    mbar_arrive_expect_tx(fb, tiles * 3 * UNIT);
+                    for (int t = 0; t < tiles; ++t)
+                        for (int c = 0; c < 3; ++c)
+                            tma_load_3d(smem_u32(smem + (3 * t + c) * UNIT), &tmQ, fb, 64 * c, it.head,
+                                        it.row0 + TQ * t);
+                }
+                for (int i = 0; ok && i < n; ++i) {
+                    const int row = it.k0 + TK * i;
+                    for (int c = 0; c < 5; ++c, ++u) {
+                        const uint32_t s = u % NU, fb = smem_u32(&sh.full[s]);
+                        ok = mbar_wait(smem_u32(&sh.empty[s]), ((u / NU) & 1) ^ 1, abort_flag, a.err);
+                        if (!ok) break;
+                        const uint32_t dst = smem_u32(smem + RING_OFF + s * UNIT);
+                        mbar_arrive_expect_tx(fb, UNIT);
+                        if (c < 2) tma_load_3d(dst, &tmKn, fb, 64 * c, it.head, row);
+                        else if (c == 2) tma_load_3d(dst, &tmKr, fb, 0, 0, row);
+                        else tma_load_3d(dst, &tmV, fb, 64 * (c - 3), it.head, row);
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            if (lane == 0) {
+                ok = mbar_wait(smem_u32(&sh.next_bar), k & 1, abort_flag, a.err);
+                if (ok) id = next_block_answer(smem_u32(sh.next_resp));
+                fence_proxy_async_smem();        // the answer is read before the next one may be written
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            id = __shfl_sync(0xffffffffu, id, 0);
+        }
+        if (lane == 0) {
+            // the loads in flight land before the block exits
+            const uint32_t pend = u < NU ? u : NU;
+            for (uint32_t j = 1; j <= pend; ++j) {
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(smem_u32(&sh.full[(u - j) % NU]), ((u - j) / NU) & 1))
+                    if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(a.err, DEV_ERR_TIMEOUT); break; }
+            }
+            if (nq > 0) {
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(smem_u32(&sh.q_full), (nq - 1) & 1))
+                    if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(a.err, DEV_ERR_TIMEOUT); break; }
+            }
+            if (!ok) {                           // an answer may still be on its way
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(smem_u32(&sh.next_bar), k & 1))
+                    if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ MMA
+        constexpr uint32_t id_s = idesc_bf16_f32(TQ, TK), id_o = idesc_bf16_f32_t(TQ, kDv, 0, 1);
+        uint32_t u = 0, nq = 0, np[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (lane == 0) ok = mbar_wait(smem_u32(bar), parity, abort_flag, a.err);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            return ok;
+        };
+        auto score = [&](int t, uint32_t u0) {          // S_t = Q_t K^T from units u0 .. u0 + 2
+            if (lane == 0) {
+                tc_fence_after();
+                for (int c = 0; c < 3; ++c) {
+                    const uint64_t ad = smem_desc_sw128(smem_u32(smem + (3 * t + c) * UNIT));
+                    const uint64_t bd = smem_desc_sw128(smem_u32(smem + RING_OFF + ((u0 + c) % NU) * UNIT));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_bf16(tm_s + 128 * t, ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || kk > 0);
+                }
+                tc_commit(smem_u32(&sh.s_full[t]));
+            }
+            __syncwarp();
+        };
+        auto release = [&](uint32_t u0, int n) {
+            if (lane == 0)
+                for (int c = 0; c < n; ++c) tc_commit(smem_u32(&sh.empty[(u0 + c) % NU]));
+            __syncwarp();
+        };
+        for (uint32_t k = 0;; ++k) {
+            const uint32_t slot = k & 1;
+            if (!wait(&sh.item_full[slot], (k >> 1) & 1)) break;
+            const Item it = sh.item[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[slot]));
+            if (it.valid < 0) break;
+            const int n = max(it.n[0], it.n[1]);
+            if (it.valid == 0 || n == 0) continue;
+            if (!wait(&sh.q_full, nq++ & 1)) break;
+            auto wait_units = [&](uint32_t u0, int cnt) {
+                for (int c = 0; c < cnt && ok; ++c) wait(&sh.full[(u0 + c) % NU], ((u0 + c) / NU) & 1);
+                return ok;
+            };
+            if (!wait_units(u, 3)) break;
+            for (int t = 0; t < 2; ++t)
+                if (it.n[t] > 0) score(t, u);
+            release(u, 3);
+            for (int i = 0; i < n; ++i) {
+                const uint32_t uv = u + 3, uk = u + 5;        // V of tile i, K of tile i + 1
+                if (!wait_units(uv, 2)) break;
+                // rows past the sequence's last key: p there is zero, but what lies in V's rows need not be finite
+                const int keys = min(TK, it.lk - TK * i), steps = (keys + 15) >> 4, zrows = 16 * steps - keys;
+                if (zrows > 0) {
+                    for (int c = 0; c < 2; ++c) {
+                        // every lane sees the unit complete before writing into it
+                        if (!mbar_wait(smem_u32(&sh.full[(uv + c) % NU]), ((uv + c) / NU) & 1, abort_flag, a.err)) continue;
+                        uint8_t* un = smem + RING_OFF + ((uv + c) % NU) * UNIT;
+                        for (int z = lane; z < zrows * 8; z += 32)
+                            *reinterpret_cast<uint4*>(un + keys * 128 + z * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                for (int t = 0; t < 2; ++t) {
+                    if (i < it.n[t]) {
+                        if (!wait(&sh.p_full[t], np[t]++ & 1)) break;
+                        if (lane == 0) {
+                            tc_fence_after();
+                            for (int kk = 0; kk < steps; ++kk) {
+                                const uint32_t base = smem_u32(smem + RING_OFF);
+                                const uint32_t v0 = base + (uv % NU) * UNIT, v1 = base + ((uv + 1) % NU) * UNIT;
+                                // V's two 64-column halves are two ring units: one N = 128 product, or two of 64
+                                // when they wrap around the ring's end
+                                constexpr uint32_t id_h = idesc_bf16_f32_t(TQ, 64, 0, 1);
+                                const uint32_t acc = i > 0 || kk > 0;
+                                if (v1 == v0 + UNIT) {
+                                    tc_mma_bf16_ts(tm_o + 128 * t, tm_s + 128 * t + 8 * kk,
+                                                   smem_desc_sw128_mn(v0 + 2048 * kk, UNIT), id_o, acc);
+                                } else {
+                                    tc_mma_bf16_ts(tm_o + 128 * t, tm_s + 128 * t + 8 * kk,
+                                                   smem_desc_sw128_mn(v0 + 2048 * kk, UNIT), id_h, acc);
+                                    tc_mma_bf16_ts(tm_o + 128 * t + 64, tm_s + 128 * t + 8 * kk,
+                                                   smem_desc_sw128_mn(v1 + 2048 * kk, UNIT), id_h, acc);
+                                }
+                            }
+                            tc_commit(smem_u32(&sh.pv_done[t]));
+                        }
+                        __syncwarp();
+                    }
+                    if (t == 0 && i + 1 < n && !wait_units(uk, 3)) break;
+                    if (t == 1) release(uv, 2);
+                    if (i + 1 < it.n[t]) score(t, uk);
+                }
+                if (!ok) break;
+                if (i + 1 < n) release(uk, 3);
+                u += 5;
+            }
+            if (!ok) break;
+            if (lane == 0) tc_commit(smem_u32(&sh.q_empty));
+            __syncwarp();
+        }
+        if (lane == 0) {
+            tc_commit(smem_u32(&sh.fin));          // every MMA completes before TMEM is released
+            const uint64_t t0 = globaltimer_ns();
+            while (!mbar_try_wait(smem_u32(&sh.fin), 0))
+                if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(a.err, DEV_ERR_TIMEOUT); break; }
+        }
+        __syncwarp();
     } else {
-        const float inv = z > 0.f ? 1.f / z : 0.f;
+        // ------------------------------------------- softmax and output of tile t
+        const int t = warp >> 2;
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tm_s + 128 * t + lane_base, to = tm_o + 128 * t + lane_base;
+        const int r = 128 * t + 32 * (warp & 3) + lane;
+        const float c = a.scale * 1.4426950408889634f;
+        uint32_t ns = 0, npv = 0;
+        bool ok = true;
+        for (uint32_t k = 0; ok; ++k) {
+            const uint32_t slot = k & 1;
+            if (!mbar_wait(smem_u32(&sh.item_full[slot]), (k >> 1) & 1, abort_flag, a.err)) break;
+            const Item it = sh.item[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[slot]));
+            if (it.valid < 0) break;
+            if (it.valid == 0 || 128 * t >= it.rows) continue;
+            const int limit = row_limit(it, a.causal, r);
+            float m = 0.f, l = 0.f;
+            for (int i = 0; i < it.n[t]; ++i) {
+                if (!mbar_wait(smem_u32(&sh.s_full[t]), ns++ & 1, abort_flag, a.err)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t s[4][32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] *= inv;
-        st_bf16(a.out_w + t * a.o_row + h * a.o_head + 4 * lane, acc);
-        if (lane == 0) a.lse_w[static_cast<long long>(h) * a.Tq + t] = m + logf(z);
-    }
-}
-
-// One warp per key: for every head, dk_n and dv; dk_r summed over the heads in order.
-__global__ void __launch_bounds__(128) prefill_key_kernel(LatentPrefillArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long j = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (j >= a.Tk) return;
-    const int b = seq_of(a.cu_k, a.B, static_cast<int>(j));
-    if (b < 0) return;
-    const Seq s = seq_at(a, b);
-    if (!s.ok) return;
-    float kr[2], dkr[2] = {};
-    ld_bf16(kr, a.kr + j * a.kr_row + 2 * lane);
-    const int first = a.causal ? max(s.q0, s.q1 - (s.k1 - static_cast<int>(j))) : s.q0;
-    for (int h = 0; h < a.H; ++h) {
-        float kn[4], v[4], dkn[4] = {}, dv[4] = {};
-        ld_bf16(kn, a.kn + j * a.kn_row + h * a.kn_head + 4 * lane);
-        ld_bf16(v, a.v + j * a.v_row + h * a.v_head + 4 * lane);
-        for (int t = first; t < s.q1; ++t) {
-            float qn[4], qr[2], dO[4], o[4];
-            const __nv_bfloat16* q = a.q + t * a.q_row + h * a.q_head;
-            ld_bf16(qn, q + 4 * lane);
-            ld_bf16(qr, q + kNope + 2 * lane);
-            ld_bf16(dO, a.d_out + t * a.do_row + h * a.do_head + 4 * lane);
-            ld_bf16(o, a.out + t * a.o_row + h * a.o_head + 4 * lane);
-            const float x = warp_sum(dot(qn, kn) + dot(qr, kr)) * a.scale;
-            const float p = __expf(x - a.lse[static_cast<long long>(h) * a.Tq + t]);
-            const float ds = p * (warp_sum(dot(dO, v)) - warp_sum(dot(dO, o))) * a.scale;
+                for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
+                tmem_ld_wait();
+                const int lim = limit - TK * i;
+                if (__any_sync(0xffffffffu, lim < TK)) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) { dkn[i] += ds * qn[i]; dv[i] += p * dO[i]; }
+                    for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) dkr[i] += ds * qr[i];
+                        for (int j = 0; j < 32; ++j)
+                            if (32 * q + j >= lim) s[q][j] = 0xff800000u;      // -inf
+                }
+                float mx[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+                    for (int j = 1; j < 32; ++j) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][j]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                if (i == 0) {
+                    m = top == -CUDART_INF_F ? 0.f : top;
+                } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
+                    // O and l to the new maximum, once PV of the tile before is in O
+                    const float mn = fmaxf(m, top), al = exp2_fast(m - mn);
+                    m = mn;
+                    l *= al;
+                    if (!mbar_wait(smem_u32(&sh.pv_done[t]), (npv + i - 1) & 1, abort_flag, a.err)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t o[32];
+                        tmem_ld32(to + 32 * q, o);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * al);
+                        tmem_st32(to + 32 * q, o);
+                    }
+                }
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const float x0 = exp2_fast(fmaf(__uint_as_float(s[2 * q + j / 16][2 * (j & 15)]), c, -m));
+                        const float x1 = exp2_fast(fmaf(__uint_as_float(s[2 * q + j / 16][2 * (j & 15) + 1]), c, -m));
+                        sum[j & 1] += x0;
+                        sum[2 + (j & 1)] += x1;
+                        p[j] = pack_bf16x2(x0, x1);
+                    }
+                    tmem_st32(ts + 32 * q, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh.p_full[t]));
+            }
+            if (!ok) break;
+            const int n = it.n[t];
+            npv += n;
+            if (n > 0) {
+                if (!mbar_wait(smem_u32(&sh.pv_done[t]), (npv - 1) & 1, abort_flag, a.err)) break;
+                tc_fence_after();
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const bool mine = r < it.rows;
+            __nv_bfloat16* dst = a.out_w + (static_cast<long long>(it.row0) + r) * a.o_row +
+                                 static_cast<long long>(it.head) * a.o_head;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[32];
+                if (n > 0) {
+                    tmem_ld32(to + 32 * q, o);
+                    tmem_ld_wait();
+                }
+                if (mine) {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            w[j] = l > 0.f ? pack_bf16x2(__uint_as_float(o[8 * v + 2 * j]) * inv,
+                                                         __uint_as_float(o[8 * v + 2 * j + 1]) * inv) : 0u;
+                        reinterpret_cast<uint4*>(dst)[4 * q + v] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (mine)
+                a.lse_w[static_cast<long long>(it.head) * a.Tq + it.row0 + r] =
+                    l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+            tc_fence_before();
         }
-        st_bf16(a.dkn + j * a.dkn_row + h * a.dkn_head + 4 * lane, dkn);
-        st_bf16(a.dv + j * a.dv_row + h * a.dv_head + 4 * lane, dv);
     }
-    st_bf16(a.dkr + j * a.dkr_row + 2 * lane, dkr);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(sh.tmem, 512);
+    }
 }
 
-size_t latent_backward_ws_bytes(int, int, int) { return 256; }
+}  // namespace pf
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t st) {
-    const long long warps = static_cast<long long>(a.Tq) * a.H;
-    prefill_query_kernel<false><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(a);
-    count_launch();
-    return cudaGetLastError();
-}
-
-cudaError_t launch_latent_backward(const LatentPrefillArgs& a, void*, cudaStream_t st) {
-    const long long warps = static_cast<long long>(a.Tq) * a.H;
-    prefill_query_kernel<true><<<static_cast<unsigned>((warps + 3) / 4), 128, 0, st>>>(a);
-    count_launch();
-    cudaError_t e = cudaGetLastError();
+    static bool attr[kMaxDevices] = {false};
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(pf::prefill_kernel), pf::SMEM, attr);
     if (e != cudaSuccess) return e;
-    prefill_key_kernel<<<static_cast<unsigned>((static_cast<long long>(a.Tk) + 3) / 4), 128, 0, st>>>(a);
+    CUtensorMap q, kn, kr, v;
+    e = make_map_rows(&q, a.q, a.Tq, a.H, kDqk, a.q_row, a.q_head, 128);
+    if (e == cudaSuccess) e = make_map_rows(&kn, a.kn, a.Tk, a.H, kNope, a.kn_row, a.kn_head, 128);
+    if (e == cudaSuccess) e = make_map_rows(&kr, a.kr, a.Tk, 1, kRope, a.kr_row, 0, 128);
+    if (e == cudaSuccess) e = make_map_rows(&v, a.v, a.Tk, a.H, kDv, a.v_row, a.v_head, 128);
+    if (e != cudaSuccess) return e;
+    const int tiles = a.Tq / (2 * pf::TQ) + a.B;             // at least the row tiles of any split into B sequences
+    pf::prefill_kernel<<<static_cast<unsigned>(tiles) * a.H, pf::THREADS, pf::SMEM, st>>>(q, kn, kr, v, a, tiles);
     count_launch();
     return cudaGetLastError();
 }
