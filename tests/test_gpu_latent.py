@@ -281,6 +281,8 @@ class Decode:
     (24, [90, 3000, 1], 3, 7),
     (128, [50], 16, 64),
     (100, [2049, 77], 1, 64),
+    (32, [152], 1, 48),                                     # far fewer tiles than SMs: empty ranges between pieces
+    (48, [190, 1, 65], 1, 64),
 ])
 def test_decode(cache, H, lens, n_q, page):
     p = Decode(H, lens, n_q, page, cache)
