@@ -297,7 +297,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             return true;
         };
         auto score = [&](uint32_t uu) {                   // S^T = K Q^T
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
                 const uint32_t q = sst + (uu % STAGES) * STAGE;
                 for (int c = 0; c < 3; ++c) {
@@ -311,7 +311,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             __syncwarp();
         };
         auto dprob = [&](uint32_t uu) {                   // dP^T = V dO^T
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
                 const uint32_t o = sst + (uu % STAGES) * STAGE + 3 * QU;
                 for (int c = 0; c < 2; ++c) {
@@ -346,7 +346,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 const int steps = (min(TQ, it.len - TQ * j) + 15) >> 4;
                 if (j == 0 && !wait(&sh.acc_empty, (nacc & 1) ^ 1)) break;
                 if (!wait(&sh.p_full[u & 1], (u >> 1) & 1)) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
                     for (int kk = 0; kk < steps; ++kk)    // P^T: queries 0-31 in columns 0-15, 32-63 in 32-47
                         tc_mma_bf16_ts(tm_dv, tm_s + 64 * (u & 1) + 32 * (kk >> 1) + 8 * (kk & 1),
@@ -354,7 +354,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 }
                 __syncwarp();
                 if (!wait(&sh.ds_full, nd++ & 1)) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
                     for (int kk = 0; kk < steps; ++kk) {
                         const uint32_t ds = tm_dp + 32 * (kk >> 1) + 8 * (kk & 1);
@@ -369,13 +369,13 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
             if (!ok) break;
             ++nacc;
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_commit(smem_u32(&sh.acc_full));
                 tc_commit(smem_u32(&sh.kv_empty));
             }
             __syncwarp();
         }
-        if (lane == 0) {
+        if (elect_one()) {
             tc_commit(smem_u32(&sh.fin));
             drain(&sh.fin, 0, a.err);
         }
@@ -656,7 +656,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
                 for (int c = 0; c < 3; ++c) {
                     const uint64_t ad = smem_desc_sw128(smem_u32(smem + Q_OFF + c * UNIT)), bd = smem_desc_sw128(unit(uu + 2 + c));
@@ -690,7 +690,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                 if (i + 1 < it.n && !products(u + 5, min(128, it.len - 128 * (i + 1)))) break;
                 if (i == 0 && !wait(&sh.acc_empty, (nacc & 1) ^ 1)) break;
                 if (!wait(&sh.ds_full, nd++ & 1)) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
                     const int steps = (min(128, it.len - 128 * i) + 15) >> 4;
                     for (int kk = 0; kk < steps; ++kk)
@@ -704,10 +704,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             }
             if (!ok) break;
             ++nacc;
-            if (lane == 0) tc_commit(smem_u32(&sh.q_empty));
+            if (elect_one()) tc_commit(smem_u32(&sh.q_empty));
             __syncwarp();
         }
-        if (lane == 0) {
+        if (elect_one()) {
             tc_commit(smem_u32(&sh.fin));
             drain(&sh.fin, 0, a.err);
         }

@@ -312,7 +312,7 @@ decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, fl
         auto score = [&](uint32_t gg, uint32_t uu) {
             if (!wait(&sh.r_full[gg & 1], (gg >> 1) & 1)) return false;
             const uint32_t d = tm_s + 64 * (gg & 1);
-            if (lane == 0) {
+            if (elect_one()) {
                 fence_proxy_async_smem();              // the copies' writes, before the tensor cores read them
                 tc_fence_after();
                 const uint64_t ad = smem_desc_sw128(smem_u32(sq + 8 * q_chunk));
@@ -325,7 +325,7 @@ decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, fl
             for (int c = 0; c < 4; ++c) {
                 const uint32_t s = (uu + c) % stages;
                 if (!wait(&sh.full[s], ((uu + c) / stages) & 1)) return false;
-                if (lane == 0) {
+                if (elect_one()) {
                     fence_proxy_async_smem();
                     tc_fence_after();
                     for (int e = 0; e < 2; ++e) {
@@ -337,7 +337,7 @@ decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, fl
                 }
                 __syncwarp();
             }
-            if (lane == 0) tc_commit(smem_u32(&sh.s_full[gg & 1]));
+            if (elect_one()) tc_commit(smem_u32(&sh.s_full[gg & 1]));
             __syncwarp();
             return true;
         };
@@ -345,15 +345,15 @@ decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, fl
             if (!wait(&sh.q_full, np & 1)) break;
             if (!score(g, u)) break;
             const int n = p.t1 - p.t0;
-            if (n == 1 && lane == 0) tc_commit(smem_u32(&sh.q_empty));
+            if (n == 1 && elect_one()) tc_commit(smem_u32(&sh.q_empty));
             for (int i = 0; i < n; ++i, ++g, u += 4) {
                 if (i + 1 < n) {
                     if (!score(g + 1, u + 4)) break;
-                    if (i + 2 == n && lane == 0) tc_commit(smem_u32(&sh.q_empty));
+                    if (i + 2 == n && elect_one()) tc_commit(smem_u32(&sh.q_empty));
                 }
                 if (i == 0 && !wait(&sh.o_empty, (np & 1) ^ 1)) break;
                 if (!wait(&sh.p_full, g & 1)) break;
-                if (lane == 0) {
+                if (elect_one()) {
                     tc_fence_after();
                     const uint64_t bd = smem_desc_sw128(smem_u32(sp));
                     for (int c = 0; c < 4; ++c) {
@@ -371,7 +371,7 @@ decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, fl
             }
             ++np;
         }
-        if (lane == 0) {
+        if (elect_one()) {
             tc_commit(smem_u32(&sh.fin));
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(smem_u32(&sh.fin), 0))

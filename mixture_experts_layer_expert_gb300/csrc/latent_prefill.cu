@@ -219,7 +219,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             return ok;
         };
         auto score = [&](int t, uint32_t u0) {          // S_t = Q_t K^T from units u0 .. u0 + 2
-            if (lane == 0) {
+            if (elect_one()) {
                 tc_fence_after();
                 for (int c = 0; c < 3; ++c) {
                     const uint64_t ad = smem_desc_sw128(smem_u32(smem + (3 * t + c) * UNIT));
@@ -233,7 +233,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             __syncwarp();
         };
         auto release = [&](uint32_t u0, int n) {
-            if (lane == 0)
+            if (elect_one())
                 for (int c = 0; c < n; ++c) tc_commit(smem_u32(&sh.empty[(u0 + c) % NU]));
             __syncwarp();
         };
@@ -274,7 +274,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 for (int t = 0; t < 2; ++t) {
                     if (i < it.n[t]) {
                         if (!wait(&sh.p_full[t], np[t]++ & 1)) break;
-                        if (lane == 0) {
+                        if (elect_one()) {
                             tc_fence_after();
                             for (int kk = 0; kk < steps; ++kk) {
                                 const uint32_t base = smem_u32(smem + RING_OFF);
@@ -306,10 +306,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 u += 5;
             }
             if (!ok) break;
-            if (lane == 0) tc_commit(smem_u32(&sh.q_empty));
+            if (elect_one()) tc_commit(smem_u32(&sh.q_empty));
             __syncwarp();
         }
-        if (lane == 0) {
+        if (elect_one()) {
             tc_commit(smem_u32(&sh.fin));          // every MMA completes before TMEM is released
             const uint64_t t0 = globaltimer_ns();
             while (!mbar_try_wait(smem_u32(&sh.fin), 0))
