@@ -593,7 +593,7 @@ fs_status fs_latent_cache_read(const fs_latent_cache* desc, const void* cache, i
  * sees no position gives out = 0, lse = -inf.  A length outside [0, max_pages
  * page_size] (that sequence counts as empty) or a page outside [0, n_pages)
  * (its positions are left out) sets the device error word (code 5).
- * n_q 1 .. 16.  The length is split over the SMs and joined in a fixed order:
+ * n_q 1 .. 16, scale > 0, n_pages page_size < 2^31.  The length is split over the SMs and joined in a fixed order:
  * results do not depend on timing.  ws: fs_latent_decode_ws_bytes bytes,
  * 256-byte aligned. */
 size_t fs_latent_decode_ws_bytes(int32_t heads, int32_t B, int32_t n_q);
@@ -606,7 +606,9 @@ fs_status fs_latent_decode(const fs_latent_cache* desc, int32_t heads, int32_t B
  * rows [cu_q[b], cu_q[b+1]) of Tq and key rows [cu_k[b], cu_k[b+1]) of Tk
  * (device int32 [n_seqs + 1], non-decreasing; either may be empty).  causal:
  * the last query sees the last key (query i of lq sees keys 0 .. lk - lq + i),
- * so more keys than queries is a cached prefix. */
+ * so more keys than queries is a cached prefix.  scale > 0.  What lies in rows
+ * outside a sequence, NaN included, does not reach it; a NaN in one of its keys or
+ * values may reach all its queries, those that do not see that key too. */
 typedef struct {
     int32_t heads, n_seqs, Tq, Tk;
     int32_t causal;

@@ -105,7 +105,7 @@ fs_status check_prefill(const fs_latent_prefill_desc* d) {
     if ((static_cast<int64_t>(d->Tq) / 128 + d->n_seqs + 1) * d->heads > 0x7fffffffLL ||
         (static_cast<int64_t>(d->Tk) / 128 + d->n_seqs + 1) * d->heads > 0x7fffffffLL)
         return FS_ERR_UNSUPPORTED;
-    return std::isfinite(d->scale) ? FS_OK : FS_ERR_INVALID_ARG;
+    return std::isfinite(d->scale) && d->scale > 0.f ? FS_OK : FS_ERR_INVALID_ARG;
 }
 
 // The operands that the forward and the backward share.
@@ -217,7 +217,7 @@ fs_status fs_latent_decode(const fs_latent_cache* desc, int32_t heads, int32_t B
     FS_CHECK(check_cache(desc));
     FS_CHECK(check_decode(heads, B, n_q));
     if (!q_latent || !q_rope || !out || max_pages < 1 || table_row < 0 || (B > 1 && table_row < max_pages) ||
-        !std::isfinite(scale))
+        !std::isfinite(scale) || !(scale > 0.f))
         return FS_ERR_INVALID_ARG;
     FS_CHECK(need(q_latent->p));
     FS_CHECK(need(q_rope->p));
@@ -226,6 +226,7 @@ fs_status fs_latent_decode(const fs_latent_cache* desc, int32_t heads, int32_t B
     FS_CHECK(need(seq_lens, 4));
     FS_CHECK(need(out->p));
     if (lse) FS_CHECK(need(lse, 4));
+    if (n_slots(desc) > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;       // records are addressed by int32
     const int64_t rows = static_cast<int64_t>(B) * n_q;
     FS_CHECK(strides(rows, heads, kLatent, q_latent->row, q_latent->head, 2, false));
     FS_CHECK(strides(rows, heads, kRope, q_rope->row, q_rope->head, 2, false));

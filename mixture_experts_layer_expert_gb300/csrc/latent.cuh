@@ -59,6 +59,14 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes16, float sca
     return pack_bf16x2(f.x * scale, f.y * scale);
 }
 
+// Two E4M3 codes as packed bf16, unscaled (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes16) {
+    uint32_t h2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<unsigned short>(codes16)));
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h2));
+    return pack_bf16x2(f.x, f.y);
+}
+
 // One packed sequence: query rows [q0, q0 + lq), key rows [k0, k0 + lk).
 struct PackedSeq {
     int q0, lq, k0, lk;
@@ -103,6 +111,12 @@ __device__ __forceinline__ int find_tile(const int32_t* cu_q, const int32_t* cu_
         before = __shfl_sync(0xffffffffu, end, 31);
     }
     return -1;
+}
+
+// mbar_wait by a whole warp with one answer for all its lanes: what follows a
+// failed wait must not split a warp that goes on to warp-wide operations.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
 }
 
 // 2^x (x <= 0 here up to rounding): one hardware operation, relative error about 2^-22.

@@ -388,7 +388,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
             const uint32_t slot = k & 1;
-            if (!mbar_wait(smem_u32(&sh.q.full[slot]), (k >> 1) & 1, abort_flag, a.err)) break;
+            if (!warp_wait(smem_u32(&sh.q.full[slot]), (k >> 1) & 1, abort_flag, a.err)) break;
             const Item it = sh.q.item[slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.q.empty[slot]));
@@ -397,12 +397,12 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             for (int j = 0; j < it.n; ++j, ++u) {
                 const uint32_t st = u % STAGES, buf = u & 1;
                 const uint32_t ts = tm_s + 64 * buf + 32 * half + lane_base, td = tm_dp + 32 * half + lane_base;
-                if (!mbar_wait(smem_u32(&sh.s_full[buf]), (u >> 1) & 1, abort_flag, a.err)) { ok = false; break; }
+                if (!warp_wait(smem_u32(&sh.s_full[buf]), (u >> 1) & 1, abort_flag, a.err)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t s[32];
                 tmem_ld32(ts, s);
                 // the statistics were written before the stage's loads were issued (the wait returns at once)
-                if (!mbar_wait(smem_u32(&sh.full[st]), (u / STAGES) & 1, abort_flag, a.err)) { ok = false; break; }
+                if (!warp_wait(smem_u32(&sh.full[st]), (u / STAGES) & 1, abort_flag, a.err)) { ok = false; break; }
                 const float4* ls = reinterpret_cast<const float4*>(&sh.lse[st][32 * half]);
                 const float4* dl = reinterpret_cast<const float4*>(&sh.delta[st][32 * half]);
                 tmem_ld_wait();
@@ -427,7 +427,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh.p_full[buf]));
-                if (!mbar_wait(smem_u32(&sh.dp_full), ndp++ & 1, abort_flag, a.err)) { ok = false; break; }
+                if (!warp_wait(smem_u32(&sh.dp_full), ndp++ & 1, abort_flag, a.err)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t d[32];
                 tmem_ld32(td, d);
@@ -449,7 +449,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
             if (!ok) break;
             if (it.n > 0) {
-                if (!mbar_wait(smem_u32(&sh.acc_full), nacc++ & 1, abort_flag, a.err)) break;
+                if (!warp_wait(smem_u32(&sh.acc_full), nacc++ & 1, abort_flag, a.err)) break;
                 tc_fence_after();
             }
             // half 0: dV, half 1: dK's unrotated part; the rotary part 32 columns each
@@ -720,7 +720,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
             const uint32_t slot = k & 1;
-            if (!mbar_wait(smem_u32(&sh.q.full[slot]), (k >> 1) & 1, abort_flag, a.err)) break;
+            if (!warp_wait(smem_u32(&sh.q.full[slot]), (k >> 1) & 1, abort_flag, a.err)) break;
             const Item it = sh.q.item[slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.q.empty[slot]));
@@ -737,7 +737,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             // keys this row sees: [0, end)
             const int end = !mine ? 0 : (a.causal ? min(it.len, it.diag + r + 1) : it.len);
             for (int i = 0; i < it.n; ++i, ++n_sp) {
-                if (!mbar_wait(smem_u32(&sh.sp_full), n_sp & 1, abort_flag, a.err)) { ok = false; break; }
+                if (!warp_wait(smem_u32(&sh.sp_full), n_sp & 1, abort_flag, a.err)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t s[2][32], d[2][32];
 #pragma unroll
@@ -766,7 +766,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                         w[16 * q + e] = pack_bf16x2(v[0], v[1]);
                     }
                 // the dQ product of the tile before has read dS
-                if (n_sp > 0 && !mbar_wait(smem_u32(&sh.dq_done), (n_sp - 1) & 1, abort_flag, a.err)) { ok = false; break; }
+                if (n_sp > 0 && !warp_wait(smem_u32(&sh.dq_done), (n_sp - 1) & 1, abort_flag, a.err)) { ok = false; break; }
                 tc_fence_after();
                 tmem_st32(tm_ds + 32 * half + lane_base, w);
                 tmem_st_wait();
@@ -776,7 +776,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             if (!ok) break;
             n_dq = n_sp;
             if (it.n > 0) {
-                if (!mbar_wait(smem_u32(&sh.dq_done), (n_dq - 1) & 1, abort_flag, a.err)) break;
+                if (!warp_wait(smem_u32(&sh.dq_done), (n_dq - 1) & 1, abort_flag, a.err)) break;
                 tc_fence_after();
             }
             __nv_bfloat16* dst = a.dq + (static_cast<long long>(it.row0) + r) * a.dq_row + it.head * a.dq_head + 96 * half;

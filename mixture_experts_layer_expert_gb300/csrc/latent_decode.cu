@@ -3,27 +3,35 @@
 //   s_i = scale (q_l . c_i + q_r . k_i),  out = sum_i softmax(s)_i c_i,  lse = log sum_i exp(s_i)
 //
 // All heads (and the n_q new tokens) of a sequence read the same records, so a
-// block takes 64 query rows (row = new token * heads + head) against tiles of 64
-// records, staged once in shared memory as bf16 and used twice:
-//   S  = Q K^T      64 rows x 64 records x 576, both K-major
-//   O^T += C^T P^T  512 (4 x 128) x rows x 64 records: the same tile read MN-major
-//                   as the A operand, P (bf16, shared memory) as the B operand
-// O^T keeps the 512-wide output in 4 x rows TMEM columns (rows rounded up to 16)
-// and a few heads cost few columns; its rescaling by a row factor is rare, as in
-// the expanded form (only when a maximum grows by 2^8).
+// block takes up to 64 query rows (row = new token * heads + head) against tiles
+// of 64 records, staged once in shared memory as bf16 and used twice as the A
+// operand of transposed products:
+//   S^T = K Q^T      64 records x rows x 576, the tile read K-major
+//   O^T += C^T P     512 (4 x 128) x rows x 64 records, the same tile read MN-major
+// so the MMAs' N is the number of rows (rounded to 16, 32 or 64) and a few heads
+// cost little; an MMA costs a fixed 28 (M = 64) or 43 (M = 128) cycles beside N/2.
+// A thread holds one record's scores for all rows.  Against a running maximum per
+// row that is only raised when a score exceeds it by 2^8, no thread needs the
+// others' scores: the sum of p stays per record until the end, and the maximum,
+// the rescaling of O^T and the shuffles they need run in a sequence's first tile
+// and on the rare tiles that raise it (one barrier with an OR decides).
 //
-// Bound: the records' bytes.  64 records are 73.7 KB (bf16) or 42 KB (FP8), 3,150 or
-// 1,790 cycles of one SM's share of the memory bandwidth; 64 rows of MMAs take
-// 1,152 + 768 cycles, 16 rows 1,152 + 576.
+// Bound: the records' bytes while the MMAs of a block of rows fit under them: 64
+// records are 73.7 KB (bf16) or 42 KB (FP8), 3,150 or 1,790 cycles of one SM's
+// share of the memory bandwidth; the MMAs take 36 x 36 + 16 x 52 = 2,130 cycles for 16
+// rows, 36 x 60 + 16 x 75 = 3,360 for 64.
 //
 // The records of all sequences form one list of tiles which is cut into equal
 // ranges, one per block (and per block of 64 rows), whatever the lengths.  A
 // sequence inside one range is finished there; one that is cut leaves fp32
 // partials (normalised O and lse) which a second kernel joins in range order.
 //
-// Warps 0-3: softmax, rescaling, output; warp 4: MMA issue; warps 5-12: page
-// lookup and loads (cp.async for bf16; FP8 codes through registers, where code *
-// scale is exact in bf16).  Ring stages of 64 records x 128 latent columns (16 KB).
+// Warps 0-3: softmax, rescaling, output; warp 4: MMA issue; warps 5-6: Q of the
+// next sequence; then the loaders.  bf16: one warp, page lookup a tile ahead and
+// TMA (a whole tile of consecutive records as two boxes per stage, else gathers of
+// four records).  FP8: codes go through registers a tile ahead and become bf16
+// unscaled; a record's scale multiplies its latent scores (the rotary part has TMEM
+// columns of its own) and its p.  Ring stages of 64 records x 128 latent columns (16 KB).
 #include <math_constants.h>
 
 #include "kernels.h"
@@ -37,28 +45,27 @@ constexpr int ROWS = 64;                      // query rows per block
 constexpr int CH = 64 * 128;                  // 64 records (or query rows) x 64 columns, 8 KB
 constexpr int PAIR = 2 * CH;                  // ring stage: 128 latent columns
 constexpr int MAXP = 11;                      // ring stages (8 with 64 query rows, 11 with 16)
-constexpr int LOADERS = 256;
-constexpr int THREADS = 160 + LOADERS;
-constexpr int CTRL = 2048;
+constexpr int MAXRAW = 6;                     // FP8: raw stages (64 records x 128 codes, 8 KB)
+constexpr int CTRL = 3072;
 constexpr size_t SMEM = 232448;               // 227 KB
 constexpr float kRescale = 8.0f;
-constexpr uint32_t NONE = 0xffffffffu;        // (a cache of 2^32 - 1 records does not fit the memory)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t NONE = 0xffffffffu;        // no record
 
 struct Meta {                                 // of each range: the sequence of its first tile
     int b, off, tiles, pad;                   // off: tiles of the sequence before the range; tiles: of the range
 };
 
 struct Shared {
-    uint64_t full[MAXP], empty[MAXP], r_full[2], r_empty[2], q_full, q_empty, s_full[2], p_full, pv_done, o_empty, fin;
+    uint64_t full[MAXP], empty[MAXP], raw_full[MAXRAW], raw_empty[MAXRAW], r_full[2], r_empty[2], info_full[4];
+    uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_empty, fin;
     uint32_t tmem;
     int abort_flag;
     int b0, tile0, left;                      // first piece of this block's range
     uint32_t live[4][2];                      // records of a tile that count (4 tiles deep)
-    int flag[2][4];
-    float alpha[2][ROWS];                     // rescaling factors of a tile; 1 / l at the end of a piece
-    uint32_t rec[2][TT];                      // each record's index, NONE: a zero row
-    float scale[2][TT];
+    alignas(16) float m[ROWS], f[ROWS];       // running maximum (log2 units), rescaling factor or 1 / l
+    float red[4][ROWS];                       // the warps' maxima or sums
+    float scale[4][TT];                       // FP8: the records' scales (4 tiles deep)
 };
 static_assert(sizeof(Shared) <= CTRL, "control area");
 
@@ -70,65 +77,208 @@ __device__ __forceinline__ int seq_len(const LatentDecodeArgs& a, int b) {
     const int n = __ldg(a.seq_lens + b);
     return n < 0 || n > static_cast<long long>(a.max_pages) * a.page_size ? 0 : n;
 }
-__device__ __forceinline__ int tiles_of(int len) { return static_cast<int>((static_cast<unsigned>(len) + TT - 1) / TT); }
-
-// Next piece of the range; b, tile, left advance.  False at the end.
-__device__ __forceinline__ bool next_piece(const LatentDecodeArgs& a, int& b, int& tile, long long& left, Piece* p) {
+// Next piece of the range (tiles of tt records); b, tile, left advance.  False at the end.
+__device__ __forceinline__ bool next_piece(const LatentDecodeArgs& a, int& b, int& tile, int& left, Piece* p, int tt = TT) {
     if (left <= 0) return false;
     int len = 0, n = 0;
     for (; b < a.B; ++b, tile = 0) {
         len = seq_len(a, b);
-        n = tiles_of(len);
+        n = static_cast<int>((static_cast<unsigned>(len) + tt - 1) / tt);
         if (tile < n) break;
     }
     if (b >= a.B) return false;
     p->b = b; p->len = len; p->n = n; p->t0 = tile;
-    p->t1 = static_cast<int>(min(static_cast<long long>(n), tile + left));
+    p->t1 = tile + min(n - tile, left);
     left -= p->t1 - p->t0;
     ++b;
     tile = 0;
     return true;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
-    const int n = ok ? 16 : 0;                // 0: sixteen zero bytes, nothing is read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+// The table's entry for position pos of sequence b (0 past the end): only the load, so that it can be issued a
+// tile ahead of its use.
+__device__ __forceinline__ int page_at(const LatentDecodeArgs& a, int b, int len, int pos) {
+    return pos < len ? __ldg(a.table + b * a.table_row + pos / a.page_size) : 0;
 }
-// The barrier receives this thread's arrival when its earlier cp.async copies are done.
-__device__ __forceinline__ void cp_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+// Record of position pos on that page, or NONE (past the end, or a page outside the cache, which is recorded).
+__device__ __forceinline__ uint32_t record_of(const LatentDecodeArgs& a, int len, int pos, int page) {
+    if (pos >= len) return NONE;
+    if (page < 0 || page >= a.n_pages) {
+        set_dev_error(a.err, DEV_ERR_PAGE);
+        return NONE;
+    }
+    return static_cast<uint32_t>(page) * static_cast<uint32_t>(a.page_size) + static_cast<uint32_t>(pos % a.page_size);
+}
+
+// 64 consecutive positions of a sequence as one load: lane l brings the records of positions l and 32 + l.
+struct Group {
+    uint32_t live0, live1;      // which count
+    int start;                  // first record
+    bool box, none;             // 64 consecutive records; no record at all
+    int y[4];                   // the four records of gather group lane & 15
+};
+__device__ __forceinline__ Group make_group(uint32_t r0, uint32_t r1, int lane) {
+    Group g;
+    g.live0 = __ballot_sync(0xffffffffu, r0 != NONE);
+    g.live1 = __ballot_sync(0xffffffffu, r1 != NONE);
+    const uint32_t start = __shfl_sync(0xffffffffu, r0, 0);
+    g.start = static_cast<int>(start);
+    g.box = __all_sync(0xffffffffu, r0 == start + lane && r1 == start + 32 + lane && r1 != NONE);
+    g.none = (g.live0 | g.live1) == 0;
+    // a record that does not count is read as a copy of one that does: its p is 0
+    const uint32_t a = __shfl_sync(0xffffffffu, r0, g.live0 ? __ffs(g.live0) - 1 : 0);
+    const uint32_t b = __shfl_sync(0xffffffffu, r1, g.live1 ? __ffs(g.live1) - 1 : 0);
+    const uint32_t some = g.live0 ? a : b;
+    if (r0 == NONE) r0 = some;
+    if (r1 == NONE) r1 = some;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int src = 4 * (lane & 7) + e;
+        const uint32_t lo = __shfl_sync(0xffffffffu, r0, src), hi = __shfl_sync(0xffffffffu, r1, src);
+        g.y[e] = static_cast<int>((lane & 8) ? hi : lo);
+    }
+    return g;
 }
 __device__ __forceinline__ void sts16(uint32_t dst, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
+// Whole warp: `chunks` boxes of 64 records x 128 bytes (columns from col on, col_step elements apart) to dst, each
+// 8 KB, completing on bar (one arrival, the bytes).  Group without records: zeros.
+__device__ __forceinline__ void load_group(const CUtensorMap* tile, const CUtensorMap* row, const Group& g, uint32_t dst,
+                                           uint32_t bar, int col, int col_step, int chunks, int lane) {
+    if (g.none) {
+        for (int i = lane; i < chunks * CH / 16; i += 32) sts16(dst + 16 * i, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar);
+    } else if (g.box) {
+        if (elect_one()) {
+            mbar_arrive_expect_tx(bar, chunks * CH);
+            for (int c = 0; c < chunks; ++c) tma_load_2d(dst + c * CH, tile, bar, col + c * col_step, g.start);
+        }
+    } else {
+        if (lane == 0) mbar_arrive_expect_tx(bar, chunks * CH);
+        __syncwarp();
+        const int c = lane >> 4;
+        if (c < chunks)
+            tma_gather4(dst + c * CH + (lane & 15) * 512, row, bar, col + c * col_step, g.y[0], g.y[1], g.y[2], g.y[3]);
+    }
+    __syncwarp();
+}
+// 16 E4M3 codes -> 32 bytes of bf16 at units y, y + 1 of the 128-byte row at base (swizzled by row r).
+__device__ __forceinline__ void put_codes(const uint4& v, uint32_t base, int y, int r) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        o[2 * i] = e4m3x2_to_bf16x2(w[i] & 0xffffu);
+        o[2 * i + 1] = e4m3x2_to_bf16x2(w[i] >> 16);
+    }
+    sts16(base + ((y ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+    sts16(base + (((y + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
+}
+// Bounded wait without regard to the abort flag, for loads in flight at the block's end.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* err) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_u32(bar), parity))
+        if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(err, DEV_ERR_TIMEOUT); break; }
+}
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+// Barrier of n threads that also tells whether any of them brought `v`.
+__device__ __forceinline__ bool bar_any(int id, int n, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
+        "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(n), "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
+}
 
-template <bool FP8>
-__global__ void __launch_bounds__(THREADS, 1)
-decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, float* __restrict__ part,
+// One warp: the range's first sequence and tile (of tt records), and its length, for the block and (write) for the join.
+__device__ __forceinline__ void find_range(const LatentDecodeArgs& a, int range, int ranges, int tt, bool write, Meta* meta,
+                                           int* b0, int* tile0, int* left) {
+    const int lane = threadIdx.x & 31;
+    auto tiles = [&](int b) { return static_cast<int>((static_cast<unsigned>(seq_len(a, b)) + tt - 1) / tt); };
+    long long total = 0;
+    for (int b = lane; b < a.B; b += 32) {
+        const int n = __ldg(a.seq_lens + b);
+        if (n < 0 || n > static_cast<long long>(a.max_pages) * a.page_size) set_dev_error(a.err, DEV_ERR_PAGE);
+        total += tiles(b);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    const long long g0 = total * range / ranges, g1 = total * (range + 1) / ranges;
+    long long before = 0;
+    int found_b = a.B, found_t = 0;
+    for (int c0 = 0; c0 < a.B; c0 += 32) {
+        const int n = c0 + lane < a.B ? tiles(c0 + lane) : 0;
+        long long end = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, end, d);
+            if (lane >= d) end += v;
+        }
+        end += before;
+        const unsigned past = __ballot_sync(0xffffffffu, end > g0);
+        if (past) {
+            const int l = __ffs(past) - 1;
+            found_b = c0 + l;
+            found_t = static_cast<int>(g0 - __shfl_sync(0xffffffffu, end - n, l));
+            break;
+        }
+        before = __shfl_sync(0xffffffffu, end, 31);
+    }
+    if (lane == 0) {
+        *b0 = found_b;
+        *tile0 = found_t;
+        *left = static_cast<int>(g1 - g0);
+        if (write) meta[range] = Meta{found_b, found_t, static_cast<int>(g1 - g0), 0};
+    }
+}
+
+// FP8: warps that turn codes into bf16 (four where 64 rows need the registers).
+template <bool FP8, int RN> constexpr int kConv = FP8 ? (RN == 64 ? 4 : 8) : 0;
+template <bool FP8, int RN> constexpr int kThreads = 32 * (8 + kConv<FP8, RN>);
+
+template <bool FP8, int RN>
+__global__ void __launch_bounds__(kThreads<FP8, RN>, 1)
+decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant__ CUtensorMap tmRow,
+              const LatentDecodeArgs a, const int rb_count, const int ranges, float* __restrict__ part,
               float* __restrict__ part_lse, Meta* __restrict__ meta) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    // all of the SM's shared memory and no static part: the block's memory starts on a 1 KB boundary
+    extern __shared__ __align__(1024) uint8_t smem[];
+    if (smem_u32(smem) & 1023u) {
+        if (threadIdx.x == 0) set_dev_error(a.err, DEV_ERR_LIMIT);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rb = blockIdx.x % rb_count, range = blockIdx.x / rb_count;
-    const int rows = min(ROWS, a.n_q * a.H - rb * ROWS), rn = (rows + 15) & ~15;
-    // Q chunks of rn rows (the MMA's 64 rows run on into what follows: rows nobody reads), P, rope ring, stage ring, control
-    const int q_chunk = rn * 128, stages = rn <= 16 ? 11 : (rn <= 32 ? 10 : (rn <= 48 ? 9 : 8));
+    const int rows = min(ROWS, a.n_q * a.H - rb * ROWS);
+    // Q (9 chunks of RN rows), P (64 records x 64 rows, 128 bytes a record), rope ring, stage ring, control
+    constexpr int QC = RN * 128, CW = kConv<FP8, RN>;
+    constexpr int raws = FP8 ? (RN == 64 ? 4 : 6) : 0;
+    constexpr int stages = (RN == 16 ? 11 : (RN == 32 ? 10 : 8)) - raws / 2;
     uint8_t* sq = smem;
-    uint8_t* sp = smem + 9 * q_chunk;
+    uint8_t* sp = smem + 9 * QC;
     uint8_t* srope = sp + CH;
-    uint8_t* sring = srope + 2 * CH;
-    Shared& sh = *reinterpret_cast<Shared*>(smem + (SMEM - 1024 - CTRL));
+    uint8_t* sraw = srope + 2 * CH;                // FP8: codes as they lie in the cache
+    uint8_t* sring = sraw + raws * CH;
+    static_assert(9 * QC + (3 + raws) * CH + stages * PAIR + CTRL <= SMEM && raws <= MAXRAW, "shared memory");
+    Shared& sh = *reinterpret_cast<Shared*>(smem + (SMEM - CTRL));
     volatile int* abort_flag = &sh.abort_flag;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < MAXP; ++i) { mbar_init(smem_u32(&sh.full[i]), LOADERS); mbar_init(smem_u32(&sh.empty[i]), 1); }
+        for (int i = 0; i < MAXP; ++i) { mbar_init(smem_u32(&sh.full[i]), FP8 ? CW : 1); mbar_init(smem_u32(&sh.empty[i]), 1); }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh.r_full[i]), LOADERS + 2);
+            mbar_init(smem_u32(&sh.r_full[i]), 1);
             mbar_init(smem_u32(&sh.r_empty[i]), 1);
             mbar_init(smem_u32(&sh.s_full[i]), 1);
         }
-        mbar_init(smem_u32(&sh.q_full), LOADERS);
+        for (int i = 0; i < MAXRAW; ++i) { mbar_init(smem_u32(&sh.raw_full[i]), 1); mbar_init(smem_u32(&sh.raw_empty[i]), FP8 ? CW : 1); }
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.info_full[i]), 1);
+        mbar_init(smem_u32(&sh.q_full), 64);
         mbar_init(smem_u32(&sh.q_empty), 1);
         mbar_init(smem_u32(&sh.p_full), 128);
         mbar_init(smem_u32(&sh.pv_done), 1);
@@ -141,166 +291,128 @@ decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, fl
         tmem_alloc(smem_u32(&sh.tmem), 512);
         tmem_relinquish();
     }
-    if (warp == 0) {
-        // this block's range of the list of tiles, and where it starts
-        long long total = 0;
-        for (int b = lane; b < a.B; b += 32) {
-            const int n = __ldg(a.seq_lens + b);
-            if (n < 0 || n > static_cast<long long>(a.max_pages) * a.page_size) set_dev_error(a.err, DEV_ERR_PAGE);
-            total += tiles_of(seq_len(a, b));
-        }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-        const long long g0 = total * range / ranges, g1 = total * (range + 1) / ranges;
-        long long before = 0;
-        int found_b = a.B, found_t = 0;
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const int n = b0 + lane < a.B ? tiles_of(seq_len(a, b0 + lane)) : 0;
-            long long end = n;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, end, d);
-                if (lane >= d) end += v;
-            }
-            end += before;
-            const unsigned past = __ballot_sync(0xffffffffu, end > g0);
-            if (past) {
-                const int l = __ffs(past) - 1;
-                found_b = b0 + l;
-                found_t = static_cast<int>(g0 - __shfl_sync(0xffffffffu, end - n, l));
-                break;
-            }
-            before = __shfl_sync(0xffffffffu, end, 31);
-        }
-        if (lane == 0) {
-            sh.b0 = found_b;
-            sh.tile0 = found_t;
-            sh.left = static_cast<int>(g1 - g0);
-            if (rb == 0) meta[range] = Meta{found_b, found_t, static_cast<int>(g1 - g0), 0};
-        }
-    }
+    if (warp == 0) find_range(a, range, ranges, TT, rb == 0, meta, &sh.b0, &sh.tile0, &sh.left);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tm_s = sh.tmem, tm_o = sh.tmem + 128;
-    int b = sh.b0, tile = sh.tile0;
-    long long left = sh.left;
+    // S^T twice, FP8: the rotary part of S^T twice (not scaled by the record), O^T
+    const uint32_t tm_s = sh.tmem, tm_r = sh.tmem + 128, tm_o = sh.tmem + 256;
+    int b = sh.b0, tile = sh.tile0, left = sh.left;
     Piece p;
 
-    if (warp >= 5) {
-        // -------------------------------------------------------------- loads
-        const int t = threadIdx.x - 160;
-        constexpr int REC = FP8 ? kRecFp8 : kRecBf16;
-        uint32_t u = 0, g = 0, np = 0;                 // ring stages, tiles, pieces so far
-        bool ok = true;
-        auto offset = [&](uint32_t rec) { return rec == NONE ? -1LL : static_cast<long long>(rec) * REC; };
-        const uint32_t ring = smem_u32(sring), rope = smem_u32(srope), qs = smem_u32(sq);
-        while (ok && next_piece(a, b, tile, left, &p)) {
-            // Q of the piece's sequence: rn rows x 72 sixteen-byte units; rows past the last are zeros
-            if (!mbar_wait(smem_u32(&sh.q_empty), (np & 1) ^ 1, abort_flag, a.err)) break;
-            for (int i = t; i < rn * 72; i += LOADERS) {
-                const int r = i / 72, x = i - r * 72, c = x >> 3, qr = rb * ROWS + r;
-                const int j = qr / a.H, h = qr - j * a.H;
-                const long long row = static_cast<long long>(p.b) * a.n_q + j;
-                const bool in = r < rows;
-                const __nv_bfloat16* src = !in ? a.ql : (c < 8 ? a.ql + row * a.ql_row + h * a.ql_head + 8 * x
-                                                               : a.qr + row * a.qr_row + h * a.qr_head + 8 * (x - 64));
-                cp16(qs + c * q_chunk + r * 128 + (((x & 7) ^ (r & 7)) << 4), src, in);
-            }
-            cp_arrive(smem_u32(&sh.q_full));
-            ++np;
-            for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
-                const int par = g & 1;
-                if (t < TT) {
-                    const int pos = ti * TT + t;
-                    uint32_t rec = NONE;
-                    float sc = 0.f;
-                    if (pos < p.len) {
-                        const int pg = pos / a.page_size;
-                        const int page = __ldg(a.table + p.b * a.table_row + pg);
-                        if (page < 0 || page >= a.n_pages)
-                            set_dev_error(a.err, DEV_ERR_PAGE);
-                        else
-                            rec = static_cast<uint32_t>(page) * static_cast<uint32_t>(a.page_size) + static_cast<uint32_t>(pos - pg * a.page_size);
+    if (warp >= 8) {
+        // ------------------------------------------- FP8 codes to bf16 stages
+        if constexpr (FP8) {
+            constexpr int NT = 32 * CW, NU = TT * 8 / NT;           // threads, 16-byte units a thread takes of a stage
+            const int t = threadIdx.x - 256;
+            uint32_t u = 0;
+            bool ok = true;
+            while (ok && next_piece(a, b, tile, left, &p)) {
+                for (int n = 4 * (p.t1 - p.t0); n > 0; --n, ++u) {
+                    const uint32_t rs = u % raws, s = u % stages;
+                    if (!warp_wait(smem_u32(&sh.raw_full[rs]), (u / raws) & 1, abort_flag, a.err)) { ok = false; break; }
+                    uint4 v[NU];
+#pragma unroll
+                    for (int e = 0; e < NU; ++e) {
+                        const int i = t + NT * e, r = i >> 3, x = i & 7;
+                        v[e] = *reinterpret_cast<const uint4*>(sraw + rs * CH + r * 128 + ((x ^ (r & 7)) << 4));
                     }
-                    sh.rec[par][t] = rec;
-                    if constexpr (FP8) {
-                        if (rec != NONE) sc = *reinterpret_cast<const float*>(a.cache + static_cast<long long>(rec) * REC + kFp8ScaleOff);
-                        sh.scale[par][t] = sc;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[rs]));
+                    if (!warp_wait(smem_u32(&sh.empty[s]), ((u / stages) & 1) ^ 1, abort_flag, a.err)) { ok = false; break; }
+#pragma unroll
+                    for (int e = 0; e < NU; ++e) {
+                        const int i = t + NT * e, r = i >> 3, x = i & 7;
+                        put_codes(v[e], smem_u32(sring) + s * PAIR + (x >> 2) * CH + r * 128, 2 * (x & 3), r);
                     }
-                    const uint32_t live = __ballot_sync(0xffffffffu, rec != NONE);
-                    if (lane == 0) sh.live[g & 3][t >> 5] = live;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
                 }
-                bar_sync(2, LOADERS);
-                // rotary keys: 64 records x 8 units
-                if (!mbar_wait(smem_u32(&sh.r_empty[par]), ((g >> 1) & 1) ^ 1, abort_flag, a.err)) { ok = false; break; }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int r = (t >> 3) + 32 * e, x = t & 7;
-                    const long long off = offset(sh.rec[par][r]);
-                    cp16(rope + par * CH + r * 128 + ((x ^ (r & 7)) << 4),
-                         a.cache + (off < 0 ? 0 : off) + (FP8 ? kFp8RopeOff : 2 * kLatent) + 16 * x, off >= 0);
-                }
-                cp_arrive(smem_u32(&sh.r_full[par]));
-                if (t < TT && lane == 0) mbar_arrive(smem_u32(&sh.r_full[par]));      // live is written
-                if constexpr (!FP8) {
-                    for (int c = 0; c < 4; ++c, ++u) {
-                        const uint32_t s = u % stages;
-                        if (!mbar_wait(smem_u32(&sh.empty[s]), ((u / stages) & 1) ^ 1, abort_flag, a.err)) { ok = false; break; }
-                        const int x = t & 15, r0 = t >> 4;             // unit of the 256 bytes, row
-                        const uint32_t dst = ring + s * PAIR + (x >> 3) * CH + (((x & 7) ^ (r0 & 7)) << 4);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int r = r0 + 16 * e;
-                            const long long off = offset(sh.rec[par][r]);
-                            cp16(dst + r * 128, a.cache + (off < 0 ? 0 : off) + 256 * c + 16 * x, off >= 0);
-                        }
-                        cp_arrive(smem_u32(&sh.full[s]));
-                    }
-                } else {
-                    // a thread takes 16 codes of a record in each stage: all loads of the tile first
-                    const int x = t & 7, r0 = t >> 3;
-                    uint4 v[4][2];
-                    float sc[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const long long off = offset(sh.rec[par][r0 + 32 * e]);
-                        sc[e] = sh.scale[par][r0 + 32 * e];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c)
-                            v[c][e] = off < 0 ? make_uint4(0, 0, 0, 0)
-                                              : __ldg(reinterpret_cast<const uint4*>(a.cache + off + 128 * c + 16 * x));
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c, ++u) {
-                        const uint32_t s = u % stages;
-                        if (!mbar_wait(smem_u32(&sh.empty[s]), ((u / stages) & 1) ^ 1, abort_flag, a.err)) { ok = false; break; }
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int r = r0 + 32 * e;
-                            const uint32_t w[4] = {v[c][e].x, v[c][e].y, v[c][e].z, v[c][e].w};
-                            uint32_t o[8];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                o[2 * i] = e4m3x2_to_bf16x2(w[i] & 0xffffu, sc[e]);
-                                o[2 * i + 1] = e4m3x2_to_bf16x2(w[i] >> 16, sc[e]);
-                            }
-                            const uint32_t base = ring + s * PAIR + (x >> 2) * CH + r * 128;
-                            const int y = 2 * (x & 3);
-                            sts16(base + ((y ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-                            sts16(base + (((y + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
-                        }
-                        fence_proxy_async_smem();
-                        mbar_arrive(smem_u32(&sh.full[s]));
-                    }
-                }
-                if (!ok) break;
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");       // nothing is in flight when the block ends
+    } else if (warp == 7) {
+        // -------------------------------------------------------------- loads
+        if (lane == 0) { tma_prefetch_desc(&tmTile); tma_prefetch_desc(&tmRow); }
+        // bf16: stages of 2 boxes for the MMAs; FP8: raw stages of 1 box for the converters
+        constexpr int depth = FP8 ? raws : stages, chunks = FP8 ? 1 : 2, step = FP8 ? 128 : 64;
+        uint64_t* full = FP8 ? sh.raw_full : sh.full;
+        uint64_t* empty = FP8 ? sh.raw_empty : sh.empty;
+        const uint32_t dst = smem_u32(FP8 ? sraw : sring), rope = smem_u32(srope);
+        uint32_t u = 0, g = 0, nr = 0;                 // stages, tiles and rope loads so far
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (lane == 0) ok = mbar_wait(smem_u32(bar), parity, abort_flag, a.err);
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            return ok;
+        };
+        while (ok && next_piece(a, b, tile, left, &p)) {
+            int n0 = page_at(a, p.b, p.len, p.t0 * TT + lane), n1 = page_at(a, p.b, p.len, p.t0 * TT + 32 + lane);
+            for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
+                // lane l: records l and 32 + l of this tile; the next tile's lookup is under way
+                const uint32_t r0 = record_of(a, p.len, ti * TT + lane, n0), r1 = record_of(a, p.len, ti * TT + 32 + lane, n1);
+                if (ti + 1 < p.t1) {
+                    n0 = page_at(a, p.b, p.len, (ti + 1) * TT + lane);
+                    n1 = page_at(a, p.b, p.len, (ti + 1) * TT + 32 + lane);
+                }
+                float s0 = 0.f, s1 = 0.f;
+                if constexpr (FP8) {
+                    if (r0 != NONE) s0 = *reinterpret_cast<const float*>(a.cache + static_cast<long long>(r0) * kRecFp8 + kFp8ScaleOff);
+                    if (r1 != NONE) s1 = *reinterpret_cast<const float*>(a.cache + static_cast<long long>(r1) * kRecFp8 + kFp8ScaleOff);
+                }
+                const Group gr = make_group(r0, r1, lane);
+                for (int c = 0; c < 4; ++c, ++u) {
+                    const uint32_t s = u % depth;
+                    if (!wait(&empty[s], ((u / depth) & 1) ^ 1)) break;
+                    load_group(&tmTile, &tmRow, gr, dst + s * (FP8 ? CH : PAIR), smem_u32(&full[s]), 128 * c, step, chunks, lane);
+                }
+                if (!ok || !wait(&sh.r_empty[g & 1], ((g >> 1) & 1) ^ 1)) break;
+                load_group(&tmTile, &tmRow, gr, rope + (g & 1) * CH, smem_u32(&sh.r_full[g & 1]), kLatent, step, 1, lane);
+                ++nr;
+                // what the softmax of this tile needs (the loader is less than four tiles ahead of it)
+                if constexpr (FP8) {
+                    sh.scale[g & 3][lane] = s0;
+                    sh.scale[g & 3][32 + lane] = s1;
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    sh.live[g & 3][0] = gr.live0;
+                    sh.live[g & 3][1] = gr.live1;
+                    mbar_arrive(smem_u32(&sh.info_full[g & 3]));
+                }
+            }
+        }
+        if (lane == 0) {                                // nothing is in flight when the block ends
+            for (uint32_t e = 1; e <= static_cast<uint32_t>(depth) && e <= u; ++e) drain(&full[(u - e) % depth], ((u - e) / depth) & 1, a.err);
+            for (uint32_t e = 1; e <= 2 && e <= nr; ++e) drain(&sh.r_full[(nr - e) & 1], ((nr - e) >> 1) & 1, a.err);
+        }
+        __syncwarp();
+    } else if (warp >= 5) {
+        // ------------------------------------------------ Q of each sequence
+        const int t = threadIdx.x - 160;
+        uint32_t np = 0;
+        while (next_piece(a, b, tile, left, &p)) {
+            if (!mbar_wait(smem_u32(&sh.q_empty), (np & 1) ^ 1, abort_flag, a.err)) break;
+            // RN rows x 72 sixteen-byte units; rows past the last are zeros
+#pragma unroll 4
+            for (int i = t; i < RN * 72; i += 64) {
+                const int r = i / 72, x = i - r * 72, c = x >> 3, qr = rb * ROWS + r;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < rows) {
+                    const int j = qr / a.H, h = qr - j * a.H;
+                    const long long row = static_cast<long long>(p.b) * a.n_q + j;
+                    v = __ldg(reinterpret_cast<const uint4*>(c < 8 ? a.ql + row * a.ql_row + h * a.ql_head + 8 * x
+                                                                   : a.qr + row * a.qr_row + h * a.qr_head + 8 * (x - 64)));
+                }
+                sts16(smem_u32(sq) + c * QC + r * 128 + (((x & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&sh.q_full));
+            ++np;
+        }
     } else if (warp == 4) {
         // ---------------------------------------------------------------- MMA
-        const uint32_t id_s = idesc_bf16_f32(ROWS, TT), id_o = idesc_bf16_f32_t(128, rn, 1, 0);
+        constexpr uint32_t id_s = idesc_bf16_f32(TT, RN), id_o = idesc_bf16_f32_t(128, RN, 1, 1);
         uint32_t u = 0, g = 0, np = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -308,67 +420,90 @@ decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, fl
             ok = __shfl_sync(0xffffffffu, ok, 0);
             return ok;
         };
-        // S of tile gg whose first ring stage is uu
-        auto score = [&](uint32_t gg, uint32_t uu) {
-            if (!wait(&sh.r_full[gg & 1], (gg >> 1) & 1)) return false;
-            const uint32_t d = tm_s + 64 * (gg & 1);
-            if (elect_one()) {
-                fence_proxy_async_smem();              // the copies' writes, before the tensor cores read them
-                tc_fence_after();
-                const uint64_t ad = smem_desc_sw128(smem_u32(sq + 8 * q_chunk));
-                const uint64_t bd = smem_desc_sw128(smem_u32(srope + (gg & 1) * CH));
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, ad + 2ull * kk, bd + 2ull * kk, id_s, kk > 0);
-                tc_commit(smem_u32(&sh.r_empty[gg & 1]));
-            }
-            __syncwarp();
-            for (int c = 0; c < 4; ++c) {
-                const uint32_t s = (uu + c) % stages;
-                if (!wait(&sh.full[s], ((uu + c) / stages) & 1)) return false;
-                if (elect_one()) {
-                    fence_proxy_async_smem();
-                    tc_fence_after();
-                    for (int e = 0; e < 2; ++e) {
-                        const uint64_t ad = smem_desc_sw128(smem_u32(sq + (2 * c + e) * q_chunk));
-                        const uint64_t bd = smem_desc_sw128(smem_u32(sring + s * PAIR + e * CH));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(d, ad + 2ull * kk, bd + 2ull * kk, id_s, 1);
-                    }
-                }
-                __syncwarp();
-            }
-            if (elect_one()) tc_commit(smem_u32(&sh.s_full[gg & 1]));
-            __syncwarp();
-            return true;
-        };
         while (ok && next_piece(a, b, tile, left, &p)) {
             if (!wait(&sh.q_full, np & 1)) break;
-            if (!score(g, u)) break;
             const int n = p.t1 - p.t0;
-            if (n == 1 && elect_one()) tc_commit(smem_u32(&sh.q_empty));
-            for (int i = 0; i < n; ++i, ++g, u += 4) {
-                if (i + 1 < n) {
-                    if (!score(g + 1, u + 4)) break;
-                    if (i + 2 == n && elect_one()) tc_commit(smem_u32(&sh.q_empty));
+            // Whatever can run next does: the next stage of the scores (at most two tiles ahead of P V, their two
+            // buffers) or P V of the next tile, which frees ring stages and goes first.
+            int si = 0, pi = 0, c = 0;
+            uint32_t spins = 0;
+            uint64_t t0 = 0;
+            while (pi < n) {
+                const uint32_t gs = g + si, gp = g + pi, us = u + 4 * si + c, rs = us % stages;
+                const bool want_s = si < n && si < pi + 2, want_p = pi < si;
+                int go = 0;
+                if (lane == 0) {
+                    if (want_p && mbar_test(smem_u32(&sh.p_full), gp & 1) &&
+                        (pi > 0 || mbar_test(smem_u32(&sh.o_empty), (np & 1) ^ 1)))
+                        go = 2;
+                    else if (want_s && (c < 4 ? mbar_test(smem_u32(&sh.full[rs]), (us / stages) & 1)
+                                              : mbar_test(smem_u32(&sh.r_full[gs & 1]), (gs >> 1) & 1)))
+                        go = 1;
                 }
-                if (i == 0 && !wait(&sh.o_empty, (np & 1) ^ 1)) break;
-                if (!wait(&sh.p_full, g & 1)) break;
-                if (elect_one()) {
-                    tc_fence_after();
-                    const uint64_t bd = smem_desc_sw128(smem_u32(sp));
-                    for (int c = 0; c < 4; ++c) {
-                        const uint32_t s = (u + c) % stages;
-                        const uint32_t v = smem_u32(sring + s * PAIR);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc_mma_bf16(tm_o + c * rn, smem_desc_sw128_mn(v + 2048 * kk, CH), bd + 2ull * kk, id_o,
-                                        i > 0 || kk > 0);
-                        tc_commit(smem_u32(&sh.empty[s]));
+                go = __shfl_sync(0xffffffffu, go, 0);
+                if (go == 0) {
+                    // nothing to do yet: bounded in time
+                    if ((++spins & 255u) == 0) {
+                        if (lane == 0) {
+                            const uint64_t now = globaltimer_ns();
+                            if (t0 == 0) t0 = now;
+                            if (*abort_flag) ok = false;
+                            else if (now - t0 > kWaitLimitNs) { ok = false; *abort_flag = 1; set_dev_error(a.err, DEV_ERR_TIMEOUT); }
+                        }
+                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                        if (!ok) break;
                     }
-                    tc_commit(smem_u32(&sh.pv_done));
+                    continue;
                 }
-                __syncwarp();
+                spins = 0;
+                t0 = 0;
+                if (go == 1) {
+                    if (elect_one()) {
+                        tc_fence_after();
+                        if (c < 4) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint64_t bd = smem_desc_sw128(smem_u32(sq + (2 * c + e) * QC));
+                                const uint64_t ad = smem_desc_sw128(smem_u32(sring + rs * PAIR + e * CH));
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk)
+                                    tc_mma_bf16(tm_s + 64 * (gs & 1), ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || e > 0 || kk > 0);
+                            }
+                        } else {
+                            const uint64_t bd = smem_desc_sw128(smem_u32(sq + 8 * QC));
+                            const uint64_t ad = smem_desc_sw128(smem_u32(srope + (gs & 1) * CH));
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma_bf16((FP8 ? tm_r : tm_s) + 64 * (gs & 1), ad + 2ull * kk, bd + 2ull * kk, id_s, !FP8 || kk > 0);
+                            tc_commit(smem_u32(&sh.r_empty[gs & 1]));
+                            tc_commit(smem_u32(&sh.s_full[gs & 1]));
+                            if (si + 1 == n) tc_commit(smem_u32(&sh.q_empty));
+                        }
+                    }
+                    __syncwarp();
+                    if (++c == 5) { c = 0; ++si; }
+                } else {
+                    if (elect_one()) {
+                        tc_fence_after();
+                        const uint64_t bd = smem_desc_sw128_mn(smem_u32(sp), CH);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t st = (u + 4 * pi + q) % stages;
+                            const uint64_t ad = smem_desc_sw128_mn(smem_u32(sring + st * PAIR), CH);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                tc_mma_bf16(tm_o + q * RN, ad + 128ull * kk, bd + 128ull * kk, id_o, pi > 0 || kk > 0);
+                            tc_commit(smem_u32(&sh.empty[st]));
+                        }
+                        tc_commit(smem_u32(&sh.pv_done));
+                    }
+                    __syncwarp();
+                    ++pi;
+                }
             }
+            if (!ok) break;
+            g += n;
+            u += 4 * n;
             ++np;
         }
         if (elect_one()) {
@@ -380,14 +515,12 @@ decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, fl
         __syncwarp();
     } else {
         // ------------------------------------- softmax, rescaling and output
-        // S rows 16 w .. 16 w + 15 lie in the first 16 lanes of warp w's TMEM quarter
-        const int r = 16 * warp + (lane & 15);
-        const bool mine = lane < 16 && r < rows;
-        const int qrow = rb * ROWS + min(r, rows - 1), j = qrow / a.H, h = qrow - j * a.H;
+        // (a wait that gives up does not leave the loops: the four warps meet at barriers)
+        // S^T rows (records) 16 w .. 16 w + 15 lie in the first 16 lanes of warp w's TMEM quarter
+        const int rec = 16 * warp + (lane & 15);
         const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
         const float c = a.scale * kLog2e;
         uint32_t g = 0;
-        bool ok = true;
         // sequences without records: zero rows, spread over the ranges
         for (int e = range; e < a.B; e += ranges) {
             if (seq_len(a, e) != 0) continue;
@@ -398,121 +531,166 @@ decode_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, fl
                 if (a.lse && (i & 63) == 0) a.lse[row * a.H + hh] = -CUDART_INF_F;
             }
         }
-        while (ok && next_piece(a, b, tile, left, &p)) {
-            const int end = p.len - (a.n_q - 1 - j);           // this row sees positions [0, end)
-            float m = -CUDART_INF_F, l = 0.f;
+        while (next_piece(a, b, tile, left, &p)) {
+            float l[RN];
+#pragma unroll
+            for (int i = 0; i < RN; ++i) l[i] = 0.f;
             for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
-                if (!mbar_wait(smem_u32(&sh.s_full[g & 1]), (g >> 1) & 1, abort_flag, a.err)) { ok = false; break; }
+                mbar_wait(smem_u32(&sh.info_full[g & 3]), (g >> 2) & 1, abort_flag, a.err);
+                mbar_wait(smem_u32(&sh.s_full[g & 1]), (g >> 1) & 1, abort_flag, a.err);
                 tc_fence_after();
-                uint32_t s[2][32];
-                tmem_ld32(tm_s + 64 * (g & 1) + lane_base, s[0]);
-                tmem_ld32(tm_s + 64 * (g & 1) + 32 + lane_base, s[1]);
-                tmem_ld_wait();
-                const int lim = mine ? end - ti * TT : 0;
-                uint32_t live[2] = {sh.live[g & 3][0], sh.live[g & 3][1]};
+                uint32_t s[RN];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int k = lim - 32 * q;
-                    live[q] &= k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u);
+                for (int q = 0; q < RN / 16; ++q) {
+                    uint32_t (&part16)[16] = *reinterpret_cast<uint32_t (*)[16]>(&s[16 * q]);
+                    tmem_ld16(tm_s + 64 * (g & 1) + 16 * q + lane_base, part16);
                 }
-                if (__any_sync(0xffffffffu, (live[0] & live[1]) != 0xffffffffu)) {
+                if constexpr (FP8) {
+                    const float sc = sh.scale[g & 3][rec];
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!((live[q] >> e) & 1u)) s[q][e] = 0xff800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    mx[q] = __uint_as_float(s[q >> 1][16 * (q & 1)]);
-#pragma unroll
-                    for (int e = 1; e < 16; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(s[q >> 1][16 * (q & 1) + e]));
-                }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
-                float al = 1.f;
-                bool grow = false;
-                if (ti == p.t0) {
-                    m = top;
-                } else if (top > m + kRescale) {               // also the first record a row sees (m = -inf)
-                    grow = true;
-                    al = exp2_fast(m - top);
-                    m = top;
-                    l *= al;
-                }
-                const bool any = __any_sync(0xffffffffu, grow);
-                if (lane < 16) sh.alpha[g & 1][r] = al;
-                if (lane == 0) sh.flag[g & 1][warp] = any;
-                bar_sync(1, 128);
-                // P and O are free once the product of the tile before is done
-                if (g > 0 && !mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err)) { ok = false; break; }
-                const int* fl = sh.flag[g & 1];
-                if (fl[0] | fl[1] | fl[2] | fl[3]) {
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int cc = 0; cc < 4 * rn; cc += 16) {
-                        uint32_t o[16];
-                        tmem_ld16(tm_o + cc + lane_base, o);
+                    for (int q = 0; q < RN / 16; ++q) {
+                        uint32_t kr[16];
+                        tmem_ld16(tm_r + 64 * (g & 1) + 16 * q + lane_base, kr);
                         tmem_ld_wait();
-                        const float4* f4 = reinterpret_cast<const float4*>(&sh.alpha[g & 1][cc % rn]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float4 f = f4[e];
-                            o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) * f.x);
-                            o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) * f.y);
-                            o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) * f.z);
-                            o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) * f.w);
-                        }
-                        tmem_st16(tm_o + cc + lane_base, o);
+                        for (int i = 0; i < 16; ++i)
+                            s[16 * q + i] = __float_as_uint(fmaf(__uint_as_float(s[16 * q + i]), sc, __uint_as_float(kr[i])));
                     }
-                    tmem_st_wait();
                 }
-                const float me = m == -CUDART_INF_F ? 0.f : m;
-                float sum[2] = {0.f, 0.f};
-                const uint32_t prow = smem_u32(sp) + r * 128;
+                tmem_ld_wait();
+                const bool live = lane < 16 && ((sh.live[g & 3][rec >> 5] >> (rec & 31)) & 1u);
+                const int pos = ti * TT + rec;
+                // rows of earlier new tokens see fewer positions: query j sees [0, len - (n_q - 1 - j))
+                const bool edge = a.n_q > 1 && ti * TT + TT > p.len - a.n_q + 1;
+                if (edge) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                    for (int i = 0; i < RN; ++i)
+                        if (pos >= p.len - (a.n_q - 1 - min((rb * ROWS + i) / a.H, a.n_q - 1))) s[i] = 0xff800000u;
+                }
+                float over = -CUDART_INF_F;                     // the largest excess over the running maxima
+                if (ti > p.t0) {
+                    const float4* m4 = reinterpret_cast<const float4*>(sh.m);
+#pragma unroll
+                    for (int q = 0; q < RN / 4; ++q) {
+                        const float4 m = m4[q];
+                        over = fmaxf(over, fmaxf(fmaxf(fmaf(__uint_as_float(s[4 * q]), c, -m.x), fmaf(__uint_as_float(s[4 * q + 1]), c, -m.y)),
+                                                 fmaxf(fmaf(__uint_as_float(s[4 * q + 2]), c, -m.z), fmaf(__uint_as_float(s[4 * q + 3]), c, -m.w))));
+                    }
+                }
+                if (bar_any(1, 128, ti == p.t0 || (live && over > kRescale))) {
+                    // new maxima: over the warp's records by shuffles, over the warps through shared memory
+                    for (int i0 = 0; i0 < RN; i0 += 16) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float v = -CUDART_INF_F;
+#pragma unroll
+                            for (int q = 0; q < RN / 16; ++q)
+                                if (i0 == 16 * q) v = __uint_as_float(s[16 * q + i]) * c;
+                            if (!live) v = -CUDART_INF_F;
+#pragma unroll
+                            for (int d = 8; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+                            if (lane == 0) sh.red[warp][i0 + i] = v;
+                        }
+                    }
+                    bar_sync(1, 128);
+                    if (threadIdx.x < RN) {
+                        const int i = threadIdx.x;
+                        const float old = ti == p.t0 ? -CUDART_INF_F : sh.m[i];
+                        // a row that has seen nothing yet keeps a harmless maximum of -1e30 (its p are 2^-inf = 0)
+                        const float top = fmaxf(fmaxf(fmaxf(sh.red[0][i], sh.red[1][i]), fmaxf(sh.red[2][i], sh.red[3][i])), -1e30f);
+                        const float nm = top > old + kRescale ? top : fmaxf(old, -1e30f);
+                        sh.f[i] = exp2_fast(old - nm);
+                        sh.m[i] = nm;
+                    }
+                    bar_sync(1, 128);
+                    if (ti > p.t0) {
+#pragma unroll
+                        for (int i = 0; i < RN; ++i) l[i] *= sh.f[i];
+                        // O^T is complete up to the tile before
+                        mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int cc = 0; cc < 4 * RN; cc += 16) {
+                            uint32_t o[16];
+                            tmem_ld16(tm_o + cc + lane_base, o);
+                            tmem_ld_wait();
+                            const float4* f4 = reinterpret_cast<const float4*>(&sh.f[cc % RN]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float4 f = f4[e];
+                                o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) * f.x);
+                                o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) * f.y);
+                                o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) * f.z);
+                                o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) * f.w);
+                            }
+                            tmem_st16(tm_o + cc + lane_base, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                // P is free once the product of the tile before is done
+                if (g > 0) mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
+                const float4* m4 = reinterpret_cast<const float4*>(sh.m);
+                const uint32_t prow = smem_u32(sp) + rec * 128;
+                const float vs = FP8 ? sh.scale[g & 3][rec] : 1.f;      // V's rows are codes
+#pragma unroll
+                for (int q = 0; q < RN / 8; ++q) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float x0 = exp2_fast(fmaf(__uint_as_float(s[q >> 2][8 * (q & 3) + 2 * e]), c, -me));
-                        const float x1 = exp2_fast(fmaf(__uint_as_float(s[q >> 2][8 * (q & 3) + 2 * e + 1]), c, -me));
-                        sum[0] += x0;
-                        sum[1] += x1;
-                        w[e] = pack_bf16x2(x0, x1);
+                    for (int e = 0; e < 2; ++e) {
+                        const float4 m = m4[2 * q + e];
+                        const int i = 8 * q + 4 * e;
+                        float x0 = exp2_fast(fmaf(__uint_as_float(s[i]), c, -m.x)), x1 = exp2_fast(fmaf(__uint_as_float(s[i + 1]), c, -m.y));
+                        float x2 = exp2_fast(fmaf(__uint_as_float(s[i + 2]), c, -m.z)), x3 = exp2_fast(fmaf(__uint_as_float(s[i + 3]), c, -m.w));
+                        if (!live) x0 = x1 = x2 = x3 = 0.f;
+                        l[i] += x0; l[i + 1] += x1; l[i + 2] += x2; l[i + 3] += x3;
+                        if constexpr (FP8) { x0 *= vs; x1 *= vs; x2 *= vs; x3 *= vs; }
+                        w[2 * e] = pack_bf16x2(x0, x1);
+                        w[2 * e + 1] = pack_bf16x2(x2, x3);
                     }
-                    if (lane < 16 && r < rn) sts16(prow + ((q ^ (r & 7)) << 4), w[0], w[1], w[2], w[3]);
+                    if (lane < 16) sts16(prow + ((q ^ (rec & 7)) << 4), w[0], w[1], w[2], w[3]);
                 }
-                l += sum[0] + sum[1];
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh.p_full));
             }
-            if (!ok) break;
-            if (!mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err)) break;
-            tc_fence_after();
-            const bool whole = p.t0 == 0 && p.t1 == p.n;
-            const long long slot = (static_cast<long long>(range) * rb_count + rb) * 2 + (p.b == sh.b0 ? 0 : 1);
-            if (lane < 16) sh.alpha[g & 1][r] = l > 0.f ? 1.f / l : 0.f;
-            if (mine) {
-                const float lse = l > 0.f ? m + log2f(l) : -CUDART_INF_F;      // log2 units
-                if (!whole) part_lse[slot * ROWS + r] = lse;
-                else if (a.lse) a.lse[(static_cast<long long>(p.b) * a.n_q + j) * a.H + h] = lse * kLn2;
+            // l over the records
+#pragma unroll
+            for (int i = 0; i < RN; ++i) {
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], d);
+                if (lane == 0) sh.red[warp][i] = l[i];
             }
             bar_sync(1, 128);
+            const bool whole = p.t0 == 0 && p.t1 == p.n;
+            const long long slot = (static_cast<long long>(range) * rb_count + rb) * 2 + (p.b == sh.b0 ? 0 : 1);
+            if (threadIdx.x < RN) {
+                const int i = threadIdx.x;
+                const float z = (sh.red[0][i] + sh.red[1][i]) + (sh.red[2][i] + sh.red[3][i]);
+                sh.f[i] = z != 0.f ? 1.f / z : 0.f;
+                if (i < rows) {
+                    const float lse = z != 0.f ? sh.m[i] + log2f(z) : -CUDART_INF_F;       // log2 units
+                    const int q = rb * ROWS + i, j = q / a.H, h = q - j * a.H;
+                    if (!whole) part_lse[slot * ROWS + i] = lse;
+                    else if (a.lse) a.lse[(static_cast<long long>(p.b) * a.n_q + j) * a.H + h] = lse * kLn2;
+                }
+            }
+            bar_sync(1, 128);
+            mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
+            tc_fence_after();
             // O^T: lane = latent element, column = row
 #pragma unroll 1
-            for (int cc = 0; cc < 4 * rn; cc += 16) {
+            for (int cc = 0; cc < 4 * RN; cc += 16) {
                 uint32_t o[16];
                 tmem_ld16(tm_o + cc + lane_base, o);
                 tmem_ld_wait();
-                const int d = (cc / rn) * 128 + 32 * warp + lane, r0 = cc % rn;
+                const int d = (cc / RN) * 128 + 32 * warp + lane, r0 = cc % RN;
                 int qq = rb * ROWS + r0, jj = qq / a.H, hh = qq - jj * a.H;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     if (r0 + e < rows) {
-                        const float f = sh.alpha[g & 1][r0 + e];
-                        const float v = f > 0.f ? __uint_as_float(o[e]) * f : 0.f;
+                        const float f = sh.f[r0 + e];
+                        const float v = f != 0.f ? __uint_as_float(o[e]) * f : 0.f;
                         if (whole)
                             a.out[(static_cast<long long>(p.b) * a.n_q + jj) * a.o_row + hh * a.o_head + d] = __float2bfloat16(v);
                         else
@@ -604,12 +782,12 @@ join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, cons
         const float4 v = __ldg(reinterpret_cast<const float4*>(part + (static_cast<long long>(slots[k]) * ROWS + r) * kLatent) + threadIdx.x);
         acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
     }
-    const float inv = z > 0.f ? 1.f / z : 0.f;
+    const float inv = z != 0.f ? 1.f / z : 0.f;
     const int j = q / a.H, h = q - j * a.H;
     const long long row = static_cast<long long>(m.b) * a.n_q + j;
     reinterpret_cast<uint2*>(a.out + row * a.o_row + h * a.o_head)[threadIdx.x] =
         make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (a.lse && threadIdx.x == 0) a.lse[row * a.H + h] = z > 0.f ? (z_ref[1] + log2f(z)) * kLn2 : -CUDART_INF_F;
+    if (a.lse && threadIdx.x == 0) a.lse[row * a.H + h] = z != 0.f ? (z_ref[1] + log2f(z)) * kLn2 : -CUDART_INF_F;
 }
 
 
@@ -629,21 +807,31 @@ size_t latent_decode_ws_bytes(int H, int, int n_q) {
 }
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, cudaStream_t st) {
-    static bool attr[2][kMaxDevices] = {{false}};
-    auto fn = fp8 ? dc::decode_kernel<true> : dc::decode_kernel<false>;
-    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), dc::SMEM, attr[fp8]);
-    if (e != cudaSuccess) return e;
+    static bool attr[2][3][kMaxDevices] = {{{false}}};
+    using Fn = void (*)(CUtensorMap, CUtensorMap, LatentDecodeArgs, int, int, float*, float*, dc::Meta*);
+    static const Fn fns[2][3] = {{dc::decode_kernel<false, 16>, dc::decode_kernel<false, 32>, dc::decode_kernel<false, 64>},
+                                 {dc::decode_kernel<true, 16>, dc::decode_kernel<true, 32>, dc::decode_kernel<true, 64>}};
     int rb, ranges;
     dc::shape(a.H, a.n_q, &rb, &ranges);
+    const int rows = a.H * a.n_q < dc::ROWS ? a.H * a.n_q : dc::ROWS;
+    const int v = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
+    const Fn fn = fns[fp8][v];
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), dc::SMEM, attr[fp8][v]);
+    CUtensorMap tile{}, row{};
+    const long long records = a.n_pages * a.page_size;
+    const int cols = fp8 ? kRecFp8 : kLatent + kRope;          // elements of a record (FP8: bytes)
+    if (e == cudaSuccess) e = make_map(&tile, a.cache, records, cols, dc::TT, fp8);
+    if (e == cudaSuccess) e = make_map(&row, a.cache, records, cols, 1, fp8);
+    if (e != cudaSuccess) return e;
     const size_t slots = static_cast<size_t>(rb) * ranges * 2;
     float* part = static_cast<float*>(ws);
     float* part_lse = part + slots * dc::ROWS * kLatent;
     dc::Meta* meta = reinterpret_cast<dc::Meta*>(part_lse + slots * dc::ROWS);
-    fn<<<static_cast<unsigned>(rb * ranges), dc::THREADS, dc::SMEM, st>>>(a, rb, ranges, part, part_lse, meta);
+    fn<<<static_cast<unsigned>(rb * ranges), 32 * (8 + (!fp8 ? 0 : (v == 2 ? 4 : 8))), dc::SMEM, st>>>(tile, row, a, rb, ranges, part,
+                                                                                       part_lse, meta);
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess || ranges == 1) return e;
-    const int rows = a.H * a.n_q < dc::ROWS ? a.H * a.n_q : dc::ROWS;
     dc::join_kernel<<<dim3(ranges - 1, rows, rb), 128, 0, st>>>(a, rb, ranges, part, part_lse, meta);
     count_launch();
     return cudaGetLastError();

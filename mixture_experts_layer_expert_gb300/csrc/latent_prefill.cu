@@ -327,7 +327,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
             const uint32_t slot = k & 1;
-            if (!mbar_wait(smem_u32(&sh.item_full[slot]), (k >> 1) & 1, abort_flag, a.err)) break;
+            if (!warp_wait(smem_u32(&sh.item_full[slot]), (k >> 1) & 1, abort_flag, a.err)) break;
             const Item it = sh.item[slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[slot]));
@@ -336,7 +336,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             const int limit = row_limit(it, a.causal, r);
             float m = 0.f, l = 0.f;
             for (int i = 0; i < it.n[t]; ++i) {
-                if (!mbar_wait(smem_u32(&sh.s_full[t]), ns++ & 1, abort_flag, a.err)) { ok = false; break; }
+                if (!warp_wait(smem_u32(&sh.s_full[t]), ns++ & 1, abort_flag, a.err)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t s[4][32];
 #pragma unroll
@@ -365,7 +365,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     const float mn = fmaxf(m, top), al = exp2_fast(m - mn);
                     m = mn;
                     l *= al;
-                    if (!mbar_wait(smem_u32(&sh.pv_done[t]), (npv + i - 1) & 1, abort_flag, a.err)) { ok = false; break; }
+                    if (!warp_wait(smem_u32(&sh.pv_done[t]), (npv + i - 1) & 1, abort_flag, a.err)) { ok = false; break; }
                     tc_fence_after();
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
@@ -400,10 +400,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             const int n = it.n[t];
             npv += n;
             if (n > 0) {
-                if (!mbar_wait(smem_u32(&sh.pv_done[t]), (npv - 1) & 1, abort_flag, a.err)) break;
+                if (!warp_wait(smem_u32(&sh.pv_done[t]), (npv - 1) & 1, abort_flag, a.err)) break;
                 tc_fence_after();
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l != 0.f ? 1.f / l : 0.f;
             const bool mine = r < it.rows;
             __nv_bfloat16* dst = a.out_w + (static_cast<long long>(it.row0) + r) * a.o_row +
                                  static_cast<long long>(it.head) * a.o_head;
@@ -420,7 +420,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         uint32_t w[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            w[j] = l > 0.f ? pack_bf16x2(__uint_as_float(o[8 * v + 2 * j]) * inv,
+                            w[j] = l != 0.f ? pack_bf16x2(__uint_as_float(o[8 * v + 2 * j]) * inv,
                                                          __uint_as_float(o[8 * v + 2 * j + 1]) * inv) : 0u;
                         reinterpret_cast<uint4*>(dst)[4 * q + v] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
@@ -428,7 +428,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
             if (mine)
                 a.lse_w[static_cast<long long>(it.head) * a.Tq + it.row0 + r] =
-                    l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
+                    l != 0.f ? (m + log2f(l)) * 0.6931471805599453f : -CUDART_INF_F;
             tc_fence_before();
         }
     }

@@ -555,20 +555,34 @@ LATENT, ROPE_DIM, NOPE_DIM, V_DIM = 512, 64, 128, 128      # widths of the laten
 LATENT_RECORD = {"bf16": 2 * (LATENT + ROPE_DIM), "fp8": LATENT + 2 * ROPE_DIM + 16}      # bytes per cached token
 
 
-def _operand(what: str, t: torch.Tensor, shape, dtype=torch.bfloat16, strided=True):
-    """Refuse a tensor whose shape, type, inner stride or device the call could not take:
-    the C entry sees only a pointer."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+def _here(stream):
+    """(current device, raw stream) of a call, without building a Stream object when none is given."""
+    try:
+        dev = torch.cuda.current_device()
+    except (RuntimeError, AssertionError) as e:
+        raise FsError(4, "current device", str(e)) from None
+    if stream is not None and stream.device_index != dev:
+        raise FsError(1, "stream", "of cuda:%d, not of the current device" % stream.device_index)
+    return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _operand(what: str, t: torch.Tensor, shape, dev: int, dtype=torch.bfloat16, strided=True):
+    """Refuse a tensor whose shape, type, inner stride or device the call could not take: the C entry sees only a
+    pointer.  Returns (pointer, strides)."""
+    st = t.stride()
+    if t.shape != shape or t.dtype is not dtype:
         raise FsError(1, what, "got %s %s, expected %s %s" % (tuple(t.shape), t.dtype, tuple(shape), dtype))
-    if (t.numel() and t.stride(-1) != 1 and t.shape[-1] > 1) or (not strided and not t.is_contiguous()):
-        raise FsError(1, what, "strides %s" % (t.stride(),))
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if (st[-1] != 1 and shape[-1] > 1) or not (strided or t.is_contiguous()):
+        raise FsError(1, what, "strides %s" % (st,))
+    if t.get_device() != dev:
         raise FsError(1, what, "tensor on %s, not on the current device" % t.device)
+    return t.data_ptr(), st
 
 
-def _rows(t: torch.Tensor) -> Rows:
-    """[rows, heads, width] or [rows, width] -> (pointer, row stride, head stride)."""
-    return Rows(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0)
+def _rows(ptr_strides) -> Rows:
+    """(pointer, strides) of [rows, heads, width] or [rows, width] -> (pointer, row stride, head stride)."""
+    p, st = ptr_strides
+    return Rows(p, st[0], st[1] if len(st) == 3 else 0)
 
 
 def make_rope(d_rot: int, layout: str = "interleaved", base: float = 10000.0, factor: float = 1.0,
@@ -578,13 +592,15 @@ def make_rope(d_rot: int, layout: str = "interleaved", base: float = 10000.0, fa
 
 def fs_rope(rope: RopeDesc, pos, x, y, inverse: bool = False, stream=None):
     """Rotate x [T, H, d_rot] (a view of the rotated part of each head) into y (which may be x)."""
-    T, H = x.shape[0], x.shape[1]
-    dt = torch.float32 if x.dtype == torch.float32 else torch.bfloat16
-    _operand("fs_rope x", x, (T, H, rope.d_rot), dt)
-    _operand("fs_rope y", y, (T, H, rope.d_rot), dt)
-    _operand("fs_rope pos", pos, (T,), torch.int32)
-    _check(lib().fs_rope(ctypes.byref(rope), T, H, _dtype_code(x), _p(pos), _p(x), x.stride(0), x.stride(1), _p(y),
-                         y.stride(0), y.stride(1), int(inverse), _stream(stream)), "fs_rope")
+    dev, st = _here(stream)
+    T, H, _ = x.shape
+    f32 = x.dtype is torch.float32
+    dt = torch.float32 if f32 else torch.bfloat16
+    xp, xs = _operand("fs_rope x", x, (T, H, rope.d_rot), dev, dt)
+    yp, ys = _operand("fs_rope y", y, (T, H, rope.d_rot), dev, dt)
+    pp, _ = _operand("fs_rope pos", pos, (T,), dev, torch.int32)
+    _check(lib().fs_rope(rope, T, H, FS_F32 if f32 else FS_BF16, pp, xp, xs[0], xs[1], yp, ys[0], ys[1], inverse,
+                         st), "fs_rope")
 
 
 def make_latent_cache(n_pages: int, page_size: int, dtype: str = "bf16") -> LatentCache:
@@ -604,36 +620,35 @@ def latent_cache_empty(desc: LatentCache, device="cuda") -> torch.Tensor:
     return torch.empty((desc.n_pages, desc.page_size, LATENT_RECORD["fp8"]), dtype=torch.uint8, device=device)
 
 
-def _cache_operand(what, desc, cache):
-    f8 = desc.dtype == FS_FP8
-    _operand(what, cache, (desc.n_pages, desc.page_size, LATENT_RECORD["fp8"] if f8 else LATENT + ROPE_DIM),
-             torch.uint8 if f8 else torch.bfloat16, strided=False)
+def _cache_operand(what, desc, cache, dev):
+    if desc.dtype == FS_FP8:
+        return _operand(what, cache, (desc.n_pages, desc.page_size, LATENT_RECORD["fp8"]), dev, torch.uint8, False)[0]
+    return _operand(what, cache, (desc.n_pages, desc.page_size, LATENT + ROPE_DIM), dev, torch.bfloat16, False)[0]
 
 
 def fs_latent_cache_write(desc: LatentCache, c, k_rope, slots, cache, rope: RopeDesc | None = None, pos=None,
                           stream=None):
     """Write c [T, 512], k_rope [T, 64] (rotated by rope at pos when given) to the slots [T] (int64; negative: skipped)."""
+    dev, st = _here(stream)
     T, what = c.shape[0], "fs_latent_cache_write"
-    _operand(what + " c", c, (T, LATENT))
-    _operand(what + " k_rope", k_rope, (T, ROPE_DIM))
-    _operand(what + " slots", slots, (T,), torch.int64)
-    _cache_operand(what + " cache", desc, cache)
-    if pos is not None:
-        _operand(what + " pos", pos, (T,), torch.int32)
-    _check(lib().fs_latent_cache_write(ctypes.byref(desc), T, _p(c), c.stride(0), _p(k_rope), k_rope.stride(0),
-                                       None if rope is None else ctypes.byref(rope), _p(pos), _p(slots), _p(cache),
-                                       _stream(stream)), what)
+    cp, cs = _operand("fs_latent_cache_write c", c, (T, LATENT), dev)
+    kp, ks = _operand("fs_latent_cache_write k_rope", k_rope, (T, ROPE_DIM), dev)
+    sp, _ = _operand("fs_latent_cache_write slots", slots, (T,), dev, torch.int64)
+    pp = None if pos is None else _operand("fs_latent_cache_write pos", pos, (T,), dev, torch.int32)[0]
+    _check(lib().fs_latent_cache_write(desc, T, cp, cs[0], kp, ks[0], rope, pp, sp,
+                                       _cache_operand("fs_latent_cache_write cache", desc, cache, dev),
+                                       st), what)
 
 
 def fs_latent_cache_read(desc: LatentCache, cache, slots, c, k_rope, stream=None):
     """Read the records of slots [T] back into c [T, 512], k_rope [T, 64] (rows with a negative slot are left)."""
+    dev, st = _here(stream)
     T, what = slots.shape[0], "fs_latent_cache_read"
-    _operand(what + " slots", slots, (T,), torch.int64)
-    _operand(what + " c", c, (T, LATENT))
-    _operand(what + " k_rope", k_rope, (T, ROPE_DIM))
-    _cache_operand(what + " cache", desc, cache)
-    _check(lib().fs_latent_cache_read(ctypes.byref(desc), _p(cache), T, _p(slots), _p(c), c.stride(0), _p(k_rope),
-                                      k_rope.stride(0), _stream(stream)), what)
+    sp, _ = _operand("fs_latent_cache_read slots", slots, (T,), dev, torch.int64)
+    cp, cs = _operand("fs_latent_cache_read c", c, (T, LATENT), dev)
+    kp, ks = _operand("fs_latent_cache_read k_rope", k_rope, (T, ROPE_DIM), dev)
+    _check(lib().fs_latent_cache_read(desc, _cache_operand("fs_latent_cache_read cache", desc, cache, dev), T, sp, cp, cs[0],
+                                      kp, ks[0], st), what)
 
 
 def fs_latent_decode_ws_bytes(heads: int, B: int, n_q: int = 1) -> int:
@@ -645,42 +660,41 @@ def fs_latent_decode(desc: LatentCache, q_latent, q_rope, cache, block_table, se
     """Absorbed attention of the newest n_q tokens of B sequences: q_latent [B n_q, H, 512], q_rope [B n_q, H, 64],
     block_table [B, max_pages] int32, seq_lens [B] int32 -> out [B n_q, H, 512], lse [B n_q, H] (or None);
     ws: fs_latent_decode_ws_bytes(H, B, n_q) bytes."""
-    what, (rows, H) = "fs_latent_decode", q_latent.shape[:2]
+    dev, st = _here(stream)
+    rows, H, _ = q_latent.shape
     B, max_pages = block_table.shape
     n_q = rows // max(B, 1)
-    _operand(what + " q_latent", q_latent, (B * n_q, H, LATENT))
-    _operand(what + " q_rope", q_rope, (B * n_q, H, ROPE_DIM))
-    _operand(what + " out", out, (B * n_q, H, LATENT))
-    _operand(what + " block_table", block_table, (B, max_pages), torch.int32)
-    _operand(what + " seq_lens", seq_lens, (B,), torch.int32)
-    _cache_operand(what + " cache", desc, cache)
-    if lse is not None:
-        _operand(what + " lse", lse, (B * n_q, H), torch.float32, strided=False)
-    _check(lib().fs_latent_decode(ctypes.byref(desc), H, B, n_q, _rows(q_latent), _rows(q_rope), _p(cache),
-                                  _p(block_table), max_pages, block_table.stride(0), _p(seq_lens), scale, _rows(out),
-                                  _p(lse), _p(ws), _nbytes(ws), _stream(stream)), what)
+    rows = B * n_q
+    ql = _rows(_operand("fs_latent_decode q_latent", q_latent, (rows, H, LATENT), dev))
+    qr = _rows(_operand("fs_latent_decode q_rope", q_rope, (rows, H, ROPE_DIM), dev))
+    op = _rows(_operand("fs_latent_decode out", out, (rows, H, LATENT), dev))
+    tp, ts = _operand("fs_latent_decode block_table", block_table, (B, max_pages), dev, torch.int32)
+    lp, _ = _operand("fs_latent_decode seq_lens", seq_lens, (B,), dev, torch.int32)
+    ep = None if lse is None else _operand("fs_latent_decode lse", lse, (rows, H), dev, torch.float32, False)[0]
+    wp, _ = _operand("fs_latent_decode ws", ws, ws.shape, dev, torch.uint8, False)
+    _check(lib().fs_latent_decode(desc, H, B, n_q, ql, qr, _cache_operand("fs_latent_decode cache", desc, cache, dev), tp,
+                                  max_pages, ts[0], lp, scale, op, ep, wp, ws.numel(), st),
+           "fs_latent_decode")
 
 
-def _prefill_operands(what, q, k_nope, k_rope, v, cu_q, cu_k, causal, scale) -> LatentPrefillDesc:
-    (Tq, H), Tk, B = q.shape[:2], k_rope.shape[0], cu_q.shape[0] - 1
-    _operand(what + " q", q, (Tq, H, NOPE_DIM + ROPE_DIM))
-    _operand(what + " k_nope", k_nope, (Tk, H, NOPE_DIM))
-    _operand(what + " k_rope", k_rope, (Tk, ROPE_DIM))
-    _operand(what + " v", v, (Tk, H, V_DIM))
-    _operand(what + " cu_q", cu_q, (B + 1,), torch.int32)
-    _operand(what + " cu_k", cu_k, (B + 1,), torch.int32)
-    return LatentPrefillDesc(H, B, Tq, Tk, int(causal), scale)
+def _prefill_operands(what, dev, q, k_nope, k_rope, v, cu_q, cu_k, causal, scale):
+    """The descriptor and the operands that the forward and the backward share."""
+    (Tq, H, _), Tk, B = q.shape, k_rope.shape[0], cu_q.shape[0] - 1
+    return (LatentPrefillDesc(H, B, Tq, Tk, bool(causal), scale),
+            _rows(_operand(what, q, (Tq, H, NOPE_DIM + ROPE_DIM), dev)), _rows(_operand(what, k_nope, (Tk, H, NOPE_DIM), dev)),
+            _rows(_operand(what, k_rope, (Tk, ROPE_DIM), dev)), _rows(_operand(what, v, (Tk, H, V_DIM), dev)),
+            _operand(what, cu_q, (B + 1,), dev, torch.int32)[0], _operand(what, cu_k, (B + 1,), dev, torch.int32)[0])
 
 
 def fs_latent_prefill(q, k_nope, k_rope, v, cu_q, cu_k, causal, scale, out, lse, stream=None):
     """Expanded attention over packed sequences: q [Tq, H, 192], k_nope and v [Tk, H, 128], k_rope [Tk, 64],
     cu_q and cu_k [B + 1] int32 -> out [Tq, H, 128], lse [H, Tq] fp32."""
     what = "fs_latent_prefill"
-    d = _prefill_operands(what, q, k_nope, k_rope, v, cu_q, cu_k, causal, scale)
-    _operand(what + " out", out, (d.Tq, d.heads, V_DIM))
-    _operand(what + " lse", lse, (d.heads, d.Tq), torch.float32, strided=False)
-    _check(lib().fs_latent_prefill(ctypes.byref(d), _rows(q), _rows(k_nope), _rows(k_rope), _rows(v), _p(cu_q),
-                                   _p(cu_k), _rows(out), _p(lse), _stream(stream)), what)
+    dev, st = _here(stream)
+    ops = _prefill_operands(what, dev, q, k_nope, k_rope, v, cu_q, cu_k, causal, scale)
+    Tq, H, _ = q.shape
+    _check(lib().fs_latent_prefill(*ops, _rows(_operand(what, out, (Tq, H, V_DIM), dev)),
+                                   _operand(what, lse, (H, Tq), dev, torch.float32, False)[0], st), what)
 
 
 def fs_latent_prefill_backward_ws_bytes(heads: int, Tq: int, Tk: int) -> int:
@@ -692,13 +706,12 @@ def fs_latent_prefill_backward(q, k_nope, k_rope, v, cu_q, cu_k, causal, scale, 
     """Gradient of fs_latent_prefill from its out and lse: dq, dk_nope, dk_rope (summed over the heads), dv in the
     inputs' shapes; ws: fs_latent_prefill_backward_ws_bytes(H, Tq, Tk) bytes."""
     what = "fs_latent_prefill_backward"
-    d = _prefill_operands(what, q, k_nope, k_rope, v, cu_q, cu_k, causal, scale)
-    _operand(what + " out", out, (d.Tq, d.heads, V_DIM))
-    _operand(what + " d_out", d_out, (d.Tq, d.heads, V_DIM))
-    _operand(what + " lse", lse, (d.heads, d.Tq), torch.float32, strided=False)
-    for name, g, like in (("dq", dq, q), ("dk_nope", dk_nope, k_nope), ("dk_rope", dk_rope, k_rope), ("dv", dv, v)):
-        _operand(what + " " + name, g, like.shape)
-    _check(lib().fs_latent_prefill_backward(ctypes.byref(d), _rows(q), _rows(k_nope), _rows(k_rope), _rows(v),
-                                            _p(cu_q), _p(cu_k), _rows(out), _p(lse), _rows(d_out), _rows(dq),
-                                            _rows(dk_nope), _rows(dk_rope), _rows(dv), _p(ws), _nbytes(ws),
-                                            _stream(stream)), what)
+    dev, st = _here(stream)
+    ops = _prefill_operands(what, dev, q, k_nope, k_rope, v, cu_q, cu_k, causal, scale)
+    Tq, H, _ = q.shape
+    grads = [_rows(_operand(what, g, like.shape, dev)) for g, like in ((dq, q), (dk_nope, k_nope), (dk_rope, k_rope), (dv, v))]
+    wp, _ = _operand(what, ws, ws.shape, dev, torch.uint8, False)
+    _check(lib().fs_latent_prefill_backward(*ops, _rows(_operand(what, out, (Tq, H, V_DIM), dev)),
+                                            _operand(what, lse, (H, Tq), dev, torch.float32, False)[0],
+                                            _rows(_operand(what, d_out, (Tq, H, V_DIM), dev)), *grads, wp, ws.numel(),
+                                            st), what)
