@@ -241,6 +241,9 @@ struct LatentDecodeArgs {
     int* err;
 };
 size_t latent_decode_ws_bytes(int H, int B, int n_q);
+// latent_decode_pair.cu: more than 64 query rows; meta: dc::Meta [ranges]
+cudaError_t launch_decode_pair(const CUtensorMap& tile, const CUtensorMap& row, const LatentDecodeArgs& a, bool fp8,
+                               int rb, int ranges, float* part, float* part_lse, void* meta, cudaStream_t st);
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, cudaStream_t st);
 
 // latent_prefill.cu (strides in elements); the backward reads out, lse and d_out

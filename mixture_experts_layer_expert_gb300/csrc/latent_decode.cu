@@ -32,30 +32,17 @@
 // four records).  FP8: codes go through registers a tile ahead and become bf16
 // unscaled; a record's scale multiplies its latent scores (the rotary part has TMEM
 // columns of its own) and its p.  Ring stages of 64 records x 128 latent columns (16 KB).
-#include <math_constants.h>
-
 #include "kernels.h"
-#include "latent.cuh"
+#include "latent_decode.cuh"
 
 namespace fs {
 namespace dc {
 
 constexpr int TT = 64;                        // records per tile
 constexpr int ROWS = 64;                      // query rows per block
-constexpr int CH = 64 * 128;                  // 64 records (or query rows) x 64 columns, 8 KB
-constexpr int PAIR = 2 * CH;                  // ring stage: 128 latent columns
 constexpr int MAXP = 11;                      // ring stages (8 with 64 query rows, 11 with 16)
 constexpr int MAXRAW = 6;                     // FP8: raw stages (64 records x 128 codes, 8 KB)
 constexpr int CTRL = 3072;
-constexpr size_t SMEM = 232448;               // 227 KB
-constexpr float kRescale = 8.0f;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr uint32_t NONE = 0xffffffffu;        // no record
-
-struct Meta {                                 // of each range: the sequence of its first tile
-    int b, off, tiles, pad;                   // off: tiles of the sequence before the range; tiles: of the range
-};
-
 struct Shared {
     uint64_t full[MAXP], empty[MAXP], raw_full[MAXRAW], raw_empty[MAXRAW], r_full[2], r_empty[2], info_full[4];
     uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_empty, fin;
@@ -68,175 +55,6 @@ struct Shared {
     float scale[4][TT];                       // FP8: the records' scales (4 tiles deep)
 };
 static_assert(sizeof(Shared) <= CTRL, "control area");
-
-struct Piece {
-    int b, t0, t1, n, len;                    // tiles [t0, t1) of the n of sequence b
-};
-
-__device__ __forceinline__ int seq_len(const LatentDecodeArgs& a, int b) {
-    const int n = __ldg(a.seq_lens + b);
-    return n < 0 || n > static_cast<long long>(a.max_pages) * a.page_size ? 0 : n;
-}
-// Next piece of the range (tiles of tt records); b, tile, left advance.  False at the end.
-__device__ __forceinline__ bool next_piece(const LatentDecodeArgs& a, int& b, int& tile, int& left, Piece* p, int tt = TT) {
-    if (left <= 0) return false;
-    int len = 0, n = 0;
-    for (; b < a.B; ++b, tile = 0) {
-        len = seq_len(a, b);
-        n = static_cast<int>((static_cast<unsigned>(len) + tt - 1) / tt);
-        if (tile < n) break;
-    }
-    if (b >= a.B) return false;
-    p->b = b; p->len = len; p->n = n; p->t0 = tile;
-    p->t1 = tile + min(n - tile, left);
-    left -= p->t1 - p->t0;
-    ++b;
-    tile = 0;
-    return true;
-}
-
-// The table's entry for position pos of sequence b (0 past the end): only the load, so that it can be issued a
-// tile ahead of its use.
-__device__ __forceinline__ int page_at(const LatentDecodeArgs& a, int b, int len, int pos) {
-    return pos < len ? __ldg(a.table + b * a.table_row + pos / a.page_size) : 0;
-}
-// Record of position pos on that page, or NONE (past the end, or a page outside the cache, which is recorded).
-__device__ __forceinline__ uint32_t record_of(const LatentDecodeArgs& a, int len, int pos, int page) {
-    if (pos >= len) return NONE;
-    if (page < 0 || page >= a.n_pages) {
-        set_dev_error(a.err, DEV_ERR_PAGE);
-        return NONE;
-    }
-    return static_cast<uint32_t>(page) * static_cast<uint32_t>(a.page_size) + static_cast<uint32_t>(pos % a.page_size);
-}
-
-// 64 consecutive positions of a sequence as one load: lane l brings the records of positions l and 32 + l.
-struct Group {
-    uint32_t live0, live1;      // which count
-    int start;                  // first record
-    bool box, none;             // 64 consecutive records; no record at all
-    int y[4];                   // the four records of gather group lane & 15
-};
-__device__ __forceinline__ Group make_group(uint32_t r0, uint32_t r1, int lane) {
-    Group g;
-    g.live0 = __ballot_sync(0xffffffffu, r0 != NONE);
-    g.live1 = __ballot_sync(0xffffffffu, r1 != NONE);
-    const uint32_t start = __shfl_sync(0xffffffffu, r0, 0);
-    g.start = static_cast<int>(start);
-    g.box = __all_sync(0xffffffffu, r0 == start + lane && r1 == start + 32 + lane && r1 != NONE);
-    g.none = (g.live0 | g.live1) == 0;
-    // a record that does not count is read as a copy of one that does: its p is 0
-    const uint32_t a = __shfl_sync(0xffffffffu, r0, g.live0 ? __ffs(g.live0) - 1 : 0);
-    const uint32_t b = __shfl_sync(0xffffffffu, r1, g.live1 ? __ffs(g.live1) - 1 : 0);
-    const uint32_t some = g.live0 ? a : b;
-    if (r0 == NONE) r0 = some;
-    if (r1 == NONE) r1 = some;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int src = 4 * (lane & 7) + e;
-        const uint32_t lo = __shfl_sync(0xffffffffu, r0, src), hi = __shfl_sync(0xffffffffu, r1, src);
-        g.y[e] = static_cast<int>((lane & 8) ? hi : lo);
-    }
-    return g;
-}
-__device__ __forceinline__ void sts16(uint32_t dst, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-// Whole warp: `chunks` boxes of 64 records x 128 bytes (columns from col on, col_step elements apart) to dst, each
-// 8 KB, completing on bar (one arrival, the bytes).  Group without records: zeros.
-__device__ __forceinline__ void load_group(const CUtensorMap* tile, const CUtensorMap* row, const Group& g, uint32_t dst,
-                                           uint32_t bar, int col, int col_step, int chunks, int lane) {
-    if (g.none) {
-        for (int i = lane; i < chunks * CH / 16; i += 32) sts16(dst + 16 * i, 0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar);
-    } else if (g.box) {
-        if (elect_one()) {
-            mbar_arrive_expect_tx(bar, chunks * CH);
-            for (int c = 0; c < chunks; ++c) tma_load_2d(dst + c * CH, tile, bar, col + c * col_step, g.start);
-        }
-    } else {
-        if (lane == 0) mbar_arrive_expect_tx(bar, chunks * CH);
-        __syncwarp();
-        const int c = lane >> 4;
-        if (c < chunks)
-            tma_gather4(dst + c * CH + (lane & 15) * 512, row, bar, col + c * col_step, g.y[0], g.y[1], g.y[2], g.y[3]);
-    }
-    __syncwarp();
-}
-// 16 E4M3 codes -> 32 bytes of bf16 at units y, y + 1 of the 128-byte row at base (swizzled by row r).
-__device__ __forceinline__ void put_codes(const uint4& v, uint32_t base, int y, int r) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[2 * i] = e4m3x2_to_bf16x2(w[i] & 0xffffu);
-        o[2 * i + 1] = e4m3x2_to_bf16x2(w[i] >> 16);
-    }
-    sts16(base + ((y ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-    sts16(base + (((y + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
-}
-// Bounded wait without regard to the abort flag, for loads in flight at the block's end.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* err) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(smem_u32(bar), parity))
-        if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(err, DEV_ERR_TIMEOUT); break; }
-}
-__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-// Barrier of n threads that also tells whether any of them brought `v`.
-__device__ __forceinline__ bool bar_any(int id, int n, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\t"
-        "bar.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"(id), "r"(n), "r"(static_cast<uint32_t>(v))
-        : "memory");
-    return r != 0;
-}
-
-// One warp: the range's first sequence and tile (of tt records), and its length, for the block and (write) for the join.
-__device__ __forceinline__ void find_range(const LatentDecodeArgs& a, int range, int ranges, int tt, bool write, Meta* meta,
-                                           int* b0, int* tile0, int* left) {
-    const int lane = threadIdx.x & 31;
-    auto tiles = [&](int b) { return static_cast<int>((static_cast<unsigned>(seq_len(a, b)) + tt - 1) / tt); };
-    long long total = 0;
-    for (int b = lane; b < a.B; b += 32) {
-        const int n = __ldg(a.seq_lens + b);
-        if (n < 0 || n > static_cast<long long>(a.max_pages) * a.page_size) set_dev_error(a.err, DEV_ERR_PAGE);
-        total += tiles(b);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-    const long long g0 = total * range / ranges, g1 = total * (range + 1) / ranges;
-    long long before = 0;
-    int found_b = a.B, found_t = 0;
-    for (int c0 = 0; c0 < a.B; c0 += 32) {
-        const int n = c0 + lane < a.B ? tiles(c0 + lane) : 0;
-        long long end = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, end, d);
-            if (lane >= d) end += v;
-        }
-        end += before;
-        const unsigned past = __ballot_sync(0xffffffffu, end > g0);
-        if (past) {
-            const int l = __ffs(past) - 1;
-            found_b = c0 + l;
-            found_t = static_cast<int>(g0 - __shfl_sync(0xffffffffu, end - n, l));
-            break;
-        }
-        before = __shfl_sync(0xffffffffu, end, 31);
-    }
-    if (lane == 0) {
-        *b0 = found_b;
-        *tile0 = found_t;
-        *left = static_cast<int>(g1 - g0);
-        if (write) meta[range] = Meta{found_b, found_t, static_cast<int>(g1 - g0), 0};
-    }
-}
 
 // FP8: warps that turn codes into bf16 (four where 64 rows need the registers).
 template <bool FP8, int RN> constexpr int kConv = FP8 ? (RN == 64 ? 4 : 8) : 0;
@@ -270,13 +88,13 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
     volatile int* abort_flag = &sh.abort_flag;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < MAXP; ++i) { mbar_init(smem_u32(&sh.full[i]), FP8 ? CW : 1); mbar_init(smem_u32(&sh.empty[i]), 1); }
+        for (int i = 0; i < MAXP; ++i) { mbar_init(smem_u32(&sh.full[i]), FP8 ? CW / 4 : 1); mbar_init(smem_u32(&sh.empty[i]), 1); }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.r_full[i]), 1);
             mbar_init(smem_u32(&sh.r_empty[i]), 1);
             mbar_init(smem_u32(&sh.s_full[i]), 1);
         }
-        for (int i = 0; i < MAXRAW; ++i) { mbar_init(smem_u32(&sh.raw_full[i]), 1); mbar_init(smem_u32(&sh.raw_empty[i]), FP8 ? CW : 1); }
+        for (int i = 0; i < MAXRAW; ++i) { mbar_init(smem_u32(&sh.raw_full[i]), 1); mbar_init(smem_u32(&sh.raw_empty[i]), FP8 ? CW / 4 : 1); }
         for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.info_full[i]), 1);
         mbar_init(smem_u32(&sh.q_full), 64);
         mbar_init(smem_u32(&sh.q_empty), 1);
@@ -303,31 +121,36 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
     if (warp >= 8) {
         // ------------------------------------------- FP8 codes to bf16 stages
         if constexpr (FP8) {
-            constexpr int NT = 32 * CW, NU = TT * 8 / NT;           // threads, 16-byte units a thread takes of a stage
-            const int t = threadIdx.x - 256;
-            uint32_t u = 0;
+            // a quarter of the warps per stage of a tile, so that four stages are under way at once
+            constexpr int NT = 8 * CW, NU = TT * 8 / NT;            // threads, 16-byte units a thread takes of a stage
+            const int t = (threadIdx.x - 256) % NT, c = (threadIdx.x - 256) / NT;
+            uint32_t u = c;
             bool ok = true;
-            while (ok && next_piece(a, b, tile, left, &p)) {
-                for (int n = 4 * (p.t1 - p.t0); n > 0; --n, ++u) {
+            while (ok && next_piece(a, b, tile, left, &p, TT)) {
+                for (int n = p.t1 - p.t0; n > 0; --n, u += 4) {
                     const uint32_t rs = u % raws, s = u % stages;
-                    if (!warp_wait(smem_u32(&sh.raw_full[rs]), (u / raws) & 1, abort_flag, a.err)) { ok = false; break; }
-                    uint4 v[NU];
+                    if (!warp_wait(smem_u32(&sh.raw_full[rs]), (u / raws) & 1, abort_flag, a.err) ||
+                        !warp_wait(smem_u32(&sh.empty[s]), ((u / stages) & 1) ^ 1, abort_flag, a.err)) { ok = false; break; }
 #pragma unroll
-                    for (int e = 0; e < NU; ++e) {
-                        const int i = t + NT * e, r = i >> 3, x = i & 7;
-                        v[e] = *reinterpret_cast<const uint4*>(sraw + rs * CH + r * 128 + ((x ^ (r & 7)) << 4));
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[rs]));
-                    if (!warp_wait(smem_u32(&sh.empty[s]), ((u / stages) & 1) ^ 1, abort_flag, a.err)) { ok = false; break; }
+                    for (int e0 = 0; e0 < NU; e0 += 4) {
+                        uint4 v[4];
 #pragma unroll
-                    for (int e = 0; e < NU; ++e) {
-                        const int i = t + NT * e, r = i >> 3, x = i & 7;
-                        put_codes(v[e], smem_u32(sring) + s * PAIR + (x >> 2) * CH + r * 128, 2 * (x & 3), r);
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = t + NT * (e0 + e), r = i >> 3, x = i & 7;
+                            v[e] = *reinterpret_cast<const uint4*>(sraw + rs * CH + r * 128 + ((x ^ (r & 7)) << 4));
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int i = t + NT * (e0 + e), r = i >> 3, x = i & 7;
+                            put_codes(v[e], smem_u32(sring) + s * PAIR + (x >> 2) * CH + r * 128, 2 * (x & 3), r);
+                        }
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+                    if (lane == 0) {
+                        mbar_arrive(smem_u32(&sh.raw_empty[rs]));
+                        mbar_arrive(smem_u32(&sh.full[s]));
+                    }
                 }
             }
         }
@@ -339,6 +162,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         uint64_t* full = FP8 ? sh.raw_full : sh.full;
         uint64_t* empty = FP8 ? sh.raw_empty : sh.empty;
         const uint32_t dst = smem_u32(FP8 ? sraw : sring), rope = smem_u32(srope);
+        const int records = static_cast<int>(a.n_pages * a.page_size);
         uint32_t u = 0, g = 0, nr = 0;                 // stages, tiles and rope loads so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -346,7 +170,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
             ok = __shfl_sync(0xffffffffu, ok, 0);
             return ok;
         };
-        while (ok && next_piece(a, b, tile, left, &p)) {
+        while (ok && next_piece(a, b, tile, left, &p, TT)) {
             int n0 = page_at(a, p.b, p.len, p.t0 * TT + lane), n1 = page_at(a, p.b, p.len, p.t0 * TT + 32 + lane);
             for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
                 // lane l: records l and 32 + l of this tile; the next tile's lookup is under way
@@ -360,14 +184,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                     if (r0 != NONE) s0 = *reinterpret_cast<const float*>(a.cache + static_cast<long long>(r0) * kRecFp8 + kFp8ScaleOff);
                     if (r1 != NONE) s1 = *reinterpret_cast<const float*>(a.cache + static_cast<long long>(r1) * kRecFp8 + kFp8ScaleOff);
                 }
-                const Group gr = make_group(r0, r1, lane);
+                const Group gr = make_group(r0, r1, records, lane);
                 for (int c = 0; c < 4; ++c, ++u) {
                     const uint32_t s = u % depth;
                     if (!wait(&empty[s], ((u / depth) & 1) ^ 1)) break;
-                    load_group(&tmTile, &tmRow, gr, dst + s * (FP8 ? CH : PAIR), smem_u32(&full[s]), 128 * c, step, chunks, lane);
+                    load_group<false>(&tmTile, &tmRow, gr, dst + s * (FP8 ? CH : PAIR), smem_u32(&full[s]), smem_u32(&full[s]), chunks * CH,
+                                      128 * c, step, chunks, lane);
                 }
                 if (!ok || !wait(&sh.r_empty[g & 1], ((g >> 1) & 1) ^ 1)) break;
-                load_group(&tmTile, &tmRow, gr, rope + (g & 1) * CH, smem_u32(&sh.r_full[g & 1]), kLatent, step, 1, lane);
+                load_group<false>(&tmTile, &tmRow, gr, rope + (g & 1) * CH, smem_u32(&sh.r_full[g & 1]), smem_u32(&sh.r_full[g & 1]), CH,
+                                  kLatent, step, 1, lane);
                 ++nr;
                 // what the softmax of this tile needs (the loader is less than four tiles ahead of it)
                 if constexpr (FP8) {
@@ -391,22 +217,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         // ------------------------------------------------ Q of each sequence
         const int t = threadIdx.x - 160;
         uint32_t np = 0;
-        while (next_piece(a, b, tile, left, &p)) {
+        while (next_piece(a, b, tile, left, &p, TT)) {
             if (!mbar_wait(smem_u32(&sh.q_empty), (np & 1) ^ 1, abort_flag, a.err)) break;
-            // RN rows x 72 sixteen-byte units; rows past the last are zeros
-#pragma unroll 4
-            for (int i = t; i < RN * 72; i += 64) {
-                const int r = i / 72, x = i - r * 72, c = x >> 3, qr = rb * ROWS + r;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    const int j = qr / a.H, h = qr - j * a.H;
-                    const long long row = static_cast<long long>(p.b) * a.n_q + j;
-                    v = __ldg(reinterpret_cast<const uint4*>(c < 8 ? a.ql + row * a.ql_row + h * a.ql_head + 8 * x
-                                                                   : a.qr + row * a.qr_row + h * a.qr_head + 8 * (x - 64)));
-                }
-                sts16(smem_u32(sq) + c * QC + r * 128 + (((x & 7) ^ (r & 7)) << 4), v.x, v.y, v.z, v.w);
-            }
-            fence_proxy_async_smem();
+            load_q<RN>(a, p.b, rb * ROWS, rows, smem_u32(sq), t);
             mbar_arrive(smem_u32(&sh.q_full));
             ++np;
         }
@@ -420,25 +233,28 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
             ok = __shfl_sync(0xffffffffu, ok, 0);
             return ok;
         };
-        while (ok && next_piece(a, b, tile, left, &p)) {
+        while (ok && next_piece(a, b, tile, left, &p, TT)) {
             if (!wait(&sh.q_full, np & 1)) break;
             const int n = p.t1 - p.t0;
-            // Whatever can run next does: the next stage of the scores (at most two tiles ahead of P V, their two
-            // buffers) or P V of the next tile, which frees ring stages and goes first.
-            int si = 0, pi = 0, c = 0;
+            // Whatever can run next does: the scores of the next tile (at most two ahead of P V, their two buffers), or
+            // P V of the next tile, which frees ring stages and goes first.
+            int si = 0, pi = 0;
             uint32_t spins = 0;
             uint64_t t0 = 0;
             while (pi < n) {
-                const uint32_t gs = g + si, gp = g + pi, us = u + 4 * si + c, rs = us % stages;
-                const bool want_s = si < n && si < pi + 2, want_p = pi < si;
+                const uint32_t gs = g + si, gp = g + pi, us = u + 4 * si;
                 int go = 0;
                 if (lane == 0) {
-                    if (want_p && mbar_test(smem_u32(&sh.p_full), gp & 1) &&
-                        (pi > 0 || mbar_test(smem_u32(&sh.o_empty), (np & 1) ^ 1)))
+                    if (pi < si && mbar_test(smem_u32(&sh.p_full), gp & 1) &&
+                        (pi > 0 || mbar_test(smem_u32(&sh.o_empty), (np & 1) ^ 1))) {
                         go = 2;
-                    else if (want_s && (c < 4 ? mbar_test(smem_u32(&sh.full[rs]), (us / stages) & 1)
-                                              : mbar_test(smem_u32(&sh.r_full[gs & 1]), (gs >> 1) & 1)))
+                    } else if (si < n && si < pi + 2) {
                         go = 1;
+#pragma unroll
+                        for (int c = 3; c >= 0; --c)
+                            if (go && !mbar_test(smem_u32(&sh.full[(us + c) % stages]), ((us + c) / stages) & 1)) go = 0;
+                        if (go && !mbar_test(smem_u32(&sh.r_full[gs & 1]), (gs >> 1) & 1)) go = 0;
+                    }
                 }
                 go = __shfl_sync(0xffffffffu, go, 0);
                 if (go == 0) {
@@ -460,28 +276,28 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 if (go == 1) {
                     if (elect_one()) {
                         tc_fence_after();
-                        if (c < 4) {
+                        const uint32_t d = tm_s + 64 * (gs & 1);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
                                 const uint64_t bd = smem_desc_sw128(smem_u32(sq + (2 * c + e) * QC));
-                                const uint64_t ad = smem_desc_sw128(smem_u32(sring + rs * PAIR + e * CH));
+                                const uint64_t ad = smem_desc_sw128(smem_u32(sring + ((us + c) % stages) * PAIR + e * CH));
 #pragma unroll
                                 for (int kk = 0; kk < 4; ++kk)
-                                    tc_mma_bf16(tm_s + 64 * (gs & 1), ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || e > 0 || kk > 0);
+                                    tc_mma_bf16(d, ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || e > 0 || kk > 0);
                             }
-                        } else {
-                            const uint64_t bd = smem_desc_sw128(smem_u32(sq + 8 * QC));
-                            const uint64_t ad = smem_desc_sw128(smem_u32(srope + (gs & 1) * CH));
+                        const uint64_t bd = smem_desc_sw128(smem_u32(sq + 8 * QC));
+                        const uint64_t ad = smem_desc_sw128(smem_u32(srope + (gs & 1) * CH));
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk)
-                                tc_mma_bf16((FP8 ? tm_r : tm_s) + 64 * (gs & 1), ad + 2ull * kk, bd + 2ull * kk, id_s, !FP8 || kk > 0);
-                            tc_commit(smem_u32(&sh.r_empty[gs & 1]));
-                            tc_commit(smem_u32(&sh.s_full[gs & 1]));
-                            if (si + 1 == n) tc_commit(smem_u32(&sh.q_empty));
-                        }
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_bf16(FP8 ? tm_r + 64 * (gs & 1) : d, ad + 2ull * kk, bd + 2ull * kk, id_s, !FP8 || kk > 0);
+                        tc_commit(smem_u32(&sh.r_empty[gs & 1]));
+                        tc_commit(smem_u32(&sh.s_full[gs & 1]));
+                        if (si + 1 == n) tc_commit(smem_u32(&sh.q_empty));
                     }
                     __syncwarp();
-                    if (++c == 5) { c = 0; ++si; }
+                    ++si;
                 } else {
                     if (elect_one()) {
                         tc_fence_after();
@@ -531,7 +347,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 if (a.lse && (i & 63) == 0) a.lse[row * a.H + hh] = -CUDART_INF_F;
             }
         }
-        while (next_piece(a, b, tile, left, &p)) {
+        while (next_piece(a, b, tile, left, &p, TT)) {
             float l[RN];
 #pragma unroll
             for (int i = 0; i < RN; ++i) l[i] = 0.f;
@@ -717,14 +533,14 @@ constexpr int kRanges = 152;                  // one block per SM
 // Joins the partials of the sequences that range boundaries cut.  Block (boundary, row, row block): the boundary
 // before range s; the first boundary inside a sequence joins all its pieces, in range order.
 __global__ void __launch_bounds__(128)
-join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, const float* __restrict__ part,
+join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, const int block_rows, const float* __restrict__ part,
             const float* __restrict__ part_lse, const Meta* __restrict__ meta) {
     __shared__ int slots[kRanges];
     __shared__ float weight[kRanges];
     __shared__ int count;
     __shared__ float z_ref[2];
     const int s = blockIdx.x + 1, r = blockIdx.y, rb = blockIdx.z;
-    const int q = rb * ROWS + r;
+    const int q = rb * block_rows + r;
     if (q >= a.n_q * a.H) return;
     const Meta m = meta[s];
     if (m.b >= a.B || m.tiles == 0 || m.off == 0) return;     // no tiles, or the sequence starts here
@@ -751,7 +567,7 @@ join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, cons
                 if (in) {
                     const int at = n + __popc(mask & ((1u << lane) - 1u));
                     slots[at] = (k * rb_count + rb) * 2 + (mk.b == m.b ? 0 : 1);
-                    weight[at] = part_lse[static_cast<long long>(slots[at]) * ROWS + r];
+                    weight[at] = part_lse[static_cast<long long>(slots[at]) * block_rows + r];
                     top = fmaxf(top, weight[at]);
                 }
                 n += __popc(mask);
@@ -779,7 +595,7 @@ join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, cons
 #pragma unroll 8
     for (int k = 0; k < n; ++k) {
         const float w = weight[k];
-        const float4 v = __ldg(reinterpret_cast<const float4*>(part + (static_cast<long long>(slots[k]) * ROWS + r) * kLatent) + threadIdx.x);
+        const float4 v = __ldg(reinterpret_cast<const float4*>(part + (static_cast<long long>(slots[k]) * block_rows + r) * kLatent) + threadIdx.x);
         acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
     }
     const float inv = z != 0.f ? 1.f / z : 0.f;
@@ -791,19 +607,21 @@ join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, cons
 }
 
 
-void shape(int H, int n_q, int* rb, int* ranges) {
-    *rb = (H * n_q + ROWS - 1) / ROWS;
-    *ranges = kRanges / *rb > 0 ? kRanges / *rb : 1;
+// Up to 64 query rows: one block per range; more: CTA pairs, 128 rows each, as many ranges as there are pairs left.
+struct Shape { int rb, ranges, block_rows; };
+Shape shape(int H, int n_q) {
+    if (H * n_q <= ROWS) return Shape{1, kRanges, ROWS};
+    const int rb = (H * n_q + 2 * ROWS - 1) / (2 * ROWS);
+    return Shape{rb, kRanges / 2 / rb, 2 * ROWS};
 }
 
 }  // namespace dc
 
 // Partials of at most two cut pieces per range and row block, their lse, the ranges' descriptions.
 size_t latent_decode_ws_bytes(int H, int, int n_q) {
-    int rb, ranges;
-    dc::shape(H, n_q, &rb, &ranges);
-    const size_t slots = static_cast<size_t>(rb) * ranges * 2;
-    return slots * dc::ROWS * (kLatent + 1) * 4 + (ranges * sizeof(dc::Meta) + 255) / 256 * 256;
+    const dc::Shape s = dc::shape(H, n_q);
+    const size_t slots = static_cast<size_t>(s.rb) * s.ranges * 2;
+    return slots * s.block_rows * (kLatent + 1) * 4 + (s.ranges * sizeof(dc::Meta) + 255) / 256 * 256;
 }
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, cudaStream_t st) {
@@ -811,28 +629,32 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, 
     using Fn = void (*)(CUtensorMap, CUtensorMap, LatentDecodeArgs, int, int, float*, float*, dc::Meta*);
     static const Fn fns[2][3] = {{dc::decode_kernel<false, 16>, dc::decode_kernel<false, 32>, dc::decode_kernel<false, 64>},
                                  {dc::decode_kernel<true, 16>, dc::decode_kernel<true, 32>, dc::decode_kernel<true, 64>}};
-    int rb, ranges;
-    dc::shape(a.H, a.n_q, &rb, &ranges);
-    const int rows = a.H * a.n_q < dc::ROWS ? a.H * a.n_q : dc::ROWS;
-    const int v = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
-    const Fn fn = fns[fp8][v];
-    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), dc::SMEM, attr[fp8][v]);
-    CUtensorMap tile{}, row{};
+    const dc::Shape sp = dc::shape(a.H, a.n_q);
+    const int all = a.H * a.n_q, rows = all < sp.block_rows ? all : sp.block_rows;
+    CUtensorMap tile, row;
     const long long records = a.n_pages * a.page_size;
     const int cols = fp8 ? kRecFp8 : kLatent + kRope;          // elements of a record (FP8: bytes)
-    if (e == cudaSuccess) e = make_map(&tile, a.cache, records, cols, dc::TT, fp8);
+    cudaError_t e = make_map(&tile, a.cache, records, cols, dc::TT, fp8);
     if (e == cudaSuccess) e = make_map(&row, a.cache, records, cols, 1, fp8);
     if (e != cudaSuccess) return e;
-    const size_t slots = static_cast<size_t>(rb) * ranges * 2;
+    const size_t slots = static_cast<size_t>(sp.rb) * sp.ranges * 2;
     float* part = static_cast<float*>(ws);
-    float* part_lse = part + slots * dc::ROWS * kLatent;
-    dc::Meta* meta = reinterpret_cast<dc::Meta*>(part_lse + slots * dc::ROWS);
-    fn<<<static_cast<unsigned>(rb * ranges), 32 * (8 + (!fp8 ? 0 : (v == 2 ? 4 : 8))), dc::SMEM, st>>>(tile, row, a, rb, ranges, part,
-                                                                                       part_lse, meta);
-    count_launch();
-    e = cudaGetLastError();
-    if (e != cudaSuccess || ranges == 1) return e;
-    dc::join_kernel<<<dim3(ranges - 1, rows, rb), 128, 0, st>>>(a, rb, ranges, part, part_lse, meta);
+    float* part_lse = part + slots * sp.block_rows * kLatent;
+    dc::Meta* meta = reinterpret_cast<dc::Meta*>(part_lse + slots * sp.block_rows);
+    if (sp.block_rows > dc::ROWS) {
+        e = launch_decode_pair(tile, row, a, fp8, sp.rb, sp.ranges, part, part_lse, meta, st);
+    } else {
+        const int v = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
+        const Fn fn = fns[fp8][v];
+        e = smem_attr_once(reinterpret_cast<const void*>(fn), dc::SMEM, attr[fp8][v]);
+        if (e != cudaSuccess) return e;
+        fn<<<static_cast<unsigned>(sp.ranges), 32 * (8 + (!fp8 ? 0 : (v == 2 ? 4 : 8))), dc::SMEM, st>>>(
+            tile, row, a, 1, sp.ranges, part, part_lse, meta);
+        count_launch();
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess || sp.ranges == 1) return e;
+    dc::join_kernel<<<dim3(sp.ranges - 1, rows, sp.rb), 128, 0, st>>>(a, sp.rb, sp.ranges, sp.block_rows, part, part_lse, meta);
     count_launch();
     return cudaGetLastError();
 }
