@@ -42,17 +42,18 @@ constexpr int TT = 64;                        // records per tile
 constexpr int ROWS = 64;                      // query rows per block
 constexpr int MAXP = 11;                      // ring stages (8 with 64 query rows, 11 with 16)
 constexpr int MAXRAW = 6;                     // FP8: raw stages (64 records x 128 codes, 8 KB)
-constexpr int CTRL = 3072;
+constexpr int CTRL = 6144;
 struct Shared {
-    uint64_t full[MAXP], empty[MAXP], raw_full[MAXRAW], raw_empty[MAXRAW], r_full[2], r_empty[2], info_full[4];
+    uint64_t full[MAXP], empty[MAXP], raw_full[MAXRAW], raw_empty[MAXRAW], r_full[2], r_empty[2], info_full[kInfo], tile_full[2], tile_empty[2];
     uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_empty, fin;
     uint32_t tmem;
     int abort_flag;
     int b0, tile0, left;                      // first piece of this block's range
-    uint32_t live[4][2];                      // records of a tile that count (4 tiles deep)
+    uint32_t live[kInfo][2];                  // records of a tile that count
     alignas(16) float m[ROWS], f[ROWS];       // running maximum (log2 units), rescaling factor or 1 / l
     float red[4][ROWS];                       // the warps' maxima or sums
-    float scale[4][TT];                       // FP8: the records' scales (4 tiles deep)
+    float scale[kInfo][TT];                   // FP8: the records' scales
+    TileRecs<TT> recs[2];
 };
 static_assert(sizeof(Shared) <= CTRL, "control area");
 
@@ -77,7 +78,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
     // Q (9 chunks of RN rows), P (64 records x 64 rows, 128 bytes a record), rope ring, stage ring, control
     constexpr int QC = RN * 128, CW = kConv<FP8, RN>;
     constexpr int raws = FP8 ? (RN == 64 ? 4 : 6) : 0;
-    constexpr int stages = (RN == 16 ? 11 : (RN == 32 ? 10 : 8)) - raws / 2;
+    constexpr int stages = (RN == 16 ? 11 : (RN == 32 ? 10 : 7)) - raws / 2;
     uint8_t* sq = smem;
     uint8_t* sp = smem + 9 * QC;
     uint8_t* srope = sp + CH;
@@ -95,8 +96,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
             mbar_init(smem_u32(&sh.s_full[i]), 1);
         }
         for (int i = 0; i < MAXRAW; ++i) { mbar_init(smem_u32(&sh.raw_full[i]), 1); mbar_init(smem_u32(&sh.raw_empty[i]), FP8 ? CW / 4 : 1); }
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.info_full[i]), 1);
-        mbar_init(smem_u32(&sh.q_full), 64);
+        for (int i = 0; i < kInfo; ++i) mbar_init(smem_u32(&sh.info_full[i]), 1);
+        for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&sh.tile_full[i]), 1); mbar_init(smem_u32(&sh.tile_empty[i]), 1); }
+        mbar_init(smem_u32(&sh.q_full), 32);
         mbar_init(smem_u32(&sh.q_empty), 1);
         mbar_init(smem_u32(&sh.p_full), 128);
         mbar_init(smem_u32(&sh.pv_done), 1);
@@ -162,7 +164,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         uint64_t* full = FP8 ? sh.raw_full : sh.full;
         uint64_t* empty = FP8 ? sh.raw_empty : sh.empty;
         const uint32_t dst = smem_u32(FP8 ? sraw : sring), rope = smem_u32(srope);
-        const int records = static_cast<int>(a.n_pages * a.page_size);
         uint32_t u = 0, g = 0, nr = 0;                 // stages, tiles and rope loads so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -171,41 +172,21 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
             return ok;
         };
         while (ok && next_piece(a, b, tile, left, &p, TT)) {
-            int n0 = page_at(a, p.b, p.len, p.t0 * TT + lane), n1 = page_at(a, p.b, p.len, p.t0 * TT + 32 + lane);
             for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
-                // lane l: records l and 32 + l of this tile; the next tile's lookup is under way
-                const uint32_t r0 = record_of(a, p.len, ti * TT + lane, n0), r1 = record_of(a, p.len, ti * TT + 32 + lane, n1);
-                if (ti + 1 < p.t1) {
-                    n0 = page_at(a, p.b, p.len, (ti + 1) * TT + lane);
-                    n1 = page_at(a, p.b, p.len, (ti + 1) * TT + 32 + lane);
-                }
-                float s0 = 0.f, s1 = 0.f;
-                if constexpr (FP8) {
-                    if (r0 != NONE) s0 = *reinterpret_cast<const float*>(a.cache + static_cast<long long>(r0) * kRecFp8 + kFp8ScaleOff);
-                    if (r1 != NONE) s1 = *reinterpret_cast<const float*>(a.cache + static_cast<long long>(r1) * kRecFp8 + kFp8ScaleOff);
-                }
-                const Group gr = make_group(r0, r1, records, lane);
+                if (!wait(&sh.tile_full[g & 1], (g >> 1) & 1)) break;
+                const Half hf = read_half(sh.recs[g & 1], 0, lane);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.tile_empty[g & 1]));
                 for (int c = 0; c < 4; ++c, ++u) {
                     const uint32_t s = u % depth;
                     if (!wait(&empty[s], ((u / depth) & 1) ^ 1)) break;
-                    load_group<false>(&tmTile, &tmRow, gr, dst + s * (FP8 ? CH : PAIR), smem_u32(&full[s]), smem_u32(&full[s]), chunks * CH,
-                                      128 * c, step, chunks, lane);
+                    load_half<false>(&tmTile, &tmRow, hf, dst + s * (FP8 ? CH : PAIR), smem_u32(&full[s]), smem_u32(&full[s]), chunks * CH,
+                                     128 * c, step, chunks, lane);
                 }
                 if (!ok || !wait(&sh.r_empty[g & 1], ((g >> 1) & 1) ^ 1)) break;
-                load_group<false>(&tmTile, &tmRow, gr, rope + (g & 1) * CH, smem_u32(&sh.r_full[g & 1]), smem_u32(&sh.r_full[g & 1]), CH,
-                                  kLatent, step, 1, lane);
+                load_half<false>(&tmTile, &tmRow, hf, rope + (g & 1) * CH, smem_u32(&sh.r_full[g & 1]), smem_u32(&sh.r_full[g & 1]), CH,
+                                 kLatent, step, 1, lane);
                 ++nr;
-                // what the softmax of this tile needs (the loader is less than four tiles ahead of it)
-                if constexpr (FP8) {
-                    sh.scale[g & 3][lane] = s0;
-                    sh.scale[g & 3][32 + lane] = s1;
-                    __syncwarp();
-                }
-                if (lane == 0) {
-                    sh.live[g & 3][0] = gr.live0;
-                    sh.live[g & 3][1] = gr.live1;
-                    mbar_arrive(smem_u32(&sh.info_full[g & 3]));
-                }
             }
         }
         if (lane == 0) {                                // nothing is in flight when the block ends
@@ -213,13 +194,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
             for (uint32_t e = 1; e <= 2 && e <= nr; ++e) drain(&sh.r_full[(nr - e) & 1], ((nr - e) >> 1) & 1, a.err);
         }
         __syncwarp();
-    } else if (warp >= 5) {
+    } else if (warp == 6) {
+        lookup_tiles<FP8, TT>(a, b, tile, left, 0, 0, sh.recs, sh.tile_full, sh.tile_empty, sh.live, sh.scale, sh.info_full,
+                              abort_flag);
+    } else if (warp == 5) {
         // ------------------------------------------------ Q of each sequence
-        const int t = threadIdx.x - 160;
         uint32_t np = 0;
         while (next_piece(a, b, tile, left, &p, TT)) {
-            if (!mbar_wait(smem_u32(&sh.q_empty), (np & 1) ^ 1, abort_flag, a.err)) break;
-            load_q<RN>(a, p.b, rb * ROWS, rows, smem_u32(sq), t);
+            if (!warp_wait(smem_u32(&sh.q_empty), (np & 1) ^ 1, abort_flag, a.err)) break;
+            load_q<RN>(a, p.b, rb * ROWS, rows, smem_u32(sq), lane);
             mbar_arrive(smem_u32(&sh.q_full));
             ++np;
         }
@@ -352,7 +335,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
 #pragma unroll
             for (int i = 0; i < RN; ++i) l[i] = 0.f;
             for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
-                mbar_wait(smem_u32(&sh.info_full[g & 3]), (g >> 2) & 1, abort_flag, a.err);
+                mbar_wait(smem_u32(&sh.info_full[g % kInfo]), (g / kInfo) & 1, abort_flag, a.err);
                 mbar_wait(smem_u32(&sh.s_full[g & 1]), (g >> 1) & 1, abort_flag, a.err);
                 tc_fence_after();
                 uint32_t s[RN];
@@ -362,7 +345,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                     tmem_ld16(tm_s + 64 * (g & 1) + 16 * q + lane_base, part16);
                 }
                 if constexpr (FP8) {
-                    const float sc = sh.scale[g & 3][rec];
+                    const float sc = sh.scale[g % kInfo][rec];
 #pragma unroll
                     for (int q = 0; q < RN / 16; ++q) {
                         uint32_t kr[16];
@@ -374,7 +357,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                     }
                 }
                 tmem_ld_wait();
-                const bool live = lane < 16 && ((sh.live[g & 3][rec >> 5] >> (rec & 31)) & 1u);
+                const bool live = lane < 16 && ((sh.live[g % kInfo][rec >> 5] >> (rec & 31)) & 1u);
                 const int pos = ti * TT + rec;
                 // rows of earlier new tokens see fewer positions: query j sees [0, len - (n_q - 1 - j))
                 const bool edge = a.n_q > 1 && ti * TT + TT > p.len - a.n_q + 1;
@@ -448,7 +431,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 if (g > 0) mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
                 const float4* m4 = reinterpret_cast<const float4*>(sh.m);
                 const uint32_t prow = smem_u32(sp) + rec * 128;
-                const float vs = FP8 ? sh.scale[g & 3][rec] : 1.f;      // V's rows are codes
+                const float vs = FP8 ? sh.scale[g % kInfo][rec] : 1.f;      // V's rows are codes
 #pragma unroll
                 for (int q = 0; q < RN / 8; ++q) {
                     uint32_t w[4];

@@ -62,45 +62,104 @@ __device__ __forceinline__ uint32_t record_of(const LatentDecodeArgs& a, int len
     return static_cast<uint32_t>(page) * static_cast<uint32_t>(a.page_size) + static_cast<uint32_t>(pos % a.page_size);
 }
 
-// 64 consecutive positions of a sequence as one load: lane l brings the records of positions l and 32 + l.
-struct Group {
-    uint32_t live0, live1;      // which count
-    int start;                  // first record
-    bool box;                   // 64 consecutive records, or none at all (start: past the cache's end)
-    int y[4];                   // the four records of gather group lane & 15
+// A tile's records as the loader needs them, for TT / 64 halves of 64 consecutive positions.
+template <int TT>
+struct TileRecs {
+    alignas(16) int rec[TT];    // record of each position; one that does not count: a copy of one that does (its p is 0)
+    int start[TT / 64];         // first record of a half that is one box: 64 consecutive records, or none at all (start
+    int box[TT / 64];           //   past the cache's end: zeros); else four records at a time are gathered
 };
-__device__ __forceinline__ Group make_group(uint32_t r0, uint32_t r1, int records, int lane) {
-    Group g;
-    g.live0 = __ballot_sync(0xffffffffu, r0 != NONE);
-    g.live1 = __ballot_sync(0xffffffffu, r1 != NONE);
-    const uint32_t start = __shfl_sync(0xffffffffu, r0, 0);
-    const bool none = (g.live0 | g.live1) == 0;
-    g.start = none ? records : static_cast<int>(start);
-    g.box = none || __all_sync(0xffffffffu, r0 == start + lane && r1 == start + 32 + lane && r1 != NONE);
-    // a record that does not count is read as a copy of one that does: its p is 0
-    const uint32_t a = __shfl_sync(0xffffffffu, r0, g.live0 ? __ffs(g.live0) - 1 : 0);
-    const uint32_t b = __shfl_sync(0xffffffffu, r1, g.live1 ? __ffs(g.live1) - 1 : 0);
-    const uint32_t some = g.live0 ? a : b;
-    if (r0 == NONE) r0 = some;
-    if (r1 == NONE) r1 = some;
+constexpr int kInfo = 6;        // depth of what the lookup leaves for the softmax (see lookup_tiles)
+
+// The lookup warp: for every tile of the block's range, its records (two tiles ahead of the loads at most),
+// which of them count and (FP8) their scales, and its part `own` of the halves asked into L2.  It is at most two
+// tiles ahead of the loads, which a full ring holds less than four tiles ahead of the softmax: slots of kInfo
+// tiles are free when they come round.
+template <bool FP8, int TT>
+__device__ __forceinline__ void lookup_tiles(const LatentDecodeArgs& a, int b, int tile, int left, int own0, int own1,
+                                             TileRecs<TT>* recs, uint64_t* tile_full, uint64_t* tile_empty,
+                                             uint32_t (*live)[TT / 32], float (*scale)[TT], uint64_t* info_full,
+                                             volatile int* abort_flag) {
+    constexpr int NE = TT / 32, REC = FP8 ? kRecFp8 : kRecBf16;
+    const int lane = threadIdx.x & 31;
+    const int records = static_cast<int>(a.n_pages * a.page_size);
+    Piece p;
+    uint32_t g = 0;
+    while (next_piece(a, b, tile, left, &p, TT)) {
+        int pg[NE];                                 // table entries of the next tile's positions 32 e + lane
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int src = 4 * (lane & 7) + e;
-        const uint32_t lo = __shfl_sync(0xffffffffu, r0, src), hi = __shfl_sync(0xffffffffu, r1, src);
-        g.y[e] = static_cast<int>((lane & 8) ? hi : lo);
+        for (int e = 0; e < NE; ++e) pg[e] = page_at(a, p.b, p.len, p.t0 * TT + 32 * e + lane);
+        for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
+            uint32_t r[NE], lv[NE];
+            float sc[NE];
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                r[e] = record_of(a, p.len, ti * TT + 32 * e + lane, pg[e]);
+                if (ti + 1 < p.t1) pg[e] = page_at(a, p.b, p.len, (ti + 1) * TT + 32 * e + lane);
+                lv[e] = __ballot_sync(0xffffffffu, r[e] != NONE);
+                sc[e] = 0.f;
+                if (r[e] != NONE) {
+                    const uint8_t* rec = a.cache + static_cast<long long>(r[e]) * REC;
+                    if (FP8) sc[e] = *reinterpret_cast<const float*>(rec + kFp8ScaleOff);
+                    if (e / 2 >= own0 && e / 2 <= own1) {
+#pragma unroll
+                        for (int q = 0; q < REC; q += 128) prefetch_l2(rec + q);
+                    }
+                }
+            }
+            if (!warp_wait(smem_u32(&tile_empty[g & 1]), ((g >> 1) & 1) ^ 1, abort_flag, a.err)) return;
+            TileRecs<TT>& t = recs[g & 1];
+#pragma unroll
+            for (int h = 0; h < TT / 64; ++h) {
+                const uint32_t r0 = r[2 * h], r1 = r[2 * h + 1], l0 = lv[2 * h], l1 = lv[2 * h + 1];
+                const uint32_t start = __shfl_sync(0xffffffffu, r0, 0);
+                const bool none = (l0 | l1) == 0;
+                const bool box = none || __all_sync(0xffffffffu, r0 == start + lane && r1 == start + 32 + lane && r1 != NONE);
+                const uint32_t s0 = __shfl_sync(0xffffffffu, r0, l0 ? __ffs(l0) - 1 : 0);
+                const uint32_t s1 = __shfl_sync(0xffffffffu, r1, l1 ? __ffs(l1) - 1 : 0);
+                const uint32_t some = l0 ? s0 : s1;
+                t.rec[64 * h + lane] = static_cast<int>(r0 == NONE ? some : r0);
+                t.rec[64 * h + 32 + lane] = static_cast<int>(r1 == NONE ? some : r1);
+                if (lane == 0) {
+                    t.start[h] = none ? records : static_cast<int>(start);
+                    t.box[h] = box;
+                }
+            }
+            const uint32_t k = g % kInfo;
+#pragma unroll
+            for (int e = 0; e < NE; ++e) {
+                if (FP8) scale[k][32 * e + lane] = sc[e];
+                if (lane == 0) live[k][e] = lv[e];
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&tile_full[g & 1]));
+                mbar_arrive(smem_u32(&info_full[k]));
+            }
+        }
     }
-    return g;
+}
+
+// One half of a tile in the loader's registers.
+struct Half {
+    int start;
+    bool box;
+    int4 y;                     // the four records of gather group lane & 15
+};
+template <int TT>
+__device__ __forceinline__ Half read_half(const TileRecs<TT>& t, int h, int lane) {
+    return Half{t.start[h], t.box[h] != 0, *reinterpret_cast<const int4*>(&t.rec[64 * h + 4 * (lane & 15)])};
 }
 __device__ __forceinline__ void sts16(uint32_t dst, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 // Whole warp: `chunks` boxes of 64 records x 128 bytes (columns from col on, col_step elements apart) to dst, each
-// 8 KB.  expect: the barrier's one arrival with this many bytes (0: another CTA makes it).  A group without
-// records is a box past the cache's end: zeros.  PAIR_BAR: bar is a shared::cluster address.
+// 8 KB.  expect: the barrier's one arrival with this many bytes (0: another CTA makes it).  PAIR_BAR: bar is a
+// shared::cluster address.
 template <bool PAIR_BAR>
-__device__ __forceinline__ void load_group(const CUtensorMap* tile, const CUtensorMap* row, const Group& g, uint32_t dst,
-                                           uint32_t bar, uint32_t local_bar, uint32_t expect, int col, int col_step, int chunks,
-                                           int lane) {
+__device__ __forceinline__ void load_half(const CUtensorMap* tile, const CUtensorMap* row, const Half& g, uint32_t dst,
+                                          uint32_t bar, uint32_t local_bar, uint32_t expect, int col, int col_step, int chunks,
+                                          int lane) {
     if (g.box) {
         if (elect_one()) {
             if (expect) mbar_arrive_expect_tx(local_bar, expect);
@@ -115,28 +174,31 @@ __device__ __forceinline__ void load_group(const CUtensorMap* tile, const CUtens
         const int c = lane >> 4;
         const uint32_t to = dst + c * CH + (lane & 15) * 512;
         if (c < chunks) {
-            if constexpr (PAIR_BAR) tma_gather4_pair(to, row, bar, col + c * col_step, g.y[0], g.y[1], g.y[2], g.y[3]);
-            else tma_gather4(to, row, bar, col + c * col_step, g.y[0], g.y[1], g.y[2], g.y[3]);
+            if constexpr (PAIR_BAR) tma_gather4_pair(to, row, bar, col + c * col_step, g.y.x, g.y.y, g.y.z, g.y.w);
+            else tma_gather4(to, row, bar, col + c * col_step, g.y.x, g.y.y, g.y.z, g.y.w);
         }
     }
     __syncwarp();
 }
-// 64 threads (t): R query rows from row0 on of sequence b (rows of them real, the others zeros) into R-row chunks of
-// 64 columns at dst.  All copies are in flight together, then visible to the tensor cores.
+// One warp: R query rows from row0 on of sequence b (rows of them real, the others zeros) into R-row chunks of 64
+// columns at dst.  All copies are in flight together, then visible to the tensor cores.
 template <int R>
-__device__ __forceinline__ void load_q(const LatentDecodeArgs& a, int b, int row0, int rows, uint32_t dst, int t) {
-    constexpr int PER = 64 / R;                 // threads per row
-    const int r = t / PER, x0 = t % PER, qr = row0 + (r < rows ? r : 0), j = qr / a.H, h = qr - j * a.H;
-    const long long row = static_cast<long long>(b) * a.n_q + j;
-    const __nv_bfloat16* ql = a.ql + row * a.ql_row + h * a.ql_head;
-    const __nv_bfloat16* qr64 = a.qr + row * a.qr_row + h * a.qr_head;
-    const int n = r < rows ? 16 : 0;            // 0: sixteen zero bytes, nothing is read
+__device__ __forceinline__ void load_q(const LatentDecodeArgs& a, int b, int row0, int rows, uint32_t dst, int lane) {
+    constexpr int PER = R < 32 ? 32 / R : 1;    // threads per row
+#pragma unroll
+    for (int r = lane / PER; r < R; r += 32 / PER) {
+        const int qr = row0 + (r < rows ? r : 0), j = qr / a.H, h = qr - j * a.H;
+        const long long row = static_cast<long long>(b) * a.n_q + j;
+        const __nv_bfloat16* ql = a.ql + row * a.ql_row + h * a.ql_head;
+        const __nv_bfloat16* qr64 = a.qr + row * a.qr_row + h * a.qr_head;
+        const int n = r < rows ? 16 : 0;        // 0: sixteen zero bytes, nothing is read
 #pragma unroll 8
-    for (int x = x0; x < 72; x += PER) {
-        const __nv_bfloat16* src = x < 64 ? ql + 8 * x : qr64 + 8 * (x - 64);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (x >> 3) * (R * 128) + r * 128 + (((x & 7) ^ (r & 7)) << 4)),
-                     "l"(src), "r"(n)
-                     : "memory");
+        for (int x = lane % PER; x < 72; x += PER) {
+            const __nv_bfloat16* src = x < 64 ? ql + 8 * x : qr64 + 8 * (x - 64);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + (x >> 3) * (R * 128) + r * 128 + (((x & 7) ^ (r & 7)) << 4)),
+                         "l"(src), "r"(n)
+                         : "memory");
+        }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     fence_proxy_async_smem();

@@ -18,7 +18,7 @@
 //
 // Per CTA: warps 0-3 softmax, rescaling and output (thread = row of the lane and half of the records);
 // warp 4 MMA issue in the even CTA, in the odd one it tells the even CTA which stages have
-// arrived; warps 5-6 Q; warp 7 page lookup and TMA; FP8: warps 8-15 turn raw codes into bf16 stages.
+// arrived; warp 5 Q; warp 6 page lookup; warp 7 TMA; FP8: warps 8-15 turn raw codes into bf16 stages.
 #include "kernels.h"
 #include "latent_decode.cuh"
 
@@ -28,19 +28,20 @@ using namespace dc;
 
 constexpr int TT = 128;                       // records per tile
 constexpr int ROWS = 64;                      // query rows per CTA
-constexpr int MAXP = 7, MAXRAW = 5;
-constexpr int CTRL = 3072;
+constexpr int MAXP = 7, MAXRAW = 4;
+constexpr int CTRL = 6144;
 template <bool FP8> constexpr int kThreads = FP8 ? 512 : 256;
 
 struct Shared {
-    uint64_t full[MAXP], empty[MAXP], peer[MAXP], raw_full[MAXRAW], raw_empty[MAXRAW], r_full[2], r_empty[2], info_full[4];
+    uint64_t full[MAXP], empty[MAXP], peer[MAXP], raw_full[MAXRAW], raw_empty[MAXRAW], r_full[2], r_empty[2], info_full[kInfo], tile_full[2], tile_empty[2];
     uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_empty, fin;
     uint32_t tmem;
     int abort_flag;
     int b0, tile0, left;
-    uint32_t live[4][4];                      // records of a tile that count (4 tiles deep)
+    uint32_t live[kInfo][4];                  // records of a tile that count
     float red[2][ROWS];
-    alignas(16) float scale[4][TT];           // FP8: the records' scales
+    alignas(16) float scale[kInfo][TT];       // FP8: the records' scales
+    TileRecs<TT> recs[2];
 };
 static_assert(sizeof(Shared) <= CTRL, "control area");
 
@@ -62,7 +63,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
     const int cid = static_cast<int>(blockIdx.x >> 1), rb = cid % rb_count, range = cid / rb_count;
     const int row0 = rb * 2 * ROWS + rank * ROWS;                     // first query row of this CTA
     const int rows = max(0, min(ROWS, a.n_q * a.H - row0));
-    constexpr int QC = ROWS * 128, raws = FP8 ? 5 : 0, stages = FP8 ? 5 : 7;
+    constexpr int QC = ROWS * 128, raws = FP8 ? 4 : 0, stages = FP8 ? 5 : 7;
     uint8_t* sq = smem;                            // Q: 9 chunks of 64 rows x 64 columns
     uint8_t* sp = smem + 9 * QC;                   // P: 2 chunks of 64 rows x 64 records
     uint8_t* srope = sp + 2 * CH;                  // rotary keys of this CTA's 64 records, twice
@@ -83,8 +84,9 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
             mbar_init(smem_u32(&sh.r_full[i]), 1);
             mbar_init(smem_u32(&sh.r_empty[i]), 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.info_full[i]), 1);
-        mbar_init(smem_u32(&sh.q_full), 4);        // two warps of each CTA
+        for (int i = 0; i < kInfo; ++i) mbar_init(smem_u32(&sh.info_full[i]), 1);
+        for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&sh.tile_full[i]), 1); mbar_init(smem_u32(&sh.tile_empty[i]), 1); }
+        mbar_init(smem_u32(&sh.q_full), 2);        // a warp of each CTA
         mbar_init(smem_u32(&sh.q_empty), 1);
         mbar_init(smem_u32(&sh.s_full[0]), 1);
         mbar_init(smem_u32(&sh.s_full[1]), 1);
@@ -154,7 +156,6 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
         uint64_t* full = FP8 ? sh.raw_full : sh.full;
         uint64_t* empty = FP8 ? sh.raw_empty : sh.empty;
         const uint32_t dst = smem_u32(FP8 ? sraw : sring);
-        const int records = static_cast<int>(a.n_pages * a.page_size);
         uint32_t u = 0, g = 0;                          // stages and tiles so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -162,71 +163,33 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
             ok = __shfl_sync(0xffffffffu, ok, 0);
             return ok;
         };
-        auto stage = [&](const Group& gr, int col) {
+        auto stage = [&](const Half& gr, int col) {
             const uint32_t s = u % depth;
             if (!wait(&empty[s], ((u / depth) & 1) ^ 1)) return false;
             const uint32_t lb = smem_u32(&full[s]);
             // bf16: both CTAs' loads complete on the even CTA's barrier, which expects the bytes of both
             if constexpr (FP8)
-                load_group<false>(&tmTile, &tmRow, gr, dst + s * CH, lb, lb, CH, col, step, chunks, lane);
+                load_half<false>(&tmTile, &tmRow, gr, dst + s * CH, lb, lb, CH, col, step, chunks, lane);
             else
-                load_group<true>(&tmTile, &tmRow, gr, dst + s * PAIR, map_to_cta(lb, 0), lb, rank ? 0 : 2 * PAIR, col, step, chunks, lane);
+                load_half<true>(&tmTile, &tmRow, gr, dst + s * PAIR, map_to_cta(lb, 0), lb, rank ? 0 : 2 * PAIR, col, step, chunks, lane);
             ++u;
             return true;
         };
         while (ok && next_piece(a, b, tile, left, &p, TT)) {
-            int pg[4];                                  // table entries of the next tile's positions 32 e + lane
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pg[e] = page_at(a, p.b, p.len, p.t0 * TT + 32 * e + lane);
-            Group cur[2], nxt[2];
-            // K of tile ti (its groups into nxt), then V of tile ti - 1 (cur)
+            Half cur[2], nxt[2];
+            // K of tile ti (its halves into nxt), then V of tile ti - 1 (cur)
             for (int ti = p.t0; ti <= p.t1 && ok; ++ti) {
                 if (ti < p.t1) {
-                    uint32_t r[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) r[e] = record_of(a, p.len, ti * TT + 32 * e + lane, pg[e]);
-                    if (ti + 1 < p.t1) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) pg[e] = page_at(a, p.b, p.len, (ti + 1) * TT + 32 * e + lane);
-                    }
-                    float sc[4];
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sc[e] = r[e] == NONE ? 0.f : *reinterpret_cast<const float*>(
-                                                             a.cache + static_cast<long long>(r[e]) * kRecFp8 + kFp8ScaleOff);
-                    }
-                    nxt[0] = make_group(r[0], r[1], records, lane);
-                    nxt[1] = make_group(r[2], r[3], records, lane);
-                    const Group own = rank ? nxt[1] : nxt[0];
+                    if (!wait(&sh.tile_full[g & 1], (g >> 1) & 1)) break;
+                    nxt[0] = read_half(sh.recs[g & 1], 0, lane);
+                    nxt[1] = read_half(sh.recs[g & 1], 1, lane);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.tile_empty[g & 1]));
+                    const Half own = rank ? nxt[1] : nxt[0];
                     for (int c = 0; c < 4 && ok; ++c) stage(own, 128 * c);
                     if (!ok || !wait(&sh.r_empty[g & 1], ((g >> 1) & 1) ^ 1)) break;
-                    load_group<true>(&tmTile, &tmRow, own, smem_u32(srope) + (g & 1) * CH, leader_bar(&sh.r_full[g & 1]),
-                                     smem_u32(&sh.r_full[g & 1]), rank ? 0 : 2 * CH, kLatent, step, 1, lane);
-                    if constexpr (FP8) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) sh.scale[g & 3][32 * e + lane] = sc[e];
-                        __syncwarp();
-                    }
-                    // the next tile's half of this CTA into L2: its stages' loads then take an L2 hit's latency
-                    if (ti + 1 < p.t1) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int k = 2 * rank + e, pos = (ti + 1) * TT + 32 * k + lane;
-                            const int page = k == 0 ? pg[0] : (k == 1 ? pg[1] : (k == 2 ? pg[2] : pg[3]));
-                            if (pos < p.len && page >= 0 && page < a.n_pages) {
-                                constexpr int REC = FP8 ? kRecFp8 : kRecBf16;
-                                const uint8_t* rec = a.cache + (static_cast<long long>(page) * a.page_size + pos % a.page_size) * REC;
-#pragma unroll
-                                for (int q = 0; q < REC; q += 128) prefetch_l2(rec + q);
-                            }
-                        }
-                    }
-                    if (lane == 0) {
-                        sh.live[g & 3][0] = nxt[0].live0; sh.live[g & 3][1] = nxt[0].live1;
-                        sh.live[g & 3][2] = nxt[1].live0; sh.live[g & 3][3] = nxt[1].live1;
-                        mbar_arrive(smem_u32(&sh.info_full[g & 3]));
-                    }
+                    load_half<true>(&tmTile, &tmRow, own, smem_u32(srope) + (g & 1) * CH, leader_bar(&sh.r_full[g & 1]),
+                                    smem_u32(&sh.r_full[g & 1]), rank ? 0 : 2 * CH, kLatent, step, 1, lane);
                     ++g;
                 }
                 if (ti > p.t0)                          // V: column halves j, record halves h
@@ -243,13 +206,15 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
                 for (uint32_t e = 1; e <= 2 && e <= g; ++e) drain(&sh.r_full[(g - e) & 1], ((g - e) >> 1) & 1, a.err);
         }
         __syncwarp();
-    } else if (warp >= 5) {
+    } else if (warp == 6) {
+        lookup_tiles<FP8, TT>(a, b, tile, left, rank, rank, sh.recs, sh.tile_full, sh.tile_empty, sh.live, sh.scale,
+                              sh.info_full, abort_flag);
+    } else if (warp == 5) {
         // ------------------------------------------------ Q of each sequence
-        const int t = threadIdx.x - 160;
         uint32_t np = 0;
         while (next_piece(a, b, tile, left, &p, TT)) {
             if (!warp_wait(smem_u32(&sh.q_empty), (np & 1) ^ 1, abort_flag, a.err)) break;
-            load_q<ROWS>(a, p.b, row0, rows, smem_u32(sq), t);
+            load_q<ROWS>(a, p.b, row0, rows, smem_u32(sq), lane);
             __syncwarp();
             if (lane == 0) arrive_even(leader_bar(&sh.q_full));
             ++np;
@@ -376,14 +341,14 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
             const int end = mine ? p.len - (a.n_q - 1 - j) : 0;        // this row sees positions [0, end)
             float m = -CUDART_INF_F, l = 0.f;
             for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
-                mbar_wait(smem_u32(&sh.info_full[g & 3]), (g >> 2) & 1, abort_flag, a.err);
+                mbar_wait(smem_u32(&sh.info_full[g % kInfo]), (g / kInfo) & 1, abort_flag, a.err);
                 mbar_wait(smem_u32(&sh.s_full[g & 1]), (g >> 1) & 1, abort_flag, a.err);
                 tc_fence_after();
                 uint32_t s[2][32];
                 tmem_ld32(tm_s + 64 * (g & 1) + lane_base, s[0]);
                 tmem_ld32(tm_s + 64 * (g & 1) + 32 + lane_base, s[1]);
                 tmem_ld_wait();
-                const float4* sc4 = reinterpret_cast<const float4*>(&sh.scale[g & 3][64 * th]);
+                const float4* sc4 = reinterpret_cast<const float4*>(&sh.scale[g % kInfo][64 * th]);
                 if constexpr (FP8) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -403,7 +368,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
                     }
                 }
                 const int lim = end - ti * TT - 64 * th;
-                uint32_t live[2] = {sh.live[g & 3][2 * th], sh.live[g & 3][2 * th + 1]};
+                uint32_t live[2] = {sh.live[g % kInfo][2 * th], sh.live[g % kInfo][2 * th + 1]};
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int k = lim - 32 * q;
