@@ -113,10 +113,37 @@ __device__ __forceinline__ int find_tile(const int32_t* cu_q, const int32_t* cu_
     return -1;
 }
 
-// mbar_wait by a whole warp with one answer for all its lanes: what follows a
+// mbar_wait (common.cuh) with its loop out of line.  These kernels run six or more different loops at once on an
+// SM, each with several waits: inlined, the loops outgrow the instruction caches (no-instruction stalls were a
+// quarter of all warp cycles).
+static __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((it & 255u) == 0) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                *abort_flag = 1;
+                set_dev_error(err, DEV_ERR_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
+    return mbar_try_wait(bar, parity) || wait_long(bar, parity, abort_flag, err);
+}
+// For loads in flight at a block's end: bounded, without regard to the abort flag.
+static __device__ __noinline__ void drain_bar(uint64_t* bar, uint32_t parity, int* err) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_u32(bar), parity))
+        if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(err, DEV_ERR_TIMEOUT); break; }
+}
+
+// wait_bar by a whole warp with one answer for all its lanes: what follows a
 // failed wait must not split a warp that goes on to warp-wide operations.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* err) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, err));
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, err));
 }
 
 // 2^x (x <= 0 here up to rounding): one hardware operation, relative error about 2^-22.

@@ -94,13 +94,6 @@ struct Queue {
     Item item[2];
 };
 
-// Bounded drain of a barrier phase without regard to the abort flag.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* err) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(smem_u32(bar), parity))
-        if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(err, DEV_ERR_TIMEOUT); break; }
-}
-
 // Zero rows [from, to) of `units` units of `unit` bytes (128-byte rows), by one warp.
 __device__ __forceinline__ void zero_rows(uint8_t* base, int units, int unit, int from, int to, int lane) {
     const int n = (to - from) * 8;
@@ -198,8 +191,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                     it.diag = a.causal ? first - from : -(1 << 30);
                 }
             }
-            if (lane == 0) ok = mbar_wait(smem_u32(&sh.q.empty[slot]), ((k >> 1) & 1) ^ 1, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(&sh.q.empty[slot]), ((k >> 1) & 1) ^ 1, abort_flag, a.err);
             if (!ok) break;
             if (lane == 0) {
                 sh.q.item[slot] = it;
@@ -208,7 +200,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             if (id < 0) break;
             if (it.valid == 1 && it.n > 0) {
                 if (lane == 0) {
-                    ok = mbar_wait(smem_u32(&sh.kv_empty), (nkv & 1) ^ 1, abort_flag, a.err);
+                    ok = wait_bar(smem_u32(&sh.kv_empty), (nkv & 1) ^ 1, abort_flag, a.err);
                     if (ok) {
                         const uint32_t fb = smem_u32(&sh.kv_full);
                         mbar_arrive_expect_tx(fb, 5 * UNIT);
@@ -238,8 +230,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                             dl[e] = __ldg(delta + at);
                         }
                     }
-                    if (lane == 0) ok = mbar_wait(smem_u32(&sh.empty[s]), ((u / STAGES) & 1) ^ 1, abort_flag, a.err);
-                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    ok = warp_wait(smem_u32(&sh.empty[s]), ((u / STAGES) & 1) ^ 1, abort_flag, a.err);
                     if (!ok) break;
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -259,7 +250,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
             if (!ok) break;
             if (lane == 0) {
-                ok = mbar_wait(smem_u32(&sh.q.next_bar), k & 1, abort_flag, a.err);
+                ok = wait_bar(smem_u32(&sh.q.next_bar), k & 1, abort_flag, a.err);
                 if (ok) id = next_block_answer(smem_u32(sh.q.next_resp));
                 fence_proxy_async_smem();
             }
@@ -268,9 +259,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         }
         if (lane == 0) {
             const uint32_t pend = u < STAGES ? u : STAGES;
-            for (uint32_t j = 1; j <= pend; ++j) drain(&sh.full[(u - j) % STAGES], ((u - j) / STAGES) & 1, a.err);
-            if (nkv > 0) drain(&sh.kv_full, (nkv - 1) & 1, a.err);
-            if (!ok) drain(&sh.q.next_bar, k & 1, a.err);
+            for (uint32_t j = 1; j <= pend; ++j) drain_bar(&sh.full[(u - j) % STAGES], ((u - j) / STAGES) & 1, a.err);
+            if (nkv > 0) drain_bar(&sh.kv_full, (nkv - 1) & 1, a.err);
+            if (!ok) drain_bar(&sh.q.next_bar, k & 1, a.err);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -279,8 +270,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         uint32_t u = 0, nkv = 0, nd = 0, nacc = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (lane == 0) ok = mbar_wait(smem_u32(bar), parity, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(bar), parity, abort_flag, a.err);
             return ok;
         };
         const uint32_t sk = smem_u32(smem + K_OFF), sv = smem_u32(smem + V_OFF), sst = smem_u32(smem + ST_OFF);
@@ -289,7 +279,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             const uint32_t s = uu % STAGES;
             if (!wait(&sh.full[s], (uu / STAGES) & 1)) return false;
             if (left < TQ) {
-                if (mbar_wait(smem_u32(&sh.full[s]), (uu / STAGES) & 1, abort_flag, a.err))
+                if (wait_bar(smem_u32(&sh.full[s]), (uu / STAGES) & 1, abort_flag, a.err))
                     zero_rows(smem + ST_OFF + s * STAGE, 5, QU, left, TQ, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -377,7 +367,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         }
         if (elect_one()) {
             tc_commit(smem_u32(&sh.fin));
-            drain(&sh.fin, 0, a.err);
+            drain_bar(&sh.fin, 0, a.err);
         }
         __syncwarp();
     } else {
@@ -585,8 +575,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                     it.n = max(0, end + 127) / 128;
                 }
             }
-            if (lane == 0) ok = mbar_wait(smem_u32(&sh.q.empty[slot]), ((k >> 1) & 1) ^ 1, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(&sh.q.empty[slot]), ((k >> 1) & 1) ^ 1, abort_flag, a.err);
             if (!ok) break;
             if (lane == 0) {
                 sh.q.item[slot] = it;
@@ -594,7 +583,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             }
             if (id < 0) break;
             if (it.valid == 1 && it.n > 0 && lane == 0) {
-                ok = mbar_wait(smem_u32(&sh.q_empty), (nq & 1) ^ 1, abort_flag, a.err);
+                ok = wait_bar(smem_u32(&sh.q_empty), (nq & 1) ^ 1, abort_flag, a.err);
                 if (ok) {
                     ++nq;
                     const uint32_t fb = smem_u32(&sh.q_full);
@@ -608,7 +597,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                     const int row = it.other0 + 128 * i;
                     for (int c = 0; c < 5; ++c, ++u) {
                         const uint32_t s = u % NU, fb = smem_u32(&sh.full[s]);
-                        ok = mbar_wait(smem_u32(&sh.empty[s]), ((u / NU) & 1) ^ 1, abort_flag, a.err);
+                        ok = wait_bar(smem_u32(&sh.empty[s]), ((u / NU) & 1) ^ 1, abort_flag, a.err);
                         if (!ok) break;
                         const uint32_t dst = smem_u32(smem + RING_OFF + s * UNIT);
                         mbar_arrive_expect_tx(fb, UNIT);
@@ -621,7 +610,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             if (lane == 0) {
-                ok = mbar_wait(smem_u32(&sh.q.next_bar), k & 1, abort_flag, a.err);
+                ok = wait_bar(smem_u32(&sh.q.next_bar), k & 1, abort_flag, a.err);
                 if (ok) id = next_block_answer(smem_u32(sh.q.next_resp));
                 fence_proxy_async_smem();
             }
@@ -630,9 +619,9 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         }
         if (lane == 0) {
             const uint32_t pend = u < NU ? u : NU;
-            for (uint32_t j = 1; j <= pend; ++j) drain(&sh.full[(u - j) % NU], ((u - j) / NU) & 1, a.err);
-            if (nq > 0) drain(&sh.q_full, (nq - 1) & 1, a.err);
-            if (!ok) drain(&sh.q.next_bar, k & 1, a.err);
+            for (uint32_t j = 1; j <= pend; ++j) drain_bar(&sh.full[(u - j) % NU], ((u - j) / NU) & 1, a.err);
+            if (nq > 0) drain_bar(&sh.q_full, (nq - 1) & 1, a.err);
+            if (!ok) drain_bar(&sh.q.next_bar, k & 1, a.err);
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -640,8 +629,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         uint32_t u = 0, nq = 0, nfree = 0, nd = 0, nacc = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (lane == 0) ok = mbar_wait(smem_u32(bar), parity, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(bar), parity, abort_flag, a.err);
             return ok;
         };
         auto unit = [&](uint32_t uu) { return smem_u32(smem + RING_OFF + (uu % NU) * UNIT); };
@@ -651,7 +639,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             if (!ok) return false;
             if (keys < 128) {       // K's rows past the last key meet ds = 0, but need not be finite
                 for (int c = 2; c < 5; ++c)
-                    if (mbar_wait(smem_u32(&sh.full[(uu + c) % NU]), ((uu + c) / NU) & 1, abort_flag, a.err))
+                    if (wait_bar(smem_u32(&sh.full[(uu + c) % NU]), ((uu + c) / NU) & 1, abort_flag, a.err))
                         zero_rows(smem + RING_OFF + ((uu + c) % NU) * UNIT, 1, UNIT, keys, (keys + 15) & ~15, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -709,7 +697,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         }
         if (elect_one()) {
             tc_commit(smem_u32(&sh.fin));
-            drain(&sh.fin, 0, a.err);
+            drain_bar(&sh.fin, 0, a.err);
         }
         __syncwarp();
     } else {

@@ -45,7 +45,7 @@ constexpr int MAXRAW = 6;                     // FP8: raw stages (64 records x 1
 constexpr int CTRL = 6144;
 struct Shared {
     uint64_t full[MAXP], empty[MAXP], raw_full[MAXRAW], raw_empty[MAXRAW], r_full[2], r_empty[2], info_full[kInfo], tile_full[2], tile_empty[2];
-    uint64_t q_full, q_empty, s_full[2], p_full, pv_done, o_empty, fin;
+    uint64_t q_empty, s_full[2], s_free[2], p_full, pv_done, o_empty, fin[2];
     uint32_t tmem;
     int abort_flag;
     int b0, tile0, left;                      // first piece of this block's range
@@ -94,16 +94,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
             mbar_init(smem_u32(&sh.r_full[i]), 1);
             mbar_init(smem_u32(&sh.r_empty[i]), 1);
             mbar_init(smem_u32(&sh.s_full[i]), 1);
+            mbar_init(smem_u32(&sh.s_free[i]), 4);
+            mbar_init(smem_u32(&sh.fin[i]), 1);
         }
         for (int i = 0; i < MAXRAW; ++i) { mbar_init(smem_u32(&sh.raw_full[i]), 1); mbar_init(smem_u32(&sh.raw_empty[i]), FP8 ? CW / 4 : 1); }
         for (int i = 0; i < kInfo; ++i) mbar_init(smem_u32(&sh.info_full[i]), 1);
         for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&sh.tile_full[i]), 1); mbar_init(smem_u32(&sh.tile_empty[i]), 1); }
-        mbar_init(smem_u32(&sh.q_full), 32);
         mbar_init(smem_u32(&sh.q_empty), 1);
         mbar_init(smem_u32(&sh.p_full), 128);
         mbar_init(smem_u32(&sh.pv_done), 1);
         mbar_init(smem_u32(&sh.o_empty), 128);
-        mbar_init(smem_u32(&sh.fin), 1);
         sh.abort_flag = 0;
         fence_mbar_init();
     }
@@ -167,8 +167,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         uint32_t u = 0, g = 0, nr = 0;                 // stages, tiles and rope loads so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (lane == 0) ok = mbar_wait(smem_u32(bar), parity, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(bar), parity, abort_flag, a.err);
             return ok;
         };
         while (ok && next_piece(a, b, tile, left, &p, TT)) {
@@ -190,126 +189,96 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
             }
         }
         if (lane == 0) {                                // nothing is in flight when the block ends
-            for (uint32_t e = 1; e <= static_cast<uint32_t>(depth) && e <= u; ++e) drain(&full[(u - e) % depth], ((u - e) / depth) & 1, a.err);
-            for (uint32_t e = 1; e <= 2 && e <= nr; ++e) drain(&sh.r_full[(nr - e) & 1], ((nr - e) >> 1) & 1, a.err);
+            for (uint32_t e = 1; e <= static_cast<uint32_t>(depth) && e <= u; ++e) drain_bar(&full[(u - e) % depth], ((u - e) / depth) & 1, a.err);
+            for (uint32_t e = 1; e <= 2 && e <= nr; ++e) drain_bar(&sh.r_full[(nr - e) & 1], ((nr - e) >> 1) & 1, a.err);
         }
         __syncwarp();
     } else if (warp == 6) {
         lookup_tiles<FP8, TT>(a, b, tile, left, 0, 0, sh.recs, sh.tile_full, sh.tile_empty, sh.live, sh.scale, sh.info_full,
                               abort_flag);
-    } else if (warp == 5) {
-        // ------------------------------------------------ Q of each sequence
-        uint32_t np = 0;
-        while (next_piece(a, b, tile, left, &p, TT)) {
-            if (!warp_wait(smem_u32(&sh.q_empty), (np & 1) ^ 1, abort_flag, a.err)) break;
-            load_q<RN>(a, p.b, rb * ROWS, rows, smem_u32(sq), lane);
-            mbar_arrive(smem_u32(&sh.q_full));
-            ++np;
-        }
     } else if (warp == 4) {
-        // ---------------------------------------------------------------- MMA
-        constexpr uint32_t id_s = idesc_bf16_f32(TT, RN), id_o = idesc_bf16_f32_t(128, RN, 1, 1);
+        // ---------------------- Q of each sequence, scores: S^T of every tile as it arrives
+        constexpr uint32_t id_s = idesc_bf16_f32(TT, RN);
         uint32_t u = 0, g = 0, np = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (lane == 0) ok = mbar_wait(smem_u32(bar), parity, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(bar), parity, abort_flag, a.err);
             return ok;
         };
         while (ok && next_piece(a, b, tile, left, &p, TT)) {
-            if (!wait(&sh.q_full, np & 1)) break;
-            const int n = p.t1 - p.t0;
-            // Whatever can run next does: the scores of the next tile (at most two ahead of P V, their two buffers), or
-            // P V of the next tile, which frees ring stages and goes first.
-            int si = 0, pi = 0;
-            uint32_t spins = 0;
-            uint64_t t0 = 0;
-            while (pi < n) {
-                const uint32_t gs = g + si, gp = g + pi, us = u + 4 * si;
-                int go = 0;
-                if (lane == 0) {
-                    if (pi < si && mbar_test(smem_u32(&sh.p_full), gp & 1) &&
-                        (pi > 0 || mbar_test(smem_u32(&sh.o_empty), (np & 1) ^ 1))) {
-                        go = 2;
-                    } else if (si < n && si < pi + 2) {
-                        go = 1;
-#pragma unroll
-                        for (int c = 3; c >= 0; --c)
-                            if (go && !mbar_test(smem_u32(&sh.full[(us + c) % stages]), ((us + c) / stages) & 1)) go = 0;
-                        if (go && !mbar_test(smem_u32(&sh.r_full[gs & 1]), (gs >> 1) & 1)) go = 0;
-                    }
-                }
-                go = __shfl_sync(0xffffffffu, go, 0);
-                if (go == 0) {
-                    // nothing to do yet: bounded in time
-                    if ((++spins & 255u) == 0) {
-                        if (lane == 0) {
-                            const uint64_t now = globaltimer_ns();
-                            if (t0 == 0) t0 = now;
-                            if (*abort_flag) ok = false;
-                            else if (now - t0 > kWaitLimitNs) { ok = false; *abort_flag = 1; set_dev_error(a.err, DEV_ERR_TIMEOUT); }
-                        }
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
-                        if (!ok) break;
-                    }
-                    continue;
-                }
-                spins = 0;
-                t0 = 0;
-                if (go == 1) {
+            if (!wait(&sh.q_empty, (np & 1) ^ 1)) break;      // the scores of the piece before are complete
+            load_q<RN>(a, p.b, rb * ROWS, rows, smem_u32(sq), lane);
+            __syncwarp();
+            ++np;
+            for (int n = p.t1 - p.t0; n > 0; --n, ++g) {
+                if (!wait(&sh.s_free[g & 1], ((g >> 1) & 1) ^ 1)) break;
+                const uint32_t d = tm_s + 64 * (g & 1);
+                for (int c = 0; c < 4; ++c, ++u) {
+                    const uint32_t s = u % stages;
+                    if (!wait(&sh.full[s], (u / stages) & 1)) break;
                     if (elect_one()) {
                         tc_fence_after();
-                        const uint32_t d = tm_s + 64 * (gs & 1);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint64_t bd = smem_desc_sw128(smem_u32(sq + (2 * c + e) * QC));
-                                const uint64_t ad = smem_desc_sw128(smem_u32(sring + ((us + c) % stages) * PAIR + e * CH));
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    tc_mma_bf16(d, ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || e > 0 || kk > 0);
-                            }
-                        const uint64_t bd = smem_desc_sw128(smem_u32(sq + 8 * QC));
-                        const uint64_t ad = smem_desc_sw128(smem_u32(srope + (gs & 1) * CH));
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            tc_mma_bf16(FP8 ? tm_r + 64 * (gs & 1) : d, ad + 2ull * kk, bd + 2ull * kk, id_s, !FP8 || kk > 0);
-                        tc_commit(smem_u32(&sh.r_empty[gs & 1]));
-                        tc_commit(smem_u32(&sh.s_full[gs & 1]));
-                        if (si + 1 == n) tc_commit(smem_u32(&sh.q_empty));
-                    }
-                    __syncwarp();
-                    ++si;
-                } else {
-                    if (elect_one()) {
-                        tc_fence_after();
-                        const uint64_t bd = smem_desc_sw128_mn(smem_u32(sp), CH);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const uint32_t st = (u + 4 * pi + q) % stages;
-                            const uint64_t ad = smem_desc_sw128_mn(smem_u32(sring + st * PAIR), CH);
+                        for (int e = 0; e < 2; ++e) {
+                            const uint64_t bd = smem_desc_sw128(smem_u32(sq + (2 * c + e) * QC));
+                            const uint64_t ad = smem_desc_sw128(smem_u32(sring + s * PAIR + e * CH));
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                tc_mma_bf16(tm_o + q * RN, ad + 128ull * kk, bd + 128ull * kk, id_o, pi > 0 || kk > 0);
-                            tc_commit(smem_u32(&sh.empty[st]));
+                                tc_mma_bf16(d, ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || e > 0 || kk > 0);
                         }
-                        tc_commit(smem_u32(&sh.pv_done));
                     }
                     __syncwarp();
-                    ++pi;
                 }
+                if (!ok || !wait(&sh.r_full[g & 1], (g >> 1) & 1)) break;
+                if (elect_one()) {
+                    tc_fence_after();
+                    const uint64_t bd = smem_desc_sw128(smem_u32(sq + 8 * QC));
+                    const uint64_t ad = smem_desc_sw128(smem_u32(srope + (g & 1) * CH));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_bf16(FP8 ? tm_r + 64 * (g & 1) : d, ad + 2ull * kk, bd + 2ull * kk, id_s, !FP8 || kk > 0);
+                    tc_commit(smem_u32(&sh.r_empty[g & 1]));
+                    tc_commit(smem_u32(&sh.s_full[g & 1]));
+                    if (n == 1) tc_commit(smem_u32(&sh.q_empty));
+                }
+                __syncwarp();
             }
-            if (!ok) break;
-            g += n;
-            u += 4 * n;
-            ++np;
         }
         if (elect_one()) {
-            tc_commit(smem_u32(&sh.fin));
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(smem_u32(&sh.fin), 0))
-                if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(a.err, DEV_ERR_TIMEOUT); break; }
+            tc_commit(smem_u32(&sh.fin[0]));
+            drain_bar(&sh.fin[0], 0, a.err);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------------------------- O^T += C^T P
+        constexpr uint32_t id_o = idesc_bf16_f32_t(128, RN, 1, 1);
+        uint32_t u = 0, g = 0, np = 0;
+        bool ok = true;
+        while (ok && next_piece(a, b, tile, left, &p, TT)) {
+            for (int i = 0; i < p.t1 - p.t0; ++i, ++g) {
+                if (i == 0) ok = warp_wait(smem_u32(&sh.o_empty), (np++ & 1) ^ 1, abort_flag, a.err);
+                if (!ok || !(ok = warp_wait(smem_u32(&sh.p_full), g & 1, abort_flag, a.err))) break;
+                if (elect_one()) {
+                    tc_fence_after();
+                    const uint64_t bd = smem_desc_sw128_mn(smem_u32(sp), CH);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t st = (u + q) % stages;
+                        const uint64_t ad = smem_desc_sw128_mn(smem_u32(sring + st * PAIR), CH);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            tc_mma_bf16(tm_o + q * RN, ad + 128ull * kk, bd + 128ull * kk, id_o, i > 0 || kk > 0);
+                        tc_commit(smem_u32(&sh.empty[st]));
+                    }
+                    tc_commit(smem_u32(&sh.pv_done));
+                }
+                __syncwarp();
+                u += 4;
+            }
+        }
+        if (elect_one()) {
+            tc_commit(smem_u32(&sh.fin[1]));
+            drain_bar(&sh.fin[1], 0, a.err);
         }
         __syncwarp();
     } else {
@@ -335,8 +304,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
 #pragma unroll
             for (int i = 0; i < RN; ++i) l[i] = 0.f;
             for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
-                mbar_wait(smem_u32(&sh.info_full[g % kInfo]), (g / kInfo) & 1, abort_flag, a.err);
-                mbar_wait(smem_u32(&sh.s_full[g & 1]), (g >> 1) & 1, abort_flag, a.err);
+                wait_bar(smem_u32(&sh.info_full[g % kInfo]), (g / kInfo) & 1, abort_flag, a.err);
+                wait_bar(smem_u32(&sh.s_full[g & 1]), (g >> 1) & 1, abort_flag, a.err);
                 tc_fence_after();
                 uint32_t s[RN];
 #pragma unroll
@@ -357,6 +326,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                     }
                 }
                 tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.s_free[g & 1]));
                 const bool live = lane < 16 && ((sh.live[g % kInfo][rec >> 5] >> (rec & 31)) & 1u);
                 const int pos = ti * TT + rec;
                 // rows of earlier new tokens see fewer positions: query j sees [0, len - (n_q - 1 - j))
@@ -406,7 +378,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
 #pragma unroll
                         for (int i = 0; i < RN; ++i) l[i] *= sh.f[i];
                         // O^T is complete up to the tile before
-                        mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
+                        wait_bar(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
                         tc_fence_after();
 #pragma unroll 1
                         for (int cc = 0; cc < 4 * RN; cc += 16) {
@@ -428,7 +400,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                     }
                 }
                 // P is free once the product of the tile before is done
-                if (g > 0) mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
+                if (g > 0) wait_bar(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
                 const float4* m4 = reinterpret_cast<const float4*>(sh.m);
                 const uint32_t prow = smem_u32(sp) + rec * 128;
                 const float vs = FP8 ? sh.scale[g % kInfo][rec] : 1.f;      // V's rows are codes
@@ -475,7 +447,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 }
             }
             bar_sync(1, 128);
-            mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
+            wait_bar(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
             tc_fence_after();
             // O^T: lane = latent element, column = row
 #pragma unroll 1

@@ -215,12 +215,6 @@ __device__ __forceinline__ void put_codes(const uint4& v, uint32_t base, int y, 
     sts16(base + ((y ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
     sts16(base + (((y + 1) ^ (r & 7)) << 4), o[4], o[5], o[6], o[7]);
 }
-// Bounded wait without regard to the abort flag, for loads in flight at the block's end.
-__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity, int* err) {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait(smem_u32(bar), parity))
-        if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(err, DEV_ERR_TIMEOUT); break; }
-}
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 // Barrier of n threads that also tells whether any of them brought `v`.
 __device__ __forceinline__ bool bar_any(int id, int n, bool v) {

@@ -159,8 +159,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
         uint32_t u = 0, g = 0;                          // stages and tiles so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (lane == 0) ok = mbar_wait(smem_u32(bar), parity, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(bar), parity, abort_flag, a.err);
             return ok;
         };
         auto stage = [&](const Half& gr, int col) {
@@ -201,9 +200,9 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
         if (lane == 0) {                                // nothing is in flight when the block ends
             // (the even CTA waits for both CTAs' loads; the pair leaves together)
             if (FP8 || rank == 0)
-                for (uint32_t e = 1; e <= static_cast<uint32_t>(depth) && e <= u; ++e) drain(&full[(u - e) % depth], ((u - e) / depth) & 1, a.err);
+                for (uint32_t e = 1; e <= static_cast<uint32_t>(depth) && e <= u; ++e) drain_bar(&full[(u - e) % depth], ((u - e) / depth) & 1, a.err);
             if (rank == 0)
-                for (uint32_t e = 1; e <= 2 && e <= g; ++e) drain(&sh.r_full[(g - e) & 1], ((g - e) >> 1) & 1, a.err);
+                for (uint32_t e = 1; e <= 2 && e <= g; ++e) drain_bar(&sh.r_full[(g - e) & 1], ((g - e) >> 1) & 1, a.err);
         }
         __syncwarp();
     } else if (warp == 6) {
@@ -243,15 +242,14 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
         uint32_t u = 0, g = 0, np = 0, gp = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (lane == 0) ok = mbar_wait(smem_u32(bar), parity, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(bar), parity, abort_flag, a.err);
             return ok;
         };
         auto wait_stage = [&](uint32_t uu) {
             const uint32_t s = uu % stages, par = (uu / stages) & 1;
             if (lane == 0)
-                ok = mbar_wait(smem_u32(&sh.full[s]), par, abort_flag, a.err) &&
-                     (!FP8 || mbar_wait(smem_u32(&sh.peer[s]), par, abort_flag, a.err));
+                ok = wait_bar(smem_u32(&sh.full[s]), par, abort_flag, a.err) &&
+                     (!FP8 || wait_bar(smem_u32(&sh.peer[s]), par, abort_flag, a.err));
             ok = __shfl_sync(0xffffffffu, ok, 0);
             return ok;
         };
@@ -316,7 +314,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
         }
         if (elect_one()) {
             tc_commit_pair_multicast(smem_u32(&sh.fin), 1);
-            drain(&sh.fin, 0, a.err);
+            drain_bar(&sh.fin, 0, a.err);
         }
         __syncwarp();
     } else {
@@ -341,8 +339,8 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
             const int end = mine ? p.len - (a.n_q - 1 - j) : 0;        // this row sees positions [0, end)
             float m = -CUDART_INF_F, l = 0.f;
             for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
-                mbar_wait(smem_u32(&sh.info_full[g % kInfo]), (g / kInfo) & 1, abort_flag, a.err);
-                mbar_wait(smem_u32(&sh.s_full[g & 1]), (g >> 1) & 1, abort_flag, a.err);
+                wait_bar(smem_u32(&sh.info_full[g % kInfo]), (g / kInfo) & 1, abort_flag, a.err);
+                wait_bar(smem_u32(&sh.s_full[g & 1]), (g >> 1) & 1, abort_flag, a.err);
                 tc_fence_after();
                 uint32_t s[2][32];
                 tmem_ld32(tm_s + 64 * (g & 1) + lane_base, s[0]);
@@ -400,7 +398,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
                     m = nm;
                     l *= f;
                     if (!first) {
-                        mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
+                        wait_bar(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
                         tc_fence_after();
 #pragma unroll 1
                         for (int cc = 0; cc < 256; cc += 32) {
@@ -432,7 +430,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
                     w[2 * q + 1] = pack_bf16x2(x[2], x[3]);
                 }
                 l += sum[0] + sum[1];
-                if (g > 0) mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
+                if (g > 0) wait_bar(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
                 const uint32_t prow = smem_u32(sp) + th * CH + hr * 128;
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
@@ -455,7 +453,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
                 if (!whole) part_lse[prow] = lse;
                 else if (a.lse) a.lse[orow * a.H + h] = lse * kLn2;
             }
-            mbar_wait(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
+            wait_bar(smem_u32(&sh.pv_done), (g - 1) & 1, abort_flag, a.err);
             tc_fence_after();
             // O: TMEM column 128 j + i of lanes 64 th .. is output element 256 j + 128 th + i
 #pragma unroll 1

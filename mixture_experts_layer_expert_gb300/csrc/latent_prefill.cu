@@ -143,8 +143,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     }
                 }
             }
-            if (lane == 0) ok = mbar_wait(smem_u32(&sh.item_empty[slot]), (use & 1) ^ 1, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(&sh.item_empty[slot]), (use & 1) ^ 1, abort_flag, a.err);
             if (!ok) break;
             if (lane == 0) {
                 sh.item[slot] = it;
@@ -153,7 +152,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (id < 0) break;
             const int n = max(it.n[0], it.n[1]);
             if (it.valid == 1 && n > 0 && lane == 0) {
-                ok = mbar_wait(smem_u32(&sh.q_empty), (nq & 1) ^ 1, abort_flag, a.err);
+                ok = wait_bar(smem_u32(&sh.q_empty), (nq & 1) ^ 1, abort_flag, a.err);
                 if (ok) {
                     ++nq;
                     const uint32_t fb = smem_u32(&sh.q_full);
@@ -168,7 +167,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     const int row = it.k0 + TK * i;
                     for (int c = 0; c < 5; ++c, ++u) {
                         const uint32_t s = u % NU, fb = smem_u32(&sh.full[s]);
-                        ok = mbar_wait(smem_u32(&sh.empty[s]), ((u / NU) & 1) ^ 1, abort_flag, a.err);
+                        ok = wait_bar(smem_u32(&sh.empty[s]), ((u / NU) & 1) ^ 1, abort_flag, a.err);
                         if (!ok) break;
                         const uint32_t dst = smem_u32(smem + RING_OFF + s * UNIT);
                         mbar_arrive_expect_tx(fb, UNIT);
@@ -181,7 +180,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             if (lane == 0) {
-                ok = mbar_wait(smem_u32(&sh.next_bar), k & 1, abort_flag, a.err);
+                ok = wait_bar(smem_u32(&sh.next_bar), k & 1, abort_flag, a.err);
                 if (ok) id = next_block_answer(smem_u32(sh.next_resp));
                 fence_proxy_async_smem();        // the answer is read before the next one may be written
             }
@@ -192,19 +191,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             // the loads in flight land before the block exits
             const uint32_t pend = u < NU ? u : NU;
             for (uint32_t j = 1; j <= pend; ++j) {
-                const uint64_t t0 = globaltimer_ns();
-                while (!mbar_try_wait(smem_u32(&sh.full[(u - j) % NU]), ((u - j) / NU) & 1))
-                    if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(a.err, DEV_ERR_TIMEOUT); break; }
+                drain_bar(&sh.full[(u - j) % NU], ((u - j) / NU) & 1, a.err);
             }
             if (nq > 0) {
-                const uint64_t t0 = globaltimer_ns();
-                while (!mbar_try_wait(smem_u32(&sh.q_full), (nq - 1) & 1))
-                    if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(a.err, DEV_ERR_TIMEOUT); break; }
+                drain_bar(&sh.q_full, (nq - 1) & 1, a.err);
             }
             if (!ok) {                           // an answer may still be on its way
-                const uint64_t t0 = globaltimer_ns();
-                while (!mbar_try_wait(smem_u32(&sh.next_bar), k & 1))
-                    if (globaltimer_ns() - t0 > kWaitLimitNs) break;
+                drain_bar(&sh.next_bar, k & 1, a.err);
             }
         }
         __syncwarp();
@@ -214,8 +207,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         uint32_t u = 0, nq = 0, np[2] = {0, 0};
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
-            if (lane == 0) ok = mbar_wait(smem_u32(bar), parity, abort_flag, a.err);
-            ok = __shfl_sync(0xffffffffu, ok, 0);
+            ok = warp_wait(smem_u32(bar), parity, abort_flag, a.err);
             return ok;
         };
         auto score = [&](int t, uint32_t u0) {          // S_t = Q_t K^T from units u0 .. u0 + 2
@@ -263,7 +255,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 if (zrows > 0) {
                     for (int c = 0; c < 2; ++c) {
                         // every lane sees the unit complete before writing into it
-                        if (!mbar_wait(smem_u32(&sh.full[(uv + c) % NU]), ((uv + c) / NU) & 1, abort_flag, a.err)) continue;
+                        if (!wait_bar(smem_u32(&sh.full[(uv + c) % NU]), ((uv + c) / NU) & 1, abort_flag, a.err)) continue;
                         uint8_t* un = smem + RING_OFF + ((uv + c) % NU) * UNIT;
                         for (int z = lane; z < zrows * 8; z += 32)
                             *reinterpret_cast<uint4*>(un + keys * 128 + z * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -311,9 +303,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
         if (elect_one()) {
             tc_commit(smem_u32(&sh.fin));          // every MMA completes before TMEM is released
-            const uint64_t t0 = globaltimer_ns();
-            while (!mbar_try_wait(smem_u32(&sh.fin), 0))
-                if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(a.err, DEV_ERR_TIMEOUT); break; }
+            drain_bar(&sh.fin, 0, a.err);
         }
         __syncwarp();
     } else {
