@@ -51,6 +51,7 @@ struct Shared {
     int b0, tile0, left;                      // first piece of this block's range
     uint32_t live[kInfo][2];                  // records of a tile that count
     alignas(16) float m[ROWS], f[ROWS];       // running maximum (log2 units), rescaling factor or 1 / l
+    int lag[ROWS];                            // a row sees positions [0, length - lag)
     float red[4][ROWS];                       // the warps' maxima or sums
     float scale[kInfo][TT];                   // FP8: the records' scales
     TileRecs<TT> recs[2];
@@ -111,6 +112,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         tmem_alloc(smem_u32(&sh.tmem), 512);
         tmem_relinquish();
     }
+    if (threadIdx.x < ROWS) sh.lag[threadIdx.x] = a.n_q - 1 - min((rb * ROWS + static_cast<int>(threadIdx.x)) / a.H, a.n_q - 1);
     if (warp == 0) find_range(a, range, ranges, TT, rb == 0, meta, &sh.b0, &sh.tile0, &sh.left);
     tc_fence_before();
     __syncthreads();
@@ -133,7 +135,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                     const uint32_t rs = u % raws, s = u % stages;
                     if (!warp_wait(smem_u32(&sh.raw_full[rs]), (u / raws) & 1, abort_flag, a.err) ||
                         !warp_wait(smem_u32(&sh.empty[s]), ((u / stages) & 1) ^ 1, abort_flag, a.err)) { ok = false; break; }
-#pragma unroll
+#pragma unroll 1
                     for (int e0 = 0; e0 < NU; e0 += 4) {
                         uint4 v[4];
 #pragma unroll
@@ -176,6 +178,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 const Half hf = read_half(sh.recs[g & 1], 0, lane);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.tile_empty[g & 1]));
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c, ++u) {
                     const uint32_t s = u % depth;
                     if (!wait(&empty[s], ((u / depth) & 1) ^ 1)) break;
@@ -213,6 +216,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
             for (int n = p.t1 - p.t0; n > 0; --n, ++g) {
                 if (!wait(&sh.s_free[g & 1], ((g >> 1) & 1) ^ 1)) break;
                 const uint32_t d = tm_s + 64 * (g & 1);
+#pragma unroll 1
                 for (int c = 0; c < 4; ++c, ++u) {
                     const uint32_t s = u % stages;
                     if (!wait(&sh.full[s], (u / stages) & 1)) break;
@@ -261,7 +265,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 if (elect_one()) {
                     tc_fence_after();
                     const uint64_t bd = smem_desc_sw128_mn(smem_u32(sp), CH);
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         const uint32_t st = (u + q) % stages;
                         const uint64_t ad = smem_desc_sw128_mn(smem_u32(sring + st * PAIR), CH);
@@ -336,7 +340,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 if (edge) {
 #pragma unroll
                     for (int i = 0; i < RN; ++i)
-                        if (pos >= p.len - (a.n_q - 1 - min((rb * ROWS + i) / a.H, a.n_q - 1))) s[i] = 0xff800000u;
+                        if (pos >= p.len - sh.lag[i]) s[i] = 0xff800000u;
                 }
                 float over = -CUDART_INF_F;                     // the largest excess over the running maxima
                 if (ti > p.t0) {

@@ -22,7 +22,7 @@
 // Warps 0-3 / 4-7: softmax and output of tile 0 / 1 (thread = row = TMEM lane);
 // warp 8: work distribution and TMA loads; warp 9: MMA issue.  K, V and the
 // shared rotary key go through a ring of eight 16 KB units (128 rows x 64
-// columns): three of K (two of k_n, one of k_r), two of V per key tile.
+// columns): three of K (two of k_n, one of k_r), two of V per key tile, one barrier for each three and two.
 // Blocks take further items from the grid's not yet started blocks (cluster
 // launch control), so the next item's loads overlap this item's last tiles, and
 // items are numbered with the longest key range of each sequence first.
@@ -53,7 +53,7 @@ struct Item {
 };
 
 struct Shared {
-    uint64_t full[NU], empty[NU], q_full, q_empty, s_full[2], p_full[2], pv_done[2], item_full[2], item_empty[2];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], q_full, q_empty, s_full[2], p_full[2], pv_done[2], item_full[2], item_empty[2];
     uint64_t next_bar, fin;
     alignas(16) uint32_t next_resp[4];
     uint32_t tmem;
@@ -82,10 +82,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NU; ++i) { mbar_init(smem_u32(&sh.full[i]), 1); mbar_init(smem_u32(&sh.empty[i]), 1); }
         mbar_init(smem_u32(&sh.q_full), 1);
         mbar_init(smem_u32(&sh.q_empty), 1);
         for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&sh.k_full[t]), 1);
+            mbar_init(smem_u32(&sh.k_empty[t]), 1);
+            mbar_init(smem_u32(&sh.v_full[t]), 1);
+            mbar_init(smem_u32(&sh.v_empty[t]), 1);
             mbar_init(smem_u32(&sh.s_full[t]), 1);
             mbar_init(smem_u32(&sh.p_full[t]), 128);
             mbar_init(smem_u32(&sh.pv_done[t]), 1);
@@ -106,13 +109,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
     tc_fence_after();
     const uint32_t tm_s = sh.tmem, tm_o = sh.tmem + 256;      // S_t at 128 t, O_t at 256 + 128 t
 
+    const uint32_t ring = smem_u32(smem + RING_OFF);
     if (warp == 8) {
         // ------------------------------------------------ items and loads
         if (lane == 0) {
             tma_prefetch_desc(&tmQ); tma_prefetch_desc(&tmKn); tma_prefetch_desc(&tmKr); tma_prefetch_desc(&tmV);
         }
-        uint32_t u = 0;               // units loaded so far
-        uint32_t nq = 0;              // Q loads so far
+        uint32_t j = 0, u = 0;        // key tiles loaded so far, the ring unit the next one starts at
+        uint32_t nq = 0, nk = 0, nv = 0;      // loads of Q, K and V tiles so far
         int id = blockIdx.x;
         bool ok = true;
         uint32_t k = 0;
@@ -163,18 +167,27 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                             tma_load_3d(smem_u32(smem + (3 * t + c) * UNIT), &tmQ, fb, 64 * c, it.head,
                                         it.row0 + TQ * t);
                 }
-                for (int i = 0; ok && i < n; ++i) {
-                    const int row = it.k0 + TK * i;
-                    for (int c = 0; c < 5; ++c, ++u) {
-                        const uint32_t s = u % NU, fb = smem_u32(&sh.full[s]);
-                        ok = wait_bar(smem_u32(&sh.empty[s]), ((u / NU) & 1) ^ 1, abort_flag, a.err);
-                        if (!ok) break;
-                        const uint32_t dst = smem_u32(smem + RING_OFF + s * UNIT);
-                        mbar_arrive_expect_tx(fb, UNIT);
-                        if (c < 2) tma_load_3d(dst, &tmKn, fb, 64 * c, it.head, row);
-                        else if (c == 2) tma_load_3d(dst, &tmKr, fb, 0, 0, row);
-                        else tma_load_3d(dst, &tmV, fb, 64 * (c - 3), it.head, row);
-                    }
+                // K of tile j takes the units that V and the last of K of tile j - 2 held, V those of K of tile j - 1 ...
+                // (units 5 j .. 5 j + 4 of a ring of 8): waits on whole K and V tiles, a barrier each
+                for (int i = 0; ok && i < n; ++i, ++j, u = (u + 5) & 7) {
+                    const int row = it.k0 + TK * i, par = j & 1;
+                    const uint32_t ph = (j >> 1) & 1;
+                    ok = wait_bar(smem_u32(&sh.v_empty[par]), ph ^ 1, abort_flag, a.err) &&
+                         wait_bar(smem_u32(&sh.k_empty[par]), ph ^ 1, abort_flag, a.err);
+                    if (!ok) break;
+                    uint32_t fb = smem_u32(&sh.k_full[par]);
+                    mbar_arrive_expect_tx(fb, 3 * UNIT);
+                    tma_load_3d(ring + u * UNIT, &tmKn, fb, 0, it.head, row);
+                    tma_load_3d(ring + ((u + 1) & 7) * UNIT, &tmKn, fb, 64, it.head, row);
+                    tma_load_3d(ring + ((u + 2) & 7) * UNIT, &tmKr, fb, 0, 0, row);
+                    ++nk;
+                    if (j > 0) ok = wait_bar(smem_u32(&sh.k_empty[par ^ 1]), ((j - 1) >> 1) & 1, abort_flag, a.err);
+                    if (!ok) break;
+                    fb = smem_u32(&sh.v_full[par]);
+                    mbar_arrive_expect_tx(fb, 2 * UNIT);
+                    tma_load_3d(ring + ((u + 3) & 7) * UNIT, &tmV, fb, 0, it.head, row);
+                    tma_load_3d(ring + ((u + 4) & 7) * UNIT, &tmV, fb, 64, it.head, row);
+                    ++nv;
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -189,10 +202,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         }
         if (lane == 0) {
             // the loads in flight land before the block exits
-            const uint32_t pend = u < NU ? u : NU;
-            for (uint32_t j = 1; j <= pend; ++j) {
-                drain_bar(&sh.full[(u - j) % NU], ((u - j) / NU) & 1, a.err);
-            }
+            for (uint32_t e = 1; e <= 2 && e <= nk; ++e) drain_bar(&sh.k_full[(nk - e) & 1], ((nk - e) >> 1) & 1, a.err);
+            for (uint32_t e = 1; e <= 2 && e <= nv; ++e) drain_bar(&sh.v_full[(nv - e) & 1], ((nv - e) >> 1) & 1, a.err);
             if (nq > 0) {
                 drain_bar(&sh.q_full, (nq - 1) & 1, a.err);
             }
@@ -203,19 +214,21 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         __syncwarp();
     } else if (warp == 9) {
         // ------------------------------------------------------------ MMA
-        constexpr uint32_t id_s = idesc_bf16_f32(TQ, TK), id_o = idesc_bf16_f32_t(TQ, kDv, 0, 1);
-        uint32_t u = 0, nq = 0, np[2] = {0, 0};
+        constexpr uint32_t id_s = idesc_bf16_f32(TQ, TK), id_o = idesc_bf16_f32_t(TQ, kDv, 0, 1), id_h = idesc_bf16_f32_t(TQ, 64, 0, 1);
+        uint32_t j = 0, u = 0, nq = 0, np[2] = {0, 0};        // key tiles so far, ring unit of the current one
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = warp_wait(smem_u32(bar), parity, abort_flag, a.err);
             return ok;
         };
-        auto score = [&](int t, uint32_t u0) {          // S_t = Q_t K^T from units u0 .. u0 + 2
+        const uint64_t dq = smem_desc_sw128(smem_u32(smem)), dk = smem_desc_sw128(ring), dv = smem_desc_sw128_mn(ring, UNIT);
+        auto score = [&](int t, uint32_t u0) {                // S_t = Q_t K^T, K at units u0 .. u0 + 2
             if (elect_one()) {
                 tc_fence_after();
+#pragma unroll
                 for (int c = 0; c < 3; ++c) {
-                    const uint64_t ad = smem_desc_sw128(smem_u32(smem + (3 * t + c) * UNIT));
-                    const uint64_t bd = smem_desc_sw128(smem_u32(smem + RING_OFF + ((u0 + c) % NU) * UNIT));
+                    const uint64_t ad = dq + static_cast<uint64_t>((3 * t + c) * (UNIT >> 4));
+                    const uint64_t bd = dk + static_cast<uint64_t>(((u0 + c) & 7) * (UNIT >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
                         tc_mma_bf16(tm_s + 128 * t, ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || kk > 0);
@@ -224,82 +237,79 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
             __syncwarp();
         };
-        auto release = [&](uint32_t u0, int n) {
-            if (elect_one())
-                for (int c = 0; c < n; ++c) tc_commit(smem_u32(&sh.empty[(u0 + c) % NU]));
+        auto commit = [&](uint64_t* bar) {
+            if (elect_one()) tc_commit(smem_u32(bar));
             __syncwarp();
         };
         for (uint32_t k = 0;; ++k) {
             const uint32_t slot = k & 1;
             if (!wait(&sh.item_full[slot], (k >> 1) & 1)) break;
-            const Item it = sh.item[slot];
+            const int valid = sh.item[slot].valid, n0 = sh.item[slot].n[0], n1 = sh.item[slot].n[1], lk = sh.item[slot].lk;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.item_empty[slot]));
-            if (it.valid < 0) break;
-            const int n = max(it.n[0], it.n[1]);
-            if (it.valid == 0 || n == 0) continue;
+            if (valid < 0) break;
+            const int n = max(n0, n1);
+            if (valid == 0 || n == 0) continue;
             if (!wait(&sh.q_full, nq++ & 1)) break;
-            auto wait_units = [&](uint32_t u0, int cnt) {
-                for (int c = 0; c < cnt && ok; ++c) wait(&sh.full[(u0 + c) % NU], ((u0 + c) / NU) & 1);
-                return ok;
-            };
-            if (!wait_units(u, 3)) break;
-            for (int t = 0; t < 2; ++t)
-                if (it.n[t] > 0) score(t, u);
-            release(u, 3);
-            for (int i = 0; i < n; ++i) {
-                const uint32_t uv = u + 3, uk = u + 5;        // V of tile i, K of tile i + 1
-                if (!wait_units(uv, 2)) break;
+            if (!wait(&sh.k_full[j & 1], (j >> 1) & 1)) break;
+            if (n0 > 0) score(0, u);
+            if (n1 > 0) score(1, u);
+            commit(&sh.k_empty[j & 1]);
+#pragma unroll 1
+            for (int i = 0; i < n; ++i, ++j, u = (u + 5) & 7) {
+                const uint32_t un = (u + 5) & 7;              // K of tile i + 1
+                if (!wait(&sh.v_full[j & 1], (j >> 1) & 1)) break;
                 // rows past the sequence's last key: p there is zero, but what lies in V's rows need not be finite
-                const int keys = min(TK, it.lk - TK * i), steps = (keys + 15) >> 4, zrows = 16 * steps - keys;
+                const int keys = min(TK, lk - TK * i), steps = (keys + 15) >> 4, zrows = 16 * steps - keys;
                 if (zrows > 0) {
                     for (int c = 0; c < 2; ++c) {
-                        // every lane sees the unit complete before writing into it
-                        if (!wait_bar(smem_u32(&sh.full[(uv + c) % NU]), ((uv + c) / NU) & 1, abort_flag, a.err)) continue;
-                        uint8_t* un = smem + RING_OFF + ((uv + c) % NU) * UNIT;
+                        uint8_t* unit = smem + RING_OFF + ((u + 3 + c) & 7) * UNIT;
                         for (int z = lane; z < zrows * 8; z += 32)
-                            *reinterpret_cast<uint4*>(un + keys * 128 + z * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(unit + keys * 128 + z * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
+#pragma unroll 1
                 for (int t = 0; t < 2; ++t) {
-                    if (i < it.n[t]) {
+                    const int nt = t ? n1 : n0;
+                    if (i < nt) {
                         if (!wait(&sh.p_full[t], np[t]++ & 1)) break;
                         if (elect_one()) {
                             tc_fence_after();
-                            for (int kk = 0; kk < steps; ++kk) {
-                                const uint32_t base = smem_u32(smem + RING_OFF);
-                                const uint32_t v0 = base + (uv % NU) * UNIT, v1 = base + ((uv + 1) % NU) * UNIT;
-                                // V's two 64-column halves are two ring units: one N = 128 product, or two of 64
-                                // when they wrap around the ring's end
-                                constexpr uint32_t id_h = idesc_bf16_f32_t(TQ, 64, 0, 1);
-                                const uint32_t acc = i > 0 || kk > 0;
-                                if (v1 == v0 + UNIT) {
-                                    tc_mma_bf16_ts(tm_o + 128 * t, tm_s + 128 * t + 8 * kk,
-                                                   smem_desc_sw128_mn(v0 + 2048 * kk, UNIT), id_o, acc);
-                                } else {
-                                    tc_mma_bf16_ts(tm_o + 128 * t, tm_s + 128 * t + 8 * kk,
-                                                   smem_desc_sw128_mn(v0 + 2048 * kk, UNIT), id_h, acc);
-                                    tc_mma_bf16_ts(tm_o + 128 * t + 64, tm_s + 128 * t + 8 * kk,
-                                                   smem_desc_sw128_mn(v1 + 2048 * kk, UNIT), id_h, acc);
+                            const uint32_t uv = (u + 3) & 7;
+                            const uint64_t v0 = dv + static_cast<uint64_t>(uv * (UNIT >> 4));
+                            const uint32_t d = tm_o + 128 * t, pa = tm_s + 128 * t;
+                            if (uv != 7 && steps == 8) {
+#pragma unroll
+                                for (int kk = 0; kk < 8; ++kk)
+                                    tc_mma_bf16_ts(d, pa + 8 * kk, v0 + 128ull * kk, id_o, i > 0 || kk > 0);
+                            } else if (uv != 7) {
+#pragma unroll 1
+                                for (int kk = 0; kk < steps; ++kk)
+                                    tc_mma_bf16_ts(d, pa + 8 * kk, v0 + 128ull * kk, id_o, i > 0 || kk > 0);
+                            } else {                          // V's two halves lie at the ring's two ends
+#pragma unroll 1
+                                for (int kk = 0; kk < steps; ++kk) {
+                                    tc_mma_bf16_ts(d, pa + 8 * kk, v0 + 128ull * kk, id_h, i > 0 || kk > 0);
+                                    tc_mma_bf16_ts(d + 64, pa + 8 * kk, dv + 128ull * kk, id_h, i > 0 || kk > 0);
                                 }
                             }
                             tc_commit(smem_u32(&sh.pv_done[t]));
+                            if (t == 1) tc_commit(smem_u32(&sh.v_empty[j & 1]));
                         }
                         __syncwarp();
+                    } else if (t == 1) {
+                        commit(&sh.v_empty[j & 1]);
                     }
-                    if (t == 0 && i + 1 < n && !wait_units(uk, 3)) break;
-                    if (t == 1) release(uv, 2);
-                    if (i + 1 < it.n[t]) score(t, uk);
+                    if (t == 0 && i + 1 < n && !wait(&sh.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1)) break;
+                    if (i + 1 < nt) score(t, un);
                 }
                 if (!ok) break;
-                if (i + 1 < n) release(uk, 3);
-                u += 5;
+                if (i + 1 < n) commit(&sh.k_empty[(j + 1) & 1]);
             }
             if (!ok) break;
-            if (elect_one()) tc_commit(smem_u32(&sh.q_empty));
-            __syncwarp();
+            commit(&sh.q_empty);
         }
         if (elect_one()) {
             tc_commit(smem_u32(&sh.fin));          // every MMA completes before TMEM is released
@@ -325,34 +335,36 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (it.valid == 0 || 128 * t >= it.rows) continue;
             const int limit = row_limit(it, a.causal, r);
             float m = 0.f, l = 0.f;
-            for (int i = 0; i < it.n[t]; ++i) {
+            const int n = t ? it.n[1] : it.n[0];
+            for (int i = 0; i < n; ++i) {
                 if (!warp_wait(smem_u32(&sh.s_full[t]), ns++ & 1, abort_flag, a.err)) { ok = false; break; }
                 tc_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
-                tmem_ld_wait();
+                // two passes over the scores, 32 columns at a time: the loop bodies stay small and the registers few
                 const int lim = limit - TK * i;
-                if (__any_sync(0xffffffffu, lim < TK)) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                const bool edge = __any_sync(0xffffffffu, lim < TK);
+                float mx[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll 1
+                for (int q = 0; q < TK; q += 32) {
+                    uint32_t s[32];
+                    tmem_ld32(ts + q, s);
+                    tmem_ld_wait();
+                    if (edge) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
-                            if (32 * q + j >= lim) s[q][j] = 0xff800000u;      // -inf
-                }
-                float mx[4];
+                            if (q + j >= lim) s[j] = 0xff800000u;      // -inf
+                    }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    mx[q] = __uint_as_float(s[q][0]);
-#pragma unroll
-                    for (int j = 1; j < 32; ++j) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][j]));
+                    for (int j = 0; j < 32; j += 2) {
+                        mx[0] = fmaxf(mx[0], __uint_as_float(s[j]));
+                        mx[1] = fmaxf(mx[1], __uint_as_float(s[j + 1]));
+                    }
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+                const float top = fmaxf(mx[0], mx[1]) * c;
                 if (i == 0) {
-                    m = top == -CUDART_INF_F ? 0.f : top;
+                    m = top;
                 } else if (__any_sync(0xffffffffu, top > m + kRescale)) {
-                    // O and l to the new maximum, once PV of the tile before is in O
-                    const float mn = fmaxf(m, top), al = exp2_fast(m - mn);
+                    // O and l to the new maximum (a row without one so far, m = -inf, has nothing in them)
+                    const float mn = fmaxf(m, top), al = mn == -CUDART_INF_F ? 1.f : exp2_fast(m - mn);
                     m = mn;
                     l *= al;
                     if (!warp_wait(smem_u32(&sh.pv_done[t]), (npv + i - 1) & 1, abort_flag, a.err)) { ok = false; break; }
@@ -367,27 +379,34 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                         tmem_st32(to + 32 * q, o);
                     }
                 }
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float me = m == -CUDART_INF_F ? 0.f : m;
+                float sum[2] = {0.f, 0.f};
+#pragma unroll 1
+                for (int q = 0; q < TK; q += 32) {
+                    uint32_t s[32], p[16];
+                    tmem_ld32(ts + q, s);
+                    tmem_ld_wait();
+                    if (edge) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t p[32];
+                        for (int j = 0; j < 32; ++j)
+                            if (q + j >= lim) s[j] = 0xff800000u;
+                    }
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float x0 = exp2_fast(fmaf(__uint_as_float(s[2 * q + j / 16][2 * (j & 15)]), c, -m));
-                        const float x1 = exp2_fast(fmaf(__uint_as_float(s[2 * q + j / 16][2 * (j & 15) + 1]), c, -m));
-                        sum[j & 1] += x0;
-                        sum[2 + (j & 1)] += x1;
+                    for (int j = 0; j < 16; ++j) {
+                        const float x0 = exp2_fast(fmaf(__uint_as_float(s[2 * j]), c, -me));
+                        const float x1 = exp2_fast(fmaf(__uint_as_float(s[2 * j + 1]), c, -me));
+                        sum[0] += x0;
+                        sum[1] += x1;
                         p[j] = pack_bf16x2(x0, x1);
                     }
-                    tmem_st32(ts + 32 * q, p);
+                    tmem_st16(ts + q / 2, p);       // P's columns q / 2 .. hold scores that were read before
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += sum[0] + sum[1];
                 tmem_st_wait();
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh.p_full[t]));
             }
             if (!ok) break;
-            const int n = it.n[t];
             npv += n;
             if (n > 0) {
                 if (!warp_wait(smem_u32(&sh.pv_done[t]), (npv - 1) & 1, abort_flag, a.err)) break;
