@@ -47,21 +47,6 @@ __device__ __forceinline__ bool next_piece(const LatentDecodeArgs& a, int& b, in
     return true;
 }
 
-// The table's entry for position pos of sequence b (0 past the end): only the load, so that it can be issued a
-// tile ahead of its use.
-__device__ __forceinline__ int page_at(const LatentDecodeArgs& a, int b, int len, int pos) {
-    return pos < len ? __ldg(a.table + b * a.table_row + pos / a.page_size) : 0;
-}
-// Record of position pos on that page, or NONE (past the end, or a page outside the cache, which is recorded).
-__device__ __forceinline__ uint32_t record_of(const LatentDecodeArgs& a, int len, int pos, int page) {
-    if (pos >= len) return NONE;
-    if (page < 0 || page >= a.n_pages) {
-        set_dev_error(a.err, DEV_ERR_PAGE);
-        return NONE;
-    }
-    return static_cast<uint32_t>(page) * static_cast<uint32_t>(a.page_size) + static_cast<uint32_t>(pos % a.page_size);
-}
-
 // A tile's records as the loader needs them, for TT / 64 halves of 64 consecutive positions.
 template <int TT>
 struct TileRecs {
@@ -72,9 +57,10 @@ struct TileRecs {
 constexpr int kInfo = 6;        // depth of what the lookup leaves for the softmax (see lookup_tiles)
 
 // The lookup warp: for every tile of the block's range, its records (two tiles ahead of the loads at most),
-// which of them count and (FP8) their scales, and its part `own` of the halves asked into L2.  It is at most two
-// tiles ahead of the loads, which a full ring holds less than four tiles ahead of the softmax: slots of kInfo
-// tiles are free when they come round.
+// which of them count and (FP8) their scales, and its halves own0 .. own1 asked into L2.  Three tiles are under
+// way: the table's entries of one, the scales of the tile before, the publication of the tile before that, so no
+// load is waited for in the iteration that issues it.  It is at most two tiles ahead of the loads, which a full
+// ring holds less than four tiles ahead of the softmax: slots of kInfo tiles are free when they come round.
 template <bool FP8, int TT>
 __device__ __forceinline__ void lookup_tiles(const LatentDecodeArgs& a, int b, int tile, int left, int own0, int own1,
                                              TileRecs<TT>* recs, uint64_t* tile_full, uint64_t* tile_empty,
@@ -83,58 +69,83 @@ __device__ __forceinline__ void lookup_tiles(const LatentDecodeArgs& a, int b, i
     constexpr int NE = TT / 32, REC = FP8 ? kRecFp8 : kRecBf16;
     const int lane = threadIdx.x & 31;
     const int records = static_cast<int>(a.n_pages * a.page_size);
+    const int step_pages = TT / a.page_size, step_off = TT % a.page_size;
     Piece p;
     uint32_t g = 0;
     while (next_piece(a, b, tile, left, &p, TT)) {
-        int pg[NE];                                 // table entries of the next tile's positions 32 e + lane
+        const int32_t* table = a.table + p.b * a.table_row;
+        int pi[NE], off[NE], page[NE], poff[NE];     // page index and offset of the next tile's positions 32 e + lane
+        uint32_t r[NE];                              // records (and scales) of the tile to publish next
+        float sc[NE];
 #pragma unroll
-        for (int e = 0; e < NE; ++e) pg[e] = page_at(a, p.b, p.len, p.t0 * TT + 32 * e + lane);
-        for (int ti = p.t0; ti < p.t1; ++ti, ++g) {
-            uint32_t r[NE], lv[NE];
-            float sc[NE];
+        for (int e = 0; e < NE; ++e) {
+            const int pos = p.t0 * TT + 32 * e + lane;
+            pi[e] = pos / a.page_size;
+            off[e] = pos - pi[e] * a.page_size;
+            page[e] = poff[e] = 0;
+            r[e] = NONE;
+            sc[e] = 0.f;
+        }
+#pragma unroll 1
+        for (int ti = p.t0; ti < p.t1 + 2; ++ti) {
+            if (ti >= p.t0 + 2) {                    // publish tile ti - 2
+                if (!warp_wait(smem_u32(&tile_empty[g & 1]), ((g >> 1) & 1) ^ 1, abort_flag, a.err)) return;
+                TileRecs<TT>& t = recs[g & 1];
+                const uint32_t k = g % kInfo;
 #pragma unroll
-            for (int e = 0; e < NE; ++e) {
-                r[e] = record_of(a, p.len, ti * TT + 32 * e + lane, pg[e]);
-                if (ti + 1 < p.t1) pg[e] = page_at(a, p.b, p.len, (ti + 1) * TT + 32 * e + lane);
-                lv[e] = __ballot_sync(0xffffffffu, r[e] != NONE);
-                sc[e] = 0.f;
-                if (r[e] != NONE) {
-                    const uint8_t* rec = a.cache + static_cast<long long>(r[e]) * REC;
-                    if (FP8) sc[e] = *reinterpret_cast<const float*>(rec + kFp8ScaleOff);
-                    if (e / 2 >= own0 && e / 2 <= own1) {
-#pragma unroll
-                        for (int q = 0; q < REC; q += 128) prefetch_l2(rec + q);
+                for (int h = 0; h < TT / 64; ++h) {
+                    const uint32_t r0 = r[2 * h], r1 = r[2 * h + 1];
+                    const uint32_t l0 = __ballot_sync(0xffffffffu, r0 != NONE), l1 = __ballot_sync(0xffffffffu, r1 != NONE);
+                    const uint32_t start = __shfl_sync(0xffffffffu, r0, 0);
+                    const bool none = (l0 | l1) == 0;
+                    const bool box = none || __all_sync(0xffffffffu, r0 == start + lane && r1 == start + 32 + lane && r1 != NONE);
+                    const uint32_t s0 = __shfl_sync(0xffffffffu, r0, l0 ? __ffs(l0) - 1 : 0);
+                    const uint32_t s1 = __shfl_sync(0xffffffffu, r1, l1 ? __ffs(l1) - 1 : 0);
+                    const uint32_t some = l0 ? s0 : s1;
+                    t.rec[64 * h + lane] = static_cast<int>(r0 == NONE ? some : r0);
+                    t.rec[64 * h + 32 + lane] = static_cast<int>(r1 == NONE ? some : r1);
+                    if (FP8) {
+                        scale[k][64 * h + lane] = sc[2 * h];
+                        scale[k][64 * h + 32 + lane] = sc[2 * h + 1];
+                    }
+                    if (lane == 0) {
+                        t.start[h] = none ? records : static_cast<int>(start);
+                        t.box[h] = box;
+                        live[k][2 * h] = l0;
+                        live[k][2 * h + 1] = l1;
                     }
                 }
-            }
-            if (!warp_wait(smem_u32(&tile_empty[g & 1]), ((g >> 1) & 1) ^ 1, abort_flag, a.err)) return;
-            TileRecs<TT>& t = recs[g & 1];
-#pragma unroll
-            for (int h = 0; h < TT / 64; ++h) {
-                const uint32_t r0 = r[2 * h], r1 = r[2 * h + 1], l0 = lv[2 * h], l1 = lv[2 * h + 1];
-                const uint32_t start = __shfl_sync(0xffffffffu, r0, 0);
-                const bool none = (l0 | l1) == 0;
-                const bool box = none || __all_sync(0xffffffffu, r0 == start + lane && r1 == start + 32 + lane && r1 != NONE);
-                const uint32_t s0 = __shfl_sync(0xffffffffu, r0, l0 ? __ffs(l0) - 1 : 0);
-                const uint32_t s1 = __shfl_sync(0xffffffffu, r1, l1 ? __ffs(l1) - 1 : 0);
-                const uint32_t some = l0 ? s0 : s1;
-                t.rec[64 * h + lane] = static_cast<int>(r0 == NONE ? some : r0);
-                t.rec[64 * h + 32 + lane] = static_cast<int>(r1 == NONE ? some : r1);
+                __syncwarp();
                 if (lane == 0) {
-                    t.start[h] = none ? records : static_cast<int>(start);
-                    t.box[h] = box;
+                    mbar_arrive(smem_u32(&tile_full[g & 1]));
+                    mbar_arrive(smem_u32(&info_full[k]));
                 }
+                ++g;
             }
-            const uint32_t k = g % kInfo;
 #pragma unroll
             for (int e = 0; e < NE; ++e) {
-                if (FP8) scale[k][32 * e + lane] = sc[e];
-                if (lane == 0) live[k][e] = lv[e];
-            }
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&tile_full[g & 1]));
-                mbar_arrive(smem_u32(&info_full[k]));
+                // records of tile ti - 1 from its pages; a page outside the cache is recorded and its positions left out
+                r[e] = NONE;
+                sc[e] = 0.f;
+                if (ti > p.t0 && (ti - 1) * TT + 32 * e + lane < p.len) {
+                    if (page[e] < 0 || page[e] >= a.n_pages) {
+                        set_dev_error(a.err, DEV_ERR_PAGE);
+                    } else {
+                        r[e] = static_cast<uint32_t>(page[e]) * static_cast<uint32_t>(a.page_size) + static_cast<uint32_t>(poff[e]);
+                        const uint8_t* rec = a.cache + static_cast<long long>(r[e]) * REC;
+                        if (FP8) sc[e] = *reinterpret_cast<const float*>(rec + kFp8ScaleOff);
+                        if (e / 2 >= own0 && e / 2 <= own1) {
+#pragma unroll 1
+                            for (int q = 0; q < REC; q += 128) prefetch_l2(rec + q);
+                        }
+                    }
+                }
+                // the table's entry of tile ti
+                poff[e] = off[e];
+                if (ti < p.t1 && ti * TT + 32 * e + lane < p.len) page[e] = __ldg(table + pi[e]);
+                pi[e] += step_pages;
+                off[e] += step_off;
+                if (off[e] >= a.page_size) { off[e] -= a.page_size; ++pi[e]; }
             }
         }
     }
