@@ -41,7 +41,7 @@ namespace dc {
 constexpr int TT = 64;                        // records per tile
 constexpr int ROWS = 64;                      // query rows per block
 constexpr int MAXP = 11;                      // ring stages (8 with 64 query rows, 11 with 16)
-constexpr int MAXRAW = 6;                     // FP8: raw stages (64 records x 128 codes, 8 KB)
+constexpr int MAXRAW = 4;                     // FP8: raw stages (64 records x 128 codes, 8 KB)
 constexpr int CTRL = 6144;
 struct Shared {
     uint64_t full[MAXP], empty[MAXP], raw_full[MAXRAW], raw_empty[MAXRAW], r_full[2], r_empty[2], info_full[kInfo], tile_full[2], tile_empty[2];
@@ -78,7 +78,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
     const int rows = min(ROWS, a.n_q * a.H - rb * ROWS);
     // Q (9 chunks of RN rows), P (64 records x 64 rows, 128 bytes a record), rope ring, stage ring, control
     constexpr int QC = RN * 128, CW = kConv<FP8, RN>;
-    constexpr int raws = FP8 ? (RN == 64 ? 4 : 6) : 0;
+    constexpr int raws = FP8 ? 4 : 0;
     constexpr int stages = (RN == 16 ? 11 : (RN == 32 ? 10 : 7)) - raws / 2;
     uint8_t* sq = smem;
     uint8_t* sp = smem + 9 * QC;
@@ -319,14 +319,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 }
                 if constexpr (FP8) {
                     const float sc = sh.scale[g % kInfo][rec];
+                    constexpr int W = RN == 16 ? 16 : 32;        // columns of the rotary part at a time
 #pragma unroll
-                    for (int q = 0; q < RN / 16; ++q) {
-                        uint32_t kr[16];
-                        tmem_ld16(tm_r + 64 * (g & 1) + 16 * q + lane_base, kr);
+                    for (int q = 0; q < RN; q += W) {
+                        uint32_t kr[W];
+                        if constexpr (W == 16) tmem_ld16(tm_r + 64 * (g & 1) + q + lane_base, kr);
+                        else tmem_ld32(tm_r + 64 * (g & 1) + q + lane_base, kr);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            s[16 * q + i] = __float_as_uint(fmaf(__uint_as_float(s[16 * q + i]), sc, __uint_as_float(kr[i])));
+                        for (int i = 0; i < W; ++i)
+                            s[q + i] = __float_as_uint(fmaf(__uint_as_float(s[q + i]), sc, __uint_as_float(kr[i])));
                     }
                 }
                 tmem_ld_wait();
