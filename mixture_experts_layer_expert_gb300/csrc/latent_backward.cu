@@ -54,23 +54,24 @@ __global__ void __launch_bounds__(256) delta_kernel(LatentPrefillArgs a, float* 
     if (lane == 0 && w < n) delta[static_cast<long long>(h) * a.Tq + t] = s;
 }
 
-// dk_rope[j] = sum over the heads, in order, of the fp32 partials [H][Tk][64]; a block takes 128 keys of a sequence.
+// dk_rope[j] = sum over the heads, in order, of the fp32 partials [H][Tk][64].  A block takes 16 keys of a 128-key
+// tile (blockIdx.y), a thread 4 columns of one: enough blocks to cover the loads' latency.
 __global__ void __launch_bounds__(256) rope_sum_kernel(LatentPrefillArgs a, const float* __restrict__ part) {
     PackedSeq s;
     const int tile = find_tile(a.cu_q, a.cu_k, a.B, a.Tq, a.Tk, 128, true, blockIdx.x, nullptr, &s);
     if (tile < 0) return;
-    const int rows = min(128, s.lk - 128 * tile);
-    const int c = (threadIdx.x & 15) * 4;
-    for (int r = threadIdx.x >> 4; r < rows; r += 16) {
-        const long long row = s.k0 + 128LL * tile + r;
-        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int r = 128 * tile + 16 * blockIdx.y + (threadIdx.x >> 4), c = (threadIdx.x & 15) * 4;
+    if (r >= s.lk) return;
+    const long long row = s.k0 + r;
+    const float4* src = reinterpret_cast<const float4*>(part + row * kRope + c);
+    const long long step = static_cast<long long>(a.Tk) * kRope / 4;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-        for (int h = 0; h < a.H; ++h) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(part + (static_cast<long long>(h) * a.Tk + row) * kRope + c));
-            t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
-        }
-        *reinterpret_cast<uint2*>(a.dkr + row * a.dkr_row + c) = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+    for (int h = 0; h < a.H; ++h) {
+        const float4 v = __ldg(src + h * step);
+        t.x += v.x; t.y += v.y; t.z += v.z; t.w += v.w;
     }
+    *reinterpret_cast<uint2*>(a.dkr + row * a.dkr_row + c) = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
 }
 
 constexpr int THREADS = 320;                    // warps 0-7: elementwise and output, 8: loads, 9: MMA
@@ -266,7 +267,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
         __syncwarp();
     } else if (warp == 9) {
         constexpr uint32_t id_s = idesc_bf16_f32(128, TQ);
-        constexpr uint32_t id_v = idesc_bf16_f32_t(128, kDv, 0, 1), id_r = idesc_bf16_f32_t(128, kRope, 0, 1);
+        constexpr uint32_t id_v = idesc_bf16_f32_t(128, kDv, 0, 1), id_k = idesc_bf16_f32_t(128, kDqk, 0, 1);
         uint32_t u = 0, nkv = 0, nd = 0, nacc = 0;
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -286,76 +287,75 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
             return true;
         };
-        auto score = [&](uint32_t uu) {                   // S^T = K Q^T
-            if (elect_one()) {
-                tc_fence_after();
-                const uint32_t q = sst + (uu % STAGES) * STAGE;
-                for (int c = 0; c < 3; ++c) {
-                    const uint64_t ad = smem_desc_sw128(sk + c * UNIT), bd = smem_desc_sw128(q + c * QU);
+        // issued by one lane: S^T = K Q^T and dP^T = V dO^T of the queries in stage uu
+        const uint64_t dk = smem_desc_sw128(sk), dvd = smem_desc_sw128(sv), dst = smem_desc_sw128(sst), dmn = smem_desc_sw128_mn(sst, QU);
+        auto score = [&](uint32_t uu) {
+            const uint64_t q = dst + static_cast<uint64_t>((uu % STAGES) * (STAGE >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_bf16(tm_s + 64 * (uu & 1), ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || kk > 0);
-                }
-                tc_commit(smem_u32(&sh.s_full[uu & 1]));
-            }
-            __syncwarp();
+            for (int c = 0; c < 3; ++c)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_bf16(tm_s + 64 * (uu & 1), dk + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk),
+                                q + static_cast<uint64_t>(c * (QU >> 4) + 2 * kk), id_s, c > 0 || kk > 0);
+            tc_commit(smem_u32(&sh.s_full[uu & 1]));
         };
-        auto dprob = [&](uint32_t uu) {                   // dP^T = V dO^T
-            if (elect_one()) {
-                tc_fence_after();
-                const uint32_t o = sst + (uu % STAGES) * STAGE + 3 * QU;
-                for (int c = 0; c < 2; ++c) {
-                    const uint64_t ad = smem_desc_sw128(sv + c * UNIT), bd = smem_desc_sw128(o + c * QU);
+        auto dprob = [&](uint32_t uu) {
+            const uint64_t o = dst + static_cast<uint64_t>((uu % STAGES) * (STAGE >> 4) + 3 * (QU >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_bf16(tm_dp, ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || kk > 0);
-                }
-                tc_commit(smem_u32(&sh.dp_full));
-            }
-            __syncwarp();
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    tc_mma_bf16(tm_dp, dvd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk),
+                                o + static_cast<uint64_t>(c * (QU >> 4) + 2 * kk), id_s, c > 0 || kk > 0);
+            tc_commit(smem_u32(&sh.dp_full));
         };
         for (uint32_t k = 0;; ++k) {
             const uint32_t slot = k & 1;
             if (!wait(&sh.q.full[slot], (k >> 1) & 1)) break;
-            const Item it = sh.q.item[slot];
+            const int valid = sh.q.item[slot].valid, n = sh.q.item[slot].n, len = sh.q.item[slot].len;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.q.empty[slot]));
-            if (it.valid < 0) break;
-            if (it.valid == 0 || it.n == 0) continue;
+            if (valid < 0) break;
+            if (valid == 0 || n == 0) continue;
             if (!wait(&sh.kv_full, nkv++ & 1)) break;
-            if (!stage_in(u, it.len)) break;
-            score(u);
-            dprob(u);
-            for (int j = 0; j < it.n; ++j, ++u) {
-                const uint32_t st = sst + (u % STAGES) * STAGE;
-                if (j + 1 < it.n) {
-                    if (!stage_in(u + 1, it.len - TQ * (j + 1))) break;
-                    score(u + 1);
-                }
-                const uint32_t acc = j > 0;
-                const int steps = (min(TQ, it.len - TQ * j) + 15) >> 4;
-                if (j == 0 && !wait(&sh.acc_empty, (nacc & 1) ^ 1)) break;
+            if (!stage_in(u, len)) break;
+            if (elect_one()) {
+                tc_fence_after();
+                score(u);
+                dprob(u);
+            }
+            __syncwarp();
+            if (!wait(&sh.acc_empty, (nacc & 1) ^ 1)) break;
+            // two waits a tile, each behind queued MMAs: S(j+1) with dV(j), dK(j) with dP(j+1)
+#pragma unroll 1
+            for (int j = 0; j < n; ++j, ++u) {
+                const uint32_t acc = j > 0, so = (u % STAGES) * (STAGE >> 4);
+                const bool more = j + 1 < n;
+                const int steps = (min(TQ, len - TQ * j) + 15) >> 4;
+                if (more && !stage_in(u + 1, len - TQ * (j + 1))) break;
                 if (!wait(&sh.p_full[u & 1], (u >> 1) & 1)) break;
                 if (elect_one()) {
                     tc_fence_after();
-                    for (int kk = 0; kk < steps; ++kk)    // P^T: queries 0-31 in columns 0-15, 32-63 in 32-47
-                        tc_mma_bf16_ts(tm_dv, tm_s + 64 * (u & 1) + 32 * (kk >> 1) + 8 * (kk & 1),
-                                       smem_desc_sw128_mn(st + 3 * QU + 2048 * kk, QU), id_v, acc | (kk > 0));
+                    if (more) score(u + 1);
+                    const uint64_t o = dmn + static_cast<uint64_t>(so + 3 * (QU >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)        // P^T: queries 0-31 in columns 0-15, 32-63 in 32-47
+                        if (kk < steps)
+                            tc_mma_bf16_ts(tm_dv, tm_s + 64 * (u & 1) + 32 * (kk >> 1) + 8 * (kk & 1), o + 128ull * kk, id_v, acc | (kk > 0));
                 }
                 __syncwarp();
                 if (!wait(&sh.ds_full, nd++ & 1)) break;
                 if (elect_one()) {
                     tc_fence_after();
-                    for (int kk = 0; kk < steps; ++kk) {
-                        const uint32_t ds = tm_dp + 32 * (kk >> 1) + 8 * (kk & 1);
-                        tc_mma_bf16_ts(tm_dk, ds, smem_desc_sw128_mn(st + 2048 * kk, QU), id_v, acc | (kk > 0));
-                        tc_mma_bf16_ts(tm_dk + 128, ds, smem_desc_sw128_mn(st + 2 * QU + 2048 * kk, QU), id_r,
-                                       acc | (kk > 0));
-                    }
+                    const uint64_t q = dmn + static_cast<uint64_t>(so);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (kk < steps)                   // 192 columns: the unrotated 128 and the rotary 64
+                            tc_mma_bf16_ts(tm_dk, tm_dp + 32 * (kk >> 1) + 8 * (kk & 1), q + 128ull * kk, id_k, acc | (kk > 0));
                     tc_commit(smem_u32(&sh.empty[u % STAGES]));
+                    if (more) dprob(u + 1);
                 }
                 __syncwarp();
-                if (j + 1 < it.n) dprob(u + 1);
             }
             if (!ok) break;
             ++nacc;
@@ -497,12 +497,12 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 
 // ------------------------------------------------------------------ pass 3
 namespace dq {
-constexpr int NU = 9;                               // ring units: per key tile V (2), then K (3)
-constexpr int Q_OFF = 0, DO_OFF = 3 * UNIT, RING_OFF = 5 * UNIT, BAR_OFF = RING_OFF + NU * UNIT;
+// Q, dO resident; K twice (three units each), V once: K of a tile is held until its dQ product, V only until dP
+constexpr int Q_OFF = 0, DO_OFF = 3 * UNIT, K_OFF = 5 * UNIT, V_OFF = 11 * UNIT, BAR_OFF = 13 * UNIT;
 constexpr size_t SMEM = 1024 + BAR_OFF + 512;
 
 struct Shared {
-    uint64_t full[NU], empty[NU], q_full, q_empty, sp_full, sp_free, ds_full, dq_done, acc_empty, fin;
+    uint64_t k_full[2], k_empty[2], v_full, v_empty, q_full, q_empty, sp_full, sp_free, ds_full, dq_done, acc_empty, fin;
     uint32_t tmem;
     int abort_flag;
     Queue q;
@@ -520,7 +520,9 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
     volatile int* abort_flag = &sh.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < NU; ++i) { mbar_init(smem_u32(&sh.full[i]), 1); mbar_init(smem_u32(&sh.empty[i]), 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&sh.k_full[i]), 1); mbar_init(smem_u32(&sh.k_empty[i]), 1); }
+        mbar_init(smem_u32(&sh.v_full), 1);
+        mbar_init(smem_u32(&sh.v_empty), 1);
         mbar_init(smem_u32(&sh.q_full), 1);
         mbar_init(smem_u32(&sh.q_empty), 1);
         mbar_init(smem_u32(&sh.sp_full), 1);
@@ -548,7 +550,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             tma_prefetch_desc(&tmQ); tma_prefetch_desc(&tmKn); tma_prefetch_desc(&tmKr); tma_prefetch_desc(&tmV);
             tma_prefetch_desc(&tmDo);
         }
-        uint32_t u = 0, nq = 0, k = 0;
+        uint32_t u = 0, nq = 0, nk = 0, nv = 0, k = 0;
         int id = blockIdx.x;
         bool ok = true;
         for (; ok; ++k) {
@@ -593,18 +595,24 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                     for (int c = 0; c < 2; ++c)
                         tma_load_3d(smem_u32(smem + DO_OFF + c * UNIT), &tmDo, fb, 64 * c, it.head, it.row0);
                 }
-                for (int i = 0; ok && i < it.n; ++i) {
+                for (int i = 0; ok && i < it.n; ++i, ++u) {
                     const int row = it.other0 + 128 * i;
-                    for (int c = 0; c < 5; ++c, ++u) {
-                        const uint32_t s = u % NU, fb = smem_u32(&sh.full[s]);
-                        ok = wait_bar(smem_u32(&sh.empty[s]), ((u / NU) & 1) ^ 1, abort_flag, a.err);
-                        if (!ok) break;
-                        const uint32_t dst = smem_u32(smem + RING_OFF + s * UNIT);
-                        mbar_arrive_expect_tx(fb, UNIT);
-                        if (c < 2) tma_load_3d(dst, &tmV, fb, 64 * c, it.head, row);
-                        else if (c < 4) tma_load_3d(dst, &tmKn, fb, 64 * (c - 2), it.head, row);
-                        else tma_load_3d(dst, &tmKr, fb, 0, 0, row);
-                    }
+                    ok = wait_bar(smem_u32(&sh.k_empty[u & 1]), ((u >> 1) & 1) ^ 1, abort_flag, a.err);
+                    if (!ok) break;
+                    uint32_t fb = smem_u32(&sh.k_full[u & 1]);
+                    const uint32_t kd = smem_u32(smem + K_OFF) + (u & 1) * 3 * UNIT, vd = smem_u32(smem + V_OFF);
+                    mbar_arrive_expect_tx(fb, 3 * UNIT);
+                    tma_load_3d(kd, &tmKn, fb, 0, it.head, row);
+                    tma_load_3d(kd + UNIT, &tmKn, fb, 64, it.head, row);
+                    tma_load_3d(kd + 2 * UNIT, &tmKr, fb, 0, 0, row);
+                    ++nk;
+                    ok = wait_bar(smem_u32(&sh.v_empty), (u & 1) ^ 1, abort_flag, a.err);
+                    if (!ok) break;
+                    fb = smem_u32(&sh.v_full);
+                    mbar_arrive_expect_tx(fb, 2 * UNIT);
+                    tma_load_3d(vd, &tmV, fb, 0, it.head, row);
+                    tma_load_3d(vd + UNIT, &tmV, fb, 64, it.head, row);
+                    ++nv;
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -618,46 +626,49 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             id = __shfl_sync(0xffffffffu, id, 0);
         }
         if (lane == 0) {
-            const uint32_t pend = u < NU ? u : NU;
-            for (uint32_t j = 1; j <= pend; ++j) drain_bar(&sh.full[(u - j) % NU], ((u - j) / NU) & 1, a.err);
+            for (uint32_t e = 1; e <= 2 && e <= nk; ++e) drain_bar(&sh.k_full[(nk - e) & 1], ((nk - e) >> 1) & 1, a.err);
+            if (nv > 0) drain_bar(&sh.v_full, (nv - 1) & 1, a.err);
             if (nq > 0) drain_bar(&sh.q_full, (nq - 1) & 1, a.err);
             if (!ok) drain_bar(&sh.q.next_bar, k & 1, a.err);
         }
         __syncwarp();
     } else if (warp == 9) {
-        constexpr uint32_t id_s = idesc_bf16_f32(128, 128), id_h = idesc_bf16_f32_t(128, 64, 0, 1);
-        uint32_t u = 0, nq = 0, nfree = 0, nd = 0, nacc = 0;
+        constexpr uint32_t id_s = idesc_bf16_f32(128, 128), id_q = idesc_bf16_f32_t(128, kDqk, 0, 1);
+        uint32_t u = 0, nq = 0, nacc = 0;                     // key tiles so far
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             ok = warp_wait(smem_u32(bar), parity, abort_flag, a.err);
             return ok;
         };
-        auto unit = [&](uint32_t uu) { return smem_u32(smem + RING_OFF + (uu % NU) * UNIT); };
-        // S = Q K^T and dP = dO V^T of the key tile at units uu (V) and uu + 2 (K); keys: rows of the tile in the sequence
+        const uint64_t dqd = smem_desc_sw128(smem_u32(smem + Q_OFF)), dod = smem_desc_sw128(smem_u32(smem + DO_OFF)),
+                       dkd = smem_desc_sw128(smem_u32(smem + K_OFF)), dvd = smem_desc_sw128(smem_u32(smem + V_OFF)),
+                       dkm = smem_desc_sw128_mn(smem_u32(smem + K_OFF), UNIT);
+        // S = Q K^T and dP = dO V^T of key tile uu, which holds `keys` rows of the sequence
         auto products = [&](uint32_t uu, int keys) {
-            for (int c = 0; c < 5 && ok; ++c) wait(&sh.full[(uu + c) % NU], ((uu + c) / NU) & 1);
-            if (!ok) return false;
+            if (!wait(&sh.k_full[uu & 1], (uu >> 1) & 1)) return false;
             if (keys < 128) {       // K's rows past the last key meet ds = 0, but need not be finite
-                for (int c = 2; c < 5; ++c)
-                    if (wait_bar(smem_u32(&sh.full[(uu + c) % NU]), ((uu + c) / NU) & 1, abort_flag, a.err))
-                        zero_rows(smem + RING_OFF + ((uu + c) % NU) * UNIT, 1, UNIT, keys, (keys + 15) & ~15, lane);
+                zero_rows(smem + K_OFF + (uu & 1) * 3 * UNIT, 3, UNIT, keys, (keys + 15) & ~15, lane);
                 fence_proxy_async_smem();
                 __syncwarp();
             }
+            if (!wait(&sh.v_full, uu & 1)) return false;
             if (elect_one()) {
                 tc_fence_after();
-                for (int c = 0; c < 3; ++c) {
-                    const uint64_t ad = smem_desc_sw128(smem_u32(smem + Q_OFF + c * UNIT)), bd = smem_desc_sw128(unit(uu + 2 + c));
+                const uint64_t kd = dkd + static_cast<uint64_t>((uu & 1) * 3 * (UNIT >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(tm_s, ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || kk > 0);
-                }
-                for (int c = 0; c < 2; ++c) {
-                    const uint64_t ad = smem_desc_sw128(smem_u32(smem + DO_OFF + c * UNIT)), bd = smem_desc_sw128(unit(uu + c));
+                for (int c = 0; c < 3; ++c)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) tc_mma_bf16(tm_dp, ad + 2ull * kk, bd + 2ull * kk, id_s, c > 0 || kk > 0);
-                }
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_bf16(tm_s, dqd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk), kd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk),
+                                    id_s, c > 0 || kk > 0);
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_bf16(tm_dp, dod + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk), dvd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk),
+                                    id_s, c > 0 || kk > 0);
                 tc_commit(smem_u32(&sh.sp_full));
-                for (int c = 0; c < 2; ++c) tc_commit(smem_u32(&sh.empty[(uu + c) % NU]));
+                tc_commit(smem_u32(&sh.v_empty));
             }
             __syncwarp();
             return true;
@@ -665,28 +676,29 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         for (uint32_t k = 0;; ++k) {
             const uint32_t slot = k & 1;
             if (!wait(&sh.q.full[slot], (k >> 1) & 1)) break;
-            const Item it = sh.q.item[slot];
+            const int valid = sh.q.item[slot].valid, n = sh.q.item[slot].n, len = sh.q.item[slot].len;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sh.q.empty[slot]));
-            if (it.valid < 0) break;
-            if (it.valid == 0 || it.n == 0) continue;
+            if (valid < 0) break;
+            if (valid == 0 || n == 0) continue;
             if (!wait(&sh.q_full, nq++ & 1)) break;
             // S and dP of the item before have been read (its last ds is complete)
-            if (!products(u, min(128, it.len))) break;
-            for (int i = 0; i < it.n; ++i, u += 5) {
-                if (!wait(&sh.sp_free, nfree++ & 1)) break;
-                if (i + 1 < it.n && !products(u + 5, min(128, it.len - 128 * (i + 1)))) break;
-                if (i == 0 && !wait(&sh.acc_empty, (nacc & 1) ^ 1)) break;
-                if (!wait(&sh.ds_full, nd++ & 1)) break;
+            if (!products(u, min(128, len))) break;
+            if (!wait(&sh.acc_empty, (nacc & 1) ^ 1)) break;
+#pragma unroll 1
+            for (int i = 0; i < n; ++i, ++u) {
+                if (!wait(&sh.sp_free, u & 1)) break;
+                if (i + 1 < n && !products(u + 1, min(128, len - 128 * (i + 1)))) break;
+                if (!wait(&sh.ds_full, u & 1)) break;
                 if (elect_one()) {
                     tc_fence_after();
-                    const int steps = (min(128, it.len - 128 * i) + 15) >> 4;
-                    for (int kk = 0; kk < steps; ++kk)
-                        for (int c = 0; c < 3; ++c)
-                            tc_mma_bf16_ts(tm_dq + 64 * c, tm_ds + 8 * kk, smem_desc_sw128_mn(unit(u + 2 + c) + 2048 * kk, UNIT),
-                                           id_h, i > 0 || kk > 0);
+                    const int steps = (min(128, len - 128 * i) + 15) >> 4;
+                    const uint64_t kd = dkm + static_cast<uint64_t>((u & 1) * 3 * (UNIT >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        if (kk < steps) tc_mma_bf16_ts(tm_dq, tm_ds + 8 * kk, kd + 128ull * kk, id_q, i > 0 || kk > 0);
                     tc_commit(smem_u32(&sh.dq_done));
-                    for (int c = 2; c < 5; ++c) tc_commit(smem_u32(&sh.empty[(u + c) % NU]));
+                    tc_commit(smem_u32(&sh.k_empty[u & 1]));
                 }
                 __syncwarp();
             }
@@ -839,7 +851,7 @@ cudaError_t launch_latent_backward(const LatentPrefillArgs& a, void* ws, cudaStr
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    bw::rope_sum_kernel<<<ktiles, 256, 0, st>>>(a, part);
+    bw::rope_sum_kernel<<<dim3(ktiles, 8), 256, 0, st>>>(a, part);
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
