@@ -103,12 +103,26 @@ __device__ __forceinline__ void zero_rows(uint8_t* base, int units, int unit, in
             *reinterpret_cast<uint4*>(base + c * unit + from * 128 + z * 16) = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// A warp's 32 rows x 64 bytes go out through shared memory (2 KB, the row's four 16-byte chunks rotated against bank
+// conflicts): a store instruction then covers eight rows' whole 64-byte runs instead of 32 rows' 16 bytes.
+__device__ __forceinline__ void store_rows(uint4* buf, int lane, const uint32_t* w, uint8_t* dst, long long row_bytes, int rows) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) buf[4 * lane + (v ^ ((lane >> 1) & 3))] = make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2), v = lane & 3;
+        if (r < rows) *reinterpret_cast<uint4*>(dst + r * row_bytes + 16 * v) = buf[4 * r + (v ^ ((r >> 1) & 3))];
+    }
+    __syncwarp();
+}
+
 // ------------------------------------------------------------------ pass 2
 namespace kv {
 constexpr int TQ = 64, STAGES = 3;
 constexpr int QU = 64 * 64 * 2;                     // 64 rows x 64 columns, 8 KB
 constexpr int STAGE = 5 * QU;                       // Q (3 units), dO (2 units)
-constexpr int K_OFF = 0, V_OFF = 3 * UNIT, ST_OFF = 5 * UNIT, BAR_OFF = ST_OFF + STAGES * STAGE;
+constexpr int K_OFF = 0, V_OFF = 3 * UNIT, ST_OFF = 5 * UNIT, OUT_OFF = ST_OFF + STAGES * STAGE, BAR_OFF = OUT_OFF + 8 * 2048;
 constexpr size_t SMEM = 1024 + BAR_OFF + 2560;
 
 struct Shared {
@@ -325,18 +339,23 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 dprob(u);
             }
             __syncwarp();
+            if (n > 1) {
+                if (!stage_in(u + 1, len - TQ)) break;
+                if (elect_one()) {
+                    tc_fence_after();
+                    score(u + 1);
+                }
+                __syncwarp();
+            }
             if (!wait(&sh.acc_empty, (nacc & 1) ^ 1)) break;
-            // two waits a tile, each behind queued MMAs: S(j+1) with dV(j), dK(j) with dP(j+1)
+            // S runs two tiles ahead: its buffer was P^T of the tile whose dV has been issued
 #pragma unroll 1
             for (int j = 0; j < n; ++j, ++u) {
                 const uint32_t acc = j > 0, so = (u % STAGES) * (STAGE >> 4);
-                const bool more = j + 1 < n;
                 const int steps = (min(TQ, len - TQ * j) + 15) >> 4;
-                if (more && !stage_in(u + 1, len - TQ * (j + 1))) break;
                 if (!wait(&sh.p_full[u & 1], (u >> 1) & 1)) break;
                 if (elect_one()) {
                     tc_fence_after();
-                    if (more) score(u + 1);
                     const uint64_t o = dmn + static_cast<uint64_t>(so + 3 * (QU >> 4));
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)        // P^T: queries 0-31 in columns 0-15, 32-63 in 32-47
@@ -353,9 +372,17 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                         if (kk < steps)                   // 192 columns: the unrotated 128 and the rotary 64
                             tc_mma_bf16_ts(tm_dk, tm_dp + 32 * (kk >> 1) + 8 * (kk & 1), q + 128ull * kk, id_k, acc | (kk > 0));
                     tc_commit(smem_u32(&sh.empty[u % STAGES]));
-                    if (more) dprob(u + 1);
+                    if (j + 1 < n) dprob(u + 1);
                 }
                 __syncwarp();
+                if (j + 2 < n) {
+                    if (!stage_in(u + 2, len - TQ * (j + 2))) break;
+                    if (elect_one()) {
+                        tc_fence_after();
+                        score(u + 2);
+                    }
+                    __syncwarp();
+                }
             }
             if (!ok) break;
             ++nacc;
@@ -443,47 +470,38 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
                 tc_fence_after();
             }
             // half 0: dV, half 1: dK's unrotated part; the rotary part 32 columns each
-            const bool mine = r < it.rows;
-            const long long row = static_cast<long long>(it.row0) + r;
+            const int rows = it.rows - 32 * (warp & 3);
+            const long long row = static_cast<long long>(it.row0) + 32 * (warp & 3);         // of the warp's first
+            uint4* buf = reinterpret_cast<uint4*>(smem + OUT_OFF + 2048 * warp);
             __nv_bfloat16* dst = half == 0 ? a.dv + row * a.dv_row + it.head * a.dv_head
                                            : a.dkn + row * a.dkn_row + it.head * a.dkn_head;
+            const long long dst_row = 2 * (half == 0 ? a.dv_row : a.dkn_row);
             const float mul = half == 0 ? 1.f : a.scale;
             const uint32_t acc = (half == 0 ? tm_dv : tm_dk) + lane_base;
+            uint32_t o[32];
+            const bool any = it.n > 0;
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                uint32_t o[32];
-                if (it.n > 0) {
-                    tmem_ld32(acc + 32 * q, o);
+            for (int q = 0; q < 5; ++q) {
+                if (any) {
+                    tmem_ld32(q < 4 ? acc + 32 * q : tm_dk + 128 + 32 * half + lane_base, o);
                     tmem_ld_wait();
                 }
-                if (mine) {
+                if (q == 4) break;
+                uint32_t w[16];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = it.n > 0 ? pack_bf16x2(__uint_as_float(o[8 * v + 2 * e]) * mul,
-                                                          __uint_as_float(o[8 * v + 2 * e + 1]) * mul) : 0u;
-                        reinterpret_cast<uint4*>(dst)[4 * q + v] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
+                for (int e = 0; e < 16; ++e)
+                    w[e] = any ? pack_bf16x2(__uint_as_float(o[2 * e]) * mul, __uint_as_float(o[2 * e + 1]) * mul) : 0u;
+                store_rows(buf, lane, w, reinterpret_cast<uint8_t*>(dst + 32 * q), dst_row, rows);
             }
-            uint32_t o[32];
-            if (it.n > 0) {
-                tmem_ld32(tm_dk + 128 + 32 * half + lane_base, o);
-                tmem_ld_wait();
+            if (any) {
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh.acc_empty));
             }
-            if (mine) {
-                float4* part = reinterpret_cast<float4*>(
-                    rope_part + (static_cast<long long>(it.head) * a.Tk + row) * kRope + 32 * half);
 #pragma unroll
-                for (int v = 0; v < 8; ++v)
-                    part[v] = it.n > 0 ? make_float4(__uint_as_float(o[4 * v]) * a.scale, __uint_as_float(o[4 * v + 1]) * a.scale,
-                                                     __uint_as_float(o[4 * v + 2]) * a.scale, __uint_as_float(o[4 * v + 3]) * a.scale)
-                                       : make_float4(0.f, 0.f, 0.f, 0.f);
-            }
+            for (int e = 0; e < 32; ++e) o[e] = any ? __float_as_uint(__uint_as_float(o[e]) * a.scale) : 0u;
+            uint8_t* part = reinterpret_cast<uint8_t*>(rope_part + (static_cast<long long>(it.head) * a.Tk + row) * kRope + 32 * half);
+            store_rows(buf, lane, o, part, 4 * kRope, rows);
+            store_rows(buf, lane, o + 16, part + 64, 4 * kRope, rows);
         }
     }
     tc_fence_before();
@@ -498,7 +516,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
 // ------------------------------------------------------------------ pass 3
 namespace dq {
 // Q, dO resident; K twice (three units each), V once: K of a tile is held until its dQ product, V only until dP
-constexpr int Q_OFF = 0, DO_OFF = 3 * UNIT, K_OFF = 5 * UNIT, V_OFF = 11 * UNIT, BAR_OFF = 13 * UNIT;
+constexpr int Q_OFF = 0, DO_OFF = 3 * UNIT, K_OFF = 5 * UNIT, V_OFF = 11 * UNIT, OUT_OFF = 13 * UNIT, BAR_OFF = OUT_OFF + 8 * 2048;
 constexpr size_t SMEM = 1024 + BAR_OFF + 512;
 
 struct Shared {
@@ -651,7 +669,6 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                 fence_proxy_async_smem();
                 __syncwarp();
             }
-            if (!wait(&sh.v_full, uu & 1)) return false;
             if (elect_one()) {
                 tc_fence_after();
                 const uint64_t kd = dkd + static_cast<uint64_t>((uu & 1) * 3 * (UNIT >> 4));
@@ -661,6 +678,11 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                     for (int kk = 0; kk < 4; ++kk)
                         tc_mma_bf16(tm_s, dqd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk), kd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk),
                                     id_s, c > 0 || kk > 0);
+            }
+            __syncwarp();
+            if (!wait(&sh.v_full, uu & 1)) return false;
+            if (elect_one()) {
+                tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -779,25 +801,20 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                 if (!warp_wait(smem_u32(&sh.dq_done), (n_dq - 1) & 1, abort_flag, a.err)) break;
                 tc_fence_after();
             }
-            __nv_bfloat16* dst = a.dq + (static_cast<long long>(it.row0) + r) * a.dq_row + it.head * a.dq_head + 96 * half;
+            const bool any = it.n > 0;
+            uint4* buf = reinterpret_cast<uint4*>(smem + OUT_OFF + 2048 * warp);
+            __nv_bfloat16* dst = a.dq + (static_cast<long long>(it.row0) + 32 * (warp & 3)) * a.dq_row + it.head * a.dq_head + 96 * half;
 #pragma unroll 1
             for (int q = 0; q < 3; ++q) {
-                uint32_t o[32];
-                if (it.n > 0) {
+                uint32_t o[32], w[16];
+                if (any) {
                     tmem_ld32(tm_dq + 96 * half + 32 * q + lane_base, o);
                     tmem_ld_wait();
                 }
-                if (mine) {
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = it.n > 0 ? pack_bf16x2(__uint_as_float(o[8 * v + 2 * e]) * a.scale,
-                                                          __uint_as_float(o[8 * v + 2 * e + 1]) * a.scale) : 0u;
-                        reinterpret_cast<uint4*>(dst)[4 * q + v] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
+                for (int e = 0; e < 16; ++e)
+                    w[e] = any ? pack_bf16x2(__uint_as_float(o[2 * e]) * a.scale, __uint_as_float(o[2 * e + 1]) * a.scale) : 0u;
+                store_rows(buf, lane, w, reinterpret_cast<uint8_t*>(dst + 32 * q), 2 * a.dq_row, it.rows - 32 * (warp & 3));
             }
             if (it.n > 0) {
                 tc_fence_before();
