@@ -520,7 +520,7 @@ constexpr int Q_OFF = 0, DO_OFF = 3 * UNIT, K_OFF = 5 * UNIT, V_OFF = 11 * UNIT,
 constexpr size_t SMEM = 1024 + BAR_OFF + 512;
 
 struct Shared {
-    uint64_t k_full[2], k_empty[2], v_full, v_empty, q_full, q_empty, sp_full, sp_free, ds_full, dq_done, acc_empty, fin;
+    uint64_t k_full[2], k_empty[2], v_full, v_empty, q_full, q_empty, sp_full, sp_free, ds_full, acc_empty, fin;
     uint32_t tmem;
     int abort_flag;
     Queue q;
@@ -546,7 +546,6 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         mbar_init(smem_u32(&sh.sp_full), 1);
         mbar_init(smem_u32(&sh.sp_free), 256);
         mbar_init(smem_u32(&sh.ds_full), 256);
-        mbar_init(smem_u32(&sh.dq_done), 1);
         mbar_init(smem_u32(&sh.acc_empty), 256);
         for (int t = 0; t < 2; ++t) { mbar_init(smem_u32(&sh.q.full[t]), 1); mbar_init(smem_u32(&sh.q.empty[t]), 9); }
         mbar_init(smem_u32(&sh.q.next_bar), 1);
@@ -615,22 +614,22 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                 }
                 for (int i = 0; ok && i < it.n; ++i, ++u) {
                     const int row = it.other0 + 128 * i;
+                    const uint32_t kd = smem_u32(smem + K_OFF) + (u & 1) * 3 * UNIT, vd = smem_u32(smem + V_OFF);
+                    ok = wait_bar(smem_u32(&sh.v_empty), (u & 1) ^ 1, abort_flag, a.err);
+                    if (!ok) break;
+                    uint32_t fb = smem_u32(&sh.v_full);
+                    mbar_arrive_expect_tx(fb, 2 * UNIT);
+                    tma_load_3d(vd, &tmV, fb, 0, it.head, row);
+                    tma_load_3d(vd + UNIT, &tmV, fb, 64, it.head, row);
+                    ++nv;
                     ok = wait_bar(smem_u32(&sh.k_empty[u & 1]), ((u >> 1) & 1) ^ 1, abort_flag, a.err);
                     if (!ok) break;
-                    uint32_t fb = smem_u32(&sh.k_full[u & 1]);
-                    const uint32_t kd = smem_u32(smem + K_OFF) + (u & 1) * 3 * UNIT, vd = smem_u32(smem + V_OFF);
+                    fb = smem_u32(&sh.k_full[u & 1]);
                     mbar_arrive_expect_tx(fb, 3 * UNIT);
                     tma_load_3d(kd, &tmKn, fb, 0, it.head, row);
                     tma_load_3d(kd + UNIT, &tmKn, fb, 64, it.head, row);
                     tma_load_3d(kd + 2 * UNIT, &tmKr, fb, 0, 0, row);
                     ++nk;
-                    ok = wait_bar(smem_u32(&sh.v_empty), (u & 1) ^ 1, abort_flag, a.err);
-                    if (!ok) break;
-                    fb = smem_u32(&sh.v_full);
-                    mbar_arrive_expect_tx(fb, 2 * UNIT);
-                    tma_load_3d(vd, &tmV, fb, 0, it.head, row);
-                    tma_load_3d(vd + UNIT, &tmV, fb, 64, it.head, row);
-                    ++nv;
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -661,8 +660,21 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         const uint64_t dqd = smem_desc_sw128(smem_u32(smem + Q_OFF)), dod = smem_desc_sw128(smem_u32(smem + DO_OFF)),
                        dkd = smem_desc_sw128(smem_u32(smem + K_OFF)), dvd = smem_desc_sw128(smem_u32(smem + V_OFF)),
                        dkm = smem_desc_sw128_mn(smem_u32(smem + K_OFF), UNIT);
-        // S = Q K^T and dP = dO V^T of key tile uu, which holds `keys` rows of the sequence
+        // dP = dO V^T and S = Q K^T of key tile uu, which holds `keys` rows of the sequence; dP first: its V came long
+        // ago, while K's place has only just been left by the dQ product before
         auto products = [&](uint32_t uu, int keys) {
+            if (!wait(&sh.v_full, uu & 1)) return false;
+            if (elect_one()) {
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        tc_mma_bf16(tm_dp, dod + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk), dvd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk),
+                                    id_s, c > 0 || kk > 0);
+                tc_commit(smem_u32(&sh.v_empty));
+            }
+            __syncwarp();
             if (!wait(&sh.k_full[uu & 1], (uu >> 1) & 1)) return false;
             if (keys < 128) {       // K's rows past the last key meet ds = 0, but need not be finite
                 zero_rows(smem + K_OFF + (uu & 1) * 3 * UNIT, 3, UNIT, keys, (keys + 15) & ~15, lane);
@@ -678,19 +690,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                     for (int kk = 0; kk < 4; ++kk)
                         tc_mma_bf16(tm_s, dqd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk), kd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk),
                                     id_s, c > 0 || kk > 0);
-            }
-            __syncwarp();
-            if (!wait(&sh.v_full, uu & 1)) return false;
-            if (elect_one()) {
-                tc_fence_after();
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        tc_mma_bf16(tm_dp, dod + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk), dvd + static_cast<uint64_t>(c * (UNIT >> 4) + 2 * kk),
-                                    id_s, c > 0 || kk > 0);
                 tc_commit(smem_u32(&sh.sp_full));
-                tc_commit(smem_u32(&sh.v_empty));
             }
             __syncwarp();
             return true;
@@ -719,7 +719,6 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
 #pragma unroll
                     for (int kk = 0; kk < 8; ++kk)
                         if (kk < steps) tc_mma_bf16_ts(tm_dq, tm_ds + 8 * kk, kd + 128ull * kk, id_q, i > 0 || kk > 0);
-                    tc_commit(smem_u32(&sh.dq_done));
                     tc_commit(smem_u32(&sh.k_empty[u & 1]));
                 }
                 __syncwarp();
@@ -738,7 +737,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
         const int half = warp >> 2, r = 32 * (warp & 3) + lane;      // query row; keys [64 half, 64 half + 64)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const float c = a.scale * kLog2e;
-        uint32_t n_sp = 0, n_dq = 0;
+        uint32_t n_sp = 0;
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
             const uint32_t slot = k & 1;
@@ -788,7 +787,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                         w[16 * q + e] = pack_bf16x2(v[0], v[1]);
                     }
                 // the dQ product of the tile before has read dS
-                if (n_sp > 0 && !warp_wait(smem_u32(&sh.dq_done), (n_sp - 1) & 1, abort_flag, a.err)) { ok = false; break; }
+                if (n_sp > 0 && !warp_wait(smem_u32(&sh.k_empty[(n_sp - 1) & 1]), ((n_sp - 1) >> 1) & 1, abort_flag, a.err)) { ok = false; break; }
                 tc_fence_after();
                 tmem_st32(tm_ds + 32 * half + lane_base, w);
                 tmem_st_wait();
@@ -796,9 +795,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
                 mbar_arrive(smem_u32(&sh.ds_full));
             }
             if (!ok) break;
-            n_dq = n_sp;
             if (it.n > 0) {
-                if (!warp_wait(smem_u32(&sh.dq_done), (n_dq - 1) & 1, abort_flag, a.err)) break;
+                if (!warp_wait(smem_u32(&sh.k_empty[(n_sp - 1) & 1]), ((n_sp - 1) >> 1) & 1, abort_flag, a.err)) break;
                 tc_fence_after();
             }
             const bool any = it.n > 0;
