@@ -39,15 +39,15 @@ struct RopeTab {
     int inverse;                 // rotate by minus the angle (the gradient)
 };
 
-// cos and sin (times mscale) of pair i at position pos.
-__device__ __forceinline__ float2 rope_cs(const RopeTab& tab, int i, int pos) {
-    const uint64_t turns = static_cast<uint64_t>(static_cast<int64_t>(pos)) * tab.frac[i];
+// cos and sin (times mscale) of a pair with frequency frac at position pos.
+__device__ __forceinline__ float2 rope_cs(uint64_t frac, float mscale, int inverse, int pos) {
+    const uint64_t turns = static_cast<uint64_t>(static_cast<int64_t>(pos)) * frac;
     // signed fraction of a turn in [-1/2, 1/2), rounded once to fp32; the angle is pi * (2 * fraction)
     const float h = __ll2float_rn(static_cast<int64_t>(turns)) * 0x1p-63f;
     float s, c;
     sincospif(h, &s, &c);
-    s *= tab.mscale;
-    return make_float2(c * tab.mscale, tab.inverse ? -s : s);
+    s *= mscale;
+    return make_float2(c * mscale, inverse ? -s : s);
 }
 
 // Two E4M3 codes (low byte first) times the row's power-of-two scale, as packed

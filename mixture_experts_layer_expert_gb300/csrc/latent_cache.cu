@@ -3,39 +3,15 @@
 // on the way) and reading records back as bf16 rows.
 //
 // Memory bound: 1,152 bytes of bf16 rows on one side, a record (1,152 or 656
-// bytes) on the other.  One warp per token: each lane holds 16 consecutive
-// latent elements, so the row maximum is one warp reduction, 16 codes leave as
-// one 16-byte store, and nothing is read twice; lanes 0-7 carry the rotary key.
+// bytes) on the other.  A warp takes a token at a time: each lane holds 16
+// consecutive latent elements, so the row maximum is one warp reduction, 16 codes
+// leave as one 16-byte store, and nothing is read twice; the 32 lanes carry the 32
+// rotated pairs, one sine and cosine each.  A lane's frequency stays in a register
+// over the warp's tokens (a lane-dependent read of the parameter bank is 32 reads).
 #include "kernels.h"
 #include "latent.cuh"
 
 namespace fs {
-
-// 8 elements [8l, 8l + 8) of the rotated 64-element key of lane l (l < 8).
-__device__ __forceinline__ uint4 rotate_key8(const RopeTab& tab, const __nv_bfloat16* kr, int l, int pos) {
-    const uint4 own = *reinterpret_cast<const uint4*>(kr + 8 * l);
-    const uint32_t w[4] = {own.x, own.y, own.z, own.w};
-    uint32_t o[4];
-    if (!tab.half) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 cs = rope_cs(tab, 4 * l + i, pos);
-            const float a = bf16lo(w[i]), b = bf16hi(w[i]);
-            o[i] = pack_bf16x2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
-        }
-    } else {
-        const bool first = l < 4;                // element i pairs with i + 32
-        const uint4 oth = *reinterpret_cast<const uint4*>(kr + 8 * (first ? l + 4 : l - 4));
-        const uint32_t q[4] = {oth.x, oth.y, oth.z, oth.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 c0 = rope_cs(tab, 8 * (l & 3) + 2 * i, pos), c1 = rope_cs(tab, 8 * (l & 3) + 2 * i + 1, pos);
-            const float s0 = first ? -c0.y : c0.y, s1 = first ? -c1.y : c1.y;
-            o[i] = pack_bf16x2(bf16lo(w[i]) * c0.x + bf16lo(q[i]) * s0, bf16hi(w[i]) * c1.x + bf16hi(q[i]) * s1);
-        }
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
-}
 
 template <bool FP8>
 __global__ void __launch_bounds__(256)
@@ -44,30 +20,45 @@ cache_write_kernel(const __grid_constant__ RopeTab tab, long long T, const __nv_
                    const int32_t* __restrict__ pos, const int64_t* __restrict__ slots, uint8_t* __restrict__ cache,
                    long long n_slots, int* err) {
     const int lane = threadIdx.x & 31;
-    const long long t = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (t >= T) return;
-    const long long slot = __ldg(slots + t);
-    if (slot < 0) return;                        // a padding row: nothing is written
-    if (slot >= n_slots) {
-        if (lane == 0) set_dev_error(err, DEV_ERR_PAGE);
-        return;
-    }
-    uint8_t* rec = cache + slot * (FP8 ? kRecFp8 : kRecBf16);
-    const uint4* src = reinterpret_cast<const uint4*>(c + t * c_row) + 2 * lane;
-    const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
-    if (lane < 8) {
-        const __nv_bfloat16* k = kr + t * kr_row;
-        const uint4 w = pos ? rotate_key8(tab, k, lane, __ldg(pos + t)) : *reinterpret_cast<const uint4*>(k + 8 * lane);
-        *reinterpret_cast<uint4*>(rec + (FP8 ? kFp8RopeOff : 2 * kLatent) + 16 * lane) = w;
-    }
-    if constexpr (FP8) {
-        const RowQuant q = row_quant(warp_max(fmaxf(absmax_bf16x8(v0), absmax_bf16x8(v1))));
-        const uint2 a = quant_bf16x8(v0, q), b = quant_bf16x8(v1, q);
-        reinterpret_cast<uint4*>(rec)[lane] = make_uint4(a.x, a.y, b.x, b.y);
-        if (lane == 8) *reinterpret_cast<uint4*>(rec + kFp8ScaleOff) = make_uint4(__float_as_uint(q.scale), 0, 0, 0);
-    } else {
-        reinterpret_cast<uint4*>(rec)[2 * lane] = v0;
-        reinterpret_cast<uint4*>(rec)[2 * lane + 1] = v1;
+    const long long step = static_cast<long long>(gridDim.x) * 8;
+    const uint64_t frac = pos ? tab.frac[lane] : 0;
+    for (long long t = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < T; t += step) {
+        // the rows' loads do not wait for the slot's
+        const long long slot = __ldg(slots + t);
+        const uint4* src = reinterpret_cast<const uint4*>(c + t * c_row) + 2 * lane;
+        const uint4 v0 = __ldg(src), v1 = __ldg(src + 1);
+        const uint16_t* k = reinterpret_cast<const uint16_t*>(kr + t * kr_row);
+        const bool half = pos && tab.half;           // lane's pair: elements lane, lane + 32, else 2 lane, 2 lane + 1
+        uint32_t w = half ? __ldg(k + lane) | static_cast<uint32_t>(__ldg(k + lane + 32)) << 16
+                          : __ldg(reinterpret_cast<const uint32_t*>(k) + lane);
+        const int p = pos ? __ldg(pos + t) : 0;
+        if (slot < 0) continue;                      // a padding row: nothing is written
+        if (slot >= n_slots) {
+            if (lane == 0) set_dev_error(err, DEV_ERR_PAGE);
+            continue;
+        }
+        uint8_t* rec = cache + slot * (FP8 ? kRecFp8 : kRecBf16);
+        if (pos) {
+            const float2 cs = rope_cs(frac, tab.mscale, tab.inverse, p);
+            const float a = bf16lo(w), b = bf16hi(w);
+            w = pack_bf16x2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
+        }
+        uint8_t* rope = rec + (FP8 ? kFp8RopeOff : 2 * kLatent);
+        if (half) {
+            reinterpret_cast<uint16_t*>(rope)[lane] = static_cast<uint16_t>(w);
+            reinterpret_cast<uint16_t*>(rope)[lane + 32] = static_cast<uint16_t>(w >> 16);
+        } else {
+            reinterpret_cast<uint32_t*>(rope)[lane] = w;
+        }
+        if constexpr (FP8) {
+            const RowQuant q = row_quant(warp_max(fmaxf(absmax_bf16x8(v0), absmax_bf16x8(v1))));
+            const uint2 a = quant_bf16x8(v0, q), b = quant_bf16x8(v1, q);
+            reinterpret_cast<uint4*>(rec)[lane] = make_uint4(a.x, a.y, b.x, b.y);
+            if (lane == 8) *reinterpret_cast<uint4*>(rec + kFp8ScaleOff) = make_uint4(__float_as_uint(q.scale), 0, 0, 0);
+        } else {
+            reinterpret_cast<uint4*>(rec)[2 * lane] = v0;
+            reinterpret_cast<uint4*>(rec)[2 * lane + 1] = v1;
+        }
     }
 }
 
@@ -106,13 +97,15 @@ cache_read_kernel(long long T, const int64_t* __restrict__ slots, const uint8_t*
             *reinterpret_cast<const uint4*>(rec + (FP8 ? kFp8RopeOff : 2 * kLatent) + 16 * lane);
 }
 
+constexpr long long kWriteBlocks = 152 * 6;       // as many as are resident at once
+
 cudaError_t launch_cache_write(const RopeTab* tab, bool fp8, long long T, const void* c, long long c_row,
                                const void* kr, long long kr_row, const int32_t* pos, const int64_t* slots, void* cache,
                                long long n_slots, cudaStream_t st) {
     static const RopeTab none{};
     const RopeTab& rt = tab ? *tab : none;
     const int32_t* p = tab ? pos : nullptr;
-    const unsigned blocks = static_cast<unsigned>((T + 7) / 8);
+    const unsigned blocks = static_cast<unsigned>(min((T + 7) / 8, kWriteBlocks));
     auto* cc = static_cast<const __nv_bfloat16*>(c);
     auto* kk = static_cast<const __nv_bfloat16*>(kr);
     auto* out = static_cast<uint8_t*>(cache);

@@ -59,7 +59,7 @@ rope_kernel(const __grid_constant__ RopeTab tab, long long n, int groups, int hc
     constexpr int NF = HALF ? N : N / 2;         // pairs per thread
     float2 cs[NF];
 #pragma unroll
-    for (int i = 0; i < NF; ++i) cs[i] = rope_cs(tab, g * NF + i, p);
+    for (int i = 0; i < NF; ++i) cs[i] = rope_cs(tab.frac[g * NF + i], tab.mscale, tab.inverse, p);
     const T* xt = x + t * x_row + g * N;
     T* yt = y + t * y_row + g * N;
     const int half = tab.d_rot / 2;
