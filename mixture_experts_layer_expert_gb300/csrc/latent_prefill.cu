@@ -66,10 +66,30 @@ __device__ __forceinline__ int row_limit(const Item& it, bool causal, int r) {
     return causal ? min(it.lk, it.off + r + 1) : it.lk;
 }
 
-// Softmax of one query tile: the calling thread owns row r of the item (TMEM lane r & 127).
-struct RowState {
-    float m, l;           // running maximum (log2 units, scaled), sum of 2^(s - m)
-};
+// A warp's 32 rows x 64 bytes, a row a lane: four lanes exchange their 16-byte chunks, so that a store instruction covers
+// eight rows' whole 64-byte runs instead of 32 rows' 16 bytes.
+__device__ __forceinline__ void store_rows(int lane, const uint32_t* w, uint8_t* dst, long long row_bytes, int rows) {
+    const int q = lane & 3;
+    uint32_t got[4][4];                          // [s]: chunk q of the row of lane ^ s
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = (q ^ s) & 1 ? w[4 + e] : w[e], hi = (q ^ s) & 1 ? w[12 + e] : w[8 + e];
+            got[s][e] = __shfl_xor_sync(0xffffffffu, (q ^ s) & 2 ? hi : lo, s);
+        }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int r = (lane & ~3) + j;           // this row came in round j ^ q
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = (j ^ q) & 1 ? got[1][e] : got[0][e], hi = (j ^ q) & 1 ? got[3][e] : got[2][e];
+            v[e] = (j ^ q) & 2 ? hi : lo;
+        }
+        if (r < rows) *reinterpret_cast<uint4*>(dst + r * row_bytes + 16 * q) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+}
 
 __global__ void __launch_bounds__(THREADS, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmKn,
@@ -255,6 +275,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (n0 > 0) score(0, u);
             if (n1 > 0) score(1, u);
             commit(&sh.k_empty[j & 1]);
+            // Q is free, and the next item's on its way, once the last scores are there
+            if (n == 1) commit(&sh.q_empty);
 #pragma unroll 1
             for (int i = 0; i < n; ++i, ++j, u = (u + 5) & 7) {
                 const uint32_t un = (u + 5) & 7;              // K of tile i + 1
@@ -307,9 +329,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                 }
                 if (!ok) break;
                 if (i + 1 < n) commit(&sh.k_empty[(j + 1) & 1]);
+                if (i + 2 == n) commit(&sh.q_empty);
             }
             if (!ok) break;
-            commit(&sh.q_empty);
         }
         if (elect_one()) {
             tc_commit(smem_u32(&sh.fin));          // every MMA completes before TMEM is released
@@ -414,7 +436,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             }
             const float inv = l != 0.f ? 1.f / l : 0.f;
             const bool mine = r < it.rows;
-            __nv_bfloat16* dst = a.out_w + (static_cast<long long>(it.row0) + r) * a.o_row +
+            __nv_bfloat16* dst = a.out_w + (static_cast<long long>(it.row0) + r - lane) * a.o_row +
                                  static_cast<long long>(it.head) * a.o_head;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
@@ -423,17 +445,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
                     tmem_ld32(to + 32 * q, o);
                     tmem_ld_wait();
                 }
-                if (mine) {
+                uint32_t w[16];
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            w[j] = l != 0.f ? pack_bf16x2(__uint_as_float(o[8 * v + 2 * j]) * inv,
-                                                         __uint_as_float(o[8 * v + 2 * j + 1]) * inv) : 0u;
-                        reinterpret_cast<uint4*>(dst)[4 * q + v] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
+                for (int j = 0; j < 16; ++j)
+                    w[j] = l != 0.f ? pack_bf16x2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv) : 0u;
+                store_rows(lane, w, reinterpret_cast<uint8_t*>(dst + 32 * q), 2 * a.o_row, it.rows - (r - lane));
             }
             if (mine)
                 a.lse_w[static_cast<long long>(it.head) * a.Tq + it.row0 + r] =
