@@ -3,8 +3,8 @@
 //   s_i = scale (q_l . c_i + q_r . k_i),  out = sum_i softmax(s)_i c_i,  lse = log sum_i exp(s_i)
 //
 // All heads (and the n_q new tokens) of a sequence read the same records, so a
-// block takes up to 64 query rows (row = new token * heads + head) against tiles
-// of 64 records, staged once in shared memory as bf16 and used twice as the A
+// block takes up to 64 query rows (row = new token * heads + head; more rows go to
+// CTA pairs, latent_decode_pair.cu) against tiles of 64 records, staged once in shared memory as bf16 and used twice as the A
 // operand of transposed products:
 //   S^T = K Q^T      64 records x rows x 576, the tile read K-major
 //   O^T += C^T P     512 (4 x 128) x rows x 64 records, the same tile read MN-major
@@ -22,16 +22,16 @@
 // rows, 36 x 60 + 16 x 75 = 3,360 for 64.
 //
 // The records of all sequences form one list of tiles which is cut into equal
-// ranges, one per block (and per block of 64 rows), whatever the lengths.  A
+// ranges, one per block, whatever the lengths.  A
 // sequence inside one range is finished there; one that is cut leaves fp32
 // partials (normalised O and lse) which a second kernel joins in range order.
 //
-// Warps 0-3: softmax, rescaling, output; warp 4: MMA issue; warps 5-6: Q of the
-// next sequence; then the loaders.  bf16: one warp, page lookup a tile ahead and
-// TMA (a whole tile of consecutive records as two boxes per stage, else gathers of
-// four records).  FP8: codes go through registers a tile ahead and become bf16
-// unscaled; a record's scale multiplies its latent scores (the rotary part has TMEM
-// columns of its own) and its p.  Ring stages of 64 records x 128 latent columns (16 KB).
+// Warps 0-3: softmax, rescaling, output; warp 4: Q of each sequence and the MMAs of the
+// scores; warp 5: the MMAs of P C; warp 6: page lookup, three tiles ahead; warp 7: TMA (a
+// tile of consecutive records as two boxes per stage, else gathers of four records) into
+// ring stages of 64 records x 128 latent columns (16 KB).  FP8: raw codes come into a ring of
+// their own, warps 8 .. turn them into bf16 stages unscaled; a record's scale multiplies its
+// latent scores (the rotary part has TMEM columns of its own) and its p.
 #include "kernels.h"
 #include "latent_decode.cuh"
 
@@ -65,8 +65,8 @@ template <bool FP8, int RN> constexpr int kThreads = 32 * (8 + kConv<FP8, RN>);
 template <bool FP8, int RN>
 __global__ void __launch_bounds__(kThreads<FP8, RN>, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant__ CUtensorMap tmRow,
-              const LatentDecodeArgs a, const int rb_count, const int ranges, float* __restrict__ part,
-              float* __restrict__ part_lse, Meta* __restrict__ meta) {
+              const LatentDecodeArgs a, const int ranges, float* __restrict__ part, float* __restrict__ part_lse,
+              Meta* __restrict__ meta) {
     // all of the SM's shared memory and no static part: the block's memory starts on a 1 KB boundary
     extern __shared__ __align__(1024) uint8_t smem[];
     if (smem_u32(smem) & 1023u) {
@@ -74,8 +74,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rb = blockIdx.x % rb_count, range = blockIdx.x / rb_count;
-    const int rows = min(ROWS, a.n_q * a.H - rb * ROWS);
+    const int range = blockIdx.x, rows = a.n_q * a.H;
     // Q (9 chunks of RN rows), P (64 records x 64 rows, 128 bytes a record), rope ring, stage ring, control
     constexpr int QC = RN * 128, CW = kConv<FP8, RN>;
     constexpr int raws = FP8 ? 4 : 0;
@@ -112,8 +111,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         tmem_alloc(smem_u32(&sh.tmem), 512);
         tmem_relinquish();
     }
-    if (threadIdx.x < ROWS) sh.lag[threadIdx.x] = a.n_q - 1 - min((rb * ROWS + static_cast<int>(threadIdx.x)) / a.H, a.n_q - 1);
-    if (warp == 0) find_range(a, range, ranges, TT, rb == 0, meta, &sh.b0, &sh.tile0, &sh.left);
+    if (threadIdx.x < ROWS) sh.lag[threadIdx.x] = a.n_q - 1 - min(static_cast<int>(threadIdx.x) / a.H, a.n_q - 1);
+    if (warp == 0) find_range(a, range, ranges, TT, true, meta, &sh.b0, &sh.tile0, &sh.left);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -210,7 +209,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         };
         while (ok && next_piece(a, b, tile, left, &p, TT)) {
             if (!wait(&sh.q_empty, (np & 1) ^ 1)) break;      // the scores of the piece before are complete
-            load_q<RN>(a, p.b, rb * ROWS, rows, smem_u32(sq), lane);
+            load_q<RN>(a, p.b, 0, rows, smem_u32(sq), lane);
             __syncwarp();
             ++np;
             for (int n = p.t1 - p.t0; n > 0; --n, ++g) {
@@ -297,7 +296,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         for (int e = range; e < a.B; e += ranges) {
             if (seq_len(a, e) != 0) continue;
             for (int i = threadIdx.x; i < rows * 64; i += 128) {
-                const int q = rb * ROWS + (i >> 6), jj = q / a.H, hh = q - jj * a.H;
+                const int q = i >> 6, jj = q / a.H, hh = q - jj * a.H;
                 const long long row = static_cast<long long>(e) * a.n_q + jj;
                 reinterpret_cast<uint4*>(a.out + row * a.o_row + hh * a.o_head)[i & 63] = make_uint4(0, 0, 0, 0);
                 if (a.lse && (i & 63) == 0) a.lse[row * a.H + hh] = -CUDART_INF_F;
@@ -440,14 +439,14 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
             }
             bar_sync(1, 128);
             const bool whole = p.t0 == 0 && p.t1 == p.n;
-            const long long slot = (static_cast<long long>(range) * rb_count + rb) * 2 + (p.b == sh.b0 ? 0 : 1);
+            const long long slot = static_cast<long long>(range) * 2 + (p.b == sh.b0 ? 0 : 1);
             if (threadIdx.x < RN) {
                 const int i = threadIdx.x;
                 const float z = (sh.red[0][i] + sh.red[1][i]) + (sh.red[2][i] + sh.red[3][i]);
                 sh.f[i] = z != 0.f ? 1.f / z : 0.f;
                 if (i < rows) {
                     const float lse = z != 0.f ? sh.m[i] + log2f(z) : -CUDART_INF_F;       // log2 units
-                    const int q = rb * ROWS + i, j = q / a.H, h = q - j * a.H;
+                    const int j = i / a.H, h = i - j * a.H;
                     if (!whole) part_lse[slot * ROWS + i] = lse;
                     else if (a.lse) a.lse[(static_cast<long long>(p.b) * a.n_q + j) * a.H + h] = lse * kLn2;
                 }
@@ -462,7 +461,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 tmem_ld16(tm_o + cc + lane_base, o);
                 tmem_ld_wait();
                 const int d = (cc / RN) * 128 + 32 * warp + lane, r0 = cc % RN;
-                int qq = rb * ROWS + r0, jj = qq / a.H, hh = qq - jj * a.H;
+                int qq = r0, jj = qq / a.H, hh = qq - jj * a.H;
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     if (r0 + e < rows) {
@@ -567,7 +566,6 @@ join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, cons
     if (a.lse && threadIdx.x == 0) a.lse[row * a.H + h] = z != 0.f ? (z_ref[1] + log2f(z)) * kLn2 : -CUDART_INF_F;
 }
 
-
 // Up to 64 query rows: one block per range; more: CTA pairs, 128 rows each, as many ranges as there are pairs left.
 struct Shape { int rb, ranges, block_rows; };
 Shape shape(int H, int n_q) {
@@ -587,7 +585,7 @@ size_t latent_decode_ws_bytes(int H, int, int n_q) {
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, cudaStream_t st) {
     static bool attr[2][3][kMaxDevices] = {{{false}}};
-    using Fn = void (*)(CUtensorMap, CUtensorMap, LatentDecodeArgs, int, int, float*, float*, dc::Meta*);
+    using Fn = void (*)(CUtensorMap, CUtensorMap, LatentDecodeArgs, int, float*, float*, dc::Meta*);
     static const Fn fns[2][3] = {{dc::decode_kernel<false, 16>, dc::decode_kernel<false, 32>, dc::decode_kernel<false, 64>},
                                  {dc::decode_kernel<true, 16>, dc::decode_kernel<true, 32>, dc::decode_kernel<true, 64>}};
     const dc::Shape sp = dc::shape(a.H, a.n_q);
@@ -610,7 +608,7 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, 
         e = smem_attr_once(reinterpret_cast<const void*>(fn), dc::SMEM, attr[fp8][v]);
         if (e != cudaSuccess) return e;
         fn<<<static_cast<unsigned>(sp.ranges), 32 * (8 + (!fp8 ? 0 : (v == 2 ? 4 : 8))), dc::SMEM, st>>>(
-            tile, row, a, 1, sp.ranges, part, part_lse, meta);
+            tile, row, a, sp.ranges, part, part_lse, meta);
         count_launch();
         e = cudaGetLastError();
     }

@@ -459,6 +459,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
 #pragma unroll 1
             for (int cc = 0; cc < 256; cc += 32) {
                 uint32_t o[32];
+                __syncwarp();
                 tmem_ld32(tm_o + cc + lane_base, o);
                 tmem_ld_wait();
                 if (!mine) continue;

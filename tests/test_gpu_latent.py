@@ -302,6 +302,75 @@ def test_decode_many_sequences(cache):
     p.check()
 
 
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+def test_decode_thousands_of_sequences_of_one_token_or_none(cache):
+    p = Decode(3, [i % 2 for i in range(5000)], 1, 2, cache)
+    p.run()
+    _no_dev_error()
+    p.check()
+
+
+@pytest.mark.parametrize("H", [2, 128])
+def test_decode_long_sequence(H):
+    """One sequence over all SMs; the short one behind it shares the last range."""
+    p = Decode(H, [70001, 9], 1, 64, "bf16")
+    p.run()
+    _no_dev_error()
+    p.check()
+
+
+@pytest.mark.parametrize("H,cache", [(16, "fp8"), (80, "bf16")])
+def test_decode_shared_and_repeated_pages(H, cache):
+    """Sequences that share a prefix's pages, and one whose table names a page twice; lse not asked for."""
+    p = Decode(H, [640, 300, 200], 1, 64, cache)
+    p.table[1, :2] = p.table[0, :2]
+    p.table[2, 1] = p.table[2, 0]
+    cut = lambda t, u: tuple(torch.cat([x[:128], y[128:]]) for x, y in zip(t, u))
+    p.rows[1] = cut(p.rows[0], p.rows[1])
+    p.rows[2] = tuple(torch.cat([x[:64], x[:64], x[128:]]) for x in p.rows[2])
+    p.run()
+    _no_dev_error()
+    p.check()
+    first = p.out.clone()
+    p.out.fill_(SENTINEL)
+    fs.fs_latent_decode(p.desc, p.ql, p.qr, p.cache, p.table, p.seq, SCALE, p.out[..., :512], None, p.ws)
+    _no_dev_error()
+    assert torch.equal(p.out, first)
+
+
+def test_decode_heads_outside_rows():
+    """Queries and outputs laid out head by head."""
+    p = Decode(48, [129, 700], 2, 64, "bf16")
+    p.run()
+    hm = lambda t, w: t[..., :w].transpose(0, 1).contiguous().transpose(0, 1)
+    out = hm(torch.full_like(p.out, SENTINEL), 512)
+    lse = torch.empty_like(p.lse)
+    fs.fs_latent_decode(p.desc, hm(p.ql, 512), hm(p.qr, 64), p.cache, p.table, p.seq, SCALE, out, lse, p.ws)
+    _no_dev_error()
+    assert torch.equal(out, p.out[..., :512]) and torch.equal(lse, p.lse)
+
+
+def test_calls_on_two_streams_at_once():
+    """Decode and prefill, forward and backward, in turn on two streams with a workspace each."""
+    jobs = [(Decode(128, [900, 2000, 5], 1, 64, "bf16", seed=s), Prefill(4, [300, 129], [300, 200], True)) for s in (0, 1)]
+
+    def run(d, f):
+        d.run()
+        f.forward()
+        f.backward()
+        return [t.clone() for t in (d.out, d.lse, f.out, f.lse, f.dq, f.dkr, f.dkv)]
+    want = [run(*j) for j in jobs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in jobs], [None, None]
+    for _ in range(3):
+        for i, (s, j) in enumerate(zip(streams, jobs)):
+            with torch.cuda.stream(s):
+                got[i] = run(*j)
+    _no_dev_error()
+    for w, t in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, t))
+
+
 def test_decode_large_scores():
     """Scores of several hundred: the running maximum, not the exponent's range, carries them."""
     p = Decode(16, [700, 64], 1, 64, "bf16", q_std=20.0)
@@ -534,6 +603,30 @@ def test_prefill_repeats_and_replays_bit_identically():
         graph.replay()
         _no_dev_error()
         assert all(torch.equal(a, b) for a, b in zip(keep, (p.out, p.lse, p.dq, p.dkr, p.dkv)))
+
+
+def test_prefill_many_sequences_and_heads_outside_rows():
+    """Hundreds of short sequences, empty ones among them, with operands laid out head by head."""
+    g = torch.Generator().manual_seed(5)
+    lq = [int(x) for x in torch.randint(0, 9, (300,), generator=g)]
+    lk = [int(n + x) if n else int(x) for n, x in zip(lq, torch.randint(0, 9, (300,), generator=g))]
+    p = Prefill(3, lq, lk, True)
+    p.forward()
+    p.backward()
+    _no_dev_error()
+    p.check_forward()
+    p.check_backward()
+    hm = lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)
+    q, kn, v, do, out = hm(p.q), hm(p.kn), hm(p.v), hm(p.do), hm(torch.full_like(p.out, SENTINEL))
+    lse = torch.full_like(p.lse, SENTINEL)
+    fs.fs_latent_prefill(q, kn, p.kr, v, p.cu_q, p.cu_k, True, SCALE, out, lse)
+    assert torch.equal(out, p.out) and torch.equal(lse, p.lse)
+    dq, dkn, dv = (hm(torch.full_like(t, SENTINEL)) for t in (q, kn, v))
+    dkr = torch.full_like(p.dkr, SENTINEL)
+    fs.fs_latent_prefill_backward(q, kn, p.kr, v, p.cu_q, p.cu_k, True, SCALE, out, lse, do, dq, dkn, dkr, dv, p.ws)
+    _no_dev_error()
+    assert torch.equal(dq, p.dq) and torch.equal(dkr, p.dkr)
+    assert torch.equal(dkn, p.dkv[..., :128]) and torch.equal(dv, p.dkv[..., 128:])
 
 
 def test_prefill_bad_offsets():
