@@ -591,10 +591,11 @@ fs_status fs_latent_cache_read(const fs_latent_cache* desc, const void* cache, i
  * sequence b is offset i % page_size of page block_table[b table_row + i /
  * page_size]; the table's entries past the sequence are not read.  A row that
  * sees no position gives out = 0, lse = -inf.  A length outside [0, max_pages
- * page_size] (that sequence counts as empty) or a page outside [0, n_pages)
- * (its positions are left out) sets the device error word (code 5).
- * n_q 1 .. 16, scale > 0, n_pages page_size < 2^31.  The length is split over the SMs and joined in a fixed order:
- * results do not depend on timing.  ws: fs_latent_decode_ws_bytes bytes,
+ * page_size] or above 2^31 - 257 (that sequence counts as empty) or a page
+ * outside [0, n_pages) (its positions are left out) sets the device error word
+ * (code 5).  n_q 1 .. 16, scale > 0, n_pages page_size < 2^31.  The length is
+ * split over the SMs and joined in a fixed order: results do not depend on
+ * timing.  ws: fs_latent_decode_ws_bytes bytes,
  * 256-byte aligned. */
 size_t fs_latent_decode_ws_bytes(int32_t heads, int32_t B, int32_t n_q);
 fs_status fs_latent_decode(const fs_latent_cache* desc, int32_t heads, int32_t B, int32_t n_q,

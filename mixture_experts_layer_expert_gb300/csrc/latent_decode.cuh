@@ -25,9 +25,13 @@ struct Piece {
     int b, t0, t1, n, len;                    // tiles [t0, t1) of the n of sequence b
 };
 
+// Whether a sequence's length is one that its table can hold (and whose last tile's positions fit an int).
+__device__ __forceinline__ bool good_len(const LatentDecodeArgs& a, int n) {
+    return n >= 0 && n <= 0x7fffffff - 256 && n <= static_cast<long long>(a.max_pages) * a.page_size;
+}
 __device__ __forceinline__ int seq_len(const LatentDecodeArgs& a, int b) {
     const int n = __ldg(a.seq_lens + b);
-    return n < 0 || n > static_cast<long long>(a.max_pages) * a.page_size ? 0 : n;
+    return good_len(a, n) ? n : 0;
 }
 // Next piece of the range (tiles of tt records); b, tile, left advance.  False at the end.
 __device__ __forceinline__ bool next_piece(const LatentDecodeArgs& a, int& b, int& tile, int& left, Piece* p, int tt) {
@@ -54,13 +58,15 @@ struct TileRecs {
     int start[TT / 64];         // first record of a half that is one box: 64 consecutive records, or none at all (start
     int box[TT / 64];           //   past the cache's end: zeros); else four records at a time are gathered
 };
-constexpr int kInfo = 6;        // depth of what the lookup leaves for the softmax (see lookup_tiles)
+constexpr int kInfo = 8;        // depth of what the lookup leaves for the softmax (see lookup_tiles)
 
 // The lookup warp: for every tile of the block's range, its records (two tiles ahead of the loads at most),
 // which of them count and (FP8) their scales, and its halves own0 .. own1 asked into L2.  Three tiles are under
 // way: the table's entries of one, the scales of the tile before, the publication of the tile before that, so no
-// load is waited for in the iteration that issues it.  It is at most two tiles ahead of the loads, which a full
-// ring holds less than four tiles ahead of the softmax: slots of kInfo tiles are free when they come round.
+// load is waited for in the iteration that issues it.  Tile g is published once the loads of tile g - 3 are all
+// issued; the last of them needed its place in the ring, which holds 11 stages at most (with FP8 that of the raw
+// stage four before it, converted into a ring of 9 at most), and that place was left by the product P C of tile
+// g - 5 (g - 6) or a later one: the softmax is past that tile, so kInfo slots are enough.
 template <bool FP8, int TT>
 __device__ __forceinline__ void lookup_tiles(const LatentDecodeArgs& a, int b, int tile, int left, int own0, int own1,
                                              TileRecs<TT>* recs, uint64_t* tile_full, uint64_t* tile_empty,
@@ -247,7 +253,7 @@ __device__ __forceinline__ void find_range(const LatentDecodeArgs& a, int range,
     long long total = 0;
     for (int b = lane; b < a.B; b += 32) {
         const int n = __ldg(a.seq_lens + b);
-        if (n < 0 || n > static_cast<long long>(a.max_pages) * a.page_size) set_dev_error(a.err, DEV_ERR_PAGE);
+        if (!good_len(a, n)) set_dev_error(a.err, DEV_ERR_PAGE);
         total += tiles(b);
     }
 #pragma unroll
@@ -280,7 +286,6 @@ __device__ __forceinline__ void find_range(const LatentDecodeArgs& a, int range,
         if (write) meta[range] = Meta{found_b, found_t, static_cast<int>(g1 - g0), 0};
     }
 }
-
 
 }  // namespace dc
 }  // namespace fs

@@ -29,7 +29,7 @@ using namespace dc;
 constexpr int TT = 128;                       // records per tile
 constexpr int ROWS = 64;                      // query rows per CTA
 constexpr int MAXP = 7, MAXRAW = 4;
-constexpr int CTRL = 6144;
+constexpr int CTRL = 7168;
 template <bool FP8> constexpr int kThreads = FP8 ? 512 : 256;
 
 struct Shared {
