@@ -19,7 +19,11 @@
 // Bound: the records' bytes while the MMAs of a block of rows fit under them: 64
 // records are 73.7 KB (bf16) or 42 KB (FP8), 3,150 or 1,790 cycles of one SM's
 // share of the memory bandwidth; the MMAs take 36 x 36 + 16 x 52 = 2,130 cycles for 16
-// rows, 36 x 60 + 16 x 75 = 3,360 for 64.
+// rows, 36 x 60 + 16 x 75 = 3,360 for 64.  Measured: 256 sequences of up to 8,191 tokens
+// x 16 heads on an FP8 cache 223 us (3.1 TB/s; 3,400 cycles a tile, the chain of
+// conversion, scores, softmax and P C over the 2.25 tiles that the ring holds: faster
+// conversion, an earlier release of the raw stages or one wait for all four stages did
+// not shorten it); one sequence of 4,097 tokens x 16 heads, join included, 26.6 us.
 //
 // The records of all sequences form one list of tiles which is cut into equal
 // ranges, one per block, whatever the lengths.  A
@@ -490,23 +494,27 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
 
 constexpr int kRanges = 152;                  // one block per SM
 
-// Joins the partials of the sequences that range boundaries cut.  Block (boundary, row, row block): the boundary
-// before range s; the first boundary inside a sequence joins all its pieces, in range order.
-__global__ void __launch_bounds__(128)
+// Joins the partials of the sequences that range boundaries cut.  Block (boundary, RB rows, row block): the
+// boundary before range s; the first boundary inside a sequence joins all its pieces, in range order, a row on
+// 8 / RB warps.  RB = 8 for batches (a block per row spent its time on the search for the pieces, 2 us of dependent
+// loads in four waves of blocks: 64 sequences x 128 rows 15.9 us, now 9.7); RB = 1 where a sequence has more than 8
+// pieces on average (one sequence of 65 pieces x 16 rows: 16 us more with a warp per row).
+constexpr int kJoinWarps = 8;
+template <int RB>
+__global__ void __launch_bounds__(32 * kJoinWarps)
 join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, const int block_rows, const float* __restrict__ part,
             const float* __restrict__ part_lse, const Meta* __restrict__ meta) {
+    constexpr int W = kJoinWarps / RB;
+    __shared__ float sums[W > 1 ? W : 1][W > 1 ? kLatent : 1];
     __shared__ int slots[kRanges];
-    __shared__ float weight[kRanges];
+    __shared__ float weight[kJoinWarps][kRanges];
     __shared__ int count;
-    __shared__ float z_ref[2];
-    const int s = blockIdx.x + 1, r = blockIdx.y, rb = blockIdx.z;
-    const int q = rb * block_rows + r;
-    if (q >= a.n_q * a.H) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int s = blockIdx.x + 1, r = blockIdx.y * RB + warp / W, rb = blockIdx.z, q = rb * block_rows + r;
     const Meta m = meta[s];
     if (m.b >= a.B || m.tiles == 0 || m.off == 0) return;     // no tiles, or the sequence starts here
-    if (threadIdx.x < 32) {
+    if (warp == 0) {
         // the range before (empty ones, where there are fewer tiles than ranges, aside) holds the piece before
-        const int lane = threadIdx.x;
         int first = s - 1;
         for (;; first -= 32) {
             const int k = first - lane;
@@ -515,7 +523,6 @@ join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, cons
             if (first < 32) break;                            // (cannot be: m.off > 0)
         }
         int n = 0;
-        float top = -CUDART_INF_F;
         const Meta mf = meta[first < 0 ? 0 : first];
         if (first >= 0 && !(mf.b == m.b && mf.off > 0)) {     // else an earlier boundary is inside the sequence too
             for (int k0 = first; k0 < ranges; k0 += 32) {
@@ -524,46 +531,67 @@ join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, cons
                 if (k < ranges) mk = meta[k];
                 const bool in = mk.tiles > 0 && (mk.b == m.b || k == first);
                 const unsigned mask = __ballot_sync(0xffffffffu, in);
-                if (in) {
-                    const int at = n + __popc(mask & ((1u << lane) - 1u));
-                    slots[at] = (k * rb_count + rb) * 2 + (mk.b == m.b ? 0 : 1);
-                    weight[at] = part_lse[static_cast<long long>(slots[at]) * block_rows + r];
-                    top = fmaxf(top, weight[at]);
-                }
+                if (in) slots[n + __popc(mask & ((1u << lane) - 1u))] = (k * rb_count + rb) * 2 + (mk.b == m.b ? 0 : 1);
                 n += __popc(mask);
+                if (__any_sync(0xffffffffu, mk.tiles > 0 && mk.b > m.b)) break;      // a later sequence's range
             }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            __syncwarp();
-            const float ref = top == -CUDART_INF_F ? 0.f : top;
-            float z = 0.f;
-            for (int k = lane; k < n; k += 32) {
-                weight[k] = exp2_fast(weight[k] - ref);
-                z += weight[k];
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
-            if (lane == 0) { z_ref[0] = z; z_ref[1] = ref; }
         }
         if (lane == 0) count = n;
     }
     __syncthreads();
     const int n = count;
-    if (n == 0) return;
-    const float z = z_ref[0];
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-        const float w = weight[k];
-        const float4 v = __ldg(reinterpret_cast<const float4*>(part + (static_cast<long long>(slots[k]) * block_rows + r) * kLatent) + threadIdx.x);
-        acc.x += w * v.x; acc.y += w * v.y; acc.z += w * v.z; acc.w += w * v.w;
+    if (n == 0 || r >= block_rows || q >= a.n_q * a.H) return;      // (with RB = 1 the whole block)
+    float* wt = weight[warp];
+    float top = -CUDART_INF_F;
+    for (int k = lane; k < n; k += 32) {
+        wt[k] = __ldg(part_lse + static_cast<long long>(slots[k]) * block_rows + r);
+        top = fmaxf(top, wt[k]);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float ref = top == -CUDART_INF_F ? 0.f : top;
+    float z = 0.f;
+    for (int k = lane; k < n; k += 32) {
+        wt[k] = exp2_fast(wt[k] - ref);
+        z += wt[k];
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+    __syncwarp();
+    float4 acc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = warp % W; k < n; k += W) {
+        const float w = wt[k];
+        const float4* src = reinterpret_cast<const float4*>(part + (static_cast<long long>(slots[k]) * block_rows + r) * kLatent) + lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = __ldg(src + 32 * i);
+            acc[i].x += w * v.x; acc[i].y += w * v.y; acc[i].z += w * v.z; acc[i].w += w * v.w;
+        }
+    }
+    if constexpr (W > 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(sums[warp])[lane + 32 * i] = acc[i];
+        __syncthreads();
+        if (warp > 0) return;
+#pragma unroll
+        for (int w = 1; w < W; ++w)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 v = reinterpret_cast<const float4*>(sums[w])[lane + 32 * i];
+                acc[i].x += v.x; acc[i].y += v.y; acc[i].z += v.z; acc[i].w += v.w;
+            }
     }
     const float inv = z != 0.f ? 1.f / z : 0.f;
     const int j = q / a.H, h = q - j * a.H;
     const long long row = static_cast<long long>(m.b) * a.n_q + j;
-    reinterpret_cast<uint2*>(a.out + row * a.o_row + h * a.o_head)[threadIdx.x] =
-        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    if (a.lse && threadIdx.x == 0) a.lse[row * a.H + h] = z != 0.f ? (z_ref[1] + log2f(z)) * kLn2 : -CUDART_INF_F;
+    uint2* dst = reinterpret_cast<uint2*>(a.out + row * a.o_row + h * a.o_head) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        dst[32 * i] = make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+    if (a.lse && lane == 0) a.lse[row * a.H + h] = z != 0.f ? (ref + log2f(z)) * kLn2 : -CUDART_INF_F;
 }
 
 // Up to 64 query rows: one block per range; more: CTA pairs, 128 rows each, as many ranges as there are pairs left.
@@ -613,7 +641,10 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, 
         e = cudaGetLastError();
     }
     if (e != cudaSuccess || sp.ranges == 1) return e;
-    dc::join_kernel<<<dim3(sp.ranges - 1, rows, sp.rb), 128, 0, st>>>(a, sp.rb, sp.ranges, sp.block_rows, part, part_lse, meta);
+    if (a.B <= sp.ranges / 8)
+        dc::join_kernel<1><<<dim3(sp.ranges - 1, rows, sp.rb), 32 * dc::kJoinWarps, 0, st>>>(a, sp.rb, sp.ranges, sp.block_rows, part, part_lse, meta);
+    else
+        dc::join_kernel<8><<<dim3(sp.ranges - 1, (rows + 7) / 8, sp.rb), 32 * dc::kJoinWarps, 0, st>>>(a, sp.rb, sp.ranges, sp.block_rows, part, part_lse, meta);
     count_launch();
     return cudaGetLastError();
 }

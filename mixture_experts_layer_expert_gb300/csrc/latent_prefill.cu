@@ -17,12 +17,16 @@
 //
 // Bound: 2 x 128 x 128 x 320 flops per key tile and query tile; q, k, v and out
 // are a few bytes per thousand flops.  Exponentials, 128 x 128 per tile, take
-// less issue time than the tile's MMAs.
+// less issue time than the tile's MMAs: 12 x 107 + 8 x 75 = 1,884 cycles (an MMA
+// with both operands in shared memory costs 43 cycles beside N / 2).  Measured: 4 x
+// 2,048 tokens x 128 heads, causal, 620 us, 1.11 PFLOP/s of the pairs that count; the
+// tiles on the diagonal do 1/17 more than those.
 //
 // Warps 0-3 / 4-7: softmax and output of tile 0 / 1 (thread = row = TMEM lane);
 // warp 8: work distribution and TMA loads; warp 9: MMA issue.  K, V and the
 // shared rotary key go through a ring of eight 16 KB units (128 rows x 64
-// columns): three of K (two of k_n, one of k_r), two of V per key tile, one barrier for each three and two.
+// columns): three of K (two of k_n, one of k_r), two of V per key tile, one barrier
+// for each three and two.
 // Blocks take further items from the grid's not yet started blocks (cluster
 // launch control), so the next item's loads overlap this item's last tiles, and
 // items are numbered with the longest key range of each sequence first.

@@ -5,9 +5,11 @@
 // Memory bound: x is read and y written once.  A thread owns one 16-byte vector
 // (interleaved layout) or one vector of each half (half layout) of a token, has
 // the vector's cos and sin computed once, and walks over up to 8 heads with it,
-// so the sine costs an eighth of a per-element evaluation; neighbouring threads
+// so the sine costs an eighth of a per-element evaluation (fewer heads a thread, for
+// more threads, cost 12.3 us instead of 10.6 for 1,024 tokens x 128 heads x 64); neighbouring threads
 // cover neighbouring vectors, then neighbouring heads, so every warp access is
-// whole 128-byte lines when the heads are contiguous.
+// whole 128-byte lines when the heads are contiguous.  Measured: 65,536 tokens x 32
+// heads x 128, bf16, 170 us (6.3 TB/s, 0.93 of a copy's rate).
 #include "kernels.h"
 #include "latent.cuh"
 
