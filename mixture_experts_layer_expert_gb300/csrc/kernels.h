@@ -242,7 +242,7 @@ struct LatentDecodeArgs {
 };
 size_t latent_decode_ws_bytes(int H, int B, int n_q);
 // latent_decode_pair.cu: more than 64 query rows; meta: dc::Meta [ranges]
-cudaError_t launch_decode_pair(const CUtensorMap& tile, const CUtensorMap& row, const LatentDecodeArgs& a, bool fp8,
+cudaError_t launch_decode_pair(const CUtensorMap& tile, const CUtensorMap& run, const CUtensorMap& row, const LatentDecodeArgs& a, bool fp8,
                                int rb, int ranges, float* part, float* part_lse, void* meta, cudaStream_t st);
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, cudaStream_t st);
 

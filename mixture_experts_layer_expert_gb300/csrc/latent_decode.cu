@@ -68,7 +68,7 @@ template <bool FP8, int RN> constexpr int kThreads = 32 * (8 + kConv<FP8, RN>);
 
 template <bool FP8, int RN>
 __global__ void __launch_bounds__(kThreads<FP8, RN>, 1)
-decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant__ CUtensorMap tmRow,
+decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant__ CUtensorMap tmRun, const __grid_constant__ CUtensorMap tmRow,
               const LatentDecodeArgs a, const int ranges, float* __restrict__ part, float* __restrict__ part_lse,
               Meta* __restrict__ meta) {
     // all of the SM's shared memory and no static part: the block's memory starts on a 1 KB boundary
@@ -163,7 +163,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
         }
     } else if (warp == 7) {
         // -------------------------------------------------------------- loads
-        if (lane == 0) { tma_prefetch_desc(&tmTile); tma_prefetch_desc(&tmRow); }
+        if (lane == 0) { tma_prefetch_desc(&tmTile); tma_prefetch_desc(&tmRun); tma_prefetch_desc(&tmRow); }
         // bf16: stages of 2 boxes for the MMAs; FP8: raw stages of 1 box for the converters
         constexpr int depth = FP8 ? raws : stages, chunks = FP8 ? 1 : 2, step = FP8 ? 128 : 64;
         uint64_t* full = FP8 ? sh.raw_full : sh.full;
@@ -185,11 +185,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
                 for (int c = 0; c < 4; ++c, ++u) {
                     const uint32_t s = u % depth;
                     if (!wait(&empty[s], ((u / depth) & 1) ^ 1)) break;
-                    load_half<false>(&tmTile, &tmRow, hf, dst + s * (FP8 ? CH : PAIR), smem_u32(&full[s]), smem_u32(&full[s]), chunks * CH,
+                    load_half<false>(&tmTile, &tmRun, &tmRow, hf, dst + s * (FP8 ? CH : PAIR), smem_u32(&full[s]), smem_u32(&full[s]), chunks * CH,
                                      128 * c, step, chunks, lane);
                 }
                 if (!ok || !wait(&sh.r_empty[g & 1], ((g >> 1) & 1) ^ 1)) break;
-                load_half<false>(&tmTile, &tmRow, hf, rope + (g & 1) * CH, smem_u32(&sh.r_full[g & 1]), smem_u32(&sh.r_full[g & 1]), CH,
+                load_half<false>(&tmTile, &tmRun, &tmRow, hf, rope + (g & 1) * CH, smem_u32(&sh.r_full[g & 1]), smem_u32(&sh.r_full[g & 1]), CH,
                                  kLatent, step, 1, lane);
                 ++nr;
             }
@@ -613,15 +613,16 @@ size_t latent_decode_ws_bytes(int H, int, int n_q) {
 
 cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, cudaStream_t st) {
     static bool attr[2][3][kMaxDevices] = {{{false}}};
-    using Fn = void (*)(CUtensorMap, CUtensorMap, LatentDecodeArgs, int, float*, float*, dc::Meta*);
+    using Fn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, LatentDecodeArgs, int, float*, float*, dc::Meta*);
     static const Fn fns[2][3] = {{dc::decode_kernel<false, 16>, dc::decode_kernel<false, 32>, dc::decode_kernel<false, 64>},
                                  {dc::decode_kernel<true, 16>, dc::decode_kernel<true, 32>, dc::decode_kernel<true, 64>}};
     const dc::Shape sp = dc::shape(a.H, a.n_q);
     const int all = a.H * a.n_q, rows = all < sp.block_rows ? all : sp.block_rows;
-    CUtensorMap tile, row;
+    CUtensorMap tile, run, row;
     const long long records = a.n_pages * a.page_size;
     const int cols = fp8 ? kRecFp8 : kLatent + kRope;          // elements of a record (FP8: bytes)
     cudaError_t e = make_map(&tile, a.cache, records, cols, dc::TT, fp8);
+    if (e == cudaSuccess) e = make_map(&run, a.cache, records, cols, 16, fp8);
     if (e == cudaSuccess) e = make_map(&row, a.cache, records, cols, 1, fp8);
     if (e != cudaSuccess) return e;
     const size_t slots = static_cast<size_t>(sp.rb) * sp.ranges * 2;
@@ -629,14 +630,14 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, 
     float* part_lse = part + slots * sp.block_rows * kLatent;
     dc::Meta* meta = reinterpret_cast<dc::Meta*>(part_lse + slots * sp.block_rows);
     if (sp.block_rows > dc::ROWS) {
-        e = launch_decode_pair(tile, row, a, fp8, sp.rb, sp.ranges, part, part_lse, meta, st);
+        e = launch_decode_pair(tile, run, row, a, fp8, sp.rb, sp.ranges, part, part_lse, meta, st);
     } else {
         const int v = rows <= 16 ? 0 : (rows <= 32 ? 1 : 2);
         const Fn fn = fns[fp8][v];
         e = smem_attr_once(reinterpret_cast<const void*>(fn), dc::SMEM, attr[fp8][v]);
         if (e != cudaSuccess) return e;
         fn<<<static_cast<unsigned>(sp.ranges), 32 * (8 + (!fp8 ? 0 : (v == 2 ? 4 : 8))), dc::SMEM, st>>>(
-            tile, row, a, sp.ranges, part, part_lse, meta);
+            tile, run, row, a, sp.ranges, part, part_lse, meta);
         count_launch();
         e = cudaGetLastError();
     }

@@ -161,20 +161,26 @@ __device__ __forceinline__ void lookup_tiles(const LatentDecodeArgs& a, int b, i
 struct Half {
     int start;
     bool box;
+    bool run;                   // the sixteen records of lane group lane / 4 follow one another
     int4 y;                     // the four records of gather group lane & 15
 };
 template <int TT>
 __device__ __forceinline__ Half read_half(const TileRecs<TT>& t, int h, int lane) {
-    return Half{t.start[h], t.box[h] != 0, *reinterpret_cast<const int4*>(&t.rec[64 * h + 4 * (lane & 15)])};
+    const int4 y = *reinterpret_cast<const int4*>(&t.rec[64 * h + 4 * (lane & 15)]);
+    const int first = __shfl_sync(0xffffffffu, y.x, lane & 28) + 4 * (lane & 3);
+    const unsigned next = __ballot_sync(0xffffffffu, y.x == first && y.y == first + 1 && y.z == first + 2 && y.w == first + 3);
+    return Half{t.start[h], t.box[h] != 0, ((next >> (lane & 28)) & 15u) == 15u, y};
 }
 __device__ __forceinline__ void sts16(uint32_t dst, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 // Whole warp: `chunks` boxes of 64 records x 128 bytes (columns from col on, col_step elements apart) to dst, each
-// 8 KB.  expect: the barrier's one arrival with this many bytes (0: another CTA makes it).  PAIR_BAR: bar is a
+// 8 KB; records that do not follow one another come in boxes of sixteen where those do (pages of a multiple of 16),
+// else by gathers of four, which take the TMA unit about 100 cycles each (48-token pages, FP8, 256 query rows: 230 us
+// with gathers alone, 162 so).  expect: the barrier's one arrival with this many bytes (0: another CTA makes it).  PAIR_BAR: bar is a
 // shared::cluster address.
 template <bool PAIR_BAR>
-__device__ __forceinline__ void load_half(const CUtensorMap* tile, const CUtensorMap* row, const Half& g, uint32_t dst,
+__device__ __forceinline__ void load_half(const CUtensorMap* tile, const CUtensorMap* run, const CUtensorMap* row, const Half& g, uint32_t dst,
                                           uint32_t bar, uint32_t local_bar, uint32_t expect, int col, int col_step, int chunks,
                                           int lane) {
     if (g.box) {
@@ -190,7 +196,12 @@ __device__ __forceinline__ void load_half(const CUtensorMap* tile, const CUtenso
         __syncwarp();
         const int c = lane >> 4;
         const uint32_t to = dst + c * CH + (lane & 15) * 512;
-        if (c < chunks) {
+        if (c < chunks && g.run) {
+            if ((lane & 3) == 0) {
+                if constexpr (PAIR_BAR) tma_load_2d_pair(to, run, bar, col + c * col_step, g.y.x);
+                else tma_load_2d(to, run, bar, col + c * col_step, g.y.x);
+            }
+        } else if (c < chunks) {
             if constexpr (PAIR_BAR) tma_gather4_pair(to, row, bar, col + c * col_step, g.y.x, g.y.y, g.y.z, g.y.w);
             else tma_gather4(to, row, bar, col + c * col_step, g.y.x, g.y.y, g.y.z, g.y.w);
         }

@@ -16,7 +16,7 @@
 // Bound: with 128 rows a record's 139 k multiply-adds meet its 1,152 bytes at about the balance of tensor
 // rate and memory; here the MMAs' fixed costs decide.  Measured: 64 sequences of 2,000 to 14,000 tokens x 128
 // heads, bf16 cache, 164 us (850 TFLOP/s, 3.6 TB/s of records; on blocks of 64 rows it was 388 us); 32 sequences x
-// 128 heads x 2 new tokens, FP8 cache, 218 us.
+// 128 heads x 2 new tokens, FP8 cache, 149 us.
 //
 // Per CTA: warps 0-3 softmax, rescaling and output (thread = row of the lane and half of the records);
 // warp 4 MMA issue in the even CTA, in the odd one it tells the even CTA which stages have
@@ -56,7 +56,7 @@ __device__ __forceinline__ void arrive_even(uint32_t cluster_bar) {
 
 template <bool FP8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads<FP8>, 1)
-decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant__ CUtensorMap tmRow,
+decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant__ CUtensorMap tmRun, const __grid_constant__ CUtensorMap tmRow,
                    const LatentDecodeArgs a, const int rb_count, const int ranges, float* __restrict__ part,
                    float* __restrict__ part_lse, Meta* __restrict__ meta) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -153,7 +153,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
         }
     } else if (warp == 7) {
         // -------------------------------------------------------------- loads
-        if (lane == 0) { tma_prefetch_desc(&tmTile); tma_prefetch_desc(&tmRow); }
+        if (lane == 0) { tma_prefetch_desc(&tmTile); tma_prefetch_desc(&tmRun); tma_prefetch_desc(&tmRow); }
         constexpr int depth = FP8 ? MAXRAW : stages, chunks = FP8 ? 1 : 2, step = FP8 ? 128 : 64;
         uint64_t* full = FP8 ? sh.raw_full : sh.full;
         uint64_t* empty = FP8 ? sh.raw_empty : sh.empty;
@@ -170,9 +170,9 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
             const uint32_t lb = smem_u32(&full[s]);
             // bf16: both CTAs' loads complete on the even CTA's barrier, which expects the bytes of both
             if constexpr (FP8)
-                load_half<false>(&tmTile, &tmRow, gr, dst + s * CH, lb, lb, CH, col, step, chunks, lane);
+                load_half<false>(&tmTile, &tmRun, &tmRow, gr, dst + s * CH, lb, lb, CH, col, step, chunks, lane);
             else
-                load_half<true>(&tmTile, &tmRow, gr, dst + s * PAIR, map_to_cta(lb, 0), lb, rank ? 0 : 2 * PAIR, col, step, chunks, lane);
+                load_half<true>(&tmTile, &tmRun, &tmRow, gr, dst + s * PAIR, map_to_cta(lb, 0), lb, rank ? 0 : 2 * PAIR, col, step, chunks, lane);
             ++u;
             return true;
         };
@@ -189,7 +189,7 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
                     const Half own = rank ? nxt[1] : nxt[0];
                     for (int c = 0; c < 4 && ok; ++c) stage(own, 128 * c);
                     if (!ok || !wait(&sh.r_empty[g & 1], ((g >> 1) & 1) ^ 1)) break;
-                    load_half<true>(&tmTile, &tmRow, own, smem_u32(srope) + (g & 1) * CH, leader_bar(&sh.r_full[g & 1]),
+                    load_half<true>(&tmTile, &tmRun, &tmRow, own, smem_u32(srope) + (g & 1) * CH, leader_bar(&sh.r_full[g & 1]),
                                     smem_u32(&sh.r_full[g & 1]), rank ? 0 : 2 * CH, kLatent, step, 1, lane);
                     ++g;
                 }
@@ -498,13 +498,13 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
 
 }  // namespace dp
 
-cudaError_t launch_decode_pair(const CUtensorMap& tile, const CUtensorMap& row, const LatentDecodeArgs& a, bool fp8,
+cudaError_t launch_decode_pair(const CUtensorMap& tile, const CUtensorMap& run, const CUtensorMap& row, const LatentDecodeArgs& a, bool fp8,
                                int rb, int ranges, float* part, float* part_lse, void* meta, cudaStream_t st) {
     static bool attr[2][kMaxDevices] = {{false}};
     auto fn = fp8 ? dp::decode_pair_kernel<true> : dp::decode_pair_kernel<false>;
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(fn), dc::SMEM, attr[fp8]);
     if (e != cudaSuccess) return e;
-    fn<<<static_cast<unsigned>(2 * rb * ranges), fp8 ? 512 : 256, dc::SMEM, st>>>(tile, row, a, rb, ranges, part, part_lse,
+    fn<<<static_cast<unsigned>(2 * rb * ranges), fp8 ? 512 : 256, dc::SMEM, st>>>(tile, run, row, a, rb, ranges, part, part_lse,
                                                                                   static_cast<dc::Meta*>(meta));
     count_launch();
     return cudaGetLastError();
