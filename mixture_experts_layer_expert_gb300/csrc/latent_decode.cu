@@ -494,37 +494,53 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
 
 constexpr int kRanges = 152;                  // one block per SM
 
-// Joins the partials of the sequences that range boundaries cut.  Block (boundary, RB rows, row block): the
-// boundary before range s; the first boundary inside a sequence joins all its pieces, in range order, a row on
-// 8 / RB warps.  RB = 8 for batches (a block per row spent its time on the search for the pieces, 2 us of dependent
-// loads in four waves of blocks: 64 sequences x 128 rows 15.9 us, now 9.7); RB = 1 where a sequence has more than 8
+// Joins the partials of the sequences that range boundaries cut, in range order, a row on 8 / RB warps.  Block
+// (boundary, RB rows, row block): of the boundaries inside a sequence, the one before range s, the first joins; with
+// RB = 1 (sequence, row, row block), which looks for its s.  RB = 8 for batches (a block per row spent its time on the search for the pieces, 2 us of dependent
+// loads in four waves of blocks: 64 sequences x 128 rows 15.9 us, now 9.2); RB = 1 where a sequence has more than 8
 // pieces on average (one sequence of 65 pieces x 16 rows: 16 us more with a warp per row).
 constexpr int kJoinWarps = 8;
+static_assert(32 * kJoinWarps >= kRanges, "a thread a range");
 template <int RB>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, const int block_rows, const float* __restrict__ part,
-            const float* __restrict__ part_lse, const Meta* __restrict__ meta) {
+            const float* __restrict__ part_lse, const Meta* __restrict__ all_meta) {
     constexpr int W = kJoinWarps / RB;
     __shared__ float sums[W > 1 ? W : 1][W > 1 ? kLatent : 1];
     __shared__ int slots[kRanges];
     __shared__ float weight[kJoinWarps][kRanges];
     __shared__ int count;
+    __shared__ Meta meta[kRanges];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int s = blockIdx.x + 1, r = blockIdx.y * RB + warp / W, rb = blockIdx.z, q = rb * block_rows + r;
-    const Meta m = meta[s];
-    if (m.b >= a.B || m.tiles == 0 || m.off == 0) return;     // no tiles, or the sequence starts here
+    if (threadIdx.x < ranges) meta[threadIdx.x] = all_meta[threadIdx.x];      // one latency for the whole search
+    __syncthreads();
+    const int r = blockIdx.y * RB + warp / W, rb = blockIdx.z, q = rb * block_rows + r;
+    int s = blockIdx.x + 1;
+    Meta m{static_cast<int>(blockIdx.x), 1, 1, 0};
+    if constexpr (RB > 1) {
+        m = meta[s];
+        if (m.b >= a.B || m.tiles == 0 || m.off == 0) return; // no tiles, or the sequence starts here
+    }
     if (warp == 0) {
+        if constexpr (RB == 1) {
+            s = 0;
+            for (int k0 = 0; k0 < ranges && s == 0; k0 += 32) {
+                Meta mk{-1, 0, 0, 0};
+                if (k0 + lane < ranges) mk = meta[k0 + lane];
+                const unsigned inside = __ballot_sync(0xffffffffu, mk.b == m.b && mk.tiles > 0 && mk.off > 0);
+                if (inside) s = k0 + __ffs(inside) - 1;       // (range 0 starts with a sequence)
+            }
+        }
         // the range before (empty ones, where there are fewer tiles than ranges, aside) holds the piece before
         int first = s - 1;
-        for (;; first -= 32) {
+        for (; first >= 0; first -= 32) {
             const int k = first - lane;
             const unsigned some = __ballot_sync(0xffffffffu, k >= 0 && meta[k < 0 ? 0 : k].tiles > 0);
             if (some) { first -= __ffs(some) - 1; break; }
-            if (first < 32) break;                            // (cannot be: m.off > 0)
         }
         int n = 0;
         const Meta mf = meta[first < 0 ? 0 : first];
-        if (first >= 0 && !(mf.b == m.b && mf.off > 0)) {     // else an earlier boundary is inside the sequence too
+        if (s > 0 && first >= 0 && !(mf.b == m.b && mf.off > 0)) {     // else an earlier boundary is inside the sequence too
             for (int k0 = first; k0 < ranges; k0 += 32) {
                 const int k = k0 + lane;
                 Meta mk{-1, 0, 0, 0};
@@ -643,7 +659,7 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, 
     }
     if (e != cudaSuccess || sp.ranges == 1) return e;
     if (a.B <= sp.ranges / 8)
-        dc::join_kernel<1><<<dim3(sp.ranges - 1, rows, sp.rb), 32 * dc::kJoinWarps, 0, st>>>(a, sp.rb, sp.ranges, sp.block_rows, part, part_lse, meta);
+        dc::join_kernel<1><<<dim3(a.B, rows, sp.rb), 32 * dc::kJoinWarps, 0, st>>>(a, sp.rb, sp.ranges, sp.block_rows, part, part_lse, meta);
     else
         dc::join_kernel<8><<<dim3(sp.ranges - 1, (rows + 7) / 8, sp.rb), 32 * dc::kJoinWarps, 0, st>>>(a, sp.rb, sp.ranges, sp.block_rows, part, part_lse, meta);
     count_launch();
