@@ -595,8 +595,9 @@ fs_status fs_latent_cache_read(const fs_latent_cache* desc, const void* cache, i
  * outside [0, n_pages) (its positions are left out) sets the device error word
  * (code 5).  n_q 1 .. 16, scale > 0, n_pages page_size < 2^31.  The length is
  * split over the SMs and joined in a fixed order: results do not depend on
- * timing.  ws: fs_latent_decode_ws_bytes bytes,
- * 256-byte aligned. */
+ * timing.  (A wait in the kernel ends after 2 s with code 3; one sequence of more
+ * than 10^8 positions with 2,048 query rows would come near that.)
+ * ws: fs_latent_decode_ws_bytes bytes, 256-byte aligned. */
 size_t fs_latent_decode_ws_bytes(int32_t heads, int32_t B, int32_t n_q);
 fs_status fs_latent_decode(const fs_latent_cache* desc, int32_t heads, int32_t B, int32_t n_q,
                            const fs_rows* q_latent, const fs_rows* q_rope, const void* cache,
