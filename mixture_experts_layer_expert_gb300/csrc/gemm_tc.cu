@@ -1279,24 +1279,6 @@ cudaError_t make_map(CUtensorMap* m, const void* base, long long rows, long long
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// A [rows, heads, width] bf16 operand with strides in elements (3D map: column,
-// head, row), box 64 columns x 1 head x box_rows rows, 128-byte swizzle.  The
-// stride of a dimension of extent 1 is never used and may be anything.
-cudaError_t make_map_rows(CUtensorMap* m, const void* base, long long rows, int heads, int width, long long row,
-                          long long head, int box_rows) {
-    cudaError_t e = get_encode();
-    if (e != cudaSuccess) return e;
-    cuuint64_t gdim[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
-    cuuint64_t gstride[2] = {heads > 1 ? static_cast<cuuint64_t>(head) * 2 : static_cast<cuuint64_t>(width) * 2,
-                             rows > 1 ? static_cast<cuuint64_t>(row) * 2 : static_cast<cuuint64_t>(width) * 2};
-    cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
-    cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // 3D tensor map over the tiled weight layout [nblocks][256][128 bytes] (each
 // block a contiguous 32 KB tile of 256 rows) with a box of box_rows x 128 bytes.
 cudaError_t make_map_blocked(CUtensorMap* m, const void* base, long long nblocks, int box_rows, bool f8) {

@@ -30,6 +30,7 @@
 // Blocks take further items from the grid's not yet started blocks (cluster
 // launch control), so the next item's loads overlap this item's last tiles, and
 // items are numbered with the longest key range of each sequence first.
+#include <cudaTypedefs.h>
 #include <math_constants.h>
 
 #include "kernels.h"
@@ -470,6 +471,31 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
 }
 
 }  // namespace pf
+
+// A [rows, heads, width] bf16 operand with strides in elements (3D map: column,
+// head, row), box 64 columns x 1 head x box_rows rows, 128-byte swizzle.  The
+// stride of a dimension of extent 1 is never used and may be anything.
+cudaError_t make_map_rows(CUtensorMap* m, const void* base, long long rows, int heads, int width, long long row,
+                          long long head, int box_rows) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    if (!encode) {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    cuuint64_t gdim[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+    cuuint64_t gstride[2] = {heads > 1 ? static_cast<cuuint64_t>(head) * 2 : static_cast<cuuint64_t>(width) * 2,
+                             rows > 1 ? static_cast<cuuint64_t>(row) * 2 : static_cast<cuuint64_t>(width) * 2};
+    cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(box_rows)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 cudaError_t launch_latent_prefill(const LatentPrefillArgs& a, cudaStream_t st) {
     static bool attr[kMaxDevices] = {false};
