@@ -41,7 +41,12 @@ struct Shared {
     int abort_flag;
     int b0, tile0, left;
     uint32_t live[kInfo][4];                  // records of a tile that count
-    float red[2][ROWS];
+    // What the two warps of a row hand each other: its maximum over their halves of a tile's records, and its sum of p.
+    // Arrays of their own: a maximum is read behind the barrier that follows its write, but from there to a piece's
+    // end, where the sums are written, no barrier need follow (the piece's last tile may have raised the maximum).
+    // Each array's next write lies behind a barrier that its readers reach after reading: the next tile's bar_any, the
+    // barrier at the piece's end.
+    float red[2][ROWS], sum[2][ROWS];
     alignas(16) float scale[kInfo][TT];       // FP8: the records' scales
     TileRecs<TT> recs[2];
 };
@@ -442,9 +447,9 @@ decode_pair_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_cons
                 __syncwarp();
                 if (lane == 0) arrive_even(leader_bar(&sh.p_full));
             }
-            sh.red[th][hr] = l;
+            sh.sum[th][hr] = l;
             bar_sync(1, 128);
-            const float z = l + sh.red[th ^ 1][hr];
+            const float z = l + sh.sum[th ^ 1][hr];
             const float inv = z != 0.f ? 1.f / z : 0.f;
             const bool whole = p.t0 == 0 && p.t1 == p.n;
             const long long slot = (static_cast<long long>(range) * rb_count + rb) * 2 + (p.b == sh.b0 ? 0 : 1);
