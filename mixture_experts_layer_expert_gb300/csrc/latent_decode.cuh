@@ -215,7 +215,9 @@ __device__ __forceinline__ void load_q(const LatentDecodeArgs& a, int b, int row
     constexpr int PER = R < 32 ? 32 / R : 1;    // threads per row
 #pragma unroll
     for (int r = lane / PER; r < R; r += 32 / PER) {
-        const int qr = row0 + (r < rows ? r : 0), j = qr / a.H, h = qr - j * a.H;
+        // a row past the last: sixteen zero bytes from an address inside the operand (row0 itself lies behind the last
+        // row in a pair's second CTA that has none)
+        const int qr = r < rows ? row0 + r : 0, j = qr / a.H, h = qr - j * a.H;
         const long long row = static_cast<long long>(b) * a.n_q + j;
         const __nv_bfloat16* ql = a.ql + row * a.ql_row + h * a.ql_head;
         const __nv_bfloat16* qr64 = a.qr + row * a.qr_row + h * a.qr_head;

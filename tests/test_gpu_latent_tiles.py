@@ -33,3 +33,13 @@ def test_decode_pieces_of_one_tile(cache, H, n_q):
         p.run()
         assert torch.equal(p.out, first) and torch.equal(p.lse, lse)
     _no_dev_error()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("H,n_q", [(48, 4), (43, 3), (20, 16)])
+def test_decode_last_row_block_half_empty(cache, H, n_q):
+    """More than 128 query rows whose last 128-row block has at most 64: its second CTA has none."""
+    p = Decode(H, [700, 0, 3, 129, 2500], n_q, 64, cache)
+    p.run()
+    _no_dev_error()
+    p.check()
