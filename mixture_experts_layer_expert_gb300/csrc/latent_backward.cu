@@ -34,6 +34,7 @@
 // the sum over the heads 8.4 us, dq 144 us; 617 TFLOP/s of the 832 multiply-adds over all.
 #include <math_constants.h>
 
+#include "handover.h"
 #include "kernels.h"
 #include "latent.cuh"
 
@@ -183,14 +184,18 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             tma_prefetch_desc(&tmQ); tma_prefetch_desc(&tmKn); tma_prefetch_desc(&tmKr); tma_prefetch_desc(&tmV);
             tma_prefetch_desc(&tmDo);
         }
-        uint32_t u = 0, nkv = 0, k = 0;
+        uint32_t u = 0, nkv = 0;
         int id = blockIdx.x;
         bool ok = true;
-        for (; ok; ++k) {
+        HandOver ho;
+        for (uint32_t k = 0;; ++k) {
             const uint32_t slot = k & 1;
-            if (lane == 0 && id >= 0) {
-                mbar_arrive_expect_tx(smem_u32(&sh.q.next_bar), 16);
-                next_block_request(smem_u32(sh.q.next_resp), smem_u32(&sh.q.next_bar));
+            if (id >= 0) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(smem_u32(&sh.q.next_bar), 16);
+                    next_block_request(smem_u32(sh.q.next_resp), smem_u32(&sh.q.next_bar));
+                }
+                ho.ask();
             }
             Item it{};
             it.valid = id < 0 ? -1 : 0;
@@ -271,18 +276,20 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUte
             }
             if (!ok) break;
             if (lane == 0) {
-                ok = wait_bar(smem_u32(&sh.q.next_bar), k & 1, abort_flag, a.err);
+                ok = wait_bar(smem_u32(&sh.q.next_bar), ho.parity(), abort_flag, a.err);
                 if (ok) id = next_block_answer(smem_u32(sh.q.next_resp));
                 fence_proxy_async_smem();
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            ho.answer();
             id = __shfl_sync(0xffffffffu, id, 0);
         }
         if (lane == 0) {
             const uint32_t pend = u < STAGES ? u : STAGES;
             for (uint32_t j = 1; j <= pend; ++j) drain_bar(&sh.full[(u - j) % STAGES], ((u - j) / STAGES) & 1, a.err);
             if (nkv > 0) drain_bar(&sh.kv_full, (nkv - 1) & 1, a.err);
-            if (!ok) drain_bar(&sh.q.next_bar, k & 1, a.err);
+            if (ho.pending()) drain_bar(&sh.q.next_bar, ho.parity(), a.err);       // after a wait that gave up
         }
         __syncwarp();
     } else if (warp == 9) {
@@ -573,14 +580,18 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             tma_prefetch_desc(&tmQ); tma_prefetch_desc(&tmKn); tma_prefetch_desc(&tmKr); tma_prefetch_desc(&tmV);
             tma_prefetch_desc(&tmDo);
         }
-        uint32_t u = 0, nq = 0, nk = 0, nv = 0, k = 0;
+        uint32_t u = 0, nq = 0, nk = 0, nv = 0;
         int id = blockIdx.x;
         bool ok = true;
-        for (; ok; ++k) {
+        HandOver ho;
+        for (uint32_t k = 0;; ++k) {
             const uint32_t slot = k & 1;
-            if (lane == 0 && id >= 0) {
-                mbar_arrive_expect_tx(smem_u32(&sh.q.next_bar), 16);
-                next_block_request(smem_u32(sh.q.next_resp), smem_u32(&sh.q.next_bar));
+            if (id >= 0) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(smem_u32(&sh.q.next_bar), 16);
+                    next_block_request(smem_u32(sh.q.next_resp), smem_u32(&sh.q.next_bar));
+                }
+                ho.ask();
             }
             Item it{};
             it.valid = id < 0 ? -1 : 0;
@@ -641,18 +652,20 @@ dq_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUten
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             if (lane == 0) {
-                ok = wait_bar(smem_u32(&sh.q.next_bar), k & 1, abort_flag, a.err);
+                ok = wait_bar(smem_u32(&sh.q.next_bar), ho.parity(), abort_flag, a.err);
                 if (ok) id = next_block_answer(smem_u32(sh.q.next_resp));
                 fence_proxy_async_smem();
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            ho.answer();
             id = __shfl_sync(0xffffffffu, id, 0);
         }
         if (lane == 0) {
             for (uint32_t e = 1; e <= 2 && e <= nk; ++e) drain_bar(&sh.k_full[(nk - e) & 1], ((nk - e) >> 1) & 1, a.err);
             if (nv > 0) drain_bar(&sh.v_full, (nv - 1) & 1, a.err);
             if (nq > 0) drain_bar(&sh.q_full, (nq - 1) & 1, a.err);
-            if (!ok) drain_bar(&sh.q.next_bar, k & 1, a.err);
+            if (ho.pending()) drain_bar(&sh.q.next_bar, ho.parity(), a.err);       // after a wait that gave up
         }
         __syncwarp();
     } else if (warp == 9) {

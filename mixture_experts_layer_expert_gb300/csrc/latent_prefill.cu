@@ -33,6 +33,7 @@
 #include <cudaTypedefs.h>
 #include <math_constants.h>
 
+#include "handover.h"
 #include "kernels.h"
 #include "latent.cuh"
 
@@ -144,12 +145,15 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
         uint32_t nq = 0, nk = 0, nv = 0;      // loads of Q, K and V tiles so far
         int id = blockIdx.x;
         bool ok = true;
-        uint32_t k = 0;
-        for (; ok; ++k) {
+        HandOver ho;
+        for (uint32_t k = 0;; ++k) {
             const uint32_t slot = k & 1, use = k >> 1;
-            if (lane == 0 && id >= 0) {
-                mbar_arrive_expect_tx(smem_u32(&sh.next_bar), 16);
-                next_block_request(smem_u32(sh.next_resp), smem_u32(&sh.next_bar));
+            if (id >= 0) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(smem_u32(&sh.next_bar), 16);
+                    next_block_request(smem_u32(sh.next_resp), smem_u32(&sh.next_bar));
+                }
+                ho.ask();
             }
             Item it{};
             it.valid = id < 0 ? -1 : 0;
@@ -218,11 +222,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             ok = __shfl_sync(0xffffffffu, ok, 0);
             if (!ok) break;
             if (lane == 0) {
-                ok = wait_bar(smem_u32(&sh.next_bar), k & 1, abort_flag, a.err);
+                ok = wait_bar(smem_u32(&sh.next_bar), ho.parity(), abort_flag, a.err);
                 if (ok) id = next_block_answer(smem_u32(sh.next_resp));
                 fence_proxy_async_smem();        // the answer is read before the next one may be written
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            ho.answer();
             id = __shfl_sync(0xffffffffu, id, 0);
         }
         if (lane == 0) {
@@ -232,9 +238,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ 
             if (nq > 0) {
                 drain_bar(&sh.q_full, (nq - 1) & 1, a.err);
             }
-            if (!ok) {                           // an answer may still be on its way
-                drain_bar(&sh.next_bar, k & 1, a.err);
-            }
+            if (ho.pending()) drain_bar(&sh.next_bar, ho.parity(), a.err);       // after a wait that gave up
         }
         __syncwarp();
     } else if (warp == 9) {
