@@ -555,7 +555,7 @@ fs_status fs_rope(const fs_rope_desc* rope, int64_t T, int32_t H, int32_t dtype,
  *            bytes: 656 bytes.  c is quantised as a row of FS_FP8 (scale 2^e, e
  *            the smallest integer with max |c_i| 2^-e <= 448, nearest even), so
  *            a value read back is code * scale exactly.
- * page_size >= 1; n_pages < 2^31. */
+ * page_size >= 1; n_pages < 2^31; the cache's bytes < 2^63. */
 typedef struct {
     int64_t n_pages;
     int32_t page_size;

@@ -84,7 +84,8 @@ fs_status check_cache(const fs_latent_cache* c) {
     if (c->dtype < FS_BF16 || c->dtype > FS_MXFP8) return FS_ERR_INVALID_ARG;
     if (c->dtype != FS_BF16 && c->dtype != FS_FP8) return FS_ERR_UNSUPPORTED;
     if (c->n_pages > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;      // block tables are int32
-    return FS_OK;
+    const int64_t rec = c->dtype == FS_FP8 ? kRecFp8 : kRecBf16;   // a record's byte offset is an int64
+    return c->n_pages * c->page_size <= INT64_MAX / rec ? FS_OK : FS_ERR_UNSUPPORTED;
 }
 bool is_fp8(const fs_latent_cache* c) { return c->dtype == FS_FP8; }
 int64_t n_slots(const fs_latent_cache* c) { return c->n_pages * c->page_size; }

@@ -1,0 +1,33 @@
+"""Limits of the attention entry points at the ends of their integer and floating-point ranges, without a GPU: every
+refusal comes before any CUDA call."""
+import ctypes
+
+import pytest
+
+from mixture_experts_layer_expert_gb300 import build, fs
+
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+V = ctypes.c_void_p(0x10000)            # 16-byte aligned, never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    lib = fs.lib()
+    before = fs.fs_launch_count()
+    yield lib
+    assert fs.fs_launch_count() == before
+
+
+def test_cache_whose_bytes_pass_64_bits(L):
+    """(2^31 - 1)^2 records have no byte count: the size is 0 and the calls refuse, not a size modulo 2^64."""
+    top = 2 ** 31 - 1
+    for dtype, rec in (("bf16", 1152), ("fp8", 656)):
+        most = (2 ** 63 - 1) // rec // top                        # pages of 2^31 - 1 records that 63 bits still count
+        assert fs.fs_latent_cache_bytes(fs.make_latent_cache(most, top, dtype)) == most * top * rec
+        for pages in (most + 1, top):
+            big = fs.make_latent_cache(pages, top, dtype)
+            assert fs.fs_latent_cache_bytes(big) == 0
+            d = ctypes.byref(big)
+            assert L.fs_latent_cache_write(d, 4, V, 512, V, 64, None, None, V, V, None) == UNSUPPORTED
+            assert L.fs_latent_cache_read(d, V, 4, V, V, 512, V, 64, None) == UNSUPPORTED
