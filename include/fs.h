@@ -538,7 +538,7 @@ typedef struct {
     double base;         /* > 1 */
     double factor;       /* >= 1; 1 = no scaling (the next three are not read) */
     double orig_len, beta_fast, beta_slow;
-    double mscale;       /* > 0 */
+    double mscale;       /* > 0, a normal fp32 number */
 } fs_rope_desc;
 
 /* Rotates the d_rot elements at x + t x_row + h x_head of T tokens and H heads

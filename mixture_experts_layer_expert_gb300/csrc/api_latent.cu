@@ -1,6 +1,7 @@
 // api_latent.cu -- the C ABI of the attention operators: rotary positions, the
 // paged latent cache, absorbed and expanded latent attention.  Argument checks
 // and launches only; see include/fs.h for the contracts.
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/fs.h"
@@ -47,7 +48,7 @@ fs_status rope_table(const fs_rope_desc* r, bool inverse, RopeTab* tab) {
     if (!r) return FS_ERR_INVALID_ARG;
     if (r->d_rot < 2 || (r->layout != FS_ROPE_INTERLEAVED && r->layout != FS_ROPE_HALF)) return FS_ERR_INVALID_ARG;
     if (!(r->base > 1.0) || !std::isfinite(r->base) || !(r->factor >= 1.0) || !std::isfinite(r->factor) ||
-        !(r->mscale > 0.0) || !std::isfinite(r->mscale))
+        !(r->mscale >= FLT_MIN) || !(r->mscale <= FLT_MAX))
         return FS_ERR_INVALID_ARG;
     if (r->d_rot % 16 || r->d_rot > kMaxRot) return FS_ERR_UNSUPPORTED;
     const double two_pi = 6.283185307179586476925286766559;

@@ -8,6 +8,7 @@ from mixture_experts_layer_expert_gb300 import build, fs
 
 INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
 V = ctypes.c_void_p(0x10000)            # 16-byte aligned, never dereferenced
+ODD = ctypes.c_void_p(0x10002)
 
 
 @pytest.fixture(scope="module")
@@ -31,3 +32,15 @@ def test_cache_whose_bytes_pass_64_bits(L):
             d = ctypes.byref(big)
             assert L.fs_latent_cache_write(d, 4, V, 512, V, 64, None, None, V, V, None) == UNSUPPORTED
             assert L.fs_latent_cache_read(d, V, 4, V, V, 512, V, 64, None) == UNSUPPORTED
+
+
+def test_rope_mscale_outside_fp32(L):
+    """mscale multiplies in fp32: one that would become 0, subnormal or infinite there is refused, one at the range's ends is not
+    refused for its value (the misaligned operand behind it is)."""
+    def call(mscale, pos):
+        rope = ctypes.byref(fs.make_rope(64, mscale=mscale))
+        return L.fs_rope(rope, 4, 2, 0, pos, V, 128, 64, V, 128, 64, 0, None)
+    for bad in (1e39, 1e300, 1e-40, 1e-46, 5e-324, float("inf"), float("nan"), -1.0):
+        assert call(bad, ODD) == INVALID, bad
+    for good in (3.4e38, 1.0, 1e-37):
+        assert call(good, ODD) == UNSUPPORTED                     # the misaligned pos, checked after the table
