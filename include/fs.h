@@ -608,7 +608,8 @@ fs_status fs_latent_decode(const fs_latent_cache* desc, int32_t heads, int32_t B
  * rows [cu_q[b], cu_q[b+1]) of Tq and key rows [cu_k[b], cu_k[b+1]) of Tk
  * (device int32 [n_seqs + 1], non-decreasing; either may be empty).  causal:
  * the last query sees the last key (query i of lq sees keys 0 .. lk - lq + i),
- * so more keys than queries is a cached prefix.  scale > 0.  What lies in rows
+ * so more keys than queries is a cached prefix.  scale > 0; Tq and Tk at most
+ * 2^29.  What lies in rows
  * outside a sequence, NaN included, does not reach it; a NaN in one of its keys or
  * values may reach all its queries, those that do not see that key too. */
 typedef struct {

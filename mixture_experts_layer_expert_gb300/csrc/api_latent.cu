@@ -92,6 +92,7 @@ bool is_fp8(const fs_latent_cache* c) { return c->dtype == FS_FP8; }
 int64_t n_slots(const fs_latent_cache* c) { return c->n_pages * c->page_size; }
 
 constexpr int kMaxHeads = 128, kMaxNq = 16;
+constexpr int kMaxRows = 1 << 29;      // packed rows: the kernels' sums and differences of two row indexes fit an int32
 
 fs_status check_decode(int32_t H, int32_t B, int32_t n_q) {
     if (H < 1 || B < 1 || n_q < 1) return FS_ERR_INVALID_ARG;
@@ -102,7 +103,7 @@ fs_status check_decode(int32_t H, int32_t B, int32_t n_q) {
 
 fs_status check_prefill(const fs_latent_prefill_desc* d) {
     if (!d || d->heads < 1 || d->n_seqs < 1 || d->Tq < 1 || d->Tk < 1) return FS_ERR_INVALID_ARG;
-    if (d->heads > kMaxHeads) return FS_ERR_UNSUPPORTED;
+    if (d->heads > kMaxHeads || d->Tq > kMaxRows || d->Tk > kMaxRows) return FS_ERR_UNSUPPORTED;
     // row tiles of 128 times heads index a grid
     if ((static_cast<int64_t>(d->Tq) / 128 + d->n_seqs + 1) * d->heads > 0x7fffffffLL ||
         (static_cast<int64_t>(d->Tk) / 128 + d->n_seqs + 1) * d->heads > 0x7fffffffLL)
@@ -271,7 +272,7 @@ fs_status fs_latent_prefill(const fs_latent_prefill_desc* desc, const fs_rows* q
 }
 
 size_t fs_latent_prefill_backward_ws_bytes(int32_t heads, int32_t Tq, int32_t Tk) {
-    if (heads < 1 || heads > kMaxHeads || Tq < 1 || Tk < 1) return 0;
+    if (heads < 1 || heads > kMaxHeads || Tq < 1 || Tk < 1 || Tq > kMaxRows || Tk > kMaxRows) return 0;
     return latent_backward_ws_bytes(heads, Tq, Tk);
 }
 

@@ -44,3 +44,18 @@ def test_rope_mscale_outside_fp32(L):
         assert call(bad, ODD) == INVALID, bad
     for good in (3.4e38, 1.0, 1e-37):
         assert call(good, ODD) == UNSUPPORTED                     # the misaligned pos, checked after the table
+
+
+def test_prefill_rows_past_the_kernels_index_range(L):
+    """Row and key indexes of a packed batch, their differences and tile ends are int32 in the kernels: 2^29 rows of
+    queries or keys leave room for all of them, more are refused (one head's rows would pass the card's memory)."""
+    top = 2 ** 29
+    r = ctypes.byref(fs.Rows(0x10000, 192, 192))
+    W = ctypes.c_void_p(0x1000000)
+    for Tq, Tk in ((top + 1, 96), (64, top + 1), (2 ** 31 - 1, 2 ** 31 - 1), (top, top)):
+        want = UNSUPPORTED if max(Tq, Tk) > top else INVALID
+        d = ctypes.byref(fs.LatentPrefillDesc(1, 2, Tq, Tk, 0, 0.1))
+        # past the limit refused as such; at it, the missing cu_q is what is refused
+        assert L.fs_latent_prefill(d, r, r, r, r, None, V, r, V, None) == want
+        assert L.fs_latent_prefill_backward(d, r, r, r, r, None, V, r, V, r, r, r, r, r, W, 1 << 40, None) == want
+        assert (fs.fs_latent_prefill_backward_ws_bytes(1, Tq, Tk) == 0) == (want == UNSUPPORTED)
