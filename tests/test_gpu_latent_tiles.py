@@ -2,11 +2,13 @@
 of stages and its running maxima are at work: many short sequences, many tiles a
 block, scores that grow along the sequence.  Against the 64-bit definitions with
 the bounds of latent_ref.py."""
+import math
+
 import pytest
 import torch
 
 from mixture_experts_layer_expert_gb300 import fs
-from test_gpu_latent import Decode, SENTINEL, _no_dev_error
+from test_gpu_latent import DEV, SCALE, SENTINEL, Decode, _no_dev_error, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +45,70 @@ def test_decode_last_row_block_half_empty(cache, H, n_q):
     p.run()
     _no_dev_error()
     p.check()
+
+
+class Rising(Decode):
+    """Records whose score jumps by 7.5 (15) over the rest, at positions of a sequence's second and later tiles: the
+    running maximum is raised by more than 2^8 in the middle of a block's work, while what came before still makes
+    several percent of the row's sum, so that a sum or an output that is not rescaled (or twice) shows.  Every fourth
+    head falls where the others rise."""
+
+    def __init__(self, H, lens, n_q, page, cache, seed=0):
+        super().__init__(H, lens, n_q, page, cache, seed)
+        g = gen(seed + 77)
+        u = torch.where(torch.rand(512, generator=g, device=DEV) < 0.5, -1.0, 1.0) / math.sqrt(512)
+        sign = torch.where(torch.arange(H, device=DEV) % 4 == 3, -1.0, 1.0)
+        self.ql.copy_(randn(g, self.ql.shape, 0.2, torch.float32) + 7.5 / (10 * SCALE) * sign[:, None] * u)
+        self.qr.mul_(0.3)
+        for b, n in enumerate(lens):
+            i = torch.arange(n, device=DEV)
+            c, kr = randn(g, (n, 512), 1.0, torch.float32), randn(g, (n, 64))
+            c -= (c @ u)[:, None] * u                                    # scores rise by the jumps alone
+            jump = (i % 211 == 130).float() + (i % 601 == 400).float()
+            c = (c + 10 * jump[:, None] * u).to(torch.bfloat16)
+            slots = self.table[b].long()[i // page] * page + i % page
+            fs.fs_latent_cache_write(self.desc, c, kr, slots, self.cache)
+            cb, kb = torch.empty_like(c), torch.empty_like(kr)
+            fs.fs_latent_cache_read(self.desc, self.cache, slots, cb, kb)
+            self.rows[b] = (cb, kb)
+
+    def check_rises(self):
+        """Three heads of four exceed the first 128 records' maximum by more than 2^8 at record 130."""
+        c, kr = self.rows[0]
+        s = torch.cat([self.ql[0], self.qr[0]], -1).double() @ torch.cat([c, kr], -1)[:131].double().T * SCALE
+        over = (s[:, 130] - s[:, :128].amax(1)) / math.log(2.0) > 8.0
+        assert over.float().mean() > 0.6
+
+
+# query rows 16, 32, 64 (one CTA), 128, 256, 300, 512 (CTA pairs, one to four row blocks); pages that are a tile's half or
+# whole, that end inside a tile, that are no multiple of four
+VARIANTS = [(16, 1, 64), (16, 1, 48), (32, 1, 48), (16, 2, 7), (64, 1, 7), (16, 4, 64), (128, 1, 64), (128, 1, 7),
+            (128, 2, 48), (100, 3, 64), (128, 4, 48)]
+
+
+def _run_twice_and_check(p):
+    p.check_rises()
+    p.run()
+    _no_dev_error()
+    p.check()
+    first, lse = p.out.clone(), p.lse.clone()
+    p.ws.fill_(0xFF)
+    p.out.fill_(SENTINEL)
+    p.run()
+    _no_dev_error()
+    assert torch.equal(p.out, first) and torch.equal(p.lse, lse)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("H,n_q,page", VARIANTS)
+def test_decode_raised_maxima_in_many_sequences(cache, H, n_q, page):
+    """Several pieces of several tiles a block: rings wrap, Q changes, maxima rise inside a piece."""
+    _run_twice_and_check(Rising(H, [200 + (97 * i) % 201 for i in range(300)], n_q, page, cache))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("H,n_q,page", VARIANTS)
+def test_decode_raised_maxima_in_a_long_sequence(cache, H, n_q, page):
+    """A sequence over all blocks, several tiles each, with shorter ones behind it; partials of rows that have risen and
+    rows that have not meet in the join."""
+    _run_twice_and_check(Rising(H, [40000, 9, 4000], n_q, page, cache))
