@@ -1,14 +1,14 @@
 """GPU parity of absorbed attention where a block's pieces of one tile, its rings
-of stages and its running maxima are at work: many short sequences, many tiles a
-block, scores that grow along the sequence.  Against the 64-bit definitions with
-the bounds of latent_ref.py."""
+of stages and its running maxima are at work (many short sequences, many tiles a
+block, scores that grow along the sequence), and expanded attention over long
+keys.  Against the 64-bit definitions with the bounds of latent_ref.py."""
 import math
 
 import pytest
 import torch
 
 from mixture_experts_layer_expert_gb300 import fs
-from test_gpu_latent import DEV, SCALE, SENTINEL, Decode, _no_dev_error, gen, randn
+from test_gpu_latent import DEV, SCALE, SENTINEL, Decode, Prefill, _no_dev_error, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -112,3 +112,19 @@ def test_decode_raised_maxima_in_a_long_sequence(cache, H, n_q, page):
     """A sequence over all blocks, several tiles each, with shorter ones behind it; partials of rows that have risen and
     rows that have not meet in the join."""
     _run_twice_and_check(Rising(H, [40000, 9, 4000], n_q, page, cache))
+
+
+@pytest.mark.parametrize("H,lq,lk,causal", [
+    (3, [300], [9000], True),                  # a chunk of a prompt behind a long cached prefix
+    (2, [2300, 1, 130], [2300, 4100, 5000], True),
+    (2, [700], [3000], False),
+])
+@pytest.mark.parametrize("q_std", [1.0, 12.0])
+def test_prefill_long_keys(H, lq, lk, causal, q_std):
+    """Dozens of key tiles an item; with scores of some tens maxima rise in the middle of them."""
+    p = Prefill(H, lq, lk, causal, q_std=q_std)
+    p.forward()
+    p.backward()
+    _no_dev_error()
+    p.check_forward()
+    p.check_backward()
