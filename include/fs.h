@@ -554,7 +554,9 @@ fs_status fs_rope(const fs_rope_desc* rope, int64_t T, int32_t H, int32_t dtype,
  *   FS_FP8:  512 E4M3 codes of c, k_r (64 bf16), the fp32 scale of c, 12 zero
  *            bytes: 656 bytes.  c is quantised as a row of FS_FP8 (scale 2^e, e
  *            the smallest integer with max |c_i| 2^-e <= 448, nearest even), so
- *            a value read back is code * scale exactly.
+ *            a value read back is code * scale exactly, subnormal numbers
+ *            included (but infinity for a magnitude above 31 2^123, within 3% of
+ *            the largest bf16, whose code times scale is 2^128).
  * page_size >= 1; n_pages < 2^31; the cache's bytes < 2^63. */
 typedef struct {
     int64_t n_pages;

@@ -51,7 +51,9 @@ __device__ __forceinline__ float2 rope_cs(uint64_t frac, float mscale, int inver
 }
 
 // Two E4M3 codes (low byte first) times the row's power-of-two scale, as packed
-// bf16: exact (3 mantissa bits) while the products stay normal bf16 numbers.
+// bf16: exact (3 mantissa bits) in the normal range; below it too for a row that
+// was bf16 (its values are multiples of 2^-133, bf16's smallest step, and rounding
+// to fewer bits leaves them so).
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t codes16, float scale) {
     uint32_t h2;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<unsigned short>(codes16)));

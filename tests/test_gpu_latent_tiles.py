@@ -7,6 +7,7 @@ import math
 import pytest
 import torch
 
+import latent_ref as ref
 from mixture_experts_layer_expert_gb300 import fs
 from test_gpu_latent import DEV, SCALE, SENTINEL, Decode, Prefill, _no_dev_error, gen, randn
 
@@ -128,3 +129,27 @@ def test_prefill_long_keys(H, lq, lk, causal, q_std):
     _no_dev_error()
     p.check_forward()
     p.check_backward()
+
+
+def test_fp8_cache_over_the_whole_exponent_range():
+    """A row's largest value from bf16's smallest subnormal to its largest number: what is read back is code * scale
+    exactly; only 2^128 (from magnitudes above 31 2^123) has no bf16 and is infinity."""
+    g = gen(8)
+    e = torch.arange(-133, 128, device=DEV)
+    c = (torch.rand((e.numel(), 512), generator=g, device=DEV).double() * 2 - 1) * ref.pow2(e)[:, None]
+    c[:, 7] = ref.pow2(e)                                            # the row's exponent, whatever was drawn
+    c[:, 8] = ref.pow2(e) * 2.0 ** -9
+    c[-1, 9] = 2.0 ** 128 * (1 - 2.0 ** -8)                          # the largest bf16
+    c = c.float().to(torch.bfloat16)
+    assert c.isfinite().all()
+    T = c.shape[0]
+    desc = fs.make_latent_cache(T, 1, "fp8")
+    buf = fs.latent_cache_empty(desc)
+    slots, kr = torch.arange(T, device=DEV), randn(g, (T, 64))
+    fs.fs_latent_cache_write(desc, c, kr, slots, buf)
+    cb, kb = torch.empty_like(c), torch.empty_like(kr)
+    fs.fs_latent_cache_read(desc, buf, slots, cb, kb)
+    _no_dev_error()
+    want, _ = ref.fp8_rows(c)
+    want = torch.where(want.abs() >= 2.0 ** 128, want.sign() * math.inf, want)
+    assert want.isinf().sum() == 1 and torch.equal(cb.double(), want) and torch.equal(kb, kr)
