@@ -595,7 +595,10 @@ fs_status fs_latent_cache_read(const fs_latent_cache* desc, const void* cache, i
  * sees no position gives out = 0, lse = -inf.  A length outside [0, max_pages
  * page_size] or above 2^31 - 257 (that sequence counts as empty) or a page
  * outside [0, n_pages) (its positions are left out) sets the device error word
- * (code 5).  n_q 1 .. 16, scale > 0, n_pages page_size < 2^31.  The length is
+ * (code 5).  What lies in records outside a sequence, NaN included, does not reach
+ * it; a NaN or an infinity in one of its records may reach all its n_q x heads rows,
+ * those that do not see that position too (it meets p = 0 in the second product); one
+ * in a query stays in its row.  n_q 1 .. 16, scale > 0, n_pages page_size < 2^31.  The length is
  * split over the SMs and joined in a fixed order: results do not depend on
  * timing.  (A wait in the kernel ends after 2 s with code 3; one sequence of more
  * than 10^8 positions with 2,048 query rows would come near that.)
@@ -611,9 +614,11 @@ fs_status fs_latent_decode(const fs_latent_cache* desc, int32_t heads, int32_t B
  * (device int32 [n_seqs + 1], non-decreasing; either may be empty).  causal:
  * the last query sees the last key (query i of lq sees keys 0 .. lk - lq + i),
  * so more keys than queries is a cached prefix.  scale > 0; Tq and Tk at most
- * 2^29.  What lies in rows
- * outside a sequence, NaN included, does not reach it; a NaN in one of its keys or
- * values may reach all its queries, those that do not see that key too. */
+ * 2^29.  What lies in rows outside a sequence, NaN included, does not reach it.
+ * Inside a sequence a masked pair enters the products as 0, so a NaN or an infinity
+ * of one of its keys or values may reach all its queries, those that do not see
+ * that key too, and in the gradient one of a query's q or d_out all its keys'
+ * gradients. */
 typedef struct {
     int32_t heads, n_seqs, Tq, Tk;
     int32_t causal;

@@ -153,3 +153,40 @@ def test_fp8_cache_over_the_whole_exponent_range():
     want, _ = ref.fp8_rows(c)
     want = torch.where(want.abs() >= 2.0 ** 128, want.sign() * math.inf, want)
     assert want.isinf().sum() == 1 and torch.equal(cb.double(), want) and torch.equal(kb, kr)
+
+
+@pytest.mark.parametrize("cache", ["bf16", "fp8"])
+@pytest.mark.parametrize("H,n_q", [(16, 2), (64, 1), (128, 1), (128, 2)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_decode_nan_and_infinity_stay_in_their_sequence(cache, H, n_q, value):
+    """NaN or infinity in the last record of two sequences and in a query row of a third: every other row keeps its
+    result bit for bit (the blocks that hold them hold other sequences too)."""
+    lens = [40 + (29 * i) % 150 for i in range(400)]
+    p = Decode(H, lens, n_q, 16, cache)
+    p.run()
+    _no_dev_error()
+    p.check()
+    keep, lse = p.out.clone(), p.lse.clone()
+    bad = [5, 333]
+    for b in bad:
+        last = lens[b] - 1
+        rec = p.cache.view(-1, p.cache.shape[-1])[int(p.table[b, last // 16]) * 16 + last % 16]
+        if cache == "bf16":
+            rec[:512:3] = value
+        else:
+            rec[:512:3] = 0x7F                                       # E4M3 has NaN only
+            if math.isinf(value):
+                rec[640:644].view(torch.float32).fill_(value)        # the scale
+    p.ql[77 * n_q, H // 2, 11] = value
+    p.out.fill_(SENTINEL)
+    p.lse.fill_(SENTINEL)
+    p.run()
+    _no_dev_error()
+    same = torch.ones(p.out.shape[:2], dtype=torch.bool, device=DEV)
+    for b in bad:
+        same[b * n_q:(b + 1) * n_q] = False
+    same[77 * n_q, H // 2] = False
+    assert torch.equal(p.out[same], keep[same]) and torch.equal(p.lse[same], lse[same])
+    newest = torch.stack([p.out[b * n_q + n_q - 1, :, :512] for b in bad])
+    assert not newest.isfinite().all(-1).any()                       # the rows that see the record show it
+    assert not p.out[77 * n_q, H // 2, :512].isfinite().all()
