@@ -499,7 +499,9 @@ fs_status fs_farskip_stack_backward(const fs_layer_desc* desc, int32_t L, int32_
  * so a few new tokens attend over the cached c directly (absorbed form); the
  * per-head products with W_UK and W_UV are the caller's.  These widths are
  * fixed, heads 1 .. 128, activations bf16 (scores, softmax statistics and sums
- * fp32; probabilities enter the second product as bf16).
+ * fp32; probabilities enter the second product as bf16).  Scores past about 2^30 in
+ * magnitude are outside what fp32 resolves here: their own rounding passes the
+ * exponential's range, and such a row may come out as 0, infinity or NaN.
  *
  * Row operands are (pointer, row stride, head stride) in elements, the vector
  * itself contiguous: 16-byte aligned pointers, strides multiples of 16 bytes
