@@ -44,7 +44,7 @@ namespace dc {
 
 constexpr int TT = 64;                        // records per tile
 constexpr int ROWS = 64;                      // query rows per block
-constexpr int MAXP = 11;                      // ring stages (8 with 64 query rows, 11 with 16)
+constexpr int MAXP = 11;                      // ring stages: 11, 10, 7 with 16, 32, 64 query rows; FP8: 9, 8, 5
 constexpr int MAXRAW = 4;                     // FP8: raw stages (64 records x 128 codes, 8 KB)
 constexpr int CTRL = 6144;
 struct Shared {
@@ -492,7 +492,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tmTile, const __grid_constant_
     }
 }
 
-constexpr int kRanges = 152;                  // one block per SM
+constexpr int kRanges = 152;                  // ranges at most: a block per SM of the full part
 
 // Joins the partials of the sequences that range boundaries cut, in range order, a row on 8 / RB warps.  Block
 // (boundary, RB rows, row block): of the boundaries inside a sequence, the one before range s, the first joins; with
@@ -611,18 +611,21 @@ join_kernel(const LatentDecodeArgs a, const int rb_count, const int ranges, cons
 }
 
 // Up to 64 query rows: one block per range; more: CTA pairs, 128 rows each, as many ranges as there are pairs left.
+// A block takes an SM's whole shared memory and ranges are of equal length, so blocks beyond the device's `sms`
+// would be a second wave as long as the first.
 struct Shape { int rb, ranges, block_rows; };
-Shape shape(int H, int n_q) {
-    if (H * n_q <= ROWS) return Shape{1, kRanges, ROWS};
-    const int rb = (H * n_q + 2 * ROWS - 1) / (2 * ROWS);
-    return Shape{rb, kRanges / 2 / rb, 2 * ROWS};
+Shape shape(int H, int n_q, int sms) {
+    sms = sms < kRanges ? sms : kRanges;
+    if (H * n_q <= ROWS) return Shape{1, sms, ROWS};
+    const int rb = (H * n_q + 2 * ROWS - 1) / (2 * ROWS), ranges = sms / 2 / rb;
+    return Shape{rb, ranges > 0 ? ranges : 1, 2 * ROWS};
 }
 
 }  // namespace dc
 
-// Partials of at most two cut pieces per range and row block, their lse, the ranges' descriptions.
+// Partials of at most two cut pieces per range and row block, their lse, the ranges' descriptions; enough for any device.
 size_t latent_decode_ws_bytes(int H, int, int n_q) {
-    const dc::Shape s = dc::shape(H, n_q);
+    const dc::Shape s = dc::shape(H, n_q, dc::kRanges);
     const size_t slots = static_cast<size_t>(s.rb) * s.ranges * 2;
     return slots * s.block_rows * (kLatent + 1) * 4 + (s.ranges * sizeof(dc::Meta) + 255) / 256 * 256;
 }
@@ -632,12 +635,15 @@ cudaError_t launch_latent_decode(const LatentDecodeArgs& a, bool fp8, void* ws, 
     using Fn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, LatentDecodeArgs, int, float*, float*, dc::Meta*);
     static const Fn fns[2][3] = {{dc::decode_kernel<false, 16>, dc::decode_kernel<false, 32>, dc::decode_kernel<false, 64>},
                                  {dc::decode_kernel<true, 16>, dc::decode_kernel<true, 32>, dc::decode_kernel<true, 64>}};
-    const dc::Shape sp = dc::shape(a.H, a.n_q);
+    int sms = 0;
+    cudaError_t e = num_sms(&sms);
+    if (e != cudaSuccess) return e;
+    const dc::Shape sp = dc::shape(a.H, a.n_q, sms);
     const int all = a.H * a.n_q, rows = all < sp.block_rows ? all : sp.block_rows;
     CUtensorMap tile, run, row;
     const long long records = a.n_pages * a.page_size;
     const int cols = fp8 ? kRecFp8 : kLatent + kRope;          // elements of a record (FP8: bytes)
-    cudaError_t e = make_map(&tile, a.cache, records, cols, dc::TT, fp8);
+    e = make_map(&tile, a.cache, records, cols, dc::TT, fp8);
     if (e == cudaSuccess) e = make_map(&run, a.cache, records, cols, 16, fp8);
     if (e == cudaSuccess) e = make_map(&row, a.cache, records, cols, 1, fp8);
     if (e != cudaSuccess) return e;
