@@ -8,8 +8,9 @@
 // leave as one 16-byte store, and nothing is read twice; the 32 lanes carry the 32
 // rotated pairs, one sine and cosine each.  A lane's frequency stays in a register
 // over the warp's tokens (a lane-dependent read of the parameter bank is 32 reads).
-// Measured, 65,533 tokens, FP8: written in 27.0 us (4.4 TB/s; 40.5 with eight lanes
-// rotating four pairs each), read in 21.5 us (5.5 TB/s).
+// Measured, 65,533 tokens, FP8: written in 27.2 us (4.4 TB/s; 40.5 with eight lanes
+// rotating four pairs each), read in 21.4 us (5.5 TB/s).  A writing warp asks for its next
+// two tokens only when these are stored, so its loads stand still meanwhile.
 #include "kernels.h"
 #include "latent.cuh"
 

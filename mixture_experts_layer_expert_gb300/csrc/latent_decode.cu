@@ -20,7 +20,7 @@
 // records are 73.7 KB (bf16) or 42 KB (FP8), 3,150 or 1,790 cycles of one SM's
 // share of the memory bandwidth; the MMAs take 36 x 36 + 16 x 52 = 2,130 cycles for 16
 // rows, 36 x 60 + 16 x 75 = 3,360 for 64.  Measured: 256 sequences of up to 8,191 tokens
-// x 16 heads on an FP8 cache 223 us (3.1 TB/s; 3,400 cycles a tile, the chain of
+// x 16 heads on an FP8 cache 223 us (3.2 TB/s; 3,400 cycles a tile, the chain of
 // conversion, scores, softmax and P C over the 2.25 tiles that the ring holds: faster
 // conversion, an earlier release of the raw stages or one wait for all four stages did
 // not shorten it); one sequence of 4,097 tokens x 16 heads, join included, 26.6 us.
@@ -62,7 +62,8 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= CTRL, "control area");
 
-// FP8: warps that turn codes into bf16 (four where 64 rows need the registers).
+// FP8: warps that turn codes into bf16 (four where 64 rows need the registers; their 384 threads leave 168
+// a thread, and 456 bytes are spilled).
 template <bool FP8, int RN> constexpr int kConv = FP8 ? (RN == 64 ? 4 : 8) : 0;
 template <bool FP8, int RN> constexpr int kThreads = 32 * (8 + kConv<FP8, RN>);
 

@@ -15,8 +15,8 @@
 //
 // Bound: with 128 rows a record's 139 k multiply-adds meet its 1,152 bytes at about the balance of tensor
 // rate and memory; here the MMAs' fixed costs decide.  Measured: 64 sequences of 2,000 to 14,000 tokens x 128
-// heads, bf16 cache, 164 us (850 TFLOP/s, 3.6 TB/s of records; on blocks of 64 rows it was 388 us); 32 sequences x
-// 128 heads x 2 new tokens, FP8 cache, 149 us.
+// heads, bf16 cache, 164 us (890 TFLOP/s, 3.8 TB/s; on blocks of 64 rows it was 388 us); 32 sequences x
+// 128 heads x 2 new tokens, FP8 cache, 149 us (its 512 threads leave 128 registers: 20 bytes are spilled).
 //
 // Per CTA: warps 0-3 softmax, rescaling and output (thread = row of the lane and half of the records);
 // warp 4 MMA issue in the even CTA, in the odd one it tells the even CTA which stages have

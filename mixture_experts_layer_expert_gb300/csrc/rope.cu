@@ -9,7 +9,10 @@
 // more threads, cost 12.3 us instead of 10.6 for 1,024 tokens x 128 heads x 64); neighbouring threads
 // cover neighbouring vectors, then neighbouring heads, so every warp access is
 // whole 128-byte lines when the heads are contiguous.  Measured: 65,536 tokens x 32
-// heads x 128, bf16, 170 us (6.3 TB/s, 0.93 of a copy's rate).
+// heads x 128, bf16, 170 us (6.3 TB/s, 0.93 of a copy's rate).  x and y may be the same,
+// so a thread's next load stays behind its last store: its eight heads are eight round
+// trips in turn.  Where all threads fit the SMs at once (the 1,024 tokens above: 131,072
+// threads, 2.1 MB in flight) these latencies, not the traffic's 5 us, are most of the time.
 #include "kernels.h"
 #include "latent.cuh"
 
