@@ -24,11 +24,11 @@
  *     the kernel records a code in the library's device error word and skips
  *     the work; fs_get_error() reads and clears it.
  *   - Row-major layouts throughout.  Activations are [rows, d] in the
- *     activation type: bf16 for FS_BF16, FS_FP8 and FS_MXFP8, fp32 for FS_F32 (the
- *     FP8 paths' E4M3 operands live inside the expert steps, see FS_FP8); gate weights and
+ *     activation type: bf16 for FS_BF16, FS_FP8, FS_MXFP8 and FS_MXFP4, fp32 for FS_F32 (the
+ *     quantised paths' operands live inside the expert steps, see FS_FP8); gate weights and
  *     logits are fp32; indices int32.
  *   - Pointers must be 16-byte aligned; d and c must be multiples of 64;
- *     n_shared * c_shared must be a multiple of 64 (FS_FP8, FS_MXFP8: d, c and c_shared
+ *     n_shared * c_shared must be a multiple of 64 (FS_FP8, FS_MXFP8, FS_MXFP4: d, c and c_shared
  *     multiples of 128).  Otherwise FS_ERR_UNSUPPORTED.
  *   - Workspace: `ws` is caller-owned device scratch of at least
  *     fs_workspace_bytes(desc, L) bytes (L = 0 for the single-step calls),
@@ -80,7 +80,15 @@ typedef enum {
  * block_scale).  The stored bf16 hidden h is quantised in blocks of 32 by the
  * gate/up GEMM itself.  Dispatch pads each expert's segment to a multiple of
  * 128 rows (see fs_dispatch).  d, c, c_shared multiples of 128. */
-typedef enum { FS_BF16 = 0, FS_F32 = 1, FS_FP8 = 2, FS_MXFP8 = 3 } fs_dtype;
+/* FS_MXFP4: the MX path with 4-bit elements: E2M1 codes (0, 0.5, 1, 1.5, 2, 3,
+ * 4, 6 and a sign), two in a byte with the even element in the low nibble, one
+ * UE8M0 scale 2^e per 32, e the smallest integer with max |x_i| 2^-e <= 6
+ * (clamped to -127), codes nearest with ties to even (kind::mxf4, at twice
+ * E4M3's rate and half its bytes).  Everything said of FS_MXFP8 holds for it,
+ * with fs_mx4_rows_bytes matrices.  E2M1 has no NaN and no infinity: a block
+ * that holds one gets the scale byte 255 (NaN), so that the products of its row
+ * are NaN. */
+typedef enum { FS_BF16 = 0, FS_F32 = 1, FS_FP8 = 2, FS_MXFP8 = 3, FS_MXFP4 = 4 } fs_dtype;
 
 /* Gate rule s() applied to the top-k logits z (after the optional bias):
  *   SOFTMAX         w_s = exp(z_s) / sum over ALL experts of exp(z_j)
@@ -117,8 +125,8 @@ typedef enum {
  * Every call validates it first: T, d, E, k, c >= 1, k <= E, n_shared >= 0 and
  * c_shared >= 1 when n_shared > 0, else FS_ERR_INVALID_ARG (an empty batch,
  * T = 0, is such an error: the caller skips the call); d, c, c_shared multiples
- * of 64 (128 for FS_FP8 and FS_MXFP8), E <= 512, k <= 16 and T k < 2^31 - 1024
- * (FS_MXFP8: T k + 127 E + 128 < 2^31 - 1024), else FS_ERR_UNSUPPORTED. */
+ * of 64 (128 for FS_FP8, FS_MXFP8 and FS_MXFP4), E <= 512, k <= 16 and T k < 2^31 - 1024
+ * (FS_MXFP8, FS_MXFP4: T k + 127 E + 128 < 2^31 - 1024), else FS_ERR_UNSUPPORTED. */
 typedef struct {
     int32_t T, d, E, k, c, n_shared, c_shared;
     int32_t dtype;   /* fs_dtype */
@@ -164,8 +172,11 @@ size_t fs_workspace_bytes_attn(const fs_layer_desc* desc, int L);
  *         128 elements of K, byte (r / 128) 512 + (r % 32) 16 + ((r % 128) / 32) 4 + b
  *         holds the scale of tile row r, block b (0..3) of those 128 elements
  *         (rows past N: 127, a unit scale).
+ *   MXFP4: the codes tiled [G][ceil(N/256)][ceil(K/256)][256][128 bytes], 256
+ *         elements of K per 128 bytes (rows past N and elements past K zero),
+ *         then the block scales as for MXFP8.
  * fs_packed_bytes gives the size (0 for invalid arguments; K % 64 == 0, FP8:
- * K % 128 == 0, MXFP8: K and N multiples of 128). */
+ * K % 128 == 0, MXFP8: K and N multiples of 128, MXFP4: K of 128, N of 8). */
 size_t fs_packed_bytes(int32_t G, int32_t N, int32_t K, int32_t dtype);
 
 /* Gate/up: the page's W1 (up) and W2 (gate), each [G, c, d], as one packed
@@ -178,7 +189,8 @@ fs_status fs_pack_w13(int32_t G, int32_t c, int32_t d, int32_t dtype,
                       const void* w1, const void* w2, void* w13, void* stream);
 
 /* Down: the page's W3 [G, d, c] as a packed [G, N = d, K = c] matrix
- * (fs_packed_bytes(G, d, c, dtype) bytes). */
+ * (fs_packed_bytes(G, d, c, dtype) bytes).  FS_MXFP4 with G = 1 and d any multiple
+ * of 8 packs the weight of fs_linear_mx4 (N = d, K = c). */
 fs_status fs_pack_w3(int32_t G, int32_t d, int32_t c, int32_t dtype, const void* w3, void* w3p,
                      void* stream);
 
@@ -220,8 +232,30 @@ size_t fs_mx_rows_bytes(int64_t rows, int32_t cols);
  * cols % 128 == 0. */
 fs_status fs_quantize_rows_mx(int64_t rows, int32_t cols, const void* x, void* q, void* stream);
 
+/* 4-bit MX matrix [rows, cols]: rows128 rows of cols / 2 bytes of E2M1 codes,
+ * then from byte offset rows128 * cols / 2 rounded up to a multiple of 256 the
+ * block scales in the chunks of an MX matrix.  Its size in bytes, or 0 for
+ * rows < 1 or cols not a positive multiple of 128. */
+size_t fs_mx4_rows_bytes(int64_t rows, int32_t cols);
+
+/* Quantise bf16 rows x [rows, cols] to the 4-bit MX matrix q (see FS_MXFP4; the
+ * rows up to rows128 get zero codes and unit scales).  cols % 128 == 0;
+ * rows < 2^31 - 1024. */
+fs_status fs_quantize_rows_mx4(int64_t rows, int32_t cols, const void* x, void* q, void* stream);
+
+/* Dense product in 4 bits: y [rows, N] = q w^T (fp32 accumulate, rounded once),
+ * q a 4-bit MX matrix [rows, K] (fs_quantize_rows_mx4), w the FS_MXFP4 pack of a
+ * weight [N, K] (fs_pack_w3 with G = 1), y bf16 or fp32 (y_dtype) with row stride
+ * y_row >= N elements, a multiple of 16 bytes.  For the projections around the
+ * layer (queries, the latent's expansions, the output).  K % 128 == 0, N % 8 == 0,
+ * rows < 2^31 - 1024.  Elements of y between N and y_row are left as they were.
+ * ws: fs_linear_mx4_ws_bytes bytes (0 for invalid sizes), 256-byte aligned. */
+size_t fs_linear_mx4_ws_bytes(int64_t rows, int32_t N, int32_t K);
+fs_status fs_linear_mx4(int64_t rows, int32_t N, int32_t K, const void* q, const void* w, void* y, int32_t y_dtype,
+                        int64_t y_row, void* ws, size_t ws_bytes, void* stream);
+
 /* Rows of fs_dispatch's x_perm and of fs_grouped_swiglu's y_perm for desc:
- * T k, or for FS_MXFP8 (128-row aligned expert segments) T k + 127 E rounded
+ * T k, or for FS_MXFP8 and FS_MXFP4 (128-row aligned expert segments) T k + 127 E rounded
  * up to a multiple of 128.  0 for an invalid desc. */
 int64_t fs_dispatch_rows(const fs_layer_desc* desc);
 

@@ -76,6 +76,9 @@ int cuda_error_status(cudaError_t e) { return cuda_status(e); }
         if (e_ != cudaSuccess) return cuda_status(e_); \
     } while (0)
 
+// Rows of a 4-bit MX matrix: tile row numbers and their ends stay inside an int.
+constexpr int64_t kMaxMx4Rows = 0x7fffffffLL - 1024;
+
 // ------------------------------------------------------------- validation
 static inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 static inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -84,31 +87,33 @@ static fs_status check_desc(const fs_layer_desc* d) {
     if (!d) return FS_ERR_INVALID_ARG;
     if (d->T < 1 || d->d < 1 || d->E < 1 || d->k < 1 || d->c < 1 || d->n_shared < 0) return FS_ERR_INVALID_ARG;
     if (d->k > d->E) return FS_ERR_INVALID_ARG;
-    if (d->dtype != FS_BF16 && d->dtype != FS_F32 && d->dtype != FS_FP8 && d->dtype != FS_MXFP8)
-        return FS_ERR_INVALID_ARG;
+    if (d->dtype < FS_BF16 || d->dtype > FS_MXFP4) return FS_ERR_INVALID_ARG;
     if (d->gate < FS_GATE_SOFTMAX || d->gate > FS_GATE_SIGMOID_NORM) return FS_ERR_INVALID_ARG;
     if (d->n_shared > 0 && d->c_shared < 1) return FS_ERR_INVALID_ARG;
     if (d->d % 64 || d->c % 64) return FS_ERR_UNSUPPORTED;
     if (d->n_shared > 0 && d->c_shared % 64) return FS_ERR_UNSUPPORTED;
-    if ((d->dtype == FS_FP8 || d->dtype == FS_MXFP8) &&
+    if ((d->dtype == FS_FP8 || d->dtype == FS_MXFP8 || d->dtype == FS_MXFP4) &&
         (d->d % 128 || d->c % 128 || (d->n_shared > 0 && d->c_shared % 128)))
         return FS_ERR_UNSUPPORTED;
     if (d->E > kMaxExperts || d->k > kMaxTopK) return FS_ERR_UNSUPPORTED;
     const long long rows = static_cast<long long>(d->T) * d->k;
     if (rows > 0x7fffffffLL - 1024) return FS_ERR_UNSUPPORTED;
     // MX: the 128-row-padded expert segments must fit the same bound
-    if (d->dtype == FS_MXFP8 && rows + 127LL * d->E + 128 > 0x7fffffffLL - 1024) return FS_ERR_UNSUPPORTED;
+    if ((d->dtype == FS_MXFP8 || d->dtype == FS_MXFP4) && rows + 127LL * d->E + 128 > 0x7fffffffLL - 1024) return FS_ERR_UNSUPPORTED;
     return FS_OK;
 }
 
-// Activations (GEMM inputs u_k, y_perm, u_next) are bf16 for FS_BF16, FS_FP8
-// and FS_MXFP8 (whose expert operands are quantised inside the path), fp32 for
+// Activations (GEMM inputs u_k, y_perm, u_next) are bf16 for FS_BF16, FS_FP8,
+// FS_MXFP8 and FS_MXFP4 (whose expert operands are quantised inside the path), fp32 for
 // FS_F32.
 static inline int elem_bytes(const fs_layer_desc* d) { return d->dtype == FS_F32 ? 4 : 2; }
 static inline int act_dtype(const fs_layer_desc* d) { return d->dtype == FS_F32 ? FS_F32 : FS_BF16; }
 static inline bool is_fp8(const fs_layer_desc* d) { return d->dtype == FS_FP8; }
-static inline bool is_mx(const fs_layer_desc* d) { return d->dtype == FS_MXFP8; }
-static inline int qmode(const fs_layer_desc* d) { return is_fp8(d) ? kQuantRow : (is_mx(d) ? kQuantMx : kQuantNone); }
+static inline bool is_mx4(const fs_layer_desc* d) { return d->dtype == FS_MXFP4; }
+static inline bool is_mx(const fs_layer_desc* d) { return d->dtype == FS_MXFP8 || is_mx4(d); }
+static inline int qmode(const fs_layer_desc* d) {
+    return is_fp8(d) ? kQuantRow : (is_mx4(d) ? kQuantMx4 : (is_mx(d) ? kQuantMx : kQuantNone));
+}
 // Rows of x_perm / y_perm: T k, or with the MX path's 128-row-aligned expert
 // segments T k + 127 E rounded up to 128.
 static inline long long perm_rows(const fs_layer_desc* d) {
@@ -144,14 +149,14 @@ static Layout layout(const fs_layer_desc* d, int L) {
     const bool f8 = is_fp8(d), mxq = is_mx(d);
     const long long prow = perm_rows(d);
     // MX: the hidden goes straight from the gate/up epilogue into an MX matrix
-    l.h_r = take(mxq ? mx_rows_bytes(prow, d->c) : rows * d->c * es);
+    l.h_r = take(mxq ? mx_rows_bytes(is_mx4(d), prow, d->c) : rows * d->c * es);
     l.hq_r = take(f8 ? fp8_rows_bytes(static_cast<long long>(rows), d->c) : 0);   // FP8: quantised h
     l.plan_s = take(4 * sizeof(int));
     l.plan_s2 = take(4 * sizeof(int));
-    l.h_s = take(mxq ? (cw ? mx_rows_bytes(static_cast<long long>(T), static_cast<int>(cw)) : 0) : T * cw * es);
+    l.h_s = take(mxq ? (cw ? mx_rows_bytes(is_mx4(d), static_cast<long long>(T), static_cast<int>(cw)) : 0) : T * cw * es);
     l.hq_s = take(f8 && cw ? fp8_rows_bytes(static_cast<long long>(T), static_cast<int>(cw)) : 0);
     l.uq = take(f8 && cw ? fp8_rows_bytes(static_cast<long long>(T), d->d)
-                         : (mxq && cw ? mx_rows_bytes(static_cast<long long>(T), d->d) : 0));   // quantised u_k
+                         : (mxq && cw ? mx_rows_bytes(is_mx4(d), static_cast<long long>(T), d->d) : 0));   // quantised u_k
     l.plan_a = take(4 * sizeof(int));
     l.end0 = o;
     l.topk_idx = take(rows * 4);
@@ -161,7 +166,7 @@ static Layout layout(const fs_layer_desc* d, int L) {
     l.pos = take(rows * 4);
     l.perm = take(static_cast<size_t>(perm_rows(d)) * 4);
     l.x_perm = take(f8 ? fp8_rows_bytes(static_cast<long long>(rows), d->d)
-                       : (mxq ? mx_rows_bytes(prow, d->d) : rows * dm * es));
+                       : (mxq ? mx_rows_bytes(is_mx4(d), prow, d->d) : rows * dm * es));
     l.y_perm = take(static_cast<size_t>(prow) * dm * es);
     l.s_out = take(cw ? T * dm * 4 : 0);     // S in fp32
     // The residual stream between blocks is fp32; the last block writes the
@@ -211,7 +216,7 @@ static OverlapLayout layout_overlap(const fs_layer_desc* d, int L) {
         l.pos[i] = on ? take(rows * 4) : 0;
         l.perm[i] = on ? take(static_cast<size_t>(prow) * 4) : 0;
         l.x_perm[i] = on ? take(is_fp8(d) ? fp8_rows_bytes(static_cast<long long>(rows), d->d)
-                                          : (is_mx(d) ? mx_rows_bytes(prow, d->d) : rows * dm * es))
+                                          : (is_mx(d) ? mx_rows_bytes(is_mx4(d), prow, d->d) : rows * dm * es))
                          : 0;
         l.s_out[i] = on ? take(T * dm * 4) : 0;
         l.ostar[i] = on ? take(T * dm * 4) : 0;
@@ -305,14 +310,15 @@ static fs_status swiglu_impl(const fs_layer_desc* d, const void* x, long long x_
         // groups start at multiples of 128; the hidden is written as an MX matrix
         const long long xr = mx_rows128(x_rows);
         const int max_mt = ceil_div(xr, 128) + G;
-        const uint8_t* xs = static_cast<const uint8_t*>(x) + mx_sf_offset(xr, d->d);
+        const bool f4 = is_mx4(d);
+        const uint8_t* xs = static_cast<const uint8_t*>(x) + mx_sf_offset(f4, xr, d->d);
         uint8_t* hc = static_cast<uint8_t*>(h);
-        uint8_t* hs = hc + mx_sf_offset(xr, cw);
+        uint8_t* hs = hc + mx_sf_offset(f4, xr, cw);
         FS_TRY(launch_plan(offsets, G, offsets ? static_cast<int>(xr) : rows, 128, plan, st));
-        FS_TRY(launch_mx_gemm(EPI_SWIGLU, x, xr, xs, w13, packed_sf_mx(w13, G, 2 * cw, d->d), G, 2 * cw, d->d, plan,
-                              max_mt, hc, cw, cw, hs, st));
-        FS_TRY(launch_mx_gemm(y_f32 ? EPI_F32 : EPI_BF16, hc, xr, hs, w3, packed_sf_mx(w3, G, d->d, cw), G, d->d, cw,
-                              plan, max_mt, y, d->d, d->d, nullptr, st));
+        FS_TRY(launch_mx_gemm(f4, EPI_SWIGLU, x, xr, xs, w13, packed_sf_mx(f4, w13, G, 2 * cw, d->d), G, 2 * cw, d->d,
+                              plan, rows, max_mt, hc, mx_row_bytes(f4, cw), cw, hs, st));
+        FS_TRY(launch_mx_gemm(f4, y_f32 ? EPI_F32 : EPI_BF16, hc, xr, hs, w3, packed_sf_mx(f4, w3, G, d->d, cw), G, d->d,
+                              cw, plan, rows, max_mt, y, d->d, d->d, nullptr, st));
     } else if (is_fp8(d)) {
         const int bm = tc_block_m_f8();
         const int max_mt = ceil_div(rows, bm) + G;
@@ -383,7 +389,7 @@ static fs_status shared_impl(const fs_layer_desc* d, const void* u, const void* 
         if (!u_q_ready) FS_TRY(launch_quant_rows(u, d->T, d->d, at<void>(ws, l.uq), st));
     } else if (is_mx(d)) {
         x = at<void>(ws, l.uq);
-        if (!u_q_ready) FS_TRY(launch_quant_rows_mx(u, d->T, d->d, at<void>(ws, l.uq), st));
+        if (!u_q_ready) FS_TRY(launch_quant_rows_mx(is_mx4(d), u, d->T, d->d, at<void>(ws, l.uq), st));
     }
     return swiglu_impl(d, x, d->T, nullptr, d->T, nullptr, 1, d->n_shared * d->c_shared, w13s, w3s, s_out, true,
                        at<int>(ws, l.plan_s), at<void>(ws, l.h_s), at<void>(ws, l.hq_s), st, nullptr, cmb,
@@ -478,19 +484,20 @@ size_t fs_workspace_bytes_overlap(const fs_layer_desc* desc, int L) {
     return layout_overlap(desc, L).end;
 }
 
-static inline bool valid_dtype(int32_t t) { return t == FS_BF16 || t == FS_F32 || t == FS_FP8 || t == FS_MXFP8; }
+static inline bool valid_dtype(int32_t t) { return t >= FS_BF16 && t <= FS_MXFP4; }
+static inline bool mx_dtype(int32_t t) { return t == FS_MXFP8 || t == FS_MXFP4; }
 
 fs_status fs_pack_w13(int32_t G, int32_t c, int32_t d, int32_t dtype, const void* w1, const void* w2, void* w13,
                       void* stream) {
     if (G < 1 || c < 1 || d < 1 || !valid_dtype(dtype)) return FS_ERR_INVALID_ARG;
-    const int q = (dtype == FS_FP8 || dtype == FS_MXFP8) ? 128 : 64;
+    const int q = (dtype == FS_FP8 || mx_dtype(dtype)) ? 128 : 64;
     if (c % q || d % q) return FS_ERR_UNSUPPORTED;
     FS_CHECK(need(w1));
     FS_CHECK(need(w2));
     FS_CHECK(need(w13));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == FS_MXFP8)
-        FS_TRY(launch_pack_w13_mx(G, c, d, w1, w2, w13, st));
+    if (mx_dtype(dtype))
+        FS_TRY(launch_pack_w13_mx(dtype == FS_MXFP4, G, c, d, w1, w2, w13, st));
     else if (dtype == FS_FP8)
         FS_TRY(launch_pack_w13_fp8(G, c, d, w1, w2, w13, st));
     else
@@ -501,19 +508,21 @@ fs_status fs_pack_w13(int32_t G, int32_t c, int32_t d, int32_t dtype, const void
 size_t fs_packed_bytes(int32_t G, int32_t N, int32_t K, int32_t dtype) {
     if (G < 1 || N < 1 || K < 1 || K % 64 || !valid_dtype(dtype)) return 0;
     if (dtype == FS_FP8) return K % 128 ? 0 : packed_bytes_fp8(G, N, K);
-    if (dtype == FS_MXFP8) return (K % 128 || N % 128) ? 0 : packed_bytes_mx(G, N, K);
+    if (dtype == FS_MXFP8) return (K % 128 || N % 128) ? 0 : packed_bytes_mx(false, G, N, K);
+    if (dtype == FS_MXFP4) return (K % 128 || N % 8) ? 0 : packed_bytes_mx(true, G, N, K);
     return packed_bytes(G, N, K, dtype == FS_BF16 ? 2 : 4);
 }
 
 fs_status fs_pack_w3(int32_t G, int32_t d, int32_t c, int32_t dtype, const void* w3, void* w3p, void* stream) {
     if (G < 1 || c < 1 || d < 1 || !valid_dtype(dtype)) return FS_ERR_INVALID_ARG;
-    const int q = (dtype == FS_FP8 || dtype == FS_MXFP8) ? 128 : 64;
-    if (c % q || d % q) return FS_ERR_UNSUPPORTED;
+    const int q = (dtype == FS_FP8 || mx_dtype(dtype)) ? 128 : 64;
+    // a 4-bit pack also serves fs_linear_mx4, whose outputs are as few as 8
+    if (c % q || d % (dtype == FS_MXFP4 ? 8 : q)) return FS_ERR_UNSUPPORTED;
     FS_CHECK(need(w3));
     FS_CHECK(need(w3p));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == FS_MXFP8)
-        FS_TRY(launch_pack_w3_mx(G, d, c, w3, w3p, st));
+    if (mx_dtype(dtype))
+        FS_TRY(launch_pack_w3_mx(dtype == FS_MXFP4, G, d, c, w3, w3p, st));
     else if (dtype == FS_FP8)
         FS_TRY(launch_pack_w3_fp8(G, d, c, w3, w3p, st));
     else
@@ -524,13 +533,13 @@ fs_status fs_pack_w3(int32_t G, int32_t d, int32_t c, int32_t dtype, const void*
 fs_status fs_pack_w3_shared(int32_t n_shared, int32_t c_shared, int32_t d, int32_t dtype, const void* w3s,
                             void* w3cat, void* stream) {
     if (n_shared < 1 || c_shared < 1 || d < 1 || !valid_dtype(dtype)) return FS_ERR_INVALID_ARG;
-    const int q = (dtype == FS_FP8 || dtype == FS_MXFP8) ? 128 : 64;
+    const int q = (dtype == FS_FP8 || mx_dtype(dtype)) ? 128 : 64;
     if (c_shared % q || d % q) return FS_ERR_UNSUPPORTED;
     FS_CHECK(need(w3s));
     FS_CHECK(need(w3cat));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == FS_MXFP8)
-        FS_TRY(launch_pack_w3_shared_mx(n_shared, c_shared, d, w3s, w3cat, st));
+    if (mx_dtype(dtype))
+        FS_TRY(launch_pack_w3_shared_mx(dtype == FS_MXFP4, n_shared, c_shared, d, w3s, w3cat, st));
     else if (dtype == FS_FP8)
         FS_TRY(launch_pack_w3_shared_fp8(n_shared, c_shared, d, w3s, w3cat, st));
     else
@@ -554,7 +563,12 @@ fs_status fs_quantize_rows_fp8(int64_t rows, int32_t cols, const void* x, void* 
 
 size_t fs_mx_rows_bytes(int64_t rows, int32_t cols) {
     if (rows < 1 || cols < 1 || cols % 128) return 0;
-    return mx_rows_bytes(rows, cols);
+    return mx_rows_bytes(false, rows, cols);
+}
+
+size_t fs_mx4_rows_bytes(int64_t rows, int32_t cols) {
+    if (rows < 1 || cols < 1 || cols % 128) return 0;
+    return mx_rows_bytes(true, rows, cols);
 }
 
 fs_status fs_quantize_rows_mx(int64_t rows, int32_t cols, const void* x, void* q, void* stream) {
@@ -562,7 +576,48 @@ fs_status fs_quantize_rows_mx(int64_t rows, int32_t cols, const void* x, void* q
     if (cols % 128 || rows > 0x7fffffffLL) return FS_ERR_UNSUPPORTED;
     FS_CHECK(need(x));
     FS_CHECK(need(q));
-    FS_TRY(launch_quant_rows_mx(x, rows, cols, q, static_cast<cudaStream_t>(stream)));
+    FS_TRY(launch_quant_rows_mx(false, x, rows, cols, q, static_cast<cudaStream_t>(stream)));
+    return FS_OK;
+}
+
+fs_status fs_quantize_rows_mx4(int64_t rows, int32_t cols, const void* x, void* q, void* stream) {
+    if (rows < 1 || cols < 1) return FS_ERR_INVALID_ARG;
+    if (cols % 128 || rows > kMaxMx4Rows) return FS_ERR_UNSUPPORTED;
+    FS_CHECK(need(x));
+    FS_CHECK(need(q));
+    FS_TRY(launch_quant_rows_mx(true, x, rows, cols, q, static_cast<cudaStream_t>(stream)));
+    return FS_OK;
+}
+
+static fs_status check_linear_mx4(int64_t rows, int32_t N, int32_t K) {
+    if (rows < 1 || N < 1 || K < 1) return FS_ERR_INVALID_ARG;
+    if (K % 128 || N % 8 || rows > kMaxMx4Rows) return FS_ERR_UNSUPPORTED;
+    // the GEMM counts its 128 x 256 tiles in an int
+    if ((rows + 127) / 128 * ((static_cast<int64_t>(N) + 255) / 256) > 0x7fffffffLL - 1024) return FS_ERR_UNSUPPORTED;
+    return FS_OK;
+}
+
+size_t fs_linear_mx4_ws_bytes(int64_t rows, int32_t N, int32_t K) {
+    if (check_linear_mx4(rows, N, K) != FS_OK) return 0;
+    return 256;
+}
+
+fs_status fs_linear_mx4(int64_t rows, int32_t N, int32_t K, const void* q, const void* w, void* y, int32_t y_dtype,
+                        int64_t y_row, void* ws, size_t ws_bytes, void* stream) {
+    FS_CHECK(check_linear_mx4(rows, N, K));
+    if (y_dtype != FS_BF16 && y_dtype != FS_F32) return FS_ERR_INVALID_ARG;
+    FS_CHECK(need(q));
+    FS_CHECK(need(w));
+    FS_CHECK(need(y));
+    if (y_row < N) return FS_ERR_INVALID_ARG;
+    if (y_row % (y_dtype == FS_BF16 ? 8 : 4) || y_row > (int64_t(1) << 36)) return FS_ERR_UNSUPPORTED;
+    if (!ws) return FS_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < fs_linear_mx4_ws_bytes(rows, N, K)) return FS_ERR_WORKSPACE;
+    const long long r128 = mx_rows128(rows);
+    FS_TRY(launch_mx_gemm(true, y_dtype == FS_BF16 ? EPI_BF16 : EPI_F32, q, r128,
+                          static_cast<const uint8_t*>(q) + mx_sf_offset(true, rows, K), w, packed_sf_mx(true, w, 1, N, K), 1,
+                          N, K, nullptr, static_cast<int>(rows), static_cast<int>(r128 / 128), y, y_row, N, nullptr,
+                          static_cast<cudaStream_t>(stream)));
     return FS_OK;
 }
 

@@ -257,7 +257,8 @@ cudaError_t launch_dispatch(const int32_t* topk_idx, const void* u, int T, int d
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    dispatch_scan_kernel<<<1, 1024, 0, st>>>(scratch, nc, E, counts, offsets, qmode == kQuantMx ? 1 : 0);
+    dispatch_scan_kernel<<<1, 1024, 0, st>>>(scratch, nc, E, counts, offsets,
+                                             qmode == kQuantMx || qmode == kQuantMx4 ? 1 : 0);
     count_launch();
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
@@ -269,7 +270,8 @@ cudaError_t launch_dispatch(const int32_t* topk_idx, const void* u, int T, int d
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (!x_perm) return cudaSuccess;     // the caller gathers rows itself (no permuted copy)
-    if (qmode == kQuantMx) return launch_dispatch_copy_mx(u, T, d, k, pos, x_perm, rows_cap, u_q, st);
+    if (qmode == kQuantMx || qmode == kQuantMx4)
+        return launch_dispatch_copy_mx(qmode == kQuantMx4, u, T, d, k, pos, x_perm, rows_cap, u_q, st);
     if (fp8) {
         const long long rows = static_cast<long long>(T) * k;
         uint8_t* xq = static_cast<uint8_t*>(x_perm);

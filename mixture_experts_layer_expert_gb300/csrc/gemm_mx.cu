@@ -1,8 +1,8 @@
-// gemm_mx.cu -- persistent grouped GEMM on block-scaled FP8 operands (the MX
-// expert path): tcgen05.mma kind::mxf8f6f4.block_scale with E4M3 codes in
-// shared memory (TMA, 128-byte swizzle) and one UE8M0 scale per row per 32
-// elements of K for each operand, the scales copied into TMEM with tcgen05.cp
-// (layouts in mx.cuh).  fp32 accumulate in TMEM.
+// gemm_mx.cu -- persistent grouped GEMM on block-scaled operands (the MX expert
+// paths): E4M3 codes with tcgen05.mma kind::mxf8f6f4.block_scale, or E2M1 codes
+// (4 bits) with kind::mxf4.block_scale, in shared memory (TMA, 128-byte swizzle)
+// and one UE8M0 scale per row per 32 elements of K for each operand, the scales
+// copied into TMEM with tcgen05.cp (layouts in mx.cuh).  fp32 accumulate in TMEM.
 //
 // The grouped structure, warp roles, tile order and bounded waits are those of
 // gemm_tc.cu (one CTA per SM, 10 warps: TMA producer, MMA issuer, 8 epilogue
@@ -14,9 +14,13 @@
 //    store: the next tile's MMAs wait for that copy only.
 //  * every group's rows start at a multiple of 128 (the MX Dispatch pads each
 //    expert's segment), so an A tile's scales are one 512-byte chunk per stage.
-// One stage = 128 K elements: A 128 x 128 B + B 256 x 128 B of codes, 512 B of
-// A scales, 1 KB of B scales; per stage 4 MMAs of 128 x 256 x 32, MMA kk using
-// byte kk of each scale word (the 4 blocks of 32 of the stage).
+// One stage = 128 bytes of K: A 128 x 128 B + B 256 x 128 B of codes.
+//   E4M3: 128 elements, one chunk of scales (512 B of A, 1 KB of B); 4 MMAs of
+//         128 x 256 x 32, MMA kk using byte kk of each scale word.
+//   E2M1: 256 elements, two chunks; 4 MMAs of 128 x 256 x 64, MMA kk using bytes
+//         2 (kk & 1) and + 1 of chunk kk / 2.  K is a multiple of 128, so a row's
+//         last stage may be half full: it has one chunk and two MMAs (the codes
+//         behind it are zeros of the weight tile or of the TMA load's fill).
 //
 // Epilogues: EPI_SWIGLU writes the hidden h = SiLU(g) u rounded to bf16 and
 // quantised in blocks of 32 straight into an MX matrix (codes and scales: the
@@ -33,33 +37,42 @@ namespace mx {
 
 constexpr int BM = 128;
 constexpr int BN = 256;
-constexpr int BK = 128;                       // K elements (bytes) per stage
+constexpr int BK = 128;                       // bytes of K per stage
 constexpr int STAGES = 4;
 constexpr int A_STAGE = BM * BK;              // 16 KB
 constexpr int B_STAGE = BN * BK;              // 32 KB
 constexpr int STAGE_BYTES = A_STAGE + B_STAGE;
-constexpr int SFA_BYTES = 512;
-constexpr int SFB_BYTES = 1024;
-constexpr int SF_STAGE = SFA_BYTES + SFB_BYTES;
+constexpr int SFA_CHUNK = 512;                // scales of 128 rows x 4 blocks
+constexpr int SFB_CHUNK = 1024;               // of 256 rows x 4 blocks
 constexpr int SF_OFF = STAGES * STAGE_BYTES;                  // scale chunks after the code stages
-constexpr int BAR_OFF = SF_OFF + STAGES * SF_STAGE;
-constexpr int BAR_BYTES = 256;
-constexpr int PLAN_OFF = BAR_OFF + BAR_BYTES;
-constexpr int PIECE_OFF = (PLAN_OFF + 2 * (kMaxGroups + 1) * 4 + 1023) / 1024 * 1024;
-constexpr int PIECE_BYTES = 2048;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr size_t SMEM_BYTES = 1024 + PIECE_OFF + EPI_WARPS * PIECE_BYTES;
+constexpr int PIECE_BYTES = 2048;
+constexpr int BAR_BYTES = 256;
 constexpr int TMEM_COLS = 512;
 constexpr int SF_SLOTS = 8;                   // scale-factor slots in TMEM (a ring, two per smem stage)
-constexpr int SF_COL0 = BN;                   // slot j: A scales at SF_COL0 + 12 j (4 columns), B at + 4 (8)
+constexpr int SF_COL0 = BN;                   // slot j starts at SF_COL0 + SF_COLS j: A's columns, then B's
 constexpr int kGroupM = 16;
-static_assert(SMEM_BYTES <= 232448, "shared memory");
-static_assert(SF_COL0 + 12 * SF_SLOTS <= TMEM_COLS, "TMEM columns");
+
+// What differs between the two element formats.
+template <bool F4>
+struct Fmt {
+    static constexpr int CHUNKS = F4 ? 2 : 1;                 // scale chunks (128 elements) per stage
+    static constexpr int MAX_GROUPS = F4 ? kMaxExperts : kMaxGroups;   // the second chunk takes the room of half the plan
+    static constexpr int SF_STAGE = CHUNKS * (SFA_CHUNK + SFB_CHUNK);
+    static constexpr int SFA_BYTES = CHUNKS * SFA_CHUNK;
+    static constexpr int SF_COLS = CHUNKS * 12;               // TMEM columns per slot: 4 of A and 8 of B per chunk
+    static constexpr int BAR_OFF = SF_OFF + STAGES * SF_STAGE;
+    static constexpr int PLAN_OFF = BAR_OFF + BAR_BYTES;
+    static constexpr int PIECE_OFF = (PLAN_OFF + 2 * (MAX_GROUPS + 1) * 4 + 1023) / 1024 * 1024;
+    static constexpr size_t SMEM_BYTES = 1024 + PIECE_OFF + EPI_WARPS * PIECE_BYTES;
+    static_assert(SMEM_BYTES <= 232448, "shared memory");
+    static_assert(SF_COL0 + SF_COLS * SF_SLOTS <= TMEM_COLS, "TMEM columns");
+};
 
 struct Args {
-    const int* plan;          // [2 (G + 1)]: m-tile prefix, row starts (multiples of 128)
-    int G, N, K, n_tiles, max_mtiles;
+    const int* plan;          // [2 (G + 1)]: m-tile prefix, row starts (multiples of 128); null: one group of `rows` rows
+    int G, rows, N, K, n_tiles, max_mtiles;
     const uint8_t* a_sf;      // A scale chunks [rows128 / 128][K / 128][512]
     const uint8_t* b_sf;      // B scale chunks [G][n_tiles][K / 128][1024]
     void* out;
@@ -87,23 +100,35 @@ __device__ __forceinline__ void sf_copy(uint32_t taddr, uint32_t saddr) {
     asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// D (fp32, TMEM) (+)= (A * sA) (B * sB)^T, E4M3 codes with UE8M0 block scales.
+// D (fp32, TMEM) (+)= (A * sA) (B * sB)^T, E4M3 or E2M1 codes with UE8M0 block scales.
+template <bool F4>
 __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                        uint32_t sfb, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    if constexpr (F4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+                d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
 }
 
-// Instruction descriptor, kind::mxf8f6f4: B scale byte (bits 4-5), A and B
-// E4M3 (format 0 in bits 7-9, 10-12), K-major, N >> 3 (17-22), UE8M0 scales
-// (bit 23), M >> 4 (24-28), A scale byte (29-30).
+// Instruction descriptor: B scale byte (bits 4-5), A and B formats (bits 7-9,
+// 10-12: 0 = E4M3 of kind::mxf8f6f4, 1 = E2M1 of kind::mxf4), K-major, N >> 3
+// (17-22), UE8M0 scales (bit 23), M >> 4 (24-28), A scale byte (29-30).
+template <bool F4>
 __host__ __device__ constexpr uint32_t idesc_mx(int M, int N, int sf_id) {
-    return (static_cast<uint32_t>(sf_id) << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) |
-           (static_cast<uint32_t>(M >> 4) << 24) | (static_cast<uint32_t>(sf_id) << 29);
+    return (static_cast<uint32_t>(sf_id) << 4) | (F4 ? (1u << 7) | (1u << 10) : 0u) |
+           (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24) |
+           (static_cast<uint32_t>(sf_id) << 29);
 }
 
 struct Tile {
@@ -152,13 +177,14 @@ __device__ __forceinline__ void store_piece(const CUtensorMap* tmo, uint8_t* pie
     }
 }
 
-template <int EPI>
+template <int EPI, bool F4>
 __global__ void __launch_bounds__(THREADS, 1)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmO, const Args args) {
+    using F = Fmt<F4>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + F::BAR_OFF);
     uint64_t* full = bars;                 // [STAGES]
     uint64_t* empty = bars + STAGES;       // [STAGES]
     uint64_t* tfull = bars + 2 * STAGES;   // [1]
@@ -166,14 +192,20 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     uint64_t* fin = tempty + 1;            // [1]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(fin + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    int* mt_start = reinterpret_cast<int*>(smem + PLAN_OFF);
+    int* mt_start = reinterpret_cast<int*>(smem + F::PLAN_OFF);
     int* row_start = mt_start + (args.G + 1);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     const int G = args.G;
 
-    for (int i = threadIdx.x; i < 2 * (G + 1); i += THREADS) mt_start[i] = args.plan[i];
+    if (args.plan) {
+        for (int i = threadIdx.x; i < 2 * (G + 1); i += THREADS) mt_start[i] = args.plan[i];
+    } else if (threadIdx.x == 0) {
+        mt_start[0] = row_start[0] = 0;
+        mt_start[1] = (args.rows + BM - 1) / BM;
+        row_start[1] = args.rows;
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
@@ -200,7 +232,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         total_mtiles = 0;
     }
     const int total = total_mtiles * args.n_tiles;
-    const int num_kb = args.K / BK;
+    const int chunks = args.K / 128;                              // scale chunks along K
+    const int num_kb = (chunks + F::CHUNKS - 1) / F::CHUNKS;      // stages
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -213,18 +246,20 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             bool ok = true;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 const Tile tl = decode(t, mt_start, row_start, G, args.n_tiles);
-                const uint8_t* sfa = args.a_sf + static_cast<size_t>(tl.a_row / BM) * num_kb * SFA_BYTES;
-                const uint8_t* sfb = args.b_sf + (static_cast<size_t>(tl.g) * args.n_tiles + tl.n) * num_kb * SFB_BYTES;
+                const uint8_t* sfa = args.a_sf + static_cast<size_t>(tl.a_row / BM) * chunks * SFA_CHUNK;
+                const uint8_t* sfb = args.b_sf + (static_cast<size_t>(tl.g) * args.n_tiles + tl.n) * chunks * SFB_CHUNK;
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.err)) { ok = false; break; }
                     const uint32_t fb = smem_u32(&full[stage]);
-                    mbar_arrive_expect_tx(fb, STAGE_BYTES + SF_STAGE);
+                    const int nc = min(F::CHUNKS, chunks - kb * F::CHUNKS);
+                    mbar_arrive_expect_tx(fb, STAGE_BYTES + nc * (SFA_CHUNK + SFB_CHUNK));
                     uint8_t* sa = smem + stage * STAGE_BYTES;
-                    uint8_t* sf = smem + SF_OFF + stage * SF_STAGE;
+                    uint8_t* sf = smem + SF_OFF + stage * F::SF_STAGE;
                     tma_load_2d(smem_u32(sa), &tmA, fb, kb * BK, tl.a_row);
                     tma_load_3d(smem_u32(sa + A_STAGE), &tmB, fb, 0, 0, (tl.g * args.n_tiles + tl.n) * num_kb + kb);
-                    bulk_load(smem_u32(sf), sfa + static_cast<size_t>(kb) * SFA_BYTES, SFA_BYTES, fb);
-                    bulk_load(smem_u32(sf + SFA_BYTES), sfb + static_cast<size_t>(kb) * SFB_BYTES, SFB_BYTES, fb);
+                    bulk_load(smem_u32(sf), sfa + static_cast<size_t>(kb) * F::SFA_BYTES, nc * SFA_CHUNK, fb);
+                    bulk_load(smem_u32(sf + F::SFA_BYTES), sfb + static_cast<size_t>(kb) * F::CHUNKS * SFB_CHUNK,
+                              nc * SFB_CHUNK, fb);
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -257,18 +292,26 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, args.err)) { ok = false; break; }
                     tc_fence_after();
                     uint8_t* sa = smem + stage * STAGE_BYTES;
-                    const uint32_t sf = smem_u32(smem + SF_OFF + stage * SF_STAGE);
-                    const uint32_t tsa = tmem_base + SF_COL0 + 12u * slot;
-                    const uint32_t tsb = tsa + 4u;
-                    sf_copy(tsa, sf);                       // A: 128 rows x 4 blocks
-                    sf_copy(tsb, sf + SFA_BYTES);           // B rows 0..127
-                    sf_copy(tsb + 4u, sf + SFA_BYTES + 512u);   // B rows 128..255
+                    const uint32_t sf = smem_u32(smem + SF_OFF + stage * F::SF_STAGE);
+                    // chunk q: A's columns at tsa + 4 q, B's at tsb + 8 q (rows 0..127, then 128..255)
+                    const uint32_t tsa = tmem_base + SF_COL0 + static_cast<uint32_t>(F::SF_COLS) * slot;
+                    const uint32_t tsb = tsa + 4u * F::CHUNKS;
                     const uint64_t adesc = smem_desc_sw128(smem_u32(sa));
                     const uint64_t bdesc = smem_desc_sw128(smem_u32(sa + A_STAGE));
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_mx(tmem_base, adesc + 2ull * kk, bdesc + 2ull * kk, idesc_mx(BM, BN, kk), tsa, tsb,
-                               (kb > 0 || kk > 0) ? 1u : 0u);
+                    for (int q = 0; q < F::CHUNKS; ++q) {
+                        if (q > 0 && kb * F::CHUNKS + q >= chunks) break;
+                        sf_copy(tsa + 4u * q, sf + q * SFA_CHUNK);
+                        sf_copy(tsb + 8u * q, sf + F::SFA_BYTES + q * SFB_CHUNK);
+                        sf_copy(tsb + 8u * q + 4u, sf + F::SFA_BYTES + q * SFB_CHUNK + 512u);
+                        constexpr int MMAS = 4 / F::CHUNKS;
+#pragma unroll
+                        for (int j = 0; j < MMAS; ++j) {
+                            const int kk = q * MMAS + j;
+                            mma_mx<F4>(tmem_base, adesc + 2ull * kk, bdesc + 2ull * kk, idesc_mx<F4>(BM, BN, j * F::CHUNKS),
+                                       tsa + 4u * q, tsb + 8u * q, (kb > 0 || kk > 0) ? 1u : 0u);
+                        }
+                    }
                     tc_commit(smem_u32(&empty[stage]));
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                     slot = (slot + 1u) % SF_SLOTS;
@@ -288,7 +331,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const int quarter = warp & 3;
         const int half = (warp - 2) >> 2;          // which 128 columns of the tile
         const int r = quarter * 32 + lane;
-        uint8_t* piece = smem + PIECE_OFF + (warp - 2) * PIECE_BYTES;
+        uint8_t* piece = smem + F::PIECE_OFF + (warp - 2) * PIECE_BYTES;
         int it = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
             const Tile tl = decode(t, mt_start, row_start, G, args.n_tiles);
@@ -326,24 +369,30 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                             h[j] = __bfloat162float(__float2bfloat16_rn(silu_f(g) * u));
                             amax = fmaxf(amax, fabsf(h[j]));
                         }
-                        const MxQuant m = mx_quant(amax);
-                        uint32_t c[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            float a0, a1, a2, a3;
-                            if (!m.q.wide) {
-                                a0 = h[4 * j] * m.q.mult; a1 = h[4 * j + 1] * m.q.mult;
-                                a2 = h[4 * j + 2] * m.q.mult; a3 = h[4 * j + 3] * m.q.mult;
-                            } else {
-                                a0 = scaled_wide(h[4 * j], m.q.e); a1 = scaled_wide(h[4 * j + 1], m.q.e);
-                                a2 = scaled_wide(h[4 * j + 2], m.q.e); a3 = scaled_wide(h[4 * j + 3], m.q.e);
+                        if constexpr (F4) {
+                            const Mx4Quant m = mx4_quant(h);
+                            *reinterpret_cast<uint4*>(H + (hc0 + 32 * b) / 2) = mx4_codes32(h, m.mult);
+                            args.h_sf[mx_sf_byte(orow, (hc0 + 32 * b) / 32, args.out_cols)] = m.ue8m0;
+                        } else {
+                            const MxQuant m = mx_quant(amax);
+                            uint32_t c[8];
+    #pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                float a0, a1, a2, a3;
+                                if (!m.q.wide) {
+                                    a0 = h[4 * j] * m.q.mult; a1 = h[4 * j + 1] * m.q.mult;
+                                    a2 = h[4 * j + 2] * m.q.mult; a3 = h[4 * j + 3] * m.q.mult;
+                                } else {
+                                    a0 = scaled_wide(h[4 * j], m.q.e); a1 = scaled_wide(h[4 * j + 1], m.q.e);
+                                    a2 = scaled_wide(h[4 * j + 2], m.q.e); a3 = scaled_wide(h[4 * j + 3], m.q.e);
+                                }
+                                c[j] = cvt_e4m3x2(a0, a1) | (cvt_e4m3x2(a2, a3) << 16);
                             }
-                            c[j] = cvt_e4m3x2(a0, a1) | (cvt_e4m3x2(a2, a3) << 16);
+                            uint4* dst = reinterpret_cast<uint4*>(H + hc0 + 32 * b);
+                            dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
+                            dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
+                            args.h_sf[mx_sf_byte(orow, (hc0 + 32 * b) / 32, args.out_cols)] = m.ue8m0;
                         }
-                        uint4* dst = reinterpret_cast<uint4*>(H + hc0 + 32 * b);
-                        dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
-                        dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
-                        args.h_sf[mx_sf_byte(orow, (hc0 + 32 * b) / 32, args.out_cols)] = m.ue8m0;
                     }
                 }
             } else if constexpr (EPI == EPI_BF16) {
@@ -362,7 +411,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                         uint4* dst = reinterpret_cast<uint4*>(Y + orow * args.ldo + c_base + c0);
 #pragma unroll
                         for (int w = 0; w < 4; ++w)
-                            dst[w] = make_uint4(pk[4 * w], pk[4 * w + 1], pk[4 * w + 2], pk[4 * w + 3]);
+                            if (c_base + c0 + 8 * w < args.out_cols) dst[w] = make_uint4(pk[4 * w], pk[4 * w + 1], pk[4 * w + 2], pk[4 * w + 3]);
                     }
                 }
             } else {   // EPI_F32
@@ -393,23 +442,26 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 }  // namespace mx
 
 // ------------------------------------------------------------------- host
-template <int EPI>
+template <int EPI, bool F4>
 static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
-                                  const uint8_t* b_sf, int G, int N, int K, const int* plan, int max_mtiles, void* out,
+                                  const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles, void* out,
                                   long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
     static bool set_mx[kMaxDevices];
-    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(mx::mx_gemm_kernel<EPI>), mx::SMEM_BYTES, set_mx);
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(mx::mx_gemm_kernel<EPI, F4>), mx::Fmt<F4>::SMEM_BYTES, set_mx);
     if (e != cudaSuccess) return e;
-    if (K % 128 || N % 128 || a_rows % 128 || G < 1 || G > kMaxGroups) return cudaErrorInvalidValue;
+    if (K % 128 || N % (F4 ? 8 : 128) || a_rows % 128 || G < 1 || G > mx::Fmt<F4>::MAX_GROUPS) return cudaErrorInvalidValue;
+    const int row_bytes = F4 ? K / 2 : K;
+    const int stages = (row_bytes + mx::BK - 1) / mx::BK;      // the last one of a 4-bit row may be half full
     CUtensorMap ta, tb, to;
-    e = make_map(&ta, A, a_rows, K, 128, true);
+    e = make_map(&ta, A, a_rows, row_bytes, 128, true);
     if (e != cudaSuccess) return e;
     const int n_tiles = (N + mx::BN - 1) / mx::BN;
-    e = make_map_blocked(&tb, B, static_cast<long long>(G) * n_tiles * (K / 128), mx::BN, true);
+    e = make_map_blocked(&tb, B, static_cast<long long>(G) * n_tiles * stages, mx::BN, true);
     if (e != cudaSuccess) return e;
     mx::Args args;
     args.plan = plan;
     args.G = G;
+    args.rows = rows;
     args.N = N;
     args.K = K;
     args.n_tiles = n_tiles;
@@ -428,34 +480,44 @@ static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t
         if (e != cudaSuccess) return e;
         args.tma_out = 1;
     }
-    if (EPI == EPI_SWIGLU && (!h_sf || ldo < out_cols)) return cudaErrorInvalidValue;
+    if (EPI == EPI_SWIGLU && (!h_sf || ldo < (F4 ? out_cols / 2 : out_cols))) return cudaErrorInvalidValue;
     int sms = 0;
     e = num_sms(&sms);
     if (e != cudaSuccess) return e;
     const long long max_tiles = static_cast<long long>(max_mtiles) * n_tiles;
     int grid = static_cast<int>(max_tiles < sms ? max_tiles : sms);
     if (grid < 1) grid = 1;
-    mx::mx_gemm_kernel<EPI><<<grid, mx::THREADS, mx::SMEM_BYTES, st>>>(ta, tb, to, args);
+    mx::mx_gemm_kernel<EPI, F4><<<grid, mx::THREADS, mx::Fmt<F4>::SMEM_BYTES, st>>>(ta, tb, to, args);
     count_launch();
     return cudaGetLastError();
 }
 
-cudaError_t launch_mx_gemm(int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
-                           const uint8_t* b_sf, int G, int N, int K, const int* plan, int max_mtiles, void* out,
-                           long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
+template <bool F4>
+static cudaError_t launch_mx_fmt(int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
+                                 const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
+                                 void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
     switch (epi) {
         case EPI_SWIGLU:
-            return launch_mx_impl<EPI_SWIGLU>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, max_mtiles, out, ldo, out_cols,
-                                              h_sf, st);
+            return launch_mx_impl<EPI_SWIGLU, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+                                                  out_cols, h_sf, st);
         case EPI_BF16:
-            return launch_mx_impl<EPI_BF16>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, max_mtiles, out, ldo, out_cols,
-                                            h_sf, st);
+            return launch_mx_impl<EPI_BF16, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+                                                out_cols, h_sf, st);
         case EPI_F32:
-            return launch_mx_impl<EPI_F32>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, max_mtiles, out, ldo, out_cols,
-                                           h_sf, st);
+            return launch_mx_impl<EPI_F32, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+                                               out_cols, h_sf, st);
         default:
             return cudaErrorInvalidValue;
     }
+}
+
+cudaError_t launch_mx_gemm(bool f4, int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
+                           const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
+                           void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
+    return f4 ? launch_mx_fmt<true>(epi, A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo, out_cols,
+                                    h_sf, st)
+              : launch_mx_fmt<false>(epi, A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo, out_cols,
+                                     h_sf, st);
 }
 
 }  // namespace fs

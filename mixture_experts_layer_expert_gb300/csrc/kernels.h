@@ -117,24 +117,25 @@ cudaError_t num_sms(int* out);
 constexpr int kMaxDevices = 64;
 cudaError_t smem_attr_once(const void* fn, size_t bytes, bool (&set)[kMaxDevices]);
 
-// gemm_mx.cu: block-scaled FP8 operands (kind::mxf8f6f4.block_scale).  A is an
-// MX matrix of a_rows (a multiple of 128) rows and K columns (codes A, scale
+// gemm_mx.cu: block-scaled operands, E4M3 codes (f4 false) or E2M1.  A is an MX
+// matrix of a_rows (a multiple of 128) rows and K columns (codes A, scale
 // chunks a_sf), B MX-packed weights [G, N, K] (codes, chunks b_sf); groups
-// start at multiples of 128 rows.  EPI_SWIGLU writes the hidden as an MX
-// matrix (codes at out with row stride ldo bytes, chunks at h_sf; out_cols = c);
-// EPI_BF16 / EPI_F32 write bf16 / fp32 rows.
-cudaError_t launch_mx_gemm(int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
-                           const uint8_t* b_sf, int G, int N, int K, const int* plan, int max_mtiles, void* out,
-                           long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st);
+// start at multiples of 128 rows (plan nullptr: one group of `rows` rows).
+// EPI_SWIGLU writes the hidden as an MX matrix (codes at out with row stride
+// ldo bytes, chunks at h_sf; out_cols = c); EPI_BF16 / EPI_F32 write bf16 / fp32
+// rows.  N a multiple of 128 (E2M1 without EPI_SWIGLU: of 8).
+cudaError_t launch_mx_gemm(bool f4, int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
+                           const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
+                           void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st);
 
-// mx.cu: MX packs and quantisation (layouts in mx.cuh)
-size_t packed_bytes_mx(int G, int N, int K);
-const uint8_t* packed_sf_mx(const void* packed, int G, int N, int K);
-cudaError_t launch_pack_w13_mx(int G, int c, int d, const void* w1, const void* w2, void* w13, cudaStream_t st);
-cudaError_t launch_pack_w3_mx(int G, int d, int c, const void* w3, void* w3p, cudaStream_t st);
-cudaError_t launch_pack_w3_shared_mx(int ns, int cs, int d, const void* w3s, void* w3cat, cudaStream_t st);
-cudaError_t launch_quant_rows_mx(const void* x, long long rows, int cols, void* q, cudaStream_t st);
-cudaError_t launch_dispatch_copy_mx(const void* u, int T, int d, int k, const int32_t* pos, void* x_q,
+// mx.cu: MX packs and quantisation (layouts in mx.cuh), E4M3 or E2M1 (f4)
+size_t packed_bytes_mx(bool f4, int G, int N, int K);
+const uint8_t* packed_sf_mx(bool f4, const void* packed, int G, int N, int K);
+cudaError_t launch_pack_w13_mx(bool f4, int G, int c, int d, const void* w1, const void* w2, void* w13, cudaStream_t st);
+cudaError_t launch_pack_w3_mx(bool f4, int G, int d, int c, const void* w3, void* w3p, cudaStream_t st);
+cudaError_t launch_pack_w3_shared_mx(bool f4, int ns, int cs, int d, const void* w3s, void* w3cat, cudaStream_t st);
+cudaError_t launch_quant_rows_mx(bool f4, const void* x, long long rows, int cols, void* q, cudaStream_t st);
+cudaError_t launch_dispatch_copy_mx(bool f4, const void* u, int T, int d, int k, const int32_t* pos, void* x_q,
                                     long long rows_cap, void* u_q, cudaStream_t st);
 
 // gemm_simt.cu (fp32 operands, fp32 FMA)
@@ -155,9 +156,9 @@ size_t dispatch_ws_bytes(int T, int E);
 // qmode kQuantRow: x_perm is an FP8 row-scaled matrix [T k, d] (fp8.cuh) and u
 // (bf16) is quantised per token on the way; kQuantMx: each expert's segment
 // starts at a multiple of 128 rows (offsets padded) and x_perm is an MX matrix
-// of rows_cap rows (mx.cuh), u quantised in blocks of 32; u_q (nullable)
-// receives the quantised u [T, d] in the same form.
-enum { kQuantNone = 0, kQuantRow = 1, kQuantMx = 2 };
+// of rows_cap rows (mx.cuh), u quantised in blocks of 32; kQuantMx4: the same
+// with 4-bit codes; u_q (nullable) receives the quantised u [T, d] in the same form.
+enum { kQuantNone = 0, kQuantRow = 1, kQuantMx = 2, kQuantMx4 = 3 };
 cudaError_t launch_dispatch_noalloc(const int32_t* topk_idx, const void* u, int T, int d, int E, int k, int elem_bytes,
                                     int32_t* counts, int32_t* offsets, int32_t* pos, int32_t* perm_src,
                                     void* x_perm, cudaStream_t st, int qmode, long long rows_cap);

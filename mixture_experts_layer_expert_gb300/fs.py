@@ -18,8 +18,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libfs.so")
 _lib = None
 
-FS_BF16, FS_F32, FS_FP8, FS_MXFP8 = 0, 1, 2, 3
-DTYPES = {"bf16": FS_BF16, "f32": FS_F32, "fp8": FS_FP8, "mxfp8": FS_MXFP8}
+FS_BF16, FS_F32, FS_FP8, FS_MXFP8, FS_MXFP4 = 0, 1, 2, 3, 4
+DTYPES = {"bf16": FS_BF16, "f32": FS_F32, "fp8": FS_FP8, "mxfp8": FS_MXFP8, "mxfp4": FS_MXFP4}
 GATES = {"softmax": 0, "softmax_renorm": 1, "sigmoid": 2, "sigmoid_norm": 3}
 WIRINGS = {"partial": 0, "outdated": 1, "disabled": 2, "attn_farskip": 3, "attn_plain": 4}
 STATUS = {0: "FS_OK", 1: "FS_ERR_INVALID_ARG", 2: "FS_ERR_UNSUPPORTED", 3: "FS_ERR_WORKSPACE",
@@ -108,6 +108,10 @@ _SIGS = {
     "fs_quantize_rows_fp8": (_I32, [ctypes.c_int64, _I32, _VP, _VP, _VP]),
     "fs_mx_rows_bytes": (_SZ, [ctypes.c_int64, _I32]),
     "fs_quantize_rows_mx": (_I32, [ctypes.c_int64, _I32, _VP, _VP, _VP]),
+    "fs_mx4_rows_bytes": (_SZ, [ctypes.c_int64, _I32]),
+    "fs_quantize_rows_mx4": (_I32, [ctypes.c_int64, _I32, _VP, _VP, _VP]),
+    "fs_linear_mx4_ws_bytes": (_SZ, [ctypes.c_int64, _I32, _I32]),
+    "fs_linear_mx4": (_I32, [ctypes.c_int64, _I32, _I32, _VP, _VP, _VP, _I32, _I64, _VP, _SZ, _VP]),
     "fs_dispatch_rows": (ctypes.c_int64, [ctypes.POINTER(LayerDesc)]),
     "fs_rope": (_I32, [ctypes.POINTER(RopeDesc), _I64, _I32, _I32, _VP, _VP, _I64, _I64, _VP, _I64, _I64, _I32, _VP]),
     "fs_latent_cache_bytes": (_SZ, [ctypes.POINTER(LatentCache)]),
@@ -210,6 +214,62 @@ def fs_mx_rows_bytes(rows: int, cols: int) -> int:
 
 def fs_quantize_rows_mx(rows, cols, x, q, stream=None):
     _check(lib().fs_quantize_rows_mx(rows, cols, _p(x), _p(q), _stream(stream)), "fs_quantize_rows_mx")
+
+
+def fs_mx4_rows_bytes(rows: int, cols: int) -> int:
+    return int(lib().fs_mx4_rows_bytes(rows, cols))
+
+
+def mx4_rows_empty(rows: int, cols: int, device="cuda") -> torch.Tensor:
+    """A byte buffer for a 4-bit MX matrix [rows, cols] (codes, then block-scale chunks)."""
+    n = fs_mx4_rows_bytes(rows, cols)
+    if n == 0:
+        raise FsError(1, "fs_mx4_rows_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mx4_rows_split(buf: torch.Tensor, rows: int, cols: int):
+    """Views (code bytes [rows128, cols / 2], scale bytes [rows128 / 128, cols / 128, 512]) of a 4-bit MX matrix."""
+    r128 = (rows + 127) // 128 * 128
+    off = (r128 * cols // 2 + 255) // 256 * 256
+    return (buf[:r128 * cols // 2].view(r128, cols // 2),
+            buf[off:off + r128 // 128 * cols // 128 * 512].view(r128 // 128, cols // 128, 512))
+
+
+def fs_quantize_rows_mx4(rows, cols, x, q, stream=None):
+    """Quantise bf16 rows x [rows, cols] into q, a 4-bit MX matrix (mx4_rows_empty)."""
+    dev, st = _here(stream)
+    xp, _ = _operand("fs_quantize_rows_mx4 x", x, (rows, cols), dev, strided=False)
+    qp, _ = _operand("fs_quantize_rows_mx4 q", q, (fs_mx4_rows_bytes(rows, cols),), dev, torch.uint8, False)
+    _check(lib().fs_quantize_rows_mx4(rows, cols, xp, qp, st), "fs_quantize_rows_mx4")
+
+
+def pack_linear_mx4(w: torch.Tensor, stream=None) -> torch.Tensor:
+    """The FS_MXFP4 pack of a bf16 weight [N, K] for fs_linear_mx4."""
+    N, K = w.shape
+    dev, _ = _here(stream)
+    _operand("pack_linear_mx4 w", w, (N, K), dev, strided=False)
+    out = _packed(1, N, K, FS_MXFP4, w)
+    fs_pack_w3(1, N, K, FS_MXFP4, w, out, stream)
+    return out
+
+
+def fs_linear_mx4_ws_bytes(rows: int, N: int, K: int) -> int:
+    return int(lib().fs_linear_mx4_ws_bytes(rows, N, K))
+
+
+def fs_linear_mx4(q, w, y, K, ws, stream=None):
+    """y [rows, N] (bf16 or fp32, any row stride of 16-byte multiples) = the product of the 4-bit MX matrix q [rows, K]
+    with the pack w of a weight [N, K]; ws: fs_linear_mx4_ws_bytes(rows, N, K) bytes."""
+    dev, st = _here(stream)
+    what, (rows, N) = "fs_linear_mx4", y.shape
+    f32 = y.dtype is torch.float32
+    yp, ys = _operand("fs_linear_mx4 y", y, (rows, N), dev, torch.float32 if f32 else torch.bfloat16)
+    qp, _ = _operand("fs_linear_mx4 q", q, (fs_mx4_rows_bytes(rows, K),), dev, torch.uint8, False)
+    wp, _ = _operand("fs_linear_mx4 w", w, (fs_packed_bytes(1, N, K, FS_MXFP4),), dev, torch.uint8, False)
+    sp, _ = _operand("fs_linear_mx4 ws", ws, ws.shape, dev, torch.uint8, False)
+    _check(lib().fs_linear_mx4(rows, N, K, qp, wp, yp, FS_F32 if f32 else FS_BF16, ys[0] if rows > 1 else max(ys[0], N),
+                               sp, ws.numel(), st), what)
 
 
 def fs_dispatch_rows(desc) -> int:
@@ -362,7 +422,7 @@ def _packed(G, N, K, dt, like):
     n = fs_packed_bytes(G, N, K, dt)
     if n == 0:
         raise FsError(1, "fs_packed_bytes")
-    if dt in (FS_FP8, FS_MXFP8):
+    if dt in (FS_FP8, FS_MXFP8, FS_MXFP4):
         return torch.empty(n, dtype=torch.uint8, device=like.device)
     return torch.empty(n // like.element_size(), dtype=like.dtype, device=like.device)
 
