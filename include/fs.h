@@ -517,6 +517,57 @@ fs_status fs_farskip_stack_backward(const fs_layer_desc* desc, int32_t L, int32_
                                     const float* d_os, float* dx, const fs_block_grads* grads,
                                     void* ws, size_t ws_bytes, void* stream);
 
+/* fs_farskip_stack_backward with another term of the loss that depends on the
+ * router logits: d_logits [L] (host array) holds per block NULL or a device
+ * [T, E] fp32 gradient with respect to that block's logits, which is added to the
+ * gate's dz before its rounding and so reaches du and dW_R. */
+fs_status fs_farskip_stack_backward_aux(const fs_layer_desc* desc, int32_t L, int32_t wiring,
+                                        const fs_block_weights* blocks, const fs_block_weights_t* blocks_t,
+                                        const void* saved, size_t saved_bytes, const float* d_o, const float* d_os,
+                                        const float* const* d_logits, float* dx, const fs_block_grads* grads, void* ws,
+                                        size_t ws_bytes, void* stream);
+
+/* Where fs_farskip_stack_train keeps block `block`'s (0-based) router logits
+ * [T, E] and top-k indices [T, k] in `saved`: fs_balance_loss's operands. */
+fs_status fs_train_saved_routing(const fs_layer_desc* desc, int32_t L, int32_t block, const void* saved,
+                                 const float** logits, const int32_t** topk_idx);
+
+/* Balance loss of a router, with the per-expert counts.  T rows in n_seqs
+ * sequences with borders cu (device int32 [n_seqs + 1], non-decreasing, any may be
+ * empty; NULL with n_seqs = 1: all rows).  For sequence q with n counted rows
+ * (mask [T] NULL or mask != 0):
+ *   s_te = softmax(z_t + b)_e (gates SOFTMAX*), sigmoid(z_te + b_e) over its row sum (SIGMOID*)
+ *   counts_qe = the rows' slots in topk_idx [T, k] that name e,  f_qe = E counts_qe / (k n)
+ *   probs_qe = mean s_te,   loss = coef / n_seqs * sum_q sum_e f_qe probs_qe
+ * A sequence with n = 0 has zero counts and probs and adds nothing.  Its gradient
+ * (counts are constants; d_loss device fp32 scalar, NULL = 1):
+ *   d_logits_te = d_loss coef / (n_seqs n) s_te (f_qe - sum_j f_qj s_tj) [(1 - sigmoid(z_te + b_e)), SIGMOID*]
+ * zero for rows that the mask leaves out; rows outside every sequence are left as
+ * they were.  A row whose logits are all -infinity scores zero; a NaN or +infinity
+ * makes its row's scores NaN.  Sums are fp32 in a fixed order: results repeat bit
+ * for bit.  An index outside [0, E) sets the device error word (code 1) and is not
+ * counted; inconsistent borders set it (code 2) and leave their sequence's gradient,
+ * with zero counts.
+ * logits and d_logits are fp32 with row strides >= E elements; E <= 512, k <= 16,
+ * n_seqs <= 65,535.  counts [n_seqs, E] and tokens [n_seqs] (n) int32, probs
+ * [n_seqs, E] and loss [1] fp32.  ws: fs_balance_ws_bytes bytes, 256-byte aligned;
+ * it holds nothing between calls, calls that may run at the same time need one each. */
+typedef struct {
+    int32_t T, E, k;
+    int32_t gate;        /* fs_gate */
+    int32_t n_seqs;
+    float coef;
+} fs_balance_desc;
+
+size_t fs_balance_ws_bytes(const fs_balance_desc* desc);
+fs_status fs_balance_loss(const fs_balance_desc* desc, const float* logits, int64_t logits_row, const float* bias,
+                          const int32_t* topk_idx, const int32_t* cu, const uint8_t* mask, int32_t* counts,
+                          int32_t* tokens, float* probs, float* loss, void* ws, size_t ws_bytes, void* stream);
+fs_status fs_balance_loss_backward(const fs_balance_desc* desc, const float* logits, int64_t logits_row,
+                                   const float* bias, const int32_t* cu, const uint8_t* mask, const int32_t* counts,
+                                   const int32_t* tokens, const float* d_loss, float* d_logits, int64_t d_row,
+                                   void* stream);
+
 /* ---------------------------------------------------------------- attention
  * The operators of an attention sub-layer whose keys and values come from one
  * latent vector per token (latent attention, the attention of the DeepSeek

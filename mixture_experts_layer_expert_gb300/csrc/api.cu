@@ -1143,10 +1143,11 @@ fs_status fs_farskip_stack_train(const fs_layer_desc* desc, int32_t L, int32_t w
     return FS_OK;
 }
 
-fs_status fs_farskip_stack_backward(const fs_layer_desc* desc, int32_t L, int32_t wiring,
-                                    const fs_block_weights* blocks, const fs_block_weights_t* blocks_t,
-                                    const void* saved, size_t saved_bytes, const float* d_o, const float* d_os,
-                                    float* dx, const fs_block_grads* grads, void* ws, size_t ws_bytes, void* stream) {
+// d_logits (nullable): per block another term's gradient with respect to the router logits.
+static fs_status backward_impl(const fs_layer_desc* desc, int32_t L, int32_t wiring, const fs_block_weights* blocks,
+                               const fs_block_weights_t* blocks_t, const void* saved, size_t saved_bytes,
+                               const float* d_o, const float* d_os, const float* const* d_logits, float* dx,
+                               const fs_block_grads* grads, void* ws, size_t ws_bytes, void* stream) {
     FS_CHECK(check_train(desc, L, wiring));
     if (!blocks || !blocks_t || !grads) return FS_ERR_INVALID_ARG;
     FS_CHECK(need(d_o));
@@ -1252,8 +1253,8 @@ fs_status fs_farskip_stack_backward(const fs_layer_desc* desc, int32_t L, int32_
                                   dm, dm, nullptr, 0, true, st, &acc));
         }
         // router: dz through the gate rule, du += dz W_R
-        FS_TRY(launch_gate_backward(reinterpret_cast<const float*>(sv(blk, sl.logits)), bw.bias, idx, w, dw, T, E,
-                                    bl.Epad, k, desc->gate, dz, st));
+        FS_TRY(launch_gate_backward(reinterpret_cast<const float*>(sv(blk, sl.logits)), bw.bias, idx, w, dw,
+                                    d_logits ? d_logits[blk] : nullptr, T, E, bl.Epad, k, desc->gate, dz, st));
         FS_TRY(launch_tc_gemm(EPI_F32, dz, T, bt.w_rt, 1, dm, bl.Epad, plan_s, ceil_div(T, bm) + 1, target, dm, dm,
                               nullptr, 0, true, st, &acc));
         // weight gradients: contractions over each expert's rows (all T rows for
@@ -1269,6 +1270,38 @@ fs_status fs_farskip_stack_backward(const fs_layer_desc* desc, int32_t L, int32_
         }
         FS_TRY(launch_wgrad_gemm(dz, bl.Epad, u, dm, T, nullptr, 1, E, dm, gr.dw_r, nullptr, 0, 0, st));
     }
+    return FS_OK;
+}
+
+fs_status fs_farskip_stack_backward(const fs_layer_desc* desc, int32_t L, int32_t wiring,
+                                    const fs_block_weights* blocks, const fs_block_weights_t* blocks_t,
+                                    const void* saved, size_t saved_bytes, const float* d_o, const float* d_os,
+                                    float* dx, const fs_block_grads* grads, void* ws, size_t ws_bytes, void* stream) {
+    return backward_impl(desc, L, wiring, blocks, blocks_t, saved, saved_bytes, d_o, d_os, nullptr, dx, grads, ws,
+                         ws_bytes, stream);
+}
+
+fs_status fs_farskip_stack_backward_aux(const fs_layer_desc* desc, int32_t L, int32_t wiring,
+                                        const fs_block_weights* blocks, const fs_block_weights_t* blocks_t,
+                                        const void* saved, size_t saved_bytes, const float* d_o, const float* d_os,
+                                        const float* const* d_logits, float* dx, const fs_block_grads* grads, void* ws,
+                                        size_t ws_bytes, void* stream) {
+    FS_CHECK(check_train(desc, L, wiring));
+    if (!d_logits) return FS_ERR_INVALID_ARG;
+    for (int b = 0; b < L; ++b)
+        if (reinterpret_cast<uintptr_t>(d_logits[b]) & 3u) return FS_ERR_UNSUPPORTED;
+    return backward_impl(desc, L, wiring, blocks, blocks_t, saved, saved_bytes, d_o, d_os, d_logits, dx, grads, ws,
+                         ws_bytes, stream);
+}
+
+fs_status fs_train_saved_routing(const fs_layer_desc* desc, int32_t L, int32_t block, const void* saved,
+                                 const float** logits, const int32_t** topk_idx) {
+    FS_CHECK(check_train(desc, L, FS_WIRE_PARTIAL));
+    if (block < 0 || block >= L || !saved || !logits || !topk_idx) return FS_ERR_INVALID_ARG;
+    const SavedLayout sl = saved_layout(desc);
+    const uint8_t* p = static_cast<const uint8_t*>(saved) + static_cast<size_t>(block) * sl.size;
+    *logits = reinterpret_cast<const float*>(p + sl.logits);
+    *topk_idx = reinterpret_cast<const int32_t*>(p + sl.idx);
     return FS_OK;
 }
 

@@ -128,15 +128,17 @@ gather_sum_kernel(const uint4* __restrict__ dx_perm, const int32_t* __restrict__
 
 // Gate-rule backward, one warp per token: dz = d w / d z applied to dw (z =
 // logits + bias; the chosen experts e_s with weights w_s), written as bf16 into
-// a dense row of E_pad columns (zeros elsewhere):
+// a dense row of E_pad columns (zeros elsewhere), plus extra [T, E] where given
+// (another term's gradient with respect to the logits, added before the rounding):
 //   SOFTMAX         dz_j = -c p_j + [j = e_s] dw_s w_s,  c = sum_s dw_s w_s
 //   SOFTMAX_RENORM  dz_{e_r} = w_r (dw_r - c)
 //   SIGMOID         dz_{e_s} = dw_s sig (1 - sig)
 //   SIGMOID_NORM    dz_{e_r} = (dw_r - c) / sum_s sig_s * sig_r (1 - sig_r)
 __global__ void __launch_bounds__(kBwdWarps * 32)
 gate_backward_kernel(const float* __restrict__ logits, const float* __restrict__ bias,
-                     const int32_t* __restrict__ idx, const float* __restrict__ w, const float* __restrict__ dw, int T,
-                     int E, int E_pad, int k, int gate, __nv_bfloat16* __restrict__ dz, int* err) {
+                     const int32_t* __restrict__ idx, const float* __restrict__ w, const float* __restrict__ dw,
+                     const float* __restrict__ extra, int T, int E, int E_pad, int k, int gate,
+                     __nv_bfloat16* __restrict__ dz, int* err) {
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * kBwdWarps + (threadIdx.x >> 5);
     if (t >= T) return;
@@ -147,6 +149,7 @@ gate_backward_kernel(const float* __restrict__ logits, const float* __restrict__
     float c = 0.0f;
     for (int s = 0; s < k; ++s) c += dws[s] * ws[s];
     __nv_bfloat16* out = dz + static_cast<long long>(t) * E_pad;
+    const float* more = extra ? extra + static_cast<long long>(t) * E : nullptr;
     if (gate == 0) {   // softmax over all experts
         const int e0 = e[0];
         if (e0 < 0 || e0 >= E) { set_dev_error(err, DEV_ERR_EXPERT_INDEX); return; }
@@ -161,12 +164,13 @@ gate_backward_kernel(const float* __restrict__ logits, const float* __restrict__
                 v = -c * (__expf(z[j] + (bias ? bias[j] : 0.0f) - zmax) / den);
                 for (int s = 0; s < k; ++s)
                     if (e[s] == j) v += dws[s] * ws[s];
+                if (more) v += more[j];
             }
             out[j] = __float2bfloat16_rn(v);
         }
         return;
     }
-    for (int j = lane; j < E_pad; j += 32) out[j] = __float2bfloat16_rn(0.0f);
+    for (int j = lane; j < E_pad; j += 32) out[j] = __float2bfloat16_rn(more && j < E ? more[j] : 0.0f);
     __syncwarp();
     float den = 0.0f;
     if (gate == 3)
@@ -184,7 +188,7 @@ gate_backward_kernel(const float* __restrict__ logits, const float* __restrict__
             const float sg = 1.0f / (1.0f + __expf(-(z[j] + (bias ? bias[j] : 0.0f))));
             v = gate == 2 ? dws[lane] * sg * (1.0f - sg) : (dws[lane] - c) / den * sg * (1.0f - sg);
         }
-        out[j] = __float2bfloat16_rn(v);
+        out[j] = __float2bfloat16_rn(more ? v + more[j] : v);
     }
 }
 
@@ -312,10 +316,10 @@ cudaError_t launch_gather_sum(const void* dx_perm, const int32_t* pos, int T, in
 }
 
 cudaError_t launch_gate_backward(const float* logits, const float* bias, const int32_t* idx, const float* w,
-                                 const float* dw, int T, int E, int E_pad, int k, int gate, void* dz,
-                                 cudaStream_t st) {
+                                 const float* dw, const float* extra, int T, int E, int E_pad, int k, int gate,
+                                 void* dz, cudaStream_t st) {
     gate_backward_kernel<<<(T + kBwdWarps - 1) / kBwdWarps, kBwdWarps * 32, 0, st>>>(
-        logits, bias, idx, w, dw, T, E, E_pad, k, gate, static_cast<__nv_bfloat16*>(dz), dev_error_ptr());
+        logits, bias, idx, w, dw, extra, T, E, E_pad, k, gate, static_cast<__nv_bfloat16*>(dz), dev_error_ptr());
     count_launch();
     return cudaGetLastError();
 }

@@ -199,8 +199,8 @@ cudaError_t launch_combine_backward(const float* dO, const float* dOs, const voi
 cudaError_t launch_gather_sum(const void* dx_perm, const int32_t* pos, int T, int d, int k, float* du,
                               cudaStream_t st);
 cudaError_t launch_gate_backward(const float* logits, const float* bias, const int32_t* idx, const float* w,
-                                 const float* dw, int T, int E, int E_pad, int k, int gate, void* dz,
-                                 cudaStream_t st);
+                                 const float* dw, const float* extra, int T, int E, int E_pad, int k, int gate,
+                                 void* dz, cudaStream_t st);
 cudaError_t launch_wait_selftest(uint64_t limit_ns, cudaStream_t st);
 cudaError_t launch_copy(void* dst, const void* src, size_t bytes, cudaStream_t st);   // bytes % 16 == 0
 cudaError_t launch_zero(void* dst, size_t bytes, cudaStream_t st);                    // bytes % 16 == 0
@@ -210,6 +210,28 @@ cudaError_t launch_pack_t(int mode, int G, int Np, int Kp, int c, int d, int cs,
 
 // Records a CUDA error's text for fs_last_cuda_error (api.cu); the library status.
 int cuda_error_status(cudaError_t e);
+
+// balance.cu: the router's balance loss, counts and gradient.  S sequences with borders
+// cu [S + 1] on the device (null: one sequence of all T rows)
+struct BalanceArgs {
+    const float* z;
+    long long z_row;
+    const float* bias;
+    const int32_t* idx;
+    const uint8_t* mask;
+    const int32_t* cu;
+    int T, E, k, S;
+    bool sigmoid;
+    float coef;
+    int32_t* counts;
+    int32_t* tokens;
+    float* probs;
+    float* loss;
+};
+size_t balance_ws_bytes(int T, int E, int S);
+cudaError_t launch_balance(const BalanceArgs& b, void* ws, cudaStream_t st);
+cudaError_t launch_balance_backward(const BalanceArgs& b, const float* d_loss, float* dz, long long dz_row,
+                                    cudaStream_t st);
 
 // rope.cu
 struct RopeTab;

@@ -56,6 +56,10 @@ class RopeDesc(ctypes.Structure):
         (n, ctypes.c_double) for n in ("base", "factor", "orig_len", "beta_fast", "beta_slow", "mscale")]
 
 
+class BalanceDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "gate", "n_seqs")] + [("coef", ctypes.c_float)]
+
+
 class LatentCache(ctypes.Structure):
     _fields_ = [("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
@@ -105,6 +109,16 @@ _SIGS = {
     "fs_farskip_stack_backward": (_I32, [ctypes.POINTER(LayerDesc), _I32, _I32, ctypes.POINTER(BlockWeights),
                                          ctypes.POINTER(BlockWeightsT), _VP, _SZ, _VP, _VP, _VP,
                                          ctypes.POINTER(BlockGrads), _VP, _SZ, _VP]),
+    "fs_farskip_stack_backward_aux": (_I32, [ctypes.POINTER(LayerDesc), _I32, _I32, ctypes.POINTER(BlockWeights),
+                                             ctypes.POINTER(BlockWeightsT), _VP, _SZ, _VP, _VP, ctypes.POINTER(_VP),
+                                             _VP, ctypes.POINTER(BlockGrads), _VP, _SZ, _VP]),
+    "fs_train_saved_routing": (_I32, [ctypes.POINTER(LayerDesc), _I32, _I32, _VP, ctypes.POINTER(_VP),
+                                      ctypes.POINTER(_VP)]),
+    "fs_balance_ws_bytes": (_SZ, [ctypes.POINTER(BalanceDesc)]),
+    "fs_balance_loss": (_I32, [ctypes.POINTER(BalanceDesc), _VP, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                               _SZ, _VP]),
+    "fs_balance_loss_backward": (_I32, [ctypes.POINTER(BalanceDesc), _VP, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                        _I64, _VP]),
     "fs_quantize_rows_fp8": (_I32, [ctypes.c_int64, _I32, _VP, _VP, _VP]),
     "fs_mx_rows_bytes": (_SZ, [ctypes.c_int64, _I32]),
     "fs_quantize_rows_mx": (_I32, [ctypes.c_int64, _I32, _VP, _VP, _VP]),
@@ -555,6 +569,50 @@ def _grads_struct(g: dict) -> BlockGrads:
     return BlockGrads(*[_p(g.get(k)) for k in ("dW_R", "dW1", "dW2", "dW3", "dW1s", "dW2s", "dW3s")])
 
 
+def make_balance(T: int, E: int, k: int, gate: str, n_seqs: int = 1, coef: float = 1.0) -> BalanceDesc:
+    return BalanceDesc(T, E, k, GATES[gate], n_seqs, coef)
+
+
+def fs_balance_ws_bytes(desc: BalanceDesc) -> int:
+    return int(lib().fs_balance_ws_bytes(ctypes.byref(desc)))
+
+
+def _balance_operands(what, dev, desc, logits, bias, cu, mask, counts, tokens):
+    """(logits, row stride, bias, cu, mask, counts, tokens) of both directions."""
+    T, E, S, f32, i32 = desc.T, desc.E, desc.n_seqs, torch.float32, torch.int32
+    opt = lambda name, t, shape, dt: None if t is None else _operand(what + " " + name, t, shape, dev, dt, False)[0]
+    zp, zs = _operand(what + " logits", logits, (T, E), dev, f32)
+    return (zp, zs[0] if T > 1 else max(zs[0], E), opt("bias", bias, (E,), f32), opt("cu", cu, (S + 1,), i32),
+            opt("mask", mask, (T,), torch.uint8), opt("counts", counts, (S, E), i32), opt("tokens", tokens, (S,), i32))
+
+
+def fs_balance_loss(desc: BalanceDesc, logits, topk_idx, counts, tokens, probs, loss, ws, bias=None, cu=None, mask=None,
+                    stream=None):
+    """Balance loss of router logits [T, E] (fp32, any row stride) and top-k indices [T, k] int32: counts [S, E] and
+    tokens [S] int32, probs [S, E] and loss [1] fp32; cu [S + 1] int32 borders and mask [T] uint8 optional;
+    ws: fs_balance_ws_bytes(desc) bytes."""
+    dev, st = _here(stream)
+    what = "fs_balance_loss"
+    zp, zr, bp, cp, mp, np_, tp = _balance_operands(what, dev, desc, logits, bias, cu, mask, counts, tokens)
+    ip, _ = _operand(what + " topk_idx", topk_idx, (desc.T, desc.k), dev, torch.int32, False)
+    pp, _ = _operand(what + " probs", probs, (desc.n_seqs, desc.E), dev, torch.float32, False)
+    lp, _ = _operand(what + " loss", loss, (1,), dev, torch.float32, False)
+    wp, _ = _operand(what + " ws", ws, ws.shape, dev, torch.uint8, False)
+    _check(lib().fs_balance_loss(desc, zp, zr, bp, ip, cp, mp, np_, tp, pp, lp, wp, ws.numel(), st), what)
+
+
+def fs_balance_loss_backward(desc: BalanceDesc, logits, counts, tokens, d_loss, d_logits, bias=None, cu=None, mask=None,
+                             stream=None):
+    """d_logits [T, E] fp32 from fs_balance_loss's counts and tokens and d_loss [1] (None: 1)."""
+    dev, st = _here(stream)
+    what = "fs_balance_loss_backward"
+    zp, zr, bp, cp, mp, np_, tp = _balance_operands(what, dev, desc, logits, bias, cu, mask, counts, tokens)
+    gp = None if d_loss is None else _operand(what + " d_loss", d_loss, (1,), dev, torch.float32, False)[0]
+    dp, ds = _operand(what + " d_logits", d_logits, (desc.T, desc.E), dev, torch.float32)
+    _check(lib().fs_balance_loss_backward(desc, zp, zr, bp, cp, mp, np_, tp, gp, dp,
+                                          ds[0] if desc.T > 1 else max(ds[0], desc.E), st), what)
+
+
 class FarSkipTrainer:
     """Forward (keeping what the backward reads) and backward of an L-block
     FarSkip MoE stack on one GPU (bf16, MoE wirings): two library calls."""
@@ -587,24 +645,75 @@ class FarSkipTrainer:
         self.dx = torch.empty((self.T, d), **f32)
 
     def forward(self, x: torch.Tensor, stream=None):
+        self.bal_ready = False              # the balance loss belongs to one forward
         arr = (BlockWeights * self.L)(*[block_struct(b) for b in self.blocks])
         _check(lib().fs_farskip_stack_train(ctypes.byref(self.desc), self.L, WIRINGS[self.wiring], arr, _p(x),
                                             _p(self.o_full), _p(self.o_partial), _p(self.saved), _nbytes(self.saved),
                                             _p(self.ws), _nbytes(self.ws), _stream(stream)), "fs_farskip_stack_train")
         return self.o_full, self.o_partial
 
+    def balance_loss(self, coef: float, cu: torch.Tensor | None = None, mask: torch.Tensor | None = None, stream=None):
+        """Balance loss of every block's router in the last forward: loss [L, 1] fp32 and counts [L, S, E] int32 (also
+        kept for backward's d_balance).  cu [S + 1] int32: sequence borders; mask [T] uint8: 0 leaves a token out."""
+        cfg, S, dev = self.cfg, 1 if cu is None else cu.shape[0] - 1, self.o_full.device
+        desc = make_balance(self.T, cfg.E, cfg.k, cfg.gate, S, coef)
+        n = fs_balance_ws_bytes(desc)
+        if n == 0:
+            raise FsError(1, "fs_balance_ws_bytes")
+        b = getattr(self, "bal", None)
+        if b is None or b["counts"].shape[1] != S:
+            i32, f32 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.float32, device=dev)
+            b = {"counts": torch.empty((self.L, S, cfg.E), **i32), "tokens": torch.empty((self.L, S), **i32),
+                 "probs": torch.empty((self.L, S, cfg.E), **f32), "loss": torch.empty((self.L, 1), **f32),
+                 "d_logits": torch.zeros((self.L, self.T, cfg.E), **f32),
+                 "ws": torch.empty(n, dtype=torch.uint8, device=dev)}
+        b.update(desc=desc, cu=cu, mask=mask)
+        self.bal = b
+        cur, st = _here(stream)
+        cp = None if cu is None else _operand("balance_loss cu", cu, (S + 1,), cur, torch.int32, False)[0]
+        mp = None if mask is None else _operand("balance_loss mask", mask, (self.T,), cur, torch.uint8, False)[0]
+        for blk in range(self.L):
+            z, idx = self._routing(blk)
+            _check(lib().fs_balance_loss(desc, z, cfg.E, _p(self.blocks[blk]["bias"]), idx, cp, mp,
+                                         _p(b["counts"][blk]), _p(b["tokens"][blk]), _p(b["probs"][blk]),
+                                         _p(b["loss"][blk]), _p(b["ws"]), n, st), "fs_balance_loss")
+        self.bal_ready = True
+        return b["loss"], b["counts"]
+
+    def _routing(self, blk: int):
+        z, idx = _VP(), _VP()
+        _check(lib().fs_train_saved_routing(ctypes.byref(self.desc), self.L, blk, _p(self.saved), ctypes.byref(z),
+                                            ctypes.byref(idx)), "fs_train_saved_routing")
+        return z, idx
+
     def backward(self, d_o: torch.Tensor, d_os: torch.Tensor | None = None, stream=None,
-                 dx: torch.Tensor | None = None):
+                 dx: torch.Tensor | None = None, d_balance: torch.Tensor | None = None):
         """Gradients for the last forward: dx (into `dx` when given, else self.dx)
-        and the weight gradients (self.grads)."""
+        and the weight gradients (self.grads).  d_balance [1] fp32 on the device: the gradient of the loss with
+        respect to the sum of balance_loss's losses, which then goes into the routers' gradients."""
         out = self.dx if dx is None else dx
         arr = (BlockWeights * self.L)(*[block_struct(b) for b in self.blocks])
         arr_t = (BlockWeightsT * self.L)(*[_block_t_struct(b) for b in self.blocks_t])
         gr = (BlockGrads * self.L)(*[_grads_struct(g) for g in self.grads])
-        _check(lib().fs_farskip_stack_backward(ctypes.byref(self.desc), self.L, WIRINGS[self.wiring], arr, arr_t,
-                                               _p(self.saved), _nbytes(self.saved), _p(d_o), _p(d_os), _p(out),
-                                               gr, _p(self.ws_b), _nbytes(self.ws_b), _stream(stream)),
-               "fs_farskip_stack_backward")
+        head = (ctypes.byref(self.desc), self.L, WIRINGS[self.wiring], arr, arr_t, _p(self.saved), _nbytes(self.saved),
+                _p(d_o), _p(d_os))
+        tail = (_p(out), gr, _p(self.ws_b), _nbytes(self.ws_b), _stream(stream))
+        if d_balance is None:
+            _check(lib().fs_farskip_stack_backward(*head, *tail), "fs_farskip_stack_backward")
+            return out, self.grads
+        if not getattr(self, "bal_ready", False):
+            raise FsError(1, "backward", "d_balance without a balance_loss of the last forward")
+        b = self.bal
+        cur, st = _here(stream)
+        gp, _ = _operand("backward d_balance", d_balance, (1,), cur, torch.float32, False)
+        extra = (_VP * self.L)()
+        for blk in range(self.L):
+            z, _ = self._routing(blk)
+            extra[blk] = b["d_logits"][blk].data_ptr()
+            _check(lib().fs_balance_loss_backward(b["desc"], z, self.cfg.E, _p(self.blocks[blk]["bias"]), _p(b["cu"]),
+                                                  _p(b["mask"]), _p(b["counts"][blk]), _p(b["tokens"][blk]), gp,
+                                                  extra[blk], self.cfg.E, st), "fs_balance_loss_backward")
+        _check(lib().fs_farskip_stack_backward_aux(*head, extra, *tail), "fs_farskip_stack_backward_aux")
         return out, self.grads
 
 
