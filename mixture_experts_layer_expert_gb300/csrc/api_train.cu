@@ -1,6 +1,8 @@
 // api_train.cu -- the C ABI of the training operators beside the stack's backward:
-// the router's balance loss with its gradient.  Argument checks and launches only;
+// the router's balance loss with its gradient, orthogonalised updates.  Argument checks and launches only;
 // see include/fs.h for the contracts.
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 #include "../../include/fs.h"
@@ -57,9 +59,79 @@ fs_status balance_args(const fs_balance_desc* d, const float* logits, int64_t ro
     return FS_OK;
 }
 
+// ---- orthogonalised updates
+constexpr int kMaxSteps = 16, kMaxDim = 16384;
+
+// Powers of two for X, A and B, from the largest singular value that the steps can
+// reach: s <= 1 at first (the Frobenius norm is 1), then max |a s + b s^3 + c s^5|.
+// X, A = X X^T and B have entries no larger than their own largest singular values; each
+// is stored below 2^14, a factor of four under fp16's end for what rounding adds.
+fs_status ortho_scales(const fs_orthogonalize_desc* d, OrthoScales* sc) {
+    double s = 1.0, top = 1.0, btop = 0.0;
+    for (int k = 0; k < d->steps; ++k) {
+        const double a = d->coefs[3 * k], b = d->coefs[3 * k + 1], c = d->coefs[3 * k + 2];
+        if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return FS_ERR_INVALID_ARG;
+        double next = 0.0;
+        for (int i = 0; i <= 4096; ++i) {              // what lies between the points is within the factor of four
+            const double x = s * i / 4096, u = x * x;
+            next = std::max(next, std::fabs(x * (a + u * (b + u * c))));
+            btop = std::max(btop, std::fabs(u * (b + u * c)));
+        }
+        s = next;
+        top = std::max(top, s);
+        if (!(s <= 8.0) || !(btop <= 1024.0)) return FS_ERR_UNSUPPORTED;      // the steps would not stay bounded
+    }
+    const auto below = [](double limit, double v) { return static_cast<float>(std::exp2(std::floor(std::log2(limit / v)))); };
+    sc->x = below(16384.0, top);
+    sc->a = below(16384.0, top * top);
+    sc->b = below(16384.0, std::max(btop, 1.0));
+    return FS_OK;
+}
+
+fs_status check_ortho(const fs_orthogonalize_desc* d, OrthoScales* sc) {
+    if (!d || d->batch < 1 || d->m < 1 || d->n < 1 || d->steps < 1) return FS_ERR_INVALID_ARG;
+    if (d->dtype < FS_BF16 || d->dtype > FS_MXFP4) return FS_ERR_INVALID_ARG;
+    if (!std::isfinite(d->scale) || !(d->eps >= 0.f) || !std::isfinite(d->eps)) return FS_ERR_INVALID_ARG;
+    if (d->dtype != FS_BF16 && d->dtype != FS_F32) return FS_ERR_UNSUPPORTED;
+    if (d->m > kMaxDim || d->n > kMaxDim || d->steps > kMaxSteps) return FS_ERR_UNSUPPORTED;
+    return ortho_scales(d, sc);
+}
+
+// Strides of a [batch, m, n] operand: rows inside matrices.
+fs_status ortho_strides(const fs_orthogonalize_desc* d, int64_t row, int64_t mat) {
+    if (row < d->n || (d->batch > 1 && mat < (d->m - 1) * row + d->n)) return FS_ERR_INVALID_ARG;
+    return row <= (int64_t(1) << 31) && mat <= kMaxStride ? FS_OK : FS_ERR_UNSUPPORTED;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t fs_orthogonalize_ws_bytes(const fs_orthogonalize_desc* desc) {
+    OrthoScales sc;
+    if (check_ortho(desc, &sc) != FS_OK) return 0;
+    return ortho_ws_bytes(desc->batch, desc->m, desc->n);
+}
+
+fs_status fs_orthogonalize(const fs_orthogonalize_desc* desc, const void* g, int64_t g_row, int64_t g_mat, void* out,
+                           int64_t out_row, int64_t out_mat, void* ws, size_t ws_bytes, void* stream) {
+    OrthoArgs o;
+    FS_CHECK(check_ortho(desc, &o.scales));
+    o.f32 = desc->dtype == FS_F32;
+    FS_CHECK(need(g, o.f32 ? 4 : 2));
+    FS_CHECK(need(out, 2));
+    FS_CHECK(ortho_strides(desc, g_row, g_mat));
+    FS_CHECK(ortho_strides(desc, out_row, out_mat));
+    if (!ws) return FS_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < fs_orthogonalize_ws_bytes(desc)) return FS_ERR_WORKSPACE;
+    o.g = g; o.g_row = g_row; o.g_mat = desc->batch > 1 ? g_mat : 0;
+    o.out = static_cast<__nv_bfloat16*>(out); o.out_row = out_row;
+    o.out_mat = desc->batch > 1 ? out_mat : (desc->m * out_row + 7) / 8 * 8;      // one matrix: any legal stride
+    o.batch = desc->batch; o.m = desc->m; o.n = desc->n; o.steps = desc->steps;
+    o.coefs = desc->coefs; o.eps = desc->eps; o.scale = desc->scale;
+    FS_TRY(launch_orthogonalize(o, ws, static_cast<cudaStream_t>(stream)));
+    return FS_OK;
+}
 
 size_t fs_balance_ws_bytes(const fs_balance_desc* desc) {
     if (check_balance(desc) != FS_OK) return 0;

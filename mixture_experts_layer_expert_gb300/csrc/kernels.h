@@ -233,6 +233,25 @@ cudaError_t launch_balance(const BalanceArgs& b, void* ws, cudaStream_t st);
 cudaError_t launch_balance_backward(const BalanceArgs& b, const float* d_loss, float* dz, long long dz_row,
                                     cudaStream_t st);
 
+// ortho.cu: Newton-Schulz steps on a batch of matrices [m, n] (strides in elements)
+struct OrthoScales {
+    float x, a, b;             // powers of two that X, A = X X^T and B = b A + c A A are stored with
+};
+struct OrthoArgs {
+    const void* g;             // fp32 or bf16
+    long long g_row, g_mat;
+    bool f32;
+    __nv_bfloat16* out;
+    long long out_row, out_mat;
+    int batch, m, n, steps;
+    const float* coefs;        // host [steps][3]
+    double eps;
+    float scale;
+    OrthoScales scales;
+};
+size_t ortho_ws_bytes(int batch, int m, int n);
+cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st);
+
 // rope.cu
 struct RopeTab;
 cudaError_t launch_rope(const RopeTab& tab, bool f32, long long T, int H, const int32_t* pos, const void* x,

@@ -1,0 +1,762 @@
+// ortho.cu -- orthogonalised updates: Newton-Schulz steps on a batch of matrices
+// (the expert weights' gradients).
+//
+//   X = G / (|G|_F + eps);  per step  A = X X^T,  B = b A + c A A,  X = a X + B X
+// with X [r, q], r <= q (a tall G works as its transpose).  2 r^2 q + r^3 of the
+// multiply-adds are the symmetric products' halves.
+//
+// Rounding.  The steps multiply small singular values by a each time (3.4445^5 =
+// 485 for the usual coefficients), and with them any error in directions that G
+// does not have: gradients of experts with fewer tokens than rows have many.  X
+// rounded to bf16 between the steps is 10 to 30% off for such G, in fp16 1 to 4%.
+// So X is a pair of fp16 numbers H + L 2^-11 (22 bits), and the products read H only:
+// an error of H enters through B X, whose left side has no component outside G's own
+// directions, and the term a X is exact to 22 bits.  What remains is 0.1 to 0.2%, below
+// the rounding of a bf16 result.  A and B are fp16.  All three carry powers of two that
+// keep the largest values the coefficients allow below 2^15 (see OrthoScales); sums fp32.
+//
+// One GEMM serves the three products: CTA pairs (2-SM MMA) on 256 x 256 tiles, operands
+// by TMA in five stages of 64 along K, two accumulators in TMEM.  X X^T and A A compute
+// the tiles on and above the diagonal and store each 32 x 32 piece and its transpose.
+// B X reads X as the MN-major operand, where it lies.  The epilogue's own inputs (the piece
+// of A, of H and L) come and go by TMA through two 4 KB buffers per warp.
+#include <cudaTypedefs.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace fs {
+namespace ortho {
+
+constexpr int BT = 256;                       // tile rows and columns of a pair
+constexpr int BK = 64;
+constexpr int STAGES = 5;
+constexpr int A_STAGE = 128 * BK * 2;         // this CTA's 128 rows of the first operand
+constexpr int B_STAGE = 128 * BK * 2;         // its 128 rows (or columns) of the second
+constexpr int STAGE_BYTES = A_STAGE + B_STAGE;
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int NACC = 2;
+constexpr int TMEM_COLS = 512;
+constexpr int PIECE = 32 * 32 * 2;            // 32 x 32 fp16
+constexpr int BUF = 2 * PIECE;
+constexpr int EPI_OFF = STAGES * STAGE_BYTES;
+constexpr int BAR_OFF = EPI_OFF + EPI_WARPS * 2 * BUF;
+constexpr size_t SMEM_BYTES = 1024 + BAR_OFF + 512;
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+
+// GRAM: A = X X^T;  POLY: B = b A + c A A;  STEP: X = a X + B X;  LAST: the same, as the bf16 result
+enum { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
+
+struct Args {
+    int R, C, batch, kb;          // tiles of rows and columns, matrices, stages along K
+    int rows, cols;               // extents of the output (cols padded to 64)
+    float alpha, beta;            // out = alpha in + beta acc
+    __nv_bfloat16* out;           // LAST: result [m, n]
+    long long out_row, out_mat;
+    int m, n, tall, tma_out;
+    int* err;
+};
+
+struct Tile {
+    int z, i, j;
+};
+
+__device__ __forceinline__ int tiles_per_matrix(const Args& a, bool sym) { return sym ? a.R * (a.R + 1) / 2 : a.R * a.C; }
+
+template <bool SYM>
+__device__ __forceinline__ Tile decode(int t, const Args& a, int per) {
+    Tile r;
+    r.z = t / per;
+    const int x = t - r.z * per;
+    if constexpr (SYM) {               // column by column of the upper triangle: tile (i, j), i <= j, is j (j + 1) / 2 + i
+        int j = static_cast<int>((sqrtf(8.0f * static_cast<float>(x) + 1.0f) - 1.0f) * 0.5f);
+        while (j * (j + 1) / 2 > x) --j;
+        while ((j + 1) * (j + 2) / 2 <= x) ++j;
+        r.j = j;
+        r.i = x - j * (j + 1) / 2;
+    } else {
+        r.j = x / a.R;
+        r.i = x - r.j * a.R;
+    }
+    return r;
+}
+
+__device__ __forceinline__ void store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                     reinterpret_cast<uint64_t>(tmap)),
+                 "r"(src), "r"(x), "r"(y), "r"(z)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    tc_mma_bf16_pair(d, adesc, bdesc, idesc, acc);      // kind::f16; the descriptor says fp16
+}
+
+// Instruction descriptor, kind::f16: fp32 accumulator, A and B fp16 (formats 0), B MN-major if b_mn.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+
+// 16-byte chunk q of row `row` in a 32 x 32 piece with the 64-byte swizzle.
+__device__ __forceinline__ int chunk_at(int row, int q) { return row * 64 + ((q ^ ((row >> 1) & 3)) << 4); }
+// Element (row, col) of it.
+__device__ __forceinline__ int elem_at(int row, int col) { return chunk_at(row, col >> 3) + (col & 7) * 2; }
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+            const __grid_constant__ CUtensorMap tmIn, const __grid_constant__ CUtensorMap tmInL,
+            const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmOutL, const Args args) {
+    constexpr bool SYM = MODE == GRAM || MODE == POLY;
+    constexpr bool B_MN = !SYM;
+    constexpr bool LOADS = MODE != GRAM;
+    constexpr uint32_t LOAD_BYTES = SYM ? PIECE : 2 * PIECE;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
+    uint64_t* full = bars;
+    uint64_t* empty = bars + STAGES;
+    uint64_t* tfull = bars + 2 * STAGES;
+    uint64_t* tempty = tfull + NACC;
+    uint64_t* fin = tempty + NACC;
+    uint64_t* ebar = fin + 1;                      // [EPI_WARPS][2]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ebar + 2 * EPI_WARPS);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        for (int a = 0; a < NACC; ++a) {
+            mbar_init(smem_u32(&tfull[a]), 1);
+            mbar_init(smem_u32(&tempty[a]), 2 * EPI_WARPS);
+        }
+        mbar_init(smem_u32(fin), 1);
+        for (int i = 0; i < 2 * EPI_WARPS; ++i) mbar_init(smem_u32(&ebar[i]), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    const int per = tiles_per_matrix(args, SYM);
+    const int total = per * args.batch;
+    const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(nclusters_x());
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            tma_prefetch_desc(&tmA);
+            tma_prefetch_desc(&tmB);
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = cid; t < total && ok; t += ncl) {
+                const Tile tl = decode<SYM>(t, args, per);
+                const int a_row = tl.i * BT + static_cast<int>(rank) * 128;
+                const int b_row = tl.j * BT + static_cast<int>(rank) * 128;
+                for (int kb = 0; kb < args.kb; ++kb) {
+                    if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.err)) { ok = false; break; }
+                    const uint32_t fb_local = smem_u32(&full[stage]);
+                    if (leader) mbar_arrive_expect_tx(fb_local, 2 * STAGE_BYTES);
+                    const uint32_t fb = map_to_cta(fb_local, 0);
+                    const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_STAGE;
+                    tma_load_3d_pair(sa, &tmA, fb, kb * BK, a_row, tl.z);
+                    if constexpr (B_MN) {          // two boxes of 64 K rows x 64 columns
+                        tma_load_3d_pair(sb, &tmB, fb, b_row, kb * BK, tl.z);
+                        tma_load_3d_pair(sb + 8192, &tmB, fb, b_row + 64, kb * BK, tl.z);
+                    } else {
+                        tma_load_3d_pair(sb, &tmB, fb, kb * BK, b_row, tl.z);
+                    }
+                    ++issued;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (leader) {       // the loads of both CTAs complete on this CTA's barriers
+                const int pending = issued < STAGES ? issued : STAGES;
+                for (int j = 1; j <= pending; ++j) {
+                    int s = stage - j;
+                    uint32_t ph = phase;
+                    if (s < 0) { s += STAGES; ph ^= 1u; }
+                    const uint64_t t0 = globaltimer_ns();
+                    while (!mbar_try_wait(smem_u32(&full[s]), ph)) {
+                        if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(args.err, DEV_ERR_TIMEOUT); break; }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // ----------------------------------------------------------------- MMA
+        if (leader) {
+            constexpr uint32_t idesc = idesc_f16(BT, BT, B_MN);
+            int stage = 0, it = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int t = cid; t < total && ok; t += ncl, ++it) {
+                const int acc = it & 1;
+                const uint32_t use = static_cast<uint32_t>(it >> 1);
+                if (!mbar_wait(smem_u32(&tempty[acc]), (use & 1u) ^ 1u, abort_flag, args.err)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BT);
+                for (int kb = 0; kb < args.kb; ++kb) {
+                    if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, args.err)) { ok = false; break; }
+                    tc_fence_after();
+                    __syncwarp();
+                    if (elect_one()) {
+                        const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
+                        const uint64_t adesc = smem_desc_sw128(sa);
+                        const uint64_t bdesc = B_MN ? smem_desc_sw128_mn(sa + A_STAGE, 8192) : smem_desc_sw128(sa + A_STAGE);
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)        // 16 of K: 32 bytes of a row, or 16 rows of 128 bytes
+                            mma_f16_pair(d_tmem, adesc + 2ull * kk, bdesc + (B_MN ? 128ull : 2ull) * kk, idesc,
+                                         (kb > 0 || kk > 0) ? 1u : 0u);
+                        tc_commit_pair_multicast(smem_u32(&empty[stage]), 0x3);
+                        if (kb == args.kb - 1) tc_commit_pair_multicast(smem_u32(&tfull[acc]), 0x3);
+                    }
+                    __syncwarp();
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            __syncwarp();
+            if (elect_one()) tc_commit_pair_multicast(smem_u32(fin), 0x3);
+            __syncwarp();
+        }
+        // both CTAs: every MMA writing this CTA's TMEM has completed
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(fin), 0)) {
+            if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(args.err, DEV_ERR_TIMEOUT); break; }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------------------ epilogue
+        const int quarter = warp & 3, half = (warp - 2) >> 2, ew = warp - 2;
+        uint8_t* buf0 = smem + EPI_OFF + ew * 2 * BUF;
+        int it = 0;
+        uint32_t asked = 0, used = 0;              // pieces whose inputs were asked for, and taken
+        for (int t = cid; t < total; t += ncl, ++it) {
+            const Tile tl = decode<SYM>(t, args, per);
+            const int row0 = tl.i * BT + static_cast<int>(rank) * 128 + quarter * 32;
+            const int col0 = tl.j * BT + half * 128;
+            // this warp's pieces [first, last) of four along its 128 columns
+            int last = row0 < args.rows ? min(4, (args.cols - col0 + 31) / 32) : 0;
+            int first = SYM && col0 < row0 ? (row0 - col0) / 32 : 0;
+            if (last < first) last = first;
+            const int acc = it & 1;
+            const uint32_t use = static_cast<uint32_t>(it >> 1);
+            auto ask = [&](int c) {
+                const uint32_t b = asked & 1u;
+                if (lane == 0) {
+                    bulk_wait_read0();              // the buffer's last store has read it
+                    const uint32_t bar = smem_u32(&ebar[2 * ew + b]), dst = smem_u32(buf0 + b * BUF);
+                    mbar_arrive_expect_tx(bar, LOAD_BYTES);
+                    tma_load_3d(dst, &tmIn, bar, col0 + 32 * c, row0, tl.z);
+                    if constexpr (!SYM) tma_load_3d(dst + PIECE, &tmInL, bar, col0 + 32 * c, row0, tl.z);
+                }
+                ++asked;
+            };
+            if (LOADS && first < last) {
+                __syncwarp();
+                ask(first);
+            }
+            if (!mbar_wait(smem_u32(&tfull[acc]), use & 1u, abort_flag, args.err)) break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                   static_cast<uint32_t>(acc * BT + half * 128);
+            bool ok = true;
+#pragma unroll 1
+            for (int c = first; c < last; ++c) {
+                uint32_t v[32];
+                tmem_ld32(tbase + 32 * c, v);
+                tmem_ld_wait();
+                const uint32_t b = LOADS ? used & 1u : static_cast<uint32_t>(c) & 1u;
+                uint8_t* buf = buf0 + b * BUF;
+                const int x = col0 + 32 * c;
+                if constexpr (LOADS) {
+                    if (c + 1 < last) ask(c + 1);
+                    if (!mbar_wait(smem_u32(&ebar[2 * ew + b]), (used >> 1) & 1u, abort_flag, args.err)) { ok = false; break; }
+                    ++used;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const uint4 h = *reinterpret_cast<const uint4*>(buf + chunk_at(lane, q));
+                        const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+                        uint32_t lw[4] = {0, 0, 0, 0};
+                        if constexpr (!SYM) {
+                            const uint4 l = *reinterpret_cast<const uint4*>(buf + PIECE + chunk_at(lane, q));
+                            lw[0] = l.x; lw[1] = l.y; lw[2] = l.z; lw[3] = l.w;
+                        }
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            float2 in = unpack_half2(hw[w]);
+                            if constexpr (!SYM) {
+                                const float2 lo = unpack_half2(lw[w]);
+                                in.x += lo.x * 0x1p-11f;
+                                in.y += lo.y * 0x1p-11f;
+                            }
+                            uint32_t& v0 = v[8 * q + 2 * w];
+                            uint32_t& v1 = v[8 * q + 2 * w + 1];
+                            v0 = __float_as_uint(args.alpha * in.x + args.beta * __uint_as_float(v0));
+                            v1 = __float_as_uint(args.alpha * in.y + args.beta * __uint_as_float(v1));
+                        }
+                    }
+                    __syncwarp();
+                } else {
+                    if (lane == 0) bulk_wait_read0();
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(args.beta * __uint_as_float(v[j]));
+                }
+                if constexpr (MODE == LAST) {
+                    // the result's piece, transposed for a tall matrix
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int w = 0; w < 4; ++w)
+                            p[w] = pack_bf16x2(__uint_as_float(v[8 * q + 2 * w]), __uint_as_float(v[8 * q + 2 * w + 1]));
+                        if (!args.tall) {
+                            *reinterpret_cast<uint4*>(buf + chunk_at(lane, q)) = make_uint4(p[0], p[1], p[2], p[3]);
+                        } else {
+#pragma unroll
+                            for (int w = 0; w < 8; ++w)
+                                *reinterpret_cast<uint16_t*>(buf + elem_at(8 * q + w, lane)) =
+                                    static_cast<uint16_t>(p[w >> 1] >> (16 * (w & 1)));
+                        }
+                    }
+                    const int oy = args.tall ? x : row0, ox = args.tall ? row0 : x;      // piece's corner in the result
+                    if (args.tma_out) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            store_3d(&tmOut, smem_u32(buf), ox, oy, tl.z);
+                            bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        uint16_t* o = reinterpret_cast<uint16_t*>(args.out) + tl.z * args.out_mat;
+                        if (ox + lane < args.n)
+                            for (int y = 0; y < 32 && oy + y < args.m; ++y)
+                                o[(oy + y) * args.out_row + ox + lane] =
+                                    *reinterpret_cast<const uint16_t*>(buf + elem_at(y, lane));
+                        __syncwarp();
+                    }
+                } else {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int w = 0; w < 16; ++w)
+                        p[w] = pack_half2(__uint_as_float(v[2 * w]), __uint_as_float(v[2 * w + 1]));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        *reinterpret_cast<uint4*>(buf + chunk_at(lane, q)) =
+                            make_uint4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+                    if constexpr (SYM) {
+                        if (x > row0) {
+#pragma unroll
+                            for (int w = 0; w < 32; ++w)
+                                *reinterpret_cast<uint16_t*>(buf + PIECE + elem_at(w, lane)) =
+                                    static_cast<uint16_t>(p[w >> 1] >> (16 * (w & 1)));
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t l[4];
+#pragma unroll
+                            for (int w = 0; w < 4; ++w) {
+                                const float2 h = unpack_half2(p[4 * q + w]);
+                                l[w] = pack_half2((__uint_as_float(v[8 * q + 2 * w]) - h.x) * 0x1p11f,
+                                                  (__uint_as_float(v[8 * q + 2 * w + 1]) - h.y) * 0x1p11f);
+                            }
+                            *reinterpret_cast<uint4*>(buf + PIECE + chunk_at(lane, q)) = make_uint4(l[0], l[1], l[2], l[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        store_3d(&tmOut, smem_u32(buf), x, row0, tl.z);
+                        if constexpr (SYM) {
+                            if (x > row0) store_3d(&tmOut, smem_u32(buf + PIECE), row0, x, tl.z);
+                        } else {
+                            store_3d(&tmOutL, smem_u32(buf + PIECE), x, row0, tl.z);
+                        }
+                        bulk_commit();
+                    }
+                }
+            }
+            if (!ok) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(map_to_cta(smem_u32(&tempty[acc]), 0));
+        }
+        if (lane == 0) {
+            while (used != asked) {                // a wait gave up: this warp's loads end before its buffers do
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait(smem_u32(&ebar[2 * ew + (used & 1u)]), (used >> 1) & 1u)) {
+                    if (globaltimer_ns() - t0 > kWaitLimitNs) { set_dev_error(args.err, DEV_ERR_TIMEOUT); break; }
+                }
+                ++used;
+            }
+            bulk_wait0();
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    }
+}
+
+// ------------------------------------------------------------- preparation
+constexpr int NORM_BLOCKS = 64;               // at most, per matrix
+
+struct Source {
+    const void* g;
+    long long row, mat;
+    int m, n, f32, vec;
+};
+
+__device__ __forceinline__ float at(const Source& s, const void* base, long long i) {
+    return s.f32 ? static_cast<const float*>(base)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
+}
+
+// Sums of squares over fp32's whole range: three partial sums, of values above 2^40 (scaled by
+// 2^-88), below 2^-50 (by 2^100) and between, none of which can overflow or vanish.
+struct Squares {
+    float big = 0.f, mid = 0.f, small = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float a = fabsf(x);
+        if (a > 0x1p40f) big += (x * 0x1p-88f) * (x * 0x1p-88f);
+        else if (a < 0x1p-50f) small += (x * 0x1p100f) * (x * 0x1p100f);
+        else mid += x * x;                     // a NaN lands here
+    }
+};
+
+__global__ void __launch_bounds__(256) norm_kernel(const Source s, float* part) {
+    __shared__ float sh[8][3];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const size_t es = s.f32 ? 4 : 2;
+    const uint8_t* g = static_cast<const uint8_t*>(s.g) + static_cast<long long>(blockIdx.y) * s.mat * es;
+    Squares q;
+    for (int i = blockIdx.x * 8 + warp; i < s.m; i += gridDim.x * 8) {
+        const uint8_t* row = g + i * s.row * es;
+        if (s.vec) {
+            const int nv = s.n / (16 / static_cast<int>(es));
+#pragma unroll 4
+            for (int v = lane; v < nv; v += 32) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4*>(row) + v);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (s.f32) {
+                        q.add(__uint_as_float(w[k]));
+                    } else {
+                        q.add(bf16lo(w[k]));
+                        q.add(bf16hi(w[k]));
+                    }
+                }
+            }
+        } else {
+            for (int j = lane; j < s.n; j += 32) q.add(at(s, row, j));
+        }
+    }
+    float v[3] = {q.big, q.mid, q.small};
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+        if (lane == 0) sh[warp][k] = v[k];
+    }
+    __syncthreads();
+    if (threadIdx.x < 3) {
+        float t = 0.f;
+        for (int w = 0; w < 8; ++w) t += sh[w][threadIdx.x];
+        part[(static_cast<long long>(blockIdx.y) * gridDim.x + blockIdx.x) * 3 + threadIdx.x] = t;
+    }
+}
+
+// X = G / (|G| + eps) as H + L 2^-11 times 2^xs, transposed for a tall G; a 64 x 64 tile per block.
+// Columns past q up to the padded width are zero.
+__global__ void __launch_bounds__(256)
+scale_kernel(const Source s, const float* part, int nb, double eps, float xscale, int tall, int tiles_n, __half* H,
+             __half* L, int r, int qp) {
+    __shared__ float tile[64][65];
+    __shared__ float f1, f2;
+    const int z = blockIdx.y;
+    const int ti = blockIdx.x / tiles_n, tj = blockIdx.x - ti * tiles_n;      // tile of G
+    if (threadIdx.x < 32) {
+        double big = 0, mid = 0, small = 0;
+        for (int i = threadIdx.x; i < nb; i += 32) {
+            const float* p = part + (static_cast<long long>(z) * nb + i) * 3;
+            big += p[0];
+            mid += p[1];
+            small += p[2];
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            big += __shfl_xor_sync(0xffffffffu, big, o);
+            mid += __shfl_xor_sync(0xffffffffu, mid, o);
+            small += __shfl_xor_sync(0xffffffffu, small, o);
+        }
+        if (threadIdx.x == 0) {
+            const double norm = sqrt(big * 0x1p176 + mid + small * 0x1p-200) + eps;
+            // x / norm in two fp32 factors, the first a power of two: no intermediate leaves fp32's range
+            int e = 0;
+            frexp(norm, &e);
+            int k = -e;
+            k = k < -126 ? -126 : (k > 127 ? 127 : k);
+            const bool fine = norm > 0.0 && norm < INFINITY;
+            f1 = fine ? static_cast<float>(ldexp(1.0, k)) : (norm == 0.0 ? 0.0f : NAN);     // zeros stay zeros
+            f2 = fine ? static_cast<float>(xscale / (norm * ldexp(1.0, k))) : 1.0f;
+        }
+    }
+    const size_t es = s.f32 ? 4 : 2;
+    const uint8_t* g = static_cast<const uint8_t*>(s.g) + static_cast<long long>(z) * s.mat * es;
+    const int lr = threadIdx.x >> 2, seg = (threadIdx.x & 3) * 16;
+    const int i = ti * 64 + lr, j0 = tj * 64 + seg;
+    const uint8_t* row = g + static_cast<long long>(i) * s.row * es;
+    if (s.vec && i < s.m && j0 + 16 <= s.n) {
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) {
+            if (s.f32) {
+                const float4 x = __ldg(reinterpret_cast<const float4*>(row) + (j0 + v) / 4);
+                tile[lr][seg + v] = x.x; tile[lr][seg + v + 1] = x.y; tile[lr][seg + v + 2] = x.z; tile[lr][seg + v + 3] = x.w;
+            } else {
+                const uint2 x = __ldg(reinterpret_cast<const uint2*>(row) + (j0 + v) / 4);
+                tile[lr][seg + v] = bf16lo(x.x); tile[lr][seg + v + 1] = bf16hi(x.x);
+                tile[lr][seg + v + 2] = bf16lo(x.y); tile[lr][seg + v + 3] = bf16hi(x.y);
+            }
+        }
+    } else {
+        for (int v = 0; v < 16; ++v) tile[lr][seg + v] = i < s.m && j0 + v < s.n ? at(s, row, j0 + v) : 0.0f;
+    }
+    __syncthreads();
+    const int xr = (tall ? tj : ti) * 64 + lr, xc = (tall ? ti : tj) * 64 + seg;
+    if (xr >= r) return;
+    uint32_t h[8], l[8];
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        float x[2];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) x[w] = (tall ? tile[seg + 2 * v + w][lr] : tile[lr][seg + 2 * v + w]) * f1 * f2;
+        h[v] = pack_half2(x[0], x[1]);
+        const float2 b = unpack_half2(h[v]);
+        l[v] = pack_half2((x[0] - b.x) * 0x1p11f, (x[1] - b.y) * 0x1p11f);
+    }
+    const long long at_ = (static_cast<long long>(z) * r + xr) * qp + xc;
+    uint4* ho = reinterpret_cast<uint4*>(H + at_);
+    uint4* lo = reinterpret_cast<uint4*>(L + at_);
+    ho[0] = make_uint4(h[0], h[1], h[2], h[3]);
+    ho[1] = make_uint4(h[4], h[5], h[6], h[7]);
+    lo[0] = make_uint4(l[0], l[1], l[2], l[3]);
+    lo[1] = make_uint4(l[4], l[5], l[6], l[7]);
+}
+
+// ------------------------------------------------------------------- host
+struct Shape {
+    int r, q, rp, qp;
+    bool tall;
+};
+Shape shape(int m, int n) {
+    Shape s;
+    s.tall = m > n;
+    s.r = s.tall ? n : m;
+    s.q = s.tall ? m : n;
+    s.rp = (s.r + 63) / 64 * 64;
+    s.qp = (s.q + 63) / 64 * 64;
+    return s;
+}
+
+struct Layout {
+    int group;                       // matrices in flight
+    size_t h[2], l, a, b, part, end;
+};
+size_t up(size_t x) { return (x + 1023) / 1024 * 1024; }
+// Matrices are worked on in groups whose buffers stay within 2 GiB (one matrix at least).
+Layout layout(int batch, int m, int n) {
+    const Shape s = shape(m, n);
+    const size_t x = static_cast<size_t>(s.r) * s.qp * 2, sq = static_cast<size_t>(s.r) * s.rp * 2;
+    const size_t each = 3 * x + 2 * sq + NORM_BLOCKS * 12;
+    size_t g = (size_t(2) << 30) / each;
+    g = g < 1 ? 1 : (g > 16384 ? 16384 : g);
+    if (g > static_cast<size_t>(batch)) g = batch;
+    const size_t rounds = (batch + g - 1) / g;
+    g = (batch + rounds - 1) / rounds;            // rounds of equal size
+    Layout l;
+    l.group = static_cast<int>(g);
+    size_t o = 0;
+    auto take = [&](size_t bytes) { const size_t at_ = o; o = up(o + bytes); return at_; };
+    l.h[0] = take(g * x);
+    l.h[1] = take(g * x);
+    l.l = take(g * x);
+    l.a = take(g * sq);
+    l.b = take(g * sq);
+    l.part = take(g * NORM_BLOCKS * 12);
+    l.end = o;
+    return l;
+}
+
+cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, void* base, long long cols, long long rows, long long mats,
+                   long long row_bytes, long long mat_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    cuuint64_t gdim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
+    cuuint64_t gstride[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(mat_bytes)};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(map, type, 3, base, gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// fp16 [mats, rows, cols] contiguous: boxes of 64 columns for the products, pieces of 32 x 32 for the epilogue.
+cudaError_t operand(CUtensorMap* map, void* base, int cols, int rows, int mats, int box_rows) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols, rows, mats, cols * 2LL,
+                  static_cast<long long>(rows) * cols * 2, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+cudaError_t pieces(CUtensorMap* map, void* base, int cols, int rows, int mats) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, base, cols, rows, mats, cols * 2LL,
+                  static_cast<long long>(rows) * cols * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <int MODE>
+cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in, const CUtensorMap& in_l,
+                        const CUtensorMap& out, const CUtensorMap& out_l, const Args& args, int sms, cudaStream_t st) {
+    static bool set[kMaxDevices];
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(gemm_kernel<MODE>), SMEM_BYTES, set);
+    if (e != cudaSuccess) return e;
+    const long long tiles = static_cast<long long>(MODE <= POLY ? args.R * (args.R + 1) / 2 : args.R * args.C) * args.batch;
+    const int clusters = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+    gemm_kernel<MODE><<<2 * clusters, THREADS, SMEM_BYTES, st>>>(a, b, in, in_l, out, out_l, args);
+    count_launch();
+    return cudaGetLastError();
+}
+
+}  // namespace ortho
+
+size_t ortho_ws_bytes(int batch, int m, int n) { return ortho::layout(batch, m, n).end; }
+
+cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) {
+    using namespace ortho;
+    const Shape s = shape(o.m, o.n);
+    const Layout l = layout(o.batch, o.m, o.n);
+    int sms = 0;
+    cudaError_t e = num_sms(&sms);
+    if (e != cudaSuccess) return e;
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    const size_t es = o.f32 ? 4 : 2;
+    const bool vec = (reinterpret_cast<uintptr_t>(o.g) & 15u) == 0 && o.g_row * es % 16 == 0 && o.g_mat * es % 16 == 0 &&
+                     o.n * es % 16 == 0;
+    const bool tma_out = (reinterpret_cast<uintptr_t>(o.out) & 15u) == 0 && o.out_row % 8 == 0 && o.out_mat % 8 == 0;
+    for (int z0 = 0; z0 < o.batch; z0 += l.group) {
+        const int nb = o.batch - z0 < l.group ? o.batch - z0 : l.group;
+        const Source src{static_cast<const uint8_t*>(o.g) + z0 * o.g_mat * static_cast<long long>(es), o.g_row, o.g_mat, o.m,
+                         o.n, o.f32, vec};
+        float* part = reinterpret_cast<float*>(w + l.part);
+        int blocks = (o.m + 7) / 8;
+        blocks = blocks > NORM_BLOCKS ? NORM_BLOCKS : blocks;
+        norm_kernel<<<dim3(blocks, nb), 256, 0, st>>>(src, part);
+        count_launch();
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        __half* H[2] = {reinterpret_cast<__half*>(w + l.h[0]), reinterpret_cast<__half*>(w + l.h[1])};
+        __half* L = reinterpret_cast<__half*>(w + l.l);
+        // tiles of G; for X's padded width the last ones reach past it
+        const int tm = (s.tall ? s.qp : s.rp) / 64, tn = (s.tall ? s.rp : s.qp) / 64;
+        scale_kernel<<<dim3(tm * tn, nb), 256, 0, st>>>(src, part, blocks, o.eps, o.scales.x, s.tall, tn, H[0], L, s.r, s.qp);
+        count_launch();
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+
+        CUtensorMap xk[2], xn[2], xp[2], lp, ak, ap, bk, bp, op;
+        void *A = w + l.a, *B = w + l.b;
+        for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+            e = operand(&xk[i], H[i], s.qp, s.r, nb, 128);
+            if (e == cudaSuccess) e = operand(&xn[i], H[i], s.qp, s.r, nb, 64);
+            if (e == cudaSuccess) e = pieces(&xp[i], H[i], s.qp, s.r, nb);
+        }
+        if (e == cudaSuccess) e = pieces(&lp, L, s.qp, s.r, nb);
+        if (e == cudaSuccess) e = operand(&ak, A, s.rp, s.r, nb, 128);
+        if (e == cudaSuccess) e = pieces(&ap, A, s.rp, s.r, nb);
+        if (e == cudaSuccess) e = operand(&bk, B, s.rp, s.r, nb, 128);
+        if (e == cudaSuccess) e = pieces(&bp, B, s.rp, s.r, nb);
+        __nv_bfloat16* out = o.out + z0 * o.out_mat;
+        op = xp[0];
+        if (e == cudaSuccess && tma_out)
+            e = encode(&op, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, out, o.n, o.m, nb, o.out_row * 2, o.out_mat * 2, 32, 32,
+                       CU_TENSOR_MAP_SWIZZLE_64B);
+        if (e != cudaSuccess) return e;
+
+        Args g{};
+        g.R = (s.r + BT - 1) / BT;
+        g.batch = nb;
+        g.rows = s.r;
+        g.m = o.m;
+        g.n = o.n;
+        g.tall = s.tall;
+        g.out = out;
+        g.out_row = o.out_row;
+        g.out_mat = o.out_mat;
+        g.tma_out = tma_out;
+        g.err = dev_error_ptr();
+        const OrthoScales& sc = o.scales;
+        int cur = 0;
+        for (int k = 0; k < o.steps; ++k, cur ^= 1) {
+            const float ca = o.coefs[3 * k], cb = o.coefs[3 * k + 1], cc = o.coefs[3 * k + 2];
+            const bool last = k == o.steps - 1;
+            Args a = g;
+            a.C = a.R;
+            a.cols = s.rp;
+            a.kb = s.qp / BK;
+            a.beta = sc.a / (sc.x * sc.x);
+            e = launch_gemm<GRAM>(xk[cur], xk[cur], ap, ap, ap, ap, a, sms, st);
+            if (e != cudaSuccess) return e;
+            a.kb = s.rp / BK;
+            a.alpha = cb * (sc.b / sc.a);
+            a.beta = cc * (sc.b / (sc.a * sc.a));
+            e = launch_gemm<POLY>(ak, ak, ap, ap, bp, bp, a, sms, st);
+            if (e != cudaSuccess) return e;
+            a.C = (s.qp + BT - 1) / BT;
+            a.cols = s.qp;
+            a.alpha = ca;
+            a.beta = 1.0f / sc.b;
+            if (!last) {
+                e = launch_gemm<STEP>(bk, xn[cur], xp[cur], lp, xp[cur ^ 1], lp, a, sms, st);
+            } else {
+                a.alpha *= o.scale / sc.x;
+                a.beta *= o.scale / sc.x;
+                e = launch_gemm<LAST>(bk, xn[cur], xp[cur], lp, op, op, a, sms, st);
+            }
+            if (e != cudaSuccess) return e;
+        }
+    }
+    return cudaSuccess;
+}
+
+}  // namespace fs

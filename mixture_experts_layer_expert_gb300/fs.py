@@ -60,6 +60,11 @@ class BalanceDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "gate", "n_seqs")] + [("coef", ctypes.c_float)]
 
 
+class OrthogonalizeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "m", "n", "dtype", "steps")] + [
+        ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("coefs", ctypes.c_float * 48)]
+
+
 class LatentCache(ctypes.Structure):
     _fields_ = [("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
@@ -114,6 +119,8 @@ _SIGS = {
                                              _VP, ctypes.POINTER(BlockGrads), _VP, _SZ, _VP]),
     "fs_train_saved_routing": (_I32, [ctypes.POINTER(LayerDesc), _I32, _I32, _VP, ctypes.POINTER(_VP),
                                       ctypes.POINTER(_VP)]),
+    "fs_orthogonalize_ws_bytes": (_SZ, [ctypes.POINTER(OrthogonalizeDesc)]),
+    "fs_orthogonalize": (_I32, [ctypes.POINTER(OrthogonalizeDesc), _VP, _I64, _I64, _VP, _I64, _I64, _VP, _SZ, _VP]),
     "fs_balance_ws_bytes": (_SZ, [ctypes.POINTER(BalanceDesc)]),
     "fs_balance_loss": (_I32, [ctypes.POINTER(BalanceDesc), _VP, _I64, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                _SZ, _VP]),
@@ -613,6 +620,34 @@ def fs_balance_loss_backward(desc: BalanceDesc, logits, counts, tokens, d_loss, 
                                           ds[0] if desc.T > 1 else max(ds[0], desc.E), st), what)
 
 
+NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5      # coefficients (a, b, c) of the usual five steps
+
+
+def make_orthogonalize(batch: int, m: int, n: int, dtype: str = "f32", scale: float = 1.0, coefs=NEWTON_SCHULZ,
+                       eps: float = 1e-7) -> OrthogonalizeDesc:
+    """Steps of (a, b, c) on a batch of [m, n] matrices of type dtype ("f32" or "bf16")."""
+    flat = [float(x) for abc in coefs for x in abc]
+    if len(flat) > 48 or len(flat) != 3 * len(coefs):
+        raise FsError(1, "make_orthogonalize", "%d steps, at most 16 of three coefficients" % len(coefs))
+    return OrthogonalizeDesc(batch, m, n, DTYPES[dtype], len(coefs), eps, scale, (ctypes.c_float * 48)(*flat))
+
+
+def fs_orthogonalize_ws_bytes(desc: OrthogonalizeDesc) -> int:
+    return int(lib().fs_orthogonalize_ws_bytes(ctypes.byref(desc)))
+
+
+def fs_orthogonalize(desc: OrthogonalizeDesc, g, out, ws, stream=None):
+    """out [batch, m, n] bf16 = the orthogonalised g [batch, m, n] (fp32 or bf16 as desc says; any row and matrix
+    strides); ws: fs_orthogonalize_ws_bytes(desc) bytes."""
+    dev, st = _here(stream)
+    what, shape = "fs_orthogonalize", (desc.batch, desc.m, desc.n)
+    gp, gs = _operand(what + " g", g, shape, dev, torch.float32 if desc.dtype == FS_F32 else torch.bfloat16)
+    op, os_ = _operand(what + " out", out, shape, dev)
+    wp, _ = _operand(what + " ws", ws, ws.shape, dev, torch.uint8, False)
+    row = lambda s: s[1] if desc.m > 1 else max(s[1], desc.n)
+    _check(lib().fs_orthogonalize(desc, gp, row(gs), gs[0], op, row(os_), os_[0], wp, ws.numel(), st), what)
+
+
 class FarSkipTrainer:
     """Forward (keeping what the backward reads) and backward of an L-block
     FarSkip MoE stack on one GPU (bf16, MoE wirings): two library calls."""
@@ -715,6 +750,27 @@ class FarSkipTrainer:
                                                   extra[blk], self.cfg.E, st), "fs_balance_loss_backward")
         _check(lib().fs_farskip_stack_backward_aux(*head, extra, *tail), "fs_farskip_stack_backward_aux")
         return out, self.grads
+
+    def orthogonalized(self, names=("dW1", "dW2", "dW3"), scale: float = 1.0, coefs=NEWTON_SCHULZ, eps: float = 1e-7,
+                       stream=None):
+        """The orthogonalised updates (bf16) of every block's weight gradients of these names: a list of dicts like
+        self.grads.  Each expert's matrix is one of a batch."""
+        updates = []
+        for blk in range(self.L):
+            upd = {}
+            for name in names:
+                g = self.grads[blk][name]
+                g3 = g if g.dim() == 3 else g[None]
+                desc = make_orthogonalize(*g3.shape, "f32", scale, coefs, eps)
+                need = fs_orthogonalize_ws_bytes(desc)
+                if need == 0:
+                    raise FsError(1, "fs_orthogonalize_ws_bytes")
+                if getattr(self, "ws_o", None) is None or self.ws_o.numel() < need:
+                    self.ws_o = torch.empty(need, dtype=torch.uint8, device=g.device)
+                upd[name] = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+                fs_orthogonalize(desc, g3, upd[name].view(g3.shape), self.ws_o, stream)
+            updates.append(upd)
+        return updates
 
 
 # ----------------------------------------------------------------- attention
