@@ -60,7 +60,7 @@ fs_status balance_args(const fs_balance_desc* d, const float* logits, int64_t ro
 }
 
 // ---- orthogonalised updates
-constexpr int kMaxSteps = 16, kMaxDim = 16384;
+constexpr int kMaxDim = 16384;
 
 // Powers of two for X, A and B, from the largest singular value that the steps can
 // reach: s <= 1 at first (the Frobenius norm is 1), then max |a s + b s^3 + c s^5|.
@@ -93,7 +93,7 @@ fs_status check_ortho(const fs_orthogonalize_desc* d, OrthoScales* sc) {
     if (d->dtype < FS_BF16 || d->dtype > FS_MXFP4) return FS_ERR_INVALID_ARG;
     if (!std::isfinite(d->scale) || !(d->eps >= 0.f) || !std::isfinite(d->eps)) return FS_ERR_INVALID_ARG;
     if (d->dtype != FS_BF16 && d->dtype != FS_F32) return FS_ERR_UNSUPPORTED;
-    if (d->m > kMaxDim || d->n > kMaxDim || d->steps > kMaxSteps) return FS_ERR_UNSUPPORTED;
+    if (d->m > kMaxDim || d->n > kMaxDim || d->steps > kMaxOrthoSteps) return FS_ERR_UNSUPPORTED;
     return ortho_scales(d, sc);
 }
 

@@ -11,8 +11,9 @@
 //
 // Both directions read every logit once and are bound by HBM; the work per logit is
 // one exponential (two and a reciprocal for the sigmoids).  A warp owns a token: its
-// row sits in registers (E <= 512: 16 a lane), two tokens in flight, max and sums by
-// shuffles.  Forward: the token axis is cut into equal ranges, one per block, whatever
+// row sits in registers (E <= 512: 16 a lane), 64 KB of rows in flight on an SM, max and sums by
+// shuffles.  Up to 1,024 rows of one sequence are one block's work, in one launch.  Otherwise,
+// forward: the token axis is cut into equal ranges, one per block, whatever
 // the sequences' lengths; what a block finds of a sequence goes to slot (block + sequence)
 // of the workspace, which no other pair has because both only grow along the axis.  A second
 // kernel adds a sequence's slots in order.  No float atomics: results repeat bit for bit.
@@ -22,10 +23,16 @@
 namespace fs {
 namespace bal {
 
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
+// Warps of a block and tokens a warp has in flight, by elements a lane: one block fills an SM.
+template <int EPL>
+struct Cfg {
+    static constexpr int WARPS = EPL == 16 ? 16 : 32;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int U = EPL == 4 ? 4 : 2;
+};
 constexpr int FIN_E = 32;                 // experts per block of the second kernel
-constexpr int FIN_P = 16;                 // slots it reads at a time
+constexpr int FIN_P = 32;                 // slots it reads at a time
+constexpr int ONE_ROWS = 1024;            // at most this many rows of one sequence in one block
 
 struct Args {
     const float* z;
@@ -134,15 +141,18 @@ __device__ __forceinline__ float finish(const Args& a, int q, int e, float sum, 
                  : 0.0f;
 }
 
-template <int EPL, bool VEC, bool SIG>
-__global__ void __launch_bounds__(THREADS)
+// ONE: a single block over one sequence, which finishes it too.
+template <int EPL, bool VEC, bool SIG, bool ONE>
+__global__ void __launch_bounds__(Cfg<EPL>::THREADS, 1)
 piece_kernel(const Args a) {
+    constexpr int WARPS = Cfg<EPL>::WARPS, THREADS = Cfg<EPL>::THREADS, U = Cfg<EPL>::U;
     __shared__ float sums[WARPS][32 * EPL];
     __shared__ int cnt[32 * EPL];
     __shared__ int ntok;
+    __shared__ float terms[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = blockIdx.x * a.chunk, c1 = a.T - c0 < a.chunk ? a.T : c0 + a.chunk;     // no sum past an int
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
+    if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
     float bias[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -151,9 +161,13 @@ piece_kernel(const Args a) {
     }
     for (int q = a.cu ? first_seq(a.cu, a.S, c0) : 0; q < a.S; ++q) {
         const int q0 = a.cu ? a.cu[q] : 0, q1 = a.cu ? a.cu[q + 1] : a.T;
-        if (q0 >= c1) break;
-        const int lo = max(q0, c0), hi = min(q1, c1);
-        if (lo >= hi) continue;
+        if (!ONE && q0 >= c1) break;
+        int lo = max(q0, c0), hi = min(q1, c1);
+        if (ONE && (q0 < 0 || q1 < q0 || q1 > a.T)) {
+            if (threadIdx.x == 0) set_dev_error(a.err, DEV_ERR_OFFSETS);
+            lo = hi = 0;
+        }
+        if (!ONE && lo >= hi) continue;
         for (int e = threadIdx.x; e < a.E; e += THREADS) cnt[e] = 0;
         if (threadIdx.x == 0) ntok = 0;
         __syncthreads();
@@ -161,19 +175,19 @@ piece_kernel(const Args a) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) acc[j] = 0.0f;
         int n = 0;
-        for (int t0 = lo + warp; t0 < hi; t0 += 2 * WARPS) {
-            float v[2][EPL], rest[EPL];
-            bool on[2];
-            int pick[2];
+        for (int t0 = lo + warp; t0 < hi; t0 += U * WARPS) {
+            float v[U][EPL], rest[EPL];
+            bool on[U];
+            int pick[U];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int t = t0 + u * WARPS;
                 on[u] = t < hi && !(a.mask && a.mask[t] == 0);
                 pick[u] = on[u] && lane < a.k ? a.idx[static_cast<long long>(t) * a.k + lane] : -1;
                 if (on[u]) load_row<EPL, VEC>(a.z + t * a.z_row, a.E, lane, -INFINITY, v[u]);
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
                 if (!on[u]) continue;
                 ++n;
                 if (lane < a.k) {
@@ -191,6 +205,24 @@ piece_kernel(const Args a) {
         for (int j = 0; j < EPL; ++j) sums[warp][elem<VEC>(j, lane)] = acc[j];
         if (lane == 0) atomicAdd(&ntok, n);
         __syncthreads();
+        if constexpr (ONE) {
+            float term = 0.0f;
+            for (int e = threadIdx.x; e < a.E; e += THREADS) {
+                float s = sums[0][e];
+#pragma unroll
+                for (int w = 1; w < WARPS; ++w) s += sums[w][e];
+                term += finish(a, 0, e, s, cnt[e], ntok);
+            }
+            term = warp_sum(term);
+            if (lane == 0) terms[warp] = term;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                for (int w = 1; w < WARPS; ++w) term += terms[w];
+                a.tokens[0] = ntok;
+                *a.loss = a.coef * term;
+            }
+            return;
+        }
         const long long slot = static_cast<long long>(blockIdx.x) + q;
         for (int e = threadIdx.x; e < a.E; e += THREADS) {
             float s = sums[0][e];
@@ -214,6 +246,7 @@ finish_kernel(const Args a) {
     __shared__ bool last;
     const int x = threadIdx.x % FIN_E, y = threadIdx.x / FIN_E;
     const int e = blockIdx.x * FIN_E + x, q = blockIdx.y;
+    cudaGridDependencySynchronize();
     int q0 = a.cu ? a.cu[q] : 0, q1 = a.cu ? a.cu[q + 1] : a.T;
     if (q0 < 0 || q1 < q0 || q1 > a.T) {
         if (threadIdx.x == 0) set_dev_error(a.err, DEV_ERR_OFFSETS);
@@ -304,8 +337,9 @@ __device__ __forceinline__ void store_row(float* p, int E, int lane, const float
 }
 
 template <int EPL, bool VEC, bool SIG>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(Cfg<EPL>::THREADS, 1)
 backward_kernel(const BwdArgs a) {
+    constexpr int WARPS = Cfg<EPL>::WARPS, U = Cfg<EPL>::U;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = blockIdx.x * a.chunk, c1 = a.T - c0 < a.chunk ? a.T : c0 + a.chunk;     // no sum past an int
     const float g = (a.d_loss ? *a.d_loss : 1.0f) * a.coef / static_cast<float>(a.S);
@@ -332,18 +366,18 @@ backward_kernel(const BwdArgs a) {
             const int e = elem<VEC>(j, lane);
             f[j] = e < a.E ? unit * static_cast<float>(a.counts[static_cast<long long>(q) * a.E + e]) : 0.0f;
         }
-        for (int t0 = lo + warp; t0 < hi; t0 += 2 * WARPS) {
-            float v[2][EPL], rest[EPL];
-            bool in[2], on[2];
+        for (int t0 = lo + warp; t0 < hi; t0 += U * WARPS) {
+            float v[U][EPL], rest[EPL];
+            bool in[U], on[U];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
                 const int t = t0 + u * WARPS;
                 in[u] = t < hi;
                 on[u] = in[u] && !(a.mask && a.mask[t] == 0);
                 if (on[u]) load_row<EPL, VEC>(a.z + t * a.z_row, a.E, lane, -INFINITY, v[u]);
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < U; ++u) {
                 if (!in[u]) continue;
                 if (on[u]) {
 #pragma unroll
@@ -368,12 +402,11 @@ backward_kernel(const BwdArgs a) {
     }
 }
 
-// Rows a block takes: at least two for each warp, and enough blocks for three on each SM.
+// Rows a block takes, a multiple of what its warps hold at once (warps: a row each, in steps of 16): one block
+// on each SM, fewer where that would leave warps without a row.
 int chunk_rows(int T) {
-    const long long want = 152LL * 3;
-    long long c = (T + want - 1) / want;
-    c = (c + 2 * WARPS - 1) / (2 * WARPS) * (2 * WARPS);
-    return static_cast<int>(c);
+    const long long c = (static_cast<long long>(T) + 151) / 152;
+    return static_cast<int>((c + 31) / 32 * 32);
 }
 int blocks(int T) { return (T + chunk_rows(T) - 1) / chunk_rows(T); }
 int expert_blocks(int E) { return (E + FIN_E - 1) / FIN_E; }
@@ -403,31 +436,40 @@ bool vec_ok(const void* p, long long row, int E) {
 
 size_t balance_ws_bytes(int T, int E, int S) { return bal::layout(T, E, S).end; }
 
-#define FS_BALANCE(KERNEL, VEC, E, GRID, ARGS)                                                        \
-    do {                                                                                              \
-        if ((E) <= 128) KERNEL<4, VEC, SIG><<<GRID, bal::THREADS, 0, st>>>(ARGS);                      \
-        else if ((E) <= 256) KERNEL<8, VEC, SIG><<<GRID, bal::THREADS, 0, st>>>(ARGS);                 \
-        else KERNEL<16, VEC, SIG><<<GRID, bal::THREADS, 0, st>>>(ARGS);                                \
+// KERNEL<elements a lane, TAIL...> for E experts.
+#define FS_BALANCE(KERNEL, E, GRID, ARGS, ...)                                                              \
+    do {                                                                                                    \
+        if ((E) <= 128) KERNEL<4, __VA_ARGS__><<<GRID, bal::Cfg<4>::THREADS, 0, st>>>(ARGS);                 \
+        else if ((E) <= 256) KERNEL<8, __VA_ARGS__><<<GRID, bal::Cfg<8>::THREADS, 0, st>>>(ARGS);            \
+        else KERNEL<16, __VA_ARGS__><<<GRID, bal::Cfg<16>::THREADS, 0, st>>>(ARGS);                          \
     } while (0)
 
 template <bool SIG>
 static cudaError_t balance_fwd(const bal::Args& a, cudaStream_t st) {
-    if (bal::vec_ok(a.z, a.z_row, a.E)) FS_BALANCE(bal::piece_kernel, true, a.E, bal::blocks(a.T), a);
-    else FS_BALANCE(bal::piece_kernel, false, a.E, bal::blocks(a.T), a);
+    const bool vec = bal::vec_ok(a.z, a.z_row, a.E);
+    if (a.S == 1 && a.T <= bal::ONE_ROWS) {
+        if (vec) FS_BALANCE(bal::piece_kernel, a.E, 1, a, true, SIG, true);
+        else FS_BALANCE(bal::piece_kernel, a.E, 1, a, false, SIG, true);
+        count_launch();
+        return cudaGetLastError();
+    }
+    if (vec) FS_BALANCE(bal::piece_kernel, a.E, bal::blocks(a.T), a, true, SIG, false);
+    else FS_BALANCE(bal::piece_kernel, a.E, bal::blocks(a.T), a, false, SIG, false);
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    bal::finish_kernel<<<dim3(bal::expert_blocks(a.E), a.S), bal::FIN_E * bal::FIN_P, 0, st>>>(a);
+    // launched while the first kernel drains; it waits for that kernel's end before it reads
+    e = launch_after(bal::finish_kernel, dim3(bal::expert_blocks(a.E), a.S), bal::FIN_E * bal::FIN_P, 0, st, a);
     count_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 template <bool SIG>
 static cudaError_t balance_bwd(const bal::BwdArgs& a, cudaStream_t st) {
     if (bal::vec_ok(a.z, a.z_row, a.E) && bal::vec_ok(a.dz, a.dz_row, a.E))
-        FS_BALANCE(bal::backward_kernel, true, a.E, bal::blocks(a.T), a);
+        FS_BALANCE(bal::backward_kernel, a.E, bal::blocks(a.T), a, true, SIG);
     else
-        FS_BALANCE(bal::backward_kernel, false, a.E, bal::blocks(a.T), a);
+        FS_BALANCE(bal::backward_kernel, a.E, bal::blocks(a.T), a, false, SIG);
     count_launch();
     return cudaGetLastError();
 }
@@ -437,7 +479,8 @@ cudaError_t launch_balance(const BalanceArgs& b, void* ws, cudaStream_t st) {
     uint8_t* w = static_cast<uint8_t*>(ws);
     bal::Args a;
     a.z = b.z; a.z_row = b.z_row; a.bias = b.bias; a.idx = b.idx; a.mask = b.mask; a.cu = b.cu;
-    a.T = b.T; a.E = b.E; a.k = b.k; a.S = b.S; a.chunk = bal::chunk_rows(b.T);
+    a.T = b.T; a.E = b.E; a.k = b.k; a.S = b.S;
+    a.chunk = b.S == 1 && b.T <= bal::ONE_ROWS ? bal::ONE_ROWS : bal::chunk_rows(b.T);
     a.coef = b.coef;
     a.part = reinterpret_cast<float*>(w + l.part);
     a.part_c = reinterpret_cast<int32_t*>(w + l.part_c);

@@ -234,6 +234,7 @@ cudaError_t launch_balance_backward(const BalanceArgs& b, const float* d_loss, f
                                     cudaStream_t st);
 
 // ortho.cu: Newton-Schulz steps on a batch of matrices [m, n] (strides in elements)
+constexpr int kMaxOrthoSteps = 16;
 struct OrthoScales {
     float x, a, b;             // powers of two that X, A = X X^T and B = b A + c A A are stored with
 };
@@ -251,6 +252,9 @@ struct OrthoArgs {
 };
 size_t ortho_ws_bytes(int batch, int m, int n);
 cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st);
+// ortho_small.cu: a matrix in one cluster of blocks, all steps in one launch (no workspace)
+bool ortho_small_fits(int m, int n);
+cudaError_t launch_ortho_small(const OrthoArgs& o, cudaStream_t st);
 
 // rope.cu
 struct RopeTab;

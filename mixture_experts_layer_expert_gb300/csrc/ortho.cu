@@ -9,11 +9,15 @@
 // 485 for the usual coefficients), and with them any error in directions that G
 // does not have: gradients of experts with fewer tokens than rows have many.  X
 // rounded to bf16 between the steps is 10 to 30% off for such G, in fp16 1 to 4%.
-// So X is a pair of fp16 numbers H + L 2^-11 (22 bits), and the products read H only:
-// an error of H enters through B X, whose left side has no component outside G's own
-// directions, and the term a X is exact to 22 bits.  What remains is 0.1 to 0.2%, below
-// the rounding of a bf16 result.  A and B are fp16.  All three carry powers of two that
-// keep the largest values the coefficients allow below 2^15 (see OrthoScales); sums fp32.
+// So X is a pair of fp16 numbers H + L 2^-11 (22 bits) as long as the steps to come can
+// multiply by more than four, and the products read H only: an error of H enters through
+// B H, whose left side has no component outside G's own directions, and the term a X is
+// exact to 22 bits.  A and B are fp16, B's diagonal (its largest part once the rows are
+// nearly orthonormal) fp32 and applied to H in the epilogue.  What remains is 0.06 to 0.15%,
+// below the rounding of a bf16 result (without the diagonal 0.2%; with L until the last
+// step no better, with L only while the steps multiply by more than 16 0.25%).  All three
+// carry powers of two that keep the largest values the coefficients allow below 2^14 (see
+// OrthoScales); sums fp32.
 //
 // One GEMM serves the three products: CTA pairs (2-SM MMA) on 256 x 256 tiles, operands
 // by TMA in five stages of 64 along K, two accumulators in TMEM.  X X^T and A A compute
@@ -25,6 +29,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "ortho.cuh"
 
 namespace fs {
 namespace ortho {
@@ -52,7 +57,9 @@ enum { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
 struct Args {
     int R, C, batch, kb;          // tiles of rows and columns, matrices, stages along K
     int rows, cols;               // extents of the output (cols padded to 64)
-    float alpha, beta;            // out = alpha in + beta acc
+    float alpha, beta;            // out = alpha in + beta acc (+ beta diag H)
+    int low_in, low_out;          // X comes and goes as a pair
+    float* diag;                  // [batch][rows] B's diagonal, times its power of two
     __nv_bfloat16* out;           // LAST: result [m, n]
     long long out_row, out_mat;
     int m, n, tall, tma_out;
@@ -94,18 +101,6 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d, uint64_t adesc, uint64_
     tc_mma_bf16_pair(d, adesc, bdesc, idesc, acc);      // kind::f16; the descriptor says fp16
 }
 
-// Instruction descriptor, kind::f16: fp32 accumulator, A and B fp16 (formats 0), B MN-major if b_mn.
-__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
-    return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
-           (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-__device__ __forceinline__ float2 unpack_half2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
-
 // 16-byte chunk q of row `row` in a 32 x 32 piece with the 64-byte swizzle.
 __device__ __forceinline__ int chunk_at(int row, int q) { return row * 64 + ((q ^ ((row >> 1) & 3)) << 4); }
 // Element (row, col) of it.
@@ -119,7 +114,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     constexpr bool SYM = MODE == GRAM || MODE == POLY;
     constexpr bool B_MN = !SYM;
     constexpr bool LOADS = MODE != GRAM;
-    constexpr uint32_t LOAD_BYTES = SYM ? PIECE : 2 * PIECE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
@@ -159,6 +153,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    cudaGridDependencySynchronize();
     const int per = tiles_per_matrix(args, SYM);
     const int total = per * args.batch;
     const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(nclusters_x());
@@ -269,9 +264,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 if (lane == 0) {
                     bulk_wait_read0();              // the buffer's last store has read it
                     const uint32_t bar = smem_u32(&ebar[2 * ew + b]), dst = smem_u32(buf0 + b * BUF);
-                    mbar_arrive_expect_tx(bar, LOAD_BYTES);
+                    const bool low = !SYM && args.low_in;
+                    mbar_arrive_expect_tx(bar, low ? 2 * PIECE : PIECE);
                     tma_load_3d(dst, &tmIn, bar, col0 + 32 * c, row0, tl.z);
-                    if constexpr (!SYM) tma_load_3d(dst + PIECE, &tmInL, bar, col0 + 32 * c, row0, tl.z);
+                    if (low) tma_load_3d(dst + PIECE, &tmInL, bar, col0 + 32 * c, row0, tl.z);
                 }
                 ++asked;
             };
@@ -279,6 +275,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 __syncwarp();
                 ask(first);
             }
+            float* drow = nullptr;                 // this lane's row of B's diagonal
+            if (MODE != GRAM && row0 + lane < args.rows) drow = args.diag + static_cast<long long>(tl.z) * args.rows + row0 + lane;
+            const float d = !SYM && drow ? __ldg(drow) : 0.0f;
             if (!mbar_wait(smem_u32(&tfull[acc]), use & 1u, abort_flag, args.err)) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -301,22 +300,25 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         const uint4 h = *reinterpret_cast<const uint4*>(buf + chunk_at(lane, q));
                         const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
                         uint32_t lw[4] = {0, 0, 0, 0};
-                        if constexpr (!SYM) {
+                        if (!SYM && args.low_in) {
                             const uint4 l = *reinterpret_cast<const uint4*>(buf + PIECE + chunk_at(lane, q));
                             lw[0] = l.x; lw[1] = l.y; lw[2] = l.z; lw[3] = l.w;
                         }
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
                             float2 in = unpack_half2(hw[w]);
+                            uint32_t& v0 = v[8 * q + 2 * w];
+                            uint32_t& v1 = v[8 * q + 2 * w + 1];
+                            float a0 = __uint_as_float(v0), a1 = __uint_as_float(v1);
                             if constexpr (!SYM) {
+                                a0 += d * in.x;
+                                a1 += d * in.y;
                                 const float2 lo = unpack_half2(lw[w]);
                                 in.x += lo.x * 0x1p-11f;
                                 in.y += lo.y * 0x1p-11f;
                             }
-                            uint32_t& v0 = v[8 * q + 2 * w];
-                            uint32_t& v1 = v[8 * q + 2 * w + 1];
-                            v0 = __float_as_uint(args.alpha * in.x + args.beta * __uint_as_float(v0));
-                            v1 = __float_as_uint(args.alpha * in.y + args.beta * __uint_as_float(v1));
+                            v0 = __float_as_uint(args.alpha * in.x + args.beta * a0);
+                            v1 = __float_as_uint(args.alpha * in.y + args.beta * a1);
                         }
                     }
                     __syncwarp();
@@ -325,6 +327,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(args.beta * __uint_as_float(v[j]));
+                }
+                if (MODE == POLY && x == row0) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (j == lane) {
+                            if (drow) *drow = __uint_as_float(v[j]);
+                            v[j] = 0u;
+                        }
                 }
                 if constexpr (MODE == LAST) {
                     // the result's piece, transposed for a tall matrix
@@ -376,7 +386,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                                 *reinterpret_cast<uint16_t*>(buf + PIECE + elem_at(w, lane)) =
                                     static_cast<uint16_t>(p[w >> 1] >> (16 * (w & 1)));
                         }
-                    } else {
+                    } else if (args.low_out) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             uint32_t l[4];
@@ -395,7 +405,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         store_3d(&tmOut, smem_u32(buf), x, row0, tl.z);
                         if constexpr (SYM) {
                             if (x > row0) store_3d(&tmOut, smem_u32(buf + PIECE), row0, x, tl.z);
-                        } else {
+                        } else if (args.low_out) {
                             store_3d(&tmOutL, smem_u32(buf + PIECE), x, row0, tl.z);
                         }
                         bulk_commit();
@@ -430,29 +440,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 }
 
 // ------------------------------------------------------------- preparation
-constexpr int NORM_BLOCKS = 64;               // at most, per matrix
-
-struct Source {
-    const void* g;
-    long long row, mat;
-    int m, n, f32, vec;
-};
-
-__device__ __forceinline__ float at(const Source& s, const void* base, long long i) {
-    return s.f32 ? static_cast<const float*>(base)[i] : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
-}
-
-// Sums of squares over fp32's whole range: three partial sums, of values above 2^40 (scaled by
-// 2^-88), below 2^-50 (by 2^100) and between, none of which can overflow or vanish.
-struct Squares {
-    float big = 0.f, mid = 0.f, small = 0.f;
-    __device__ __forceinline__ void add(float x) {
-        const float a = fabsf(x);
-        if (a > 0x1p40f) big += (x * 0x1p-88f) * (x * 0x1p-88f);
-        else if (a < 0x1p-50f) small += (x * 0x1p100f) * (x * 0x1p100f);
-        else mid += x * x;                     // a NaN lands here
-    }
-};
+constexpr int NORM_BLOCKS = 256;              // at most, per matrix
 
 __global__ void __launch_bounds__(256) norm_kernel(const Source s, float* part) {
     __shared__ float sh[8][3];
@@ -479,6 +467,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const Source s, float* part) 
                 }
             }
         } else {
+#pragma unroll 8
             for (int j = lane; j < s.n; j += 32) q.add(at(s, row, j));
         }
     }
@@ -505,6 +494,7 @@ scale_kernel(const Source s, const float* part, int nb, double eps, float xscale
     __shared__ float tile[64][65];
     __shared__ float f1, f2;
     const int z = blockIdx.y;
+    cudaGridDependencySynchronize();
     const int ti = blockIdx.x / tiles_n, tj = blockIdx.x - ti * tiles_n;      // tile of G
     if (threadIdx.x < 32) {
         double big = 0, mid = 0, small = 0;
@@ -521,15 +511,7 @@ scale_kernel(const Source s, const float* part, int nb, double eps, float xscale
             small += __shfl_xor_sync(0xffffffffu, small, o);
         }
         if (threadIdx.x == 0) {
-            const double norm = sqrt(big * 0x1p176 + mid + small * 0x1p-200) + eps;
-            // x / norm in two fp32 factors, the first a power of two: no intermediate leaves fp32's range
-            int e = 0;
-            frexp(norm, &e);
-            int k = -e;
-            k = k < -126 ? -126 : (k > 127 ? 127 : k);
-            const bool fine = norm > 0.0 && norm < INFINITY;
-            f1 = fine ? static_cast<float>(ldexp(1.0, k)) : (norm == 0.0 ? 0.0f : NAN);     // zeros stay zeros
-            f2 = fine ? static_cast<float>(xscale / (norm * ldexp(1.0, k))) : 1.0f;
+            norm_factors(big, mid, small, eps, xscale, &f1, &f2);
         }
     }
     const size_t es = s.f32 ? 4 : 2;
@@ -591,14 +573,14 @@ Shape shape(int m, int n) {
 
 struct Layout {
     int group;                       // matrices in flight
-    size_t h[2], l, a, b, part, end;
+    size_t h[2], l, a, b, diag, part, end;
 };
 size_t up(size_t x) { return (x + 1023) / 1024 * 1024; }
 // Matrices are worked on in groups whose buffers stay within 2 GiB (one matrix at least).
 Layout layout(int batch, int m, int n) {
     const Shape s = shape(m, n);
     const size_t x = static_cast<size_t>(s.r) * s.qp * 2, sq = static_cast<size_t>(s.r) * s.rp * 2;
-    const size_t each = 3 * x + 2 * sq + NORM_BLOCKS * 12;
+    const size_t each = 3 * x + 2 * sq + static_cast<size_t>(s.r) * 4 + NORM_BLOCKS * 12;
     size_t g = (size_t(2) << 30) / each;
     g = g < 1 ? 1 : (g > 16384 ? 16384 : g);
     if (g > static_cast<size_t>(batch)) g = batch;
@@ -613,6 +595,7 @@ Layout layout(int batch, int m, int n) {
     l.l = take(g * x);
     l.a = take(g * sq);
     l.b = take(g * sq);
+    l.diag = take(g * s.r * 4);
     l.part = take(g * NORM_BLOCKS * 12);
     l.end = o;
     return l;
@@ -655,17 +638,20 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtens
     if (e != cudaSuccess) return e;
     const long long tiles = static_cast<long long>(MODE <= POLY ? args.R * (args.R + 1) / 2 : args.R * args.C) * args.batch;
     const int clusters = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
-    gemm_kernel<MODE><<<2 * clusters, THREADS, SMEM_BYTES, st>>>(a, b, in, in_l, out, out_l, args);
+    e = launch_after(gemm_kernel<MODE>, dim3(2 * clusters), dim3(THREADS), SMEM_BYTES, st, a, b, in, in_l, out, out_l, args);
     count_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace ortho
 
-size_t ortho_ws_bytes(int batch, int m, int n) { return ortho::layout(batch, m, n).end; }
+size_t ortho_ws_bytes(int batch, int m, int n) {
+    return ortho_small_fits(m, n) ? 256 : ortho::layout(batch, m, n).end;
+}
 
 cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) {
     using namespace ortho;
+    if (ortho_small_fits(o.m, o.n)) return launch_ortho_small(o, st);
     const Shape s = shape(o.m, o.n);
     const Layout l = layout(o.batch, o.m, o.n);
     int sms = 0;
@@ -673,14 +659,12 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
     if (e != cudaSuccess) return e;
     uint8_t* w = static_cast<uint8_t*>(ws);
     const size_t es = o.f32 ? 4 : 2;
-    const bool vec = (reinterpret_cast<uintptr_t>(o.g) & 15u) == 0 && o.g_row * es % 16 == 0 && o.g_mat * es % 16 == 0 &&
-                     o.n * es % 16 == 0;
     const bool tma_out = (reinterpret_cast<uintptr_t>(o.out) & 15u) == 0 && o.out_row % 8 == 0 && o.out_mat % 8 == 0;
     for (int z0 = 0; z0 < o.batch; z0 += l.group) {
         const int nb = o.batch - z0 < l.group ? o.batch - z0 : l.group;
-        const Source src{static_cast<const uint8_t*>(o.g) + z0 * o.g_mat * static_cast<long long>(es), o.g_row, o.g_mat, o.m,
-                         o.n, o.f32, vec};
+        const Source src = source(o, static_cast<const uint8_t*>(o.g) + z0 * o.g_mat * static_cast<long long>(es));
         float* part = reinterpret_cast<float*>(w + l.part);
+        // a row per warp; the split depends on the matrix alone, so that a matrix's result does not depend on its batch
         int blocks = (o.m + 7) / 8;
         blocks = blocks > NORM_BLOCKS ? NORM_BLOCKS : blocks;
         norm_kernel<<<dim3(blocks, nb), 256, 0, st>>>(src, part);
@@ -690,9 +674,10 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
         __half* L = reinterpret_cast<__half*>(w + l.l);
         // tiles of G; for X's padded width the last ones reach past it
         const int tm = (s.tall ? s.qp : s.rp) / 64, tn = (s.tall ? s.rp : s.qp) / 64;
-        scale_kernel<<<dim3(tm * tn, nb), 256, 0, st>>>(src, part, blocks, o.eps, o.scales.x, s.tall, tn, H[0], L, s.r, s.qp);
+        e = launch_after(scale_kernel, dim3(tm * tn, nb), dim3(256), 0, st, src, part, blocks, o.eps, o.scales.x, s.tall, tn,
+                         H[0], L, s.r, s.qp);
         count_launch();
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if (e != cudaSuccess) return e;
 
         CUtensorMap xk[2], xn[2], xp[2], lp, ak, ap, bk, bp, op;
         void *A = w + l.a, *B = w + l.b;
@@ -725,7 +710,15 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
         g.out_mat = o.out_mat;
         g.tma_out = tma_out;
         g.err = dev_error_ptr();
+        g.diag = reinterpret_cast<float*>(w + l.diag);
         const OrthoScales& sc = o.scales;
+        // X stays a pair while the steps from here on can multiply by more than four
+        bool low[kMaxOrthoSteps + 1] = {};
+        double grow = 1.0;
+        for (int k = o.steps - 1; k >= 0; --k) {
+            grow *= fabs(o.coefs[3 * k]) > 1.0f ? fabs(o.coefs[3 * k]) : 1.0;
+            low[k] = grow > 4.0;
+        }
         int cur = 0;
         for (int k = 0; k < o.steps; ++k, cur ^= 1) {
             const float ca = o.coefs[3 * k], cb = o.coefs[3 * k + 1], cc = o.coefs[3 * k + 2];
@@ -744,6 +737,8 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
             if (e != cudaSuccess) return e;
             a.C = (s.qp + BT - 1) / BT;
             a.cols = s.qp;
+            a.low_in = low[k];
+            a.low_out = low[k + 1];
             a.alpha = ca;
             a.beta = 1.0f / sc.b;
             if (!last) {

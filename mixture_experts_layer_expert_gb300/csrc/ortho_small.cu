@@ -1,0 +1,425 @@
+// ortho_small.cu -- orthogonalised updates of matrices whose shorter side is at
+// most 128: all steps of a matrix in one launch.
+//
+// The mathematics is ortho.cu's.  A cluster of C thread blocks holds one matrix: block c a
+// slice of up to 256 columns of X, in fp32 registers (a row and 128 columns a thread) and as the
+// fp16 operand H in shared memory.  Per step
+//   the block's share of X X^T (128 x 128, tensor cores) -> summed over the cluster through
+//   distributed shared memory, each block a band of rows, in rank order -> A (fp16) in every block
+//   B = b A + c A A in every block (the same bits), its diagonal kept apart in fp32
+//   X = a X + B H for the block's columns.
+// H serves both products where it lies: K-major for X X^T, MN-major for B H.  X never leaves the
+// block, so it is carried in full fp32.
+// Bound by latency: five steps of 128 x 128 .. 2,048 are three products of a few hundred
+// cycles each behind each other, with two cluster barriers a step.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "ortho.cuh"
+
+namespace fs {
+namespace ortho {
+namespace small {
+
+constexpr int R = 128;                         // rows held (r <= R; the rest are zero)
+constexpr int W = 256;                         // columns a block can hold
+constexpr int THREADS = 256;
+constexpr int BLOCK = R * 64 * 2;              // 64 columns of fp16: the 128-byte-swizzle tile, 16 KB
+constexpr int H_OFF = 0;
+constexpr int A_OFF = H_OFF + (W / 64) * BLOCK;
+constexpr int B_OFF = A_OFF + 2 * BLOCK;
+constexpr int P_OFF = B_OFF + 2 * BLOCK;
+constexpr int P_ROW = R + 4;                   // floats: 16-byte accesses of 8 rows fall into different banks
+constexpr int D_OFF = P_OFF + R * P_ROW * 4;   // fp32: B's diagonal
+constexpr int N_OFF = D_OFF + R * 4;           // sums of squares of the cluster's blocks, 16 x 4 floats
+constexpr int S_OFF = N_OFF + 16 * 16;         // of this block's warps, 8 x 4 floats, then the two factors
+constexpr int BAR_OFF = S_OFF + 8 * 16 + 16;
+constexpr size_t SMEM_BYTES = 1024 + BAR_OFF + 32;
+constexpr int D_A = 0, D_AA = 128, D_X = 256;  // TMEM columns
+static_assert(SMEM_BYTES <= 232448, "shared memory");
+
+struct Args {
+    Source src;
+    __nv_bfloat16* out;
+    long long out_row, out_mat;
+    int out_vec;
+    int r, q, tall, steps, width;              // width: columns per block, a multiple of 64
+    float scale, eps;
+    OrthoScales sc;
+    float coefs[48];
+    int* err;
+};
+
+// Element (row, col) of a [128][64 n] operand in swizzled tiles of 64 columns; `col` a multiple of 8: its 16-byte chunk.
+__device__ __forceinline__ uint32_t chunk(int row, int col) {
+    return (col >> 6) * BLOCK + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint4 v) {
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ int cluster_size() {
+    uint32_t n;
+    asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return static_cast<int>(n);
+}
+
+__global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant__ Args a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t base = smem_u32(smem);
+    uint64_t* bar = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    float* dvec = reinterpret_cast<float*>(smem + D_OFF);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, half = warp >> 2;
+    const int row = quarter * 32 + lane;
+    const int C = cluster_size(), rank = static_cast<int>(cluster_ctarank());
+    const int z = blockIdx.x / C;
+    const int col_first = rank * a.width + half * 128;              // this thread's first column of X
+    const int ncol = min(128, a.width - half * 128);                // and how many it holds (a multiple of 64, may be <= 0)
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(bar), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    // ---- the block's slice of G, and the norm
+    float x[128];
+    Squares sq;
+    {
+        const size_t es = a.src.f32 ? 4 : 2;
+        const uint8_t* g = static_cast<const uint8_t*>(a.src.g) + static_cast<long long>(z) * a.src.mat * es;
+        const long long step = a.tall ? a.src.row : 1;              // from a column of X to the next
+        const uint8_t* p = g + ((a.tall ? row : static_cast<long long>(row) * a.src.row) + col_first * step) * es;
+        const int valid = row < a.r ? min(ncol, a.q - col_first) : 0;
+        if (a.src.vec && !a.tall) {
+#pragma unroll
+            for (int c = 0; c < 128; c += 8) {
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (c < valid) {                                     // q is a multiple of the vector (8 bf16, 4 fp32)
+                    if (a.src.f32) {
+                        const float4 u = __ldg(reinterpret_cast<const float4*>(p) + c / 4);
+                        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+                        if (c + 4 < valid) {
+                            const float4 w = __ldg(reinterpret_cast<const float4*>(p) + c / 4 + 1);
+                            v[4] = w.x; v[5] = w.y; v[6] = w.z; v[7] = w.w;
+                        }
+                    } else {
+                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + c / 8);
+                        v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
+                        v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[c + k] = v[k];
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) x[c] = c < valid ? at(a.src, p, c * step) : 0.0f;
+        }
+#pragma unroll
+        for (int c = 0; c < 128; ++c) sq.add(x[c]);
+    }
+    {
+        float v[3] = {sq.big, sq.mid, sq.small};
+        float* mine = reinterpret_cast<float*>(smem + S_OFF) + warp * 4;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            if (lane == 0) mine[k] = v[k];
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                          // every block of the cluster runs before its memory is written
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    if (threadIdx.x < C) {                   // this block's sums to block threadIdx.x
+        float s[3] = {0.f, 0.f, 0.f};
+        for (int w = 0; w < 8; ++w)
+            for (int k = 0; k < 3; ++k) s[k] += reinterpret_cast<float*>(smem + S_OFF)[w * 4 + k];
+        st_cluster(map_to_cta(base + N_OFF + rank * 16, threadIdx.x),
+                   make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), 0u));
+    }
+    __syncwarp();
+    cluster_sync();
+    float* factors = reinterpret_cast<float*>(smem + S_OFF + 8 * 16);
+    if (threadIdx.x == 0) {
+        double big = 0, mid = 0, sml = 0;
+        for (int c = 0; c < C; ++c) {
+            const float* p = reinterpret_cast<const float*>(smem + N_OFF) + c * 4;
+            big += p[0];
+            mid += p[1];
+            sml += p[2];
+        }
+        norm_factors(big, mid, sml, a.eps, a.sc.x, &factors[0], &factors[1]);
+    }
+    __syncthreads();
+    {
+        const float f1 = factors[0], f2 = factors[1];
+#pragma unroll
+        for (int c = 0; c < 128; ++c) x[c] = x[c] * f1 * f2;
+    }
+
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    constexpr uint32_t idesc_sq = idesc_f16(R, R, 0);
+    const uint32_t idesc_x = idesc_f16(R, a.width, 1);
+    uint32_t phase = 0;
+    bool ok = true;          // after a wait that gave up the phases go on (the cluster's barriers have to match), unwaited
+    auto finish_mma = [&]() {
+        if (ok) ok = mbar_wait(smem_u32(bar), phase, abort_flag, a.err);
+        phase ^= 1u;
+        tc_fence_after();
+    };
+
+#pragma unroll 1
+    for (int k = 0; k < a.steps; ++k) {
+        const float ca = a.coefs[3 * k], cb = a.coefs[3 * k + 1], cc = a.coefs[3 * k + 2];
+        // ---- H
+#pragma unroll
+        for (int c = 0; c < 128; c += 8) {
+            if (c < ncol)
+                *reinterpret_cast<uint4*>(smem + H_OFF + chunk(row, half * 128 + c)) =
+                    make_uint4(pack_half2(x[c], x[c + 1]), pack_half2(x[c + 2], x[c + 3]), pack_half2(x[c + 4], x[c + 5]),
+                               pack_half2(x[c + 6], x[c + 7]));
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        // ---- this block's share of X X^T
+        if (warp == 0) {
+            tc_fence_after();
+            if (elect_one()) {
+                for (int kk = 0; kk < a.width / 16; ++kk) {
+                    const uint64_t d = smem_desc_sw128(base + H_OFF + (kk >> 2) * BLOCK) + 2ull * (kk & 3);
+                    tc_mma_bf16(tmem + D_A, d, d, idesc_sq, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(smem_u32(bar));
+            }
+            __syncwarp();
+        }
+        finish_mma();
+        const float fa = a.sc.a / (a.sc.x * a.sc.x);
+        if (C == 1) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                const int c0 = half * 64 + h * 32;
+                tmem_ld32(taddr + D_A + c0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t p[4];
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        p[w] = pack_half2(fa * __uint_as_float(v[8 * q + 2 * w]), fa * __uint_as_float(v[8 * q + 2 * w + 1]));
+                    *reinterpret_cast<uint4*>(smem + A_OFF + chunk(row, c0 + 8 * q)) = make_uint4(p[0], p[1], p[2], p[3]);
+                }
+            }
+        } else {
+            float* P = reinterpret_cast<float*>(smem + P_OFF) + row * P_ROW;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t v[32];
+                const int c0 = half * 64 + h * 32;
+                tmem_ld32(taddr + D_A + c0, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    *reinterpret_cast<uint4*>(P + c0 + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            }
+            cluster_sync();
+            // rows [rank 128 / C, ..): eight columns a thread, summed in rank order, sent to every block
+            const int band = R / C;
+            for (int g = threadIdx.x; g < band * 16; g += THREADS) {
+                const int r = rank * band + (g >> 4), c0 = (g & 15) * 8;
+                const uint32_t at_ = base + P_OFF + (r * P_ROW + c0) * 4;
+                float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t p = map_to_cta(at_, c);
+                    const float4 u = ld_cluster(p), w = ld_cluster(p + 16);
+                    s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
+                    s[4] += w.x; s[5] += w.y; s[6] += w.z; s[7] += w.w;
+                }
+                const uint4 p = make_uint4(pack_half2(fa * s[0], fa * s[1]), pack_half2(fa * s[2], fa * s[3]),
+                                           pack_half2(fa * s[4], fa * s[5]), pack_half2(fa * s[6], fa * s[7]));
+                const uint32_t dst = base + A_OFF + chunk(r, c0);
+#pragma unroll 4
+                for (int c = 0; c < C; ++c) st_cluster(map_to_cta(dst, c), p);
+            }
+            cluster_sync();
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        // ---- B = b A + c A A
+        if (warp == 0) {
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < R / 16; ++kk) {
+                    const uint64_t d = smem_desc_sw128(base + A_OFF + (kk >> 2) * BLOCK) + 2ull * (kk & 3);
+                    tc_mma_bf16(tmem + D_AA, d, d, idesc_sq, kk > 0 ? 1u : 0u);
+                }
+                tc_commit(smem_u32(bar));
+            }
+            __syncwarp();
+        }
+        finish_mma();
+        const float f1 = cb * (a.sc.b / a.sc.a), f2 = cc * (a.sc.b / (a.sc.a * a.sc.a));
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t v[32];
+            const int c0 = half * 64 + h * 32;
+            tmem_ld32(taddr + D_AA + c0, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 av = *reinterpret_cast<const uint4*>(smem + A_OFF + chunk(row, c0 + 8 * q));
+                const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
+                uint32_t p[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float2 in = unpack_half2(aw[w]);
+                    const int c = c0 + 8 * q + 2 * w;
+                    float b0 = f1 * in.x + f2 * __uint_as_float(v[8 * q + 2 * w]);
+                    float b1 = f1 * in.y + f2 * __uint_as_float(v[8 * q + 2 * w + 1]);
+                    if (c == row) { dvec[row] = b0; b0 = 0.0f; }
+                    if (c + 1 == row) { dvec[row] = b1; b1 = 0.0f; }
+                    p[w] = pack_half2(b0, b1);
+                }
+                *reinterpret_cast<uint4*>(smem + B_OFF + chunk(row, c0 + 8 * q)) = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncthreads();
+        // ---- X = a X + B H
+        if (warp == 0) {
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < R / 16; ++kk)
+                    tc_mma_bf16(tmem + D_X, smem_desc_sw128(base + B_OFF + (kk >> 2) * BLOCK) + 2ull * (kk & 3),
+                                smem_desc_sw128_mn(base + H_OFF, BLOCK) + 128ull * kk, idesc_x, kk > 0 ? 1u : 0u);
+                tc_commit(smem_u32(bar));
+            }
+            __syncwarp();
+        }
+        const float d = dvec[row] * (1.0f / a.sc.b), fx = 1.0f / a.sc.b;
+        finish_mma();
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+            if (c < ncol) {
+                uint32_t v[32];
+                tmem_ld32(taddr + D_X + half * 128 + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const float h = __half2float(__float2half_rn(x[c + j]));
+                    x[c + j] = ca * x[c + j] + d * h + fx * __uint_as_float(v[j]);
+                }
+            }
+        }
+    }
+    // ---- the result
+    if (row < a.r) {
+        const float f = a.scale / a.sc.x;
+        const int valid = min(ncol, a.q - col_first);
+        uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + z * a.out_mat;
+        if (a.tall) {
+            o += static_cast<long long>(col_first) * a.out_row + row;
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+                if (c < valid) o[c * a.out_row] = static_cast<uint16_t>(pack_bf16x2(f * x[c], 0.0f));
+        } else {
+            o += row * a.out_row + col_first;
+#pragma unroll
+            for (int c = 0; c < 128; c += 8) {
+                if (a.out_vec && c + 8 <= valid) {
+                    *reinterpret_cast<uint4*>(o + c) =
+                        make_uint4(pack_bf16x2(f * x[c], f * x[c + 1]), pack_bf16x2(f * x[c + 2], f * x[c + 3]),
+                                   pack_bf16x2(f * x[c + 4], f * x[c + 5]), pack_bf16x2(f * x[c + 6], f * x[c + 7]));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (c + j < valid) o[c + j] = static_cast<uint16_t>(pack_bf16x2(f * x[c + j], 0.0f));
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                          // no block leaves while another may read its memory
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace small
+}  // namespace ortho
+
+// Blocks of a cluster for q columns, 0 if the matrix does not fit one.
+static int small_cluster(int r, int q) {
+    if (r > ortho::small::R) return 0;
+    int c = 1;
+    while (c * ortho::small::W < q) c *= 2;
+    return c <= 8 ? c : 0;
+}
+
+bool ortho_small_fits(int m, int n) { return small_cluster(m < n ? m : n, m < n ? n : m) > 0; }
+
+cudaError_t launch_ortho_small(const OrthoArgs& o, cudaStream_t st) {
+    using namespace ortho::small;
+    using ortho::source;
+    static bool set[kMaxDevices];
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(small_kernel), SMEM_BYTES, set);
+    if (e != cudaSuccess) return e;
+    Args a{};
+    a.src = source(o, o.g);
+    a.out = o.out;
+    a.out_row = o.out_row;
+    a.out_mat = o.out_mat;
+    a.out_vec = (reinterpret_cast<uintptr_t>(o.out) & 15u) == 0 && o.out_row % 8 == 0 && o.out_mat % 8 == 0;
+    a.tall = o.m > o.n;
+    a.r = a.tall ? o.n : o.m;
+    a.q = a.tall ? o.m : o.n;
+    a.steps = o.steps;
+    a.scale = o.scale;
+    a.eps = static_cast<float>(o.eps);
+    a.sc = o.scales;
+    for (int i = 0; i < 3 * o.steps; ++i) a.coefs[i] = o.coefs[i];
+    a.err = dev_error_ptr();
+    const int C = small_cluster(a.r, a.q);
+    a.width = ((a.q + C - 1) / C + 63) / 64 * 64;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = C;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(o.batch) * C);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, small_kernel, a);
+    count_launch();
+    return e;
+}
+
+}  // namespace fs

@@ -584,13 +584,10 @@ def fs_balance_ws_bytes(desc: BalanceDesc) -> int:
     return int(lib().fs_balance_ws_bytes(ctypes.byref(desc)))
 
 
-def _balance_operands(what, dev, desc, logits, bias, cu, mask, counts, tokens):
-    """(logits, row stride, bias, cu, mask, counts, tokens) of both directions."""
-    T, E, S, f32, i32 = desc.T, desc.E, desc.n_seqs, torch.float32, torch.int32
-    opt = lambda name, t, shape, dt: None if t is None else _operand(what + " " + name, t, shape, dev, dt, False)[0]
-    zp, zs = _operand(what + " logits", logits, (T, E), dev, f32)
-    return (zp, zs[0] if T > 1 else max(zs[0], E), opt("bias", bias, (E,), f32), opt("cu", cu, (S + 1,), i32),
-            opt("mask", mask, (T,), torch.uint8), opt("counts", counts, (S, E), i32), opt("tokens", tokens, (S,), i32))
+def _logit_rows(what, t, desc, dev):
+    """(pointer, row stride) of a [T, E] fp32 operand with any row stride."""
+    p, st = _operand(what, t, (desc.T, desc.E), dev, torch.float32)
+    return p, st[0] if desc.T > 1 else max(st[0], desc.E)
 
 
 def fs_balance_loss(desc: BalanceDesc, logits, topk_idx, counts, tokens, probs, loss, ws, bias=None, cu=None, mask=None,
@@ -599,12 +596,12 @@ def fs_balance_loss(desc: BalanceDesc, logits, topk_idx, counts, tokens, probs, 
     tokens [S] int32, probs [S, E] and loss [1] fp32; cu [S + 1] int32 borders and mask [T] uint8 optional;
     ws: fs_balance_ws_bytes(desc) bytes."""
     dev, st = _here(stream)
-    what = "fs_balance_loss"
-    zp, zr, bp, cp, mp, np_, tp = _balance_operands(what, dev, desc, logits, bias, cu, mask, counts, tokens)
-    ip, _ = _operand(what + " topk_idx", topk_idx, (desc.T, desc.k), dev, torch.int32, False)
-    pp, _ = _operand(what + " probs", probs, (desc.n_seqs, desc.E), dev, torch.float32, False)
-    lp, _ = _operand(what + " loss", loss, (1,), dev, torch.float32, False)
-    wp, _ = _operand(what + " ws", ws, ws.shape, dev, torch.uint8, False)
+    what, T, E, S, f32, i32 = "fs_balance_loss", desc.T, desc.E, desc.n_seqs, torch.float32, torch.int32
+    zp, zr = _logit_rows("fs_balance_loss logits", logits, desc, dev)
+    bp, ip, cp, mp, np_, tp, pp, lp, wp = _ptrs(what, dev, (
+        ("bias", bias, (E,), f32), ("topk_idx", topk_idx, (T, desc.k), i32), ("cu", cu, (S + 1,), i32),
+        ("mask", mask, (T,), torch.uint8), ("counts", counts, (S, E), i32), ("tokens", tokens, (S,), i32),
+        ("probs", probs, (S, E), f32), ("loss", loss, (1,), f32), ("ws", ws, ws.shape, torch.uint8)))
     _check(lib().fs_balance_loss(desc, zp, zr, bp, ip, cp, mp, np_, tp, pp, lp, wp, ws.numel(), st), what)
 
 
@@ -612,12 +609,13 @@ def fs_balance_loss_backward(desc: BalanceDesc, logits, counts, tokens, d_loss, 
                              stream=None):
     """d_logits [T, E] fp32 from fs_balance_loss's counts and tokens and d_loss [1] (None: 1)."""
     dev, st = _here(stream)
-    what = "fs_balance_loss_backward"
-    zp, zr, bp, cp, mp, np_, tp = _balance_operands(what, dev, desc, logits, bias, cu, mask, counts, tokens)
-    gp = None if d_loss is None else _operand(what + " d_loss", d_loss, (1,), dev, torch.float32, False)[0]
-    dp, ds = _operand(what + " d_logits", d_logits, (desc.T, desc.E), dev, torch.float32)
-    _check(lib().fs_balance_loss_backward(desc, zp, zr, bp, cp, mp, np_, tp, gp, dp,
-                                          ds[0] if desc.T > 1 else max(ds[0], desc.E), st), what)
+    what, E, S, f32, i32 = "fs_balance_loss_backward", desc.E, desc.n_seqs, torch.float32, torch.int32
+    zp, zr = _logit_rows("fs_balance_loss_backward logits", logits, desc, dev)
+    dp, dr = _logit_rows("fs_balance_loss_backward d_logits", d_logits, desc, dev)
+    bp, cp, mp, np_, tp, gp = _ptrs(what, dev, (
+        ("bias", bias, (E,), f32), ("cu", cu, (S + 1,), i32), ("mask", mask, (desc.T,), torch.uint8),
+        ("counts", counts, (S, E), i32), ("tokens", tokens, (S,), i32), ("d_loss", d_loss, (1,), f32)))
+    _check(lib().fs_balance_loss_backward(desc, zp, zr, bp, cp, mp, np_, tp, gp, dp, dr, st), what)
 
 
 NEWTON_SCHULZ = ((3.4445, -4.7750, 2.0315),) * 5      # coefficients (a, b, c) of the usual five steps
@@ -802,6 +800,19 @@ def _operand(what: str, t: torch.Tensor, shape, dev: int, dtype=torch.bfloat16, 
     if t.get_device() != dev:
         raise FsError(1, what, "tensor on %s, not on the current device" % t.device)
     return t.data_ptr(), st
+
+
+def _ptrs(what: str, dev: int, specs):
+    """Pointers of contiguous operands (name, tensor or None, shape, type), refused as by _operand."""
+    out = []
+    for name, t, shape, dtype in specs:
+        if t is None:
+            out.append(None)
+        elif t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev:
+            out.append(t.data_ptr())
+        else:
+            out.append(_operand("%s %s" % (what, name), t, shape, dev, dtype, False)[0])
+    return out
 
 
 def _rows(ptr_strides) -> Rows:

@@ -36,13 +36,19 @@ def half(x, e):
 
 
 def rounded(g, coefs=USUAL, eps=1e-7, scale=1.0):
-    """With H = fp16(X), L = fp16 of the rest; A and B fp16; powers of two as for singular values below 2."""
+    """With H = fp16(X), L = fp16 of the rest while later steps can multiply by more than four; A and B fp16, B's
+    diagonal apart and applied to H; powers of two as for singular values below 2."""
     x = start(g, eps)
-    for a, b, c in coefs:
+    for k, (a, b, c) in enumerate(coefs):
         h = half(x, 13)
-        x = h + half(x - h, 24)
+        grow = 1.0
+        for later in coefs[k:]:
+            grow *= max(1.0, abs(later[0]))
+        x = h + half(x - h, 24) if grow > 4 else h
         s = half(h @ h.T, 12)
-        x = a * x + half(b * s + c * (s @ s), 10) @ h
+        m = b * s + c * (s @ s)
+        d = torch.diag(m)
+        x = a * x + d[:, None] * h + half(m - torch.diag(d), 10) @ h
     x = x * scale
     return x.T if g.shape[0] > g.shape[1] else x
 
