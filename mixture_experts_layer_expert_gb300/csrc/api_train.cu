@@ -71,11 +71,24 @@ fs_status ortho_scales(const fs_orthogonalize_desc* d, OrthoScales* sc) {
     for (int k = 0; k < d->steps; ++k) {
         const double a = d->coefs[3 * k], b = d->coefs[3 * k + 1], c = d->coefs[3 * k + 2];
         if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return FS_ERR_INVALID_ARG;
+        // |a x + b x^3 + c x^5| on [0, s]: its ends and where a + 3 b u + 5 c u^2 = 0, u = x^2;
+        // |b u + c u^2|: its ends and u = -b / 2c
         double next = 0.0;
-        for (int i = 0; i <= 4096; ++i) {              // what lies between the points is within the factor of four
-            const double x = s * i / 4096, u = x * x;
-            next = std::max(next, std::fabs(x * (a + u * (b + u * c))));
-            btop = std::max(btop, std::fabs(u * (b + u * c)));
+        const auto point = [&](double u) {
+            if (!(u > 0.0) || u > s * s) return;
+            next = std::max(next, std::sqrt(u) * std::fabs(a + u * (b + u * c)));
+            btop = std::max(btop, u * std::fabs(b + u * c));
+        };
+        point(s * s);
+        if (c != 0.0) {
+            const double disc = 9.0 * b * b - 20.0 * a * c;
+            if (disc >= 0.0) {
+                point((-3.0 * b + std::sqrt(disc)) / (10.0 * c));
+                point((-3.0 * b - std::sqrt(disc)) / (10.0 * c));
+            }
+            point(-b / (2.0 * c));
+        } else if (b != 0.0) {
+            point(-a / (3.0 * b));
         }
         s = next;
         top = std::max(top, s);
@@ -123,7 +136,8 @@ fs_status fs_orthogonalize(const fs_orthogonalize_desc* desc, const void* g, int
     FS_CHECK(ortho_strides(desc, g_row, g_mat));
     FS_CHECK(ortho_strides(desc, out_row, out_mat));
     if (!ws) return FS_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < fs_orthogonalize_ws_bytes(desc)) return FS_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < ortho_ws_bytes(desc->batch, desc->m, desc->n))
+        return FS_ERR_WORKSPACE;
     o.g = g; o.g_row = g_row; o.g_mat = desc->batch > 1 ? g_mat : 0;
     o.out = static_cast<__nv_bfloat16*>(out); o.out_row = out_row;
     o.out_mat = desc->batch > 1 ? out_mat : (desc->m * out_row + 7) / 8 * 8;      // one matrix: any legal stride

@@ -86,39 +86,44 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 __device__ __forceinline__ float warp_top(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+__device__ __forceinline__ float recip(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// Logits -> scores, for the sigmoids shifted by min(max z, 0) so that rows far below
-// zero keep their ratios.  rest (sigmoids): 1 - sigma.  A row of -infinity scores zero.
+// Logits -> scores times *inv.  rest (sigmoids): 1 - sigma.  A row of -infinity scores zero.  Sigmoids
+// of a row whose logits all lie below -60 are exponentials to fp32, and their ratios a softmax's.
 template <int EPL, bool SIG>
-__device__ __forceinline__ void scores(float (&v)[EPL], float (&rest)[EPL]) {
+__device__ __forceinline__ void scores(float (&v)[EPL], float (&rest)[EPL], float* inv) {
     float top = v[0];
 #pragma unroll
     for (int j = 1; j < EPL; ++j) top = fmaxf(top, v[j]);
-    top = warp_top(top);
-    const bool none = top == -INFINITY;
-    const float m = none ? 0.0f : (SIG ? fminf(top, 0.0f) : top);
     float sum = 0.0f;
+    if (SIG && __any_sync(0xffffffffu, top > -60.0f)) {
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) {
-        if constexpr (SIG) {
-            const float e = __expf(-fabsf(v[j])), r = __fdividef(1.0f, 1.0f + e);
-            const float z = v[j];
-            v[j] = __expf(fminf(z, 0.0f) - m) * r;
-            if (z != z) v[j] = z;                          // fminf drops a NaN
-            rest[j] = z >= 0.0f ? e * r : r;
-        } else {
-            v[j] = __expf(v[j] - m);
+        for (int j = 0; j < EPL; ++j) {
+            const float u = __expf(-v[j]);
+            v[j] = recip(1.0f + u);
+            rest[j] = u == INFINITY ? 1.0f : u * v[j];
+            sum += v[j];
         }
-        sum += v[j];
+    } else {
+        top = warp_top(top);
+        const float m = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) {
+            v[j] = __expf(v[j] - m);
+            rest[j] = 1.0f;
+            sum += v[j];
+        }
     }
     sum = warp_sum(sum);
-    const float inv = none ? 0.0f : 1.0f / sum;
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) v[j] *= inv;
+    *inv = sum == 0.0f ? 0.0f : 1.0f / sum;
 }
 
 // First sequence that may hold row t or a later one: the last q with cu[q] <= t (0 if none).
@@ -152,6 +157,7 @@ piece_kernel(const Args a) {
     __shared__ float terms[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = blockIdx.x * a.chunk, c1 = a.T - c0 < a.chunk ? a.T : c0 + a.chunk;     // no sum past an int
+    cudaGridDependencySynchronize();
     if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
     float bias[EPL];
 #pragma unroll
@@ -196,9 +202,10 @@ piece_kernel(const Args a) {
                 }
 #pragma unroll
                 for (int j = 0; j < EPL; ++j) v[u][j] += bias[j];
-                scores<EPL, SIG>(v[u], rest);
+                float inv;
+                scores<EPL, SIG>(v[u], rest, &inv);
 #pragma unroll
-                for (int j = 0; j < EPL; ++j) acc[j] += v[u][j];
+                for (int j = 0; j < EPL; ++j) acc[j] += v[u][j] * inv;
             }
         }
 #pragma unroll
@@ -342,6 +349,7 @@ backward_kernel(const BwdArgs a) {
     constexpr int WARPS = Cfg<EPL>::WARPS, U = Cfg<EPL>::U;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c0 = blockIdx.x * a.chunk, c1 = a.T - c0 < a.chunk ? a.T : c0 + a.chunk;     // no sum past an int
+    cudaGridDependencySynchronize();
     const float g = (a.d_loss ? *a.d_loss : 1.0f) * a.coef / static_cast<float>(a.S);
     float bias[EPL], f[EPL];
 #pragma unroll
@@ -382,14 +390,16 @@ backward_kernel(const BwdArgs a) {
                 if (on[u]) {
 #pragma unroll
                     for (int j = 0; j < EPL; ++j) v[u][j] += bias[j];
-                    scores<EPL, SIG>(v[u], rest);
+                    float inv;
+                    scores<EPL, SIG>(v[u], rest, &inv);
                     float dot = 0.0f;
 #pragma unroll
                     for (int j = 0; j < EPL; ++j) dot += f[j] * v[u][j];
-                    dot = warp_sum(dot);
+                    dot = warp_sum(dot) * inv;
+                    const float by = scale * inv;
 #pragma unroll
                     for (int j = 0; j < EPL; ++j) {
-                        v[u][j] *= scale * (f[j] - dot);
+                        v[u][j] *= by * (f[j] - dot);
                         if constexpr (SIG) v[u][j] *= rest[j];
                     }
                 } else {
@@ -436,42 +446,33 @@ bool vec_ok(const void* p, long long row, int E) {
 
 size_t balance_ws_bytes(int T, int E, int S) { return bal::layout(T, E, S).end; }
 
-// KERNEL<elements a lane, TAIL...> for E experts.
-#define FS_BALANCE(KERNEL, E, GRID, ARGS, ...)                                                              \
-    do {                                                                                                    \
-        if ((E) <= 128) KERNEL<4, __VA_ARGS__><<<GRID, bal::Cfg<4>::THREADS, 0, st>>>(ARGS);                 \
-        else if ((E) <= 256) KERNEL<8, __VA_ARGS__><<<GRID, bal::Cfg<8>::THREADS, 0, st>>>(ARGS);            \
-        else KERNEL<16, __VA_ARGS__><<<GRID, bal::Cfg<16>::THREADS, 0, st>>>(ARGS);                          \
-    } while (0)
+// KERNEL<elements a lane, TAIL...> for E experts, launched while what comes before it on the stream drains (each
+// waits for that before it reads).
+#define FS_BALANCE(KERNEL, E, GRID, ARGS, ...)                                                                          \
+    (E) <= 128 ? launch_after(KERNEL<4, __VA_ARGS__>, dim3(GRID), dim3(bal::Cfg<4>::THREADS), 0, st, ARGS)               \
+    : (E) <= 256 ? launch_after(KERNEL<8, __VA_ARGS__>, dim3(GRID), dim3(bal::Cfg<8>::THREADS), 0, st, ARGS)             \
+                 : launch_after(KERNEL<16, __VA_ARGS__>, dim3(GRID), dim3(bal::Cfg<16>::THREADS), 0, st, ARGS)
 
 template <bool SIG>
 static cudaError_t balance_fwd(const bal::Args& a, cudaStream_t st) {
     const bool vec = bal::vec_ok(a.z, a.z_row, a.E);
-    if (a.S == 1 && a.T <= bal::ONE_ROWS) {
-        if (vec) FS_BALANCE(bal::piece_kernel, a.E, 1, a, true, SIG, true);
-        else FS_BALANCE(bal::piece_kernel, a.E, 1, a, false, SIG, true);
-        count_launch();
-        return cudaGetLastError();
-    }
-    if (vec) FS_BALANCE(bal::piece_kernel, a.E, bal::blocks(a.T), a, true, SIG, false);
-    else FS_BALANCE(bal::piece_kernel, a.E, bal::blocks(a.T), a, false, SIG, false);
     count_launch();
-    cudaError_t e = cudaGetLastError();
+    if (a.S == 1 && a.T <= bal::ONE_ROWS)
+        return vec ? (FS_BALANCE(bal::piece_kernel, a.E, 1, a, true, SIG, true))
+                   : (FS_BALANCE(bal::piece_kernel, a.E, 1, a, false, SIG, true));
+    const cudaError_t e = vec ? (FS_BALANCE(bal::piece_kernel, a.E, bal::blocks(a.T), a, true, SIG, false))
+                              : (FS_BALANCE(bal::piece_kernel, a.E, bal::blocks(a.T), a, false, SIG, false));
     if (e != cudaSuccess) return e;
-    // launched while the first kernel drains; it waits for that kernel's end before it reads
-    e = launch_after(bal::finish_kernel, dim3(bal::expert_blocks(a.E), a.S), bal::FIN_E * bal::FIN_P, 0, st, a);
     count_launch();
-    return e;
+    return launch_after(bal::finish_kernel, dim3(bal::expert_blocks(a.E), a.S), dim3(bal::FIN_E * bal::FIN_P), 0, st, a);
 }
 
 template <bool SIG>
 static cudaError_t balance_bwd(const bal::BwdArgs& a, cudaStream_t st) {
-    if (bal::vec_ok(a.z, a.z_row, a.E) && bal::vec_ok(a.dz, a.dz_row, a.E))
-        FS_BALANCE(bal::backward_kernel, a.E, bal::blocks(a.T), a, true, SIG);
-    else
-        FS_BALANCE(bal::backward_kernel, a.E, bal::blocks(a.T), a, false, SIG);
+    const bool vec = bal::vec_ok(a.z, a.z_row, a.E) && bal::vec_ok(a.dz, a.dz_row, a.E);
     count_launch();
-    return cudaGetLastError();
+    return vec ? (FS_BALANCE(bal::backward_kernel, a.E, bal::blocks(a.T), a, true, SIG))
+               : (FS_BALANCE(bal::backward_kernel, a.E, bal::blocks(a.T), a, false, SIG));
 }
 
 cudaError_t launch_balance(const BalanceArgs& b, void* ws, cudaStream_t st) {

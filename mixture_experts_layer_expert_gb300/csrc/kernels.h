@@ -252,9 +252,10 @@ struct OrthoArgs {
 };
 size_t ortho_ws_bytes(int batch, int m, int n);
 cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st);
-// ortho_small.cu: a matrix in one cluster of blocks, all steps in one launch (no workspace)
+// ortho_small.cu: a matrix in one cluster of blocks, all steps in one launch
 bool ortho_small_fits(int m, int n);
-cudaError_t launch_ortho_small(const OrthoArgs& o, cudaStream_t st);
+size_t ortho_small_ws_bytes(int batch, int m, int n);
+cudaError_t launch_ortho_small(const OrthoArgs& o, void* ws, cudaStream_t st);
 
 // rope.cu
 struct RopeTab;

@@ -646,12 +646,12 @@ cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtens
 }  // namespace ortho
 
 size_t ortho_ws_bytes(int batch, int m, int n) {
-    return ortho_small_fits(m, n) ? 256 : ortho::layout(batch, m, n).end;
+    return ortho_small_fits(m, n) ? ortho_small_ws_bytes(batch, m, n) : ortho::layout(batch, m, n).end;
 }
 
 cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) {
     using namespace ortho;
-    if (ortho_small_fits(o.m, o.n)) return launch_ortho_small(o, st);
+    if (ortho_small_fits(o.m, o.n)) return launch_ortho_small(o, ws, st);
     const Shape s = shape(o.m, o.n);
     const Layout l = layout(o.batch, o.m, o.n);
     int sms = 0;

@@ -55,6 +55,13 @@ struct Squares {
 // fp32's range on the way.  A matrix of zeros stays zero, one with a NaN or infinity becomes NaN.
 __device__ __forceinline__ void norm_factors(double big, double mid, double small, double eps, float xscale, float* f1,
                                              float* f2) {
+    // the usual case, without the slow 64-bit functions: 2^28 values below 2^-50 add at most 2^-72, 2^-28 of it
+    if (big == 0.0 && mid > 0x1p-44 && mid < 0x1p80) {
+        const float n = sqrtf(static_cast<float>(mid)) + static_cast<float>(eps);
+        *f1 = 1.0f;
+        *f2 = xscale / n;
+        return;
+    }
     const double norm = sqrt(big * 0x1p176 + mid + small * 0x1p-200) + eps;
     int e = 0;
     frexp(norm, &e);

@@ -4,14 +4,16 @@
 // The mathematics is ortho.cu's.  A cluster of C thread blocks holds one matrix: block c a
 // slice of up to 256 columns of X, in fp32 registers (a row and 128 columns a thread) and as the
 // fp16 operand H in shared memory.  Per step
-//   the block's share of X X^T (128 x 128, tensor cores) -> summed over the cluster through
-//   distributed shared memory, each block a band of rows, in rank order -> A (fp16) in every block
+//   the block's share of X X^T (tensor cores) -> summed over the cluster in rank order, each block
+//   a band of rows -> A (fp16) in every block
 //   B = b A + c A A in every block (the same bits), its diagonal kept apart in fp32
 //   X = a X + B H for the block's columns.
 // H serves both products where it lies: K-major for X X^T, MN-major for B H.  X never leaves the
-// block, so it is carried in full fp32.
-// Bound by latency: five steps of 128 x 128 .. 2,048 are three products of a few hundred
-// cycles each behind each other, with two cluster barriers a step.
+// block, so it is carried in full fp32.  The shares go through the workspace, that is L2:
+// distributed shared memory moves about 14 bytes a cycle and SM, and the exchange of a 128 x 128
+// share took 11,000 cycles of a step that way.
+// Bound by latency: three products of some hundred cycles each behind each other, what lies
+// between them, and two cluster barriers a step.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -31,6 +33,7 @@ constexpr int A_OFF = H_OFF + (W / 64) * BLOCK;
 constexpr int B_OFF = A_OFF + 2 * BLOCK;
 constexpr int P_OFF = B_OFF + 2 * BLOCK;
 constexpr int P_ROW = R + 4;                   // floats: 16-byte accesses of 8 rows fall into different banks
+constexpr int SHARE = R * R * 4;               // bytes of a block's share of X X^T in the workspace
 constexpr int D_OFF = P_OFF + R * P_ROW * 4;   // fp32: B's diagonal
 constexpr int N_OFF = D_OFF + R * 4;           // sums of squares of the cluster's blocks, 16 x 4 floats
 constexpr int S_OFF = N_OFF + 16 * 16;         // of this block's warps, 8 x 4 floats, then the two factors
@@ -45,6 +48,8 @@ struct Args {
     long long out_row, out_mat;
     int out_vec;
     int r, q, tall, steps, width;              // width: columns per block, a multiple of 64
+    int rr, batch;                             // rr: r rounded up to 64
+    uint8_t* ws;                               // per block a share, then per cluster A [rr][rr] fp16
     float scale, eps;
     OrthoScales sc;
     float coefs[48];
@@ -56,11 +61,6 @@ __device__ __forceinline__ uint32_t chunk(int row, int col) {
     return (col >> 6) * BLOCK + row * 128 + ((((col >> 3) & 7) ^ (row & 7)) << 4);
 }
 
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-    return v;
-}
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint4 v) {
     asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
@@ -81,7 +81,11 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, half = warp >> 2;
     const int row = quarter * 32 + lane;
     const int C = cluster_size(), rank = static_cast<int>(cluster_ctarank());
-    const int z = blockIdx.x / C;
+    const int cluster = blockIdx.x / C, clusters = gridDim.x / C;
+    const int rr = a.rr, cols_a = rr / 2;                           // columns of A and B that this thread's half takes
+    float* share = reinterpret_cast<float*>(a.ws + static_cast<size_t>(blockIdx.x) * SHARE);
+    const float* shares = reinterpret_cast<const float*>(a.ws + static_cast<size_t>(cluster) * C * SHARE);
+    uint8_t* a_out = a.ws + static_cast<size_t>(gridDim.x) * SHARE + static_cast<size_t>(cluster) * (R * R * 2);
     const int col_first = rank * a.width + half * 128;              // this thread's first column of X
     const int ncol = min(128, a.width - half * 128);                // and how many it holds (a multiple of 64, may be <= 0)
 
@@ -94,6 +98,25 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    cudaGridDependencySynchronize();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                          // every block of the cluster runs before its memory is written
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    const uint32_t idesc_sq = idesc_f16(R, rr, 0);
+    const uint32_t idesc_x = idesc_f16(R, a.width, 1);
+    uint32_t phase = 0;
+    bool ok = true;          // after a wait that gave up the phases go on (the cluster's barriers have to match), unwaited
+    auto finish_mma = [&]() {
+        if (ok) ok = mbar_wait(smem_u32(bar), phase, abort_flag, a.err);
+        phase ^= 1u;
+        tc_fence_after();
+    };
+
+#pragma unroll 1
+    for (int z = cluster; z < a.batch; z += clusters) {
     // ---- the block's slice of G, and the norm
     float x[128];
     Squares sq;
@@ -128,8 +151,17 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
 #pragma unroll
             for (int c = 0; c < 128; ++c) x[c] = c < valid ? at(a.src, p, c * step) : 0.0f;
         }
+        // squares: as they are where none can overflow or matters below 2^-63, else range by range
+        float top = 0.f;
 #pragma unroll
-        for (int c = 0; c < 128; ++c) sq.add(x[c]);
+        for (int c = 0; c < 128; ++c) top = fmaxf(top, fabsf(x[c]));
+        if ((top >= 0x1p-40f && top <= 0x1p40f) || top == 0.0f) {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) sq.mid += x[c] * x[c];
+        } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c) sq.add(x[c]);
+        }
     }
     {
         float v[3] = {sq.big, sq.mid, sq.small};
@@ -141,11 +173,7 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
             if (lane == 0) mine[k] = v[k];
         }
     }
-    tc_fence_before();
     __syncthreads();
-    cluster_sync();                          // every block of the cluster runs before its memory is written
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
     if (threadIdx.x < C) {                   // this block's sums to block threadIdx.x
         float s[3] = {0.f, 0.f, 0.f};
         for (int w = 0; w < 8; ++w)
@@ -172,17 +200,6 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
 #pragma unroll
         for (int c = 0; c < 128; ++c) x[c] = x[c] * f1 * f2;
     }
-
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-    constexpr uint32_t idesc_sq = idesc_f16(R, R, 0);
-    const uint32_t idesc_x = idesc_f16(R, a.width, 1);
-    uint32_t phase = 0;
-    bool ok = true;          // after a wait that gave up the phases go on (the cluster's barriers have to match), unwaited
-    auto finish_mma = [&]() {
-        if (ok) ok = mbar_wait(smem_u32(bar), phase, abort_flag, a.err);
-        phase ^= 1u;
-        tc_fence_after();
-    };
 
 #pragma unroll 1
     for (int k = 0; k < a.steps; ++k) {
@@ -215,8 +232,9 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         if (C == 1) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                if (32 * h >= cols_a || row >= rr) break;
                 uint32_t v[32];
-                const int c0 = half * 64 + h * 32;
+                const int c0 = half * cols_a + h * 32;
                 tmem_ld32(taddr + D_A + c0, v);
                 tmem_ld_wait();
 #pragma unroll
@@ -232,35 +250,37 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
             float* P = reinterpret_cast<float*>(smem + P_OFF) + row * P_ROW;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                if (32 * h >= cols_a || row >= rr) break;
                 uint32_t v[32];
-                const int c0 = half * 64 + h * 32;
+                const int c0 = half * cols_a + h * 32;
                 tmem_ld32(taddr + D_A + c0, v);
                 tmem_ld_wait();
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
                     *reinterpret_cast<uint4*>(P + c0 + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
             }
+            __syncthreads();
+            const int vr = rr / 4, lg = rr == 64 ? 4 : 5;           // float4 per row, and its logarithm
+            for (int i = threadIdx.x; i < rr * vr; i += THREADS)
+                __stcg(reinterpret_cast<float4*>(share) + i,
+                       *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + P_OFF) + (i >> lg) * P_ROW + (i & (vr - 1)) * 4));
             cluster_sync();
-            // rows [rank 128 / C, ..): eight columns a thread, summed in rank order, sent to every block
-            const int band = R / C;
-            for (int g = threadIdx.x; g < band * 16; g += THREADS) {
-                const int r = rank * band + (g >> 4), c0 = (g & 15) * 8;
-                const uint32_t at_ = base + P_OFF + (r * P_ROW + c0) * 4;
-                float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            // rows [rank rr / C, ..) of A, four columns a thread, summed in rank order
+            const int first = rank * (rr / C) * vr;
+            for (int i = threadIdx.x; i < rr / C * vr; i += THREADS) {
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
                 for (int c = 0; c < C; ++c) {
-                    const uint32_t p = map_to_cta(at_, c);
-                    const float4 u = ld_cluster(p), w = ld_cluster(p + 16);
-                    s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
-                    s[4] += w.x; s[5] += w.y; s[6] += w.z; s[7] += w.w;
+                    const float4 u = __ldcg(reinterpret_cast<const float4*>(shares + c * (SHARE / 4)) + first + i);
+                    t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
                 }
-                const uint4 p = make_uint4(pack_half2(fa * s[0], fa * s[1]), pack_half2(fa * s[2], fa * s[3]),
-                                           pack_half2(fa * s[4], fa * s[5]), pack_half2(fa * s[6], fa * s[7]));
-                const uint32_t dst = base + A_OFF + chunk(r, c0);
-#pragma unroll 4
-                for (int c = 0; c < C; ++c) st_cluster(map_to_cta(dst, c), p);
+                __stcg(reinterpret_cast<uint2*>(a_out) + first + i, make_uint2(pack_half2(fa * t.x, fa * t.y), pack_half2(fa * t.z, fa * t.w)));
             }
             cluster_sync();
+            for (int i = threadIdx.x; i < rr * rr / 8; i += THREADS) {
+                const int r = i >> (lg - 1), c0 = (i & (vr / 2 - 1)) * 8;
+                *reinterpret_cast<uint4*>(smem + A_OFF + chunk(r, c0)) = __ldcg(reinterpret_cast<const uint4*>(a_out) + i);
+            }
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -269,8 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         if (warp == 0) {
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < R / 16; ++kk) {
+                for (int kk = 0; kk < rr / 16; ++kk) {
                     const uint64_t d = smem_desc_sw128(base + A_OFF + (kk >> 2) * BLOCK) + 2ull * (kk & 3);
                     tc_mma_bf16(tmem + D_AA, d, d, idesc_sq, kk > 0 ? 1u : 0u);
                 }
@@ -282,8 +301,9 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         const float f1 = cb * (a.sc.b / a.sc.a), f2 = cc * (a.sc.b / (a.sc.a * a.sc.a));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
+            if (32 * h >= cols_a || row >= rr) break;
             uint32_t v[32];
-            const int c0 = half * 64 + h * 32;
+            const int c0 = half * cols_a + h * 32;
             tmem_ld32(taddr + D_AA + c0, v);
             tmem_ld_wait();
 #pragma unroll
@@ -311,19 +331,18 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         if (warp == 0) {
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < R / 16; ++kk)
+                for (int kk = 0; kk < rr / 16; ++kk)
                     tc_mma_bf16(tmem + D_X, smem_desc_sw128(base + B_OFF + (kk >> 2) * BLOCK) + 2ull * (kk & 3),
                                 smem_desc_sw128_mn(base + H_OFF, BLOCK) + 128ull * kk, idesc_x, kk > 0 ? 1u : 0u);
                 tc_commit(smem_u32(bar));
             }
             __syncwarp();
         }
-        const float d = dvec[row] * (1.0f / a.sc.b), fx = 1.0f / a.sc.b;
+        const float d = row < rr ? dvec[row] * (1.0f / a.sc.b) : 0.0f, fx = 1.0f / a.sc.b;
         finish_mma();
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
-            if (c < ncol) {
+            if (c < ncol && quarter * 32 < rr) {
                 uint32_t v[32];
                 tmem_ld32(taddr + D_X + half * 128 + c, v);
                 tmem_ld_wait();
@@ -361,6 +380,8 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
             }
         }
     }
+    __syncthreads();                         // the norm's words are free again
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync();                          // no block leaves while another may read its memory
@@ -383,7 +404,16 @@ static int small_cluster(int r, int q) {
 
 bool ortho_small_fits(int m, int n) { return small_cluster(m < n ? m : n, m < n ? n : m) > 0; }
 
-cudaError_t launch_ortho_small(const OrthoArgs& o, cudaStream_t st) {
+// Clusters in flight: as many as 152 SMs hold.
+static int small_clusters(int batch, int C) { return batch < 152 / C ? batch : 152 / C; }
+
+size_t ortho_small_ws_bytes(int batch, int m, int n) {
+    const int C = small_cluster(m < n ? m : n, m < n ? n : m);
+    if (C == 1) return 256;
+    return static_cast<size_t>(small_clusters(batch, C)) * (C * ortho::small::SHARE + ortho::small::R * ortho::small::R * 2);
+}
+
+cudaError_t launch_ortho_small(const OrthoArgs& o, void* ws, cudaStream_t st) {
     using namespace ortho::small;
     using ortho::source;
     static bool set[kMaxDevices];
@@ -404,19 +434,24 @@ cudaError_t launch_ortho_small(const OrthoArgs& o, cudaStream_t st) {
     a.sc = o.scales;
     for (int i = 0; i < 3 * o.steps; ++i) a.coefs[i] = o.coefs[i];
     a.err = dev_error_ptr();
+    a.ws = static_cast<uint8_t*>(ws);
+    a.batch = o.batch;
+    a.rr = (a.r + 63) / 64 * 64;
     const int C = small_cluster(a.r, a.q);
     a.width = ((a.q + C - 1) / C + 63) / 64 * 64;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = C;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(o.batch) * C);
+    cfg.gridDim = dim3(static_cast<unsigned>(small_clusters(o.batch, C)) * C);
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = SMEM_BYTES;
     cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     e = cudaLaunchKernelEx(&cfg, small_kernel, a);
     count_launch();
     return e;
