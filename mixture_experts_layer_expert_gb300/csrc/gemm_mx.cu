@@ -36,32 +36,34 @@ namespace fs {
 namespace mx {
 
 constexpr int BM = 128;
-constexpr int BN = 256;
 constexpr int BK = 128;                       // bytes of K per stage
-constexpr int STAGES = 4;
 constexpr int A_STAGE = BM * BK;              // 16 KB
-constexpr int B_STAGE = BN * BK;              // 32 KB
-constexpr int STAGE_BYTES = A_STAGE + B_STAGE;
 constexpr int SFA_CHUNK = 512;                // scales of 128 rows x 4 blocks
-constexpr int SFB_CHUNK = 1024;               // of 256 rows x 4 blocks
-constexpr int SF_OFF = STAGES * STAGE_BYTES;                  // scale chunks after the code stages
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int PIECE_BYTES = 2048;
 constexpr int BAR_BYTES = 256;
 constexpr int TMEM_COLS = 512;
-constexpr int SF_SLOTS = 8;                   // scale-factor slots in TMEM (a ring, two per smem stage)
-constexpr int SF_COL0 = BN;                   // slot j starts at SF_COL0 + SF_COLS j: A's columns, then B's
 constexpr int kGroupM = 16;
 
-// What differs between the two element formats.
-template <bool F4>
+// What differs between the two element formats and the tile widths.  BN = 64 (E2M1, one group) is for
+// products with too few tiles of 256 columns for the SMs: four times the blocks stream the weights.
+template <bool F4, int BN>
 struct Fmt {
+    static constexpr int STAGES = BN == 256 ? 4 : 8;
+    static constexpr int B_STAGE = BN * BK;                   // 32 KB (8 KB)
+    static constexpr int STAGE_BYTES = A_STAGE + B_STAGE;
     static constexpr int CHUNKS = F4 ? 2 : 1;                 // scale chunks (128 elements) per stage
-    static constexpr int MAX_GROUPS = F4 ? kMaxExperts : kMaxGroups;   // the second chunk takes the room of half the plan
-    static constexpr int SF_STAGE = CHUNKS * (SFA_CHUNK + SFB_CHUNK);
+    // groups of the plan (E2M1: its second chunk takes the room of half of them)
+    static constexpr int MAX_GROUPS = BN < 256 ? 1 : (F4 ? kMaxExperts : kMaxGroups);
+    static constexpr int SFB_CHUNK = BN == 256 ? 1024 : 512;  // of 256 rows x 4 blocks (128 rows: a tile of 64 is half of one)
     static constexpr int SFA_BYTES = CHUNKS * SFA_CHUNK;
-    static constexpr int SF_COLS = CHUNKS * 12;               // TMEM columns per slot: 4 of A and 8 of B per chunk
+    static constexpr int SF_STAGE = CHUNKS * (SFA_CHUNK + SFB_CHUNK);
+    static constexpr int SFB_COLS = SFB_CHUNK / 128;          // TMEM columns of a chunk of B
+    static constexpr int SF_COLS = CHUNKS * (4 + SFB_COLS);   // per slot: A's columns, then B's
+    static constexpr int SF_SLOTS = 2 * STAGES;               // scale-factor slots in TMEM, a ring
+    static constexpr int SF_COL0 = BN;                        // behind the accumulator
+    static constexpr int SF_OFF = STAGES * STAGE_BYTES;       // shared memory: scale chunks after the code stages
     static constexpr int BAR_OFF = SF_OFF + STAGES * SF_STAGE;
     static constexpr int PLAN_OFF = BAR_OFF + BAR_BYTES;
     static constexpr int PIECE_OFF = (PLAN_OFF + 2 * (MAX_GROUPS + 1) * 4 + 1023) / 1024 * 1024;
@@ -131,6 +133,22 @@ __host__ __device__ constexpr uint32_t idesc_mx(int M, int N, int sf_id) {
            (static_cast<uint32_t>(sf_id) << 29);
 }
 
+// SiLU(g) u of two columns as bf16, in some ten instructions a value: this epilogue's code is run
+// once a tile, and with few rows by one warp, at the rate at which instructions are fetched (with
+// silu_f's division and exponential the 64 values of a thread took 24,000 cycles then, and the gate/up
+// product of 61 tokens over 64 experts 86 us instead of 36).
+// g / (1 + 2^(-g log2 e)) with the approximate exponential and reciprocal (2 units of 2^-23 each).
+__device__ __forceinline__ float swiglu_fast(uint32_t gate, uint32_t up) {
+    const float g = __uint_as_float(gate);
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return g * r * __uint_as_float(up);
+}
+__device__ __forceinline__ uint32_t swiglu_pair(uint32_t g0, uint32_t u0, uint32_t g1, uint32_t u1) {
+    return pack_bf16x2(swiglu_fast(g0, u0), swiglu_fast(g1, u1));
+}
+
 struct Tile {
     int g, m, n, a_row, rows_valid;
 };
@@ -177,11 +195,14 @@ __device__ __forceinline__ void store_piece(const CUtensorMap* tmo, uint8_t* pie
     }
 }
 
-template <int EPI, bool F4>
+template <int EPI, bool F4, int BN>
 __global__ void __launch_bounds__(THREADS, 1)
 mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmO, const Args args) {
-    using F = Fmt<F4>;
+    using F = Fmt<F4, BN>;
+    constexpr int STAGES = F::STAGES, STAGE_BYTES = F::STAGE_BYTES, SFB_CHUNK = F::SFB_CHUNK, SFB_COLS = F::SFB_COLS;
+    constexpr int HALF = BN / 2;                // columns of an epilogue warp
+    static_assert(BN == 256 || EPI != EPI_SWIGLU, "the hidden's blocks need gate and up in one warp's columns");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + F::BAR_OFF);
@@ -199,6 +220,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int lane = threadIdx.x & 31;
     const int G = args.G;
 
+    if constexpr (F4) cudaGridDependencySynchronize();
     if (args.plan) {
         for (int i = threadIdx.x; i < 2 * (G + 1); i += THREADS) mt_start[i] = args.plan[i];
     } else if (threadIdx.x == 0) {
@@ -234,6 +256,8 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int total = total_mtiles * args.n_tiles;
     const int chunks = args.K / 128;                              // scale chunks along K
     const int num_kb = (chunks + F::CHUNKS - 1) / F::CHUNKS;      // stages
+    constexpr int SUB = 256 / BN;                                 // tiles per 256-row block of the packed weights
+    const int tiles256 = (args.n_tiles + SUB - 1) / SUB;
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
@@ -247,19 +271,25 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 const Tile tl = decode(t, mt_start, row_start, G, args.n_tiles);
                 const uint8_t* sfa = args.a_sf + static_cast<size_t>(tl.a_row / BM) * chunks * SFA_CHUNK;
-                const uint8_t* sfb = args.b_sf + (static_cast<size_t>(tl.g) * args.n_tiles + tl.n) * chunks * SFB_CHUNK;
+                const uint8_t* sfb = args.b_sf + (static_cast<size_t>(tl.g) * tiles256 + tl.n / SUB) * chunks * 1024 +
+                                     (BN == 256 ? 0 : (tl.n % SUB) / 2 * 512);
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.err)) { ok = false; break; }
                     const uint32_t fb = smem_u32(&full[stage]);
                     const int nc = min(F::CHUNKS, chunks - kb * F::CHUNKS);
                     mbar_arrive_expect_tx(fb, STAGE_BYTES + nc * (SFA_CHUNK + SFB_CHUNK));
                     uint8_t* sa = smem + stage * STAGE_BYTES;
-                    uint8_t* sf = smem + SF_OFF + stage * F::SF_STAGE;
+                    uint8_t* sf = smem + F::SF_OFF + stage * F::SF_STAGE;
                     tma_load_2d(smem_u32(sa), &tmA, fb, kb * BK, tl.a_row);
-                    tma_load_3d(smem_u32(sa + A_STAGE), &tmB, fb, 0, 0, (tl.g * args.n_tiles + tl.n) * num_kb + kb);
+                    tma_load_3d(smem_u32(sa + A_STAGE), &tmB, fb, 0, tl.n % SUB * BN, (tl.g * tiles256 + tl.n / SUB) * num_kb + kb);
                     bulk_load(smem_u32(sf), sfa + static_cast<size_t>(kb) * F::SFA_BYTES, nc * SFA_CHUNK, fb);
-                    bulk_load(smem_u32(sf + F::SFA_BYTES), sfb + static_cast<size_t>(kb) * F::CHUNKS * SFB_CHUNK,
-                              nc * SFB_CHUNK, fb);
+                    if constexpr (BN == 256) {
+                        bulk_load(smem_u32(sf + F::SFA_BYTES), sfb + static_cast<size_t>(kb) * F::CHUNKS * 1024, nc * 1024, fb);
+                    } else {
+                        for (int q = 0; q < nc; ++q)
+                            bulk_load(smem_u32(sf + F::SFA_BYTES + q * 512), sfb + (static_cast<size_t>(kb) * F::CHUNKS + q) * 1024,
+                                      512, fb);
+                    }
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -285,6 +315,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             int it = 0;
             uint32_t slot = 0;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
+                const Tile tl = decode(t, mt_start, row_start, G, args.n_tiles);
                 // the epilogue has copied the previous tile out of TMEM
                 if (!mbar_wait(smem_u32(tempty), (static_cast<uint32_t>(it) & 1u) ^ 1u, abort_flag, args.err)) break;
                 tc_fence_after();
@@ -292,9 +323,9 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, args.err)) { ok = false; break; }
                     tc_fence_after();
                     uint8_t* sa = smem + stage * STAGE_BYTES;
-                    const uint32_t sf = smem_u32(smem + SF_OFF + stage * F::SF_STAGE);
-                    // chunk q: A's columns at tsa + 4 q, B's at tsb + 8 q (rows 0..127, then 128..255)
-                    const uint32_t tsa = tmem_base + SF_COL0 + static_cast<uint32_t>(F::SF_COLS) * slot;
+                    const uint32_t sf = smem_u32(smem + F::SF_OFF + stage * F::SF_STAGE);
+                    // chunk q: A's columns at tsa + 4 q, B's behind them (rows 0..127, then 128..255)
+                    const uint32_t tsa = tmem_base + F::SF_COL0 + static_cast<uint32_t>(F::SF_COLS) * slot;
                     const uint32_t tsb = tsa + 4u * F::CHUNKS;
                     const uint64_t adesc = smem_desc_sw128(smem_u32(sa));
                     const uint64_t bdesc = smem_desc_sw128(smem_u32(sa + A_STAGE));
@@ -302,19 +333,20 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     for (int q = 0; q < F::CHUNKS; ++q) {
                         if (q > 0 && kb * F::CHUNKS + q >= chunks) break;
                         sf_copy(tsa + 4u * q, sf + q * SFA_CHUNK);
-                        sf_copy(tsb + 8u * q, sf + F::SFA_BYTES + q * SFB_CHUNK);
-                        sf_copy(tsb + 8u * q + 4u, sf + F::SFA_BYTES + q * SFB_CHUNK + 512u);
+                        const uint32_t tb = tsb + static_cast<uint32_t>(SFB_COLS) * q;
+                        sf_copy(tb, sf + F::SFA_BYTES + q * SFB_CHUNK);
+                        if constexpr (BN == 256) sf_copy(tb + 4u, sf + F::SFA_BYTES + q * SFB_CHUNK + 512u);
                         constexpr int MMAS = 4 / F::CHUNKS;
 #pragma unroll
                         for (int j = 0; j < MMAS; ++j) {
                             const int kk = q * MMAS + j;
                             mma_mx<F4>(tmem_base, adesc + 2ull * kk, bdesc + 2ull * kk, idesc_mx<F4>(BM, BN, j * F::CHUNKS),
-                                       tsa + 4u * q, tsb + 8u * q, (kb > 0 || kk > 0) ? 1u : 0u);
+                                       tsa + 4u * q, tb + (BN == 256 ? 0u : 2u * (tl.n & 1)), (kb > 0 || kk > 0) ? 1u : 0u);
                         }
                     }
                     tc_commit(smem_u32(&empty[stage]));
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    slot = (slot + 1u) % SF_SLOTS;
+                    slot = (slot + 1u) % F::SF_SLOTS;
                 }
                 if (!ok) break;
                 tc_commit(smem_u32(tfull));
@@ -337,13 +369,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             const Tile tl = decode(t, mt_start, row_start, G, args.n_tiles);
             if (!mbar_wait(smem_u32(tfull), static_cast<uint32_t>(it) & 1u, abort_flag, args.err)) break;
             tc_fence_after();
-            // this warp's 32 rows x 128 columns, copied out of TMEM at once
-            const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
-            uint32_t v[128];
-            tmem_ld32(tb, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-            tmem_ld32(tb + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-            tmem_ld32(tb + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
-            tmem_ld32(tb + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
+            // this warp's 32 rows and half of the columns, copied out of TMEM at once
+            const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * HALF);
+            uint32_t v[HALF];
+#pragma unroll
+            for (int c = 0; c < HALF; c += 32) tmem_ld32(tb + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
@@ -360,23 +390,31 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     uint8_t* H = static_cast<uint8_t*>(args.out) + orow * args.ldo;
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        float h[32];
-                        float amax = 0.0f;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float g = __uint_as_float(v[32 * b + j]), u = __uint_as_float(v[64 + 32 * b + j]);
-                            // the stored hidden: bf16 rounding of SiLU(g) u
-                            h[j] = __bfloat162float(__float2bfloat16_rn(silu_f(g) * u));
-                            amax = fmaxf(amax, fabsf(h[j]));
-                        }
                         if constexpr (F4) {
-                            const Mx4Quant m = mx4_quant(h);
-                            *reinterpret_cast<uint4*>(H + (hc0 + 32 * b) / 2) = mx4_codes32(h, m.mult);
+                            uint32_t h[16];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                h[j] = swiglu_pair(v[32 * b + 2 * j], v[64 + 32 * b + 2 * j], v[32 * b + 2 * j + 1],
+                                                   v[64 + 32 * b + 2 * j + 1]);
+                            const Mx4Quant m = mx4_scale(absmax_bits(h));
+                            *reinterpret_cast<uint4*>(H + (hc0 + 32 * b) / 2) =
+                                make_uint4(mx4_codes8(h[0], h[1], h[2], h[3], m.mult), mx4_codes8(h[4], h[5], h[6], h[7], m.mult),
+                                           mx4_codes8(h[8], h[9], h[10], h[11], m.mult),
+                                           mx4_codes8(h[12], h[13], h[14], h[15], m.mult));
                             args.h_sf[mx_sf_byte(orow, (hc0 + 32 * b) / 32, args.out_cols)] = m.ue8m0;
                         } else {
+                            float h[32];
+                            float amax = 0.0f;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float g = __uint_as_float(v[32 * b + j]), u = __uint_as_float(v[64 + 32 * b + j]);
+                                // the stored hidden: bf16 rounding of SiLU(g) u
+                                h[j] = __bfloat162float(__float2bfloat16_rn(silu_f(g) * u));
+                                amax = fmaxf(amax, fabsf(h[j]));
+                            }
                             const MxQuant m = mx_quant(amax);
                             uint32_t c[8];
-    #pragma unroll
+#pragma unroll
                             for (int j = 0; j < 8; ++j) {
                                 float a0, a1, a2, a3;
                                 if (!m.q.wide) {
@@ -396,10 +434,10 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                 }
             } else if constexpr (EPI == EPI_BF16) {
-                const int c_base = tl.n * BN + half * 128;
+                const int c_base = tl.n * BN + half * HALF;
                 __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(args.out);
 #pragma unroll
-                for (int c0 = 0; c0 < 128; c0 += 32) {
+                for (int c0 = 0; c0 < HALF; c0 += 32) {
                     if (c_base + c0 >= args.out_cols) break;
                     uint32_t pk[16];
 #pragma unroll
@@ -415,11 +453,11 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                     }
                 }
             } else {   // EPI_F32
-                const int c_base = tl.n * BN + half * 128;
+                const int c_base = tl.n * BN + half * HALF;
                 float* Z = static_cast<float*>(args.out);
                 if (row_ok) {
 #pragma unroll
-                    for (int c0 = 0; c0 < 128; c0 += 4) {
+                    for (int c0 = 0; c0 < HALF; c0 += 4) {
                         if (c_base + c0 >= args.out_cols) break;
                         *reinterpret_cast<uint4*>(Z + orow * args.ldo + c_base + c0) =
                             make_uint4(v[c0], v[c0 + 1], v[c0 + 2], v[c0 + 3]);
@@ -442,21 +480,21 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 }  // namespace mx
 
 // ------------------------------------------------------------------- host
-template <int EPI, bool F4>
+template <int EPI, bool F4, int BN = 256>
 static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
                                   const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles, void* out,
                                   long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
     static bool set_mx[kMaxDevices];
-    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(mx::mx_gemm_kernel<EPI, F4>), mx::Fmt<F4>::SMEM_BYTES, set_mx);
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(mx::mx_gemm_kernel<EPI, F4, BN>), mx::Fmt<F4, BN>::SMEM_BYTES, set_mx);
     if (e != cudaSuccess) return e;
-    if (K % 128 || N % (F4 ? 8 : 128) || a_rows % 128 || G < 1 || G > mx::Fmt<F4>::MAX_GROUPS) return cudaErrorInvalidValue;
+    if (K % 128 || N % (F4 ? 8 : 128) || a_rows % 128 || G < 1 || G > mx::Fmt<F4, BN>::MAX_GROUPS) return cudaErrorInvalidValue;
     const int row_bytes = F4 ? K / 2 : K;
     const int stages = (row_bytes + mx::BK - 1) / mx::BK;      // the last one of a 4-bit row may be half full
     CUtensorMap ta, tb, to;
     e = make_map(&ta, A, a_rows, row_bytes, 128, true);
     if (e != cudaSuccess) return e;
-    const int n_tiles = (N + mx::BN - 1) / mx::BN;
-    e = make_map_blocked(&tb, B, static_cast<long long>(G) * n_tiles * stages, mx::BN, true);
+    const int n_tiles = (N + BN - 1) / BN;
+    e = make_map_blocked(&tb, B, static_cast<long long>(G) * ((N + 255) / 256) * stages, BN, true);
     if (e != cudaSuccess) return e;
     mx::Args args;
     args.plan = plan;
@@ -487,8 +525,11 @@ static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t
     const long long max_tiles = static_cast<long long>(max_mtiles) * n_tiles;
     int grid = static_cast<int>(max_tiles < sms ? max_tiles : sms);
     if (grid < 1) grid = 1;
-    mx::mx_gemm_kernel<EPI, F4><<<grid, mx::THREADS, mx::Fmt<F4>::SMEM_BYTES, st>>>(ta, tb, to, args);
     count_launch();
+    if (F4)         // set up while the kernel before it drains; it waits for that one's end before it reads
+        return launch_after(mx::mx_gemm_kernel<EPI, F4, BN>, dim3(grid), dim3(mx::THREADS), mx::Fmt<F4, BN>::SMEM_BYTES, st,
+                            ta, tb, to, args);
+    mx::mx_gemm_kernel<EPI, F4, BN><<<grid, mx::THREADS, mx::Fmt<F4, BN>::SMEM_BYTES, st>>>(ta, tb, to, args);
     return cudaGetLastError();
 }
 
@@ -496,6 +537,20 @@ template <bool F4>
 static cudaError_t launch_mx_fmt(int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
                                  const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
                                  void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
+    if constexpr (F4) {
+        // one group whose tiles of 256 columns would leave half of the SMs idle
+        int sms = 0;
+        const cudaError_t e = num_sms(&sms);
+        if (e != cudaSuccess) return e;
+        if (!plan && 2LL * max_mtiles * ((N + 255) / 256) <= sms) {
+            if (epi == EPI_BF16)
+                return launch_mx_impl<EPI_BF16, F4, 64>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+                                                        out_cols, h_sf, st);
+            if (epi == EPI_F32)
+                return launch_mx_impl<EPI_F32, F4, 64>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+                                                       out_cols, h_sf, st);
+        }
+    }
     switch (epi) {
         case EPI_SWIGLU:
             return launch_mx_impl<EPI_SWIGLU, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,

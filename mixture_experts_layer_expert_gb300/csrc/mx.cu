@@ -17,30 +17,28 @@ namespace fs {
 
 // One warp per row r < rows128 (grid-stride): x [rows, cols] bf16 -> q, an MX
 // matrix; rows past `rows` get zero codes and unit scales.
-template <bool F4>
 __global__ void __launch_bounds__(256)
 quant_rows_mx_kernel(const uint4* __restrict__ x, long long rows, int cols, uint8_t* __restrict__ q) {
     const int lane = threadIdx.x & 31;
     const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
-    using Codes = typename MxLane<F4>::Codes;
     const int nv = cols / 8;
-    uint8_t* sf = q + mx_sf_offset(F4, rows, cols);
+    uint8_t* sf = q + mx_sf_offset(false, rows, cols);
     const long long r128 = mx_rows128(rows);
     for (long long r = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < r128; r += nwarps) {
-        Codes* dst = reinterpret_cast<Codes*>(q + r * mx_row_bytes(F4, cols));
+        uint2* dst = reinterpret_cast<uint2*>(q + r * cols);
         for (int v0 = 0; v0 < nv; v0 += 32) {
             const int v = v0 + lane;
             const bool act = v < nv;
             if (r < rows) {
                 const uint4 a = act ? __ldg(x + r * nv + v) : make_uint4(0, 0, 0, 0);
                 uint8_t byte;
-                const Codes c = MxLane<F4>::quant(a, &byte);
+                const uint2 c = MxLane<false>::quant(a, &byte);
                 if (act) {
                     dst[v] = c;
                     if ((lane & 3) == 0) sf[mx_sf_byte(r, v / 4, cols)] = byte;
                 }
             } else if (act) {
-                dst[v] = MxLane<F4>::zero();
+                dst[v] = make_uint2(0, 0);
                 if ((lane & 3) == 0) sf[mx_sf_byte(r, v / 4, cols)] = 127;
             }
         }
@@ -50,35 +48,133 @@ quant_rows_mx_kernel(const uint4* __restrict__ x, long long rows, int cols, uint
 // One warp per token: u[t] quantised in 32-element blocks once; its codes and
 // scale bytes go to every slot's row pos[t, s] of x_q (an MX matrix of
 // rows_cap rows) and, when u_q is set, to row t of u_q (an MX matrix [T, d]).
-template <bool F4>
 __global__ void __launch_bounds__(256)
 dispatch_copy_mx_kernel(const uint4* __restrict__ u, int T, int d, int k, const int32_t* __restrict__ pos,
                         uint8_t* __restrict__ x_q, long long rows_cap, uint8_t* __restrict__ u_q) {
     const int lane = threadIdx.x & 31;
     const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
     if (t >= T) return;
-    using Codes = typename MxLane<F4>::Codes;
-    const int nv = d / 8, rb = mx_row_bytes(F4, d);
+    const int nv = d / 8;
     const int my_p = lane < k ? pos[static_cast<long long>(t) * k + lane] : -1;
-    uint8_t* xsf = x_q + mx_sf_offset(F4, rows_cap, d);
-    uint8_t* usf = u_q ? u_q + mx_sf_offset(F4, T, d) : nullptr;
+    uint8_t* xsf = x_q + mx_sf_offset(false, rows_cap, d);
+    uint8_t* usf = u_q ? u_q + mx_sf_offset(false, T, d) : nullptr;
     const uint4* src = u + static_cast<long long>(t) * nv;
     for (int v0 = 0; v0 < nv; v0 += 32) {
         const int v = v0 + lane;
         const bool act = v < nv;
         const uint4 a = act ? __ldg(src + v) : make_uint4(0, 0, 0, 0);
         uint8_t byte;
-        const Codes c = MxLane<F4>::quant(a, &byte);
+        const uint2 c = MxLane<false>::quant(a, &byte);
         const bool lead = (lane & 3) == 0;
         for (int s = 0; s < k; ++s) {
             const int p = __shfl_sync(0xffffffffu, my_p, s);
             if (p < 0 || !act) continue;
-            reinterpret_cast<Codes*>(x_q + static_cast<long long>(p) * rb)[v] = c;
+            reinterpret_cast<uint2*>(x_q + static_cast<long long>(p) * d)[v] = c;
             if (lead) xsf[mx_sf_byte(p, v / 4, d)] = byte;
         }
         if (u_q && act) {
-            reinterpret_cast<Codes*>(u_q + static_cast<long long>(t) * rb)[v] = c;
+            reinterpret_cast<uint2*>(u_q + static_cast<long long>(t) * d)[v] = c;
             if (lead) usf[mx_sf_byte(t, v / 4, d)] = byte;
+        }
+    }
+}
+
+// ---- 4-bit codes.  A lane holds 16 elements, half a block: 8 bytes of codes, so that a
+// warp's store of 512 elements is 256 consecutive bytes, and the four scale bytes of a chunk's
+// row (8 lanes) leave as one word.  Two such steps are in flight.  A row is shared by gridDim.y
+// warps of `per` steps each where there are fewer rows than warps that fill the SMs.
+
+// The codes of a lane's 16 elements; *word: in lanes 0, 8, 16, 24 the four scale bytes of the 8 lanes.
+__device__ __forceinline__ uint2 mx4_lane16(const uint4& a, const uint4& b, uint32_t* word) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t top = absmax_bits(w);
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    const Mx4Quant m = mx4_scale(top);
+    uint32_t s = m.ue8m0;
+    s |= __shfl_down_sync(0xffffffffu, s, 2) << 8;
+    s |= __shfl_down_sync(0xffffffffu, s, 4) << 16;
+    *word = s;
+    return make_uint2(mx4_codes8(w[0], w[1], w[2], w[3], m.mult), mx4_codes8(w[4], w[5], w[6], w[7], m.mult));
+}
+
+// x [rows, cols] -> q.  Zero rows behind them have zero codes and unit scales by themselves.
+__global__ void __launch_bounds__(256)
+quant_rows_mx4_kernel(const uint4* __restrict__ x, long long rows, int cols, int per, uint8_t* __restrict__ q) {
+    const int lane = threadIdx.x & 31;
+    const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
+    const int n16 = cols / 16;
+    const int first = blockIdx.y * per * 32, last = min(n16, first + per * 32);
+    uint8_t* sf = q + mx_sf_offset(true, rows, cols);
+    const long long r128 = mx_rows128(rows);
+    cudaGridDependencySynchronize();
+    for (long long r = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5; r < r128; r += nwarps) {
+        const uint4* src = x + r * 2 * n16;
+        uint2* dst = reinterpret_cast<uint2*>(q + r * (cols / 2));
+        for (int v0 = first; v0 < last; v0 += 64) {
+            uint4 a[2], b[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int v = v0 + 32 * s + lane;
+                const bool act = r < rows && v < last;
+                a[s] = act ? __ldg(src + 2 * v) : make_uint4(0, 0, 0, 0);
+                b[s] = act ? __ldg(src + 2 * v + 1) : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int v = v0 + 32 * s + lane;
+                if (v0 + 32 * s >= last) break;
+                uint32_t word;
+                const uint2 c = mx4_lane16(a[s], b[s], &word);
+                if (v < last) {
+                    dst[v] = c;
+                    if ((lane & 7) == 0) *reinterpret_cast<uint32_t*>(sf + mx_sf_byte(r, v / 2, cols)) = word;
+                }
+            }
+        }
+    }
+}
+
+// As dispatch_copy_mx_kernel.
+__global__ void __launch_bounds__(256)
+dispatch_copy_mx4_kernel(const uint4* __restrict__ u, int T, int d, int k, const int32_t* __restrict__ pos, int per,
+                         uint8_t* __restrict__ x_q, long long rows_cap, uint8_t* __restrict__ u_q) {
+    const int lane = threadIdx.x & 31;
+    const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
+    if (t >= T) return;
+    const int n16 = d / 16, rb = d / 2;
+    const int first = blockIdx.y * per * 32, last = min(n16, first + per * 32);
+    const int my_p = lane < k ? pos[static_cast<long long>(t) * k + lane] : -1;
+    uint8_t* xsf = x_q + mx_sf_offset(true, rows_cap, d);
+    uint8_t* usf = u_q ? u_q + mx_sf_offset(true, T, d) : nullptr;
+    const uint4* src = u + static_cast<long long>(t) * 2 * n16;
+    const bool lead = (lane & 7) == 0;
+    for (int v0 = first; v0 < last; v0 += 64) {
+        uint2 c[2];
+        uint32_t word[2];
+        uint4 a[2], b[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int v = v0 + 32 * s + lane;
+            a[s] = v < last ? __ldg(src + 2 * v) : make_uint4(0, 0, 0, 0);
+            b[s] = v < last ? __ldg(src + 2 * v + 1) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s) c[s] = mx4_lane16(a[s], b[s], &word[s]);
+        for (int slot = 0; slot <= k; ++slot) {              // the last one: u_q's row
+            const bool own = slot == k;
+            if (own && !u_q) break;
+            const int p = own ? t : __shfl_sync(0xffffffffu, my_p, slot);
+            if (p < 0) continue;
+            uint2* dst = reinterpret_cast<uint2*>((own ? u_q : x_q) + static_cast<long long>(p) * rb);
+            uint8_t* sf = own ? usf : xsf;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int v = v0 + 32 * s + lane;
+                if (v < last) {
+                    dst[v] = c[s];
+                    if (lead) *reinterpret_cast<uint32_t*>(sf + mx_sf_byte(p, v / 2, d)) = word[s];
+                }
+            }
         }
     }
 }
@@ -158,23 +254,41 @@ cudaError_t launch_pack_w3_shared_mx(bool f4, int ns, int cs, int d, const void*
     return launch_pack_mx(f4, s, 1, w3cat, st);
 }
 
+// Steps of 512 elements that a warp takes of a row, so that `rows` rows give 152 x 16 warps where they can.
+static int mx4_steps(long long rows, int cols) {
+    const int steps = (cols + 511) / 512;
+    long long split = 152LL * 16 / rows;
+    split = split < 1 ? 1 : (split > steps ? steps : split);
+    return static_cast<int>((steps + split - 1) / split);
+}
+
 cudaError_t launch_quant_rows_mx(bool f4, const void* x, long long rows, int cols, void* q, cudaStream_t st) {
-    const int grid = mx_grid(mx_rows128(rows));
+    const long long r128 = mx_rows128(rows);
     const uint4* src = static_cast<const uint4*>(x);
-    if (f4) quant_rows_mx_kernel<true><<<grid, 256, 0, st>>>(src, rows, cols, static_cast<uint8_t*>(q));
-    else quant_rows_mx_kernel<false><<<grid, 256, 0, st>>>(src, rows, cols, static_cast<uint8_t*>(q));
+    uint8_t* dst = static_cast<uint8_t*>(q);
     count_launch();
+    if (f4) {
+        const int per = mx4_steps(r128, cols);
+        return launch_after(quant_rows_mx4_kernel, dim3(mx_grid(r128), ((cols + 511) / 512 + per - 1) / per), dim3(256), 0, st,
+                            src, rows, cols, per, dst);
+    }
+    quant_rows_mx_kernel<<<mx_grid(r128), 256, 0, st>>>(src, rows, cols, dst);
     return cudaGetLastError();
 }
 
 cudaError_t launch_dispatch_copy_mx(bool f4, const void* u, int T, int d, int k, const int32_t* pos, void* x_q,
                                     long long rows_cap, void* u_q, cudaStream_t st) {
-    const int grid = static_cast<int>((static_cast<long long>(T) + 7) / 8);
+    const unsigned grid = static_cast<unsigned>((static_cast<long long>(T) + 7) / 8);
     const uint4* src = static_cast<const uint4*>(u);
     uint8_t *xq = static_cast<uint8_t*>(x_q), *uq = static_cast<uint8_t*>(u_q);
-    if (f4) dispatch_copy_mx_kernel<true><<<grid, 256, 0, st>>>(src, T, d, k, pos, xq, rows_cap, uq);
-    else dispatch_copy_mx_kernel<false><<<grid, 256, 0, st>>>(src, T, d, k, pos, xq, rows_cap, uq);
     count_launch();
+    if (f4) {
+        const int per = mx4_steps(T, d);
+        dispatch_copy_mx4_kernel<<<dim3(grid, ((d + 511) / 512 + per - 1) / per), 256, 0, st>>>(src, T, d, k, pos, per, xq,
+                                                                                                rows_cap, uq);
+    } else {
+        dispatch_copy_mx_kernel<<<grid, 256, 0, st>>>(src, T, d, k, pos, xq, rows_cap, uq);
+    }
     return cudaGetLastError();
 }
 

@@ -96,12 +96,6 @@ __device__ __forceinline__ Mx4Quant mx4_scale(uint32_t amax_bits) {
     m.ue8m0 = finite ? static_cast<uint8_t>(e + 127) : 255;
     return m;
 }
-__device__ __forceinline__ Mx4Quant mx4_quant(const float (&h)[32]) {
-    uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) top = max(top, __float_as_uint(h[j]) & 0x7FFFFFFFu);
-    return mx4_scale(top);
-}
 // E2M1 codes of 8 values, element 0 in the lowest nibble (nearest, ties to even).
 __device__ __forceinline__ uint32_t cvt_e2m1x8(float a0, float a1, float a2, float a3, float a4, float a5, float a6,
                                                float a7) {
@@ -116,15 +110,18 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(float a0, float a1, float a2, flo
         : "f"(a0), "f"(a1), "f"(a2), "f"(a3), "f"(a4), "f"(a5), "f"(a6), "f"(a7));
     return r;
 }
-__device__ __forceinline__ uint4 mx4_codes32(const float (&h)[32], float mult) {
-    uint32_t c[4];
+// Largest magnitude of the bf16 pairs, as fp32 bits.
+template <int N>
+__device__ __forceinline__ uint32_t absmax_bits(const uint32_t (&w)[N]) {
+    uint32_t top = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float* v = &h[8 * q];
-        c[q] = cvt_e2m1x8(v[0] * mult, v[1] * mult, v[2] * mult, v[3] * mult, v[4] * mult, v[5] * mult, v[6] * mult,
-                          v[7] * mult);
-    }
-    return make_uint4(c[0], c[1], c[2], c[3]);
+    for (int i = 1; i < N; ++i) top = __vmaxu2(top, w[i] & 0x7FFF7FFFu);
+    return max(top << 16, top & 0xFFFF0000u);
+}
+// Codes of 8 bf16 values.
+__device__ __forceinline__ uint32_t mx4_codes8(uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3, float mult) {
+    return cvt_e2m1x8(bf16lo(w0) * mult, bf16hi(w0) * mult, bf16lo(w1) * mult, bf16hi(w1) * mult, bf16lo(w2) * mult,
+                      bf16hi(w2) * mult, bf16lo(w3) * mult, bf16hi(w3) * mult);
 }
 
 // Largest magnitude over the 4-lane group holding one 32-element block (lanes
@@ -161,13 +158,9 @@ struct MxLane<true> {
     static __device__ __forceinline__ Codes zero() { return 0; }
     static __device__ __forceinline__ Codes quant(const uint4& a, uint8_t* byte) {
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max((w[i] & 0x7FFFu) << 16, w[i] & 0x7FFF0000u));
-        const Mx4Quant m = mx4_scale(group4_max(top));
+        const Mx4Quant m = mx4_scale(group4_max(absmax_bits(w)));
         *byte = m.ue8m0;
-        return cvt_e2m1x8(bf16lo(w[0]) * m.mult, bf16hi(w[0]) * m.mult, bf16lo(w[1]) * m.mult, bf16hi(w[1]) * m.mult,
-                          bf16lo(w[2]) * m.mult, bf16hi(w[2]) * m.mult, bf16lo(w[3]) * m.mult, bf16hi(w[3]) * m.mult);
+        return mx4_codes8(w[0], w[1], w[2], w[3], m.mult);
     }
 };
 
