@@ -21,7 +21,9 @@
 //
 // One GEMM serves the three products: CTA pairs (2-SM MMA) on 256 x 256 tiles, operands
 // by TMA in five stages of 64 along K, two accumulators in TMEM.  X X^T and A A compute
-// the tiles on and above the diagonal and store each 32 x 32 piece and its transpose.
+// the tiles on and above the diagonal and store each 32 x 32 piece and its transpose; their
+// tiles are 256 x 128 where few tiles leave clusters idle (five matrices of 333 rows: 15 tiles or 20;
+// a half tile takes 0.7 of a whole one's time, its MMAs being bound by the operand reads).
 // B X reads X as the MN-major operand, where it lies.  The epilogue's own inputs (the piece
 // of A, of H and L) come and go by TMA through two 4 KB buffers per warp.
 #include <cudaTypedefs.h>
@@ -34,11 +36,11 @@
 namespace fs {
 namespace ortho {
 
-constexpr int BT = 256;                       // tile rows and columns of a pair
+constexpr int BT = 256;                       // tile rows of a pair (and columns: BN)
 constexpr int BK = 64;
 constexpr int STAGES = 5;
 constexpr int A_STAGE = 128 * BK * 2;         // this CTA's 128 rows of the first operand
-constexpr int B_STAGE = 128 * BK * 2;         // its 128 rows (or columns) of the second
+constexpr int B_STAGE = 128 * BK * 2;         // room for its BN / 2 rows (or columns) of the second
 constexpr int STAGE_BYTES = A_STAGE + B_STAGE;
 constexpr int EPI_WARPS = 8;
 constexpr int THREADS = 64 + 32 * EPI_WARPS;
@@ -70,19 +72,33 @@ struct Tile {
     int z, i, j;
 };
 
-__device__ __forceinline__ int tiles_per_matrix(const Args& a, bool sym) { return sym ? a.R * (a.R + 1) / 2 : a.R * a.C; }
+// Tiles of a matrix: R x C, or of R x C those that reach the diagonal or lie above it.
+template <bool SYM, int BN>
+__host__ __device__ __forceinline__ int tiles_per_matrix(int R, int C) {
+    if (!SYM) return R * C;
+    if (BN == BT) return R * (R + 1) / 2;
+    const int m = C / 2;                   // columns 2m and 2m + 1 of tiles have m + 1 each
+    return (m + 1) * (m + (C & 1));
+}
 
-template <bool SYM>
+template <bool SYM, int BN>
 __device__ __forceinline__ Tile decode(int t, const Args& a, int per) {
     Tile r;
     r.z = t / per;
     const int x = t - r.z * per;
-    if constexpr (SYM) {               // column by column of the upper triangle: tile (i, j), i <= j, is j (j + 1) / 2 + i
+    if constexpr (SYM && BN == BT) {   // column by column of the upper triangle: tile (i, j), i <= j, is j (j + 1) / 2 + i
         int j = static_cast<int>((sqrtf(8.0f * static_cast<float>(x) + 1.0f) - 1.0f) * 0.5f);
         while (j * (j + 1) / 2 > x) --j;
         while ((j + 1) * (j + 2) / 2 <= x) ++j;
         r.j = j;
         r.i = x - j * (j + 1) / 2;
+    } else if constexpr (SYM) {        // the first tile of column 2m is m (m + 1)
+        int m = static_cast<int>((sqrtf(4.0f * static_cast<float>(x) + 1.0f) - 1.0f) * 0.5f);
+        while (m * (m + 1) > x) --m;
+        while ((m + 1) * (m + 2) <= x) ++m;
+        const int rem = x - m * (m + 1);
+        r.j = 2 * m + rem / (m + 1);
+        r.i = rem % (m + 1);
     } else {
         r.j = x / a.R;
         r.i = x - r.j * a.R;
@@ -106,7 +122,7 @@ __device__ __forceinline__ int chunk_at(int row, int q) { return row * 64 + ((q 
 // Element (row, col) of it.
 __device__ __forceinline__ int elem_at(int row, int col) { return chunk_at(row, col >> 3) + (col & 7) * 2; }
 
-template <int MODE>
+template <int MODE, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
             const __grid_constant__ CUtensorMap tmIn, const __grid_constant__ CUtensorMap tmInL,
@@ -114,6 +130,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     constexpr bool SYM = MODE == GRAM || MODE == POLY;
     constexpr bool B_MN = !SYM;
     constexpr bool LOADS = MODE != GRAM;
+    constexpr int HALF = BN / 2;                   // columns of an epilogue warp, and operand rows of a CTA
+    constexpr int PIECES = HALF / 32;
+    static_assert(BN == BT || SYM, "the MN-major operand comes in boxes of 64 columns, two a CTA");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + BAR_OFF);
@@ -154,7 +173,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     cudaGridDependencySynchronize();
-    const int per = tiles_per_matrix(args, SYM);
+    const int per = tiles_per_matrix<SYM, BN>(args.R, args.C);
     const int total = per * args.batch;
     const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(nclusters_x());
 
@@ -167,13 +186,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             uint32_t phase = 0;
             bool ok = true;
             for (int t = cid; t < total && ok; t += ncl) {
-                const Tile tl = decode<SYM>(t, args, per);
+                const Tile tl = decode<SYM, BN>(t, args, per);
                 const int a_row = tl.i * BT + static_cast<int>(rank) * 128;
-                const int b_row = tl.j * BT + static_cast<int>(rank) * 128;
+                const int b_row = tl.j * BN + static_cast<int>(rank) * HALF;
                 for (int kb = 0; kb < args.kb; ++kb) {
                     if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.err)) { ok = false; break; }
                     const uint32_t fb_local = smem_u32(&full[stage]);
-                    if (leader) mbar_arrive_expect_tx(fb_local, 2 * STAGE_BYTES);
+                    if (leader) mbar_arrive_expect_tx(fb_local, 2 * (A_STAGE + HALF * BK * 2));
                     const uint32_t fb = map_to_cta(fb_local, 0);
                     const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_STAGE;
                     tma_load_3d_pair(sa, &tmA, fb, kb * BK, a_row, tl.z);
@@ -204,7 +223,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     } else if (warp == 1) {
         // ----------------------------------------------------------------- MMA
         if (leader) {
-            constexpr uint32_t idesc = idesc_f16(BT, BT, B_MN);
+            constexpr uint32_t idesc = idesc_f16(BT, BN, B_MN);
             int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -213,7 +232,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 const uint32_t use = static_cast<uint32_t>(it >> 1);
                 if (!mbar_wait(smem_u32(&tempty[acc]), (use & 1u) ^ 1u, abort_flag, args.err)) break;
                 tc_fence_after();
-                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BT);
+                const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
                 for (int kb = 0; kb < args.kb; ++kb) {
                     if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, args.err)) { ok = false; break; }
                     tc_fence_after();
@@ -249,12 +268,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         uint8_t* buf0 = smem + EPI_OFF + ew * 2 * BUF;
         int it = 0;
         uint32_t asked = 0, used = 0;              // pieces whose inputs were asked for, and taken
+        [[maybe_unused]] uint32_t stored = 0;
         for (int t = cid; t < total; t += ncl, ++it) {
-            const Tile tl = decode<SYM>(t, args, per);
+            const Tile tl = decode<SYM, BN>(t, args, per);
             const int row0 = tl.i * BT + static_cast<int>(rank) * 128 + quarter * 32;
-            const int col0 = tl.j * BT + half * 128;
-            // this warp's pieces [first, last) of four along its 128 columns
-            int last = row0 < args.rows ? min(4, (args.cols - col0 + 31) / 32) : 0;
+            const int col0 = tl.j * BN + half * HALF;
+            // this warp's pieces [first, last) along its columns
+            int last = row0 < args.rows ? min(PIECES, (args.cols - col0 + 31) / 32) : 0;
             int first = SYM && col0 < row0 ? (row0 - col0) / 32 : 0;
             if (last < first) last = first;
             const int acc = it & 1;
@@ -281,14 +301,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (!mbar_wait(smem_u32(&tfull[acc]), use & 1u, abort_flag, args.err)) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                   static_cast<uint32_t>(acc * BT + half * 128);
+                                   static_cast<uint32_t>(acc * BN + half * HALF);
             bool ok = true;
 #pragma unroll 1
             for (int c = first; c < last; ++c) {
                 uint32_t v[32];
                 tmem_ld32(tbase + 32 * c, v);
                 tmem_ld_wait();
-                const uint32_t b = LOADS ? used & 1u : static_cast<uint32_t>(c) & 1u;
+                const uint32_t b = LOADS ? used & 1u : stored++ & 1u;
                 uint8_t* buf = buf0 + b * BUF;
                 const int x = col0 + 32 * c;
                 if constexpr (LOADS) {
@@ -323,18 +343,20 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     }
                     __syncwarp();
                 } else {
-                    if (lane == 0) bulk_wait_read0();
+                    // the store before the last one has read this buffer
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(args.beta * __uint_as_float(v[j]));
                 }
                 if (MODE == POLY && x == row0) {
+                    uint32_t on = 0;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (j == lane) {
-                            if (drow) *drow = __uint_as_float(v[j]);
-                            v[j] = 0u;
-                        }
+                    for (int j = 0; j < 32; ++j) {
+                        on = j == lane ? v[j] : on;
+                        v[j] = j == lane ? 0u : v[j];
+                    }
+                    if (drow) *drow = __uint_as_float(on);
                 }
                 if constexpr (MODE == LAST) {
                     // the result's piece, transposed for a tall matrix
@@ -364,10 +386,12 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     } else {
                         __syncwarp();
                         uint16_t* o = reinterpret_cast<uint16_t*>(args.out) + tl.z * args.out_mat;
-                        if (ox + lane < args.n)
-                            for (int y = 0; y < 32 && oy + y < args.m; ++y)
-                                o[(oy + y) * args.out_row + ox + lane] =
-                                    *reinterpret_cast<const uint16_t*>(buf + elem_at(y, lane));
+                        const bool in = ox + lane < args.n;
+                        o += oy * args.out_row + ox + lane;
+#pragma unroll
+                        for (int y = 0; y < 32; ++y)
+                            if (in && oy + y < args.m)
+                                o[y * args.out_row] = *reinterpret_cast<const uint16_t*>(buf + elem_at(y, lane));
                         __syncwarp();
                     }
                 } else {
@@ -448,27 +472,41 @@ __global__ void __launch_bounds__(256) norm_kernel(const Source s, float* part) 
     const size_t es = s.f32 ? 4 : 2;
     const uint8_t* g = static_cast<const uint8_t*>(s.g) + static_cast<long long>(blockIdx.y) * s.mat * es;
     Squares q;
+    cudaGridDependencySynchronize();
     for (int i = blockIdx.x * 8 + warp; i < s.m; i += gridDim.x * 8) {
         const uint8_t* row = g + i * s.row * es;
         if (s.vec) {
             const int nv = s.n / (16 / static_cast<int>(es));
-#pragma unroll 4
-            for (int v = lane; v < nv; v += 32) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4*>(row) + v);
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int v0 = lane; v0 < nv; v0 += 128) {
+                uint4 x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    x[k] = v0 + 32 * k < nv ? __ldg(reinterpret_cast<const uint4*>(row) + v0 + 32 * k) : make_uint4(0, 0, 0, 0);
+                float f[32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (s.f32) {
-                        q.add(__uint_as_float(w[k]));
-                    } else {
-                        q.add(bf16lo(w[k]));
-                        q.add(bf16hi(w[k]));
+                    const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        f[8 * k + 2 * h] = s.f32 ? __uint_as_float(w[h]) : bf16lo(w[h]);
+                        f[8 * k + 2 * h + 1] = s.f32 ? 0.0f : bf16hi(w[h]);
                     }
                 }
+                q.add(f);
             }
         } else {
-#pragma unroll 8
-            for (int j = lane; j < s.n; j += 32) q.add(at(s, row, j));
+            for (int j0 = lane; j0 < s.n; j0 += 512) {
+                float f[16];
+                if (s.f32) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) f[k] = j0 + 32 * k < s.n ? __ldg(reinterpret_cast<const float*>(row) + j0 + 32 * k) : 0.0f;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        f[k] = j0 + 32 * k < s.n ? __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(row) + j0 + 32 * k)) : 0.0f;
+                }
+                q.add(f);
+            }
         }
     }
     float v[3] = {q.big, q.mid, q.small};
@@ -630,17 +668,30 @@ cudaError_t pieces(CUtensorMap* map, void* base, int cols, int rows, int mats) {
                   static_cast<long long>(rows) * cols * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-template <int MODE>
-cudaError_t launch_gemm(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in, const CUtensorMap& in_l,
-                        const CUtensorMap& out, const CUtensorMap& out_l, const Args& args, int sms, cudaStream_t st) {
+template <int MODE, int BN>
+cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in, const CUtensorMap& in_l,
+                         const CUtensorMap& out, const CUtensorMap& out_l, Args args, int sms, cudaStream_t st) {
     static bool set[kMaxDevices];
-    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(gemm_kernel<MODE>), SMEM_BYTES, set);
+    cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(gemm_kernel<MODE, BN>), SMEM_BYTES, set);
     if (e != cudaSuccess) return e;
-    const long long tiles = static_cast<long long>(MODE <= POLY ? args.R * (args.R + 1) / 2 : args.R * args.C) * args.batch;
+    args.C = (args.cols + BN - 1) / BN;
+    const long long tiles = static_cast<long long>(tiles_per_matrix<MODE <= POLY, BN>(args.R, args.C)) * args.batch;
     const int clusters = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
-    e = launch_after(gemm_kernel<MODE>, dim3(2 * clusters), dim3(THREADS), SMEM_BYTES, st, a, b, in, in_l, out, out_l, args);
     count_launch();
-    return e;
+    return launch_after(gemm_kernel<MODE, BN>, dim3(2 * clusters), dim3(THREADS), SMEM_BYTES, st, a, b, in, in_l, out, out_l, args);
+}
+
+// The symmetric products: a is the map of boxes of 128 rows, b_half of 64.  The tile width whose rounds of
+// clusters take less time: measured 37 and 27 us for a tile of K = 7,168, 14 and 9 us for K = 2,048.
+template <int MODE>
+cudaError_t launch_square(const CUtensorMap& a, const CUtensorMap& b_half, const CUtensorMap& in, const CUtensorMap& out,
+                          const Args& args, int sms, cudaStream_t st) {
+    const auto rounds = [&](long long tiles) { return (tiles * args.batch + sms / 2 - 1) / (sms / 2); };
+    const int c = (args.cols + 127) / 128;
+    const long long whole = 10 * rounds(tiles_per_matrix<true, BT>(args.R, args.R));
+    const long long half = 7 * rounds(tiles_per_matrix<true, 128>(args.R, c));
+    return half < whole ? launch_tiles<MODE, 128>(a, b_half, in, in, out, out, args, sms, st)
+                        : launch_tiles<MODE, BT>(a, a, in, in, out, out, args, sms, st);
 }
 
 }  // namespace ortho
@@ -667,9 +718,8 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
         // a row per warp; the split depends on the matrix alone, so that a matrix's result does not depend on its batch
         int blocks = (o.m + 7) / 8;
         blocks = blocks > NORM_BLOCKS ? NORM_BLOCKS : blocks;
-        norm_kernel<<<dim3(blocks, nb), 256, 0, st>>>(src, part);
         count_launch();
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_after(norm_kernel, dim3(blocks, nb), dim3(256), 0, st, src, part)) != cudaSuccess) return e;
         __half* H[2] = {reinterpret_cast<__half*>(w + l.h[0]), reinterpret_cast<__half*>(w + l.h[1])};
         __half* L = reinterpret_cast<__half*>(w + l.l);
         // tiles of G; for X's padded width the last ones reach past it
@@ -679,7 +729,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
         count_launch();
         if (e != cudaSuccess) return e;
 
-        CUtensorMap xk[2], xn[2], xp[2], lp, ak, ap, bk, bp, op;
+        CUtensorMap xk[2], xn[2], xp[2], lp, ak, an, ap, bk, bp, op;
         void *A = w + l.a, *B = w + l.b;
         for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
             e = operand(&xk[i], H[i], s.qp, s.r, nb, 128);
@@ -688,6 +738,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
         }
         if (e == cudaSuccess) e = pieces(&lp, L, s.qp, s.r, nb);
         if (e == cudaSuccess) e = operand(&ak, A, s.rp, s.r, nb, 128);
+        if (e == cudaSuccess) e = operand(&an, A, s.rp, s.r, nb, 64);
         if (e == cudaSuccess) e = pieces(&ap, A, s.rp, s.r, nb);
         if (e == cudaSuccess) e = operand(&bk, B, s.rp, s.r, nb, 128);
         if (e == cudaSuccess) e = pieces(&bp, B, s.rp, s.r, nb);
@@ -724,29 +775,27 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
             const float ca = o.coefs[3 * k], cb = o.coefs[3 * k + 1], cc = o.coefs[3 * k + 2];
             const bool last = k == o.steps - 1;
             Args a = g;
-            a.C = a.R;
             a.cols = s.rp;
             a.kb = s.qp / BK;
             a.beta = sc.a / (sc.x * sc.x);
-            e = launch_gemm<GRAM>(xk[cur], xk[cur], ap, ap, ap, ap, a, sms, st);
+            e = launch_square<GRAM>(xk[cur], xn[cur], ap, ap, a, sms, st);
             if (e != cudaSuccess) return e;
             a.kb = s.rp / BK;
             a.alpha = cb * (sc.b / sc.a);
             a.beta = cc * (sc.b / (sc.a * sc.a));
-            e = launch_gemm<POLY>(ak, ak, ap, ap, bp, bp, a, sms, st);
+            e = launch_square<POLY>(ak, an, ap, bp, a, sms, st);
             if (e != cudaSuccess) return e;
-            a.C = (s.qp + BT - 1) / BT;
             a.cols = s.qp;
             a.low_in = low[k];
             a.low_out = low[k + 1];
             a.alpha = ca;
             a.beta = 1.0f / sc.b;
             if (!last) {
-                e = launch_gemm<STEP>(bk, xn[cur], xp[cur], lp, xp[cur ^ 1], lp, a, sms, st);
+                e = launch_tiles<STEP, BT>(bk, xn[cur], xp[cur], lp, xp[cur ^ 1], lp, a, sms, st);
             } else {
                 a.alpha *= o.scale / sc.x;
                 a.beta *= o.scale / sc.x;
-                e = launch_gemm<LAST>(bk, xn[cur], xp[cur], lp, op, op, a, sms, st);
+                e = launch_tiles<LAST, BT>(bk, xn[cur], xp[cur], lp, op, op, a, sms, st);
             }
             if (e != cudaSuccess) return e;
         }

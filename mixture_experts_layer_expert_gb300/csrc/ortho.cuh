@@ -49,6 +49,20 @@ struct Squares {
         else if (a < 0x1p-50f) small += (x * 0x1p100f) * (x * 0x1p100f);
         else mid += x * x;                     // a NaN lands here
     }
+    // Several at once: squared as they are where none can overflow or matters below 2^-63, else range by range.
+    template <int N>
+    __device__ __forceinline__ void add(const float (&x)[N]) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(x[i]));
+        if ((top >= 0x1p-40f && top <= 0x1p40f) || top == 0.0f) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) mid += x[i] * x[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) add(x[i]);
+        }
+    }
 };
 
 // xscale / (norm + eps) as two fp32 factors, the first a power of two: no product with them leaves

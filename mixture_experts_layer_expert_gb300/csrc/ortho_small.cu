@@ -151,17 +151,7 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
 #pragma unroll
             for (int c = 0; c < 128; ++c) x[c] = c < valid ? at(a.src, p, c * step) : 0.0f;
         }
-        // squares: as they are where none can overflow or matters below 2^-63, else range by range
-        float top = 0.f;
-#pragma unroll
-        for (int c = 0; c < 128; ++c) top = fmaxf(top, fabsf(x[c]));
-        if ((top >= 0x1p-40f && top <= 0x1p40f) || top == 0.0f) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c) sq.mid += x[c] * x[c];
-        } else {
-#pragma unroll
-            for (int c = 0; c < 128; ++c) sq.add(x[c]);
-        }
+        sq.add(x);
     }
     {
         float v[3] = {sq.big, sq.mid, sq.small};
