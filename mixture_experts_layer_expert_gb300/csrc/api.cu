@@ -314,11 +314,18 @@ static fs_status swiglu_impl(const fs_layer_desc* d, const void* x, long long x_
         const uint8_t* xs = static_cast<const uint8_t*>(x) + mx_sf_offset(f4, xr, d->d);
         uint8_t* hc = static_cast<uint8_t*>(h);
         uint8_t* hs = hc + mx_sf_offset(f4, xr, cw);
-        FS_TRY(launch_plan(offsets, G, offsets ? static_cast<int>(xr) : rows, 128, plan, st));
-        FS_TRY(launch_mx_gemm(f4, EPI_SWIGLU, x, xr, xs, w13, packed_sf_mx(f4, w13, G, 2 * cw, d->d), G, 2 * cw, d->d,
-                              plan, rows, max_mt, hc, mx_row_bytes(f4, cw), cw, hs, st));
-        FS_TRY(launch_mx_gemm(f4, y_f32 ? EPI_F32 : EPI_BF16, hc, xr, hs, w3, packed_sf_mx(f4, w3, G, d->d, cw), G, d->d,
-                              cw, plan, rows, max_mt, y, d->d, d->d, nullptr, st));
+        // 4-bit products of large groups run on CTA pairs
+        const bool pair = f4 && (offsets ? static_cast<long long>(d->T) * d->k / G : rows) >= kMx4PairRows;
+        const int mt = pair ? ceil_div(xr, 256) + G : max_mt;
+        const auto gemm = [&](int epi, const void* a, const uint8_t* as, const void* w, int N, int K, void* out, long long ldo,
+                              int out_cols, uint8_t* out_sf) {
+            const uint8_t* wsf = packed_sf_mx(f4, w, G, N, K);
+            return pair ? launch_mx4_pair_gemm(epi, a, xr, as, w, wsf, G, N, K, plan, rows, mt, out, ldo, out_cols, out_sf, st)
+                        : launch_mx_gemm(f4, epi, a, xr, as, w, wsf, G, N, K, plan, rows, mt, out, ldo, out_cols, out_sf, st);
+        };
+        FS_TRY(launch_plan(offsets, G, offsets ? static_cast<int>(xr) : rows, pair ? 256 : 128, plan, st));
+        FS_TRY(gemm(EPI_SWIGLU, x, xs, w13, 2 * cw, d->d, hc, mx_row_bytes(f4, cw), cw, hs));
+        FS_TRY(gemm(y_f32 ? EPI_F32 : EPI_BF16, hc, hs, w3, d->d, cw, y, d->d, d->d, nullptr));
     } else if (is_fp8(d)) {
         const int bm = tc_block_m_f8();
         const int max_mt = ceil_div(rows, bm) + G;
@@ -614,10 +621,16 @@ fs_status fs_linear_mx4(int64_t rows, int32_t N, int32_t K, const void* q, const
     if (!ws) return FS_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < fs_linear_mx4_ws_bytes(rows, N, K)) return FS_ERR_WORKSPACE;
     const long long r128 = mx_rows128(rows);
-    FS_TRY(launch_mx_gemm(true, y_dtype == FS_BF16 ? EPI_BF16 : EPI_F32, q, r128,
-                          static_cast<const uint8_t*>(q) + mx_sf_offset(true, rows, K), w, packed_sf_mx(true, w, 1, N, K), 1,
-                          N, K, nullptr, static_cast<int>(rows), static_cast<int>(r128 / 128), y, y_row, N, nullptr,
-                          static_cast<cudaStream_t>(stream)));
+    const int epi = y_dtype == FS_BF16 ? EPI_BF16 : EPI_F32;
+    const uint8_t* qs = static_cast<const uint8_t*>(q) + mx_sf_offset(true, rows, K);
+    const uint8_t* wsf = packed_sf_mx(true, w, 1, N, K);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (rows >= kMx4PairRows)
+        FS_TRY(launch_mx4_pair_gemm(epi, q, r128, qs, w, wsf, 1, N, K, nullptr, static_cast<int>(rows), ceil_div(rows, 256), y,
+                                    y_row, N, nullptr, st));
+    else
+        FS_TRY(launch_mx_gemm(true, epi, q, r128, qs, w, wsf, 1, N, K, nullptr, static_cast<int>(rows),
+                              static_cast<int>(r128 / 128), y, y_row, N, nullptr, st));
     return FS_OK;
 }
 

@@ -28,9 +28,7 @@
 #include <cudaTypedefs.h>
 #include <cstring>
 
-#include "common.cuh"
-#include "kernels.h"
-#include "mx.cuh"
+#include "gemm_mx.cuh"
 
 namespace fs {
 namespace mx {
@@ -39,12 +37,8 @@ constexpr int BM = 128;
 constexpr int BK = 128;                       // bytes of K per stage
 constexpr int A_STAGE = BM * BK;              // 16 KB
 constexpr int SFA_CHUNK = 512;                // scales of 128 rows x 4 blocks
-constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
-constexpr int PIECE_BYTES = 2048;
 constexpr int BAR_BYTES = 256;
 constexpr int TMEM_COLS = 512;
-constexpr int kGroupM = 16;
 
 // What differs between the two element formats and the tile widths.  BN = 64 (E2M1, one group) is for
 // products with too few tiles of 256 columns for the SMs: four times the blocks stream the weights.
@@ -70,19 +64,6 @@ struct Fmt {
     static constexpr size_t SMEM_BYTES = 1024 + PIECE_OFF + EPI_WARPS * PIECE_BYTES;
     static_assert(SMEM_BYTES <= 232448, "shared memory");
     static_assert(SF_COL0 + SF_COLS * SF_SLOTS <= TMEM_COLS, "TMEM columns");
-};
-
-struct Args {
-    const int* plan;          // [2 (G + 1)]: m-tile prefix, row starts (multiples of 128); null: one group of `rows` rows
-    int G, rows, N, K, n_tiles, max_mtiles;
-    const uint8_t* a_sf;      // A scale chunks [rows128 / 128][K / 128][512]
-    const uint8_t* b_sf;      // B scale chunks [G][n_tiles][K / 128][1024]
-    void* out;
-    long long ldo;            // output row stride (elements)
-    int out_cols;
-    uint8_t* h_sf;            // EPI_SWIGLU: scale chunks of the MX hidden out (codes at out, row stride ldo bytes)
-    int tma_out;
-    int* err;
 };
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
@@ -121,78 +102,6 @@ __device__ __forceinline__ void mma_mx(uint32_t d, uint64_t adesc, uint64_t bdes
                 d),
             "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
             : "memory");
-}
-
-// Instruction descriptor: B scale byte (bits 4-5), A and B formats (bits 7-9,
-// 10-12: 0 = E4M3 of kind::mxf8f6f4, 1 = E2M1 of kind::mxf4), K-major, N >> 3
-// (17-22), UE8M0 scales (bit 23), M >> 4 (24-28), A scale byte (29-30).
-template <bool F4>
-__host__ __device__ constexpr uint32_t idesc_mx(int M, int N, int sf_id) {
-    return (static_cast<uint32_t>(sf_id) << 4) | (F4 ? (1u << 7) | (1u << 10) : 0u) |
-           (static_cast<uint32_t>(N >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24) |
-           (static_cast<uint32_t>(sf_id) << 29);
-}
-
-// SiLU(g) u of two columns as bf16, in some ten instructions a value: this epilogue's code is run
-// once a tile, and with few rows by one warp, at the rate at which instructions are fetched (with
-// silu_f's division and exponential the 64 values of a thread took 24,000 cycles then, and the gate/up
-// product of 61 tokens over 64 experts 86 us instead of 36).
-// g / (1 + 2^(-g log2 e)) with the approximate exponential and reciprocal (2 units of 2^-23 each).
-__device__ __forceinline__ float swiglu_fast(uint32_t gate, uint32_t up) {
-    const float g = __uint_as_float(gate);
-    float e, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
-    return g * r * __uint_as_float(up);
-}
-__device__ __forceinline__ uint32_t swiglu_pair(uint32_t g0, uint32_t u0, uint32_t g1, uint32_t u1) {
-    return pack_bf16x2(swiglu_fast(g0, u0), swiglu_fast(g1, u1));
-}
-
-struct Tile {
-    int g, m, n, a_row, rows_valid;
-};
-
-__device__ __forceinline__ Tile decode(int t, const int* mt_start, const int* row_start, int G, int n_tiles) {
-    const int q = t / n_tiles;
-    int lo = 0, hi = G;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (mt_start[mid] <= q) lo = mid; else hi = mid;
-    }
-    Tile r;
-    r.g = lo;
-    const int mtiles = mt_start[lo + 1] - mt_start[lo];
-    const int local = t - mt_start[lo] * n_tiles;
-    const int GM = mtiles <= 2 * kGroupM ? mtiles : kGroupM;
-    const int blk = local / (GM * n_tiles);
-    const int gm = min(GM, mtiles - blk * GM);
-    const int rr = local - blk * GM * n_tiles;
-    r.n = rr / gm;
-    r.m = blk * GM + (rr - r.n * gm);
-    r.a_row = row_start[lo] + r.m * BM;
-    const int rem = row_start[lo + 1] - r.a_row;
-    r.rows_valid = rem < BM ? rem : BM;
-    return r;
-}
-
-// One 32 x 32 bf16 piece through the warp's staging buffer and a TMA store.
-__device__ __forceinline__ void store_piece(const CUtensorMap* tmo, uint8_t* piece, const uint32_t* pk, int lane, int x,
-                                            int y) {
-    if (lane == 0) bulk_wait_read0();
-    __syncwarp();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int sw = q ^ ((lane >> 1) & 3);
-        *reinterpret_cast<uint4*>(piece + lane * 64 + sw * 16) =
-            make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-        tma_store_2d(tmo, smem_u32(piece), x, y);
-        bulk_commit();
-    }
 }
 
 template <int EPI, bool F4, int BN>
@@ -269,7 +178,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             int issued = 0;
             bool ok = true;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const Tile tl = decode(t, mt_start, row_start, G, args.n_tiles);
+                const Tile tl = decode<BM>(t, mt_start, row_start, G, args.n_tiles);
                 const uint8_t* sfa = args.a_sf + static_cast<size_t>(tl.a_row / BM) * chunks * SFA_CHUNK;
                 const uint8_t* sfb = args.b_sf + (static_cast<size_t>(tl.g) * tiles256 + tl.n / SUB) * chunks * 1024 +
                                      (BN == 256 ? 0 : (tl.n % SUB) / 2 * 512);
@@ -315,7 +224,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             int it = 0;
             uint32_t slot = 0;
             for (int t = blockIdx.x; t < total && ok; t += gridDim.x, ++it) {
-                const Tile tl = decode(t, mt_start, row_start, G, args.n_tiles);
+                const Tile tl = decode<BM>(t, mt_start, row_start, G, args.n_tiles);
                 // the epilogue has copied the previous tile out of TMEM
                 if (!mbar_wait(smem_u32(tempty), (static_cast<uint32_t>(it) & 1u) ^ 1u, abort_flag, args.err)) break;
                 tc_fence_after();
@@ -366,7 +275,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         uint8_t* piece = smem + F::PIECE_OFF + (warp - 2) * PIECE_BYTES;
         int it = 0;
         for (int t = blockIdx.x; t < total; t += gridDim.x, ++it) {
-            const Tile tl = decode(t, mt_start, row_start, G, args.n_tiles);
+            const Tile tl = decode<BM>(t, mt_start, row_start, G, args.n_tiles);
             if (!mbar_wait(smem_u32(tfull), static_cast<uint32_t>(it) & 1u, abort_flag, args.err)) break;
             tc_fence_after();
             // this warp's 32 rows and half of the columns, copied out of TMEM at once
@@ -378,92 +287,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(tempty));
-            const bool row_ok = r < tl.rows_valid;
-            const long long orow = static_cast<long long>(tl.a_row) + r;
-            const int lanew = r & 31, q32 = r & ~31;
-            const bool piece_ok = args.tma_out && q32 + 32 <= tl.rows_valid;
-            if constexpr (EPI == EPI_SWIGLU) {
-                // packed columns of this half: gate 64 | up 64 -> hidden columns
-                // 128 n + 64 half + [0, 64), two blocks of 32
-                const int hc0 = tl.n * 128 + half * 64;
-                if (row_ok && hc0 < args.out_cols) {
-                    uint8_t* H = static_cast<uint8_t*>(args.out) + orow * args.ldo;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        if constexpr (F4) {
-                            uint32_t h[16];
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                h[j] = swiglu_pair(v[32 * b + 2 * j], v[64 + 32 * b + 2 * j], v[32 * b + 2 * j + 1],
-                                                   v[64 + 32 * b + 2 * j + 1]);
-                            const Mx4Quant m = mx4_scale(absmax_bits(h));
-                            *reinterpret_cast<uint4*>(H + (hc0 + 32 * b) / 2) =
-                                make_uint4(mx4_codes8(h[0], h[1], h[2], h[3], m.mult), mx4_codes8(h[4], h[5], h[6], h[7], m.mult),
-                                           mx4_codes8(h[8], h[9], h[10], h[11], m.mult),
-                                           mx4_codes8(h[12], h[13], h[14], h[15], m.mult));
-                            args.h_sf[mx_sf_byte(orow, (hc0 + 32 * b) / 32, args.out_cols)] = m.ue8m0;
-                        } else {
-                            float h[32];
-                            float amax = 0.0f;
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float g = __uint_as_float(v[32 * b + j]), u = __uint_as_float(v[64 + 32 * b + j]);
-                                // the stored hidden: bf16 rounding of SiLU(g) u
-                                h[j] = __bfloat162float(__float2bfloat16_rn(silu_f(g) * u));
-                                amax = fmaxf(amax, fabsf(h[j]));
-                            }
-                            const MxQuant m = mx_quant(amax);
-                            uint32_t c[8];
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                float a0, a1, a2, a3;
-                                if (!m.q.wide) {
-                                    a0 = h[4 * j] * m.q.mult; a1 = h[4 * j + 1] * m.q.mult;
-                                    a2 = h[4 * j + 2] * m.q.mult; a3 = h[4 * j + 3] * m.q.mult;
-                                } else {
-                                    a0 = scaled_wide(h[4 * j], m.q.e); a1 = scaled_wide(h[4 * j + 1], m.q.e);
-                                    a2 = scaled_wide(h[4 * j + 2], m.q.e); a3 = scaled_wide(h[4 * j + 3], m.q.e);
-                                }
-                                c[j] = cvt_e4m3x2(a0, a1) | (cvt_e4m3x2(a2, a3) << 16);
-                            }
-                            uint4* dst = reinterpret_cast<uint4*>(H + hc0 + 32 * b);
-                            dst[0] = make_uint4(c[0], c[1], c[2], c[3]);
-                            dst[1] = make_uint4(c[4], c[5], c[6], c[7]);
-                            args.h_sf[mx_sf_byte(orow, (hc0 + 32 * b) / 32, args.out_cols)] = m.ue8m0;
-                        }
-                    }
-                }
-            } else if constexpr (EPI == EPI_BF16) {
-                const int c_base = tl.n * BN + half * HALF;
-                __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(args.out);
-#pragma unroll
-                for (int c0 = 0; c0 < HALF; c0 += 32) {
-                    if (c_base + c0 >= args.out_cols) break;
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int q = 0; q < 16; ++q)
-                        pk[q] = pack_bf16x2(__uint_as_float(v[c0 + 2 * q]), __uint_as_float(v[c0 + 2 * q + 1]));
-                    if (piece_ok) {
-                        store_piece(&tmO, piece, pk, lanew, c_base + c0, tl.a_row + q32);
-                    } else if (row_ok) {
-                        uint4* dst = reinterpret_cast<uint4*>(Y + orow * args.ldo + c_base + c0);
-#pragma unroll
-                        for (int w = 0; w < 4; ++w)
-                            if (c_base + c0 + 8 * w < args.out_cols) dst[w] = make_uint4(pk[4 * w], pk[4 * w + 1], pk[4 * w + 2], pk[4 * w + 3]);
-                    }
-                }
-            } else {   // EPI_F32
-                const int c_base = tl.n * BN + half * HALF;
-                float* Z = static_cast<float*>(args.out);
-                if (row_ok) {
-#pragma unroll
-                    for (int c0 = 0; c0 < HALF; c0 += 4) {
-                        if (c_base + c0 >= args.out_cols) break;
-                        *reinterpret_cast<uint4*>(Z + orow * args.ldo + c_base + c0) =
-                            make_uint4(v[c0], v[c0 + 1], v[c0 + 2], v[c0 + 3]);
-                    }
-                }
-            }
+            epilogue<EPI, F4, HALF>(v, args, &tmO, tl.n, half, tl.a_row, tl.rows_valid, r, piece);
         }
         if (args.tma_out && lane == 0) bulk_wait0();
         __syncwarp();

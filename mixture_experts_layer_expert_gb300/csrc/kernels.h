@@ -128,6 +128,13 @@ cudaError_t launch_mx_gemm(bool f4, int epi, const void* A, long long a_rows, co
                            const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
                            void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st);
 
+// gemm_mx_pair.cu: the same for E2M1 on CTA pairs, whose plan has tiles of 256 rows.  For groups of kMx4PairRows rows
+// or more on average: below that the halves of pair tiles that lie past a group's end cost more than the pair saves.
+constexpr int kMx4PairRows = 512;
+cudaError_t launch_mx4_pair_gemm(int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
+                                 const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
+                                 void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st);
+
 // mx.cu: MX packs and quantisation (layouts in mx.cuh), E4M3 or E2M1 (f4)
 size_t packed_bytes_mx(bool f4, int G, int N, int K);
 const uint8_t* packed_sf_mx(bool f4, const void* packed, int G, int N, int K);

@@ -257,12 +257,18 @@ def mx4_rows_split(buf: torch.Tensor, rows: int, cols: int):
             buf[off:off + r128 // 128 * cols // 128 * 512].view(r128 // 128, cols // 128, 512))
 
 
+def _mx4_bytes(rows, cols):
+    """fs_mx4_rows_bytes of valid sizes (other sizes the entry points refuse), without a call into the library."""
+    r128 = (rows + 127) // 128
+    return (r128 * 64 * cols + 255) // 256 * 256 + r128 * (cols // 128) * 512
+
+
 def fs_quantize_rows_mx4(rows, cols, x, q, stream=None):
     """Quantise bf16 rows x [rows, cols] into q, a 4-bit MX matrix (mx4_rows_empty)."""
     dev, st = _here(stream)
-    xp, _ = _operand("fs_quantize_rows_mx4 x", x, (rows, cols), dev, strided=False)
-    qp, _ = _operand("fs_quantize_rows_mx4 q", q, (fs_mx4_rows_bytes(rows, cols),), dev, torch.uint8, False)
-    _check(lib().fs_quantize_rows_mx4(rows, cols, xp, qp, st), "fs_quantize_rows_mx4")
+    what = "fs_quantize_rows_mx4"
+    xp, qp = _ptrs(what, dev, (("x", x, (rows, cols), torch.bfloat16), ("q", q, (_mx4_bytes(rows, cols),), torch.uint8)))
+    _check(lib().fs_quantize_rows_mx4(rows, cols, xp, qp, st), what)
 
 
 def pack_linear_mx4(w: torch.Tensor, stream=None) -> torch.Tensor:
@@ -283,12 +289,13 @@ def fs_linear_mx4(q, w, y, K, ws, stream=None):
     """y [rows, N] (bf16 or fp32, any row stride of 16-byte multiples) = the product of the 4-bit MX matrix q [rows, K]
     with the pack w of a weight [N, K]; ws: fs_linear_mx4_ws_bytes(rows, N, K) bytes."""
     dev, st = _here(stream)
-    what, (rows, N) = "fs_linear_mx4", y.shape
+    what, (rows, N), u8 = "fs_linear_mx4", y.shape, torch.uint8
     f32 = y.dtype is torch.float32
     yp, ys = _operand("fs_linear_mx4 y", y, (rows, N), dev, torch.float32 if f32 else torch.bfloat16)
-    qp, _ = _operand("fs_linear_mx4 q", q, (fs_mx4_rows_bytes(rows, K),), dev, torch.uint8, False)
-    wp, _ = _operand("fs_linear_mx4 w", w, (fs_packed_bytes(1, N, K, FS_MXFP4),), dev, torch.uint8, False)
-    sp, _ = _operand("fs_linear_mx4 ws", ws, ws.shape, dev, torch.uint8, False)
+    tiles = (N + 255) // 256
+    qp, wp, sp = _ptrs(what, dev, (("q", q, (_mx4_bytes(rows, K),), u8),
+                                   ("w", w, (tiles * ((K + 255) // 256 * 32768 + K // 128 * 1024),), u8),
+                                   ("ws", ws, ws.shape, u8)))
     _check(lib().fs_linear_mx4(rows, N, K, qp, wp, yp, FS_F32 if f32 else FS_BF16, ys[0] if rows > 1 else max(ys[0], N),
                                sp, ws.numel(), st), what)
 
@@ -577,17 +584,24 @@ def _grads_struct(g: dict) -> BlockGrads:
 
 
 def make_balance(T: int, E: int, k: int, gate: str, n_seqs: int = 1, coef: float = 1.0) -> BalanceDesc:
-    return BalanceDesc(T, E, k, GATES[gate], n_seqs, coef)
+    d = BalanceDesc(T, E, k, GATES[gate], n_seqs, coef)
+    d.shapes = _balance_shapes(d)
+    return d
+
+
+def _balance_shapes(d):
+    """Shapes of logits, indices, borders, mask or bias, counts, tokens."""
+    return (d.T, d.E), (d.T, d.k), (d.n_seqs + 1,), (d.T,), (d.E,), (d.n_seqs, d.E), (d.n_seqs,)
 
 
 def fs_balance_ws_bytes(desc: BalanceDesc) -> int:
     return int(lib().fs_balance_ws_bytes(ctypes.byref(desc)))
 
 
-def _logit_rows(what, t, desc, dev):
+def _logit_rows(what, t, shape, dev):
     """(pointer, row stride) of a [T, E] fp32 operand with any row stride."""
-    p, st = _operand(what, t, (desc.T, desc.E), dev, torch.float32)
-    return p, st[0] if desc.T > 1 else max(st[0], desc.E)
+    p, st = _operand(what, t, shape, dev, torch.float32)
+    return p, st[0] if shape[0] > 1 else max(st[0], shape[1])
 
 
 def fs_balance_loss(desc: BalanceDesc, logits, topk_idx, counts, tokens, probs, loss, ws, bias=None, cu=None, mask=None,
@@ -596,12 +610,13 @@ def fs_balance_loss(desc: BalanceDesc, logits, topk_idx, counts, tokens, probs, 
     tokens [S] int32, probs [S, E] and loss [1] fp32; cu [S + 1] int32 borders and mask [T] uint8 optional;
     ws: fs_balance_ws_bytes(desc) bytes."""
     dev, st = _here(stream)
-    what, T, E, S, f32, i32 = "fs_balance_loss", desc.T, desc.E, desc.n_seqs, torch.float32, torch.int32
-    zp, zr = _logit_rows("fs_balance_loss logits", logits, desc, dev)
+    what, f32, i32, u8 = "fs_balance_loss", torch.float32, torch.int32, torch.uint8
+    te, tk, s1, t1, e1, se, s = getattr(desc, "shapes", None) or _balance_shapes(desc)
+    zp, zr = _logit_rows("fs_balance_loss logits", logits, te, dev)
     bp, ip, cp, mp, np_, tp, pp, lp, wp = _ptrs(what, dev, (
-        ("bias", bias, (E,), f32), ("topk_idx", topk_idx, (T, desc.k), i32), ("cu", cu, (S + 1,), i32),
-        ("mask", mask, (T,), torch.uint8), ("counts", counts, (S, E), i32), ("tokens", tokens, (S,), i32),
-        ("probs", probs, (S, E), f32), ("loss", loss, (1,), f32), ("ws", ws, ws.shape, torch.uint8)))
+        ("bias", bias, e1, f32), ("topk_idx", topk_idx, tk, i32), ("cu", cu, s1, i32), ("mask", mask, t1, u8),
+        ("counts", counts, se, i32), ("tokens", tokens, s, i32), ("probs", probs, se, f32), ("loss", loss, _ONE, f32),
+        ("ws", ws, ws.shape, u8)))
     _check(lib().fs_balance_loss(desc, zp, zr, bp, ip, cp, mp, np_, tp, pp, lp, wp, ws.numel(), st), what)
 
 
@@ -609,12 +624,13 @@ def fs_balance_loss_backward(desc: BalanceDesc, logits, counts, tokens, d_loss, 
                              stream=None):
     """d_logits [T, E] fp32 from fs_balance_loss's counts and tokens and d_loss [1] (None: 1)."""
     dev, st = _here(stream)
-    what, E, S, f32, i32 = "fs_balance_loss_backward", desc.E, desc.n_seqs, torch.float32, torch.int32
-    zp, zr = _logit_rows("fs_balance_loss_backward logits", logits, desc, dev)
-    dp, dr = _logit_rows("fs_balance_loss_backward d_logits", d_logits, desc, dev)
+    what, f32, i32 = "fs_balance_loss_backward", torch.float32, torch.int32
+    te, _, s1, t1, e1, se, s = getattr(desc, "shapes", None) or _balance_shapes(desc)
+    zp, zr = _logit_rows("fs_balance_loss_backward logits", logits, te, dev)
+    dp, dr = _logit_rows("fs_balance_loss_backward d_logits", d_logits, te, dev)
     bp, cp, mp, np_, tp, gp = _ptrs(what, dev, (
-        ("bias", bias, (E,), f32), ("cu", cu, (S + 1,), i32), ("mask", mask, (desc.T,), torch.uint8),
-        ("counts", counts, (S, E), i32), ("tokens", tokens, (S,), i32), ("d_loss", d_loss, (1,), f32)))
+        ("bias", bias, e1, f32), ("cu", cu, s1, i32), ("mask", mask, t1, torch.uint8), ("counts", counts, se, i32),
+        ("tokens", tokens, s, i32), ("d_loss", d_loss, _ONE, f32)))
     _check(lib().fs_balance_loss_backward(desc, zp, zr, bp, cp, mp, np_, tp, gp, dp, dr, st), what)
 
 
@@ -800,6 +816,9 @@ def _operand(what: str, t: torch.Tensor, shape, dev: int, dtype=torch.bfloat16, 
     if t.get_device() != dev:
         raise FsError(1, what, "tensor on %s, not on the current device" % t.device)
     return t.data_ptr(), st
+
+
+_ONE = (1,)
 
 
 def _ptrs(what: str, dev: int, specs):

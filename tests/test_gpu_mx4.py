@@ -107,7 +107,8 @@ def linear(x, w, dtype, pad=0, stream=None):
 
 
 SIZES = [(1, 8, 128), (1, 7168, 2048), (3, 264, 384), (17, 2048, 1408), (64, 1000, 7168), (127, 256, 256), (128, 40, 640),
-         (129, 2112, 512), (300, 1032, 2048), (1025, 328, 128), (5, 16384, 256), (2, 512, 16384)]
+         (129, 2112, 512), (300, 1032, 2048), (1025, 328, 128), (5, 16384, 256), (2, 512, 16384), (511, 64, 256), (512, 64, 256),
+         (600, 264, 384), (641, 520, 1408), (1500, 72, 7168), (770, 3008, 640)]
 
 
 @pytest.mark.parametrize("rows,N,K", SIZES)
@@ -206,7 +207,8 @@ def dispatch(cfg, desc, idx, u, ws):
 
 
 LAYERS = [dict(), dict(T=1, k=1, E=1), dict(T=61, E=64, k=6, c=128), dict(T=300, d=384, c=640), dict(T=513, E=4, k=4, c=128),
-          dict(T=130, E=16, k=8, d=128, c=384)]
+          dict(T=130, E=16, k=8, d=128, c=384), dict(T=700, E=2, k=2, d=384, c=640), dict(T=1100, E=3, k=2, d=128, c=128),
+          dict(T=640, E=1, k=1, d=640, c=384)]
 
 
 @pytest.mark.parametrize("kw", LAYERS)
@@ -242,8 +244,9 @@ def test_dispatch_and_routed_experts(kw):
         assert float(room.norm()) < 0.1 * float(y.norm()) * math.sqrt(cfg.c)     # the allowance stays small
 
 
-def test_shared_expert():
-    cfg = layer(T=200, n_shared=2, c_shared=128, d=384)
+@pytest.mark.parametrize("T", [200, 700])
+def test_shared_expert(T):
+    cfg = layer(T=T, n_shared=2, c_shared=128, d=384)
     desc = fs.make_desc(cfg)
     ws = fs.alloc_workspace(desc, 0)
     w = synth.make_block_weights(cfg, 0)
