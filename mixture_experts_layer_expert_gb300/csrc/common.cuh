@@ -369,6 +369,11 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
+// The same where no writes are handed over, only TMEM that this warp has read (tcgen05.wait::ld and the
+// fence before): a release at cluster scope waits 2,000 cycles for earlier global stores.
+__device__ __forceinline__ void mbar_arrive_remote_tmem(uint32_t cluster_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
 // TMA tile load into this CTA's smem whose completion is signalled on an
 // mbarrier of either CTA of the pair (cluster_bar: shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap, uint32_t cluster_bar, int32_t x,

@@ -234,7 +234,7 @@ mx4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             tmem_ld_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(map_to_cta(smem_u32(tempty), 0));
+            if (lane == 0) mbar_arrive_remote_tmem(map_to_cta(smem_u32(tempty), 0));
             epilogue<EPI, true, 128>(v, args, &tmO, tl.n, half, a_row, left < 128 ? left : 128, r, piece);
         }
         if (args.tma_out && lane == 0) bulk_wait0();

@@ -439,7 +439,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (!ok) break;
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(map_to_cta(smem_u32(&tempty[acc]), 0));
+            if (lane == 0) mbar_arrive_remote_tmem(map_to_cta(smem_u32(&tempty[acc]), 0));
         }
         if (lane == 0) {
             while (used != asked) {                // a wait gave up: this warp's loads end before its buffers do
