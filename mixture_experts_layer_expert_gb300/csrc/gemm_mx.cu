@@ -304,6 +304,39 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 }  // namespace mx
 
 // ------------------------------------------------------------------- host
+cudaError_t encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
+                       CUtensorMapL2promotion promotion) {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    if (!fn) {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess) return e;
+        if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = fn(m, type, rank, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+namespace mx {
+// The output map of a launch whose epilogue stores pieces by TMA: 32 x 32 of bf16, 32 x 16 of fp32.
+cudaError_t out_map(CUtensorMap* m, int epi, void* out, long long rows, int cols, long long ldo, int* tma_out) {
+    *tma_out = 0;
+    const int es = epi == EPI_F32 ? 4 : 2;
+    if ((epi != EPI_BF16 && epi != EPI_F32) || ldo * es % 16 || (reinterpret_cast<uintptr_t>(out) & 15u)) return cudaSuccess;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ldo) * es};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / es), 32};
+    *tma_out = 1;
+    return encode_map(m, epi == EPI_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims,
+                      strides, box, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+}  // namespace mx
+
 template <int EPI, bool F4, int BN = 256>
 static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
                                   const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles, void* out,
@@ -337,7 +370,10 @@ static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t
     args.err = dev_error_ptr();
     args.tma_out = 0;
     to = ta;
-    if (EPI == EPI_BF16 && out_cols % 32 == 0 && ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
+    if (F4) {
+        e = mx::out_map(&to, EPI, out, plan ? a_rows : rows, out_cols, ldo, &args.tma_out);
+        if (e != cudaSuccess) return e;
+    } else if (EPI == EPI_BF16 && out_cols % 32 == 0 && ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
         e = make_out_map_bf16(&to, out, a_rows, out_cols, ldo);
         if (e != cudaSuccess) return e;
         args.tma_out = 1;

@@ -81,7 +81,7 @@ __device__ __forceinline__ Tile decode(int t, const int* mt_start, const int* ro
     return r;
 }
 
-// One 32 x 32 bf16 piece through the warp's staging buffer and a TMA store.
+// One piece of 32 rows x 64 bytes (32 bf16 or 16 fp32 columns) through the warp's staging buffer and a TMA store.
 __device__ __forceinline__ void store_piece(const CUtensorMap* tmo, uint8_t* piece, const uint32_t* pk, int lane, int x,
                                             int y) {
     if (lane == 0) bulk_wait_read0();
@@ -182,7 +182,13 @@ __device__ __forceinline__ void epilogue(const uint32_t (&v)[HALF], const Args& 
     } else {   // EPI_F32
         const int c_base = n * 2 * HALF + half * HALF;
         float* Z = static_cast<float*>(args.out);
-        if (row_ok) {
+        if (piece_ok) {
+#pragma unroll
+            for (int c0 = 0; c0 < HALF; c0 += 16) {
+                if (c_base + c0 >= args.out_cols) break;
+                store_piece(tmO, piece, &v[c0], lanew, c_base + c0, a_row + q32);
+            }
+        } else if (row_ok) {
 #pragma unroll
             for (int c0 = 0; c0 < HALF; c0 += 4) {
                 if (c_base + c0 >= args.out_cols) break;
@@ -192,6 +198,9 @@ __device__ __forceinline__ void epilogue(const uint32_t (&v)[HALF], const Args& 
         }
     }
 }
+
+// gemm_mx.cu
+cudaError_t out_map(CUtensorMap* m, int epi, void* out, long long rows, int cols, long long ldo, int* tma_out);
 
 }  // namespace mx
 }  // namespace fs

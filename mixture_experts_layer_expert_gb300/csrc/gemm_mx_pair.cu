@@ -11,8 +11,6 @@
 //   tfull    (each)      the tile is complete;             tempty (even)    16 warps have copied it out
 // The scales come by tensor maps of 512-byte and 1 KB rows: those carry an mbarrier of the other CTA
 // and fill with zeros past the end (an odd number of chunks, a pair's second half past the last row).
-#include <cudaTypedefs.h>
-
 #include "gemm_mx.cuh"
 
 namespace fs {
@@ -252,23 +250,11 @@ mx4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
 // Tensor map of `rows` rows of `words` 32-bit words, boxes of two rows.
 cudaError_t scale_map(CUtensorMap* map, const void* base, long long rows, int words) {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
-        if (e != cudaSuccess) return e;
-        if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
-        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    cuuint64_t gdim[2] = {static_cast<cuuint64_t>(words), static_cast<cuuint64_t>(rows)};
-    cuuint64_t gstride[1] = {static_cast<cuuint64_t>(words) * 4};
-    cuuint32_t box[2] = {static_cast<cuuint32_t>(words), 2};
-    cuuint32_t estr[2] = {1, 1};
-    const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), gdim, gstride, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(words), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(words) * 4};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(words), 2};
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box,
+                      CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 template <int EPI>
@@ -300,11 +286,8 @@ cudaError_t launch(const void* A, long long a_rows, const uint8_t* a_sf, const v
     args.h_sf = h_sf;
     args.err = dev_error_ptr();
     to = ta;
-    if (EPI == EPI_BF16 && out_cols % 32 == 0 && ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
-        e = make_out_map_bf16(&to, out, a_rows, out_cols, ldo);
-        if (e != cudaSuccess) return e;
-        args.tma_out = 1;
-    }
+    e = out_map(&to, EPI, out, plan ? a_rows : rows, out_cols, ldo, &args.tma_out);
+    if (e != cudaSuccess) return e;
     if (EPI == EPI_SWIGLU && (!h_sf || ldo < out_cols / 2)) return cudaErrorInvalidValue;
     int sms = 0;
     e = num_sms(&sms);

@@ -111,6 +111,10 @@ cudaError_t make_map_rows(CUtensorMap* m, const void* base, long long rows, int 
                           long long head, int box_rows);
 cudaError_t make_out_map_bf16(CUtensorMap* m, void* base, long long rows, long long cols, long long ldo);
 cudaError_t num_sms(int* out);
+// gemm_mx.cu: the driver's cuTensorMapEncodeTiled for maps of other kinds.
+cudaError_t encode_map(CUtensorMap* m, CUtensorMapDataType type, int rank, void* base, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle swizzle,
+                       CUtensorMapL2promotion promotion);
 // Raise fn's dynamic shared memory limit to `bytes` on the current device, once
 // per device (the attribute belongs to each device's copy of the kernel; set[d]
 // records device d).  num_sms is cached per device too.

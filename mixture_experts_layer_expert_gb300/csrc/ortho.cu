@@ -26,7 +26,6 @@
 // a half tile takes 0.7 of a whole one's time, its MMAs being bound by the operand reads).
 // B X reads X as the MN-major operand, where it lies.  The epilogue's own inputs (the piece
 // of A, of H and L) come and go by TMA through two 4 KB buffers per warp.
-#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -524,16 +523,9 @@ __global__ void __launch_bounds__(256) norm_kernel(const Source s, float* part) 
     }
 }
 
-// X = G / (|G| + eps) as H + L 2^-11 times 2^xs, transposed for a tall G; a 64 x 64 tile per block.
-// Columns past q up to the padded width are zero.
-__global__ void __launch_bounds__(256)
-scale_kernel(const Source s, const float* part, int nb, double eps, float xscale, int tall, int tiles_n, __half* H,
-             __half* L, int r, int qp) {
-    __shared__ float tile[64][65];
-    __shared__ float f1, f2;
-    const int z = blockIdx.y;
-    cudaGridDependencySynchronize();
-    const int ti = blockIdx.x / tiles_n, tj = blockIdx.x - ti * tiles_n;      // tile of G
+// The two factors that scale matrix z, from its blocks' sums; all threads of a block call it.
+__device__ __forceinline__ void block_factors(const float* part, int nb, int z, double eps, float xscale, float* f1, float* f2) {
+    __shared__ float f[2];
     if (threadIdx.x < 32) {
         double big = 0, mid = 0, small = 0;
         for (int i = threadIdx.x; i < nb; i += 32) {
@@ -548,10 +540,77 @@ scale_kernel(const Source s, const float* part, int nb, double eps, float xscale
             mid += __shfl_xor_sync(0xffffffffu, mid, o);
             small += __shfl_xor_sync(0xffffffffu, small, o);
         }
-        if (threadIdx.x == 0) {
-            norm_factors(big, mid, small, eps, xscale, &f1, &f2);
+        if (threadIdx.x == 0) norm_factors(big, mid, small, eps, xscale, &f[0], &f[1]);
+    }
+    __syncthreads();
+    *f1 = f[0];
+    *f2 = f[1];
+}
+
+// Eight values as H and L (16 bytes each).
+__device__ __forceinline__ void split8(const float (&x)[8], uint4* h, uint4* l) {
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        hw[w] = pack_half2(x[2 * w], x[2 * w + 1]);
+        const float2 b = unpack_half2(hw[w]);
+        lw[w] = pack_half2((x[2 * w] - b.x) * 0x1p11f, (x[2 * w + 1] - b.y) * 0x1p11f);
+    }
+    *h = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    *l = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+}
+
+// X = G / (|G| + eps) as H + L 2^-11 times its power of two, rows where they are: a warp a row, eight
+// columns a lane, four such in flight.  Columns past q up to the padded width are zero.
+__global__ void __launch_bounds__(256)
+scale_rows_kernel(const Source s, const float* part, int nb, double eps, float xscale, __half* H, __half* L, int qp) {
+    const int lane = threadIdx.x & 31, z = blockIdx.y, i = blockIdx.x * 8 + (threadIdx.x >> 5);
+    cudaGridDependencySynchronize();
+    float f1, f2;
+    block_factors(part, nb, z, eps, xscale, &f1, &f2);
+    if (i >= s.m) return;
+    const size_t es = s.f32 ? 4 : 2;
+    const uint8_t* row = static_cast<const uint8_t*>(s.g) + (static_cast<long long>(z) * s.mat + static_cast<long long>(i) * s.row) * es;
+    const long long at_ = (static_cast<long long>(z) * s.m + i) * qp;
+    for (int c0 = 8 * lane; c0 < qp; c0 += 4 * 256) {
+        float x[4][8];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int c = c0 + 256 * u;
+            if (s.vec && c + 8 <= s.n) {
+                if (s.f32) {
+                    const float4 a = __ldg(reinterpret_cast<const float4*>(row) + c / 4), b = __ldg(reinterpret_cast<const float4*>(row) + c / 4 + 1);
+                    x[u][0] = a.x; x[u][1] = a.y; x[u][2] = a.z; x[u][3] = a.w;
+                    x[u][4] = b.x; x[u][5] = b.y; x[u][6] = b.z; x[u][7] = b.w;
+                } else {
+                    const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + c / 8);
+                    x[u][0] = bf16lo(a.x); x[u][1] = bf16hi(a.x); x[u][2] = bf16lo(a.y); x[u][3] = bf16hi(a.y);
+                    x[u][4] = bf16lo(a.z); x[u][5] = bf16hi(a.z); x[u][6] = bf16lo(a.w); x[u][7] = bf16hi(a.w);
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[u][k] = c + k < s.n ? at(s, row, c + k) : 0.0f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int c = c0 + 256 * u;
+            if (c >= qp) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[u][k] = x[u][k] * f1 * f2;
+            split8(x[u], reinterpret_cast<uint4*>(H + at_ + c), reinterpret_cast<uint4*>(L + at_ + c));
         }
     }
+}
+
+// The same for a tall G, transposed: a 64 x 64 tile per block.
+__global__ void __launch_bounds__(256)
+scale_tall_kernel(const Source s, const float* part, int nb, double eps, float xscale, int tiles_n, __half* H, __half* L, int r,
+                  int qp) {
+    __shared__ float tile[64][65];
+    const int z = blockIdx.y;
+    const int ti = blockIdx.x / tiles_n, tj = blockIdx.x - ti * tiles_n;      // tile of G
+    cudaGridDependencySynchronize();
     const size_t es = s.f32 ? 4 : 2;
     const uint8_t* g = static_cast<const uint8_t*>(s.g) + static_cast<long long>(z) * s.mat * es;
     const int lr = threadIdx.x >> 2, seg = (threadIdx.x & 3) * 16;
@@ -572,26 +631,18 @@ scale_kernel(const Source s, const float* part, int nb, double eps, float xscale
     } else {
         for (int v = 0; v < 16; ++v) tile[lr][seg + v] = i < s.m && j0 + v < s.n ? at(s, row, j0 + v) : 0.0f;
     }
-    __syncthreads();
-    const int xr = (tall ? tj : ti) * 64 + lr, xc = (tall ? ti : tj) * 64 + seg;
+    float f1, f2;
+    block_factors(part, nb, z, eps, xscale, &f1, &f2);      // (its barrier is the tile's too)
+    const int xr = tj * 64 + lr, xc = ti * 64 + seg;
     if (xr >= r) return;
-    uint32_t h[8], l[8];
-#pragma unroll
-    for (int v = 0; v < 8; ++v) {
-        float x[2];
-#pragma unroll
-        for (int w = 0; w < 2; ++w) x[w] = (tall ? tile[seg + 2 * v + w][lr] : tile[lr][seg + 2 * v + w]) * f1 * f2;
-        h[v] = pack_half2(x[0], x[1]);
-        const float2 b = unpack_half2(h[v]);
-        l[v] = pack_half2((x[0] - b.x) * 0x1p11f, (x[1] - b.y) * 0x1p11f);
-    }
     const long long at_ = (static_cast<long long>(z) * r + xr) * qp + xc;
-    uint4* ho = reinterpret_cast<uint4*>(H + at_);
-    uint4* lo = reinterpret_cast<uint4*>(L + at_);
-    ho[0] = make_uint4(h[0], h[1], h[2], h[3]);
-    ho[1] = make_uint4(h[4], h[5], h[6], h[7]);
-    lo[0] = make_uint4(l[0], l[1], l[2], l[3]);
-    lo[1] = make_uint4(l[4], l[5], l[6], l[7]);
+#pragma unroll
+    for (int v = 0; v < 16; v += 8) {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = tile[seg + v + k][lr] * f1 * f2;
+        split8(x, reinterpret_cast<uint4*>(H + at_ + v), reinterpret_cast<uint4*>(L + at_ + v));
+    }
 }
 
 // ------------------------------------------------------------------- host
@@ -641,22 +692,10 @@ Layout layout(int batch, int m, int n) {
 
 cudaError_t encode(CUtensorMap* map, CUtensorMapDataType type, void* base, long long cols, long long rows, long long mats,
                    long long row_bytes, long long mat_bytes, int box_cols, int box_rows, CUtensorMapSwizzle swizzle) {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    if (!fn) {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q);
-        if (e != cudaSuccess) return e;
-        if (q != cudaDriverEntryPointSuccess || !p) return cudaErrorNotSupported;
-        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }
-    cuuint64_t gdim[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
-    cuuint64_t gstride[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(mat_bytes)};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
-    cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = fn(map, type, 3, base, gdim, gstride, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(mat_bytes)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+    return encode_map(map, type, 3, base, dims, strides, box, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 // fp16 [mats, rows, cols] contiguous: boxes of 64 columns for the products, pieces of 32 x 32 for the epilogue.
 cudaError_t operand(CUtensorMap* map, void* base, int cols, int rows, int mats, int box_rows) {
@@ -722,10 +761,14 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
         if ((e = launch_after(norm_kernel, dim3(blocks, nb), dim3(256), 0, st, src, part)) != cudaSuccess) return e;
         __half* H[2] = {reinterpret_cast<__half*>(w + l.h[0]), reinterpret_cast<__half*>(w + l.h[1])};
         __half* L = reinterpret_cast<__half*>(w + l.l);
-        // tiles of G; for X's padded width the last ones reach past it
-        const int tm = (s.tall ? s.qp : s.rp) / 64, tn = (s.tall ? s.rp : s.qp) / 64;
-        e = launch_after(scale_kernel, dim3(tm * tn, nb), dim3(256), 0, st, src, part, blocks, o.eps, o.scales.x, s.tall, tn,
-                         H[0], L, s.r, s.qp);
+        if (s.tall) {                          // tiles of G; for X's padded width the last ones reach past it
+            const int tm = s.qp / 64, tn = s.rp / 64;
+            e = launch_after(scale_tall_kernel, dim3(tm * tn, nb), dim3(256), 0, st, src, part, blocks, o.eps, o.scales.x, tn,
+                             H[0], L, s.r, s.qp);
+        } else {
+            e = launch_after(scale_rows_kernel, dim3((s.r + 7) / 8, nb), dim3(256), 0, st, src, part, blocks, o.eps, o.scales.x,
+                             H[0], L, s.qp);
+        }
         count_launch();
         if (e != cudaSuccess) return e;
 
