@@ -11,7 +11,7 @@
 //
 // Both directions read every logit once and are bound by HBM; the work per logit is
 // one exponential (two and a reciprocal for the sigmoids).  A warp owns a token: its
-// row sits in registers (E <= 512: 16 a lane), 64 KB of rows in flight on an SM, max and sums by
+// row sits in registers (E <= 512: 16 a lane), the next two or four rows on their way, max and sums by
 // shuffles.  Up to 1,024 rows of one sequence are one block's work, in one launch.  Otherwise,
 // forward: the token axis is cut into equal ranges, one per block, whatever
 // the sequences' lengths; what a block finds of a sequence goes to slot (block + sequence)
@@ -26,9 +26,9 @@ namespace bal {
 // Warps of a block and tokens a warp has in flight, by elements a lane: one block fills an SM.
 template <int EPL>
 struct Cfg {
-    static constexpr int WARPS = EPL == 16 ? 16 : 32;
+    static constexpr int WARPS = EPL == 16 ? 12 : 24;
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int U = EPL == 4 ? 4 : 2;
+    static constexpr int U = EPL == 4 ? 4 : 2;              // (more spill, and are slower)
 };
 constexpr int FIN_E = 32;                 // experts per block of the second kernel
 constexpr int FIN_P = 32;                 // slots it reads at a time
@@ -181,31 +181,35 @@ piece_kernel(const Args a) {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) acc[j] = 0.0f;
         int n = 0;
+        float v[U][EPL];
+        bool on[U];
+        int pick[U];
+        auto fetch = [&](int u, int t) {           // a token's row on its way while others are worked on
+            on[u] = t < hi && !(a.mask && a.mask[t] == 0);
+            if (!on[u]) return;
+            pick[u] = lane < a.k ? a.idx[static_cast<long long>(t) * a.k + lane] : -1;
+            load_row<EPL, VEC>(a.z + t * a.z_row, a.E, lane, -INFINITY, v[u]);
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) fetch(u, lo + warp + u * WARPS);
         for (int t0 = lo + warp; t0 < hi; t0 += U * WARPS) {
-            float v[U][EPL], rest[EPL];
-            bool on[U];
-            int pick[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int t = t0 + u * WARPS;
-                on[u] = t < hi && !(a.mask && a.mask[t] == 0);
-                pick[u] = on[u] && lane < a.k ? a.idx[static_cast<long long>(t) * a.k + lane] : -1;
-                if (on[u]) load_row<EPL, VEC>(a.z + t * a.z_row, a.E, lane, -INFINITY, v[u]);
-            }
+                const bool now = on[u];
+                const int e = pick[u];
+                float w[EPL], rest[EPL], inv;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!on[u]) continue;
+                for (int j = 0; j < EPL; ++j) w[j] = v[u][j] + bias[j];
+                fetch(u, t0 + (u + U) * WARPS);
+                if (!now) continue;
                 ++n;
                 if (lane < a.k) {
-                    if (pick[u] >= 0 && pick[u] < a.E) atomicAdd(&cnt[pick[u]], 1);
+                    if (e >= 0 && e < a.E) atomicAdd(&cnt[e], 1);
                     else set_dev_error(a.err, DEV_ERR_EXPERT_INDEX);
                 }
+                scores<EPL, SIG>(w, rest, &inv);
 #pragma unroll
-                for (int j = 0; j < EPL; ++j) v[u][j] += bias[j];
-                float inv;
-                scores<EPL, SIG>(v[u], rest, &inv);
-#pragma unroll
-                for (int j = 0; j < EPL; ++j) acc[j] += v[u][j] * inv;
+                for (int j = 0; j < EPL; ++j) acc[j] += w[j] * inv;
             }
         }
 #pragma unroll
@@ -374,49 +378,50 @@ backward_kernel(const BwdArgs a) {
             const int e = elem<VEC>(j, lane);
             f[j] = e < a.E ? unit * static_cast<float>(a.counts[static_cast<long long>(q) * a.E + e]) : 0.0f;
         }
+        float v[U][EPL];
+        bool on[U];
+        auto fetch = [&](int u, int t) {
+            on[u] = t < hi && !(a.mask && a.mask[t] == 0);
+            if (on[u]) load_row<EPL, VEC>(a.z + t * a.z_row, a.E, lane, -INFINITY, v[u]);
+        };
+#pragma unroll
+        for (int u = 0; u < U; ++u) fetch(u, lo + warp + u * WARPS);
         for (int t0 = lo + warp; t0 < hi; t0 += U * WARPS) {
-            float v[U][EPL], rest[EPL];
-            bool in[U], on[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int t = t0 + u * WARPS;
-                in[u] = t < hi;
-                on[u] = in[u] && !(a.mask && a.mask[t] == 0);
-                if (on[u]) load_row<EPL, VEC>(a.z + t * a.z_row, a.E, lane, -INFINITY, v[u]);
-            }
+                const bool now = on[u];
+                float w[EPL], rest[EPL];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (!in[u]) continue;
-                if (on[u]) {
+                for (int j = 0; j < EPL; ++j) w[j] = v[u][j] + bias[j];
+                fetch(u, t + U * WARPS);
+                if (t >= hi) break;
+                if (now) {
+                    float inv, dot = 0.0f;
+                    scores<EPL, SIG>(w, rest, &inv);
 #pragma unroll
-                    for (int j = 0; j < EPL; ++j) v[u][j] += bias[j];
-                    float inv;
-                    scores<EPL, SIG>(v[u], rest, &inv);
-                    float dot = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < EPL; ++j) dot += f[j] * v[u][j];
+                    for (int j = 0; j < EPL; ++j) dot += f[j] * w[j];
                     dot = warp_sum(dot) * inv;
                     const float by = scale * inv;
 #pragma unroll
                     for (int j = 0; j < EPL; ++j) {
-                        v[u][j] *= by * (f[j] - dot);
-                        if constexpr (SIG) v[u][j] *= rest[j];
+                        w[j] *= by * (f[j] - dot);
+                        if constexpr (SIG) w[j] *= rest[j];
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < EPL; ++j) v[u][j] = 0.0f;
+                    for (int j = 0; j < EPL; ++j) w[j] = 0.0f;
                 }
-                store_row<EPL, VEC>(a.dz + (t0 + u * WARPS) * a.dz_row, a.E, lane, v[u]);
+                store_row<EPL, VEC>(a.dz + t * a.dz_row, a.E, lane, w);
             }
         }
     }
 }
 
-// Rows a block takes, a multiple of what its warps hold at once (warps: a row each, in steps of 16): one block
-// on each SM, fewer where that would leave warps without a row.
+// Rows a block takes: one block on each SM.
 int chunk_rows(int T) {
     const long long c = (static_cast<long long>(T) + 151) / 152;
-    return static_cast<int>((c + 31) / 32 * 32);
+    return static_cast<int>((c + 7) / 8 * 8);
 }
 int blocks(int T) { return (T + chunk_rows(T) - 1) / chunk_rows(T); }
 int expert_blocks(int E) { return (E + FIN_E - 1) / FIN_E; }

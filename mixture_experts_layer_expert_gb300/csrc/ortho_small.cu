@@ -35,7 +35,7 @@ constexpr int P_OFF = B_OFF + 2 * BLOCK;
 constexpr int P_ROW = R + 4;                   // floats: 16-byte accesses of 8 rows fall into different banks
 constexpr int SHARE = R * R * 4;               // bytes of a block's share of X X^T in the workspace
 constexpr int D_OFF = P_OFF + R * P_ROW * 4;   // fp32: B's diagonal
-constexpr int N_OFF = D_OFF + R * 4;           // sums of squares of the cluster's blocks, 16 x 4 floats
+constexpr int N_OFF = D_OFF + R * 4;           // sums of squares of the cluster's blocks, 16 x 4 floats at most
 constexpr int S_OFF = N_OFF + 16 * 16;         // of this block's warps, 8 x 4 floats, then the two factors
 constexpr int BAR_OFF = S_OFF + 8 * 16 + 16;
 constexpr size_t SMEM_BYTES = 1024 + BAR_OFF + 32;
@@ -389,7 +389,7 @@ static int small_cluster(int r, int q) {
     if (r > ortho::small::R) return 0;
     int c = 1;
     while (c * ortho::small::W < q) c *= 2;
-    return c <= 8 ? c : 0;
+    return c <= 16 ? c : 0;                  // (16 blocks: more than the portable 8, asked for below)
 }
 
 bool ortho_small_fits(int m, int n) { return small_cluster(m < n ? m : n, m < n ? n : m) > 0; }
@@ -409,6 +409,14 @@ cudaError_t launch_ortho_small(const OrthoArgs& o, void* ws, cudaStream_t st) {
     static bool set[kMaxDevices];
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(small_kernel), SMEM_BYTES, set);
     if (e != cudaSuccess) return e;
+    static bool wide[kMaxDevices];
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDevices && !wide[dev]) {
+        e = cudaFuncSetAttribute(small_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        wide[dev] = true;
+    }
     Args a{};
     a.src = source(o, o.g);
     a.out = o.out;
