@@ -282,8 +282,7 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * HALF);
             uint32_t v[HALF];
 #pragma unroll
-            for (int c = 0; c < HALF; c += 32) tmem_ld32(tb + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
-            tmem_ld_wait();
+            for (int c = 0; c < HALF; c += 32) tmem_ld32_sync(tb + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(tempty));

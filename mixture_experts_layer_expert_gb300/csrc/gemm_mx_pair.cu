@@ -228,8 +228,7 @@ mx4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * 128);
             uint32_t v[128];
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) tmem_ld32(tb + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
-            tmem_ld_wait();
+            for (int c = 0; c < 128; c += 32) tmem_ld32_sync(tb + c, *reinterpret_cast<uint32_t(*)[32]>(&v[c]));
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_remote_tmem(map_to_cta(smem_u32(tempty), 0));

@@ -305,8 +305,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 #pragma unroll 1
             for (int c = first; c < last; ++c) {
                 uint32_t v[32];
-                tmem_ld32(tbase + 32 * c, v);
-                tmem_ld_wait();
+                tmem_ld32_sync(tbase + 32 * c, v);
                 const uint32_t b = LOADS ? used & 1u : stored++ & 1u;
                 uint8_t* buf = buf0 + b * BUF;
                 const int x = col0 + 32 * c;

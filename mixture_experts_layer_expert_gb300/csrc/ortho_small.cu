@@ -2,7 +2,7 @@
 // most 128: all steps of a matrix in one launch.
 //
 // The mathematics is ortho.cu's.  A cluster of C thread blocks holds one matrix: block c a
-// slice of up to 256 columns of X, in fp32 registers (a row and 128 columns a thread) and as the
+// slice of up to 256 columns of X, in fp32 registers (a row and 64 columns a thread) and as the
 // fp16 operand H in shared memory.  Per step
 //   the block's share of X X^T (tensor cores) -> summed over the cluster in rank order, each block
 //   a band of rows -> A (fp16) in every block
@@ -26,18 +26,20 @@ namespace small {
 
 constexpr int R = 128;                         // rows held (r <= R; the rest are zero)
 constexpr int W = 256;                         // columns a block can hold
-constexpr int THREADS = 256;
+constexpr int THREADS = 512;                   // (256 threads with 128 columns each took 7,500 cycles a step, not N)
+constexpr int WARPS = THREADS / 32;
+constexpr int XC = W / (WARPS / 4);            // columns of X a thread holds
 constexpr int BLOCK = R * 64 * 2;              // 64 columns of fp16: the 128-byte-swizzle tile, 16 KB
 constexpr int H_OFF = 0;
 constexpr int A_OFF = H_OFF + (W / 64) * BLOCK;
 constexpr int B_OFF = A_OFF + 2 * BLOCK;
 constexpr int P_OFF = B_OFF + 2 * BLOCK;
 constexpr int P_ROW = R + 4;                   // floats: 16-byte accesses of 8 rows fall into different banks
-constexpr int SHARE = R * R * 4;               // bytes of a block's share of X X^T in the workspace
+constexpr int SHARE = 2 * R * R * 4;           // bytes of a block's shares of X X^T in the workspace, two steps' in turn
 constexpr int D_OFF = P_OFF + R * P_ROW * 4;   // fp32: B's diagonal
 constexpr int N_OFF = D_OFF + R * 4;           // sums of squares of the cluster's blocks, 16 x 4 floats at most
-constexpr int S_OFF = N_OFF + 16 * 16;         // of this block's warps, 8 x 4 floats, then the two factors
-constexpr int BAR_OFF = S_OFF + 8 * 16 + 16;
+constexpr int S_OFF = N_OFF + 16 * 16;         // of this block's warps, 4 floats each, then the two factors
+constexpr int BAR_OFF = S_OFF + WARPS * 16 + 16;
 constexpr size_t SMEM_BYTES = 1024 + BAR_OFF + 32;
 constexpr int D_A = 0, D_AA = 128, D_X = 256;  // TMEM columns
 static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -78,16 +80,16 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
     float* dvec = reinterpret_cast<float*>(smem + D_OFF);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, half = warp >> 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, group = warp >> 2;
     const int row = quarter * 32 + lane;
     const int C = cluster_size(), rank = static_cast<int>(cluster_ctarank());
     const int cluster = blockIdx.x / C, clusters = gridDim.x / C;
-    const int rr = a.rr, cols_a = rr / 2;                           // columns of A and B that this thread's half takes
+    const int rr = a.rr, cols_a = rr / 4;                           // columns of A and B that a thread takes: 16 or 32
     float* share = reinterpret_cast<float*>(a.ws + static_cast<size_t>(blockIdx.x) * SHARE);
     const float* shares = reinterpret_cast<const float*>(a.ws + static_cast<size_t>(cluster) * C * SHARE);
     uint8_t* a_out = a.ws + static_cast<size_t>(gridDim.x) * SHARE + static_cast<size_t>(cluster) * (R * R * 2);
-    const int col_first = rank * a.width + half * 128;              // this thread's first column of X
-    const int ncol = min(128, a.width - half * 128);                // and how many it holds (a multiple of 64, may be <= 0)
+    const int col_first = rank * a.width + group * XC;              // this thread's first column of X
+    const int ncol = min(XC, a.width - group * XC);                 // and how many it holds (64, or none: <= 0)
 
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(bar), 1);
@@ -117,78 +119,102 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
 
 #pragma unroll 1
     for (int z = cluster; z < a.batch; z += clusters) {
-    // ---- the block's slice of G, and the norm
-    float x[128];
-    Squares sq;
-    {
+    // ---- the block's slice of G through the share's buffer, 128 columns at a time, and the norm.  (Loops of a few
+    // instructions that read along G's rows: as straight code, each thread its own columns, this took 7,000 cycles,
+    // most of them fetching instructions.)
+    float x[XC];
+#pragma unroll
+    for (int c = 0; c < XC; ++c) x[c] = 0.0f;
+    float* P = reinterpret_cast<float*>(smem + P_OFF);
+    const float* mine = P + row * P_ROW + (group & 1) * XC;         // this thread's columns in the buffer
+#pragma unroll 1
+    for (int p = 0; p < a.width; p += 128) {
+        const int c0 = rank * a.width + p, cols = min(128, a.width - p);
         const size_t es = a.src.f32 ? 4 : 2;
         const uint8_t* g = static_cast<const uint8_t*>(a.src.g) + static_cast<long long>(z) * a.src.mat * es;
-        const long long step = a.tall ? a.src.row : 1;              // from a column of X to the next
-        const uint8_t* p = g + ((a.tall ? row : static_cast<long long>(row) * a.src.row) + col_first * step) * es;
-        const int valid = row < a.r ? min(ncol, a.q - col_first) : 0;
-        if (a.src.vec && !a.tall) {
-#pragma unroll
-            for (int c = 0; c < 128; c += 8) {
-                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                if (c < valid) {                                     // q is a multiple of the vector (8 bf16, 4 fp32)
+        if (a.tall) {                        // a column of X is a row of G
+#pragma unroll 2
+            for (int c = warp; c < cols; c += WARPS) {
+                const uint8_t* line = g + static_cast<long long>(c0 + c) * a.src.row * es;
+                for (int r = lane; r < rr; r += 32)
+                    P[r * P_ROW + c] = c0 + c < a.q && r < a.r ? at(a.src, line, r) : 0.0f;
+            }
+        } else if (a.src.vec) {              // q is a multiple of a vector, so of 4
+            const bool in = c0 + 4 * lane < a.q;
+#pragma unroll 4
+            for (int r = warp; r < rr; r += WARPS) {
+                const uint8_t* line = g + (static_cast<long long>(r) * a.src.row + c0) * es;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (in && r < a.r) {
                     if (a.src.f32) {
-                        const float4 u = __ldg(reinterpret_cast<const float4*>(p) + c / 4);
-                        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
-                        if (c + 4 < valid) {
-                            const float4 w = __ldg(reinterpret_cast<const float4*>(p) + c / 4 + 1);
-                            v[4] = w.x; v[5] = w.y; v[6] = w.z; v[7] = w.w;
-                        }
+                        v = __ldg(reinterpret_cast<const float4*>(line) + lane);
                     } else {
-                        const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + c / 8);
-                        v[0] = bf16lo(u.x); v[1] = bf16hi(u.x); v[2] = bf16lo(u.y); v[3] = bf16hi(u.y);
-                        v[4] = bf16lo(u.z); v[5] = bf16hi(u.z); v[6] = bf16lo(u.w); v[7] = bf16hi(u.w);
+                        const uint2 u = __ldg(reinterpret_cast<const uint2*>(line) + lane);
+                        v = make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
                     }
                 }
-#pragma unroll
-                for (int k = 0; k < 8; ++k) x[c + k] = v[k];
+                *reinterpret_cast<float4*>(P + r * P_ROW + 4 * lane) = v;
             }
         } else {
+#pragma unroll 2
+            for (int r = warp; r < rr; r += WARPS) {
+                const uint8_t* line = g + (static_cast<long long>(r) * a.src.row + c0) * es;
 #pragma unroll
-            for (int c = 0; c < 128; ++c) x[c] = c < valid ? at(a.src, p, c * step) : 0.0f;
+                for (int c = lane; c < 128; c += 32) P[r * P_ROW + c] = c0 + c < a.q && r < a.r ? at(a.src, line, c) : 0.0f;
+            }
         }
-        sq.add(x);
+        __syncthreads();
+        if (p == (group >> 1) * 128 && ncol > 0 && row < rr) {
+#pragma unroll
+            for (int c = 0; c < XC; c += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(mine + c);
+                x[c] = v.x; x[c + 1] = v.y; x[c + 2] = v.z; x[c + 3] = v.w;
+            }
+        }
+        __syncthreads();
     }
+    Squares sq;
+    sq.add(x);
+    float* factors = reinterpret_cast<float*>(smem + S_OFF + WARPS * 16);
     {
         float v[3] = {sq.big, sq.mid, sq.small};
-        float* mine = reinterpret_cast<float*>(smem + S_OFF) + warp * 4;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-            if (lane == 0) mine[k] = v[k];
         }
-    }
-    __syncthreads();
-    if (threadIdx.x < C) {                   // this block's sums to block threadIdx.x
-        float s[3] = {0.f, 0.f, 0.f};
-        for (int w = 0; w < 8; ++w)
-            for (int k = 0; k < 3; ++k) s[k] += reinterpret_cast<float*>(smem + S_OFF)[w * 4 + k];
-        st_cluster(map_to_cta(base + N_OFF + rank * 16, threadIdx.x),
-                   make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), 0u));
-    }
-    __syncwarp();
-    cluster_sync();
-    float* factors = reinterpret_cast<float*>(smem + S_OFF + 8 * 16);
-    if (threadIdx.x == 0) {
-        double big = 0, mid = 0, sml = 0;
-        for (int c = 0; c < C; ++c) {
-            const float* p = reinterpret_cast<const float*>(smem + N_OFF) + c * 4;
-            big += p[0];
-            mid += p[1];
-            sml += p[2];
+        if (lane == 0) *reinterpret_cast<float4*>(smem + S_OFF + warp * 16) = make_float4(v[0], v[1], v[2], 0.f);
+        __syncthreads();
+        if (warp == 0) {                     // the block's sums to every block of the cluster, a lane each
+            const float4 u = *reinterpret_cast<const float4*>(smem + S_OFF + (lane & 15) * 16);
+            v[0] = u.x; v[1] = u.y; v[2] = u.z;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            }
+            if (lane < C)
+                st_cluster(map_to_cta(base + N_OFF + rank * 16, lane),
+                           make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), 0u));
+            __syncwarp();
         }
-        norm_factors(big, mid, sml, a.eps, a.sc.x, &factors[0], &factors[1]);
+        cluster_sync();
+        if (warp == 0) {
+            const float4 u = lane < C ? *reinterpret_cast<const float4*>(smem + N_OFF + lane * 16) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[0] = u.x; v[1] = u.y; v[2] = u.z;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+            }
+            if (lane == 0) norm_factors(v[0], v[1], v[2], a.eps, a.sc.x, &factors[0], &factors[1]);
+        }
+        __syncthreads();
     }
-    __syncthreads();
     {
         const float f1 = factors[0], f2 = factors[1];
 #pragma unroll
-        for (int c = 0; c < 128; ++c) x[c] = x[c] * f1 * f2;
+        for (int c = 0; c < XC; ++c) x[c] = x[c] * f1 * f2;
     }
 
 #pragma unroll 1
@@ -196,9 +222,9 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         const float ca = a.coefs[3 * k], cb = a.coefs[3 * k + 1], cc = a.coefs[3 * k + 2];
         // ---- H
 #pragma unroll
-        for (int c = 0; c < 128; c += 8) {
+        for (int c = 0; c < XC; c += 8) {
             if (c < ncol)
-                *reinterpret_cast<uint4*>(smem + H_OFF + chunk(row, half * 128 + c)) =
+                *reinterpret_cast<uint4*>(smem + H_OFF + chunk(row, group * XC + c)) =
                     make_uint4(pack_half2(x[c], x[c + 1]), pack_half2(x[c + 2], x[c + 3]), pack_half2(x[c + 4], x[c + 5]),
                                pack_half2(x[c + 6], x[c + 7]));
         }
@@ -222,13 +248,12 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         if (C == 1) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (32 * h >= cols_a || row >= rr) break;
-                uint32_t v[32];
-                const int c0 = half * cols_a + h * 32;
-                tmem_ld32(taddr + D_A + c0, v);
-                tmem_ld_wait();
+                if (16 * h >= cols_a || row >= rr) break;
+                uint32_t v[16];
+                const int c0 = group * cols_a + h * 16;
+                tmem_ld16_sync(taddr + D_A + c0, v);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 2; ++q) {
                     uint32_t p[4];
 #pragma unroll
                     for (int w = 0; w < 4; ++w)
@@ -237,39 +262,56 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
                 }
             }
         } else {
-            float* P = reinterpret_cast<float*>(smem + P_OFF) + row * P_ROW;
+            float* prow = P + row * P_ROW;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (32 * h >= cols_a || row >= rr) break;
-                uint32_t v[32];
-                const int c0 = half * cols_a + h * 32;
-                tmem_ld32(taddr + D_A + c0, v);
-                tmem_ld_wait();
+                if (16 * h >= cols_a || row >= rr) break;
+                uint32_t v[16];
+                const int c0 = group * cols_a + h * 16;
+                tmem_ld16_sync(taddr + D_A + c0, v);
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    *reinterpret_cast<uint4*>(P + c0 + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<uint4*>(prow + c0 + 4 * q) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
             }
             __syncthreads();
+            // this step's half of the shares: a block may write its next one while another still reads
+            const int turn = (k & 1) * R * R;
             const int vr = rr / 4, lg = rr == 64 ? 4 : 5;           // float4 per row, and its logarithm
             for (int i = threadIdx.x; i < rr * vr; i += THREADS)
-                __stcg(reinterpret_cast<float4*>(share) + i,
-                       *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + P_OFF) + (i >> lg) * P_ROW + (i & (vr - 1)) * 4));
+                __stcg(reinterpret_cast<float4*>(share + turn) + i,
+                       *reinterpret_cast<const float4*>(P + (i >> lg) * P_ROW + (i & (vr - 1)) * 4));
             cluster_sync();
-            // rows [rank rr / C, ..) of A, four columns a thread, summed in rank order
-            const int first = rank * (rr / C) * vr;
-            for (int i = threadIdx.x; i < rr / C * vr; i += THREADS) {
-                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                for (int c = 0; c < C; ++c) {
-                    const float4 u = __ldcg(reinterpret_cast<const float4*>(shares + c * (SHARE / 4)) + first + i);
-                    t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+            if (C * rr <= 512) {
+                // few or small shares (128 KB at most): every block sums them whole, without a second exchange
+                for (int i = threadIdx.x; i < rr * vr; i += THREADS) {
+                    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int c = 0; c < C; ++c) {
+                        const float4 u = __ldcg(reinterpret_cast<const float4*>(shares + turn + c * (SHARE / 4)) + i);
+                        t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+                    }
+                    const int r = i >> lg, c0 = (i & (vr - 1)) * 4;
+                    *reinterpret_cast<uint2*>(smem + A_OFF + chunk(r, c0 & ~7) + (c0 & 4) * 2) =
+                        make_uint2(pack_half2(fa * t.x, fa * t.y), pack_half2(fa * t.z, fa * t.w));
                 }
-                __stcg(reinterpret_cast<uint2*>(a_out) + first + i, make_uint2(pack_half2(fa * t.x, fa * t.y), pack_half2(fa * t.z, fa * t.w)));
-            }
-            cluster_sync();
-            for (int i = threadIdx.x; i < rr * rr / 8; i += THREADS) {
-                const int r = i >> (lg - 1), c0 = (i & (vr / 2 - 1)) * 8;
-                *reinterpret_cast<uint4*>(smem + A_OFF + chunk(r, c0)) = __ldcg(reinterpret_cast<const uint4*>(a_out) + i);
+            } else {
+                // rows [rank rr / C, ..) of A, four columns a thread, summed in rank order
+                const int first = rank * (rr / C) * vr;
+                for (int i = threadIdx.x; i < rr / C * vr; i += THREADS) {
+                    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                    for (int c = 0; c < C; ++c) {
+                        const float4 u = __ldcg(reinterpret_cast<const float4*>(shares + turn + c * (SHARE / 4)) + first + i);
+                        t.x += u.x; t.y += u.y; t.z += u.z; t.w += u.w;
+                    }
+                    __stcg(reinterpret_cast<uint2*>(a_out) + first + i,
+                           make_uint2(pack_half2(fa * t.x, fa * t.y), pack_half2(fa * t.z, fa * t.w)));
+                }
+                cluster_sync();
+                for (int i = threadIdx.x; i < rr * rr / 8; i += THREADS) {
+                    const int r = i >> (lg - 1), c0 = (i & (vr / 2 - 1)) * 8;
+                    *reinterpret_cast<uint4*>(smem + A_OFF + chunk(r, c0)) = __ldcg(reinterpret_cast<const uint4*>(a_out) + i);
+                }
             }
         }
         fence_proxy_async_smem();
@@ -291,28 +333,33 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         const float f1 = cb * (a.sc.b / a.sc.a), f2 = cc * (a.sc.b / (a.sc.a * a.sc.a));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (32 * h >= cols_a || row >= rr) break;
-            uint32_t v[32];
-            const int c0 = half * cols_a + h * 32;
-            tmem_ld32(taddr + D_AA + c0, v);
-            tmem_ld_wait();
+            if (16 * h >= cols_a || row >= rr) break;
+            uint32_t v[16];
+            const int c0 = group * cols_a + h * 16;
+            tmem_ld16_sync(taddr + D_AA + c0, v);
+            const int diag = row - c0;           // the column of B's diagonal, if it is among these
+            float on = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2; ++q) {
                 const uint4 av = *reinterpret_cast<const uint4*>(smem + A_OFF + chunk(row, c0 + 8 * q));
                 const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
                 uint32_t p[4];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const float2 in = unpack_half2(aw[w]);
-                    const int c = c0 + 8 * q + 2 * w;
-                    float b0 = f1 * in.x + f2 * __uint_as_float(v[8 * q + 2 * w]);
-                    float b1 = f1 * in.y + f2 * __uint_as_float(v[8 * q + 2 * w + 1]);
-                    if (c == row) { dvec[row] = b0; b0 = 0.0f; }
-                    if (c + 1 == row) { dvec[row] = b1; b1 = 0.0f; }
+                    const int c = 8 * q + 2 * w;
+                    float b0 = f1 * in.x + f2 * __uint_as_float(v[c]);
+                    float b1 = f1 * in.y + f2 * __uint_as_float(v[c + 1]);
+                    if ((c0 >> 5) == quarter) {
+                        on = c == diag ? b0 : (c + 1 == diag ? b1 : on);
+                        b0 = c == diag ? 0.0f : b0;
+                        b1 = c + 1 == diag ? 0.0f : b1;
+                    }
                     p[w] = pack_half2(b0, b1);
                 }
                 *reinterpret_cast<uint4*>(smem + B_OFF + chunk(row, c0 + 8 * q)) = make_uint4(p[0], p[1], p[2], p[3]);
             }
+            if (diag >= 0 && diag < 16) dvec[row] = on;
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -328,49 +375,54 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
             }
             __syncwarp();
         }
-        const float d = row < rr ? dvec[row] * (1.0f / a.sc.b) : 0.0f, fx = 1.0f / a.sc.b;
+        const float d = row < rr ? dvec[row] : 0.0f, fx = 1.0f / a.sc.b;
         finish_mma();
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < XC; c += 32) {
             if (c < ncol && quarter * 32 < rr) {
                 uint32_t v[32];
-                tmem_ld32(taddr + D_X + half * 128 + c, v);
-                tmem_ld_wait();
+                tmem_ld32_sync(taddr + D_X + group * XC + c, v);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const float h = __half2float(__float2half_rn(x[c + j]));
-                    x[c + j] = ca * x[c + j] + d * h + fx * __uint_as_float(v[j]);
+                for (int j = 0; j < 32; j += 2) {
+                    const float2 h = unpack_half2(pack_half2(x[c + j], x[c + j + 1]));
+                    x[c + j] = ca * x[c + j] + fx * (d * h.x + __uint_as_float(v[j]));
+                    x[c + j + 1] = ca * x[c + j + 1] + fx * (d * h.y + __uint_as_float(v[j + 1]));
                 }
             }
         }
     }
-    // ---- the result
-    if (row < a.r) {
-        const float f = a.scale / a.sc.x;
-        const int valid = min(ncol, a.q - col_first);
+    // ---- the result, by the same way back
+    const float f = a.scale / a.sc.x;
+#pragma unroll 1
+    for (int p = 0; p < a.width; p += 128) {
+        const int c0 = rank * a.width + p, cols = min(128, min(a.width - p, a.q - c0));     // (may be negative)
+        if (p == (group >> 1) * 128 && ncol > 0 && row < rr) {
+#pragma unroll
+            for (int c = 0; c < XC; c += 4)
+                *reinterpret_cast<float4*>(P + row * P_ROW + (group & 1) * XC + c) = make_float4(f * x[c], f * x[c + 1], f * x[c + 2], f * x[c + 3]);
+        }
+        __syncthreads();
         uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + z * a.out_mat;
         if (a.tall) {
-            o += static_cast<long long>(col_first) * a.out_row + row;
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-                if (c < valid) o[c * a.out_row] = static_cast<uint16_t>(pack_bf16x2(f * x[c], 0.0f));
+#pragma unroll 2
+            for (int c = warp; c < cols; c += WARPS)
+                for (int r = lane; r < a.r; r += 32)
+                    o[static_cast<long long>(c0 + c) * a.out_row + r] = static_cast<uint16_t>(pack_bf16x2(P[r * P_ROW + c], 0.0f));
         } else {
-            o += row * a.out_row + col_first;
-#pragma unroll
-            for (int c = 0; c < 128; c += 8) {
-                if (a.out_vec && c + 8 <= valid) {
-                    *reinterpret_cast<uint4*>(o + c) =
-                        make_uint4(pack_bf16x2(f * x[c], f * x[c + 1]), pack_bf16x2(f * x[c + 2], f * x[c + 3]),
-                                   pack_bf16x2(f * x[c + 4], f * x[c + 5]), pack_bf16x2(f * x[c + 6], f * x[c + 7]));
+#pragma unroll 2
+            for (int r = warp; r < a.r; r += WARPS) {
+                uint16_t* line = o + static_cast<long long>(r) * a.out_row + c0;
+                if (a.out_vec && 4 * lane + 4 <= cols) {
+                    const float4 v = *reinterpret_cast<const float4*>(P + r * P_ROW + 4 * lane);
+                    *reinterpret_cast<uint2*>(line + 4 * lane) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
                 } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (c + j < valid) o[c + j] = static_cast<uint16_t>(pack_bf16x2(f * x[c + j], 0.0f));
+                    for (int c = a.out_vec ? 4 * lane : lane, n = 0; n < 4 && c < cols; ++n, c += a.out_vec ? 1 : 32)
+                        line[c] = static_cast<uint16_t>(pack_bf16x2(P[r * P_ROW + c], 0.0f));
                 }
             }
         }
+        __syncthreads();
     }
-    __syncthreads();                         // the norm's words are free again
     }
     tc_fence_before();
     __syncthreads();
