@@ -317,13 +317,15 @@ static fs_status swiglu_impl(const fs_layer_desc* d, const void* x, long long x_
         // 4-bit products of large groups run on CTA pairs
         const bool pair = f4 && (offsets ? static_cast<long long>(d->T) * d->k / G : rows) >= kMx4PairRows;
         const int mt = pair ? ceil_div(xr, 256) + G : max_mt;
+        const int bound = offsets ? static_cast<int>(xr) : rows;
         const auto gemm = [&](int epi, const void* a, const uint8_t* as, const void* w, int N, int K, void* out, long long ldo,
                               int out_cols, uint8_t* out_sf) {
             const uint8_t* wsf = packed_sf_mx(f4, w, G, N, K);
-            return pair ? launch_mx4_pair_gemm(epi, a, xr, as, w, wsf, G, N, K, plan, rows, mt, out, ldo, out_cols, out_sf, st)
-                        : launch_mx_gemm(f4, epi, a, xr, as, w, wsf, G, N, K, plan, rows, mt, out, ldo, out_cols, out_sf, st);
+            return pair ? launch_mx4_pair_gemm(epi, a, xr, as, w, wsf, G, N, K, offsets, bound, mt, out, ldo, out_cols, out_sf, st)
+                        : launch_mx_gemm(f4, epi, a, xr, as, w, wsf, G, N, K, plan, offsets, bound, mt, out, ldo, out_cols,
+                                         out_sf, st);
         };
-        FS_TRY(launch_plan(offsets, G, offsets ? static_cast<int>(xr) : rows, pair ? 256 : 128, plan, st));
+        if (!f4) FS_TRY(launch_plan(offsets, G, bound, 128, plan, st));
         FS_TRY(gemm(EPI_SWIGLU, x, xs, w13, 2 * cw, d->d, hc, mx_row_bytes(f4, cw), cw, hs));
         FS_TRY(gemm(y_f32 ? EPI_F32 : EPI_BF16, hc, hs, w3, d->d, cw, y, d->d, d->d, nullptr));
     } else if (is_fp8(d)) {
@@ -629,7 +631,7 @@ fs_status fs_linear_mx4(int64_t rows, int32_t N, int32_t K, const void* q, const
         FS_TRY(launch_mx4_pair_gemm(epi, q, r128, qs, w, wsf, 1, N, K, nullptr, static_cast<int>(rows), ceil_div(rows, 256), y,
                                     y_row, N, nullptr, st));
     else
-        FS_TRY(launch_mx_gemm(true, epi, q, r128, qs, w, wsf, 1, N, K, nullptr, static_cast<int>(rows),
+        FS_TRY(launch_mx_gemm(true, epi, q, r128, qs, w, wsf, 1, N, K, nullptr, nullptr, static_cast<int>(rows),
                               static_cast<int>(r128 / 128), y, y_row, N, nullptr, st));
     return FS_OK;
 }

@@ -130,12 +130,10 @@ mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int G = args.G;
 
     if constexpr (F4) cudaGridDependencySynchronize();
-    if (args.plan) {
+    if constexpr (F4) {
+        make_plan<BM>(args, mt_start, row_start);
+    } else {
         for (int i = threadIdx.x; i < 2 * (G + 1); i += THREADS) mt_start[i] = args.plan[i];
-    } else if (threadIdx.x == 0) {
-        mt_start[0] = row_start[0] = 0;
-        mt_start[1] = (args.rows + BM - 1) / BM;
-        row_start[1] = args.rows;
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -338,7 +336,7 @@ cudaError_t out_map(CUtensorMap* m, int epi, void* out, long long rows, int cols
 
 template <int EPI, bool F4, int BN = 256>
 static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
-                                  const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles, void* out,
+                                  const uint8_t* b_sf, int G, int N, int K, const int* plan, const int* offsets, int rows, int max_mtiles, void* out,
                                   long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
     static bool set_mx[kMaxDevices];
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(mx::mx_gemm_kernel<EPI, F4, BN>), mx::Fmt<F4, BN>::SMEM_BYTES, set_mx);
@@ -354,6 +352,7 @@ static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t
     if (e != cudaSuccess) return e;
     mx::Args args;
     args.plan = plan;
+    args.offsets = offsets;
     args.G = G;
     args.rows = rows;
     args.N = N;
@@ -370,7 +369,7 @@ static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t
     args.tma_out = 0;
     to = ta;
     if (F4) {
-        e = mx::out_map(&to, EPI, out, plan ? a_rows : rows, out_cols, ldo, &args.tma_out);
+        e = mx::out_map(&to, EPI, out, offsets ? a_rows : rows, out_cols, ldo, &args.tma_out);
         if (e != cudaSuccess) return e;
     } else if (EPI == EPI_BF16 && out_cols % 32 == 0 && ldo % 8 == 0 && (reinterpret_cast<uintptr_t>(out) & 15u) == 0) {
         e = make_out_map_bf16(&to, out, a_rows, out_cols, ldo);
@@ -394,31 +393,31 @@ static cudaError_t launch_mx_impl(const void* A, long long a_rows, const uint8_t
 
 template <bool F4>
 static cudaError_t launch_mx_fmt(int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
-                                 const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
+                                 const uint8_t* b_sf, int G, int N, int K, const int* plan, const int* offsets, int rows, int max_mtiles,
                                  void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
     if constexpr (F4) {
         // one group whose tiles of 256 columns would leave half of the SMs idle
         int sms = 0;
         const cudaError_t e = num_sms(&sms);
         if (e != cudaSuccess) return e;
-        if (!plan && 2LL * max_mtiles * ((N + 255) / 256) <= sms) {
+        if (!offsets && 2LL * max_mtiles * ((N + 255) / 256) <= sms) {
             if (epi == EPI_BF16)
-                return launch_mx_impl<EPI_BF16, F4, 64>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+                return launch_mx_impl<EPI_BF16, F4, 64>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, offsets, rows, max_mtiles, out, ldo,
                                                         out_cols, h_sf, st);
             if (epi == EPI_F32)
-                return launch_mx_impl<EPI_F32, F4, 64>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+                return launch_mx_impl<EPI_F32, F4, 64>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, offsets, rows, max_mtiles, out, ldo,
                                                        out_cols, h_sf, st);
         }
     }
     switch (epi) {
         case EPI_SWIGLU:
-            return launch_mx_impl<EPI_SWIGLU, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+            return launch_mx_impl<EPI_SWIGLU, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, offsets, rows, max_mtiles, out, ldo,
                                                   out_cols, h_sf, st);
         case EPI_BF16:
-            return launch_mx_impl<EPI_BF16, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+            return launch_mx_impl<EPI_BF16, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, offsets, rows, max_mtiles, out, ldo,
                                                 out_cols, h_sf, st);
         case EPI_F32:
-            return launch_mx_impl<EPI_F32, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo,
+            return launch_mx_impl<EPI_F32, F4>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, offsets, rows, max_mtiles, out, ldo,
                                                out_cols, h_sf, st);
         default:
             return cudaErrorInvalidValue;
@@ -426,11 +425,11 @@ static cudaError_t launch_mx_fmt(int epi, const void* A, long long a_rows, const
 }
 
 cudaError_t launch_mx_gemm(bool f4, int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
-                           const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
-                           void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
-    return f4 ? launch_mx_fmt<true>(epi, A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo, out_cols,
+                           const uint8_t* b_sf, int G, int N, int K, const int* plan, const int* offsets, int rows,
+                           int max_mtiles, void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
+    return f4 ? launch_mx_fmt<true>(epi, A, a_rows, a_sf, B, b_sf, G, N, K, plan, offsets, rows, max_mtiles, out, ldo, out_cols,
                                     h_sf, st)
-              : launch_mx_fmt<false>(epi, A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo, out_cols,
+              : launch_mx_fmt<false>(epi, A, a_rows, a_sf, B, b_sf, G, N, K, plan, offsets, rows, max_mtiles, out, ldo, out_cols,
                                      h_sf, st);
 }
 

@@ -15,7 +15,8 @@ constexpr int PIECE_BYTES = 2048;
 constexpr int kGroupM = 16;
 
 struct Args {
-    const int* plan;          // [2 (G + 1)]: m-tile prefix, row starts (multiples of 128); null: one group of `rows` rows
+    const int* plan;          // E4M3: [2 (G + 1)]: m-tile prefix, row starts (multiples of 128)
+    const int* offsets;       // E2M1: [G + 1] row starts on the device, or null: one group of `rows` rows
     int G, rows, N, K, n_tiles, max_mtiles;
     const uint8_t* a_sf;      // A scale chunks [rows128 / 128][K / 128][512]
     const uint8_t* b_sf;      // B scale chunks [G][n_tiles][K / 128][1024]
@@ -79,6 +80,48 @@ __device__ __forceinline__ Tile decode(int t, const int* mt_start, const int* ro
     const int rem = row_start[lo + 1] - r.a_row;
     r.rows_valid = rem < BM ? rem : BM;
     return r;
+}
+
+// E2M1: m-tile prefix and row starts of the groups in shared memory, from their offsets, by all threads of a block (its
+// own plan a block, instead of a launch before the products).  Offsets that are not increasing inside [0, rows] give no tiles.
+template <int BM>
+__device__ __forceinline__ void make_plan(const Args& args, int* mt_start, int* row_start) {
+    __shared__ int sums[THREADS / 32];
+    constexpr int PER = 2;                     // groups a thread: 640 of kMaxExperts
+    static_assert(THREADS * PER >= kMaxExperts, "groups");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = args.G;
+    int tiles[PER], bad = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int g = threadIdx.x * PER + i;
+        tiles[i] = 0;
+        if (g < G) {
+            const int a = args.offsets ? args.offsets[g] : 0, b = args.offsets ? args.offsets[g + 1] : args.rows;
+            bad |= a < 0 || b < a || b > args.rows;
+            row_start[g] = a;
+            if (g == G - 1) row_start[G] = b;
+            tiles[i] = bad ? 0 : (b - a + BM - 1) / BM;
+        }
+    }
+    int run = tiles[0] + tiles[1];
+    const int mine = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += n;
+    }
+    if (lane == 31) sums[warp] = run;
+    bad = __syncthreads_or(bad);
+    int before = run - mine;
+    for (int w = 0; w < warp; ++w) before += sums[w];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int g = threadIdx.x * PER + i;
+        if (g < G) mt_start[g] = bad ? 0 : before;
+        before += tiles[i];
+        if (g == G - 1) mt_start[G] = bad ? 0 : before;
+    }
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0) set_dev_error(args.err, DEV_ERR_OFFSETS);
 }
 
 // One piece of 32 rows x 64 bytes (32 bf16 or 16 fp32 columns) through the warp's staging buffer and a TMA store.

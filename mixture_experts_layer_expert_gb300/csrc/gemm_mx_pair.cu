@@ -96,13 +96,7 @@ mx4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         tmem_relinquish_pair();
     }
     cudaGridDependencySynchronize();
-    if (args.plan) {
-        for (int i = threadIdx.x; i < 2 * (G + 1); i += THREADS) mt_start[i] = args.plan[i];
-    } else if (threadIdx.x == 0) {
-        mt_start[0] = row_start[0] = 0;
-        mt_start[1] = (args.rows + BM - 1) / BM;
-        row_start[1] = args.rows;
-    }
+    make_plan<BM>(args, mt_start, row_start);
     tc_fence_before();
     __syncthreads();
     cluster_sync();              // the even CTA's barriers exist before the odd CTA signals them
@@ -258,7 +252,7 @@ cudaError_t scale_map(CUtensorMap* map, const void* base, long long rows, int wo
 
 template <int EPI>
 cudaError_t launch(const void* A, long long a_rows, const uint8_t* a_sf, const void* B, const uint8_t* b_sf, int G, int N, int K,
-                   const int* plan, int rows, int max_mtiles, void* out, long long ldo, int out_cols, uint8_t* h_sf,
+                   const int* offsets, int rows, int max_mtiles, void* out, long long ldo, int out_cols, uint8_t* h_sf,
                    cudaStream_t st) {
     static bool set[kMaxDevices];
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(mx4_pair_kernel<EPI>), SMEM_BYTES, set);
@@ -272,7 +266,7 @@ cudaError_t launch(const void* A, long long a_rows, const uint8_t* a_sf, const v
     if (e == cudaSuccess) e = scale_map(&sb, b_sf, static_cast<long long>(G) * n_tiles * (K / 128), 256);
     if (e != cudaSuccess) return e;
     Args args{};
-    args.plan = plan;
+    args.offsets = offsets;
     args.G = G;
     args.rows = rows;
     args.N = N;
@@ -285,7 +279,7 @@ cudaError_t launch(const void* A, long long a_rows, const uint8_t* a_sf, const v
     args.h_sf = h_sf;
     args.err = dev_error_ptr();
     to = ta;
-    e = out_map(&to, EPI, out, plan ? a_rows : rows, out_cols, ldo, &args.tma_out);
+    e = out_map(&to, EPI, out, offsets ? a_rows : rows, out_cols, ldo, &args.tma_out);
     if (e != cudaSuccess) return e;
     if (EPI == EPI_SWIGLU && (!h_sf || ldo < out_cols / 2)) return cudaErrorInvalidValue;
     int sms = 0;
@@ -301,17 +295,17 @@ cudaError_t launch(const void* A, long long a_rows, const uint8_t* a_sf, const v
 }  // namespace mx
 
 cudaError_t launch_mx4_pair_gemm(int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
-                                 const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
+                                 const uint8_t* b_sf, int G, int N, int K, const int* offsets, int rows, int max_mtiles,
                                  void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st) {
     switch (epi) {
         case EPI_SWIGLU:
-            return mx::pair::launch<EPI_SWIGLU>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo, out_cols,
+            return mx::pair::launch<EPI_SWIGLU>(A, a_rows, a_sf, B, b_sf, G, N, K, offsets, rows, max_mtiles, out, ldo, out_cols,
                                                 h_sf, st);
         case EPI_BF16:
-            return mx::pair::launch<EPI_BF16>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo, out_cols,
+            return mx::pair::launch<EPI_BF16>(A, a_rows, a_sf, B, b_sf, G, N, K, offsets, rows, max_mtiles, out, ldo, out_cols,
                                               h_sf, st);
         case EPI_F32:
-            return mx::pair::launch<EPI_F32>(A, a_rows, a_sf, B, b_sf, G, N, K, plan, rows, max_mtiles, out, ldo, out_cols,
+            return mx::pair::launch<EPI_F32>(A, a_rows, a_sf, B, b_sf, G, N, K, offsets, rows, max_mtiles, out, ldo, out_cols,
                                              h_sf, st);
         default:
             return cudaErrorInvalidValue;

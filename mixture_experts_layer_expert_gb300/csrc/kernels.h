@@ -124,19 +124,20 @@ cudaError_t smem_attr_once(const void* fn, size_t bytes, bool (&set)[kMaxDevices
 // gemm_mx.cu: block-scaled operands, E4M3 codes (f4 false) or E2M1.  A is an MX
 // matrix of a_rows (a multiple of 128) rows and K columns (codes A, scale
 // chunks a_sf), B MX-packed weights [G, N, K] (codes, chunks b_sf); groups
-// start at multiples of 128 rows (plan nullptr: one group of `rows` rows).
+// start at multiples of 128 rows: E4M3 takes launch_plan's plan, E2M1 the offsets
+// [G + 1] themselves (nullptr: one group of `rows` rows; else `rows` bounds them).
 // EPI_SWIGLU writes the hidden as an MX matrix (codes at out with row stride
 // ldo bytes, chunks at h_sf; out_cols = c); EPI_BF16 / EPI_F32 write bf16 / fp32
 // rows.  N a multiple of 128 (E2M1 without EPI_SWIGLU: of 8).
 cudaError_t launch_mx_gemm(bool f4, int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
-                           const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
-                           void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st);
+                           const uint8_t* b_sf, int G, int N, int K, const int* plan, const int* offsets, int rows,
+                           int max_mtiles, void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st);
 
-// gemm_mx_pair.cu: the same for E2M1 on CTA pairs, whose plan has tiles of 256 rows.  For groups of kMx4PairRows rows
+// gemm_mx_pair.cu: the same for E2M1 on CTA pairs, tiles of 256 rows.  For groups of kMx4PairRows rows
 // or more on average: below that the halves of pair tiles that lie past a group's end cost more than the pair saves.
 constexpr int kMx4PairRows = 512;
 cudaError_t launch_mx4_pair_gemm(int epi, const void* A, long long a_rows, const uint8_t* a_sf, const void* B,
-                                 const uint8_t* b_sf, int G, int N, int K, const int* plan, int rows, int max_mtiles,
+                                 const uint8_t* b_sf, int G, int N, int K, const int* offsets, int rows, int max_mtiles,
                                  void* out, long long ldo, int out_cols, uint8_t* h_sf, cudaStream_t st);
 
 // mx.cu: MX packs and quantisation (layouts in mx.cuh), E4M3 or E2M1 (f4)

@@ -141,6 +141,7 @@ dispatch_copy_mx4_kernel(const uint4* __restrict__ u, int T, int d, int k, const
     const int lane = threadIdx.x & 31;
     const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
     if (t >= T) return;
+    cudaGridDependencySynchronize();
     const int n16 = d / 16, rb = d / 2;
     const int first = blockIdx.y * per * 32, last = min(n16, first + per * 32);
     const int my_p = lane < k ? pos[static_cast<long long>(t) * k + lane] : -1;
@@ -284,11 +285,10 @@ cudaError_t launch_dispatch_copy_mx(bool f4, const void* u, int T, int d, int k,
     count_launch();
     if (f4) {
         const int per = mx4_steps(T, d);
-        dispatch_copy_mx4_kernel<<<dim3(grid, ((d + 511) / 512 + per - 1) / per), 256, 0, st>>>(src, T, d, k, pos, per, xq,
-                                                                                                rows_cap, uq);
-    } else {
-        dispatch_copy_mx_kernel<<<grid, 256, 0, st>>>(src, T, d, k, pos, xq, rows_cap, uq);
+        return launch_after(dispatch_copy_mx4_kernel, dim3(grid, ((d + 511) / 512 + per - 1) / per), dim3(256), 0, st, src, T, d,
+                            k, pos, per, xq, rows_cap, uq);
     }
+    dispatch_copy_mx_kernel<<<grid, 256, 0, st>>>(src, T, d, k, pos, xq, rows_cap, uq);
     return cudaGetLastError();
 }
 

@@ -355,3 +355,25 @@ def test_linear_on_another_stream_and_replayed():
         graph.replay()
         no_error()
         assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("T", [60, 1200])
+def test_inconsistent_offsets_are_reported(T):
+    """Offsets that decrease, are negative or pass the rows: code 2, no rows written (both GEMM forms)."""
+    cfg = layer(T=T, E=4, k=2)
+    desc = fs.make_desc(cfg)
+    ws = fs.alloc_workspace(desc, 0)
+    w = synth.make_block_weights(cfg, 0)
+    p = fs.pack_block(cfg, {k: v.to(DEV) if v is not None else None for k, v in w.items()})
+    idx, _ = route(cfg, 1)
+    _, offsets, _, _, xp = dispatch(cfg, desc, idx.to(DEV), synth.make_x(cfg).to(DEV), ws)
+    rows = fs.fs_dispatch_rows(desc)
+    no_error()
+    for at, value in ((2, -128), (1, rows + 128), (3, 0), (4, 2 ** 31 - 1)):
+        bad = offsets.clone()
+        bad[at] = value
+        yp = torch.full((rows, cfg.d), 3.0, dtype=torch.bfloat16, device=DEV)
+        fs.fs_grouped_swiglu(desc, xp, bad, p["w13"], p["w3"], yp, ws)
+        torch.cuda.synchronize()
+        assert fs.fs_get_error() == (5, 2)
+        assert (yp == 3.0).all()
