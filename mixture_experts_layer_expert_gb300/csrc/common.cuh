@@ -279,8 +279,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr)
         : "memory");
 }
-// tmem_ld32 and tmem_ld16 with their wait in one statement.  A load fills its registers until the wait;
-// between two statements the compiler may copy them, and under register pressure does, before they are there.
+// tmem_ld32 and tmem_ld16 with their wait in one statement: a load fills its registers until the wait, and
+// between two statements the compiler would be free to use or copy them before they are there.
 __device__ __forceinline__ void tmem_ld32_sync(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "

@@ -26,7 +26,7 @@ namespace small {
 
 constexpr int R = 128;                         // rows held (r <= R; the rest are zero)
 constexpr int W = 256;                         // columns a block can hold
-constexpr int THREADS = 512;                   // (256 threads with 128 columns each took 7,500 cycles a step, not N)
+constexpr int THREADS = 512;                   // (256 threads with 128 columns each: 8 of 256 x 128 took 35 us, not 32)
 constexpr int WARPS = THREADS / 32;
 constexpr int XC = W / (WARPS / 4);            // columns of X a thread holds
 constexpr int BLOCK = R * 64 * 2;              // 64 columns of fp16: the 128-byte-swizzle tile, 16 KB
@@ -132,12 +132,33 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         const int c0 = rank * a.width + p, cols = min(128, a.width - p);
         const size_t es = a.src.f32 ? 4 : 2;
         const uint8_t* g = static_cast<const uint8_t*>(a.src.g) + static_cast<long long>(z) * a.src.mat * es;
-        if (a.tall) {                        // a column of X is a row of G
-#pragma unroll 2
-            for (int c = warp; c < cols; c += WARPS) {
-                const uint8_t* line = g + static_cast<long long>(c0 + c) * a.src.row * es;
-                for (int r = lane; r < rr; r += 32)
-                    P[r * P_ROW + c] = c0 + c < a.q && r < a.r ? at(a.src, line, r) : 0.0f;
+        if (a.tall || !a.src.vec) {
+            // element by element along G's rows (a column of X if tall): four lines of a warp, 16 loads in flight
+            const int lines = a.tall ? cols : rr, along = a.tall ? rr : 128;
+            const int first = a.tall ? 0 : c0, end = a.tall ? a.r : a.q - c0;      // within a line: its start, what G has of it
+            const int last = a.tall ? a.q - c0 : a.r;                              // lines that G has
+#pragma unroll 1
+            for (int l0 = warp; l0 < lines; l0 += 4 * WARPS) {
+                float v[4][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int l = l0 + u * WARPS;
+                    const uint8_t* line = g + (static_cast<long long>(a.tall ? c0 + l : l) * a.src.row + first) * es;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int e = lane + 32 * k;
+                        v[u][k] = l < last && l < lines && e < end ? at(a.src, line, e) : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int l = l0 + u * WARPS;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int e = lane + 32 * k;
+                        if (l < lines && e < along) P[a.tall ? e * P_ROW + l : l * P_ROW + e] = v[u][k];
+                    }
+                }
             }
         } else if (a.src.vec) {              // q is a multiple of a vector, so of 4
             const bool in = c0 + 4 * lane < a.q;
@@ -154,13 +175,6 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
                     }
                 }
                 *reinterpret_cast<float4*>(P + r * P_ROW + 4 * lane) = v;
-            }
-        } else {
-#pragma unroll 2
-            for (int r = warp; r < rr; r += WARPS) {
-                const uint8_t* line = g + (static_cast<long long>(r) * a.src.row + c0) * es;
-#pragma unroll
-                for (int c = lane; c < 128; c += 32) P[r * P_ROW + c] = c0 + c < a.q && r < a.r ? at(a.src, line, c) : 0.0f;
             }
         }
         __syncthreads();
@@ -231,13 +245,16 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         fence_proxy_async_smem();
         tc_fence_before();
         __syncthreads();
-        // ---- this block's share of X X^T
+        // ---- this block's share of X X^T.  (The products' loops are unrolled, with descriptors made outside the
+        // election: of a loop left rolled, the second operand of B H lost the upper half of its descriptor.)
         if (warp == 0) {
             tc_fence_after();
+            const uint64_t dh = smem_desc_sw128(base + H_OFF);
             if (elect_one()) {
-                for (int kk = 0; kk < a.width / 16; ++kk) {
-                    const uint64_t d = smem_desc_sw128(base + H_OFF + (kk >> 2) * BLOCK) + 2ull * (kk & 3);
-                    tc_mma_bf16(tmem + D_A, d, d, idesc_sq, kk > 0 ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < W / 16; ++kk) {
+                    const uint64_t d = dh + static_cast<uint64_t>((kk >> 2) * (BLOCK / 16) + 2 * (kk & 3));
+                    if (16 * kk < a.width) tc_mma_bf16(tmem + D_A, d, d, idesc_sq, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(smem_u32(bar));
             }
@@ -281,8 +298,9 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
                 __stcg(reinterpret_cast<float4*>(share + turn) + i,
                        *reinterpret_cast<const float4*>(P + (i >> lg) * P_ROW + (i & (vr - 1)) * 4));
             cluster_sync();
-            if (C * rr <= 512) {
-                // few or small shares (128 KB at most): every block sums them whole, without a second exchange
+            if (rr == 64 && C <= 8) {
+                // small shares: every block sums them whole, without a second exchange (64 x 512 35 us, not 38; of
+                // 128 rows 128 x 1,024 would take 76, not 59)
                 for (int i = threadIdx.x; i < rr * vr; i += THREADS) {
                     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -320,10 +338,12 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         // ---- B = b A + c A A
         if (warp == 0) {
             tc_fence_after();
+            const uint64_t da = smem_desc_sw128(base + A_OFF);
             if (elect_one()) {
-                for (int kk = 0; kk < rr / 16; ++kk) {
-                    const uint64_t d = smem_desc_sw128(base + A_OFF + (kk >> 2) * BLOCK) + 2ull * (kk & 3);
-                    tc_mma_bf16(tmem + D_AA, d, d, idesc_sq, kk > 0 ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < R / 16; ++kk) {
+                    const uint64_t d = da + static_cast<uint64_t>((kk >> 2) * (BLOCK / 16) + 2 * (kk & 3));
+                    if (16 * kk < rr) tc_mma_bf16(tmem + D_AA, d, d, idesc_sq, kk > 0 ? 1u : 0u);
                 }
                 tc_commit(smem_u32(bar));
             }
@@ -367,10 +387,13 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         // ---- X = a X + B H
         if (warp == 0) {
             tc_fence_after();
+            const uint64_t db = smem_desc_sw128(base + B_OFF), dh = smem_desc_sw128_mn(base + H_OFF, BLOCK);
             if (elect_one()) {
-                for (int kk = 0; kk < rr / 16; ++kk)
-                    tc_mma_bf16(tmem + D_X, smem_desc_sw128(base + B_OFF + (kk >> 2) * BLOCK) + 2ull * (kk & 3),
-                                smem_desc_sw128_mn(base + H_OFF, BLOCK) + 128ull * kk, idesc_x, kk > 0 ? 1u : 0u);
+#pragma unroll
+                for (int kk = 0; kk < R / 16; ++kk) {
+                    const uint64_t d = db + static_cast<uint64_t>((kk >> 2) * (BLOCK / 16) + 2 * (kk & 3));
+                    if (16 * kk < rr) tc_mma_bf16(tmem + D_X, d, dh + 128ull * kk, idesc_x, kk > 0 ? 1u : 0u);
+                }
                 tc_commit(smem_u32(bar));
             }
             __syncwarp();
@@ -404,12 +427,13 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         __syncthreads();
         uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + z * a.out_mat;
         if (a.tall) {
-#pragma unroll 2
+#pragma unroll 4
             for (int c = warp; c < cols; c += WARPS)
-                for (int r = lane; r < a.r; r += 32)
-                    o[static_cast<long long>(c0 + c) * a.out_row + r] = static_cast<uint16_t>(pack_bf16x2(P[r * P_ROW + c], 0.0f));
+#pragma unroll
+                for (int r = lane; r < R; r += 32)
+                    if (r < a.r) o[static_cast<long long>(c0 + c) * a.out_row + r] = static_cast<uint16_t>(pack_bf16x2(P[r * P_ROW + c], 0.0f));
         } else {
-#pragma unroll 2
+#pragma unroll 4
             for (int r = warp; r < a.r; r += WARPS) {
                 uint16_t* line = o + static_cast<long long>(r) * a.out_row + c0;
                 if (a.out_vec && 4 * lane + 4 <= cols) {
