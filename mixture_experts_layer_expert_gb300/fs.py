@@ -7,6 +7,7 @@ missing, ``lib()`` raises -- there is no fallback of any kind.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -708,18 +709,20 @@ class FarSkipTrainer:
         n = fs_balance_ws_bytes(desc)
         if n == 0:
             raise FsError(1, "fs_balance_ws_bytes")
-        b = getattr(self, "bal", None)
-        if b is None or b["counts"].shape[1] != S:
-            i32, f32 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.float32, device=dev)
-            b = {"counts": torch.empty((self.L, S, cfg.E), **i32), "tokens": torch.empty((self.L, S), **i32),
-                 "probs": torch.empty((self.L, S, cfg.E), **f32), "loss": torch.empty((self.L, 1), **f32),
-                 "d_logits": torch.zeros((self.L, self.T, cfg.E), **f32),
-                 "ws": torch.empty(n, dtype=torch.uint8, device=dev)}
-        b.update(desc=desc, cu=cu, mask=mask)
-        self.bal = b
+        self.bal_ready = False
         cur, st = _here(stream)
         cp = None if cu is None else _operand("balance_loss cu", cu, (S + 1,), cur, torch.int32, False)[0]
         mp = None if mask is None else _operand("balance_loss mask", mask, (self.T,), cur, torch.uint8, False)[0]
+        b = getattr(self, "bal", None)
+        if b is None or b["counts"].shape[1] != S:
+            i32, f32 = dict(dtype=torch.int32, device=dev), dict(dtype=torch.float32, device=dev)
+            with _allocating(stream):
+                b = {"counts": torch.empty((self.L, S, cfg.E), **i32), "tokens": torch.empty((self.L, S), **i32),
+                     "probs": torch.empty((self.L, S, cfg.E), **f32), "loss": torch.empty((self.L, 1), **f32),
+                     "d_logits": torch.empty((self.L, self.T, cfg.E), **f32),
+                     "ws": torch.empty(n, dtype=torch.uint8, device=dev)}
+        b.update(desc=desc, cu=cu, mask=mask)
+        self.bal = b
         for blk in range(self.L):
             z, idx = self._routing(blk)
             _check(lib().fs_balance_loss(desc, z, cfg.E, _p(self.blocks[blk]["bias"]), idx, cp, mp,
@@ -754,6 +757,9 @@ class FarSkipTrainer:
         b = self.bal
         cur, st = _here(stream)
         gp, _ = _operand("backward d_balance", d_balance, (1,), cur, torch.float32, False)
+        if b["cu"] is not None:             # rows outside every sequence are not written, and may have been inside one
+            with _allocating(stream):
+                b["d_logits"].zero_()
         extra = (_VP * self.L)()
         for blk in range(self.L):
             z, _ = self._routing(blk)
@@ -778,9 +784,10 @@ class FarSkipTrainer:
                 need = fs_orthogonalize_ws_bytes(desc)
                 if need == 0:
                     raise FsError(1, "fs_orthogonalize_ws_bytes")
-                if getattr(self, "ws_o", None) is None or self.ws_o.numel() < need:
-                    self.ws_o = torch.empty(need, dtype=torch.uint8, device=g.device)
-                upd[name] = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
+                with _allocating(stream):
+                    if getattr(self, "ws_o", None) is None or self.ws_o.numel() < need:
+                        self.ws_o = torch.empty(need, dtype=torch.uint8, device=g.device)
+                    upd[name] = torch.empty(g.shape, dtype=torch.bfloat16, device=g.device)
                 fs_orthogonalize(desc, g3, upd[name].view(g3.shape), self.ws_o, stream)
             updates.append(upd)
         return updates
@@ -802,6 +809,11 @@ def _here(stream):
     if stream is not None and stream.device_index != dev:
         raise FsError(1, "stream", "of cuda:%d, not of the current device" % stream.device_index)
     return dev, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _allocating(stream):
+    """Context in which torch allocates, fills and recycles memory in the order of the call's stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _operand(what: str, t: torch.Tensor, shape, dev: int, dtype=torch.bfloat16, strided=True):

@@ -303,3 +303,44 @@ def test_backward_needs_its_loss():
     tr.forward(prob["x"])
     with pytest.raises(fs.FsError):
         tr.backward(torch.zeros((64, 128), device=DEV), d_balance=torch.ones(1, device=DEV))
+
+
+def test_borders_change_between_steps():
+    """Steps of one trainer with other borders, on the current and on another stream, against a fresh trainer's step: what
+    rows that are now outside every sequence had in an earlier step does not come back."""
+    cfg = configs.LayerConfig("bal", T=300, d=256, E=12, k=2, c=128, n_shared=0, c_shared=0, L=2, gate="softmax_renorm",
+                              dtype="bf16")
+    prob = synth.make_problem(cfg, device=DEV)
+    d_o = torch.randn((cfg.T, cfg.d), generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+    one = torch.tensor([100.0], device=DEV)
+
+    def step(tr, cu, stream=None):
+        tr.forward(prob["x"], stream=stream)
+        tr.balance_loss(0.5, cu=cu, stream=stream)
+        dx, grads = tr.backward(d_o, d_balance=one, stream=stream)
+        torch.cuda.synchronize()
+        no_error()
+        return [dx.clone()] + [g[n].clone() for g in grads for n in sorted(g)]
+
+    borders = [torch.tensor(v, dtype=torch.int32, device=DEV) for v in ([0, 150, 300], [0, 40, 90], [100, 100, 101], [0, 90])]
+    side = torch.cuda.Stream()
+    tr = fs.FarSkipTrainer(cfg, prob["blocks"])
+    torch.cuda.synchronize()
+    for i, cu in enumerate(borders):
+        got = step(tr, cu, side if i % 2 else None)
+        want = step(fs.FarSkipTrainer(cfg, prob["blocks"]), cu)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), i
+
+
+def test_a_refused_loss_is_no_loss():
+    cfg = configs.LayerConfig("bal", T=64, d=256, E=8, k=2, c=128, n_shared=0, c_shared=0, L=1, gate="sigmoid_norm",
+                              dtype="bf16")
+    prob = synth.make_problem(cfg, device=DEV)
+    tr = fs.FarSkipTrainer(cfg, prob["blocks"])
+    tr.forward(prob["x"])
+    tr.balance_loss(1.0)
+    for bad in (dict(cu=torch.tensor([0, 64], device=DEV)), dict(mask=torch.ones(63, dtype=torch.uint8, device=DEV))):
+        with pytest.raises(fs.FsError):
+            tr.balance_loss(1.0, **bad)
+        with pytest.raises(fs.FsError):
+            tr.backward(torch.zeros((cfg.T, cfg.d), device=DEV), d_balance=torch.ones(1, device=DEV))
