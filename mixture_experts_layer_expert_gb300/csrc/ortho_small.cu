@@ -43,6 +43,7 @@ constexpr int BAR_OFF = S_OFF + WARPS * 16 + 16;
 constexpr size_t SMEM_BYTES = 1024 + BAR_OFF + 32;
 constexpr int D_A = 0, D_AA = 128, D_X = 256;  // TMEM columns
 static_assert(SMEM_BYTES <= 232448, "shared memory");
+static_assert(H_OFF + R * P_ROW * 4 <= P_OFF, "the operands' room holds 128 columns of G");
 
 struct Args {
     Source src;
@@ -54,6 +55,7 @@ struct Args {
     uint8_t* ws;                               // per block a share, then per cluster A [rr][rr] fp16
     float scale, eps;
     OrthoScales sc;
+    float fa, fb, fc, fx;                      // storage scales of A and its products: X to A, A to B, A A to B, B X to X
     float coefs[48];
     int* err;
 };
@@ -117,75 +119,88 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         tc_fence_after();
     };
 
+    // Line l of the block's part of G or of the result: 128 elements along a row of G, which is a row of X (two lines a row
+    // if the block has more columns) or, of tall matrices, a column.
+    float* P = reinterpret_cast<float*>(smem + P_OFF);
+    float* P2 = reinterpret_cast<float*>(smem + H_OFF);
+    struct Line {
+        float* buf;
+        long long row;
+        int col;
+    };
+    const int per = a.tall ? 128 : rr, lines = a.tall ? a.width : rr * ((a.width + 127) >> 7);
+    const auto line = [&](int l) {
+        const int second = l >= per ? 1 : 0, i = l - second * per;
+        const int c0 = rank * a.width;
+        return Line{(second ? P2 : P) + i * P_ROW, a.tall ? c0 + l : i, a.tall ? 0 : c0 + 128 * second};
+    };
+    float* mine = (group < 2 ? P : P2) + (a.tall ? (group & 1) * XC * P_ROW + row : row * P_ROW + (group & 1) * XC);
+
 #pragma unroll 1
     for (int z = cluster; z < a.batch; z += clusters) {
-    // ---- the block's slice of G through the share's buffer, 128 columns at a time, and the norm.  (Loops of a few
-    // instructions that read along G's rows: as straight code, each thread its own columns, this took 7,000 cycles,
-    // most of them fetching instructions.)
+    // ---- the block's slice of G through two buffers of 128 columns (the share's and, before there are operands, theirs),
+    // and the norm.  (Loops of a few instructions that read along G's rows: as straight code, each thread its own
+    // columns, this took 7,000 cycles, most of them fetching instructions.)
     float x[XC];
 #pragma unroll
     for (int c = 0; c < XC; ++c) x[c] = 0.0f;
-    float* P = reinterpret_cast<float*>(smem + P_OFF);
-    const float* mine = P + row * P_ROW + (group & 1) * XC;         // this thread's columns in the buffer
-#pragma unroll 1
-    for (int p = 0; p < a.width; p += 128) {
-        const int c0 = rank * a.width + p, cols = min(128, a.width - p);
+    if (!a.tall && a.src.vec) {              // q is a multiple of a vector, so of 4
+        const int c0 = rank * a.width;
         const size_t es = a.src.f32 ? 4 : 2;
-        const uint8_t* g = static_cast<const uint8_t*>(a.src.g) + static_cast<long long>(z) * a.src.mat * es;
-        if (a.tall || !a.src.vec) {
-            // element by element along G's rows (a column of X if tall): four lines of a warp, 16 loads in flight
-            const int lines = a.tall ? cols : rr, along = a.tall ? rr : 128;
-            const int first = a.tall ? 0 : c0, end = a.tall ? a.r : a.q - c0;      // within a line: its start, what G has of it
-            const int last = a.tall ? a.q - c0 : a.r;                              // lines that G has
-#pragma unroll 1
-            for (int l0 = warp; l0 < lines; l0 += 4 * WARPS) {
-                float v[4][4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int l = l0 + u * WARPS;
-                    const uint8_t* line = g + (static_cast<long long>(a.tall ? c0 + l : l) * a.src.row + first) * es;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int e = lane + 32 * k;
-                        v[u][k] = l < last && l < lines && e < end ? at(a.src, line, e) : 0.0f;
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int l = l0 + u * WARPS;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int e = lane + 32 * k;
-                        if (l < lines && e < along) P[a.tall ? e * P_ROW + l : l * P_ROW + e] = v[u][k];
-                    }
+        const uint8_t* g = static_cast<const uint8_t*>(a.src.g) + (z * a.src.mat + c0) * es;
+#pragma unroll 8
+        for (int l = warp; l < lines; l += WARPS) {
+            const int r = l < rr ? l : l - rr, c = l < rr ? 0 : 128;
+            const uint8_t* at_r = g + (static_cast<long long>(r) * a.src.row + c) * es;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c0 + c + 4 * lane < a.q && r < a.r) {
+                if (a.src.f32) {
+                    v = __ldg(reinterpret_cast<const float4*>(at_r) + lane);
+                } else {
+                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(at_r) + lane);
+                    v = make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
                 }
             }
-        } else if (a.src.vec) {              // q is a multiple of a vector, so of 4
-            const bool in = c0 + 4 * lane < a.q;
-#pragma unroll 4
-            for (int r = warp; r < rr; r += WARPS) {
-                const uint8_t* line = g + (static_cast<long long>(r) * a.src.row + c0) * es;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (in && r < a.r) {
-                    if (a.src.f32) {
-                        v = __ldg(reinterpret_cast<const float4*>(line) + lane);
-                    } else {
-                        const uint2 u = __ldg(reinterpret_cast<const uint2*>(line) + lane);
-                        v = make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
-                    }
-                }
-                *reinterpret_cast<float4*>(P + r * P_ROW + 4 * lane) = v;
-            }
+            *reinterpret_cast<float4*>((l < rr ? P : P2) + r * P_ROW + 4 * lane) = v;
         }
-        __syncthreads();
-        if (p == (group >> 1) * 128 && ncol > 0 && row < rr) {
+    } else
+#pragma unroll 4
+    for (int l = warp; l < lines; l += WARPS) {
+        const Line ln = line(l);
+        const int have = ln.row < (a.tall ? a.q : a.r) ? (a.tall ? a.r : a.q) - ln.col : 0;       // of 128 elements, G has
+        const size_t es = a.src.f32 ? 4 : 2;
+        const uint8_t* g = static_cast<const uint8_t*>(a.src.g) + (z * a.src.mat + ln.row * a.src.row + ln.col) * es;
+        if (a.src.vec) {                     // `have` is a multiple of a vector, so of 4
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (4 * lane < have) {
+                if (a.src.f32) {
+                    v = __ldg(reinterpret_cast<const float4*>(g) + lane);
+                } else {
+                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(g) + lane);
+                    v = make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
+                }
+            }
+            *reinterpret_cast<float4*>(ln.buf + 4 * lane) = v;
+        } else {
+            float v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = lane + 32 * k < have ? at(a.src, g, lane + 32 * k) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) ln.buf[lane + 32 * k] = v[k];
+        }
+    }
+    __syncthreads();
+    if (ncol > 0 && row < rr) {
+        if (a.tall) {
+#pragma unroll
+            for (int c = 0; c < XC; ++c) x[c] = mine[c * P_ROW];
+        } else {
 #pragma unroll
             for (int c = 0; c < XC; c += 4) {
                 const float4 v = *reinterpret_cast<const float4*>(mine + c);
                 x[c] = v.x; x[c + 1] = v.y; x[c + 2] = v.z; x[c + 3] = v.w;
             }
         }
-        __syncthreads();
     }
     Squares sq;
     sq.add(x);
@@ -261,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
             __syncwarp();
         }
         finish_mma();
-        const float fa = a.sc.a / (a.sc.x * a.sc.x);
+        const float fa = a.fa;
         if (C == 1) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -350,36 +365,44 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
             __syncwarp();
         }
         finish_mma();
-        const float f1 = cb * (a.sc.b / a.sc.a), f2 = cc * (a.sc.b / (a.sc.a * a.sc.a));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            if (16 * h >= cols_a || row >= rr) break;
-            uint32_t v[16];
-            const int c0 = group * cols_a + h * 16;
-            tmem_ld16_sync(taddr + D_AA + c0, v);
-            const int diag = row - c0;           // the column of B's diagonal, if it is among these
+        const float f1 = cb * a.fb, f2 = cc * a.fc;
+        const auto make_b = [&](auto& v, auto load) {
+            constexpr int N = sizeof(v) / 4;
+            const int c0 = group * N;
+            load(taddr + D_AA + c0, v);
             float on = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
+            for (int q = 0; q < N / 8; ++q) {
                 const uint4 av = *reinterpret_cast<const uint4*>(smem + A_OFF + chunk(row, c0 + 8 * q));
                 const uint32_t aw[4] = {av.x, av.y, av.z, av.w};
                 uint32_t p[4];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
-                    const float2 in = unpack_half2(aw[w]);
                     const int c = 8 * q + 2 * w;
-                    float b0 = f1 * in.x + f2 * __uint_as_float(v[c]);
-                    float b1 = f1 * in.y + f2 * __uint_as_float(v[c + 1]);
-                    if ((c0 >> 5) == quarter) {
-                        on = c == diag ? b0 : (c + 1 == diag ? b1 : on);
-                        b0 = c == diag ? 0.0f : b0;
-                        b1 = c + 1 == diag ? 0.0f : b1;
-                    }
-                    p[w] = pack_half2(b0, b1);
+                    const float2 b = fma2(make_float2(f2, f2), make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])),
+                                          mul2(make_float2(f1, f1), unpack_half2(aw[w])));
+                    p[w] = pack_half2(b.x, b.y);
+                    v[c] = __float_as_uint(b.x);
+                    v[c + 1] = __float_as_uint(b.y);
                 }
                 *reinterpret_cast<uint4*>(smem + B_OFF + chunk(row, c0 + 8 * q)) = make_uint4(p[0], p[1], p[2], p[3]);
             }
-            if (diag >= 0 && diag < 16) dvec[row] = on;
+            if ((c0 >> 5) == quarter) {          // the diagonal: in fp32 elsewhere, and zero in the product's operand
+                const int diag = row - c0;
+#pragma unroll
+                for (int c = 0; c < N; ++c) on = c == diag ? __uint_as_float(v[c]) : on;
+                if (diag >= 0 && diag < N) {
+                    dvec[row] = on;
+                    *reinterpret_cast<uint16_t*>(smem + B_OFF + chunk(row, row & ~7) + (row & 7) * 2) = 0;
+                }
+            }
+        };
+        if (rr == R) {
+            uint32_t v[32];
+            make_b(v, [](uint32_t t, uint32_t (&r)[32]) { tmem_ld32_sync(t, r); });
+        } else if (row < rr) {
+            uint32_t v[16];
+            make_b(v, [](uint32_t t, uint32_t (&r)[16]) { tmem_ld16_sync(t, r); });
         }
         fence_proxy_async_smem();
         tc_fence_before();
@@ -398,7 +421,7 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
             }
             __syncwarp();
         }
-        const float d = row < rr ? dvec[row] : 0.0f, fx = 1.0f / a.sc.b;
+        const float d = row < rr ? dvec[row] : 0.0f, fx = a.fx;
         finish_mma();
 #pragma unroll
         for (int c = 0; c < XC; c += 32) {
@@ -408,45 +431,56 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                     const float2 h = unpack_half2(pack_half2(x[c + j], x[c + j + 1]));
-                    x[c + j] = ca * x[c + j] + fx * (d * h.x + __uint_as_float(v[j]));
-                    x[c + j + 1] = ca * x[c + j + 1] + fx * (d * h.y + __uint_as_float(v[j + 1]));
+                    const float2 t = fma2(make_float2(d, d), h, make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+                    const float2 n = fma2(make_float2(fx, fx), t, mul2(make_float2(ca, ca), make_float2(x[c + j], x[c + j + 1])));
+                    x[c + j] = n.x;
+                    x[c + j + 1] = n.y;
                 }
             }
         }
     }
     // ---- the result, by the same way back
     const float f = a.scale / a.sc.x;
-#pragma unroll 1
-    for (int p = 0; p < a.width; p += 128) {
-        const int c0 = rank * a.width + p, cols = min(128, min(a.width - p, a.q - c0));     // (may be negative)
-        if (p == (group >> 1) * 128 && ncol > 0 && row < rr) {
+    if (ncol > 0 && row < rr) {
+        if (a.tall) {
+#pragma unroll
+            for (int c = 0; c < XC; ++c) mine[c * P_ROW] = f * x[c];
+        } else {
 #pragma unroll
             for (int c = 0; c < XC; c += 4)
-                *reinterpret_cast<float4*>(P + row * P_ROW + (group & 1) * XC + c) = make_float4(f * x[c], f * x[c + 1], f * x[c + 2], f * x[c + 3]);
+                *reinterpret_cast<float4*>(mine + c) = make_float4(f * x[c], f * x[c + 1], f * x[c + 2], f * x[c + 3]);
         }
-        __syncthreads();
-        uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + z * a.out_mat;
-        if (a.tall) {
-#pragma unroll 4
-            for (int c = warp; c < cols; c += WARPS)
-#pragma unroll
-                for (int r = lane; r < R; r += 32)
-                    if (r < a.r) o[static_cast<long long>(c0 + c) * a.out_row + r] = static_cast<uint16_t>(pack_bf16x2(P[r * P_ROW + c], 0.0f));
-        } else {
-#pragma unroll 4
-            for (int r = warp; r < a.r; r += WARPS) {
-                uint16_t* line = o + static_cast<long long>(r) * a.out_row + c0;
-                if (a.out_vec && 4 * lane + 4 <= cols) {
-                    const float4 v = *reinterpret_cast<const float4*>(P + r * P_ROW + 4 * lane);
-                    *reinterpret_cast<uint2*>(line + 4 * lane) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                } else {
-                    for (int c = a.out_vec ? 4 * lane : lane, n = 0; n < 4 && c < cols; ++n, c += a.out_vec ? 1 : 32)
-                        line[c] = static_cast<uint16_t>(pack_bf16x2(P[r * P_ROW + c], 0.0f));
-                }
-            }
-        }
-        __syncthreads();
     }
+    __syncthreads();
+    if (!a.tall && a.out_vec && a.q % 4 == 0) {
+        const int c0 = rank * a.width;
+        uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + z * a.out_mat + c0;
+#pragma unroll 4
+        for (int l = warp; l < lines; l += WARPS) {
+            const int r = l < rr ? l : l - rr, c = (l < rr ? 0 : 128) + 4 * lane;
+            const float4 v = *reinterpret_cast<const float4*>((l < rr ? P : P2) + r * P_ROW + 4 * lane);
+            if (r < a.r && c < a.width && c0 + c < a.q)
+                *reinterpret_cast<uint2*>(o + static_cast<long long>(r) * a.out_row + c) =
+                    make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        }
+    } else
+#pragma unroll 2
+    for (int l = warp; l < lines; l += WARPS) {
+        const Line ln = line(l);
+        const int cols = a.tall ? a.r : min(a.width - (l < rr ? 0 : 128), a.q - ln.col);
+        const int have = ln.row < (a.tall ? a.q : a.r) ? cols : 0;
+        uint16_t* o = reinterpret_cast<uint16_t*>(a.out) + z * a.out_mat + ln.row * a.out_row + ln.col;
+        if (a.out_vec && 4 * lane + 4 <= have) {
+            const float4 v = *reinterpret_cast<const float4*>(ln.buf + 4 * lane);
+            *reinterpret_cast<uint2*>(o + 4 * lane) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+        } else {
+            const int step = a.out_vec ? 1 : 32;
+#pragma unroll 1
+            for (int c = a.out_vec ? 4 * lane : lane, n = 0; n < 4 && c < have; ++n, c += step)
+                o[c] = static_cast<uint16_t>(pack_bf16x2(ln.buf[c], 0.0f));
+        }
+    }
+    __syncthreads();
     }
     tc_fence_before();
     __syncthreads();
@@ -506,6 +540,10 @@ cudaError_t launch_ortho_small(const OrthoArgs& o, void* ws, cudaStream_t st) {
     a.scale = o.scale;
     a.eps = static_cast<float>(o.eps);
     a.sc = o.scales;
+    a.fa = a.sc.a / (a.sc.x * a.sc.x);
+    a.fb = a.sc.b / a.sc.a;
+    a.fc = a.sc.b / (a.sc.a * a.sc.a);
+    a.fx = 1.0f / a.sc.b;
     for (int i = 0; i < 3 * o.steps; ++i) a.coefs[i] = o.coefs[i];
     a.err = dev_error_ptr();
     a.ws = static_cast<uint8_t*>(ws);
