@@ -372,11 +372,14 @@ backward_kernel(const BwdArgs a) {
         }
         const int n = a.tokens[q];
         const float per = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
-        const float unit = static_cast<float>(a.E) * per / static_cast<float>(a.k), scale = g * per;
+        // f - 1 instead of f: the scores' sum is one, so the gradient is the same, and it is exactly zero where all f are equal
+        const float unit = per / static_cast<float>(a.k), scale = g * per;
+        const long long even = static_cast<long long>(a.k) * n;
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = elem<VEC>(j, lane);
-            f[j] = e < a.E ? unit * static_cast<float>(a.counts[static_cast<long long>(q) * a.E + e]) : 0.0f;
+            f[j] = e < a.E ? unit * static_cast<float>(static_cast<long long>(a.counts[static_cast<long long>(q) * a.E + e]) * a.E - even)
+                           : 0.0f;
         }
         float v[U][EPL];
         bool on[U];

@@ -264,6 +264,9 @@ struct OrthoArgs {
 };
 size_t ortho_ws_bytes(int batch, int m, int n);
 cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st);
+// ortho_tiny.cu: matrices of at most 16 rows or columns in fp32
+bool ortho_tiny_fits(int m, int n);
+cudaError_t launch_ortho_tiny(const OrthoArgs& o, cudaStream_t st);
 // ortho_small.cu: a matrix in one cluster of blocks, all steps in one launch
 bool ortho_small_fits(int m, int n);
 size_t ortho_small_ws_bytes(int batch, int m, int n);

@@ -735,11 +735,13 @@ cudaError_t launch_square(const CUtensorMap& a, const CUtensorMap& b_half, const
 }  // namespace ortho
 
 size_t ortho_ws_bytes(int batch, int m, int n) {
+    if (ortho_tiny_fits(m, n)) return 256;
     return ortho_small_fits(m, n) ? ortho_small_ws_bytes(batch, m, n) : ortho::layout(batch, m, n).end;
 }
 
 cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) {
     using namespace ortho;
+    if (ortho_tiny_fits(o.m, o.n)) return launch_ortho_tiny(o, st);
     if (ortho_small_fits(o.m, o.n)) return launch_ortho_small(o, ws, st);
     const Shape s = shape(o.m, o.n);
     const Layout l = layout(o.batch, o.m, o.n);

@@ -344,3 +344,22 @@ def test_a_refused_loss_is_no_loss():
             tr.balance_loss(1.0, **bad)
         with pytest.raises(fs.FsError):
             tr.backward(torch.zeros((cfg.T, cfg.d), device=DEV), d_balance=torch.ones(1, device=DEV))
+
+
+@pytest.mark.parametrize("gate", GATES)
+def test_every_expert_chosen(gate):
+    """k = E: every f is one whatever the scores, so that the loss is coef and its gradient exactly zero."""
+    g = torch.Generator().manual_seed(8)
+    for T, E in ((1, 1), (33, 2), (1201, 16)):
+        z, idx = torch.randn((T, E), generator=g) * 3, torch.argsort(torch.randn((T, E), generator=g), 1).int()
+        counts, tokens, probs, loss, dz = call(z, idx, gate, 0.9)
+        assert (counts == T).all() and not dz.any()
+        assert abs(float(loss) - 0.9) <= 0.9 * (REL + (T / 8 + 40 + E) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("gate", GATES)
+def test_even_counts_leave_no_gradient(gate):
+    T, E, k = 640, 8, 2
+    idx = ((torch.arange(T)[:, None] * k + torch.arange(k)) % E).int()
+    got = call(torch.randn((T, E), generator=torch.Generator().manual_seed(2)), idx, gate, 1.0)
+    assert (got[0] == T * k // E).all() and not got[4].any()

@@ -176,3 +176,33 @@ def test_trainers_updates():
             assert u.shape == g.shape
             check(u if g.dim() == 3 else u[None], g if g.dim() == 3 else g[None])
         assert not upd[blk]["dW1"][4].any() and upd[blk]["dW1"][0].any()
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1), (3, 1, 2), (2, 1, 300), (2, 2, 2), (5, 3, 257), (2, 4000, 1), (1, 16, 16), (160, 16, 40),
+                                   (2, 513, 16), (20, 11, 2000), (1, 7, 8192), (1, 4097, 16)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_few_rows(shape, dtype):
+    """Up to 16 rows nothing is rounded below fp32.  A step's sums (at most 16 x 2 + 13 + 16 + 17 terms) and products are
+    within 2^-24 each of their size, 80 x 2^-24 of the norm, and later steps multiply by at most 3.4445 each:
+    (3.4445^5 - 1) / 2.4445 x 80 x 2^-24 = 9.5e-4 of the norm at worst, beside half a step of bf16 for each element."""
+    b, m, n = shape
+    g = torch.stack([ref.gradient(m, n, min(m, n) + i, 3 * i + m + n) for i in range(b)]).to(dtype).to(DEV)
+    out = run(g, scale=0.3)
+    for o, x in zip(out, g):
+        want = ref.exact(x, scale=0.3)
+        off = (o.double() - want).abs() - want.abs() * 2.0 ** -8
+        assert float(off.clamp_min(0).norm()) <= 9.5e-4 * float(want.norm())
+
+
+def test_few_rows_strided_and_apart():
+    """Row and matrix strides, a NaN in one matrix, zeros in another; what lies between rows stays."""
+    for m, n in ((5, 700), (700, 5)):
+        base = torch.stack([ref.gradient(m, n + 3, 9, i) for i in range(4)]).to(DEV)
+        g, full = base[:, :, 1:n + 1], torch.full((4, m, n + 2), 7.0, dtype=torch.bfloat16, device=DEV)
+        g[1] = 0.0
+        g[2, m // 2, n // 2] = math.nan
+        out = run(g, out=full[:, :, :n])
+        assert (full[:, :, n:] == 7).all() and not out[1].any() and out[2].isnan().all()
+        for i in (0, 3):
+            assert torch.equal(out[i], run(g[i:i + 1].contiguous())[0])
+            assert float((out[i].double() - ref.exact(g[i])).norm()) <= (2.0 ** -8 + 9.5e-4) * float(ref.exact(g[i]).norm())
