@@ -9,7 +9,7 @@
 //   that a lane still holds: 155 shuffles instead of 680), over the block's warps and then the blocks in rank order
 //   A, then M = a 1 + b A + c A A, one element a thread;  X = M X, M's rows read as broadcasts.
 // Bound by latency: some 2,000 instructions a warp and step and one exchange between blocks
-// (16 x 4,000 00 us; with the 64-row tensor tiles of ortho_small.cu 38).
+// (16 x 4,000 23 us; with the 64-row tensor tiles of ortho_small.cu 38).
 #include "common.cuh"
 #include "kernels.h"
 #include "ortho.cuh"
