@@ -575,7 +575,8 @@ fs_status fs_balance_loss_backward(const fs_balance_desc* desc, const float* log
  * back).  Products are fp16 with fp32 sums; X is carried in 22 bits between the
  * steps, because they multiply what a rounding puts into directions that G lacks.
  * For five usual steps a result of 32 rows or more is within 0.3% (Frobenius, its
- * own bf16 rounding included) of the exact one, for gradients of any rank.  A matrix of zeros gives
+ * own bf16 rounding included) of the exact one, for gradients of any rank.  With at most 16 rows
+ * or columns (and 8,192 of the other) all of it is fp32.  A matrix of zeros gives
  * zeros (eps = 0 too); a NaN or infinity makes its whole matrix NaN and no other.
  * Norms are taken over fp32's whole range.
  *

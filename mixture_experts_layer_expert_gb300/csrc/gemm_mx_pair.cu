@@ -11,6 +11,10 @@
 //   tfull    (each)      the tile is complete;             tempty (even)    16 warps have copied it out
 // The scales come by tensor maps of 512-byte and 1 KB rows: those carry an mbarrier of the other CTA
 // and fill with zeros past the end (an odd number of chunks, a pair's second half past the last row).
+// Measured: 65,536 rows of 32 experts, gate/up (K = 7,168) 521 us, 7.4 PFLOP/s; down (K = 2,048) 370 us, 5.2;
+// 16,381 x 2,048 of K = 7,168 76 us, 6.3.  What bounds it: L2 to shared memory, 18 TB/s in the gate/up product (a stage's
+// 35 KB take 560 cycles at 64 bytes a cycle), and some 3,000 cycles between two tiles, in which the
+// accumulator is copied out and handed back (there is no room in TMEM for a second one beside the scales).
 #include "gemm_mx.cuh"
 
 namespace fs {
