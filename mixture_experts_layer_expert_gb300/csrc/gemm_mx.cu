@@ -22,6 +22,9 @@
 //         last stage may be half full: it has one chunk and two MMAs (the codes
 //         behind it are zeros of the weight tile or of the TMA load's fill).
 //
+// Measured, E2M1 and few rows (many run in gemm_mx_pair.cu): 61 tokens x 6 over 64 experts, d = 2,048, c = 1,408, gate/up
+// 36 us and down 22, 4.7 TB/s of weights: HBM behind the latency of the first stages and the epilogue.
+//
 // Epilogues: EPI_SWIGLU writes the hidden h = SiLU(g) u rounded to bf16 and
 // quantised in blocks of 32 straight into an MX matrix (codes and scales: the
 // down projection's A operand); EPI_BF16 writes y (bf16); EPI_F32 writes fp32.
