@@ -572,7 +572,7 @@ fs_status fs_balance_loss_backward(const fs_balance_desc* desc, const float* log
  * momentum): per matrix G [m, n] of a batch, with X its transpose if m > n,
  *   X = G / (|G|_F + eps);  steps times  A = X X^T, X = a X + (b A + c A A) X
  * with step k's coefficients coefs[3k .. 3k+2]; out = scale X (bf16, transposed
- * back).  Products are fp16 with fp32 sums; X is carried in 22 bits between the
+ * back).  Products are fp16 with fp32 sums; X is carried in 19 bits between the
  * steps, because they multiply what a rounding puts into directions that G lacks.
  * For five usual steps a result of 32 rows or more is within 0.3% (Frobenius, its
  * own bf16 rounding included) of the exact one, for gradients of any rank.  With at most 16 rows

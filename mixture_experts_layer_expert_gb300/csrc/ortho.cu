@@ -9,10 +9,11 @@
 // 485 for the usual coefficients), and with them any error in directions that G
 // does not have: gradients of experts with fewer tokens than rows have many.  X
 // rounded to bf16 between the steps is 10 to 30% off for such G, in fp16 1 to 4%.
-// So X is a pair of fp16 numbers H + L 2^-11 (22 bits) as long as the steps to come can
+// So X is a pair, H in fp16 and L a byte in 254ths of H's step (19 bits), as long as the steps to come can
 // multiply by more than four, and the products read H only: an error of H enters through
 // B H, whose left side has no component outside G's own directions, and the term a X is
-// exact to 22 bits.  A and B are fp16, B's diagonal (its largest part once the rows are
+// exact to 19 bits.  (L in fp16 was no more exact in the result and cost 1.6 GB of traffic more for 128 x 768 x
+// 2,048, mostly in the first scaling: 230 us, not 200.)  A and B are fp16, B's diagonal (its largest part once the rows are
 // nearly orthonormal) fp32 and applied to H in the epilogue.  What remains is 0.06 to 0.15%,
 // below the rounding of a bf16 result (without the diagonal 0.2%; with L until the last
 // step no better, with L only while the steps multiply by more than 16 0.25%).  All three
@@ -23,12 +24,13 @@
 // by TMA in five stages of 64 along K, two accumulators in TMEM.  X X^T and A A compute
 // the tiles on and above the diagonal and store each 32 x 32 piece and its transpose; their
 // tiles are 256 x 128 where few tiles leave clusters idle (five matrices of 333 rows: 15 tiles or 20;
-// a half tile takes 0.7 of a whole one's time, its MMAs being bound by the operand reads).
+// a half tile takes 0.7 of a whole one's time, its MMAs being bound by the operand reads), and in a last round of
+// few tiles (3 x 2,048 rows: 108 tiles on 76 pairs, 77 to 70 us).
 // B X reads X as the MN-major operand, where it lies.  The epilogue's own inputs (the piece
 // of A, of H and L) come and go by TMA through two 4 KB buffers per warp.
-// Measured, 3 x 2,048 x 7,168: X X^T 75 us and B X 125 us (1.4 PFLOP/s each; bound by the reads of operands from shared
-// memory, 620 cycles a stage for 512 of MMAs, X X^T by its 108 tiles on 76 pairs too); 128 x 768 x 2,048: B X 290 us at
-// 5.6 TB/s of X in and out as a pair, X X^T 149 us.
+// Measured, 3 x 2,048 x 7,168: X X^T 70 us and B X 122 us (1.45 PFLOP/s each; bound by the reads of operands from shared
+// memory, 620 cycles a stage for 512 of MMAs); 128 x 768 x 2,048: B X 295 us, 4.3 TB/s of DRAM and some 60% of what
+// L2 hands an SM (a tile's operands and pieces 585 KB in 13,700 cycles), X X^T 145 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -49,6 +51,7 @@ constexpr int THREADS = 64 + 32 * EPI_WARPS;
 constexpr int NACC = 2;
 constexpr int TMEM_COLS = 512;
 constexpr int PIECE = 32 * 32 * 2;            // 32 x 32 fp16
+constexpr int LOW = 32 * 32;                  // of L
 constexpr int BUF = 2 * PIECE;
 constexpr int EPI_OFF = STAGES * STAGE_BYTES;
 constexpr int BAR_OFF = EPI_OFF + EPI_WARPS * 2 * BUF;
@@ -60,6 +63,7 @@ enum { GRAM = 0, POLY = 1, STEP = 2, LAST = 3 };
 
 struct Args {
     int R, C, batch, kb;          // tiles of rows and columns, matrices, stages along K
+    int whole, units;             // tiles that are worked on whole, and units in all: the others are two each
     int rows, cols;               // extents of the output (cols padded to 64)
     float alpha, beta;            // out = alpha in + beta acc (+ beta diag H)
     int low_in, low_out;          // X comes and goes as a pair
@@ -72,6 +76,7 @@ struct Args {
 
 struct Tile {
     int z, i, j;
+    int col, cols;                // first column and how many
 };
 
 // Tiles of a matrix: R x C, or of R x C those that reach the diagonal or lie above it.
@@ -86,6 +91,11 @@ __host__ __device__ __forceinline__ int tiles_per_matrix(int R, int C) {
 template <bool SYM, int BN>
 __device__ __forceinline__ Tile decode(int t, const Args& a, int per) {
     Tile r;
+    int part = -1;                     // half of a tile, of those behind a.whole
+    if (SYM && BN == BT && t >= a.whole) {
+        part = (t - a.whole) & 1;
+        t = a.whole + (t - a.whole) / 2;
+    }
     r.z = t / per;
     const int x = t - r.z * per;
     if constexpr (SYM && BN == BT) {   // column by column of the upper triangle: tile (i, j), i <= j, is j (j + 1) / 2 + i
@@ -105,6 +115,8 @@ __device__ __forceinline__ Tile decode(int t, const Args& a, int per) {
         r.j = x / a.R;
         r.i = x - r.j * a.R;
     }
+    r.col = r.j * BN + (part > 0 ? BN / 2 : 0);
+    r.cols = part < 0 ? BN : BN / 2;
     return r;
 }
 
@@ -124,6 +136,24 @@ __device__ __forceinline__ int chunk_at(int row, int q) { return row * 64 + ((q 
 // Element (row, col) of it.
 __device__ __forceinline__ int elem_at(int row, int col) { return chunk_at(row, col >> 3) + (col & 7) * 2; }
 
+// L: what H leaves of X, one byte each: 128 + 254 (x - h) / ulp(h), so 1 to 255, and off by
+// ulp(h) / 508 at most.  For h = +-1.f 2^(E - 15), p = 2^(E - 15) stands in h's own exponent bits, ulp(h) is 2^-10 p; of a
+// subnormal h p reads 0 and L is dropped (2^-25 at most, 2^-38 of the largest X).
+__device__ __forceinline__ uint32_t low_codes2(uint32_t h, float x0, float x1) {
+    const float2 v = unpack_half2(h), inv = unpack_half2(0x78007800u - (h & 0x7C007C00u));       // 1 / p
+    constexpr float S = 254.0f * 1024.0f, M = 12582912.0f + 128.0f;      // 1.5 2^23: the integer lands in the low bits
+    const float a = fmaf((x0 - v.x) * inv.x, S, M), b = fmaf((x1 - v.y) * inv.y, S, M);
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040) & 0xffffu;
+}
+__device__ __forceinline__ float low_byte(uint32_t word, int k) {        // 2^23 + its byte k, less 2^23 + 128
+    return __uint_as_float(__byte_perm(word, 0x4B000000u, 0x7440u + k)) - (8388608.0f + 128.0f);
+}
+__device__ __forceinline__ float2 with_low(uint32_t h, uint32_t word, int k) {
+    constexpr float U = 1.0f / (254.0f * 1024.0f);
+    const float2 v = unpack_half2(h), p = unpack_half2(h & 0x7C007C00u);
+    return make_float2(fmaf(low_byte(word, k), p.x * U, v.x), fmaf(low_byte(word, k + 1), p.y * U, v.y));
+}
+
 template <int MODE, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -132,8 +162,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     constexpr bool SYM = MODE == GRAM || MODE == POLY;
     constexpr bool B_MN = !SYM;
     constexpr bool LOADS = MODE != GRAM;
-    constexpr int HALF = BN / 2;                   // columns of an epilogue warp, and operand rows of a CTA
-    constexpr int PIECES = HALF / 32;
     static_assert(BN == BT || SYM, "the MN-major operand comes in boxes of 64 columns, two a CTA");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -176,7 +204,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const uint32_t tmem_base = *tmem_slot;
     cudaGridDependencySynchronize();
     const int per = tiles_per_matrix<SYM, BN>(args.R, args.C);
-    const int total = per * args.batch;
+    const int total = args.units;
     const int cid = static_cast<int>(cluster_id_x()), ncl = static_cast<int>(nclusters_x());
 
     if (warp == 0) {
@@ -190,19 +218,19 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             for (int t = cid; t < total && ok; t += ncl) {
                 const Tile tl = decode<SYM, BN>(t, args, per);
                 const int a_row = tl.i * BT + static_cast<int>(rank) * 128;
-                const int b_row = tl.j * BN + static_cast<int>(rank) * HALF;
+                const int b_rows = tl.cols / 2, b_row = tl.col + static_cast<int>(rank) * b_rows;
                 for (int kb = 0; kb < args.kb; ++kb) {
                     if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, args.err)) { ok = false; break; }
                     const uint32_t fb_local = smem_u32(&full[stage]);
-                    if (leader) mbar_arrive_expect_tx(fb_local, 2 * (A_STAGE + HALF * BK * 2));
+                    if (leader) mbar_arrive_expect_tx(fb_local, 2 * (A_STAGE + b_rows * BK * 2));
                     const uint32_t fb = map_to_cta(fb_local, 0);
                     const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES), sb = sa + A_STAGE;
                     tma_load_3d_pair(sa, &tmA, fb, kb * BK, a_row, tl.z);
                     if constexpr (B_MN) {          // two boxes of 64 K rows x 64 columns
                         tma_load_3d_pair(sb, &tmB, fb, b_row, kb * BK, tl.z);
                         tma_load_3d_pair(sb + 8192, &tmB, fb, b_row + 64, kb * BK, tl.z);
-                    } else {
-                        tma_load_3d_pair(sb, &tmB, fb, kb * BK, b_row, tl.z);
+                    } else {               // (of half a tile in boxes of half the rows)
+                        tma_load_3d_pair(sb, tl.cols == BN ? &tmB : &tmInL, fb, kb * BK, b_row, tl.z);
                     }
                     ++issued;
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
@@ -225,7 +253,6 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     } else if (warp == 1) {
         // ----------------------------------------------------------------- MMA
         if (leader) {
-            constexpr uint32_t idesc = idesc_f16(BT, BN, B_MN);
             int stage = 0, it = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -235,6 +262,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                 if (!mbar_wait(smem_u32(&tempty[acc]), (use & 1u) ^ 1u, abort_flag, args.err)) break;
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
+                const uint32_t idesc = SYM && BN == BT && t >= args.whole ? idesc_f16(BT, BN / 2, B_MN) : idesc_f16(BT, BN, B_MN);
                 for (int kb = 0; kb < args.kb; ++kb) {
                     if (!mbar_wait(smem_u32(&full[stage]), phase, abort_flag, args.err)) { ok = false; break; }
                     tc_fence_after();
@@ -274,9 +302,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         for (int t = cid; t < total; t += ncl, ++it) {
             const Tile tl = decode<SYM, BN>(t, args, per);
             const int row0 = tl.i * BT + static_cast<int>(rank) * 128 + quarter * 32;
-            const int col0 = tl.j * BN + half * HALF;
+            const int mine = tl.cols / 2, col0 = tl.col + half * mine;
             // this warp's pieces [first, last) along its columns
-            int last = row0 < args.rows ? min(PIECES, (args.cols - col0 + 31) / 32) : 0;
+            int last = row0 < args.rows ? min(mine / 32, (args.cols - col0 + 31) / 32) : 0;
             int first = SYM && col0 < row0 ? (row0 - col0) / 32 : 0;
             if (last < first) last = first;
             const int acc = it & 1;
@@ -287,7 +315,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     bulk_wait_read0();              // the buffer's last store has read it
                     const uint32_t bar = smem_u32(&ebar[2 * ew + b]), dst = smem_u32(buf0 + b * BUF);
                     const bool low = !SYM && args.low_in;
-                    mbar_arrive_expect_tx(bar, low ? 2 * PIECE : PIECE);
+                    mbar_arrive_expect_tx(bar, low ? PIECE + LOW : PIECE);
                     tma_load_3d(dst, &tmIn, bar, col0 + 32 * c, row0, tl.z);
                     if (low) tma_load_3d(dst + PIECE, &tmInL, bar, col0 + 32 * c, row0, tl.z);
                 }
@@ -303,7 +331,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (!mbar_wait(smem_u32(&tfull[acc]), use & 1u, abort_flag, args.err)) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
-                                   static_cast<uint32_t>(acc * BN + half * HALF);
+                                   static_cast<uint32_t>(acc * BN + half * mine);
             bool ok = true;
 #pragma unroll 1
             for (int c = first; c < last; ++c) {
@@ -320,10 +348,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     for (int q = 0; q < 4; ++q) {
                         const uint4 h = *reinterpret_cast<const uint4*>(buf + chunk_at(lane, q));
                         const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-                        uint32_t lw[4] = {0, 0, 0, 0};
+                        uint32_t lw[2] = {0x80808080u, 0x80808080u};
                         if (!SYM && args.low_in) {
-                            const uint4 l = *reinterpret_cast<const uint4*>(buf + PIECE + chunk_at(lane, q));
-                            lw[0] = l.x; lw[1] = l.y; lw[2] = l.z; lw[3] = l.w;
+                            const uint2 l = *reinterpret_cast<const uint2*>(buf + PIECE + lane * 32 + 8 * q);
+                            lw[0] = l.x; lw[1] = l.y;
                         }
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
@@ -334,9 +362,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                             if constexpr (!SYM) {
                                 a0 += d * in.x;
                                 a1 += d * in.y;
-                                const float2 lo = unpack_half2(lw[w]);
-                                in.x += lo.x * 0x1p-11f;
-                                in.y += lo.y * 0x1p-11f;
+                                if (args.low_in) in = with_low(hw[w], lw[w >> 1], 2 * (w & 1));
                             }
                             v0 = __float_as_uint(args.alpha * in.x + args.beta * a0);
                             v1 = __float_as_uint(args.alpha * in.y + args.beta * a1);
@@ -413,15 +439,15 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         }
                     } else if (args.low_out) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) {
+                        for (int q = 0; q < 2; ++q) {
                             uint32_t l[4];
 #pragma unroll
                             for (int w = 0; w < 4; ++w) {
-                                const float2 h = unpack_half2(p[4 * q + w]);
-                                l[w] = pack_half2((__uint_as_float(v[8 * q + 2 * w]) - h.x) * 0x1p11f,
-                                                  (__uint_as_float(v[8 * q + 2 * w + 1]) - h.y) * 0x1p11f);
+                                const uint32_t* x = &v[16 * q + 4 * w];
+                                l[w] = low_codes2(p[8 * q + 2 * w], __uint_as_float(x[0]), __uint_as_float(x[1])) |
+                                       low_codes2(p[8 * q + 2 * w + 1], __uint_as_float(x[2]), __uint_as_float(x[3])) << 16;
                             }
-                            *reinterpret_cast<uint4*>(buf + PIECE + chunk_at(lane, q)) = make_uint4(l[0], l[1], l[2], l[3]);
+                            *reinterpret_cast<uint4*>(buf + PIECE + lane * 32 + 16 * q) = make_uint4(l[0], l[1], l[2], l[3]);
                         }
                     }
                     fence_proxy_async_smem();
@@ -549,23 +575,22 @@ __device__ __forceinline__ void block_factors(const float* part, int nb, int z, 
     *f2 = f[1];
 }
 
-// Eight values as H and L (16 bytes each).
-__device__ __forceinline__ void split8(const float (&x)[8], uint4* h, uint4* l) {
+// Eight values as H and L (16 and 8 bytes).
+__device__ __forceinline__ void split8(const float (&x)[8], uint4* h, uint2* l) {
     uint32_t hw[4], lw[4];
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
         hw[w] = pack_half2(x[2 * w], x[2 * w + 1]);
-        const float2 b = unpack_half2(hw[w]);
-        lw[w] = pack_half2((x[2 * w] - b.x) * 0x1p11f, (x[2 * w + 1] - b.y) * 0x1p11f);
+        lw[w] = low_codes2(hw[w], x[2 * w], x[2 * w + 1]);
     }
     *h = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-    *l = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+    *l = make_uint2(lw[0] | lw[1] << 16, lw[2] | lw[3] << 16);
 }
 
-// X = G / (|G| + eps) as H + L 2^-11 times its power of two, rows where they are: a warp a row, eight
+// X = G / (|G| + eps) as H and L times its power of two, rows where they are: a warp a row, eight
 // columns a lane, four such in flight.  Columns past q up to the padded width are zero.
 __global__ void __launch_bounds__(256)
-scale_rows_kernel(const Source s, const float* part, int nb, double eps, float xscale, __half* H, __half* L, int qp) {
+scale_rows_kernel(const Source s, const float* part, int nb, double eps, float xscale, __half* H, uint8_t* L, int qp) {
     const int lane = threadIdx.x & 31, z = blockIdx.y, i = blockIdx.x * 8 + (threadIdx.x >> 5);
     cudaGridDependencySynchronize();
     float f1, f2;
@@ -600,14 +625,14 @@ scale_rows_kernel(const Source s, const float* part, int nb, double eps, float x
             if (c >= qp) break;
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[u][k] = x[u][k] * f1 * f2;
-            split8(x[u], reinterpret_cast<uint4*>(H + at_ + c), reinterpret_cast<uint4*>(L + at_ + c));
+            split8(x[u], reinterpret_cast<uint4*>(H + at_ + c), reinterpret_cast<uint2*>(L + at_ + c));
         }
     }
 }
 
 // The same for a tall G, transposed: a 64 x 64 tile per block.
 __global__ void __launch_bounds__(256)
-scale_tall_kernel(const Source s, const float* part, int nb, double eps, float xscale, int tiles, int tiles_n, __half* H, __half* L,
+scale_tall_kernel(const Source s, const float* part, int nb, double eps, float xscale, int tiles, int tiles_n, __half* H, uint8_t* L,
                   int r, int qp) {
     __shared__ float tile[64][65];
     const int z = blockIdx.y;
@@ -660,7 +685,7 @@ scale_tall_kernel(const Source s, const float* part, int nb, double eps, float x
                 float x[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) x[k] = tile[c + k][lr];
-                split8(x, reinterpret_cast<uint4*>(H + at_), reinterpret_cast<uint4*>(L + at_));
+                split8(x, reinterpret_cast<uint4*>(H + at_), reinterpret_cast<uint2*>(L + at_));
             }
         }
         __syncthreads();
@@ -691,7 +716,7 @@ size_t up(size_t x) { return (x + 1023) / 1024 * 1024; }
 Layout layout(int batch, int m, int n) {
     const Shape s = shape(m, n);
     const size_t x = static_cast<size_t>(s.r) * s.qp * 2, sq = static_cast<size_t>(s.r) * s.rp * 2;
-    const size_t each = 3 * x + 2 * sq + static_cast<size_t>(s.r) * 4 + NORM_BLOCKS * 12;
+    const size_t each = 5 * x / 2 + 2 * sq + static_cast<size_t>(s.r) * 4 + NORM_BLOCKS * 12;
     size_t g = (size_t(2) << 30) / each;
     g = g < 1 ? 1 : (g > 16384 ? 16384 : g);
     if (g > static_cast<size_t>(batch)) g = batch;
@@ -703,7 +728,7 @@ Layout layout(int batch, int m, int n) {
     auto take = [&](size_t bytes) { const size_t at_ = o; o = up(o + bytes); return at_; };
     l.h[0] = take(g * x);
     l.h[1] = take(g * x);
-    l.l = take(g * x);
+    l.l = take(g * (x / 2));
     l.a = take(g * sq);
     l.b = take(g * sq);
     l.diag = take(g * s.r * 4);
@@ -729,6 +754,17 @@ cudaError_t pieces(CUtensorMap* map, void* base, int cols, int rows, int mats) {
                   static_cast<long long>(rows) * cols * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
+cudaError_t low_pieces(CUtensorMap* map, void* base, int cols, int rows, int mats) {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, cols, rows, mats, cols, static_cast<long long>(rows) * cols, 32, 32,
+                  CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+// Tiles of the last round of clusters, if there are few enough of them to be worked on in halves (0.7 of a tile's time).
+int last_round(int tiles, int clusters) {
+    const int rest = tiles % clusters;
+    return tiles > clusters && 2 * rest <= clusters ? rest : 0;
+}
+
 template <int MODE, int BN>
 cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in, const CUtensorMap& in_l,
                          const CUtensorMap& out, const CUtensorMap& out_l, Args args, int sms, cudaStream_t st) {
@@ -736,8 +772,11 @@ cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const CUten
     cudaError_t e = smem_attr_once(reinterpret_cast<const void*>(gemm_kernel<MODE, BN>), SMEM_BYTES, set);
     if (e != cudaSuccess) return e;
     args.C = (args.cols + BN - 1) / BN;
-    const long long tiles = static_cast<long long>(tiles_per_matrix<MODE <= POLY, BN>(args.R, args.C)) * args.batch;
-    const int clusters = static_cast<int>(tiles < sms / 2 ? tiles : sms / 2);
+    const int tiles = tiles_per_matrix<MODE <= POLY, BN>(args.R, args.C) * args.batch;
+    const int clusters = tiles < sms / 2 ? tiles : sms / 2;
+    const int rest = MODE <= POLY && BN == BT ? last_round(tiles, clusters) : 0;
+    args.whole = tiles - rest;
+    args.units = tiles + rest;
     count_launch();
     return launch_after(gemm_kernel<MODE, BN>, dim3(2 * clusters), dim3(THREADS), SMEM_BYTES, st, a, b, in, in_l, out, out_l, args);
 }
@@ -747,12 +786,13 @@ cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const CUten
 template <int MODE>
 cudaError_t launch_square(const CUtensorMap& a, const CUtensorMap& b_half, const CUtensorMap& in, const CUtensorMap& out,
                           const Args& args, int sms, cudaStream_t st) {
-    const auto rounds = [&](long long tiles) { return (tiles * args.batch + sms / 2 - 1) / (sms / 2); };
-    const int c = (args.cols + 127) / 128;
-    const long long whole = 10 * rounds(tiles_per_matrix<true, BT>(args.R, args.R));
-    const long long half = 7 * rounds(tiles_per_matrix<true, 128>(args.R, c));
-    return half < whole ? launch_tiles<MODE, 128>(a, b_half, in, in, out, out, args, sms, st)
-                        : launch_tiles<MODE, BT>(a, a, in, in, out, out, args, sms, st);
+    const int most = sms / 2, c = (args.cols + 127) / 128;
+    const long long tiles = static_cast<long long>(tiles_per_matrix<true, BT>(args.R, args.R)) * args.batch;
+    const long long narrow = static_cast<long long>(tiles_per_matrix<true, 128>(args.R, c)) * args.batch;
+    if (narrow > 0x3fffffff) return cudaErrorInvalidValue;
+    const long long whole = 10 * ((tiles + most - 1) / most) - (last_round(static_cast<int>(tiles), most) ? 3 : 0);
+    return 7 * ((narrow + most - 1) / most) < whole ? launch_tiles<MODE, 128>(a, b_half, in, b_half, out, out, args, sms, st)
+                                                    : launch_tiles<MODE, BT>(a, a, in, b_half, out, out, args, sms, st);
 }
 
 }  // namespace ortho
@@ -784,7 +824,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
         count_launch();
         if ((e = launch_after(norm_kernel, dim3(blocks, nb), dim3(256), 0, st, src, part)) != cudaSuccess) return e;
         __half* H[2] = {reinterpret_cast<__half*>(w + l.h[0]), reinterpret_cast<__half*>(w + l.h[1])};
-        __half* L = reinterpret_cast<__half*>(w + l.l);
+        uint8_t* L = w + l.l;
         if (s.tall) {                          // tiles of G; for X's padded width the last ones reach past it
             const int tm = s.qp / 64, tn = s.rp / 64;
             const int most = (6 * sms + nb - 1) / nb;
@@ -804,7 +844,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& o, void* ws, cudaStream_t st) 
             if (e == cudaSuccess) e = operand(&xn[i], H[i], s.qp, s.r, nb, 64);
             if (e == cudaSuccess) e = pieces(&xp[i], H[i], s.qp, s.r, nb);
         }
-        if (e == cudaSuccess) e = pieces(&lp, L, s.qp, s.r, nb);
+        if (e == cudaSuccess) e = low_pieces(&lp, L, s.qp, s.r, nb);
         if (e == cudaSuccess) e = operand(&ak, A, s.rp, s.r, nb, 128);
         if (e == cudaSuccess) e = operand(&an, A, s.rp, s.r, nb, 64);
         if (e == cudaSuccess) e = pieces(&ap, A, s.rp, s.r, nb);
