@@ -26,7 +26,7 @@ class LayerConfig:
     gate: str            # softmax | softmax_renorm | sigmoid | sigmoid_norm
     dtype: str           # "bf16" (bf16 storage, fp32 accumulate), "f32", "fp8"
                          # (bf16 storage, FP8 E4M3 expert GEMM operands with row scales)
-                         # or "mxfp8" (the same with one scale per 32-element block)
+                         # or "mxfp8" (the same with one scale per 32-element block), "mxfp4" (4-bit codes so)
     zipf_s: float | None = None   # router-bias skew (Zipf exponent) or None
     wiring: str = "partial"
     seed: int = 0
@@ -50,7 +50,7 @@ class LayerConfig:
         read every expert's, the shared experts' and the router's weights once."""
         es = 4 if self.dtype == "f32" else 2
         # FP8 expert weights: one byte per element (MX: plus one scale byte per 32)
-        wes = 1.0 if self.dtype == "fp8" else (1.0 + 1.0 / 32 if self.dtype == "mxfp8" else es)
+        wes = {"fp8": 1.0, "mxfp8": 1.0 + 1.0 / 32, "mxfp4": 0.5 + 1.0 / 32}.get(self.dtype, es)
         T, d = self.T, self.d
         act = 4.0 * T * d * es
         w = (3.0 * self.E * d * self.c + 3.0 * self.n_shared * d * self.c_shared) * wes + self.E * d * es
