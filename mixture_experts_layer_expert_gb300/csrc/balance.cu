@@ -428,7 +428,7 @@ int chunk_rows(int T) {
     const long long c = (static_cast<long long>(T) + 151) / 152;
     return static_cast<int>((c + 7) / 8 * 8);
 }
-int blocks(int T) { return (T + chunk_rows(T) - 1) / chunk_rows(T); }
+int blocks(int T) { return (T - 1) / chunk_rows(T) + 1; }       // no sum past an int
 int expert_blocks(int E) { return (E + FIN_E - 1) / FIN_E; }
 
 struct Layout {
