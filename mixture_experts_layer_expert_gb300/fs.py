@@ -584,14 +584,14 @@ def _grads_struct(g: dict) -> BlockGrads:
 
 
 def make_balance(T: int, E: int, k: int, gate: str, n_seqs: int = 1, coef: float = 1.0) -> BalanceDesc:
-    d = BalanceDesc(T, E, k, GATES[gate], n_seqs, coef)
-    d.shapes = _balance_shapes(d)
-    return d
+    return BalanceDesc(T, E, k, GATES[gate], n_seqs, coef)
 
 
 def _balance_shapes(d):
-    """Shapes of logits, indices, borders, mask or bias, counts, tokens."""
-    return (d.T, d.E), (d.T, d.k), (d.n_seqs + 1,), (d.T,), (d.E,), (d.n_seqs, d.E), (d.n_seqs,)
+    """Shapes of logits, indices, borders, mask, bias, counts, tokens, from the fields as they are now: the library
+    reads these, and they may have changed since the descriptor was made."""
+    T, E, S = d.T, d.E, d.n_seqs
+    return (T, E), (T, d.k), (S + 1,), (T,), (E,), (S, E), (S,)
 
 
 def fs_balance_ws_bytes(desc: BalanceDesc) -> int:
@@ -611,7 +611,7 @@ def fs_balance_loss(desc: BalanceDesc, logits, topk_idx, counts, tokens, probs, 
     ws: fs_balance_ws_bytes(desc) bytes."""
     dev, st = _here(stream)
     what, f32, i32, u8 = "fs_balance_loss", torch.float32, torch.int32, torch.uint8
-    te, tk, s1, t1, e1, se, s = getattr(desc, "shapes", None) or _balance_shapes(desc)
+    te, tk, s1, t1, e1, se, s = _balance_shapes(desc)
     zp, zr = _logit_rows("fs_balance_loss logits", logits, te, dev)
     bp, ip, cp, mp, np_, tp, pp, lp, wp = _ptrs(what, dev, (
         ("bias", bias, e1, f32), ("topk_idx", topk_idx, tk, i32), ("cu", cu, s1, i32), ("mask", mask, t1, u8),
@@ -625,7 +625,7 @@ def fs_balance_loss_backward(desc: BalanceDesc, logits, counts, tokens, d_loss, 
     """d_logits [T, E] fp32 from fs_balance_loss's counts and tokens and d_loss [1] (None: 1)."""
     dev, st = _here(stream)
     what, f32, i32 = "fs_balance_loss_backward", torch.float32, torch.int32
-    te, _, s1, t1, e1, se, s = getattr(desc, "shapes", None) or _balance_shapes(desc)
+    te, _, s1, t1, e1, se, s = _balance_shapes(desc)
     zp, zr = _logit_rows("fs_balance_loss_backward logits", logits, te, dev)
     dp, dr = _logit_rows("fs_balance_loss_backward d_logits", d_logits, te, dev)
     bp, cp, mp, np_, tp, gp = _ptrs(what, dev, (
