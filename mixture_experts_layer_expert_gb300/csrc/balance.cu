@@ -43,8 +43,9 @@ struct Args {
     const int32_t* idx;
     const uint8_t* mask;
     const int32_t* cu;                    // null: one sequence of all rows
-    int T, E, k, S, chunk;
+    int T, E, k, S, chunk, blocks;
     float coef;
+    int* bad;                             // [blocks] a block's share of the borders is inconsistent
     float* part;                          // [slots][E] sums of scores
     int32_t* part_c;                      // [slots][E] counts
     int32_t* part_n;                      // [slots] counted tokens
@@ -161,6 +162,12 @@ piece_kernel(const Args a) {
     const int c0 = blockIdx.x * a.chunk, c1 = a.T - c0 < a.chunk ? a.T : c0 + a.chunk;     // no sum past an int
     cudaGridDependencySynchronize();
     if (!ONE && blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
+    bool bad = false;
+    if (!ONE && a.cu)
+        for (int i = blockIdx.x * THREADS + threadIdx.x; i <= a.S; i += gridDim.x * THREADS) {
+            const int at = a.cu[i];
+            bad |= at < 0 || at > a.T || (i < a.S && a.cu[i + 1] < at);
+        }
     float bias[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
@@ -247,10 +254,15 @@ piece_kernel(const Args a) {
         if (threadIdx.x == 0) a.part_n[slot] = ntok;
         __syncthreads();
     }
+    if (!ONE && a.cu) {
+        bad = __syncthreads_or(bad);
+        if (threadIdx.x == 0) a.bad[blockIdx.x] = bad;
+    }
 }
 
 // Block (expert block, sequence): the sequence's slots added in order, its counts, mean scores
-// and share of the loss; the block that finishes last adds the shares.
+// and share of the loss; the block that finishes last adds the shares.  Where any border is inconsistent sequences may
+// share rows, and slots that no block filled be read: then every sequence counts as empty.
 __global__ void __launch_bounds__(FIN_E * FIN_P)
 finish_kernel(const Args a) {
     __shared__ float s_sum[FIN_P][FIN_E + 1];
@@ -260,11 +272,9 @@ finish_kernel(const Args a) {
     const int x = threadIdx.x % FIN_E, y = threadIdx.x / FIN_E;
     const int e = blockIdx.x * FIN_E + x, q = blockIdx.y;
     cudaGridDependencySynchronize();
+    bool bad = a.cu && threadIdx.x < a.blocks && a.bad[threadIdx.x];
     int q0 = a.cu ? a.cu[q] : 0, q1 = a.cu ? a.cu[q + 1] : a.T;
-    if (q0 < 0 || q1 < q0 || q1 > a.T) {
-        if (threadIdx.x == 0) set_dev_error(a.err, DEV_ERR_OFFSETS);
-        q0 = q1 = 0;
-    }
+    if (q0 < 0 || q1 < q0 || q1 > a.T) q0 = q1 = 0;
     const int b0 = q0 / a.chunk, b1 = q1 > q0 ? (q1 - 1) / a.chunk + 1 : b0;
     float sum = 0.0f;
     int cnt = 0, n = 0;
@@ -280,7 +290,8 @@ finish_kernel(const Args a) {
     s_sum[y][x] = sum;
     s_cnt[y][x] = cnt;
     if (x == 0) s_n[y] = n;
-    __syncthreads();
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) set_dev_error(a.err, DEV_ERR_OFFSETS);
     if (y == 0) {
         n = 0;
         sum = 0.0f;
@@ -290,6 +301,10 @@ finish_kernel(const Args a) {
             n += s_n[p];
             sum += s_sum[p][x];
             cnt += s_cnt[p][x];
+        }
+        if (bad) {
+            n = cnt = 0;
+            sum = 0.0f;
         }
         float term = e < a.E ? finish(a, q, e, sum, cnt, n) : 0.0f;
         term = warp_sum(term);
@@ -368,7 +383,7 @@ backward_kernel(const BwdArgs a) {
         if (q0 >= c1) break;
         const int lo = max(q0, c0), hi = min(q1, c1);
         if (lo + warp >= hi) continue;
-        if (q0 < 0 || q1 > a.T) {              // (q1 < q0 has no rows and is the forward's error)
+        if (q0 < 0 || q1 > a.T) {              // (the forward reports all inconsistent borders, and counts no tokens then)
             set_dev_error(a.err, DEV_ERR_OFFSETS);
             continue;
         }
@@ -432,7 +447,7 @@ int blocks(int T) { return (T - 1) / chunk_rows(T) + 1; }       // no sum past a
 int expert_blocks(int E) { return (E + FIN_E - 1) / FIN_E; }
 
 struct Layout {
-    size_t part, part_c, part_n, loss_part, done, end;
+    size_t part, part_c, part_n, loss_part, done, bad, end;
 };
 Layout layout(int T, int E, int S) {
     const size_t slots = static_cast<size_t>(blocks(T)) + S;
@@ -444,6 +459,7 @@ Layout layout(int T, int E, int S) {
     l.part_n = take(slots * 4);
     l.loss_part = take(static_cast<size_t>(S) * expert_blocks(E) * 4);
     l.done = take(4);
+    l.bad = take(static_cast<size_t>(blocks(T)) * 4);
     l.end = o;
     return l;
 }
@@ -498,6 +514,8 @@ cudaError_t launch_balance(const BalanceArgs& b, void* ws, cudaStream_t st) {
     a.part_n = reinterpret_cast<int32_t*>(w + l.part_n);
     a.loss_part = reinterpret_cast<float*>(w + l.loss_part);
     a.done = reinterpret_cast<unsigned*>(w + l.done);
+    a.bad = reinterpret_cast<int*>(w + l.bad);
+    a.blocks = bal::blocks(b.T);
     a.counts = b.counts; a.tokens = b.tokens; a.probs = b.probs; a.loss = b.loss;
     a.err = dev_error_ptr();
     return b.sigmoid ? balance_fwd<true>(a, st) : balance_fwd<false>(a, st);
