@@ -543,11 +543,12 @@ fs_status fs_train_saved_routing(const fs_layer_desc* desc, int32_t L, int32_t b
  * (counts are constants; d_loss device fp32 scalar, NULL = 1):
  *   d_logits_te = d_loss coef / (n_seqs n) s_te (f_qe - sum_j f_qj s_tj) [(1 - sigmoid(z_te + b_e)), SIGMOID*]
  * zero for rows that the mask leaves out; rows outside every sequence are left as
- * they were.  A row whose logits are all -infinity scores zero; a NaN or +infinity
- * makes its row's scores NaN.  Sums are fp32 in a fixed order: results repeat bit
- * for bit.  An index outside [0, E) sets the device error word (code 1) and is not
- * counted; borders that decrease or leave [0, T] anywhere set it (code 2): all
- * sequences then count as empty, and the gradient of a row is zero or left.
+ * they were.  A row whose logits are all -infinity scores zero; a NaN makes its
+ * row's scores NaN, and so does +infinity for SOFTMAX* (its sigmoid is one, and
+ * takes no gradient).  Sums are fp32 in a fixed order: results repeat bit for bit.
+ * An index outside [0, E) sets the device error word (code 1) and is not counted;
+ * borders that decrease or leave [0, T] anywhere set it (code 2): all sequences
+ * then count as empty, and the gradient of a row is zero or left.
  * logits and d_logits are fp32 with row strides >= E elements; E <= 512, k <= 16,
  * n_seqs <= 65,535.  counts [n_seqs, E] and tokens [n_seqs] (n) int32, probs
  * [n_seqs, E] and loss [1] fp32.  ws: fs_balance_ws_bytes bytes, 256-byte aligned;
