@@ -497,19 +497,22 @@ __global__ void __launch_bounds__(256) norm_kernel(const Source s, float* part) 
     __shared__ float sh[8][3];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const size_t es = s.f32 ? 4 : 2;
+    const int per = s.f32 ? 4 : 8;
     const uint8_t* g = static_cast<const uint8_t*>(s.g) + static_cast<long long>(blockIdx.y) * s.mat * es;
     Squares q;
     cudaGridDependencySynchronize();
     for (int i = blockIdx.x * 8 + warp; i < s.m; i += gridDim.x * 8) {
         const uint8_t* row = g + i * s.row * es;
-        if (s.vec) {
-            const int nv = s.n / (16 / static_cast<int>(es));
-            for (int v0 = lane; v0 < nv; v0 += 128) {
+        // a lane adds the elements of whole vectors, also where they are read one by one: the sum, and with it the result's
+        // last bits, depend on neither alignment nor strides
+        const int nv = (s.n + per - 1) / per;
+        for (int v0 = lane; v0 < nv; v0 += 128) {
+            float f[32];
+            if (s.vec) {
                 uint4 x[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     x[k] = v0 + 32 * k < nv ? __ldg(reinterpret_cast<const uint4*>(row) + v0 + 32 * k) : make_uint4(0, 0, 0, 0);
-                float f[32];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
@@ -519,21 +522,20 @@ __global__ void __launch_bounds__(256) norm_kernel(const Source s, float* part) 
                         f[8 * k + 2 * h + 1] = s.f32 ? 0.0f : bf16hi(w[h]);
                     }
                 }
-                q.add(f);
-            }
-        } else {
-            for (int j0 = lane; j0 < s.n; j0 += 512) {
-                float f[16];
-                if (s.f32) {
+            } else if (s.f32) {
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) f[k] = j0 + 32 * k < s.n ? __ldg(reinterpret_cast<const float*>(row) + j0 + 32 * k) : 0.0f;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        f[k] = j0 + 32 * k < s.n ? __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(row) + j0 + 32 * k)) : 0.0f;
+                for (int k = 0; k < 32; ++k) {
+                    const int j = 4 * (v0 + 32 * (k >> 3)) + ((k & 7) >> 1);
+                    f[k] = !(k & 1) && j < s.n ? __ldg(reinterpret_cast<const float*>(row) + j) : 0.0f;
                 }
-                q.add(f);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const int j = 8 * (v0 + 32 * (k >> 3)) + (k & 7);
+                    f[k] = j < s.n ? __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(row) + j)) : 0.0f;
+                }
             }
+            q.add(f);
         }
     }
     float v[3] = {q.big, q.mid, q.small};
