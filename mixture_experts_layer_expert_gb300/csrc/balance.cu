@@ -65,20 +65,20 @@ __device__ __forceinline__ int elem(int j, int lane) {
 }
 
 template <int EPL, bool VEC>
-__device__ __forceinline__ void load_row(const float* __restrict__ p, int E, int lane, float pad, float (&v)[EPL]) {
+__device__ __forceinline__ void load_row(const float* p, int E, int lane, float pad, float (&v)[EPL]) {
     if constexpr (VEC) {
 #pragma unroll
         for (int j = 0; j < EPL; j += 4) {
             const int e = elem<VEC>(j, lane);
             float4 x = make_float4(pad, pad, pad, pad);
-            if (e < E) x = __ldg(reinterpret_cast<const float4*>(p + e));
+            if (e < E) x = *reinterpret_cast<const float4*>(p + e);
             v[j] = x.x; v[j + 1] = x.y; v[j + 2] = x.z; v[j + 3] = x.w;
         }
     } else {
 #pragma unroll
         for (int j = 0; j < EPL; ++j) {
             const int e = elem<VEC>(j, lane);
-            v[j] = e < E ? __ldg(p + e) : pad;
+            v[j] = e < E ? p[e] : pad;
         }
     }
 }

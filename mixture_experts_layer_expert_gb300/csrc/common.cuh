@@ -68,7 +68,9 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
 // ------------------------------------------------------------------ launch
 // Launches a kernel that may be set up while the one before it on the stream still
 // runs; it has to call cudaGridDependencySynchronize() before it reads or writes
-// anything that that one or an earlier one touches.
+// anything that that one or an earlier one touches, and reads it by plain loads: what
+// is written during a kernel's life is not for the read-only path (__ldg, or operands
+// that are const __restrict__), whose loads may also be moved up past that call.
 template <typename... P, typename... A>
 inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A&&... args) {
     cudaLaunchAttribute attr;

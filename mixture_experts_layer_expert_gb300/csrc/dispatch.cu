@@ -163,9 +163,8 @@ dispatch_rank_kernel(const int32_t* __restrict__ topk_idx, int T, int E, int k,
 // The three steps of one chunk (T <= kChunk) in one launch: a block, thread e owns expert e.  (Three launches of a few us of
 // latency each: a decode step of 61 tokens over 64 4-bit experts 83 us, not 73.)
 __global__ void __launch_bounds__(kChunk)
-dispatch_one_chunk_kernel(const int32_t* __restrict__ topk_idx, int T, int E, int k, int32_t* __restrict__ counts,
-                          int32_t* __restrict__ offsets, int pad128, int32_t* __restrict__ pos,
-                          int32_t* __restrict__ perm_src, int* err) {
+dispatch_one_chunk_kernel(const int32_t* topk_idx, int T, int E, int k, int32_t* counts, int32_t* offsets, int pad128,
+                          int32_t* pos, int32_t* perm_src, int* err) {
     extern __shared__ uint32_t wmask[];     // [warps][E]: lane masks, then prefixes; [E] counts, then first rows
     __shared__ int warp_sums[32];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, t = threadIdx.x, warps = (T + 31) / 32;
@@ -175,17 +174,16 @@ dispatch_one_chunk_kernel(const int32_t* __restrict__ topk_idx, int T, int E, in
     __syncthreads();
     int ex[kMaxTopK], rank[kMaxTopK];
 #pragma unroll
+    for (int s = 0; s < kMaxTopK; ++s) ex[s] = s < k && t < T ? topk_idx[static_cast<long long>(t) * k + s] : -1;
+#pragma unroll
     for (int s = 0; s < kMaxTopK; ++s) {
-        ex[s] = -1;
-        if (s < k && t < T) {
-            const int e = topk_idx[static_cast<long long>(t) * k + s];
-            if (e >= 0 && e < E) {
-                ex[s] = e;
-                atomicAdd(&hist[e], 1);
-                atomicOr(&wmask[w * E + e], 1u << lane);
-            } else {
-                set_dev_error(err, DEV_ERR_EXPERT_INDEX);
-            }
+        if (s >= k || t >= T) continue;
+        if (ex[s] >= 0 && ex[s] < E) {
+            atomicAdd(&hist[ex[s]], 1);
+            atomicOr(&wmask[w * E + ex[s]], 1u << lane);
+        } else {
+            ex[s] = -1;
+            set_dev_error(err, DEV_ERR_EXPERT_INDEX);
         }
     }
     __syncwarp();

@@ -100,7 +100,7 @@ __device__ __forceinline__ uint2 mx4_lane16(const uint4& a, const uint4& b, uint
 // x [rows, cols] -> q.  Zero rows behind them have zero codes and unit scales by themselves.  Bound by HBM: 16,381 x 7,168
 // 45 us, 6.7 TB/s of rows in and codes out.
 __global__ void __launch_bounds__(256)
-quant_rows_mx4_kernel(const uint4* __restrict__ x, long long rows, int cols, int per, uint8_t* __restrict__ q) {
+quant_rows_mx4_kernel(const uint4* x, long long rows, int cols, int per, uint8_t* q) {
     const int lane = threadIdx.x & 31;
     const long long nwarps = (static_cast<long long>(gridDim.x) * blockDim.x) >> 5;
     const int n16 = cols / 16;
@@ -117,8 +117,8 @@ quant_rows_mx4_kernel(const uint4* __restrict__ x, long long rows, int cols, int
             for (int s = 0; s < 2; ++s) {
                 const int v = v0 + 32 * s + lane;
                 const bool act = r < rows && v < last;
-                a[s] = act ? __ldg(src + 2 * v) : make_uint4(0, 0, 0, 0);
-                b[s] = act ? __ldg(src + 2 * v + 1) : make_uint4(0, 0, 0, 0);
+                a[s] = act ? src[2 * v] : make_uint4(0, 0, 0, 0);
+                b[s] = act ? src[2 * v + 1] : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -137,8 +137,8 @@ quant_rows_mx4_kernel(const uint4* __restrict__ x, long long rows, int cols, int
 
 // As dispatch_copy_mx_kernel.  8,192 x 7,168 to 8 rows each 74 us: HBM, 120 MB of rows in and 250 MB of codes out.
 __global__ void __launch_bounds__(256)
-dispatch_copy_mx4_kernel(const uint4* __restrict__ u, int T, int d, int k, const int32_t* __restrict__ pos, int per,
-                         uint8_t* __restrict__ x_q, long long rows_cap, uint8_t* __restrict__ u_q) {
+dispatch_copy_mx4_kernel(const uint4* u, int T, int d, int k, const int32_t* pos, int per, uint8_t* x_q,
+                         long long rows_cap, uint8_t* u_q) {
     const int lane = threadIdx.x & 31;
     const int t = static_cast<int>((static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
     if (t >= T) return;
@@ -157,8 +157,8 @@ dispatch_copy_mx4_kernel(const uint4* __restrict__ u, int T, int d, int k, const
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             const int v = v0 + 32 * s + lane;
-            a[s] = v < last ? __ldg(src + 2 * v) : make_uint4(0, 0, 0, 0);
-            b[s] = v < last ? __ldg(src + 2 * v + 1) : make_uint4(0, 0, 0, 0);
+            a[s] = v < last ? src[2 * v] : make_uint4(0, 0, 0, 0);
+            b[s] = v < last ? src[2 * v + 1] : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s) c[s] = mx4_lane16(a[s], b[s], &word[s]);

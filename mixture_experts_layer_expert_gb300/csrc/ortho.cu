@@ -327,7 +327,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             }
             float* drow = nullptr;                 // this lane's row of B's diagonal
             if (MODE != GRAM && row0 + lane < args.rows) drow = args.diag + static_cast<long long>(tl.z) * args.rows + row0 + lane;
-            const float d = !SYM && drow ? __ldg(drow) : 0.0f;
+            const float d = !SYM && drow ? *drow : 0.0f;
             if (!mbar_wait(smem_u32(&tfull[acc]), use & 1u, abort_flag, args.err)) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(256) norm_kernel(const Source s, float* part) 
                 uint4 x[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    x[k] = v0 + 32 * k < nv ? __ldg(reinterpret_cast<const uint4*>(row) + v0 + 32 * k) : make_uint4(0, 0, 0, 0);
+                    x[k] = v0 + 32 * k < nv ? reinterpret_cast<const uint4*>(row)[v0 + 32 * k] : make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
@@ -526,13 +526,13 @@ __global__ void __launch_bounds__(256) norm_kernel(const Source s, float* part) 
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                     const int j = 4 * (v0 + 32 * (k >> 3)) + ((k & 7) >> 1);
-                    f[k] = !(k & 1) && j < s.n ? __ldg(reinterpret_cast<const float*>(row) + j) : 0.0f;
+                    f[k] = !(k & 1) && j < s.n ? reinterpret_cast<const float*>(row)[j] : 0.0f;
                 }
             } else {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) {
                     const int j = 8 * (v0 + 32 * (k >> 3)) + (k & 7);
-                    f[k] = j < s.n ? __bfloat162float(__ldg(reinterpret_cast<const __nv_bfloat16*>(row) + j)) : 0.0f;
+                    f[k] = j < s.n ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[j]) : 0.0f;
                 }
             }
             q.add(f);
@@ -608,11 +608,11 @@ scale_rows_kernel(const Source s, const float* part, int nb, double eps, float x
             const int c = c0 + 256 * u;
             if (s.vec && c + 8 <= s.n) {
                 if (s.f32) {
-                    const float4 a = __ldg(reinterpret_cast<const float4*>(row) + c / 4), b = __ldg(reinterpret_cast<const float4*>(row) + c / 4 + 1);
+                    const float4 a = reinterpret_cast<const float4*>(row)[c / 4], b = reinterpret_cast<const float4*>(row)[c / 4 + 1];
                     x[u][0] = a.x; x[u][1] = a.y; x[u][2] = a.z; x[u][3] = a.w;
                     x[u][4] = b.x; x[u][5] = b.y; x[u][6] = b.z; x[u][7] = b.w;
                 } else {
-                    const uint4 a = __ldg(reinterpret_cast<const uint4*>(row) + c / 8);
+                    const uint4 a = reinterpret_cast<const uint4*>(row)[c / 8];
                     x[u][0] = bf16lo(a.x); x[u][1] = bf16hi(a.x); x[u][2] = bf16lo(a.y); x[u][3] = bf16hi(a.y);
                     x[u][4] = bf16lo(a.z); x[u][5] = bf16hi(a.z); x[u][6] = bf16lo(a.w); x[u][7] = bf16hi(a.w);
                 }
@@ -653,9 +653,9 @@ scale_tall_kernel(const Source s, const float* part, int nb, double eps, float x
             const uint8_t* row = g + static_cast<long long>(i) * s.row * es;
             if (s.vec && i < s.m && j + 4 <= s.n) {
                 if (s.f32) {
-                    in[u] = __ldg(reinterpret_cast<const float4*>(row) + j / 4);
+                    in[u] = reinterpret_cast<const float4*>(row)[j / 4];
                 } else {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(row) + j / 4);
+                    const uint2 x = reinterpret_cast<const uint2*>(row)[j / 4];
                     in[u] = make_float4(bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y));
                 }
             } else {

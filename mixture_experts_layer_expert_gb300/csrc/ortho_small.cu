@@ -149,20 +149,29 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
         const int c0 = rank * a.width;
         const size_t es = a.src.f32 ? 4 : 2;
         const uint8_t* g = static_cast<const uint8_t*>(a.src.g) + (z * a.src.mat + c0) * es;
-#pragma unroll 8
-        for (int l = warp; l < lines; l += WARPS) {
-            const int r = l < rr ? l : l - rr, c = l < rr ? 0 : 128;
-            const uint8_t* at_r = g + (static_cast<long long>(r) * a.src.row + c) * es;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (c0 + c + 4 * lane < a.q && r < a.r) {
-                if (a.src.f32) {
-                    v = __ldg(reinterpret_cast<const float4*>(at_r) + lane);
-                } else {
-                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(at_r) + lane);
-                    v = make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
+        constexpr int U = 8;                 // loads in flight before the first store
+#pragma unroll 1
+        for (int l0 = warp; l0 < lines; l0 += U * WARPS) {
+            float4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int l = l0 + u * WARPS, r = l < rr ? l : l - rr, c = l < rr ? 0 : 128;
+                const uint8_t* at_r = g + (static_cast<long long>(r) * a.src.row + c) * es;
+                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (l < lines && c0 + c + 4 * lane < a.q && r < a.r) {
+                    if (a.src.f32) {
+                        v[u] = reinterpret_cast<const float4*>(at_r)[lane];
+                    } else {
+                        const uint2 x = reinterpret_cast<const uint2*>(at_r)[lane];
+                        v[u] = make_float4(bf16lo(x.x), bf16hi(x.x), bf16lo(x.y), bf16hi(x.y));
+                    }
                 }
             }
-            *reinterpret_cast<float4*>((l < rr ? P : P2) + r * P_ROW + 4 * lane) = v;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int l = l0 + u * WARPS;
+                if (l < lines) *reinterpret_cast<float4*>((l < rr ? P + l * P_ROW : P2 + (l - rr) * P_ROW) + 4 * lane) = v[u];
+            }
         }
     } else
 #pragma unroll 4
@@ -175,9 +184,9 @@ __global__ void __launch_bounds__(THREADS, 1) small_kernel(const __grid_constant
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             if (4 * lane < have) {
                 if (a.src.f32) {
-                    v = __ldg(reinterpret_cast<const float4*>(g) + lane);
+                    v = reinterpret_cast<const float4*>(g)[lane];
                 } else {
-                    const uint2 u = __ldg(reinterpret_cast<const uint2*>(g) + lane);
+                    const uint2 u = reinterpret_cast<const uint2*>(g)[lane];
                     v = make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
                 }
             }
