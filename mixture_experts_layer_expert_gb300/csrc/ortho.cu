@@ -419,6 +419,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                         for (int y = 0; y < 32; ++y)
                             if (in && oy + y < args.m)
                                 o[y * args.out_row] = *reinterpret_cast<const uint16_t*>(buf + elem_at(y, lane));
+                        fence_proxy_async_smem();      // the buffer's next content comes by TMA, over what was written here
                         __syncwarp();
                     }
                 } else {

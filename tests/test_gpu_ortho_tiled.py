@@ -131,3 +131,17 @@ def test_a_batchs_order_does_not_matter(m, n):
     back = run(g.flip(0).contiguous()).flip(0)
     assert torch.equal(out, back)
     assert all(torch.equal(run(g[i:i + 1])[0], out[i]) for i in (0, 3, 6))
+
+
+@pytest.mark.parametrize("m,n", [(301, 2600), (2600, 301)])
+def test_stores_by_lanes_match_stores_by_tma(m, n):
+    """Many pieces through each warp's two buffers, which take a piece's inputs by TMA after the last one's result left by lanes."""
+    g = torch.stack([ref.gradient(m, n, 40, i) for i in range(4)]).to(DEV)
+    width = (n + 7) // 8 * 8
+    whole = torch.full((4, m, width), 5.0, dtype=torch.bfloat16, device=DEV)
+    want = run(g, out=whole[:, :, :n])
+    for _ in range(5):
+        odd = torch.full((4, m, n + 1 + n % 2), 5.0, dtype=torch.bfloat16, device=DEV)
+        assert odd.stride(1) % 8
+        assert torch.equal(run(g, out=odd[:, :, :n]), want)
+        assert (odd[:, :, n:] == 5).all()
