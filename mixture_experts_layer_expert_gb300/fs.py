@@ -276,7 +276,8 @@ def pack_linear_mx4(w: torch.Tensor, stream=None) -> torch.Tensor:
     N, K = w.shape
     dev, _ = _here(stream)
     _operand("pack_linear_mx4 w", w, (N, K), dev, strided=False)
-    out = _packed(1, N, K, FS_MXFP4, w)
+    with _allocating(stream):
+        out = _packed(1, N, K, FS_MXFP4, w)
     fs_pack_w3(1, N, K, FS_MXFP4, w, out, stream)
     return out
 
@@ -458,21 +459,22 @@ def _packed(G, N, K, dt, like):
 def pack_block(cfg: LayerConfig, w: dict, stream=None) -> dict:
     """Repack one block's page-layout weights (on the GPU) into the library layout
     (FP8: quantised from the bf16 weights)."""
-    dt = DTYPES[cfg.dtype]
-    E, c, d = cfg.E, cfg.c, cfg.d
-    out = {"w_r": w["w_r"].contiguous(), "bias": None if w.get("bias") is None else w["bias"].contiguous().float()}
-    out["w13"] = _packed(E, 2 * c, d, dt, w["w1"])
-    fs_pack_w13(E, c, d, dt, w["w1"].contiguous(), w["w2"].contiguous(), out["w13"], stream)
-    out["w3"] = _packed(E, d, c, dt, w["w3"])
-    fs_pack_w3(E, d, c, dt, w["w3"].contiguous(), out["w3"], stream)
-    if w.get("w_att") is not None:
-        out["w_att"] = w["w_att"].contiguous()
-    if cfg.n_shared:
-        cw = cfg.n_shared * cfg.c_shared
-        out["w13_shared"] = _packed(1, 2 * cw, d, dt, w["w1s"])
-        fs_pack_w13(1, cw, d, dt, w["w1s"].contiguous(), w["w2s"].contiguous(), out["w13_shared"], stream)
-        out["w3_shared"] = _packed(1, d, cw, dt, w["w3s"])
-        fs_pack_w3_shared(cfg.n_shared, cfg.c_shared, d, dt, w["w3s"].contiguous(), out["w3_shared"], stream)
+    with _allocating(stream):               # copies of strided weights live and die in the order of the packs
+        dt = DTYPES[cfg.dtype]
+        E, c, d = cfg.E, cfg.c, cfg.d
+        out = {"w_r": w["w_r"].contiguous(), "bias": None if w.get("bias") is None else w["bias"].contiguous().float()}
+        out["w13"] = _packed(E, 2 * c, d, dt, w["w1"])
+        fs_pack_w13(E, c, d, dt, w["w1"].contiguous(), w["w2"].contiguous(), out["w13"], stream)
+        out["w3"] = _packed(E, d, c, dt, w["w3"])
+        fs_pack_w3(E, d, c, dt, w["w3"].contiguous(), out["w3"], stream)
+        if w.get("w_att") is not None:
+            out["w_att"] = w["w_att"].contiguous()
+        if cfg.n_shared:
+            cw = cfg.n_shared * cfg.c_shared
+            out["w13_shared"] = _packed(1, 2 * cw, d, dt, w["w1s"])
+            fs_pack_w13(1, cw, d, dt, w["w1s"].contiguous(), w["w2s"].contiguous(), out["w13_shared"], stream)
+            out["w3_shared"] = _packed(1, d, cw, dt, w["w3s"])
+            fs_pack_w3_shared(cfg.n_shared, cfg.c_shared, d, dt, w["w3s"].contiguous(), out["w3_shared"], stream)
     return out
 
 
@@ -558,19 +560,20 @@ def fs_pack_wrt(E, d, w_r, out, stream=None):
 
 def pack_block_t(cfg: LayerConfig, w: dict, stream=None) -> dict:
     """Transposed packs of one block's bf16 weights for the input-gradient GEMMs."""
-    E, c, d = cfg.E, cfg.c, cfg.d
-    epad = (E + 63) // 64 * 64
-    out = {"w13t": _packed(E, d, 2 * c, FS_BF16, w["w1"]), "w3t": _packed(E, c, d, FS_BF16, w["w3"]),
-           "w_rt": _packed(1, d, epad, FS_BF16, w["w_r"])}
-    fs_pack_w13t(E, c, d, w["w1"].contiguous(), w["w2"].contiguous(), out["w13t"], stream)
-    fs_pack_w3t(E, d, c, w["w3"].contiguous(), out["w3t"], stream)
-    fs_pack_wrt(E, d, w["w_r"].contiguous(), out["w_rt"], stream)
-    if cfg.n_shared:
-        cw = cfg.n_shared * cfg.c_shared
-        out["w13t_shared"] = _packed(1, d, 2 * cw, FS_BF16, w["w1s"])
-        out["w3t_shared"] = _packed(1, cw, d, FS_BF16, w["w3s"])
-        fs_pack_w13t(1, cw, d, w["w1s"].contiguous(), w["w2s"].contiguous(), out["w13t_shared"], stream)
-        fs_pack_w3t_shared(cfg.n_shared, cfg.c_shared, d, w["w3s"].contiguous(), out["w3t_shared"], stream)
+    with _allocating(stream):               # copies of strided weights live and die in the order of the packs
+        E, c, d = cfg.E, cfg.c, cfg.d
+        epad = (E + 63) // 64 * 64
+        out = {"w13t": _packed(E, d, 2 * c, FS_BF16, w["w1"]), "w3t": _packed(E, c, d, FS_BF16, w["w3"]),
+               "w_rt": _packed(1, d, epad, FS_BF16, w["w_r"])}
+        fs_pack_w13t(E, c, d, w["w1"].contiguous(), w["w2"].contiguous(), out["w13t"], stream)
+        fs_pack_w3t(E, d, c, w["w3"].contiguous(), out["w3t"], stream)
+        fs_pack_wrt(E, d, w["w_r"].contiguous(), out["w_rt"], stream)
+        if cfg.n_shared:
+            cw = cfg.n_shared * cfg.c_shared
+            out["w13t_shared"] = _packed(1, d, 2 * cw, FS_BF16, w["w1s"])
+            out["w3t_shared"] = _packed(1, cw, d, FS_BF16, w["w3s"])
+            fs_pack_w13t(1, cw, d, w["w1s"].contiguous(), w["w2s"].contiguous(), out["w13t_shared"], stream)
+            fs_pack_w3t_shared(cfg.n_shared, cfg.c_shared, d, w["w3s"].contiguous(), out["w3t_shared"], stream)
     return out
 
 
