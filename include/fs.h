@@ -249,7 +249,9 @@ fs_status fs_quantize_rows_mx4(int64_t rows, int32_t cols, const void* x, void* 
  * y_row >= N elements, a multiple of 16 bytes.  For the projections around the
  * layer (queries, the latent's expansions, the output).  K % 128 == 0, N % 8 == 0,
  * rows < 2^31 - 1024.  Elements of y between N and y_row are left as they were.
- * ws: fs_linear_mx4_ws_bytes bytes (0 for invalid sizes), 256-byte aligned. */
+ * ws: fs_linear_mx4_ws_bytes bytes (0 for invalid sizes), 256-byte aligned.  Nothing
+ * is kept there now (the product plans its tiles in shared memory), so that calls
+ * may share it even if they run at the same time. */
 size_t fs_linear_mx4_ws_bytes(int64_t rows, int32_t N, int32_t K);
 fs_status fs_linear_mx4(int64_t rows, int32_t N, int32_t K, const void* q, const void* w, void* y, int32_t y_dtype,
                         int64_t y_row, void* ws, size_t ws_bytes, void* stream);
@@ -574,12 +576,15 @@ fs_status fs_balance_loss_backward(const fs_balance_desc* desc, const float* log
  *   X = G / (|G|_F + eps);  steps times  A = X X^T, X = a X + (b A + c A A) X
  * with step k's coefficients coefs[3k .. 3k+2]; out = scale X (bf16, transposed
  * back).  Products are fp16 with fp32 sums; X is carried in 19 bits between the
- * steps, because they multiply what a rounding puts into directions that G lacks.
+ * steps, because they multiply what a rounding puts into directions that G lacks
+ * (in fp32 where the shorter side is at most 128 and the other at most 4,096; beyond
+ * that in fp16 alone once the steps left multiply by no more than four).
  * For five usual steps a result of 32 rows or more is within 0.3% (Frobenius, its
  * own bf16 rounding included) of the exact one, for gradients of any rank.  With at most 16 rows
  * or columns (and 8,192 of the other) all of it is fp32.  A matrix of zeros gives
  * zeros (eps = 0 too); a NaN or infinity makes its whole matrix NaN and no other.
- * Norms are taken over fp32's whole range.
+ * Norms are taken over fp32's whole range.  A result's bits depend on its matrix and
+ * the descriptor's steps, eps and scale, not on strides, alignment or the batch.
  *
  * g: fp32 or bf16 (dtype), out bf16; rows contiguous, row strides >= n, matrix strides
  * >= (m - 1) row + n elements (not read for one matrix), any alignment of whole

@@ -17,7 +17,7 @@
 // the sequences' lengths; what a block finds of a sequence goes to slot (block + sequence)
 // of the workspace, which no other pair has because both only grow along the axis.  A second
 // kernel adds a sequence's slots in order.  No float atomics: results repeat bit for bit.
-// Measured: 65,536 x 256, sigmoids, forward 19 us + 9 (3.6 TB/s of logits and indices: a block an SM with 96 KB of rows in
+// Measured: 65,536 x 256, sigmoids, forward 20 us + 7.5 (3.5 TB/s of logits and indices: a block an SM with 96 KB of rows in
 // flight, and the ramps at both ends), backward 21 us (6.4 TB/s); 256 x 8 4 us each, latency.
 #include "common.cuh"
 #include "kernels.h"
